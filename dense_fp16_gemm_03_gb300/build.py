@@ -1,7 +1,8 @@
 """Build the C-ABI shared library libgemm_f16.so in-tree (``_build/``).
 
-One translation unit, one ``-gencode`` (sm_103a), shared cudart; nvcc
-cross-compiles it on a machine without a GPU.
+Two translation units compiled side by side (the dense product, and the
+ragged products with the router), one ``-gencode`` (sm_103a), shared cudart;
+nvcc cross-compiles them on a machine without a GPU.
 """
 import glob
 import os
@@ -14,14 +15,15 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 OUT_DIR = os.path.join(PKG, "_build")
 LIB = os.path.join(OUT_DIR, "libgemm_f16.so")
-SOURCES = [os.path.join(CSRC, "gemm_api.cu")]
-DEPS = SOURCES + sorted(glob.glob(os.path.join(CSRC, "*.cuh"))) + [os.path.join(INCLUDE, "gemm_f16.h")]
+SOURCES = [os.path.join(CSRC, "gemm_api.cu"), os.path.join(CSRC, "ragged_api.cu")]
+DEPS = (SOURCES + sorted(glob.glob(os.path.join(CSRC, "*.cuh"))) + sorted(glob.glob(os.path.join(CSRC, "*.h")))
+        + sorted(glob.glob(os.path.join(INCLUDE, "*.h"))))
 
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 FLAGS = [
     "-gencode", "arch=compute_103a,code=sm_103a",
     "-O3", "-lineinfo", "-std=c++17",
-    "-Xcompiler", "-fPIC", "-shared", "-cudart", "shared",
+    "-Xcompiler", "-fPIC", "-cudart", "shared",
     "-I" + INCLUDE, "-I" + CSRC,
 ]
 
@@ -35,7 +37,17 @@ def _stale_lib(lib):
 
 def _compile(lib, extra):
     tmp = lib + ".tmp%d" % os.getpid()
-    subprocess.run([NVCC, *FLAGS, *extra, "-o", tmp, *SOURCES], check=True)
+    objects = ["%s.%d.o" % (tmp, i) for i in range(len(SOURCES))]
+    try:
+        jobs = [subprocess.Popen([NVCC, *FLAGS, *extra, "-c", "-o", o, src]) for o, src in zip(objects, SOURCES)]
+        codes = [job.wait() for job in jobs]
+        if any(codes):
+            raise subprocess.CalledProcessError(next(c for c in codes if c), NVCC)
+        subprocess.run([NVCC, *FLAGS, "-shared", "-o", tmp, *objects], check=True)
+    finally:
+        for o in objects:
+            if os.path.exists(o):
+                os.remove(o)
     os.replace(tmp, lib)
     return lib
 

@@ -20,6 +20,7 @@
 #include <random>
 #include <string.h>
 
+#include "device_state.h"
 #include "gemm_f16.h"
 #include "gemm_launch.cuh"
 
@@ -746,6 +747,26 @@ long long default_wait_limit(int64_t k_blocks)
 }
 
 }  // namespace
+
+namespace gemm_f16 {
+
+gemm_status_t current_device_state(DeviceState *out)
+{
+    DeviceInfo *dev = nullptr;
+    gemm_status_t st = device_info(&dev);
+    if (st != GEMM_OK) return st;
+    out->num_sms = dev->num_sms;
+    out->ctx_id = dev->ctx_id;
+    out->error_word = dev->error_word;
+    return GEMM_OK;
+}
+
+uint64_t next_launch_stamp()
+{
+    return next_sk_stamp();
+}
+
+}  // namespace gemm_f16
 
 extern "C" {
 

@@ -1,0 +1,679 @@
+// C ABI of the ragged products and the router (declared in include/gemm_ragged.h):
+// argument validation, the choice of kernel variant, workspace layout, tensor
+// maps and launches.  The kernels are in ragged_kernel.cuh and route_kernel.cuh.
+#include <cuda.h>
+#include <cudaTypedefs.h>
+#include <cuda_runtime.h>
+
+#include <mutex>
+#include <string.h>
+
+#include "device_state.h"
+#include "gemm_ragged.h"
+#include "ragged_kernel.cuh"
+#include "route_kernel.cuh"
+
+using namespace gemm_f16;
+
+namespace {
+
+constexpr int kMaxDevices = 64;
+constexpr int64_t kSizeLimit = int64_t(1) << 31;
+
+int64_t cdiv(int64_t a, int64_t b)
+{
+    return (a + b - 1) / b;
+}
+
+int64_t round_up(int64_t a, int64_t b)
+{
+    return cdiv(a, b) * b;
+}
+
+// ------------------------------------------------------------ variants
+
+// One compiled kernel: the CTA pair of each mode for many rows, the single CTA with a 64-row N side
+// for few.
+struct RaggedVariant {
+    int mode, cg, qcap, qbox, smem;
+    const void *fn;
+};
+
+#define RAGGED_VARIANT(MODE, CG, QCAP, ST)                                                               \
+    RaggedVariant                                                                                        \
+    {                                                                                                    \
+        MODE, CG, QCAP, RaggedCfg<MODE, CG, QCAP, ST>::kQBox, RaggedCfg<MODE, CG, QCAP, ST>::kSmemBytes, \
+            reinterpret_cast<const void *>(&gemm_ragged_kernel<MODE, CG, QCAP, ST>)                      \
+    }
+
+enum RaggedVariantId { kVNtWide, kVNtFew, kVNnWide, kVNnFew, kVTn, kVLoraUWide, kVLoraUFew, kVLoraYWide, kVLoraYFew };
+const RaggedVariant kRagged[] = {
+    RAGGED_VARIANT(kNT, 2, 256, 6), RAGGED_VARIANT(kNT, 1, 64, 8),
+    RAGGED_VARIANT(kNN, 2, 256, 6), RAGGED_VARIANT(kNN, 1, 64, 8),
+    RAGGED_VARIANT(kTN, 2, 256, 6),
+    RAGGED_VARIANT(kLoraU, 1, 256, 4), RAGGED_VARIANT(kLoraU, 1, 64, 8),
+    RAGGED_VARIANT(kLoraY, 2, 256, 6), RAGGED_VARIANT(kLoraY, 1, 64, 8),
+};
+constexpr int kNumRagged = int(sizeof(kRagged) / sizeof(kRagged[0]));
+
+struct RaggedDevice {
+    bool ready = false;
+    unsigned long long ctx_id = 0;
+    int slots[kNumRagged] = {};  // co-resident CTAs (single) or pairs of each variant
+    int num_sms = 0;
+    uint32_t *error_word = nullptr;
+};
+
+std::mutex g_ragged_mutex;
+RaggedDevice g_ragged_devices[kMaxDevices];
+
+// State of the current device for these kernels, made once per context.
+gemm_status_t ragged_device(RaggedDevice **out)
+{
+    DeviceState state;
+    gemm_status_t st = current_device_state(&state);
+    if (st != GEMM_OK) return st;
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) {
+        cudaGetLastError();
+        return GEMM_ERR_CUDA;
+    }
+    std::lock_guard<std::mutex> lock(g_ragged_mutex);
+    RaggedDevice &d = g_ragged_devices[dev];
+    if (!d.ready || d.ctx_id != state.ctx_id) {
+        RaggedDevice made;
+        made.ctx_id = state.ctx_id;
+        made.num_sms = state.num_sms;
+        made.error_word = state.error_word;
+        for (int v = 0; v < kNumRagged; ++v) {
+            const RaggedVariant &var = kRagged[v];
+            if (cudaFuncSetAttribute(var.fn, cudaFuncAttributeMaxDynamicSharedMemorySize, var.smem) != cudaSuccess) {
+                cudaGetLastError();
+                return GEMM_ERR_CUDA;
+            }
+            made.slots[v] = state.num_sms / var.cg;
+            if (var.cg > 1) {
+                cudaLaunchConfig_t cfg;
+                memset(&cfg, 0, sizeof(cfg));
+                cfg.gridDim = dim3(unsigned(made.slots[v] * var.cg), 1, 1);
+                cfg.blockDim = dim3(kRagThreads, 1, 1);
+                cfg.dynamicSmemBytes = size_t(var.smem);
+                cudaLaunchAttribute attr;
+                attr.id = cudaLaunchAttributeClusterDimension;
+                attr.val.clusterDim.x = unsigned(var.cg);
+                attr.val.clusterDim.y = 1;
+                attr.val.clusterDim.z = 1;
+                cfg.attrs = &attr;
+                cfg.numAttrs = 1;
+                int clusters = 0;
+                if (cudaOccupancyMaxActiveClusters(&clusters, var.fn, &cfg) == cudaSuccess && clusters > 0)
+                    made.slots[v] = clusters;
+                else
+                    cudaGetLastError();
+            }
+        }
+        made.ready = true;
+        d = made;
+    }
+    *out = &d;
+    return GEMM_OK;
+}
+
+// --------------------------------------------------------- tensor maps
+
+PFN_cuTensorMapEncodeTiled_v12000 g_ragged_encode = nullptr;
+
+gemm_status_t ragged_encoder(PFN_cuTensorMapEncodeTiled_v12000 *fn)
+{
+    static std::once_flag once;
+    std::call_once(once, []() {
+        void *ptr = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault, &q) ==
+                cudaSuccess &&
+            q == cudaDriverEntryPointSuccess)
+            g_ragged_encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(ptr);
+        else
+            cudaGetLastError();
+    });
+    *fn = g_ragged_encode;
+    return g_ragged_encode ? GEMM_OK : GEMM_ERR_CUDA;
+}
+
+// `count` row-major matrices of rows x cols, boxes of box_cols x box_rows in 128-byte-swizzled shared memory,
+// zeros outside a matrix.
+gemm_status_t encode_stack(CUtensorMap *map, const void *ptr, gemm_dtype_t dtype, int64_t count, int64_t rows, int64_t cols,
+                           int box_cols, int box_rows)
+{
+    PFN_cuTensorMapEncodeTiled_v12000 enc = nullptr;
+    gemm_status_t st = ragged_encoder(&enc);
+    if (st != GEMM_OK) return st;
+    const uint64_t size = dtype == GEMM_DTYPE_F32 ? 4u : 2u;
+    cuuint64_t dims[3] = {cuuint64_t(cols), cuuint64_t(rows), cuuint64_t(count)};
+    cuuint64_t strides[2] = {cuuint64_t(cols) * size, cuuint64_t(cols) * cuuint64_t(rows) * size};
+    cuuint32_t box[3] = {cuuint32_t(box_cols), cuuint32_t(box_rows), 1};
+    cuuint32_t estr[3] = {1, 1, 1};
+    const CUtensorMapDataType type = dtype == GEMM_DTYPE_F32    ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+                                     : dtype == GEMM_DTYPE_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                                                : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+    const CUresult r = enc(map, type, 3, const_cast<void *>(ptr), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                           CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    // (a matrix stride of 2^40 bytes or more cannot be described)
+    return r == CUDA_SUCCESS ? GEMM_OK : GEMM_ERR_UNSUPPORTED_SHAPE;
+}
+
+// ---------------------------------------------------------- validation
+
+gemm_status_t check_pointer(const void *p, bool used, uintptr_t align = 16)
+{
+    if (!used) return GEMM_OK;
+    if (p == nullptr) return GEMM_ERR_INVALID_ARG;
+    return (reinterpret_cast<uintptr_t>(p) & (align - 1u)) ? GEMM_ERR_ALIGNMENT : GEMM_OK;
+}
+
+gemm_status_t check_sizes(std::initializer_list<int64_t> any, std::initializer_list<int64_t> by8)
+{
+    for (int64_t v : any)
+        if (v < 0) return GEMM_ERR_INVALID_ARG;
+    for (int64_t v : by8)
+        if (v < 0) return GEMM_ERR_INVALID_ARG;
+    for (int64_t v : any)
+        if (v >= kSizeLimit) return GEMM_ERR_UNSUPPORTED_SHAPE;
+    for (int64_t v : by8)
+        if (v >= kSizeLimit || v % 8 != 0) return GEMM_ERR_UNSUPPORTED_SHAPE;
+    return GEMM_OK;
+}
+
+bool operand_type(gemm_dtype_t t)
+{
+    return t == GEMM_DTYPE_F16 || t == GEMM_DTYPE_BF16;
+}
+
+// ------------------------------------------------------------- launches
+
+gemm_status_t launch(const void *fn, unsigned grid, unsigned threads, int smem, int cluster, void **args, cudaStream_t stream)
+{
+    cudaLaunchConfig_t cfg;
+    memset(&cfg, 0, sizeof(cfg));
+    cfg.gridDim = dim3(grid, 1, 1);
+    cfg.blockDim = dim3(threads, 1, 1);
+    cfg.dynamicSmemBytes = size_t(smem);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    int na = 0;
+    if (cluster > 1) {
+        attr[na].id = cudaLaunchAttributeClusterDimension;
+        attr[na].val.clusterDim.x = unsigned(cluster);
+        attr[na].val.clusterDim.y = 1;
+        attr[na].val.clusterDim.z = 1;
+        ++na;
+    }
+    attr[na].id = cudaLaunchAttributeProgrammaticStreamSerialization;  // set-up overlaps the previous kernel's tail
+    attr[na].val.programmaticStreamSerializationAllowed = 1;
+    ++na;
+    cfg.attrs = attr;
+    cfg.numAttrs = unsigned(na);
+    if (cudaLaunchKernelExC(&cfg, fn, args) != cudaSuccess) {
+        cudaGetLastError();
+        return GEMM_ERR_LAUNCH;
+    }
+    return GEMM_OK;
+}
+
+long long wait_limit_for(int64_t k_blocks)
+{
+    return 2000000000LL + k_blocks * 65536LL;
+}
+
+// Bytes of split work for one variant: a partial tile and a flag per CTA.
+size_t split_bytes(const RaggedVariant &var, int slots)
+{
+    const size_t ctas = size_t(slots) * size_t(var.cg);
+    return ctas * 128u * size_t(var.qcap) * 4u + ctas * 8u;
+}
+
+void use_split(RaggedParams *p, const RaggedVariant &var, int slots, void *ws)
+{
+    const size_t ctas = size_t(slots) * size_t(var.cg);
+    p->sk = 1;
+    p->partials = static_cast<float *>(ws);
+    p->flags = reinterpret_cast<uint64_t *>(static_cast<char *>(ws) + ctas * 128u * size_t(var.qcap) * 4u);
+    p->stamp = next_launch_stamp();
+}
+
+gemm_status_t launch_ragged(int variant, const RaggedDevice *dev, RaggedParams &p, int64_t most_units, cudaStream_t stream)
+{
+    const RaggedVariant &var = kRagged[variant];
+    int64_t workers = dev->slots[variant];
+    if (most_units < workers) workers = most_units < 1 ? 1 : most_units;
+    p.error_word = dev->error_word;
+    void *args[1] = {&p};
+    return launch(var.fn, unsigned(workers * var.cg), kRagThreads, var.smem, var.cg, args, stream);
+}
+
+// ------------------------------------------------------ grouped products
+
+// Few rows per group: single CTAs with a 64-row N side; each group's weights are then read once and the
+// time is theirs.  More: CTA pairs.
+bool few_rows(int64_t groups, int64_t rows)
+{
+    return rows <= 64 * groups;
+}
+
+int grouped_variant(int mode, int64_t groups, int64_t rows)
+{
+    if (mode == kTN) return kVTn;
+    const bool few = few_rows(groups, rows);
+    if (mode == kNT) return few ? kVNtFew : kVNtWide;
+    return few ? kVNnFew : kVNnWide;
+}
+
+gemm_status_t grouped(int mode, gemm_dtype_t dtype, gemm_dtype_t out_type, int64_t groups, int64_t rows, int64_t n, int64_t k,
+                      const int32_t *offsets, const void *first, const void *second, void *out, void *ws, size_t ws_bytes,
+                      uint32_t skip_fill, long long wait_limit, cudaStream_t stream)
+{
+    gemm_status_t st = check_sizes({groups, rows}, {n, k});
+    if (st != GEMM_OK) return st;
+    if (!operand_type(dtype) || (out_type != dtype && !(mode == kTN && out_type == GEMM_DTYPE_F32)))
+        return GEMM_ERR_INVALID_ARG;
+    if (groups > GEMM_GROUPED_MAX_GROUPS) return GEMM_ERR_UNSUPPORTED_SHAPE;
+    const int64_t pdim = mode == kNN ? k : n;           // M side of the instruction
+    const int64_t kdim = mode == kNT ? k : mode == kNN ? n : rows;  // contraction
+    const int64_t out_rows = mode == kTN ? groups * n : rows;
+    const int64_t out_cols = mode == kNT ? n : k;
+    const size_t out_bytes = size_t(out_rows) * size_t(out_cols) * (out_type == GEMM_DTYPE_F32 ? 4u : 2u);
+    const bool sum = kdim > 0 && groups > 0;  // anything to add up
+    st = check_pointer(out, out_bytes > 0);
+    if (st == GEMM_OK) st = check_pointer(first, out_bytes > 0 && sum);
+    if (st == GEMM_OK) st = check_pointer(second, out_bytes > 0 && sum);
+    if (st == GEMM_OK) st = check_pointer(offsets, out_bytes > 0 && sum, 4);
+    if (st != GEMM_OK) return st;
+    if (out_bytes == 0) return GEMM_OK;
+    RaggedDevice *dev = nullptr;
+    st = ragged_device(&dev);
+    if (st != GEMM_OK) return st;
+    const int variant = grouped_variant(mode, groups, rows);
+    const RaggedVariant &var = kRagged[variant];
+    const size_t need = mode == kTN ? 0 : split_bytes(var, dev->slots[variant]);
+    if (ws != nullptr || ws_bytes != 0) {
+        if (ws == nullptr || ws_bytes < need) return GEMM_ERR_WORKSPACE;
+        if (reinterpret_cast<uintptr_t>(ws) & 255u) return GEMM_ERR_ALIGNMENT;
+    }
+    if (!sum) {
+        if (cudaMemsetAsync(out, 0, out_bytes, stream) != cudaSuccess) {
+            cudaGetLastError();
+            return GEMM_ERR_LAUNCH;
+        }
+        return GEMM_OK;
+    }
+    RaggedParams p;
+    memset(&p, 0, sizeof(p));
+    p.offsets = offsets;
+    p.groups = uint32_t(groups);
+    p.rows = uint32_t(rows);
+    p.pdim = uint32_t(pdim);
+    p.qdim = uint32_t(mode == kTN ? k : 0);
+    p.kdim = uint32_t(kdim);
+    p.k_blocks = uint32_t(cdiv(kdim, kRagBlockK));
+    p.tiles_p = uint32_t(cdiv(pdim, 128 * var.cg));
+    p.tiles_q = uint32_t(mode == kTN ? cdiv(k, var.qcap) : 0);
+    p.band = 8;
+    p.bf16 = dtype == GEMM_DTYPE_BF16;
+    p.out32 = out_type == GEMM_DTYPE_F32;
+    p.out = out;
+    p.skip_fill = skip_fill;
+    p.wait_limit = wait_limit ? wait_limit : wait_limit_for(p.k_blocks);
+    int64_t most;  // tiles, at most
+    if (mode == kTN) most = int64_t(p.tiles_p) * p.tiles_q * (groups < rows ? groups : rows);
+    else most = int64_t(p.tiles_p) * (rows / var.qcap + (groups < rows ? groups : rows));
+    if (most >= kSizeLimit) return GEMM_ERR_UNSUPPORTED_SHAPE;
+    if (mode == kTN) {
+        st = encode_stack(&p.tm_p, first, dtype, 1, rows, n, 64, 64);
+        if (st == GEMM_OK) st = encode_stack(&p.tm_q, second, dtype, 1, rows, k, 64, 64);
+        if (st == GEMM_OK) st = encode_stack(&p.tm_x, out, out_type, groups, n, k, p.out32 ? 32 : 64, 32);
+    } else {
+        st = encode_stack(&p.tm_p, second, dtype, groups, n, k, 64, mode == kNT ? 128 : 64);
+        if (st == GEMM_OK) st = encode_stack(&p.tm_q, first, dtype, 1, rows, kdim, kRagBlockK, var.qbox);
+        if (ws && few_rows(groups, rows)) {
+            use_split(&p, var, dev->slots[variant], ws);
+            most *= p.k_blocks;
+        }
+    }
+    if (st != GEMM_OK) return st;
+    return launch_ragged(variant, dev, p, most, stream);
+}
+
+// ------------------------------------------------------------- adapters
+
+// Rows of a tile and how the workspace is laid out: counts per tile, adapters per tile, u, split work.
+struct LoraPlan {
+    int64_t per, tiles;  // of one pass
+    int64_t pass_rows;   // rows of one pass: the kernels' table holds kRagMaxGroups tiles
+    int variant_u, variant_y;
+    bool split_y;
+    size_t counts, list, u, split, total;  // offsets
+};
+
+LoraPlan lora_plan(const RaggedDevice *dev, int64_t rows, int64_t rank)
+{
+    LoraPlan l;
+    const bool few = rows <= 64;
+    l.variant_u = few ? kVLoraUFew : kVLoraUWide;
+    l.variant_y = few ? kVLoraYFew : kVLoraYWide;
+    const RaggedVariant &y = kRagged[l.variant_y];
+    l.pass_rows = int64_t(kRagMaxGroups) * y.qcap;
+    if (rows < l.pass_rows) l.pass_rows = rows;
+    l.tiles = cdiv(l.pass_rows, y.qcap);
+    l.per = round_up(cdiv(l.pass_rows, l.tiles), 16 * y.cg);
+    l.split_y = l.tiles == 1;
+    size_t at = 0;
+    auto take = [&](size_t bytes) {
+        const size_t was = at;
+        at += size_t(round_up(int64_t(bytes), 256));
+        return was;
+    };
+    l.counts = take(size_t(l.tiles) * 4u);
+    l.list = take(size_t(l.tiles) * size_t(l.per) * 4u);
+    l.u = take(size_t(l.pass_rows) * size_t(rank) * 2u);
+    size_t split = split_bytes(kRagged[l.variant_u], dev->slots[l.variant_u]);
+    const size_t split_y = l.split_y ? split_bytes(y, dev->slots[l.variant_y]) : 0;
+    if (split_y > split) split = split_y;
+    l.split = take(split);
+    l.total = at;
+    return l;
+}
+
+}  // namespace
+
+extern "C" {
+
+gemm_status_t gemm_grouped_workspace_size(int64_t groups, int64_t rows, int64_t n, int64_t k, size_t *bytes)
+{
+    if (!bytes) return GEMM_ERR_INVALID_ARG;
+    gemm_status_t st = check_sizes({groups, rows}, {n, k});
+    if (st != GEMM_OK) return st;
+    if (groups > GEMM_GROUPED_MAX_GROUPS) return GEMM_ERR_UNSUPPORTED_SHAPE;
+    RaggedDevice *dev = nullptr;
+    st = ragged_device(&dev);
+    if (st != GEMM_OK) return st;
+    *bytes = 0;
+    for (int mode : {int(kNT), int(kNN)}) {
+        const int v = grouped_variant(mode, groups, rows);
+        const size_t need = split_bytes(kRagged[v], dev->slots[v]);
+        if (need > *bytes) *bytes = need;
+    }
+    return GEMM_OK;
+}
+
+gemm_status_t gemm_grouped_nt(gemm_dtype_t dtype, int64_t groups, int64_t rows, int64_t n, int64_t k, const int32_t *offsets,
+                              const void *x, const void *w, void *y, void *workspace, size_t ws_bytes, gemm_stream_t stream)
+{
+    return grouped(kNT, dtype, dtype, groups, rows, n, k, offsets, x, w, y, workspace, ws_bytes, ~0u, 0,
+                   reinterpret_cast<cudaStream_t>(stream));
+}
+
+gemm_status_t gemm_grouped_nn(gemm_dtype_t dtype, int64_t groups, int64_t rows, int64_t n, int64_t k, const int32_t *offsets,
+                              const void *dy, const void *w, void *dx, void *workspace, size_t ws_bytes, gemm_stream_t stream)
+{
+    return grouped(kNN, dtype, dtype, groups, rows, n, k, offsets, dy, w, dx, workspace, ws_bytes, ~0u, 0,
+                   reinterpret_cast<cudaStream_t>(stream));
+}
+
+gemm_status_t gemm_grouped_tn(gemm_dtype_t dtype, gemm_dtype_t out, int64_t groups, int64_t rows, int64_t n, int64_t k,
+                              const int32_t *offsets, const void *dy, const void *x, void *dw, void *workspace, size_t ws_bytes,
+                              gemm_stream_t stream)
+{
+    return grouped(kTN, dtype, out, groups, rows, n, k, offsets, dy, x, dw, workspace, ws_bytes, ~0u, 0,
+                   reinterpret_cast<cudaStream_t>(stream));
+}
+
+gemm_status_t gemm_grouped_stall_test(int32_t mode, gemm_dtype_t dtype, int64_t groups, int64_t rows, int64_t n, int64_t k,
+                                      const int32_t *offsets, const void *first, const void *second, void *out, void *workspace,
+                                      size_t ws_bytes, uint32_t skip_fill, long long wait_limit_cycles, gemm_stream_t stream)
+{
+    if (mode < kNT || mode > kTN || wait_limit_cycles <= 0) return GEMM_ERR_INVALID_ARG;
+    return grouped(mode, dtype, dtype, groups, rows, n, k, offsets, first, second, out, workspace, ws_bytes, skip_fill,
+                   wait_limit_cycles, reinterpret_cast<cudaStream_t>(stream));
+}
+
+gemm_status_t gemm_lora_workspace_size(int64_t rows, int64_t n, int64_t k, int64_t rank, int64_t adapters, size_t *bytes)
+{
+    if (!bytes) return GEMM_ERR_INVALID_ARG;
+    gemm_status_t st = check_sizes({rows, adapters}, {n, k, rank});
+    if (st != GEMM_OK) return st;
+    if (rank > GEMM_LORA_MAX_RANK) return GEMM_ERR_UNSUPPORTED_SHAPE;
+    RaggedDevice *dev = nullptr;
+    st = ragged_device(&dev);
+    if (st != GEMM_OK) return st;
+    *bytes = rows ? lora_plan(dev, rows, rank).total : 0;
+    return GEMM_OK;
+}
+
+gemm_status_t gemm_lora_nt(gemm_dtype_t dtype, int64_t rows, int64_t n, int64_t k, int64_t rank, int64_t adapters,
+                           const void *x, const void *w, const void *a, const void *b, const int32_t *ids, const float *scale,
+                           void *y, void *workspace, size_t ws_bytes, gemm_stream_t stream)
+{
+    gemm_status_t st = check_sizes({rows, adapters}, {n, k, rank});
+    if (st != GEMM_OK) return st;
+    if (!operand_type(dtype)) return GEMM_ERR_INVALID_ARG;
+    if (rank > GEMM_LORA_MAX_RANK) return GEMM_ERR_UNSUPPORTED_SHAPE;
+    const bool any = rows > 0 && n > 0;
+    const bool adapted = any && k > 0 && adapters > 0 && rank > 0;
+    st = check_pointer(y, any);
+    if (st == GEMM_OK) st = check_pointer(x, any && k > 0);
+    if (st == GEMM_OK) st = check_pointer(w, any && k > 0);
+    if (st == GEMM_OK) st = check_pointer(a, adapted);
+    if (st == GEMM_OK) st = check_pointer(b, adapted);
+    if (st == GEMM_OK) st = check_pointer(ids, adapted, 4);
+    if (st == GEMM_OK && scale) st = check_pointer(scale, adapted, 4);
+    if (st != GEMM_OK) return st;
+    if (!any) return GEMM_OK;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    RaggedDevice *dev = nullptr;
+    st = ragged_device(&dev);
+    if (st != GEMM_OK) return st;
+    const LoraPlan l = lora_plan(dev, rows, rank);
+    if (workspace == nullptr || ws_bytes < l.total) return GEMM_ERR_WORKSPACE;
+    if (reinterpret_cast<uintptr_t>(workspace) & 255u) return GEMM_ERR_ALIGNMENT;
+    if (k == 0) {
+        if (cudaMemsetAsync(y, 0, size_t(rows) * size_t(n) * 2u, s) != cudaSuccess) {
+            cudaGetLastError();
+            return GEMM_ERR_LAUNCH;
+        }
+        return GEMM_OK;
+    }
+    char *ws = static_cast<char *>(workspace);
+    int32_t *counts = reinterpret_cast<int32_t *>(ws + l.counts), *list = reinterpret_cast<int32_t *>(ws + l.list);
+    const RaggedVariant &vu = kRagged[l.variant_u], &vy = kRagged[l.variant_y];
+
+    RaggedParams u, p;
+    memset(&u, 0, sizeof(u));
+    u.kdim = uint32_t(k);
+    u.k_blocks = uint32_t(cdiv(k, kRagBlockK));
+    u.per = uint32_t(l.per);
+    u.band = 8;
+    u.bf16 = dtype == GEMM_DTYPE_BF16;
+    u.counts = counts;
+    u.list = list;
+    u.scale = scale;
+    u.rank = uint32_t(rank);
+    u.rank_blocks = uint32_t(cdiv(rank, kRagBlockK));
+    u.skip_fill = ~0u;
+    u.wait_limit = wait_limit_for(cdiv(k, kRagBlockK) + 4096);
+    p = u;
+    // u = scale x a^T: one tile per row tile and adapter
+    u.pdim = uint32_t(rank);
+    u.tiles_p = 1;
+    u.out = ws + l.u;
+    // y = x w^T + u b^T
+    p.pdim = uint32_t(n);
+    p.tiles_p = uint32_t(cdiv(n, 128 * vy.cg));
+    p.u = ws + l.u;
+    st = encode_stack(&p.tm_p, w, dtype, 1, n, k, kRagBlockK, 128);
+    if (st == GEMM_OK && adapted) st = encode_stack(&u.tm_p, a, dtype, adapters, rank, k, kRagBlockK, 128);
+    if (st == GEMM_OK && adapted) st = encode_stack(&p.tm_x, b, dtype, adapters, n, rank, kRagBlockK, 128);
+    if (!adapted) p.tm_x = p.tm_p;  // (never loaded from)
+    if (st != GEMM_OK) return st;
+    if (int64_t(p.tiles_p) * l.tiles >= kSizeLimit) return GEMM_ERR_UNSUPPORTED_SHAPE;
+
+    for (int64_t r0 = 0; r0 < rows; r0 += l.pass_rows) {
+        const int64_t r = rows - r0 < l.pass_rows ? rows - r0 : l.pass_rows;
+        const int64_t tiles = cdiv(r, l.per);
+        const char *xr = static_cast<const char *>(x) + size_t(r0) * size_t(k) * 2u;
+        uint32_t rr = uint32_t(r), per = uint32_t(l.per), count = adapted ? uint32_t(adapters) : 0u;
+        const int32_t *idr = ids ? ids + r0 : nullptr;
+        if (!adapted) {
+            if (cudaMemsetAsync(counts, 0, size_t(tiles) * 4u, s) != cudaSuccess) {
+                cudaGetLastError();
+                return GEMM_ERR_LAUNCH;
+            }
+        } else {
+            void *args[6] = {&idr, &rr, &per, &count, &counts, &list};
+            st = launch(reinterpret_cast<const void *>(&lora_plan_kernel), unsigned(tiles), 256, 0, 1, args, s);
+            if (st != GEMM_OK) return st;
+            u.groups = uint32_t(tiles);
+            u.rows = rr;
+            u.ids = idr;
+            st = encode_stack(&u.tm_q, xr, dtype, 1, r, k, kRagBlockK, vu.qbox);
+            if (st != GEMM_OK) return st;
+            use_split(&u, vu, dev->slots[l.variant_u], ws + l.split);
+            st = launch_ragged(l.variant_u, dev, u, r * int64_t(u.k_blocks), s);
+            if (st != GEMM_OK) return st;
+        }
+        p.groups = uint32_t(tiles);
+        p.tiles_q = uint32_t(tiles);
+        p.rows = rr;
+        p.ids = idr;
+        p.out = static_cast<char *>(y) + size_t(r0) * size_t(n) * 2u;
+        st = encode_stack(&p.tm_q, xr, dtype, 1, r, k, kRagBlockK, vy.qbox);
+        if (st != GEMM_OK) return st;
+        int64_t most = int64_t(p.tiles_p) * tiles;
+        p.sk = 0;
+        if (tiles == 1 && l.split_y) {
+            use_split(&p, vy, dev->slots[l.variant_y], ws + l.split);
+            most *= p.k_blocks;
+        }
+        st = launch_ragged(l.variant_y, dev, p, most, s);
+        if (st != GEMM_OK) return st;
+    }
+    return GEMM_OK;
+}
+
+// --------------------------------------------------------------- router
+
+static gemm_status_t check_route(gemm_dtype_t dtype, int64_t rows, int64_t experts, int64_t top)
+{
+    gemm_status_t st = check_sizes({rows, experts, top}, {});
+    if (st != GEMM_OK) return st;
+    if (dtype != GEMM_DTYPE_F16 && dtype != GEMM_DTYPE_BF16 && dtype != GEMM_DTYPE_F32) return GEMM_ERR_INVALID_ARG;
+    if (experts < 1 || top < 1 || top > experts) return GEMM_ERR_INVALID_ARG;
+    if (experts > GEMM_ROUTE_MAX_EXPERTS || top > GEMM_ROUTE_MAX_TOP || rows * top >= kSizeLimit)
+        return GEMM_ERR_UNSUPPORTED_SHAPE;
+    return GEMM_OK;
+}
+
+gemm_status_t gemm_route_workspace_size(int64_t rows, int64_t experts, int64_t top, size_t *bytes)
+{
+    if (!bytes) return GEMM_ERR_INVALID_ARG;
+    gemm_status_t st = check_route(GEMM_DTYPE_F32, rows, experts, top);
+    if (st != GEMM_OK) return st;
+    const int64_t blocks = cdiv(rows, kRouteRows);
+    *bytes = blocks > 1 ? size_t(blocks + 1) * size_t(experts) * 4u : 0;
+    return GEMM_OK;
+}
+
+// The instance of a kernel template whose lanes hold enough values for `experts`.
+#define ROUTE_INSTANCE(KERNEL, experts)                                                                               \
+    ((experts) <= 32    ? reinterpret_cast<const void *>(&KERNEL<1>)                                                  \
+     : (experts) <= 64  ? reinterpret_cast<const void *>(&KERNEL<2>)                                                  \
+     : (experts) <= 128 ? reinterpret_cast<const void *>(&KERNEL<4>)                                                  \
+     : (experts) <= 256 ? reinterpret_cast<const void *>(&KERNEL<8>)                                                  \
+     : (experts) <= 512 ? reinterpret_cast<const void *>(&KERNEL<16>)                                                 \
+                        : reinterpret_cast<const void *>(&KERNEL<32>))
+
+gemm_status_t gemm_route_topk(gemm_dtype_t dtype, int64_t rows, int64_t experts, int64_t top, int32_t renorm, const void *logits,
+                              int32_t *ids, float *weights, int32_t *offsets, int32_t *order, int32_t *position, void *workspace,
+                              size_t ws_bytes, gemm_stream_t stream)
+{
+    gemm_status_t st = check_route(dtype, rows, experts, top);
+    if (st != GEMM_OK) return st;
+    const bool any = rows > 0;
+    st = check_pointer(logits, any);
+    if (st == GEMM_OK) st = check_pointer(offsets, true, 4);
+    for (const void *ptr : {static_cast<const void *>(ids), static_cast<const void *>(weights), static_cast<const void *>(order),
+                            static_cast<const void *>(position)})
+        if (st == GEMM_OK) st = check_pointer(ptr, any, 4);
+    if (st != GEMM_OK) return st;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    DeviceState state;
+    st = current_device_state(&state);
+    if (st != GEMM_OK) return st;
+    if (!any) {
+        if (cudaMemsetAsync(offsets, 0, size_t(experts + 1) * 4u, s) != cudaSuccess) {
+            cudaGetLastError();
+            return GEMM_ERR_LAUNCH;
+        }
+        return GEMM_OK;
+    }
+    const int64_t blocks = cdiv(rows, kRouteRows);
+    if (blocks > 1) {
+        if (workspace == nullptr || ws_bytes < size_t(blocks + 1) * size_t(experts) * 4u) return GEMM_ERR_WORKSPACE;
+        if (reinterpret_cast<uintptr_t>(workspace) & 255u) return GEMM_ERR_ALIGNMENT;
+    }
+    RouteParams p;
+    memset(&p, 0, sizeof(p));
+    p.logits = logits;
+    p.dtype = uint32_t(dtype);
+    p.rows = uint32_t(rows);
+    p.experts = uint32_t(experts);
+    p.top = uint32_t(top);
+    p.renorm = renorm != 0;
+    p.blocks = uint32_t(blocks);
+    p.ids = ids;
+    p.weights = weights;
+    p.offsets = offsets;
+    p.order = order;
+    p.position = position;
+    p.hist = static_cast<int32_t *>(workspace);
+    p.totals = p.hist ? p.hist + size_t(blocks) * size_t(experts) : nullptr;
+    void *args[1] = {&p};
+    st = launch(ROUTE_INSTANCE(route_topk_kernel, experts), unsigned(blocks), kRouteThreads, 0, 1, args, s);
+    if (st != GEMM_OK || blocks == 1) return st;
+    st = launch(reinterpret_cast<const void *>(&route_scan_kernel), unsigned(cdiv(experts, 32)), 1024, 0, 1, args, s);
+    if (st != GEMM_OK) return st;
+    return launch(reinterpret_cast<const void *>(&route_place_kernel), unsigned(blocks), kRouteThreads, 0, 1, args, s);
+}
+
+gemm_status_t gemm_route_topk_grad(gemm_dtype_t dtype, int64_t rows, int64_t experts, int64_t top, int32_t renorm,
+                                   const void *logits, const int32_t *ids, const float *weights, const float *dweights,
+                                   float *dlogits, gemm_stream_t stream)
+{
+    gemm_status_t st = check_route(dtype, rows, experts, top);
+    if (st != GEMM_OK) return st;
+    const bool any = rows > 0;
+    st = check_pointer(logits, any);
+    for (const void *ptr : {static_cast<const void *>(ids), static_cast<const void *>(weights),
+                            static_cast<const void *>(dweights), static_cast<const void *>(dlogits)})
+        if (st == GEMM_OK) st = check_pointer(ptr, any, 4);
+    if (st != GEMM_OK || !any) return st;
+    DeviceState state;
+    st = current_device_state(&state);
+    if (st != GEMM_OK) return st;
+    RouteParams p;
+    memset(&p, 0, sizeof(p));
+    p.logits = logits;
+    p.dtype = uint32_t(dtype);
+    p.rows = uint32_t(rows);
+    p.experts = uint32_t(experts);
+    p.top = uint32_t(top);
+    p.renorm = renorm != 0;
+    p.ids = const_cast<int32_t *>(ids);
+    p.weights = const_cast<float *>(weights);
+    p.dweights = dweights;
+    p.dlogits = dlogits;
+    void *args[1] = {&p};
+    return launch(ROUTE_INSTANCE(route_grad_kernel, experts), unsigned(cdiv(rows, 8)), 256, 0, 1, args,
+                  reinterpret_cast<cudaStream_t>(stream));
+}
+
+}  // extern "C"

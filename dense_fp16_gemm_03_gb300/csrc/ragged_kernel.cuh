@@ -1,0 +1,1007 @@
+// Products whose second matrix depends on the row: grouped products by expert
+// (forward and both gradients) and low-rank adapters beside a shared
+// projection, as one persistent, warp-specialised sm_103a kernel.
+//
+// The matrix with the ragged extent sits on the N side of the tensor-core
+// instruction and the weights on its M side ("P" and "Q" below): the
+// instruction's N is chosen per tile in steps of 16 (one CTA) or 32 (CTA pair),
+// so a group of 40 rows costs 48 or 64 columns and not a whole tile, and a group
+// of one row streams its weights at the memory's rate.  Per mode, with w, x, dy
+// as the caller passes them:
+//
+//   kNT      y[t, n]  = sum_k w[g][n, k] x[t, k]     P = w[g] rows n, Q = x rows t
+//   kNN      dx[t, k] = sum_n w[g][n, k] dy[t, n]    P = w[g] columns k, Q = dy rows t
+//   kTN      dw[g][n, k] = sum_t dy[t, n] x[t, k]    P = dy columns n, Q = x columns k
+//   kLoraU   u[t, r]  = s sum_k a[i][r, k] x[t, k]   P = a[i] rows r, Q = x rows t, kept where ids[t] = i
+//   kLoraY   y[t, n]  = sum_k w[n, k] x[t, k] + sum_r b[i][n, r] u[t, r]
+//                                                    kNT with one group, then K blocks of b[i] against u with
+//                                                    the rows of other adapters zeroed, one per adapter of the tile
+//
+// Everything but kTN yields tiles with the output column on tensor-memory
+// lanes and the row on columns; the epilogue transposes 32 x 32 pieces through
+// shared memory and stores only rows of the tile's own group, so tiles may read
+// past a group's end (the rows there are finite work thrown away) but never
+// write there.
+//
+// Roles (256 threads; one CTA or a CTA pair per tile):
+//   warp 0      TMA producer into a STAGES-deep ring of 128-byte-swizzled stages
+//   warp 1      tensor memory and the MMA issuer (of the pair's first CTA)
+//   warps 2..5  epilogue, on one of two accumulators while the other fills
+//   warps 6, 7  helper: kTN zeroes the rows past a group's end in its last K
+//               block (both operands: a zero times an infinity of the next group
+//               would be NaN); kLoraY builds the masked u operand, and for the same
+//               reason takes infinities and NaN out of the adapter's b and has the
+//               epilogue write NaN for them into that adapter's own rows alone.  A
+//               stage that the helper touches arrives on its CTA's `tail` barrier and is
+//               released to the MMA by the `fixed` barrier.
+//
+// Group ends are read on the device (no host copy of them exists): every CTA
+// turns the offsets into a table of tile counts in shared memory, where all
+// roles look their tiles up.
+//
+// Walks: data-parallel (tile u on worker u mod workers), or with `sk` each
+// worker takes an equal run of all K-block iterations.  A run that stops
+// inside a tile publishes its fp32 partial for the worker that holds the tile's
+// last K block.  Workers walk their run backwards, so they publish first and
+// wait last, and only ever for lower-numbered workers.  Sums are added in a fixed
+// order: results repeat bit for bit.
+//
+// Every wait is bounded as in gemm_kernel.cuh: past `wait_limit` cycles the
+// thread records an error code, raises the CTA's abort flag, and all roles
+// leave, wait for copies in flight, free tensor memory and return.
+#pragma once
+
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <stdint.h>
+
+#include "ragged_ptx.cuh"
+
+namespace gemm_f16 {
+
+constexpr int kRagBlockK = 64;       // 16-bit elements per 128-byte swizzled row
+constexpr int kRagThreads = 256;
+constexpr int kRagMaxGroups = 1024;  // entries of the shared-memory group table
+constexpr int kRagEpiWarps = 4;
+constexpr int kRagHelpers = 64;      // threads of the helper warps
+constexpr int kRagMaxSmem = 232448;  // 227 KB opt-in dynamic shared memory per CTA
+
+enum RaggedMode : int { kNT = 0, kNN = 1, kTN = 2, kLoraU = 3, kLoraY = 4 };
+
+// Device error word codes (low byte, as in gemm_kernel.cuh); bits 8.. hold the CTA index.
+enum : uint32_t {
+    kRagErrEmpty = 1,
+    kRagErrFull = 2,
+    kRagErrAccEmpty = 3,
+    kRagErrAccFull = 4,
+    kRagErrDrain = 5,
+    kRagErrPartial = 6,
+    kRagErrRingDrain = 7,
+    kRagErrFixed = 10,   // the helper did not finish a stage in time
+    kRagErrTail = 11,    // a group's last K block did not arrive in time
+};
+
+struct RaggedParams {
+    CUtensorMap tm_p;     // M-side operand
+    CUtensorMap tm_q;     // N-side operand
+    CUtensorMap tm_x;     // kTN: the output; kLoraY: the adapters' b
+    const int32_t *offsets;  // [groups + 1] row offsets (kNT, kNN, kTN)
+    uint32_t groups;         // groups, or row tiles (kLoraU, kLoraY)
+    uint32_t rows;           // rows t
+    uint32_t pdim;           // extent on the M side
+    uint32_t qdim;           // kTN: extent on the N side
+    uint32_t kdim;           // contraction extent (not kTN)
+    uint32_t k_blocks;       // ceil(kdim / 64)
+    uint32_t tiles_p;        // tiles along the M side
+    uint32_t tiles_q;        // kTN, kLoraY: tiles along the N side
+    uint32_t per;            // kLoraU, kLoraY: rows of a row tile
+    uint32_t band;           // N-side tiles walked together before the M side advances
+    uint32_t sk;             // 1: equal runs of K-block iterations
+    uint32_t bf16;           // operand type: 0 fp16, 1 bf16
+    uint32_t out32;          // kTN: 1 = fp32 output
+    void *out;
+    const int32_t *ids;      // kLoraU, kLoraY: adapter of each row
+    const int32_t *counts;   // adapters present in each row tile
+    const int32_t *list;     // their numbers, `per` slots a row tile
+    const float *scale;      // per adapter, or null
+    const void *u;           // kLoraY: u [rows, rank]
+    uint32_t rank;
+    uint32_t rank_blocks;    // ceil(rank / 64)
+    float *partials;         // sk: one 128 x QCAP fp32 tile per CTA
+    uint64_t *flags;         // sk: one per CTA, `stamp` while its partial waits to be added
+    uint64_t stamp;
+    uint32_t skip_fill;      // test hook: ring fill of CTA 0 left undone (~0u: none)
+    long long wait_limit;
+    uint32_t *error_word;
+};
+
+template <int MODE, int CG, int QCAP, int STAGES>
+struct RaggedCfg {
+    static_assert(CG == 1 || CG == 2, "cta group");
+    static constexpr bool kPMn = (MODE == kNN || MODE == kTN);  // M-side operand MN-major
+    static constexpr bool kQMn = (MODE == kTN);                 // N-side operand MN-major
+    static constexpr bool kHelper = (MODE == kTN || MODE == kLoraY);
+    static constexpr int kQCta = QCAP / CG;                     // N-side extent in one CTA's stage
+    // rows per N-side box: small tiles load few rows past their own
+    static constexpr int kQBox = kQMn ? 64 : (kQCta <= 64 ? 16 : 32);
+    static constexpr int kQBoxBytes = kQMn ? 8192 : kQBox * 128;
+    static constexpr int kPBytes = 128 * 128;
+    static constexpr int kQBytes = kQCta * 128;
+    static constexpr int kStep = 16 * CG;                       // granularity of the instruction's N
+    static constexpr int kOffP = 0;
+    static constexpr int kOffQ = STAGES * kPBytes;
+    static constexpr int kOffStore = kOffQ + STAGES * kQBytes;  // per epilogue warp
+    static constexpr int kStoreBytes = (MODE == kTN) ? 4096 : 2048;
+    static constexpr int kOffTabRow = kOffStore + kRagEpiWarps * kStoreBytes;
+    static constexpr int kOffTabTile = kOffTabRow + 4 * (kRagMaxGroups + 4);
+    // full, empty, fixed, tail per stage; acc_full x2, acc_empty x2, drain, bad_free x2
+    static constexpr int kNumBars = 4 * STAGES + 7;
+    // kLoraY: for each of two tiles in flight, 128 bits per adapter of the tile (b rows that hold an infinity or
+    // NaN), and whether there are any
+    static constexpr int kOffBad = kOffTabTile + 4 * (kRagMaxGroups + 4);
+    static constexpr int kBadBytes = (MODE == kLoraY) ? QCAP * 16 : 0;
+    static constexpr int kOffBar = kOffBad + 2 * kBadBytes;
+    // last fill of each stage: its number + 1, this CTA's bytes, the bytes armed, 1 if it went to the tail barrier
+    static constexpr int kOffRec = kOffBar + kNumBars * 8;
+    static constexpr int kOffTmemSlot = kOffRec + STAGES * 16;
+    static constexpr int kOffAbort = kOffTmemSlot + 4;
+    static constexpr int kOffAnyBad = kOffAbort + 4;
+    static constexpr int kSmemBytes = kOffAnyBad + 8 + 1024;
+    static constexpr int kTmemCols = 2 * QCAP < 32 ? 32 : 2 * QCAP;
+    static_assert(kQBytes % 1024 == 0 && kOffBar % 8 == 0, "layout");
+    static_assert(kSmemBytes <= kRagMaxSmem, "shared memory budget");
+    static_assert(QCAP % (32 * CG) == 0 && QCAP <= 256, "N side");
+    static_assert(!kQMn || kQCta % 64 == 0, "whole 64-column atoms");
+};
+
+// One run of K blocks [lo, hi) of a tile.
+struct RaggedSeg {
+    uint32_t tile;
+    uint32_t g;       // group (kNT, kNN, kTN), row tile (kLoraU, kLoraY)
+    uint32_t p0;      // M-side origin of the tile (of the pair)
+    uint32_t q0;      // first row (kTN: column) on the N side
+    uint32_t qn;      // rows (columns) of the tile that count
+    uint32_t nq;      // the instruction's N
+    uint32_t row0;    // kTN: first row of the group; kLoraU: the adapter
+    uint32_t krows;   // kTN: rows of the group
+    uint32_t kb;      // K blocks of the whole tile
+    uint32_t lo, hi;
+};
+
+template <int MODE, int CG, int QCAP>
+struct RaggedWalk {
+    const RaggedParams &p;
+    const int32_t *tab_row;    // offsets (groups + 1), or counts per row tile
+    const uint32_t *tab_tile;  // tiles before each group (groups + 1)
+    uint32_t worker, workers, total;
+
+    __device__ __forceinline__ void decode(uint32_t u, RaggedSeg &s) const
+    {
+        constexpr uint32_t kStep = 16u * CG;
+        s.tile = u;
+        if constexpr (MODE == kLoraY) {
+            uint32_t pi, qi;
+            raster(u, p.tiles_q, pi, qi);
+            s.g = qi;
+            s.p0 = pi * 128u * CG;
+            s.q0 = qi * p.per;
+            s.qn = min(p.per, p.rows - s.q0);
+            s.row0 = 0;
+            s.kb = p.k_blocks + uint32_t(tab_row[qi]) * p.rank_blocks;
+        } else {
+            uint32_t lo = 0, hi = p.groups;  // tab_tile[lo] <= u < tab_tile[hi]
+            while (hi - lo > 1u) {
+                const uint32_t mid = (lo + hi) >> 1;
+                if (tab_tile[mid] <= u) lo = mid;
+                else hi = mid;
+            }
+            s.g = lo;
+            const uint32_t local = u - tab_tile[lo];
+            s.kb = p.k_blocks;
+            if constexpr (MODE == kLoraU) {
+                s.p0 = 0;
+                s.q0 = lo * p.per;
+                s.qn = min(p.per, p.rows - s.q0);
+                s.row0 = uint32_t(p.list[size_t(lo) * p.per + local]);
+            } else {
+                const uint32_t r0 = uint32_t(tab_row[lo]);
+                const uint32_t rows = uint32_t(tab_row[lo + 1]) - r0;
+                uint32_t pi, qi;
+                if constexpr (MODE == kTN) {
+                    raster(local, p.tiles_q, pi, qi);
+                    s.q0 = qi * QCAP;
+                    s.qn = min(uint32_t(QCAP), p.qdim - s.q0);
+                    s.row0 = r0;
+                    s.krows = rows;
+                    s.kb = (rows + kRagBlockK - 1u) / kRagBlockK;
+                } else {
+                    const uint32_t tq = (rows + QCAP - 1u) / QCAP;
+                    const uint32_t each = ((rows + tq - 1u) / tq + kStep - 1u) / kStep * kStep;
+                    raster(local, tq, pi, qi);
+                    s.q0 = r0 + qi * each;
+                    s.qn = min(each, r0 + rows - s.q0);
+                    s.row0 = r0;
+                }
+                s.p0 = pi * 128u * CG;
+            }
+        }
+        s.nq = (s.qn + kStep - 1u) / kStep * kStep;
+    }
+
+    // tile `t` of a tiles_p x tq grid, walked in bands of `band` N-side tiles, N side fastest
+    __device__ __forceinline__ void raster(uint32_t t, uint32_t tq, uint32_t &pi, uint32_t &qi) const
+    {
+        if (tq <= p.band) {
+            pi = t / tq;
+            qi = t - pi * tq;
+            return;
+        }
+        const uint32_t full = p.band * p.tiles_p;
+        const uint32_t b = t / full;
+        const uint32_t r = t - b * full;
+        const uint32_t w = min(p.band, tq - b * p.band);
+        pi = r / w;
+        qi = b * p.band + (r - pi * w);
+    }
+
+    __device__ __forceinline__ uint64_t run_begin(uint32_t w, uint64_t iters) const
+    {
+        return uint64_t(w) * iters / workers;
+    }
+
+    // f(seg) returns false to stop early (abort)
+    template <class F>
+    __device__ __forceinline__ void each(F &&f) const
+    {
+        RaggedSeg s;
+        if (MODE == kTN || !p.sk) {
+            for (uint32_t u = worker; u < total; u += workers) {
+                decode(u, s);
+                s.lo = 0;
+                s.hi = s.kb;
+                if (!f(s)) return;
+            }
+            return;
+        }
+        if (total == 0) return;
+        decode(0, s);
+        const uint32_t kb = s.kb;  // the same for every tile (kLoraY: there is one row tile)
+        const uint64_t iters = uint64_t(total) * kb;
+        const uint64_t begin = run_begin(worker, iters);
+        uint64_t it = run_begin(worker + 1, iters);
+        while (it > begin) {
+            const uint32_t u = uint32_t((it - 1u) / kb);
+            const uint64_t start = uint64_t(u) * kb;
+            decode(u, s);
+            s.lo = begin > start ? uint32_t(begin - start) : 0u;
+            s.hi = uint32_t(it - start);
+            if (!f(s)) return;
+            it = start + s.lo;
+        }
+    }
+};
+
+template <int CG>
+__device__ __forceinline__ bool ragged_wait(uint32_t bar, uint32_t parity, const RaggedParams &p,
+                                            volatile uint32_t *abort_flag, uint32_t code)
+{
+    auto try_once = [&]() {
+        if constexpr (CG > 1) return ptx::mbar_try_wait_cluster(bar, parity);
+        else return ptx::mbar_try_wait(bar, parity);
+    };
+    if (try_once()) return true;
+    const long long t0 = clock64();
+    for (uint32_t it = 1;; ++it) {
+        if (try_once()) return true;
+        if ((it & 31u) == 0) {
+            if (*abort_flag) return false;
+            if (clock64() - t0 > p.wait_limit) {
+                *abort_flag = 1u;
+                atomicCAS(p.error_word, 0u, code | (blockIdx.x << 8));
+                return false;
+            }
+        }
+    }
+}
+
+__device__ __forceinline__ uint32_t ragged_pack(float lo, float hi, bool bf16)
+{
+    if (bf16) {
+        __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+        return *reinterpret_cast<uint32_t *>(&h);
+    }
+    __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<uint32_t *>(&h);
+}
+
+// The group table: row offsets clamped to [0, rows] and made monotone (offsets that are not can
+// then reach no other memory), and the number of tiles before each group.  Run by the whole CTA.
+template <int MODE, int QCAP>
+__device__ __forceinline__ void ragged_table(const RaggedParams &p, int32_t *tab_row, uint32_t *tab_tile)
+{
+    constexpr bool kOffsets = (MODE == kNT || MODE == kNN || MODE == kTN);
+    const uint32_t n = p.groups + (kOffsets ? 1u : 0u);
+    for (uint32_t i = threadIdx.x; i < n; i += blockDim.x) {
+        int32_t v = kOffsets ? p.offsets[i] : p.counts[i];
+        if (kOffsets) v = max(0, min(v, int32_t(p.rows)));
+        tab_row[i] = v;
+    }
+    __syncthreads();
+    if (threadIdx.x < 32u && MODE != kLoraY) {
+        const uint32_t lane = threadIdx.x;
+        if constexpr (kOffsets) {
+            const uint32_t c = (n + 31u) / 32u, b = min(lane * c, n), e = min(b + c, n);
+            int32_t top = 0;
+            for (uint32_t i = b; i < e; ++i) top = max(top, tab_row[i]);
+            int32_t before = top;
+#pragma unroll
+            for (int d = 1; d < 32; d <<= 1) {
+                const int32_t o = __shfl_up_sync(0xffffffffu, before, d);
+                if (lane >= uint32_t(d)) before = max(before, o);
+            }
+            before = __shfl_up_sync(0xffffffffu, before, 1);
+            if (lane == 0) before = 0;
+            for (uint32_t i = b; i < e; ++i) {
+                before = max(before, tab_row[i]);
+                tab_row[i] = before;
+            }
+            __syncwarp();
+        }
+        auto tiles = [&](uint32_t g) -> uint32_t {
+            if constexpr (MODE == kLoraU) return uint32_t(tab_row[g]);
+            const uint32_t rows = uint32_t(tab_row[g + 1] - tab_row[g]);
+            if constexpr (MODE == kTN) return rows ? p.tiles_p * p.tiles_q : 0u;
+            else return (rows + QCAP - 1u) / QCAP * p.tiles_p;
+        };
+        const uint32_t c = (p.groups + 31u) / 32u, b = min(lane * c, p.groups), e = min(b + c, p.groups);
+        uint32_t sum = 0;
+        for (uint32_t i = b; i < e; ++i) sum += tiles(i);
+        uint32_t before = sum;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const uint32_t o = __shfl_up_sync(0xffffffffu, before, d);
+            if (lane >= uint32_t(d)) before += o;
+        }
+        before -= sum;
+        for (uint32_t i = b; i < e; ++i) {
+            tab_tile[i] = before;
+            before += tiles(i);
+        }
+        if (lane == 31u) tab_tile[p.groups] = before;
+    }
+    __syncthreads();
+}
+
+// After an abort: wait (bounded) until no copy into this CTA's ring, or armed on its barriers, is in
+// flight.  Run by one thread of each CTA between the teardown's two cluster barriers; `own` and
+// `peer` point at the two CTAs' fill records (peer 0: none).  The pair's first CTA owns the full
+// barriers; a tail fill lands on its own CTA's tail barrier.
+template <int STAGES, int CG>
+__device__ __noinline__ void ragged_drain(uint32_t bars, uint32_t rec, bool leader, const RaggedParams &p)
+{
+    auto wait = [&](uint32_t bar, uint32_t parity) {
+        const long long t0 = clock64();
+        while (!ptx::mbar_try_wait(bar, parity)) {
+            if (clock64() - t0 > p.wait_limit) {
+                atomicCAS(p.error_word, 0u, kRagErrRingDrain | (blockIdx.x << 8));
+                break;
+            }
+        }
+    };
+    for (uint32_t s = 0; s < uint32_t(STAGES); ++s) {
+        const uint32_t a = rec + 16u * s;
+        const uint32_t mine = ptx::ld_shared_cluster_u32(ptx::map_to_rank(a, ptx::cluster_ctarank()));
+        const uint32_t own_rank = ptx::cluster_ctarank();
+        const uint32_t my_bytes = ptx::ld_shared_cluster_u32(ptx::map_to_rank(a + 4u, own_rank));
+        const uint32_t my_armed = ptx::ld_shared_cluster_u32(ptx::map_to_rank(a + 8u, own_rank));
+        const uint32_t my_tail = ptx::ld_shared_cluster_u32(ptx::map_to_rank(a + 12u, own_rank));
+        if (mine && (my_tail & 1u)) wait(bars + 8u * (3u * STAGES + s), my_tail >> 1);
+        if (!leader) continue;
+        uint32_t other = 0, other_bytes = 0, other_tail = 0;
+        if constexpr (CG == 2) {
+            other = ptx::ld_shared_cluster_u32(ptx::map_to_rank(a, 1u));
+            other_bytes = ptx::ld_shared_cluster_u32(ptx::map_to_rank(a + 4u, 1u));
+            other_tail = ptx::ld_shared_cluster_u32(ptx::map_to_rank(a + 12u, 1u));
+        }
+        const uint32_t bar = bars + 8u * s;
+        if (mine >= other) {
+            if (!mine || (my_tail & 1u)) continue;
+            const uint32_t landing = my_bytes + (other == mine ? other_bytes : 0u);
+            if (my_armed > landing) ptx::mbar_complete_tx(bar, my_armed - landing);
+            wait(bar, ((mine - 1u) / STAGES) & 1u);
+        } else if (!(other_tail & 1u)) {
+            ptx::mbar_arrive_expect_tx(bar, other_bytes);
+            wait(bar, ((other - 1u) / STAGES) & 1u);
+        }
+    }
+}
+
+template <int MODE, int CG, int QCAP, int STAGES>
+__global__ void __launch_bounds__(kRagThreads, 1) gemm_ragged_kernel(const __grid_constant__ RaggedParams p)
+{
+    using Cfg = RaggedCfg<MODE, CG, QCAP, STAGES>;
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    const uint32_t raw = ptx::smem_addr(smem_raw);
+    const uint32_t base = (raw + 1023u) & ~1023u;
+    uint8_t *smem = smem_raw + (base - raw);
+
+    const uint32_t warp = threadIdx.x >> 5;
+    const uint32_t lane = threadIdx.x & 31u;
+    const uint32_t rank = (CG == 2) ? ptx::cluster_ctarank() : 0u;
+    const bool leader = (rank == 0);
+
+    auto bar_full = [&](uint32_t s) { return base + Cfg::kOffBar + 8u * s; };
+    auto bar_empty = [&](uint32_t s) { return base + Cfg::kOffBar + 8u * (STAGES + s); };
+    auto bar_fixed = [&](uint32_t s) { return base + Cfg::kOffBar + 8u * (2 * STAGES + s); };
+    auto bar_tail = [&](uint32_t s) { return base + Cfg::kOffBar + 8u * (3 * STAGES + s); };
+    auto bar_acc_full = [&](uint32_t b) { return base + Cfg::kOffBar + 8u * (4 * STAGES + b); };
+    auto bar_acc_empty = [&](uint32_t b) { return base + Cfg::kOffBar + 8u * (4 * STAGES + 2 + b); };
+    const uint32_t bar_drain = base + Cfg::kOffBar + 8u * (4 * STAGES + 4);
+    auto bar_bad_free = [&](uint32_t b) { return base + Cfg::kOffBar + 8u * (4 * STAGES + 5 + b); };
+    volatile uint32_t *any_bad = reinterpret_cast<volatile uint32_t *>(smem + Cfg::kOffAnyBad);
+    volatile uint32_t *abort_flag = reinterpret_cast<volatile uint32_t *>(smem + Cfg::kOffAbort);
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + Cfg::kOffTmemSlot);
+    volatile uint32_t *rec = reinterpret_cast<volatile uint32_t *>(smem + Cfg::kOffRec);
+    int32_t *tab_row = reinterpret_cast<int32_t *>(smem + Cfg::kOffTabRow);
+    uint32_t *tab_tile = reinterpret_cast<uint32_t *>(smem + Cfg::kOffTabTile);
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < STAGES; ++s) {
+            ptx::mbar_init(bar_full(s), 1);
+            ptx::mbar_init(bar_empty(s), 1);
+            ptx::mbar_init(bar_fixed(s), CG);
+            ptx::mbar_init(bar_tail(s), 1);
+            rec[4 * s] = 0u;
+        }
+        for (int b = 0; b < 2; ++b) {
+            ptx::mbar_init(bar_acc_full(b), 1);
+            ptx::mbar_init(bar_acc_empty(b), kRagEpiWarps * CG);
+            ptx::mbar_init(bar_bad_free(b), kRagEpiWarps);
+        }
+        ptx::mbar_init(bar_drain, 1);
+        *abort_flag = 0u;
+        ptx::fence_mbar_init();
+        ptx::prefetch_tmap(&p.tm_p);
+        ptx::prefetch_tmap(&p.tm_q);
+        if (MODE == kTN || MODE == kLoraY) ptx::prefetch_tmap(&p.tm_x);
+    }
+    if (warp == 1) {
+        ptx::tmem_alloc<CG>(ptx::smem_addr(tmem_slot), Cfg::kTmemCols);
+        ptx::tmem_relinquish<CG>();
+    }
+    ptx::tc_fence_before_sync();
+    if constexpr (CG == 2) ptx::cluster_sync();
+    else __syncthreads();
+    ptx::tc_fence_after_sync();
+    const uint32_t tmem_base = *tmem_slot;
+    ptx::griddep_wait();
+    ragged_table<MODE, QCAP>(p, tab_row, tab_tile);
+
+    RaggedWalk<MODE, CG, QCAP> walk{p,
+                                    tab_row,
+                                    tab_tile,
+                                    blockIdx.x / CG,
+                                    gridDim.x / CG,
+                                    MODE == kLoraY ? p.tiles_p * p.tiles_q : tab_tile[p.groups]};
+
+    // K = 16 steps of K block kb that hold anything
+    auto steps_of = [&](const RaggedSeg &s, uint32_t kb) -> uint32_t {
+        uint32_t left;
+        if (MODE == kTN) left = s.krows - kb * kRagBlockK;
+        else if (MODE == kLoraY && kb >= p.k_blocks) left = p.rank - ((kb - p.k_blocks) % p.rank_blocks) * kRagBlockK;
+        else left = p.kdim - kb * kRagBlockK;
+        return min(4u, (left + 15u) / 16u);
+    };
+    // K blocks whose stage the helper has to finish
+    auto fixed_block = [&](const RaggedSeg &s, uint32_t kb) -> bool {
+        if (MODE == kTN) return kb + 1u == s.kb && (s.krows & 15u) != 0u;
+        if (MODE == kLoraY) return kb >= p.k_blocks;
+        return false;
+    };
+
+    if (warp == 0) {
+        // ------------------------------------------------ TMA producer
+        if (lane == 0) {
+            uint32_t stage = 0, phase = 0, fills = 0, tail_uses = 0;
+            walk.each([&](const RaggedSeg &s) {
+                const uint32_t hq = s.nq / CG;
+                const uint32_t boxes = (hq + Cfg::kQBox - 1u) / Cfg::kQBox;
+                const int32_t p0 = int32_t(s.p0 + rank * 128u);
+                const int32_t q0 = int32_t(s.q0 + rank * hq);
+                for (uint32_t kb = s.lo; kb < s.hi; ++kb, ++fills) {
+                    if (!ragged_wait<CG>(bar_empty(stage), phase ^ 1u, p, abort_flag, kRagErrEmpty)) return false;
+                    if (!(blockIdx.x == 0 && fills == p.skip_fill)) {
+                        const uint32_t p_dst = base + Cfg::kOffP + stage * Cfg::kPBytes;
+                        const uint32_t q_dst = base + Cfg::kOffQ + stage * Cfg::kQBytes;
+                        const bool fix = fixed_block(s, kb);
+                        const bool extra = (MODE == kLoraY) && fix;  // adapter block: only P comes by TMA
+                        const bool tail = fix;                       // to this CTA's own tail barrier
+                        const uint32_t bytes = Cfg::kPBytes + (extra ? 0u : boxes * Cfg::kQBoxBytes);
+                        rec[4 * stage + 1] = bytes;
+                        rec[4 * stage + 2] = bytes * CG;
+                        rec[4 * stage + 3] = tail ? 1u | (((tail_uses >> stage) & 1u) << 1) : 0u;
+                        rec[4 * stage] = fills + 1u;
+                        uint32_t fb = bar_full(stage);
+                        if (tail) {
+                            if (leader) ptx::mbar_arrive(fb);  // the MMA waits for `fixed` instead
+                            fb = bar_tail(stage);
+                            tail_uses ^= 1u << stage;
+                            ptx::mbar_arrive_expect_tx(fb, bytes);
+                        } else {
+                            if (leader) ptx::mbar_arrive_expect_tx(fb, bytes * CG);
+                            if (CG == 2) fb = ptx::map_to_rank(fb, 0u);
+                        }
+                        auto load = [&](uint32_t dst, const CUtensorMap *map, int32_t x, int32_t y, int32_t z) {
+                            if (CG == 2 && !tail) ptx::tma_load_3d_pair(dst, map, fb, x, y, z);
+                            else ptx::tma_load_3d(dst, map, fb, x, y, z);
+                        };
+                        const int32_t k0 = int32_t(kb * kRagBlockK);
+                        if constexpr (MODE == kTN) {
+                            const int32_t row = int32_t(s.row0) + k0;
+                            load(p_dst, &p.tm_p, p0, row, 0);
+                            load(p_dst + 8192u, &p.tm_p, p0 + 64, row, 0);
+                            for (uint32_t b = 0; b < boxes; ++b)
+                                load(q_dst + b * 8192u, &p.tm_q, q0 + int32_t(64u * b), row, 0);
+                        } else if (extra) {
+                            const uint32_t e = kb - p.k_blocks;
+                            const uint32_t slot = e / p.rank_blocks;
+                            const int32_t adapter = p.list[size_t(s.g) * p.per + slot];
+                            load(p_dst, &p.tm_x, int32_t((e - slot * p.rank_blocks) * kRagBlockK), p0, adapter);
+                        } else {
+                            if constexpr (MODE == kNN) {
+                                load(p_dst, &p.tm_p, p0, k0, int32_t(s.g));
+                                load(p_dst + 8192u, &p.tm_p, p0 + 64, k0, int32_t(s.g));
+                            } else {
+                                const int32_t z = MODE == kNT ? int32_t(s.g) : MODE == kLoraU ? int32_t(s.row0) : 0;
+                                load(p_dst, &p.tm_p, k0, p0, z);
+                            }
+                            for (uint32_t b = 0; b < boxes; ++b)
+                                load(q_dst + b * Cfg::kQBoxBytes, &p.tm_q, k0, q0 + int32_t(b * Cfg::kQBox), 0);
+                        }
+                    }
+                    if (++stage == STAGES) {
+                        stage = 0;
+                        phase ^= 1u;
+                    }
+                }
+                return true;
+            });
+        }
+    } else if (warp == 1) {
+        // ------------------------------------------------ MMA issuer
+        if (leader && lane == 0) {
+            const uint32_t idesc0 = ragged_idesc(128u * CG, p.bf16 != 0u, Cfg::kPMn, Cfg::kQMn);
+            constexpr uint64_t kPStep = Cfg::kPMn ? (2048u >> 4) : 2u;  // K = 16 inside a swizzle atom, or two 8-row groups
+            constexpr uint64_t kQStep = Cfg::kQMn ? (2048u >> 4) : 2u;
+            uint32_t stage = 0, phase = 0, acc = 0, acc_phase = 0, fixed_uses = 0;
+            walk.each([&](const RaggedSeg &s) {
+                if (!ragged_wait<CG>(bar_acc_empty(acc), acc_phase ^ 1u, p, abort_flag, kRagErrAccEmpty)) return false;
+                ptx::tc_fence_after_sync();
+                const uint32_t d_tmem = tmem_base + acc * uint32_t(QCAP);
+                const uint32_t idesc = idesc0 | ragged_idesc_n(s.nq);
+                for (uint32_t kb = s.lo; kb < s.hi; ++kb) {
+                    if (!ragged_wait<CG>(bar_full(stage), phase, p, abort_flag, kRagErrFull)) return false;
+                    if (Cfg::kHelper && fixed_block(s, kb)) {
+                        if (!ragged_wait<CG>(bar_fixed(stage), (fixed_uses >> stage) & 1u, p, abort_flag, kRagErrFixed))
+                            return false;
+                        fixed_uses ^= 1u << stage;
+                    }
+                    ptx::tc_fence_after_sync();
+                    const uint64_t p_desc = ragged_desc(base + Cfg::kOffP + stage * Cfg::kPBytes, Cfg::kPMn);
+                    const uint64_t q_desc = ragged_desc(base + Cfg::kOffQ + stage * Cfg::kQBytes, Cfg::kQMn);
+                    const uint32_t steps = steps_of(s, kb);
+#pragma unroll
+                    for (uint32_t kk = 0; kk < 4u; ++kk)
+                        if (kk < steps)
+                            ptx::mma_f16<CG>(d_tmem, p_desc + kPStep * kk, q_desc + kQStep * kk, idesc,
+                                             (kb != s.lo || kk != 0u) ? 1u : 0u);
+                    if constexpr (CG == 1) ptx::mma_commit(bar_empty(stage));
+                    else ptx::mma_commit_pair(bar_empty(stage), uint16_t(3u));
+                    if (++stage == STAGES) {
+                        stage = 0;
+                        phase ^= 1u;
+                    }
+                }
+                if constexpr (CG == 1) ptx::mma_commit(bar_acc_full(acc));
+                else ptx::mma_commit_pair(bar_acc_full(acc), uint16_t(3u));
+                if (++acc == 2u) {
+                    acc = 0;
+                    acc_phase ^= 1u;
+                }
+                return true;
+            });
+            // no MMA may still be running when the tensor memory is freed
+            if constexpr (CG == 1) ptx::mma_commit(bar_drain);
+            else ptx::mma_commit_pair(bar_drain, uint16_t(1u));
+            const long long t0 = clock64();
+            while (!ptx::mbar_try_wait(bar_drain, 0)) {
+                if (clock64() - t0 > p.wait_limit) {
+                    atomicCAS(p.error_word, 0u, kRagErrDrain | (blockIdx.x << 8));
+                    break;
+                }
+            }
+        }
+    } else if (warp < 6u) {
+        // ------------------------------------------------ epilogue
+        const uint32_t quarter = warp & 3u;  // tensor-memory lanes [32 quarter, +32)
+        const uint32_t buf = base + Cfg::kOffStore + quarter * Cfg::kStoreBytes;
+        const bool bf16 = p.bf16 != 0u;
+        const uint32_t esize = (MODE == kTN && p.out32) ? 4u : 2u;
+
+        // what no tile covers: rows in no group, and the gradients of groups without rows
+        {
+            const uint64_t first = uint64_t(blockIdx.x) * 128u + (threadIdx.x - 64u);
+            const uint64_t stride = uint64_t(gridDim.x) * 128u;
+            auto zero = [&](uint64_t from, uint64_t count) {  // 16-byte chunks
+                uint4 *dst = static_cast<uint4 *>(p.out) + from;
+                for (uint64_t i = first; i < count; i += stride) dst[i] = make_uint4(0u, 0u, 0u, 0u);
+            };
+            if constexpr (MODE == kNT || MODE == kNN) {
+                const uint64_t pitch = uint64_t(p.pdim) / 8u;
+                const uint32_t head = uint32_t(tab_row[0]), end = uint32_t(tab_row[p.groups]);
+                if (head) zero(0, head * pitch);
+                if (end < p.rows) zero(end * pitch, (p.rows - end) * pitch);
+            }
+            if constexpr (MODE == kTN) {
+                const uint64_t each = uint64_t(p.pdim) * p.qdim * esize / 16u;
+                for (uint32_t g = 0; g < p.groups; ++g)
+                    if (tab_row[g] == tab_row[g + 1]) zero(g * each, each);
+            }
+        }
+
+        uint32_t acc = 0, acc_phase = 0;
+        uint32_t adapted = 0;  // kLoraY: segments with adapter blocks so far
+        bool let_in = false;
+        walk.each([&](const RaggedSeg &s) {
+            const bool ok = ragged_wait<CG>(bar_acc_full(acc), acc_phase, p, abort_flag, kRagErrAccFull);
+            const bool split = MODE != kTN && p.sk != 0u && (s.lo != 0u || s.hi != s.kb);
+            // the four warps meet at named barriers below when the tile is split: stop together
+            if (MODE != kTN && p.sk) {
+                if (!ptx::named_barrier_and(1, 32 * kRagEpiWarps, ok)) return false;
+            } else if (!__all_sync(0xffffffffu, ok)) {
+                return false;
+            }
+            if (!let_in) {
+                ptx::griddep_launch_dependents();
+                let_in = true;
+            }
+            ptx::tc_fence_after_sync();
+            const uint32_t t_col = tmem_base + ((quarter * 32u) << 16) + acc * uint32_t(QCAP);
+            const uint32_t prow = s.p0 + rank * 128u + quarter * 32u;  // first M-side index of this warp
+            const uint32_t chunks = (s.nq + 31u) / 32u;
+            constexpr uint32_t kSlot = 128u * QCAP;
+            // partial tile in the workspace: warp quarter, 32-column chunk, then float4 j of every lane
+            const uint32_t piece = quarter * 32u * QCAP + lane * 4u;
+            // kLoraY: NaN for the rows whose own adapter holds an infinity or NaN in this lane's row of b
+            const bool has_adapters = MODE == kLoraY && s.hi > max(s.lo, p.k_blocks);
+            const uint32_t bad_buf = adapted & 1u;
+            const bool any = has_adapters && any_bad[bad_buf] != 0u;
+            if (has_adapters) ++adapted;
+            auto spoil = [&](uint32_t c, uint32_t (&r)[32]) {
+                if (!any) return;
+                const volatile uint32_t *mask = reinterpret_cast<const volatile uint32_t *>(smem + Cfg::kOffBad + bad_buf * Cfg::kBadBytes);
+                for (int32_t i = 0; i < tab_row[s.g]; ++i) {
+                    if (!((mask[4 * i + quarter] >> lane) & 1u)) continue;
+                    const int32_t adapter = p.list[size_t(s.g) * p.per + i];
+#pragma unroll
+                    for (uint32_t j = 0; j < 32u; ++j)
+                        if (32u * c + j < s.qn && p.ids[s.q0 + 32u * c + j] == adapter) r[j] = 0x7FC00000u;
+                }
+            };
+            auto release = [&]() {
+                if (has_adapters) {
+                    __syncwarp();
+                    if (lane == 0) ptx::mbar_arrive(bar_bad_free(bad_buf));
+                }
+                ptx::tc_fence_before_sync();
+                __syncwarp();
+                if (lane == 0) {
+                    if constexpr (CG == 1) ptx::mbar_arrive(bar_acc_empty(acc));
+                    else ptx::mbar_arrive_cluster_signal(ptx::map_to_rank(bar_acc_empty(acc), 0u));
+                }
+                if (++acc == 2u) {
+                    acc = 0;
+                    acc_phase ^= 1u;
+                }
+            };
+            const bool live = prow < p.pdim;
+
+            if (split && s.hi != s.kb) {
+                // ---- publish: the worker with the tile's last K block adds this partial
+                if (live) {
+                    float *slot = p.partials + size_t(blockIdx.x) * kSlot + piece;
+                    for (uint32_t c = 0; c < chunks; ++c) {
+                        uint32_t r[32];
+                        ptx::tmem_ld_32x32b_x32_wait(t_col + 32u * c, r);
+                        if (MODE == kLoraY) spoil(c, r);
+#pragma unroll
+                        for (int j = 0; j < 8; ++j)
+                            ptx::st_global_cg_f4(slot + c * 1024u + j * 128, __uint_as_float(r[4 * j]),
+                                                 __uint_as_float(r[4 * j + 1]), __uint_as_float(r[4 * j + 2]),
+                                                 __uint_as_float(r[4 * j + 3]));
+                    }
+                }
+                release();
+                __threadfence();
+                ptx::named_barrier_sync(1, 32 * kRagEpiWarps);
+                if (threadIdx.x == 64u) ptx::st_release_gpu_u64(p.flags + blockIdx.x, p.stamp);
+                return true;
+            }
+            uint32_t w_lo = walk.worker;  // workers [w_lo, worker) hold the tile's earlier K blocks
+            if (split) {
+                const uint64_t iters = uint64_t(walk.total) * s.kb;
+                const uint64_t start = uint64_t(s.tile) * s.kb;
+                while (w_lo > 0u && walk.run_begin(w_lo, iters) > start) --w_lo;
+                if (threadIdx.x == 64u) {
+                    for (uint32_t w = w_lo; w < walk.worker; ++w) {
+                        if (walk.run_begin(w, iters) == walk.run_begin(w + 1u, iters)) continue;
+                        uint64_t *flag = p.flags + w * CG + rank;
+                        const long long t0 = clock64();
+                        while (ptx::ld_acquire_gpu_u64(flag) != p.stamp) {
+                            if (*abort_flag || clock64() - t0 > p.wait_limit) {
+                                *abort_flag = 1u;
+                                atomicCAS(p.error_word, 0u, kRagErrPartial | (blockIdx.x << 8));
+                                break;
+                            }
+                        }
+                        // taken: a launch captured in a graph comes again with the same stamp
+                        ptx::st_release_gpu_u64(flag, 0u);
+                    }
+                }
+                ptx::named_barrier_sync(1, 32 * kRagEpiWarps);
+            }
+            // 32 columns of the finished tile: the accumulator plus the other workers' partials, lowest first
+            auto chunk32 = [&](uint32_t c, uint32_t (&r)[32]) {
+                ptx::tmem_ld_32x32b_x32_wait(t_col + 32u * c, r);
+                if (MODE == kLoraY) spoil(c, r);
+                if (MODE != kTN && split) {
+                    const uint64_t iters = uint64_t(walk.total) * s.kb;
+                    for (uint32_t w = w_lo; w < walk.worker; ++w) {
+                        if (walk.run_begin(w, iters) == walk.run_begin(w + 1u, iters)) continue;
+                        const float *src = p.partials + size_t(w * CG + rank) * kSlot + piece + c * 1024u;
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) {
+                            const float4 v = ptx::ld_global_cg_f4(src + j * 128);
+                            r[4 * j] = __float_as_uint(__uint_as_float(r[4 * j]) + v.x);
+                            r[4 * j + 1] = __float_as_uint(__uint_as_float(r[4 * j + 1]) + v.y);
+                            r[4 * j + 2] = __float_as_uint(__uint_as_float(r[4 * j + 2]) + v.z);
+                            r[4 * j + 3] = __float_as_uint(__uint_as_float(r[4 * j + 3]) + v.w);
+                        }
+                    }
+                }
+            };
+            if constexpr (MODE == kTN) {
+                // rows of dw[g] on lanes: boxes of 32 rows x 128 bytes through the swizzled staging buffer
+                if (live) {
+                    const uint32_t step = p.out32 ? 1u : 2u;  // 32-column chunks per box
+                    for (uint32_t c = 0; c < chunks; c += step) {
+                        const uint32_t col = s.q0 + 32u * c;
+                        uint32_t w[32];
+                        if (p.out32) {
+                            ptx::tmem_ld_32x32b_x32_wait(t_col + 32u * c, w);
+                        } else {
+#pragma unroll
+                            for (int h = 0; h < 2; ++h) {
+                                uint32_t r[32];
+                                ptx::tmem_ld_32x32b_x32_wait(t_col + 32u * (c + h), r);
+#pragma unroll
+                                for (int j = 0; j < 16; ++j)
+                                    w[16 * h + j] = ragged_pack(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1]), bf16);
+                            }
+                        }
+                        if (lane == 0) ptx::bulk_wait_group_read<0>();
+                        __syncwarp();
+#pragma unroll
+                        for (int j = 0; j < 8; ++j)
+                            ptx::st_shared_v4(buf + lane * 128u + ((uint32_t(j) ^ (lane & 7u)) << 4), w[4 * j], w[4 * j + 1],
+                                              w[4 * j + 2], w[4 * j + 3]);
+                        ptx::fence_proxy_async_smem();
+                        __syncwarp();
+                        if (lane == 0) {
+                            ptx::tma_store_3d(&p.tm_x, buf, int32_t(col), int32_t(prow), int32_t(s.g));
+                            ptx::bulk_commit_group();
+                        }
+                    }
+                }
+                release();
+            } else {
+                // rows t on columns: 32 x 32 pieces transposed through shared memory.  A word holds rows
+                // 2i and 2i + 1 of one output column; a lane reads four columns' words and takes them apart.
+                if (live) {
+                    const float mul = (MODE == kLoraU && p.scale) ? p.scale[s.row0] : 1.0f;
+                    char *out = static_cast<char *>(p.out);
+                    const uint32_t col = prow + 4u * (lane & 7u);
+                    for (uint32_t c = 0; c < chunks; ++c) {
+                        uint32_t r[32];
+                        chunk32(c, r);
+                        __syncwarp();
+#pragma unroll
+                        for (int i = 0; i < 16; ++i)
+                            ptx::st_shared_u32(buf + uint32_t(i) * 128u + lane * 4u,
+                                               ragged_pack(__uint_as_float(r[2 * i]) * mul, __uint_as_float(r[2 * i + 1]) * mul,
+                                                           bf16));
+                        __syncwarp();
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const uint32_t pr = uint32_t(i) * 4u + (lane >> 3);
+                            const uint4 v = ptx::ld_shared_v4(buf + pr * 128u + (lane & 7u) * 16u);
+                            const uint32_t row = 32u * c + 2u * pr;  // in the tile
+                            if (col < p.pdim) {
+#pragma unroll
+                                for (uint32_t h = 0; h < 2u; ++h) {
+                                    if (row + h >= s.qn) continue;
+                                    if (MODE == kLoraU && p.ids[s.q0 + row + h] != int32_t(s.row0)) continue;
+                                    const uint32_t sel = h ? 0x7632u : 0x5410u;
+                                    ptx::st_global_v2(out + (size_t(s.q0 + row + h) * p.pdim + col) * 2u,
+                                                      __byte_perm(v.x, v.y, sel), __byte_perm(v.z, v.w, sel));
+                                }
+                            }
+                        }
+                    }
+                }
+                release();
+            }
+            return true;
+        });
+        if (MODE == kTN && lane == 0) ptx::bulk_wait_group<0>();
+    } else if constexpr (Cfg::kHelper) {
+        // ------------------------------------------------ helper
+        const uint32_t tid = threadIdx.x - 192u;
+        uint32_t fills = 0, tail_uses = 0, adapted = 0;
+        // every helper thread waits on the barrier itself; they leave together
+        auto wait_all = [&](bool ok) { return ptx::named_barrier_and(2, kRagHelpers, ok); };
+        walk.each([&](const RaggedSeg &s) {
+            const uint32_t hq = s.nq / CG;
+            const uint32_t first = fills;
+            fills += s.hi - s.lo;
+            auto hand_over = [&](uint32_t stage) {
+                ptx::fence_proxy_async_smem();
+                ptx::named_barrier_sync(2, kRagHelpers);
+                if (tid == 0) {
+                    if constexpr (CG == 1) ptx::mbar_arrive(bar_fixed(stage));
+                    else ptx::mbar_arrive_cluster(ptx::map_to_rank(bar_fixed(stage), 0u));
+                }
+            };
+            if constexpr (MODE == kTN) {
+                if (!fixed_block(s, s.kb - 1u)) return true;
+                const uint32_t stage = (fills - 1u) % STAGES;
+                if (!wait_all(ragged_wait<1>(bar_tail(stage), (tail_uses >> stage) & 1u, p, abort_flag, kRagErrTail)))
+                    return false;
+                tail_uses ^= 1u << stage;
+                const uint32_t from = s.krows % kRagBlockK, to = (from + 15u) & ~15u;
+                const uint32_t boxes = (hq + 63u) / 64u;
+                const uint32_t lines = (to - from) * 8u;  // 16-byte pieces of the rows to clear, per 64-column box
+                for (uint32_t i = tid; i < lines * (2u + boxes); i += kRagHelpers) {
+                    const uint32_t b = i / lines;
+                    const uint32_t at = (b < 2u ? base + Cfg::kOffP + stage * Cfg::kPBytes + b * 8192u
+                                                : base + Cfg::kOffQ + stage * Cfg::kQBytes + (b - 2u) * 8192u) +
+                                        from * 128u + (i - b * lines) * 16u;
+                    ptx::st_shared_v4(at, 0u, 0u, 0u, 0u);
+                }
+                hand_over(stage);
+            } else {
+                // adapter blocks: rows of this CTA's part of the tile, u where the row has the slot's adapter
+                const uint32_t row0 = s.q0 + rank * hq;
+                int32_t id[(Cfg::kQCta + kRagHelpers - 1) / kRagHelpers];
+#pragma unroll
+                for (uint32_t i = 0; i < sizeof(id) / sizeof(id[0]); ++i) {
+                    const uint32_t t = tid + i * kRagHelpers;
+                    id[i] = (t < hq && rank * hq + t < s.qn) ? p.ids[row0 + t] : -1;
+                }
+                if (s.hi <= max(s.lo, p.k_blocks)) return true;
+                // the table of b rows with infinities is free once the epilogue is done with the tile before last
+                const uint32_t bad_buf = adapted & 1u;
+                if (!wait_all(ragged_wait<1>(bar_bad_free(bad_buf), ((adapted >> 1) & 1u) ^ 1u, p, abort_flag, kRagErrFixed)))
+                    return false;
+                ++adapted;
+                uint32_t *mask = reinterpret_cast<uint32_t *>(smem + Cfg::kOffBad + bad_buf * Cfg::kBadBytes);
+                for (uint32_t i = tid; i < Cfg::kBadBytes / 4u; i += kRagHelpers) mask[i] = 0u;
+                if (tid == 0) any_bad[bad_buf] = 0u;
+                ptx::named_barrier_sync(2, kRagHelpers);
+                const uint32_t expo = p.bf16 ? 0x7F80u : 0x7C00u;  // all ones: infinity or NaN
+                for (uint32_t kb = max(s.lo, p.k_blocks); kb < s.hi; ++kb) {
+                    const uint32_t f = first + (kb - s.lo);
+                    const uint32_t stage = f % STAGES;
+                    // b has landed, so the stage is free: the producer waited for that.  (The stage's empty barrier
+                    // cannot be waited for here: it may be more than one phase away.)
+                    if (!wait_all(ragged_wait<1>(bar_tail(stage), (tail_uses >> stage) & 1u, p, abort_flag, kRagErrTail)))
+                        return false;
+                    tail_uses ^= 1u << stage;
+                    const uint32_t e = kb - p.k_blocks;
+                    const uint32_t slot = e / p.rank_blocks;
+                    const uint32_t r0 = (e - slot * p.rank_blocks) * kRagBlockK;
+                    const int32_t adapter = p.list[size_t(s.g) * p.per + slot];
+                    const uint32_t chunks = 2u * steps_of(s, kb);
+                    const uint32_t q_at = base + Cfg::kOffQ + stage * Cfg::kQBytes;
+#pragma unroll
+                    for (uint32_t i = 0; i < sizeof(id) / sizeof(id[0]); ++i) {
+                        const uint32_t t = tid + i * kRagHelpers;
+                        if (t >= hq) continue;
+                        const bool mine = id[i] == adapter;
+                        const uint4 *src = reinterpret_cast<const uint4 *>(static_cast<const char *>(p.u) +
+                                                                           (size_t(row0 + t) * p.rank + r0) * 2u);
+                        for (uint32_t c = 0; c < chunks; ++c) {
+                            const uint4 v = (mine && r0 + 8u * c < p.rank) ? src[c] : make_uint4(0u, 0u, 0u, 0u);
+                            ptx::st_shared_v4(q_at + t * 128u + ((c ^ (t & 7u)) << 4), v.x, v.y, v.z, v.w);
+                        }
+                    }
+                    // b's rows: zeros for infinities and NaN, which the other adapters' zero rows of u would turn into NaN
+                    const uint32_t p_at = base + Cfg::kOffP + stage * Cfg::kPBytes;
+                    for (uint32_t t = tid; t < 128u; t += kRagHelpers) {
+                        for (uint32_t c = 0; c < chunks; ++c) {
+                            const uint32_t at = p_at + t * 128u + ((c ^ (t & 7u)) << 4);
+                            const uint4 v = ptx::ld_shared_v4(at);
+                            uint32_t w[4] = {v.x, v.y, v.z, v.w};
+                            bool bad = false;
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) {
+                                const bool lo = (w[j] & expo) == expo, hi = (w[j] & (expo << 16)) == (expo << 16);
+                                bad |= lo | hi;
+                                w[j] &= (lo ? 0xFFFF0000u : 0xFFFFFFFFu) & (hi ? 0x0000FFFFu : 0xFFFFFFFFu);
+                            }
+                            if (bad) {
+                                ptx::st_shared_v4(at, w[0], w[1], w[2], w[3]);
+                                atomicOr(mask + 4u * slot + (t >> 5), 1u << (t & 31u));
+                                any_bad[bad_buf] = 1u;
+                            }
+                        }
+                    }
+                    hand_over(stage);
+                }
+            }
+            return true;
+        });
+    }
+
+    // ---------------------------------------------------- teardown
+    ptx::griddep_launch_dependents();
+    __syncwarp();
+    ptx::tc_fence_before_sync();
+    if constexpr (CG == 2) ptx::cluster_sync();
+    else __syncthreads();
+    ptx::tc_fence_after_sync();
+    if (threadIdx.x == 0) {
+        bool aborted = *abort_flag != 0u;
+        if constexpr (CG == 2)
+            aborted = ptx::ld_shared_cluster_u32(ptx::map_to_rank(base + Cfg::kOffAbort, 0u)) != 0u ||
+                      ptx::ld_shared_cluster_u32(ptx::map_to_rank(base + Cfg::kOffAbort, 1u)) != 0u;
+        if (aborted) ragged_drain<STAGES, CG>(base + Cfg::kOffBar, base + Cfg::kOffRec, leader, p);
+    }
+    if constexpr (CG == 2) ptx::cluster_sync();
+    if (warp == 1) ptx::tmem_dealloc<CG>(tmem_base, Cfg::kTmemCols);
+}
+
+// The adapters present in each tile of `per` rows (per <= 256), in order of first appearance: one block per
+// tile.  Rows with an id outside [0, adapters) have none.
+__global__ void __launch_bounds__(256) lora_plan_kernel(const int32_t *ids, uint32_t rows, uint32_t per, uint32_t adapters,
+                                                        int32_t *counts, int32_t *list)
+{
+    __shared__ __align__(16) int32_t s_id[256];
+    __shared__ uint32_t s_warp[8];
+    ptx::griddep_wait();
+    const uint32_t t = threadIdx.x, row = blockIdx.x * per + t;
+    int32_t id = (t < per && row < rows) ? ids[row] : -1;
+    if (uint32_t(id) >= adapters) id = -1;
+    s_id[t] = id;
+    __syncthreads();
+    // the first row with its id: every earlier one differs (four at a time, the same words for the whole warp)
+    bool first = id >= 0;
+    for (uint32_t i = 0; i < (t | 31u) + 1u; i += 4u) {
+        const int4 v = *reinterpret_cast<const int4 *>(s_id + i);
+        first &= !((v.x == id && i < t) || (v.y == id && i + 1u < t) || (v.z == id && i + 2u < t) || (v.w == id && i + 3u < t));
+    }
+    const uint32_t vote = __ballot_sync(0xffffffffu, first);
+    if ((t & 31u) == 0) s_warp[t >> 5] = __popc(vote);
+    __syncthreads();
+    uint32_t at = __popc(vote & ((1u << (t & 31u)) - 1u)), total = 0;
+    for (uint32_t w = 0; w < 8u; ++w) {
+        if (w < (t >> 5)) at += s_warp[w];
+        total += s_warp[w];
+    }
+    if (first) list[size_t(blockIdx.x) * per + at] = id;
+    if (t == 0) counts[blockIdx.x] = int32_t(total);
+    ptx::griddep_launch_dependents();
+}
+
+}  // namespace gemm_f16

@@ -1,0 +1,93 @@
+// Inline-PTX wrappers and tensor-core descriptors that the ragged products
+// use beside ptx.cuh: three-dimensional TMA copies, and descriptors whose
+// operand types, majors and N are chosen at run time.  Written from the PTX
+// ISA description of each instruction.
+#pragma once
+
+#include "ptx.cuh"
+
+namespace gemm_f16 {
+namespace ptx {
+
+// 3-D tiled load global -> this CTA's shared memory, completing on the
+// barrier `bar` (this CTA).
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const void *tmap, uint32_t bar, int32_t x, int32_t y, int32_t z)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(tmap)), "r"(bar), "r"(x), "r"(y), "r"(z)
+        : "memory");
+}
+
+// Same, for a CTA pair: the completion barrier may live in either CTA of the
+// pair (`bar` is a shared::cluster address).
+__device__ __forceinline__ void tma_load_3d_pair(uint32_t dst, const void *tmap, uint32_t bar, int32_t x, int32_t y,
+                                                 int32_t z)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(tmap)), "r"(bar), "r"(x), "r"(y), "r"(z)
+        : "memory");
+}
+
+// 3-D tiled store shared -> global (elements outside the tensor are skipped).
+__device__ __forceinline__ void tma_store_3d(const void *tmap, uint32_t src, int32_t x, int32_t y, int32_t z)
+{
+    asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(
+                     reinterpret_cast<uint64_t>(tmap)),
+                 "r"(src), "r"(x), "r"(y), "r"(z)
+                 : "memory");
+}
+
+__device__ __forceinline__ void st_shared_u32(uint32_t addr, uint32_t v)
+{
+    asm volatile("st.shared.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
+
+__device__ __forceinline__ uint4 ld_shared_v4(uint32_t addr)
+{
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr)
+                 : "memory");
+    return v;
+}
+
+__device__ __forceinline__ void st_global_v2(void *p, uint32_t a, uint32_t b)
+{
+    asm volatile("st.global.v2.b32 [%0], {%1, %2};" ::"l"(p), "r"(a), "r"(b) : "memory");
+}
+
+}  // namespace ptx
+
+// tcgen05 shared-memory matrix descriptor of a tile that TMA wrote with
+// 128-byte swizzling (rows of 128 bytes, atoms of 8 rows = 1024 bytes).
+// K-major: atoms stacked along M/N at a stride byte offset of 1024, leading
+// byte offset unused.  MN-major: 64-element-wide columns of 64 K rows, the
+// leading byte offset (8 KB) steps between columns, the stride byte offset
+// (1 KB) between groups of 8 K rows.  Fields: start address >> 4 (bits 0-13),
+// leading >> 4 (16-29), stride >> 4 (32-45), version 1 (46-48), swizzle mode 2
+// (61-63); tiles are 1024-byte aligned.
+__device__ __forceinline__ uint64_t ragged_desc(uint32_t addr, bool mn_major)
+{
+    return uint64_t((addr & 0x3FFFFu) >> 4) | (uint64_t(mn_major ? (8192u >> 4) : 1u) << 16) |
+           (uint64_t(1024 >> 4) << 32) | (uint64_t(1) << 46) | (uint64_t(2) << 61);
+}
+
+// tcgen05 instruction descriptor, kind::f16, D fp32 (bits 4-5 = 1), without
+// N: A and B both fp16 (bits 7-9, 10-12 = 0) or both bf16 (= 1), A and B
+// K-major or MN-major (bits 15, 16), M >> 4 in bits 24-28.  ragged_idesc_n adds
+// N >> 3 in bits 17-22.
+__device__ __forceinline__ uint32_t ragged_idesc(uint32_t m, bool bf16, bool a_mn, bool b_mn)
+{
+    return (1u << 4) | (bf16 ? (1u << 7) | (1u << 10) : 0u) | (a_mn ? (1u << 15) : 0u) | (b_mn ? (1u << 16) : 0u) |
+           ((m >> 4) << 24);
+}
+
+__device__ __forceinline__ uint32_t ragged_idesc_n(uint32_t n)
+{
+    return (n >> 3) << 17;
+}
+
+}  // namespace gemm_f16
