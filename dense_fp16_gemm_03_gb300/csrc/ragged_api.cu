@@ -162,6 +162,16 @@ gemm_status_t encode_stack(CUtensorMap *map, const void *ptr, gemm_dtype_t dtype
     return r == CUDA_SUCCESS ? GEMM_OK : GEMM_ERR_UNSUPPORTED_SHAPE;
 }
 
+// The N-side operand [rows, cols] in boxes of `box` rows, half and a quarter of them.
+gemm_status_t encode_rows(CUtensorMap (&maps)[3], const void *ptr, gemm_dtype_t dtype, int64_t rows, int64_t cols, int box)
+{
+    for (int i = 0; i < 3; ++i) {
+        gemm_status_t st = encode_stack(&maps[i], ptr, dtype, 1, rows, cols, kRagBlockK, box >> i);
+        if (st != GEMM_OK) return st;
+    }
+    return GEMM_OK;
+}
+
 // ---------------------------------------------------------- validation
 
 gemm_status_t check_pointer(const void *p, bool used, uintptr_t align = 16)
@@ -329,11 +339,11 @@ gemm_status_t grouped(int mode, gemm_dtype_t dtype, gemm_dtype_t out_type, int64
     if (most >= kSizeLimit) return GEMM_ERR_UNSUPPORTED_SHAPE;
     if (mode == kTN) {
         st = encode_stack(&p.tm_p, first, dtype, 1, rows, n, 64, 64);
-        if (st == GEMM_OK) st = encode_stack(&p.tm_q, second, dtype, 1, rows, k, 64, 64);
+        if (st == GEMM_OK) st = encode_stack(&p.tm_q[0], second, dtype, 1, rows, k, 64, 64);
         if (st == GEMM_OK) st = encode_stack(&p.tm_x, out, out_type, groups, n, k, p.out32 ? 32 : 64, 32);
     } else {
         st = encode_stack(&p.tm_p, second, dtype, groups, n, k, 64, mode == kNT ? 128 : 64);
-        if (st == GEMM_OK) st = encode_stack(&p.tm_q, first, dtype, 1, rows, kdim, kRagBlockK, var.qbox);
+        if (st == GEMM_OK) st = encode_rows(p.tm_q, first, dtype, rows, kdim, var.qbox);
         if (ws && few_rows(groups, rows)) {
             use_split(&p, var, dev->slots[variant], ws);
             most *= p.k_blocks;
@@ -534,7 +544,7 @@ gemm_status_t gemm_lora_nt(gemm_dtype_t dtype, int64_t rows, int64_t n, int64_t 
             u.groups = uint32_t(tiles);
             u.rows = rr;
             u.ids = idr;
-            st = encode_stack(&u.tm_q, xr, dtype, 1, r, k, kRagBlockK, vu.qbox);
+            st = encode_rows(u.tm_q, xr, dtype, r, k, vu.qbox);
             if (st != GEMM_OK) return st;
             use_split(&u, vu, dev->slots[l.variant_u], ws + l.split);
             st = launch_ragged(l.variant_u, dev, u, r * int64_t(u.k_blocks), s);
@@ -545,7 +555,7 @@ gemm_status_t gemm_lora_nt(gemm_dtype_t dtype, int64_t rows, int64_t n, int64_t 
         p.rows = rr;
         p.ids = idr;
         p.out = static_cast<char *>(y) + size_t(r0) * size_t(n) * 2u;
-        st = encode_stack(&p.tm_q, xr, dtype, 1, r, k, kRagBlockK, vy.qbox);
+        st = encode_rows(p.tm_q, xr, dtype, r, k, vy.qbox);
         if (st != GEMM_OK) return st;
         int64_t most = int64_t(p.tiles_p) * tiles;
         p.sk = 0;

@@ -84,7 +84,7 @@ enum : uint32_t {
 
 struct RaggedParams {
     CUtensorMap tm_p;     // M-side operand
-    CUtensorMap tm_q;     // N-side operand
+    CUtensorMap tm_q[3];  // N-side operand: boxes of a stage's whole, half and quarter N side (kTN: the first, 64 columns)
     CUtensorMap tm_x;     // kTN: the output; kLoraY: the adapters' b
     const int32_t *offsets;  // [groups + 1] row offsets (kNT, kNN, kTN)
     uint32_t groups;         // groups, or row tiles (kLoraU, kLoraY)
@@ -123,9 +123,9 @@ struct RaggedCfg {
     static constexpr bool kQMn = (MODE == kTN);                 // N-side operand MN-major
     static constexpr bool kHelper = (MODE == kTN || MODE == kLoraY);
     static constexpr int kQCta = QCAP / CG;                     // N-side extent in one CTA's stage
-    // rows per N-side box: small tiles load few rows past their own
-    static constexpr int kQBox = kQMn ? 64 : (kQCta <= 64 ? 16 : 32);
-    static constexpr int kQBoxBytes = kQMn ? 8192 : kQBox * 128;
+    // rows of a whole N-side box; a tile takes at most two boxes (halves and quarters) and at most a quarter's
+    // rows too many, because every further box in a K block costs the producer more than the rows do
+    static constexpr int kQBox = kQCta;
     static constexpr int kPBytes = 128 * 128;
     static constexpr int kQBytes = kQCta * 128;
     static constexpr int kStep = 16 * CG;                       // granularity of the instruction's N
@@ -305,6 +305,36 @@ __device__ __forceinline__ bool ragged_wait(uint32_t bar, uint32_t parity, const
     }
 }
 
+// The same wait by a whole warp, which leaves it together.
+template <int CG>
+__device__ __forceinline__ bool ragged_wait_warp(uint32_t bar, uint32_t parity, const RaggedParams &p,
+                                                 volatile uint32_t *abort_flag, uint32_t code)
+{
+    const bool ok = ragged_wait<CG>(bar, parity, p, abort_flag, code);
+    return __all_sync(0xffffffffu, ok);
+}
+
+// A value all lanes hold, in a form the compiler can keep in uniform registers: the operands of TMA and MMA
+// instructions live there, and moving them over for every instruction delays the issue loops.
+__device__ __forceinline__ uint32_t uniform(uint32_t v)
+{
+    return __shfl_sync(0xffffffffu, v, 0);
+}
+
+__device__ __forceinline__ void uniform(RaggedSeg &s)
+{
+    s.g = uniform(s.g);
+    s.p0 = uniform(s.p0);
+    s.q0 = uniform(s.q0);
+    s.qn = uniform(s.qn);
+    s.nq = uniform(s.nq);
+    s.row0 = uniform(s.row0);
+    s.krows = uniform(s.krows);
+    s.kb = uniform(s.kb);
+    s.lo = uniform(s.lo);
+    s.hi = uniform(s.hi);
+}
+
 __device__ __forceinline__ uint32_t ragged_pack(float lo, float hi, bool bf16)
 {
     if (bf16) {
@@ -463,7 +493,7 @@ __global__ void __launch_bounds__(kRagThreads, 1) gemm_ragged_kernel(const __gri
         *abort_flag = 0u;
         ptx::fence_mbar_init();
         ptx::prefetch_tmap(&p.tm_p);
-        ptx::prefetch_tmap(&p.tm_q);
+        ptx::prefetch_tmap(&p.tm_q[0]);
         if (MODE == kTN || MODE == kLoraY) ptx::prefetch_tmap(&p.tm_x);
     }
     if (warp == 1) {
@@ -502,22 +532,27 @@ __global__ void __launch_bounds__(kRagThreads, 1) gemm_ragged_kernel(const __gri
 
     if (warp == 0) {
         // ------------------------------------------------ TMA producer
-        if (lane == 0) {
+        {
+            const bool elected = ptx::elect_one();
             uint32_t stage = 0, phase = 0, fills = 0, tail_uses = 0;
-            walk.each([&](const RaggedSeg &s) {
+            walk.each([&](RaggedSeg &s) {
+                uniform(s);
                 const uint32_t hq = s.nq / CG;
-                const uint32_t boxes = (hq + Cfg::kQBox - 1u) / Cfg::kQBox;
+                // N-side boxes: kTN 64 columns each; otherwise in units of a quarter of the stage's rows, 1, 2, 1 + 2 or 4
+                const uint32_t boxes = (hq + 63u) / 64u;
+                const uint32_t quarters = (hq + Cfg::kQBox / 4u - 1u) / (Cfg::kQBox / 4u);
+                const uint32_t q_bytes = Cfg::kQMn ? boxes * 8192u : quarters * uint32_t(Cfg::kQBox / 4 * 128);
                 const int32_t p0 = int32_t(s.p0 + rank * 128u);
                 const int32_t q0 = int32_t(s.q0 + rank * hq);
                 for (uint32_t kb = s.lo; kb < s.hi; ++kb, ++fills) {
-                    if (!ragged_wait<CG>(bar_empty(stage), phase ^ 1u, p, abort_flag, kRagErrEmpty)) return false;
-                    if (!(blockIdx.x == 0 && fills == p.skip_fill)) {
+                    if (!ragged_wait_warp<CG>(bar_empty(stage), phase ^ 1u, p, abort_flag, kRagErrEmpty)) return false;
+                    const bool fix = fixed_block(s, kb);
+                    const bool tail = fix;                       // to this CTA's own tail barrier
+                    if (elected && !(blockIdx.x == 0 && fills == p.skip_fill)) {
                         const uint32_t p_dst = base + Cfg::kOffP + stage * Cfg::kPBytes;
                         const uint32_t q_dst = base + Cfg::kOffQ + stage * Cfg::kQBytes;
-                        const bool fix = fixed_block(s, kb);
                         const bool extra = (MODE == kLoraY) && fix;  // adapter block: only P comes by TMA
-                        const bool tail = fix;                       // to this CTA's own tail barrier
-                        const uint32_t bytes = Cfg::kPBytes + (extra ? 0u : boxes * Cfg::kQBoxBytes);
+                        const uint32_t bytes = Cfg::kPBytes + (extra ? 0u : q_bytes);
                         rec[4 * stage + 1] = bytes;
                         rec[4 * stage + 2] = bytes * CG;
                         rec[4 * stage + 3] = tail ? 1u | (((tail_uses >> stage) & 1u) << 1) : 0u;
@@ -526,7 +561,6 @@ __global__ void __launch_bounds__(kRagThreads, 1) gemm_ragged_kernel(const __gri
                         if (tail) {
                             if (leader) ptx::mbar_arrive(fb);  // the MMA waits for `fixed` instead
                             fb = bar_tail(stage);
-                            tail_uses ^= 1u << stage;
                             ptx::mbar_arrive_expect_tx(fb, bytes);
                         } else {
                             if (leader) ptx::mbar_arrive_expect_tx(fb, bytes * CG);
@@ -542,7 +576,7 @@ __global__ void __launch_bounds__(kRagThreads, 1) gemm_ragged_kernel(const __gri
                             load(p_dst, &p.tm_p, p0, row, 0);
                             load(p_dst + 8192u, &p.tm_p, p0 + 64, row, 0);
                             for (uint32_t b = 0; b < boxes; ++b)
-                                load(q_dst + b * 8192u, &p.tm_q, q0 + int32_t(64u * b), row, 0);
+                                load(q_dst + b * 8192u, &p.tm_q[0], q0 + int32_t(64u * b), row, 0);
                         } else if (extra) {
                             const uint32_t e = kb - p.k_blocks;
                             const uint32_t slot = e / p.rank_blocks;
@@ -556,10 +590,18 @@ __global__ void __launch_bounds__(kRagThreads, 1) gemm_ragged_kernel(const __gri
                                 const int32_t z = MODE == kNT ? int32_t(s.g) : MODE == kLoraU ? int32_t(s.row0) : 0;
                                 load(p_dst, &p.tm_p, k0, p0, z);
                             }
-                            for (uint32_t b = 0; b < boxes; ++b)
-                                load(q_dst + b * Cfg::kQBoxBytes, &p.tm_q, k0, q0 + int32_t(b * Cfg::kQBox), 0);
+                            if (quarters == 4u) {
+                                load(q_dst, &p.tm_q[0], k0, q0, 0);
+                            } else {
+                                if (quarters & 2u) load(q_dst, &p.tm_q[1], k0, q0, 0);
+                                if (quarters & 1u) {
+                                    const uint32_t from = quarters == 1u ? 0u : uint32_t(Cfg::kQBox) / 2u;
+                                    load(q_dst + from * 128u, &p.tm_q[2], k0, q0 + int32_t(from), 0);
+                                }
+                            }
                         }
                     }
+                    if (tail) tail_uses ^= 1u << stage;
                     if (++stage == STAGES) {
                         stage = 0;
                         phase ^= 1u;
@@ -570,41 +612,58 @@ __global__ void __launch_bounds__(kRagThreads, 1) gemm_ragged_kernel(const __gri
         }
     } else if (warp == 1) {
         // ------------------------------------------------ MMA issuer
-        if (leader && lane == 0) {
+        if (leader) {
+            const bool elected = ptx::elect_one();
+            const uint32_t tmem_u = uniform(tmem_base);
             const uint32_t idesc0 = ragged_idesc(128u * CG, p.bf16 != 0u, Cfg::kPMn, Cfg::kQMn);
             constexpr uint64_t kPStep = Cfg::kPMn ? (2048u >> 4) : 2u;  // K = 16 inside a swizzle atom, or two 8-row groups
             constexpr uint64_t kQStep = Cfg::kQMn ? (2048u >> 4) : 2u;
             uint32_t stage = 0, phase = 0, acc = 0, acc_phase = 0, fixed_uses = 0;
-            walk.each([&](const RaggedSeg &s) {
-                if (!ragged_wait<CG>(bar_acc_empty(acc), acc_phase ^ 1u, p, abort_flag, kRagErrAccEmpty)) return false;
+            walk.each([&](RaggedSeg &s) {
+                uniform(s);
+                if (!ragged_wait_warp<CG>(bar_acc_empty(acc), acc_phase ^ 1u, p, abort_flag, kRagErrAccEmpty)) return false;
                 ptx::tc_fence_after_sync();
-                const uint32_t d_tmem = tmem_base + acc * uint32_t(QCAP);
+                const uint32_t d_tmem = tmem_u + acc * uint32_t(QCAP);
                 const uint32_t idesc = idesc0 | ragged_idesc_n(s.nq);
-                for (uint32_t kb = s.lo; kb < s.hi; ++kb) {
-                    if (!ragged_wait<CG>(bar_full(stage), phase, p, abort_flag, kRagErrFull)) return false;
-                    if (Cfg::kHelper && fixed_block(s, kb)) {
-                        if (!ragged_wait<CG>(bar_fixed(stage), (fixed_uses >> stage) & 1u, p, abort_flag, kRagErrFixed))
+                // K blocks that are full and need no helper come first, four instructions each and nothing else:
+                // the issue loop has to stay ahead of the tensor cores
+                uint32_t accumulate = 0u;
+                const uint32_t whole = min(s.hi, (MODE == kTN ? s.krows : p.kdim) / uint32_t(kRagBlockK));
+                auto block = [&](uint32_t steps, bool fixed) -> bool {
+                    if (!ragged_wait_warp<CG>(bar_full(stage), phase, p, abort_flag, kRagErrFull)) return false;
+                    if (Cfg::kHelper && fixed) {
+                        if (!ragged_wait_warp<CG>(bar_fixed(stage), (fixed_uses >> stage) & 1u, p, abort_flag, kRagErrFixed))
                             return false;
                         fixed_uses ^= 1u << stage;
                     }
                     ptx::tc_fence_after_sync();
                     const uint64_t p_desc = ragged_desc(base + Cfg::kOffP + stage * Cfg::kPBytes, Cfg::kPMn);
                     const uint64_t q_desc = ragged_desc(base + Cfg::kOffQ + stage * Cfg::kQBytes, Cfg::kQMn);
-                    const uint32_t steps = steps_of(s, kb);
+                    if (elected) {
 #pragma unroll
-                    for (uint32_t kk = 0; kk < 4u; ++kk)
-                        if (kk < steps)
-                            ptx::mma_f16<CG>(d_tmem, p_desc + kPStep * kk, q_desc + kQStep * kk, idesc,
-                                             (kb != s.lo || kk != 0u) ? 1u : 0u);
-                    if constexpr (CG == 1) ptx::mma_commit(bar_empty(stage));
-                    else ptx::mma_commit_pair(bar_empty(stage), uint16_t(3u));
+                        for (uint32_t kk = 0; kk < 4u; ++kk)
+                            if (kk < steps)
+                                ptx::mma_f16<CG>(d_tmem, p_desc + kPStep * kk, q_desc + kQStep * kk, idesc,
+                                                 kk == 0u ? accumulate : 1u);
+                        if constexpr (CG == 1) ptx::mma_commit(bar_empty(stage));
+                        else ptx::mma_commit_pair(bar_empty(stage), uint16_t(3u));
+                    }
+                    accumulate = 1u;
                     if (++stage == STAGES) {
                         stage = 0;
                         phase ^= 1u;
                     }
+                    return true;
+                };
+                uint32_t kb = s.lo;
+                for (; kb < whole; ++kb)
+                    if (!block(4u, false)) return false;
+                for (; kb < s.hi; ++kb)
+                    if (!block(steps_of(s, kb), fixed_block(s, kb))) return false;
+                if (elected) {
+                    if constexpr (CG == 1) ptx::mma_commit(bar_acc_full(acc));
+                    else ptx::mma_commit_pair(bar_acc_full(acc), uint16_t(3u));
                 }
-                if constexpr (CG == 1) ptx::mma_commit(bar_acc_full(acc));
-                else ptx::mma_commit_pair(bar_acc_full(acc), uint16_t(3u));
                 if (++acc == 2u) {
                     acc = 0;
                     acc_phase ^= 1u;
@@ -612,13 +671,15 @@ __global__ void __launch_bounds__(kRagThreads, 1) gemm_ragged_kernel(const __gri
                 return true;
             });
             // no MMA may still be running when the tensor memory is freed
-            if constexpr (CG == 1) ptx::mma_commit(bar_drain);
-            else ptx::mma_commit_pair(bar_drain, uint16_t(1u));
-            const long long t0 = clock64();
-            while (!ptx::mbar_try_wait(bar_drain, 0)) {
-                if (clock64() - t0 > p.wait_limit) {
-                    atomicCAS(p.error_word, 0u, kRagErrDrain | (blockIdx.x << 8));
-                    break;
+            if (elected) {
+                if constexpr (CG == 1) ptx::mma_commit(bar_drain);
+                else ptx::mma_commit_pair(bar_drain, uint16_t(1u));
+                const long long t0 = clock64();
+                while (!ptx::mbar_try_wait(bar_drain, 0)) {
+                    if (clock64() - t0 > p.wait_limit) {
+                        atomicCAS(p.error_word, 0u, kRagErrDrain | (blockIdx.x << 8));
+                        break;
+                    }
                 }
             }
         }
