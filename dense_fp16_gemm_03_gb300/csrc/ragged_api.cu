@@ -19,6 +19,7 @@ namespace {
 
 constexpr int kMaxDevices = 64;
 constexpr int64_t kSizeLimit = int64_t(1) << 31;
+constexpr int64_t kIterLimit = (int64_t(1) << 32) - 1;  // K-block iterations of a split launch are counted in 32 bits
 
 int64_t cdiv(int64_t a, int64_t b)
 {
@@ -46,12 +47,12 @@ struct RaggedVariant {
             reinterpret_cast<const void *>(&gemm_ragged_kernel<MODE, CG, QCAP, ST>)                      \
     }
 
-enum RaggedVariantId { kVNtWide, kVNtFew, kVNnWide, kVNnFew, kVTn, kVLoraUWide, kVLoraUFew, kVLoraYWide, kVLoraYFew };
+enum RaggedVariantId { kVNtWide, kVNtFew, kVNnWide, kVNnFew, kVTn, kVLoraU, kVLoraYWide, kVLoraYFew };
 const RaggedVariant kRagged[] = {
     RAGGED_VARIANT(kNT, 2, 256, 6), RAGGED_VARIANT(kNT, 1, 64, 8),
     RAGGED_VARIANT(kNN, 2, 256, 6), RAGGED_VARIANT(kNN, 1, 64, 8),
     RAGGED_VARIANT(kTN, 2, 256, 6),
-    RAGGED_VARIANT(kLoraU, 1, 256, 4), RAGGED_VARIANT(kLoraU, 1, 64, 8),
+    RAGGED_VARIANT(kLoraU, 1, 64, 8),
     RAGGED_VARIANT(kLoraY, 2, 256, 6), RAGGED_VARIANT(kLoraY, 1, 64, 8),
 };
 constexpr int kNumRagged = int(sizeof(kRagged) / sizeof(kRagged[0]));
@@ -201,11 +202,11 @@ bool operand_type(gemm_dtype_t t)
 
 // ------------------------------------------------------------- launches
 
-gemm_status_t launch(const void *fn, unsigned grid, unsigned threads, int smem, int cluster, void **args, cudaStream_t stream)
+gemm_status_t launch(const void *fn, dim3 grid, unsigned threads, int smem, int cluster, void **args, cudaStream_t stream)
 {
     cudaLaunchConfig_t cfg;
     memset(&cfg, 0, sizeof(cfg));
-    cfg.gridDim = dim3(grid, 1, 1);
+    cfg.gridDim = grid;
     cfg.blockDim = dim3(threads, 1, 1);
     cfg.dynamicSmemBytes = size_t(smem);
     cfg.stream = stream;
@@ -258,7 +259,7 @@ gemm_status_t launch_ragged(int variant, const RaggedDevice *dev, RaggedParams &
     if (most_units < workers) workers = most_units < 1 ? 1 : most_units;
     p.error_word = dev->error_word;
     void *args[1] = {&p};
-    return launch(var.fn, unsigned(workers * var.cg), kRagThreads, var.smem, var.cg, args, stream);
+    return launch(var.fn, dim3(unsigned(workers * var.cg), 1, 1), kRagThreads, var.smem, var.cg, args, stream);
 }
 
 // ------------------------------------------------------ grouped products
@@ -344,7 +345,7 @@ gemm_status_t grouped(int mode, gemm_dtype_t dtype, gemm_dtype_t out_type, int64
     } else {
         st = encode_stack(&p.tm_p, second, dtype, groups, n, k, 64, mode == kNT ? 128 : 64);
         if (st == GEMM_OK) st = encode_rows(p.tm_q, first, dtype, rows, kdim, var.qbox);
-        if (ws && few_rows(groups, rows)) {
+        if (ws && few_rows(groups, rows) && most * p.k_blocks < kIterLimit) {
             use_split(&p, var, dev->slots[variant], ws);
             most *= p.k_blocks;
         }
@@ -355,38 +356,45 @@ gemm_status_t grouped(int mode, gemm_dtype_t dtype, gemm_dtype_t out_type, int64
 
 // ------------------------------------------------------------- adapters
 
-// Rows of a tile and how the workspace is laid out: counts per tile, adapters per tile, u, split work.
+// Rows up to which u is computed by lora_shrink_kernel and the whole product is one row tile of a single CTA.
+constexpr int64_t kLoraFewRows = 64;
+constexpr int64_t kLoraURows = 64;  // rows of a tile of the product that computes u for more rows
+
+// Rows of a tile and how the workspace is laid out: counts and lists of the adapters per row tile (of u's product
+// and of y's), u, split work.
 struct LoraPlan {
-    int64_t per, tiles;  // of one pass
-    int64_t pass_rows;   // rows of one pass: the kernels' table holds kRagMaxGroups tiles
-    int variant_u, variant_y;
-    bool split_y;
-    size_t counts, list, u, split, total;  // offsets
+    bool few;
+    int64_t per, tiles;    // y's row tiles, of one pass
+    int64_t tiles_u;
+    int64_t pass_rows;     // rows of one pass: the kernels' table holds kRagMaxGroups tiles
+    int variant_y;
+    size_t counts, list, counts_u, list_u, u, split, total;  // offsets
 };
 
 LoraPlan lora_plan(const RaggedDevice *dev, int64_t rows, int64_t rank)
 {
     LoraPlan l;
-    const bool few = rows <= 64;
-    l.variant_u = few ? kVLoraUFew : kVLoraUWide;
-    l.variant_y = few ? kVLoraYFew : kVLoraYWide;
+    l.few = rows <= kLoraFewRows;
+    l.variant_y = l.few ? kVLoraYFew : kVLoraYWide;
     const RaggedVariant &y = kRagged[l.variant_y];
-    l.pass_rows = int64_t(kRagMaxGroups) * y.qcap;
+    l.pass_rows = int64_t(kRagMaxGroups) * kLoraURows;
     if (rows < l.pass_rows) l.pass_rows = rows;
     l.tiles = cdiv(l.pass_rows, y.qcap);
     l.per = round_up(cdiv(l.pass_rows, l.tiles), 16 * y.cg);
-    l.split_y = l.tiles == 1;
+    l.tiles_u = cdiv(l.pass_rows, kLoraURows);
     size_t at = 0;
     auto take = [&](size_t bytes) {
         const size_t was = at;
         at += size_t(round_up(int64_t(bytes), 256));
         return was;
     };
-    l.counts = take(size_t(l.tiles) * 4u);
-    l.list = take(size_t(l.tiles) * size_t(l.per) * 4u);
+    l.counts = take(l.few ? 0 : size_t(l.tiles) * 4u);
+    l.list = take(l.few ? 0 : size_t(l.tiles) * size_t(l.per) * 4u);
+    l.counts_u = take(l.few ? 0 : size_t(l.tiles_u) * 4u);
+    l.list_u = take(l.few ? 0 : size_t(l.tiles_u) * size_t(kLoraURows) * 4u);
     l.u = take(size_t(l.pass_rows) * size_t(rank) * 2u);
-    size_t split = split_bytes(kRagged[l.variant_u], dev->slots[l.variant_u]);
-    const size_t split_y = l.split_y ? split_bytes(y, dev->slots[l.variant_y]) : 0;
+    size_t split = l.few ? 0 : split_bytes(kRagged[kVLoraU], dev->slots[kVLoraU]);
+    const size_t split_y = l.tiles == 1 ? split_bytes(y, dev->slots[l.variant_y]) : 0;
     if (split_y > split) split = split_y;
     l.split = take(split);
     l.total = at;
@@ -493,36 +501,37 @@ gemm_status_t gemm_lora_nt(gemm_dtype_t dtype, int64_t rows, int64_t n, int64_t 
         return GEMM_OK;
     }
     char *ws = static_cast<char *>(workspace);
-    int32_t *counts = reinterpret_cast<int32_t *>(ws + l.counts), *list = reinterpret_cast<int32_t *>(ws + l.list);
-    const RaggedVariant &vu = kRagged[l.variant_u], &vy = kRagged[l.variant_y];
+    const RaggedVariant &vu = kRagged[kVLoraU], &vy = kRagged[l.variant_y];
 
     RaggedParams u, p;
     memset(&u, 0, sizeof(u));
     u.kdim = uint32_t(k);
     u.k_blocks = uint32_t(cdiv(k, kRagBlockK));
-    u.per = uint32_t(l.per);
     u.band = 8;
     u.bf16 = dtype == GEMM_DTYPE_BF16;
-    u.counts = counts;
-    u.list = list;
     u.scale = scale;
+    u.adapters = adapted ? uint32_t(adapters) : 0u;
     u.rank = uint32_t(rank);
     u.rank_blocks = uint32_t(cdiv(rank, kRagBlockK));
     u.skip_fill = ~0u;
     u.wait_limit = wait_limit_for(cdiv(k, kRagBlockK) + 4096);
     p = u;
-    // u = scale x a^T: one tile per row tile and adapter
-    u.pdim = uint32_t(rank);
-    u.tiles_p = 1;
-    u.out = ws + l.u;
     // y = x w^T + u b^T
     p.pdim = uint32_t(n);
     p.tiles_p = uint32_t(cdiv(n, 128 * vy.cg));
+    p.per = uint32_t(l.per);
     p.u = ws + l.u;
     st = encode_stack(&p.tm_p, w, dtype, 1, n, k, kRagBlockK, 128);
-    if (st == GEMM_OK && adapted) st = encode_stack(&u.tm_p, a, dtype, adapters, rank, k, kRagBlockK, 128);
     if (st == GEMM_OK && adapted) st = encode_stack(&p.tm_x, b, dtype, adapters, n, rank, kRagBlockK, 128);
     if (!adapted) p.tm_x = p.tm_p;  // (never loaded from)
+    // u = scale x a^T for many rows: one tile per row tile and adapter in it
+    if (!l.few && adapted) {
+        u.pdim = uint32_t(rank);
+        u.tiles_p = 1;
+        u.per = uint32_t(kLoraURows);
+        u.out = ws + l.u;
+        if (st == GEMM_OK) st = encode_stack(&u.tm_p, a, dtype, adapters, rank, k, kRagBlockK, 128);
+    }
     if (st != GEMM_OK) return st;
     if (int64_t(p.tiles_p) * l.tiles >= kSizeLimit) return GEMM_ERR_UNSUPPORTED_SHAPE;
 
@@ -530,36 +539,71 @@ gemm_status_t gemm_lora_nt(gemm_dtype_t dtype, int64_t rows, int64_t n, int64_t 
         const int64_t r = rows - r0 < l.pass_rows ? rows - r0 : l.pass_rows;
         const int64_t tiles = cdiv(r, l.per);
         const char *xr = static_cast<const char *>(x) + size_t(r0) * size_t(k) * 2u;
-        uint32_t rr = uint32_t(r), per = uint32_t(l.per), count = adapted ? uint32_t(adapters) : 0u;
-        const int32_t *idr = ids ? ids + r0 : nullptr;
-        if (!adapted) {
-            if (cudaMemsetAsync(counts, 0, size_t(tiles) * 4u, s) != cudaSuccess) {
-                cudaGetLastError();
-                return GEMM_ERR_LAUNCH;
-            }
-        } else {
-            void *args[6] = {&idr, &rr, &per, &count, &counts, &list};
-            st = launch(reinterpret_cast<const void *>(&lora_plan_kernel), unsigned(tiles), 256, 0, 1, args, s);
-            if (st != GEMM_OK) return st;
-            u.groups = uint32_t(tiles);
-            u.rows = rr;
-            u.ids = idr;
-            st = encode_rows(u.tm_q, xr, dtype, r, k, vu.qbox);
-            if (st != GEMM_OK) return st;
-            use_split(&u, vu, dev->slots[l.variant_u], ws + l.split);
-            st = launch_ragged(l.variant_u, dev, u, r * int64_t(u.k_blocks), s);
-            if (st != GEMM_OK) return st;
-        }
+        const int32_t *idr = adapted ? ids + r0 : nullptr;
         p.groups = uint32_t(tiles);
         p.tiles_q = uint32_t(tiles);
-        p.rows = rr;
+        p.rows = uint32_t(r);
         p.ids = idr;
         p.out = static_cast<char *>(y) + size_t(r0) * size_t(n) * 2u;
         st = encode_rows(p.tm_q, xr, dtype, r, k, vy.qbox);
         if (st != GEMM_OK) return st;
+        if (l.few) {
+            // u by itself, beside the product: both start after what was in the stream before them
+            if (adapted) {
+                LoraShrinkParams sp;
+                sp.x = xr;
+                sp.a = a;
+                sp.ids = idr;
+                sp.scale = scale;
+                sp.u = ws + l.u;
+                sp.k = uint32_t(k);
+                sp.rank = uint32_t(rank);
+                sp.adapters = uint32_t(adapters);
+                sp.bf16 = u.bf16;
+                void *args[1] = {&sp};
+                st = launch(reinterpret_cast<const void *>(&lora_shrink_kernel), dim3(unsigned(rank / 4), unsigned(r), 1), 128, 0, 1,
+                            args, s);
+                if (st != GEMM_OK) return st;
+                p.late = 1;
+            }
+            p.counts = p.list = nullptr;
+        } else {
+            struct Side {
+                int64_t per, tiles;
+                size_t counts, list;
+            } sides[2] = {{l.per, tiles, l.counts, l.list}, {kLoraURows, cdiv(r, kLoraURows), l.counts_u, l.list_u}};
+            for (const Side &side : sides) {
+                LoraListParams lp;
+                lp.ids = idr;
+                lp.rows = uint32_t(r);
+                lp.per = uint32_t(side.per);
+                lp.adapters = u.adapters;
+                lp.counts = reinterpret_cast<int32_t *>(ws + side.counts);
+                lp.list = reinterpret_cast<int32_t *>(ws + side.list);
+                void *args[1] = {&lp};
+                if (!adapted && &side == &sides[1]) break;
+                st = launch(reinterpret_cast<const void *>(&lora_list_kernel), dim3(unsigned(side.tiles), 1, 1), 256, 0, 1, args, s);
+                if (st != GEMM_OK) return st;
+            }
+            p.counts = reinterpret_cast<int32_t *>(ws + l.counts);
+            p.list = reinterpret_cast<int32_t *>(ws + l.list);
+            if (adapted) {
+                u.counts = reinterpret_cast<int32_t *>(ws + l.counts_u);
+                u.list = reinterpret_cast<int32_t *>(ws + l.list_u);
+                u.groups = uint32_t(sides[1].tiles);
+                u.rows = uint32_t(r);
+                u.ids = idr;
+                st = encode_rows(u.tm_q, xr, dtype, r, k, vu.qbox);
+                if (st != GEMM_OK) return st;
+                u.sk = 0;
+                if (r * int64_t(u.k_blocks) < kIterLimit) use_split(&u, vu, dev->slots[kVLoraU], ws + l.split);
+                st = launch_ragged(kVLoraU, dev, u, r * int64_t(u.k_blocks), s);
+                if (st != GEMM_OK) return st;
+            }
+        }
         int64_t most = int64_t(p.tiles_p) * tiles;
         p.sk = 0;
-        if (tiles == 1 && l.split_y) {
+        if (l.tiles == 1 && most * (p.k_blocks + l.per * p.rank_blocks) < kIterLimit) {
             use_split(&p, vy, dev->slots[l.variant_y], ws + l.split);
             most *= p.k_blocks;
         }
@@ -647,11 +691,11 @@ gemm_status_t gemm_route_topk(gemm_dtype_t dtype, int64_t rows, int64_t experts,
     p.hist = static_cast<int32_t *>(workspace);
     p.totals = p.hist ? p.hist + size_t(blocks) * size_t(experts) : nullptr;
     void *args[1] = {&p};
-    st = launch(ROUTE_INSTANCE(route_topk_kernel, experts), unsigned(blocks), kRouteThreads, 0, 1, args, s);
+    st = launch(ROUTE_INSTANCE(route_topk_kernel, experts), dim3(unsigned(blocks), 1, 1), kRouteThreads, 0, 1, args, s);
     if (st != GEMM_OK || blocks == 1) return st;
-    st = launch(reinterpret_cast<const void *>(&route_scan_kernel), unsigned(cdiv(experts, 32)), 1024, 0, 1, args, s);
+    st = launch(reinterpret_cast<const void *>(&route_scan_kernel), dim3(unsigned(cdiv(experts, 32)), 1, 1), 1024, 0, 1, args, s);
     if (st != GEMM_OK) return st;
-    return launch(reinterpret_cast<const void *>(&route_place_kernel), unsigned(blocks), kRouteThreads, 0, 1, args, s);
+    return launch(reinterpret_cast<const void *>(&route_place_kernel), dim3(unsigned(blocks), 1, 1), kRouteThreads, 0, 1, args, s);
 }
 
 gemm_status_t gemm_route_topk_grad(gemm_dtype_t dtype, int64_t rows, int64_t experts, int64_t top, int32_t renorm,
@@ -682,7 +726,7 @@ gemm_status_t gemm_route_topk_grad(gemm_dtype_t dtype, int64_t rows, int64_t exp
     p.dweights = dweights;
     p.dlogits = dlogits;
     void *args[1] = {&p};
-    return launch(ROUTE_INSTANCE(route_grad_kernel, experts), unsigned(cdiv(rows, 8)), 256, 0, 1, args,
+    return launch(ROUTE_INSTANCE(route_grad_kernel, experts), dim3(unsigned(cdiv(rows, 8)), 1, 1), 256, 0, 1, args,
                   reinterpret_cast<cudaStream_t>(stream));
 }
 

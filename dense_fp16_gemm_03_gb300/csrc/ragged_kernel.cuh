@@ -105,6 +105,8 @@ struct RaggedParams {
     const int32_t *counts;   // adapters present in each row tile
     const int32_t *list;     // their numbers, `per` slots a row tile
     const float *scale;      // per adapter, or null
+    uint32_t adapters;       // kLoraY without a list
+    uint32_t late;           // kLoraY: only u comes from the previous kernel, so only the helper waits for it
     const void *u;           // kLoraY: u [rows, rank]
     uint32_t rank;
     uint32_t rank_blocks;    // ceil(rank / 64)
@@ -138,7 +140,7 @@ struct RaggedCfg {
     // full, empty, fixed, tail per stage; acc_full x2, acc_empty x2, drain, bad_free x2
     static constexpr int kNumBars = 4 * STAGES + 7;
     // kLoraY: for each of two tiles in flight, 128 bits per adapter of the tile (b rows that hold an infinity or
-    // NaN), and whether there are any
+    // NaN), and for each helper warp whether it found any
     static constexpr int kOffBad = kOffTabTile + 4 * (kRagMaxGroups + 4);
     static constexpr int kBadBytes = (MODE == kLoraY) ? QCAP * 16 : 0;
     static constexpr int kOffBar = kOffBad + 2 * kBadBytes;
@@ -147,7 +149,7 @@ struct RaggedCfg {
     static constexpr int kOffTmemSlot = kOffRec + STAGES * 16;
     static constexpr int kOffAbort = kOffTmemSlot + 4;
     static constexpr int kOffAnyBad = kOffAbort + 4;
-    static constexpr int kSmemBytes = kOffAnyBad + 8 + 1024;
+    static constexpr int kSmemBytes = kOffAnyBad + 16 + 1024;
     static constexpr int kTmemCols = 2 * QCAP < 32 ? 32 : 2 * QCAP;
     static_assert(kQBytes % 1024 == 0 && kOffBar % 8 == 0, "layout");
     static_assert(kSmemBytes <= kRagMaxSmem, "shared memory budget");
@@ -174,7 +176,9 @@ struct RaggedWalk {
     const RaggedParams &p;
     const int32_t *tab_row;    // offsets (groups + 1), or counts per row tile
     const uint32_t *tab_tile;  // tiles before each group (groups + 1)
+    const int32_t *list;       // kLoraU, kLoraY: the adapters of each row tile
     uint32_t worker, workers, total;
+    uint32_t run, longer;      // sk: K-block iterations of a worker; the first `longer` workers have one more
 
     __device__ __forceinline__ void decode(uint32_t u, RaggedSeg &s) const
     {
@@ -203,7 +207,7 @@ struct RaggedWalk {
                 s.p0 = 0;
                 s.q0 = lo * p.per;
                 s.qn = min(p.per, p.rows - s.q0);
-                s.row0 = uint32_t(p.list[size_t(lo) * p.per + local]);
+                s.row0 = uint32_t(list[size_t(lo) * p.per + local]);
             } else {
                 const uint32_t r0 = uint32_t(tab_row[lo]);
                 const uint32_t rows = uint32_t(tab_row[lo + 1]) - r0;
@@ -245,9 +249,23 @@ struct RaggedWalk {
         qi = b * p.band + (r - pi * w);
     }
 
-    __device__ __forceinline__ uint64_t run_begin(uint32_t w, uint64_t iters) const
+    // sk: all tiles have the same K blocks (kLoraY: there is one row tile).  A run shorter than kMinRun blocks
+    // would cost more in adding partials than it saves, so few iterations go to fewer workers.
+    static constexpr uint32_t kMinRun = 4;
+    __device__ __forceinline__ void plan_runs()
     {
-        return uint64_t(w) * iters / workers;
+        if (MODE == kTN || !p.sk || total == 0u) return;
+        RaggedSeg s;
+        decode(0, s);
+        const uint32_t iters = total * s.kb;  // below 2^32: the host checks
+        const uint32_t most = max(1u, iters / kMinRun);
+        if (most < workers) workers = most;
+        run = iters / workers;
+        longer = iters - run * workers;
+    }
+    __device__ __forceinline__ uint32_t run_begin(uint32_t w) const
+    {
+        return w * run + min(w, longer);
     }
 
     // f(seg) returns false to stop early (abort)
@@ -264,20 +282,20 @@ struct RaggedWalk {
             }
             return;
         }
-        if (total == 0) return;
+        if (total == 0u || worker >= workers) return;
+        const uint32_t begin = run_begin(worker);
+        uint32_t it = run_begin(worker + 1u);
         decode(0, s);
-        const uint32_t kb = s.kb;  // the same for every tile (kLoraY: there is one row tile)
-        const uint64_t iters = uint64_t(total) * kb;
-        const uint64_t begin = run_begin(worker, iters);
-        uint64_t it = run_begin(worker + 1, iters);
+        const uint32_t kb = s.kb;
         while (it > begin) {
-            const uint32_t u = uint32_t((it - 1u) / kb);
-            const uint64_t start = uint64_t(u) * kb;
+            const uint32_t u = (it - 1u) / kb;
+            const uint32_t start = u * kb;
             decode(u, s);
-            s.lo = begin > start ? uint32_t(begin - start) : 0u;
-            s.hi = uint32_t(it - start);
+            s.lo = begin > start ? begin - start : 0u;
+            s.hi = it - start;
+            const uint32_t lo = s.lo;
             if (!f(s)) return;
-            it = start + s.lo;
+            it = start + lo;
         }
     }
 };
@@ -347,9 +365,40 @@ __device__ __forceinline__ uint32_t ragged_pack(float lo, float hi, bool bf16)
 
 // The group table: row offsets clamped to [0, rows] and made monotone (offsets that are not can
 // then reach no other memory), and the number of tiles before each group.  Run by the whole CTA.
+//
+// kLoraY without a list (one row tile): the adapters present, in order of first appearance, are found here and
+// listed in the table's second half.
 template <int MODE, int QCAP>
 __device__ __forceinline__ void ragged_table(const RaggedParams &p, int32_t *tab_row, uint32_t *tab_tile)
 {
+    if (MODE == kLoraY && p.list == nullptr) {
+        const uint32_t t = threadIdx.x;
+        int32_t id = -1;
+        if (t < uint32_t(QCAP)) {
+            id = (p.adapters != 0u && t < p.rows) ? p.ids[t] : -1;
+            if (uint32_t(id) >= p.adapters) id = -1;
+            tab_row[t] = id;
+        }
+        __syncthreads();
+        bool first = id >= 0;
+        if (t < uint32_t(QCAP))
+            for (uint32_t i = 0; i < t; ++i) first &= tab_row[i] != id;
+        // at most 256 rows, in warps of 32: the number of first ones before this row
+        const uint32_t vote = __ballot_sync(0xffffffffu, first);
+        if ((t & 31u) == 0u) tab_tile[kRagMaxGroups - 16u + (t >> 5)] = uint32_t(__popc(vote));
+        __syncthreads();
+        uint32_t at = uint32_t(__popc(vote & ((1u << (t & 31u)) - 1u))), total = 0;
+        for (uint32_t w = 0; w < uint32_t(kRagThreads / 32); ++w) {
+            const uint32_t c = tab_tile[kRagMaxGroups - 16u + w];
+            if (w < (t >> 5)) at += c;
+            total += c;
+        }
+        __syncthreads();
+        if (first) tab_tile[at] = uint32_t(id);
+        if (t == 0u) tab_row[0] = int32_t(total);
+        __syncthreads();
+        return;
+    }
     constexpr bool kOffsets = (MODE == kNT || MODE == kNN || MODE == kTN);
     const uint32_t n = p.groups + (kOffsets ? 1u : 0u);
     for (uint32_t i = threadIdx.x; i < n; i += blockDim.x) {
@@ -480,7 +529,7 @@ __global__ void __launch_bounds__(kRagThreads, 1) gemm_ragged_kernel(const __gri
         for (int s = 0; s < STAGES; ++s) {
             ptx::mbar_init(bar_full(s), 1);
             ptx::mbar_init(bar_empty(s), 1);
-            ptx::mbar_init(bar_fixed(s), CG);
+            ptx::mbar_init(bar_fixed(s), (kRagHelpers / 32) * CG);
             ptx::mbar_init(bar_tail(s), 1);
             rec[4 * s] = 0u;
         }
@@ -505,15 +554,20 @@ __global__ void __launch_bounds__(kRagThreads, 1) gemm_ragged_kernel(const __gri
     else __syncthreads();
     ptx::tc_fence_after_sync();
     const uint32_t tmem_base = *tmem_slot;
-    ptx::griddep_wait();
+    if (MODE != kLoraY || !p.late) ptx::griddep_wait();
     ragged_table<MODE, QCAP>(p, tab_row, tab_tile);
 
+    const int32_t *list = (MODE == kLoraY && p.list == nullptr) ? reinterpret_cast<const int32_t *>(tab_tile) : p.list;
     RaggedWalk<MODE, CG, QCAP> walk{p,
                                     tab_row,
                                     tab_tile,
+                                    list,
                                     blockIdx.x / CG,
                                     gridDim.x / CG,
-                                    MODE == kLoraY ? p.tiles_p * p.tiles_q : tab_tile[p.groups]};
+                                    MODE == kLoraY ? p.tiles_p * p.tiles_q : tab_tile[p.groups],
+                                    0u,
+                                    0u};
+    walk.plan_runs();
 
     // K = 16 steps of K block kb that hold anything
     auto steps_of = [&](const RaggedSeg &s, uint32_t kb) -> uint32_t {
@@ -580,7 +634,7 @@ __global__ void __launch_bounds__(kRagThreads, 1) gemm_ragged_kernel(const __gri
                         } else if (extra) {
                             const uint32_t e = kb - p.k_blocks;
                             const uint32_t slot = e / p.rank_blocks;
-                            const int32_t adapter = p.list[size_t(s.g) * p.per + slot];
+                            const int32_t adapter = list[size_t(s.g) * p.per + slot];
                             load(p_dst, &p.tm_x, int32_t((e - slot * p.rank_blocks) * kRagBlockK), p0, adapter);
                         } else {
                             if constexpr (MODE == kNN) {
@@ -737,14 +791,14 @@ __global__ void __launch_bounds__(kRagThreads, 1) gemm_ragged_kernel(const __gri
             // kLoraY: NaN for the rows whose own adapter holds an infinity or NaN in this lane's row of b
             const bool has_adapters = MODE == kLoraY && s.hi > max(s.lo, p.k_blocks);
             const uint32_t bad_buf = adapted & 1u;
-            const bool any = has_adapters && any_bad[bad_buf] != 0u;
+            const bool any = has_adapters && (any_bad[2u * bad_buf] | any_bad[2u * bad_buf + 1u]) != 0u;
             if (has_adapters) ++adapted;
             auto spoil = [&](uint32_t c, uint32_t (&r)[32]) {
                 if (!any) return;
                 const volatile uint32_t *mask = reinterpret_cast<const volatile uint32_t *>(smem + Cfg::kOffBad + bad_buf * Cfg::kBadBytes);
                 for (int32_t i = 0; i < tab_row[s.g]; ++i) {
                     if (!((mask[4 * i + quarter] >> lane) & 1u)) continue;
-                    const int32_t adapter = p.list[size_t(s.g) * p.per + i];
+                    const int32_t adapter = list[size_t(s.g) * p.per + i];
 #pragma unroll
                     for (uint32_t j = 0; j < 32u; ++j)
                         if (32u * c + j < s.qn && p.ids[s.q0 + 32u * c + j] == adapter) r[j] = 0x7FC00000u;
@@ -768,6 +822,8 @@ __global__ void __launch_bounds__(kRagThreads, 1) gemm_ragged_kernel(const __gri
             };
             const bool live = prow < p.pdim;
 
+            // partials move in halves of a chunk, 16 columns: no more than the instruction's N has
+            const uint32_t halves = (s.nq + 15u) / 16u;
             if (split && s.hi != s.kb) {
                 // ---- publish: the worker with the tile's last K block adds this partial
                 if (live) {
@@ -778,9 +834,10 @@ __global__ void __launch_bounds__(kRagThreads, 1) gemm_ragged_kernel(const __gri
                         if (MODE == kLoraY) spoil(c, r);
 #pragma unroll
                         for (int j = 0; j < 8; ++j)
-                            ptx::st_global_cg_f4(slot + c * 1024u + j * 128, __uint_as_float(r[4 * j]),
-                                                 __uint_as_float(r[4 * j + 1]), __uint_as_float(r[4 * j + 2]),
-                                                 __uint_as_float(r[4 * j + 3]));
+                            if (2u * c + uint32_t(j / 4) < halves)
+                                ptx::st_global_cg_f4(slot + c * 1024u + j * 128, __uint_as_float(r[4 * j]),
+                                                     __uint_as_float(r[4 * j + 1]), __uint_as_float(r[4 * j + 2]),
+                                                     __uint_as_float(r[4 * j + 3]));
                     }
                 }
                 release();
@@ -791,12 +848,10 @@ __global__ void __launch_bounds__(kRagThreads, 1) gemm_ragged_kernel(const __gri
             }
             uint32_t w_lo = walk.worker;  // workers [w_lo, worker) hold the tile's earlier K blocks
             if (split) {
-                const uint64_t iters = uint64_t(walk.total) * s.kb;
-                const uint64_t start = uint64_t(s.tile) * s.kb;
-                while (w_lo > 0u && walk.run_begin(w_lo, iters) > start) --w_lo;
-                if (threadIdx.x == 64u) {
-                    for (uint32_t w = w_lo; w < walk.worker; ++w) {
-                        if (walk.run_begin(w, iters) == walk.run_begin(w + 1u, iters)) continue;
+                const uint32_t start = s.tile * s.kb;
+                while (w_lo > 0u && walk.run_begin(w_lo) > start) --w_lo;
+                if (warp == 2u) {
+                    for (uint32_t w = w_lo + lane; w < walk.worker; w += 32u) {
                         uint64_t *flag = p.flags + w * CG + rank;
                         const long long t0 = clock64();
                         while (ptx::ld_acquire_gpu_u64(flag) != p.stamp) {
@@ -809,25 +864,38 @@ __global__ void __launch_bounds__(kRagThreads, 1) gemm_ragged_kernel(const __gri
                         // taken: a launch captured in a graph comes again with the same stamp
                         ptx::st_release_gpu_u64(flag, 0u);
                     }
+                    __syncwarp();
                 }
                 ptx::named_barrier_sync(1, 32 * kRagEpiWarps);
             }
-            // 32 columns of the finished tile: the accumulator plus the other workers' partials, lowest first
+            // 32 columns of the finished tile: the accumulator plus the other workers' partials, lowest first,
+            // four workers' loads in flight
             auto chunk32 = [&](uint32_t c, uint32_t (&r)[32]) {
                 ptx::tmem_ld_32x32b_x32_wait(t_col + 32u * c, r);
                 if (MODE == kLoraY) spoil(c, r);
                 if (MODE != kTN && split) {
-                    const uint64_t iters = uint64_t(walk.total) * s.kb;
-                    for (uint32_t w = w_lo; w < walk.worker; ++w) {
-                        if (walk.run_begin(w, iters) == walk.run_begin(w + 1u, iters)) continue;
-                        const float *src = p.partials + size_t(w * CG + rank) * kSlot + piece + c * 1024u;
 #pragma unroll
-                        for (int j = 0; j < 8; ++j) {
-                            const float4 v = ptx::ld_global_cg_f4(src + j * 128);
-                            r[4 * j] = __float_as_uint(__uint_as_float(r[4 * j]) + v.x);
-                            r[4 * j + 1] = __float_as_uint(__uint_as_float(r[4 * j + 1]) + v.y);
-                            r[4 * j + 2] = __float_as_uint(__uint_as_float(r[4 * j + 2]) + v.z);
-                            r[4 * j + 3] = __float_as_uint(__uint_as_float(r[4 * j + 3]) + v.w);
+                    for (int h = 0; h < 2; ++h) {
+                        if (2u * c + uint32_t(h) >= halves) continue;
+                        for (uint32_t w = w_lo; w < walk.worker; w += 4u) {
+                            float4 v[4][4];
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                const float *src = p.partials + size_t((w + i) * CG + rank) * kSlot + piece + c * 1024u + h * 512;
+#pragma unroll
+                                for (int j = 0; j < 4; ++j)
+                                    v[i][j] = w + i < walk.worker ? ptx::ld_global_cg_f4(src + j * 128) : make_float4(0.f, 0.f, 0.f, 0.f);
+                            }
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                                for (int j = 0; j < 4; ++j) {
+                                    uint32_t *q = r + 16 * h + 4 * j;
+                                    q[0] = __float_as_uint(__uint_as_float(q[0]) + v[i][j].x);
+                                    q[1] = __float_as_uint(__uint_as_float(q[1]) + v[i][j].y);
+                                    q[2] = __float_as_uint(__uint_as_float(q[2]) + v[i][j].z);
+                                    q[3] = __float_as_uint(__uint_as_float(q[3]) + v[i][j].w);
+                                }
                         }
                     }
                 }
@@ -908,28 +976,32 @@ __global__ void __launch_bounds__(kRagThreads, 1) gemm_ragged_kernel(const __gri
         if (MODE == kTN && lane == 0) ptx::bulk_wait_group<0>();
     } else if constexpr (Cfg::kHelper) {
         // ------------------------------------------------ helper
+        // Two warps that share a stage's rows and never wait for each other: `fixed` counts them both.
         const uint32_t tid = threadIdx.x - 192u;
+        const uint32_t half = tid >> 5;
         uint32_t fills = 0, tail_uses = 0, adapted = 0;
-        // every helper thread waits on the barrier itself; they leave together
-        auto wait_all = [&](bool ok) { return ptx::named_barrier_and(2, kRagHelpers, ok); };
+        if (MODE == kLoraY && p.late) ptx::griddep_wait();
+        auto wait_tail = [&](uint32_t stage) {
+            const bool ok = ragged_wait_warp<1>(bar_tail(stage), (tail_uses >> stage) & 1u, p, abort_flag, kRagErrTail);
+            tail_uses ^= 1u << stage;
+            return ok;
+        };
+        auto hand_over = [&](uint32_t stage) {
+            ptx::fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+                if constexpr (CG == 1) ptx::mbar_arrive(bar_fixed(stage));
+                else ptx::mbar_arrive_cluster(ptx::map_to_rank(bar_fixed(stage), 0u));
+            }
+        };
         walk.each([&](const RaggedSeg &s) {
             const uint32_t hq = s.nq / CG;
             const uint32_t first = fills;
             fills += s.hi - s.lo;
-            auto hand_over = [&](uint32_t stage) {
-                ptx::fence_proxy_async_smem();
-                ptx::named_barrier_sync(2, kRagHelpers);
-                if (tid == 0) {
-                    if constexpr (CG == 1) ptx::mbar_arrive(bar_fixed(stage));
-                    else ptx::mbar_arrive_cluster(ptx::map_to_rank(bar_fixed(stage), 0u));
-                }
-            };
             if constexpr (MODE == kTN) {
                 if (!fixed_block(s, s.kb - 1u)) return true;
                 const uint32_t stage = (fills - 1u) % STAGES;
-                if (!wait_all(ragged_wait<1>(bar_tail(stage), (tail_uses >> stage) & 1u, p, abort_flag, kRagErrTail)))
-                    return false;
-                tail_uses ^= 1u << stage;
+                if (!wait_tail(stage)) return false;
                 const uint32_t from = s.krows % kRagBlockK, to = (from + 15u) & ~15u;
                 const uint32_t boxes = (hq + 63u) / 64u;
                 const uint32_t lines = (to - from) * 8u;  // 16-byte pieces of the rows to clear, per 64-column box
@@ -943,52 +1015,62 @@ __global__ void __launch_bounds__(kRagThreads, 1) gemm_ragged_kernel(const __gri
                 hand_over(stage);
             } else {
                 // adapter blocks: rows of this CTA's part of the tile, u where the row has the slot's adapter
+                if (s.hi <= max(s.lo, p.k_blocks)) return true;
+                constexpr uint32_t kMine = (Cfg::kQCta + kRagHelpers - 1) / kRagHelpers;  // rows of a thread
                 const uint32_t row0 = s.q0 + rank * hq;
-                int32_t id[(Cfg::kQCta + kRagHelpers - 1) / kRagHelpers];
+                int32_t id[kMine];
+                uint4 u[kMine][8];  // the first 64 of u's columns, loaded once for all slots
 #pragma unroll
-                for (uint32_t i = 0; i < sizeof(id) / sizeof(id[0]); ++i) {
+                for (uint32_t i = 0; i < kMine; ++i) {
                     const uint32_t t = tid + i * kRagHelpers;
                     id[i] = (t < hq && rank * hq + t < s.qn) ? p.ids[row0 + t] : -1;
+                    const uint4 *src = reinterpret_cast<const uint4 *>(static_cast<const char *>(p.u) +
+                                                                       size_t(row0 + t) * p.rank * 2u);
+#pragma unroll
+                    for (uint32_t c = 0; c < 8u; ++c)
+                        u[i][c] = (uint32_t(id[i]) < p.adapters && 8u * c < p.rank) ? src[c] : make_uint4(0u, 0u, 0u, 0u);
                 }
-                if (s.hi <= max(s.lo, p.k_blocks)) return true;
-                // the table of b rows with infinities is free once the epilogue is done with the tile before last
+                // the table of b rows with infinities is free once the epilogue is done with the tile before last;
+                // each warp keeps the words of its own rows, t / 32 = half and half + 2
                 const uint32_t bad_buf = adapted & 1u;
-                if (!wait_all(ragged_wait<1>(bar_bad_free(bad_buf), ((adapted >> 1) & 1u) ^ 1u, p, abort_flag, kRagErrFixed)))
+                if (!ragged_wait_warp<1>(bar_bad_free(bad_buf), ((adapted >> 1) & 1u) ^ 1u, p, abort_flag, kRagErrFixed))
                     return false;
                 ++adapted;
                 uint32_t *mask = reinterpret_cast<uint32_t *>(smem + Cfg::kOffBad + bad_buf * Cfg::kBadBytes);
-                for (uint32_t i = tid; i < Cfg::kBadBytes / 4u; i += kRagHelpers) mask[i] = 0u;
-                if (tid == 0) any_bad[bad_buf] = 0u;
-                ptx::named_barrier_sync(2, kRagHelpers);
+                for (uint32_t i = lane; i < uint32_t(tab_row[s.g]); i += 32u) mask[4u * i + half] = mask[4u * i + half + 2u] = 0u;
+                if (lane == 0) any_bad[2u * bad_buf + half] = 0u;
+                __syncwarp();
                 const uint32_t expo = p.bf16 ? 0x7F80u : 0x7C00u;  // all ones: infinity or NaN
+                uint32_t stage = (first + max(s.lo, p.k_blocks) - s.lo) % STAGES;
                 for (uint32_t kb = max(s.lo, p.k_blocks); kb < s.hi; ++kb) {
-                    const uint32_t f = first + (kb - s.lo);
-                    const uint32_t stage = f % STAGES;
-                    // b has landed, so the stage is free: the producer waited for that.  (The stage's empty barrier
-                    // cannot be waited for here: it may be more than one phase away.)
-                    if (!wait_all(ragged_wait<1>(bar_tail(stage), (tail_uses >> stage) & 1u, p, abort_flag, kRagErrTail)))
-                        return false;
-                    tail_uses ^= 1u << stage;
                     const uint32_t e = kb - p.k_blocks;
-                    const uint32_t slot = e / p.rank_blocks;
+                    const uint32_t slot = p.rank_blocks == 1u ? e : e / p.rank_blocks;
                     const uint32_t r0 = (e - slot * p.rank_blocks) * kRagBlockK;
-                    const int32_t adapter = p.list[size_t(s.g) * p.per + slot];
+                    const int32_t adapter = list[size_t(s.g) * p.per + slot];
                     const uint32_t chunks = 2u * steps_of(s, kb);
                     const uint32_t q_at = base + Cfg::kOffQ + stage * Cfg::kQBytes;
+                    // b has landed, so the stage is free: the producer waited for that.  (The stage's empty barrier
+                    // cannot be waited for here: it may be more than one phase away.)
+                    if (!wait_tail(stage)) return false;
 #pragma unroll
-                    for (uint32_t i = 0; i < sizeof(id) / sizeof(id[0]); ++i) {
+                    for (uint32_t i = 0; i < kMine; ++i) {
                         const uint32_t t = tid + i * kRagHelpers;
                         if (t >= hq) continue;
                         const bool mine = id[i] == adapter;
                         const uint4 *src = reinterpret_cast<const uint4 *>(static_cast<const char *>(p.u) +
                                                                            (size_t(row0 + t) * p.rank + r0) * 2u);
-                        for (uint32_t c = 0; c < chunks; ++c) {
-                            const uint4 v = (mine && r0 + 8u * c < p.rank) ? src[c] : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+                        for (uint32_t c = 0; c < 8u; ++c) {
+                            if (c >= chunks) continue;
+                            uint4 v = u[i][c];
+                            if (r0 != 0u && mine && r0 + 8u * c < p.rank) v = src[c];
+                            if (!mine || r0 + 8u * c >= p.rank) v = make_uint4(0u, 0u, 0u, 0u);
                             ptx::st_shared_v4(q_at + t * 128u + ((c ^ (t & 7u)) << 4), v.x, v.y, v.z, v.w);
                         }
                     }
                     // b's rows: zeros for infinities and NaN, which the other adapters' zero rows of u would turn into NaN
                     const uint32_t p_at = base + Cfg::kOffP + stage * Cfg::kPBytes;
+#pragma unroll
                     for (uint32_t t = tid; t < 128u; t += kRagHelpers) {
                         for (uint32_t c = 0; c < chunks; ++c) {
                             const uint32_t at = p_at + t * 128u + ((c ^ (t & 7u)) << 4);
@@ -1004,11 +1086,12 @@ __global__ void __launch_bounds__(kRagThreads, 1) gemm_ragged_kernel(const __gri
                             if (bad) {
                                 ptx::st_shared_v4(at, w[0], w[1], w[2], w[3]);
                                 atomicOr(mask + 4u * slot + (t >> 5), 1u << (t & 31u));
-                                any_bad[bad_buf] = 1u;
+                                any_bad[2u * bad_buf + half] = 1u;
                             }
                         }
                     }
                     hand_over(stage);
+                    if (++stage == STAGES) stage = 0;
                 }
             }
             return true;
@@ -1017,6 +1100,8 @@ __global__ void __launch_bounds__(kRagThreads, 1) gemm_ragged_kernel(const __gri
 
     // ---------------------------------------------------- teardown
     ptx::griddep_launch_dependents();
+    // (a kernel that ends counts as the end of those before it)
+    if (MODE == kLoraY && p.late) ptx::griddep_wait();
     __syncwarp();
     ptx::tc_fence_before_sync();
     if constexpr (CG == 2) ptx::cluster_sync();
@@ -1033,17 +1118,93 @@ __global__ void __launch_bounds__(kRagThreads, 1) gemm_ragged_kernel(const __gri
     if (warp == 1) ptx::tmem_dealloc<CG>(tmem_base, Cfg::kTmemCols);
 }
 
+// u = scale x a^T for few rows, one block per row and four of its u's: four warps share k, each lane adds
+// products of 8 elements at a time in fp32.  Bound by the latency of one pass over a's rows; it runs beside the
+// product that follows it, which waits for it only where it reads u.
+struct LoraShrinkParams {
+    const void *x, *a;
+    const int32_t *ids;
+    const float *scale;
+    void *u;
+    uint32_t k, rank, adapters, bf16;
+};
+
+__device__ __forceinline__ float2 ragged_unpack(uint32_t w, bool bf16)
+{
+    if (bf16) return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+    return __half22float2(*reinterpret_cast<const __half2 *>(&w));
+}
+
+__global__ void __launch_bounds__(128) lora_shrink_kernel(const __grid_constant__ LoraShrinkParams p)
+{
+    __shared__ float s_sum[4][4];
+    ptx::griddep_wait();
+    // (after the wait: what the next kernel reads from before this one is complete as well)
+    ptx::griddep_launch_dependents();
+    const uint32_t row = blockIdx.y, r0 = blockIdx.x * 4u;
+    const uint32_t lane = threadIdx.x & 31u, warp = threadIdx.x >> 5;
+    const int32_t id = p.ids[row];
+    if (uint32_t(id) >= p.adapters) return;
+    const bool bf16 = p.bf16 != 0u;
+    const uint4 *x = reinterpret_cast<const uint4 *>(static_cast<const char *>(p.x) + size_t(row) * p.k * 2u);
+    const char *a = static_cast<const char *>(p.a) + (size_t(id) * p.rank + r0) * p.k * 2u;
+    float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 2
+    for (uint32_t i = threadIdx.x; i < p.k / 8u; i += 128u) {
+        const uint4 xv = x[i];
+        uint4 av[4];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) av[r] = reinterpret_cast<const uint4 *>(a + size_t(r) * p.k * 2u)[i];
+        const uint32_t xw[4] = {xv.x, xv.y, xv.z, xv.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const float2 xf = ragged_unpack(xw[j], bf16);
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const uint32_t aw = j == 0 ? av[r].x : j == 1 ? av[r].y : j == 2 ? av[r].z : av[r].w;
+                const float2 af = ragged_unpack(aw, bf16);
+                sum[r] = fmaf(xf.x, af.x, sum[r]);
+                sum[r] = fmaf(xf.y, af.y, sum[r]);
+            }
+        }
+    }
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) sum[r] += __shfl_xor_sync(0xffffffffu, sum[r], d);
+    if (lane == 0)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) s_sum[warp][r] = sum[r];
+    __syncthreads();
+    if (threadIdx.x < 2u) {
+        const float mul = p.scale ? p.scale[id] : 1.0f;
+        float v[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const uint32_t r = threadIdx.x * 2u + uint32_t(h);
+            v[h] = ((s_sum[0][r] + s_sum[1][r]) + (s_sum[2][r] + s_sum[3][r])) * mul;
+        }
+        reinterpret_cast<uint32_t *>(static_cast<char *>(p.u) + (size_t(row) * p.rank + r0) * 2u)[threadIdx.x] =
+            ragged_pack(v[0], v[1], bf16);
+    }
+}
+
 // The adapters present in each tile of `per` rows (per <= 256), in order of first appearance: one block per
 // tile.  Rows with an id outside [0, adapters) have none.
-__global__ void __launch_bounds__(256) lora_plan_kernel(const int32_t *ids, uint32_t rows, uint32_t per, uint32_t adapters,
-                                                        int32_t *counts, int32_t *list)
+struct LoraListParams {
+    const int32_t *ids;
+    uint32_t rows, per, adapters;
+    int32_t *counts, *list;
+};
+
+__global__ void __launch_bounds__(256) lora_list_kernel(const __grid_constant__ LoraListParams p)
 {
     __shared__ __align__(16) int32_t s_id[256];
     __shared__ uint32_t s_warp[8];
     ptx::griddep_wait();
-    const uint32_t t = threadIdx.x, row = blockIdx.x * per + t;
-    int32_t id = (t < per && row < rows) ? ids[row] : -1;
-    if (uint32_t(id) >= adapters) id = -1;
+    const uint32_t t = threadIdx.x, row = blockIdx.x * p.per + t;
+    int32_t id = (p.adapters != 0u && t < p.per && row < p.rows) ? p.ids[row] : -1;
+    if (uint32_t(id) >= p.adapters) id = -1;
     s_id[t] = id;
     __syncthreads();
     // the first row with its id: every earlier one differs (four at a time, the same words for the whole warp)
@@ -1060,8 +1221,8 @@ __global__ void __launch_bounds__(256) lora_plan_kernel(const int32_t *ids, uint
         if (w < (t >> 5)) at += s_warp[w];
         total += s_warp[w];
     }
-    if (first) list[size_t(blockIdx.x) * per + at] = id;
-    if (t == 0) counts[blockIdx.x] = int32_t(total);
+    if (first) p.list[size_t(blockIdx.x) * p.per + at] = id;
+    if (t == 0) p.counts[blockIdx.x] = int32_t(total);
     ptx::griddep_launch_dependents();
 }
 

@@ -80,33 +80,41 @@ def _dtype(t, f32=False):
     raise ValueError("operands must be float16 or bfloat16%s, got %s" % (" or float32" if f32 else "", t))
 
 
-def _need(t, what, shape, dtype, device):
-    """`t` must be a contiguous CUDA tensor of this shape, type and device."""
-    if (tuple(t.shape) != tuple(shape) or t.dtype is not dtype or not t.is_cuda or t.device != device
-            or not t.is_contiguous()):
-        raise ValueError("%s must be a contiguous %s tensor of shape %s on %s" % (what, dtype, list(shape), device))
+def _need(t, what, shape, dtype, dev):
+    """`t` must be a contiguous tensor of this shape and type on CUDA device number `dev`."""
+    if t.shape != shape or t.dtype is not dtype or t.get_device() != dev or not t.is_contiguous():
+        raise ValueError("%s must be a contiguous %s tensor of shape %s on cuda:%d" % (what, dtype, list(shape), dev))
 
 
 def _operand(t, what, dims):
-    if t.dim() != dims or not t.is_cuda or not t.is_contiguous():
+    """The device number of a contiguous tensor on the current CUDA device."""
+    dev = t.get_device()
+    if dev < 0 or t.dim() != dims or not t.is_contiguous():
         raise ValueError("%s must be a contiguous CUDA tensor with %d dimensions" % (what, dims))
-    if t.device.index != _gemm._tm().cuda.current_device():
+    if dev != _gemm._tm()._C._cuda_getDevice():
         raise ValueError("%s must be on the current device" % what)
+    return dev
 
 
-def _out(t, what, shape, dtype, device):
+def _out(t, what, shape, dtype, like, dev):
     if t is None:
-        return _gemm._tm().empty(shape, dtype=dtype, device=device)
-    _need(t, what, shape, dtype, device)
+        return like.new_empty(shape, dtype=dtype)
+    _need(t, what, shape, dtype, dev)
     return t
 
 
-def _workspace(ws):
+def _workspace(ws, dev):
     if ws is None:
         return None, 0
-    if not ws.is_cuda or not ws.is_contiguous():
-        raise ValueError("workspace must be a contiguous CUDA tensor")
-    return ws.data_ptr(), ws.numel() * ws.element_size()
+    if ws.get_device() != dev or not ws.is_contiguous():
+        raise ValueError("workspace must be a contiguous CUDA tensor on cuda:%d" % dev)
+    return ws.data_ptr(), ws.nbytes
+
+
+def _stream(stream, dev):
+    if stream is None:
+        return _gemm._tm()._C._cuda_getCurrentRawStream(dev)
+    return _gemm._stream(stream)
 
 
 def _size(name, *args):
@@ -121,10 +129,10 @@ def gemm_grouped_workspace_size(groups, rows, n, k):
     return _size("gemm_grouped_workspace_size", groups, rows, n, k)
 
 
-def _offsets(offsets, device):
+def _offsets(offsets, dev):
     if offsets.dim() != 1 or offsets.shape[0] < 1:
         raise ValueError("offsets must hold groups + 1 numbers")
-    _need(offsets, "offsets", offsets.shape, _gemm._tm().int32, device)
+    _need(offsets, "offsets", offsets.shape, _gemm._tm().int32, dev)
     return offsets.shape[0] - 1
 
 
@@ -132,33 +140,37 @@ def gemm_grouped_nt(x, w, offsets, y=None, workspace=None, stream=None):
     """y[t] = x[t] . w[g]^T for the rows t in [offsets[g], offsets[g + 1]); rows of no group are zero.
 
     x [rows, k], w [groups, n, k], offsets [groups + 1] int32 on the device; returns y [rows, n]."""
-    _operand(x, "x", 2)
-    groups, rows, k = _offsets(offsets, x.device), x.shape[0], x.shape[1]
+    dev, kind = _operand(x, "x", 2), x.dtype
+    groups = _offsets(offsets, dev)
+    rows, k = x.shape
     if w.dim() != 3:
         raise ValueError("w must be [groups, n, k]")
     n = w.shape[1]
-    _need(w, "w", (groups, n, k), x.dtype, x.device)
-    kind = _dtype(x.dtype)
-    y = _out(y, "y", (rows, n), x.dtype, x.device)
-    ws, ws_bytes = _workspace(workspace)
-    _check(lib().gemm_grouped_nt(kind, groups, rows, n, k, offsets.data_ptr(), x.data_ptr(), w.data_ptr(), y.data_ptr(), ws,
-                                 ws_bytes, _gemm._stream(stream)), "gemm_grouped_nt")
+    _need(w, "w", (groups, n, k), kind, dev)
+    code = _dtype(kind)
+    y = _out(y, "y", (rows, n), kind, x, dev)
+    ws, ws_bytes = _workspace(workspace, dev)
+    st = lib().gemm_grouped_nt(code, groups, rows, n, k, offsets.data_ptr(), x.data_ptr(), w.data_ptr(), y.data_ptr(), ws,
+                               ws_bytes, _stream(stream, dev))
+    _check(st, "gemm_grouped_nt")
     return y
 
 
 def gemm_grouped_nn(dy, w, offsets, dx=None, workspace=None, stream=None):
     """dx[t] = dy[t] . w[g]: the gradient of gemm_grouped_nt's rows.  dy [rows, n]; returns dx [rows, k]."""
-    _operand(dy, "dy", 2)
-    groups, rows, n = _offsets(offsets, dy.device), dy.shape[0], dy.shape[1]
+    dev, kind = _operand(dy, "dy", 2), dy.dtype
+    groups = _offsets(offsets, dev)
+    rows, n = dy.shape
     if w.dim() != 3:
         raise ValueError("w must be [groups, n, k]")
     k = w.shape[2]
-    _need(w, "w", (groups, n, k), dy.dtype, dy.device)
-    kind = _dtype(dy.dtype)
-    dx = _out(dx, "dx", (rows, k), dy.dtype, dy.device)
-    ws, ws_bytes = _workspace(workspace)
-    _check(lib().gemm_grouped_nn(kind, groups, rows, n, k, offsets.data_ptr(), dy.data_ptr(), w.data_ptr(), dx.data_ptr(), ws,
-                                 ws_bytes, _gemm._stream(stream)), "gemm_grouped_nn")
+    _need(w, "w", (groups, n, k), kind, dev)
+    code = _dtype(kind)
+    dx = _out(dx, "dx", (rows, k), kind, dy, dev)
+    ws, ws_bytes = _workspace(workspace, dev)
+    st = lib().gemm_grouped_nn(code, groups, rows, n, k, offsets.data_ptr(), dy.data_ptr(), w.data_ptr(), dx.data_ptr(), ws,
+                               ws_bytes, _stream(stream, dev))
+    _check(st, "gemm_grouped_nn")
     return dx
 
 
@@ -166,32 +178,37 @@ def gemm_grouped_tn(dy, x, offsets, dw=None, dtype=None, workspace=None, stream=
     """dw[g] = dy_g^T . x_g: the gradient of gemm_grouped_nt's weights, zero for a group without rows.
 
     dy [rows, n], x [rows, k]; returns dw [groups, n, k] in `dtype` (the operands' type, or torch.float32)."""
-    _operand(dy, "dy", 2)
-    groups, rows, n = _offsets(offsets, dy.device), dy.shape[0], dy.shape[1]
+    dev, kind = _operand(dy, "dy", 2), dy.dtype
+    groups = _offsets(offsets, dev)
+    rows, n = dy.shape
     if x.dim() != 2:
         raise ValueError("x must be [rows, k]")
     k = x.shape[1]
-    _need(x, "x", (rows, k), dy.dtype, dy.device)
-    kind = _dtype(dy.dtype)
+    _need(x, "x", (rows, k), kind, dev)
+    code = _dtype(kind)
     if dtype is None:
-        dtype = dy.dtype if dw is None else dw.dtype
-    if dtype is not dy.dtype and dtype is not _gemm._tm().float32:
+        dtype = kind if dw is None else dw.dtype
+    if dtype is not kind and dtype is not _gemm._tm().float32:
         raise ValueError("dw must have the operands' type or float32")
-    dw = _out(dw, "dw", (groups, n, k), dtype, dy.device)
-    ws, ws_bytes = _workspace(workspace)
-    _check(lib().gemm_grouped_tn(kind, _dtype(dtype, f32=True), groups, rows, n, k, offsets.data_ptr(), dy.data_ptr(),
-                                 x.data_ptr(), dw.data_ptr(), ws, ws_bytes, _gemm._stream(stream)), "gemm_grouped_tn")
+    dw = _out(dw, "dw", (groups, n, k), dtype, dy, dev)
+    ws, ws_bytes = _workspace(workspace, dev)
+    st = lib().gemm_grouped_tn(code, _dtype(dtype, f32=True), groups, rows, n, k, offsets.data_ptr(), dy.data_ptr(),
+                               x.data_ptr(), dw.data_ptr(), ws, ws_bytes, _stream(stream, dev))
+    _check(st, "gemm_grouped_tn")
     return dw
 
 
 def gemm_grouped_stall_test(mode, first, second, offsets, out, workspace, skip_fill, wait_limit_cycles, stream=None):
     """Status of the failure-detection launch (mode 0, 1, 2: nt, nn, tn)."""
-    groups, rows = offsets.shape[0] - 1, first.shape[0]
+    dev = _operand(first, "first", 2)
+    groups, rows = _offsets(offsets, dev), first.shape[0]
     n, k = (second.shape[1], second.shape[2]) if mode < 2 else (first.shape[1], second.shape[1])
-    ws, ws_bytes = _workspace(workspace)
+    _need(second, "second", (groups, n, k) if mode < 2 else (rows, k), first.dtype, dev)
+    _need(out, "out", ((rows, n), (rows, k), (groups, n, k))[mode], first.dtype, dev)
+    ws, ws_bytes = _workspace(workspace, dev)
     return lib().gemm_grouped_stall_test(mode, _dtype(first.dtype), groups, rows, n, k, offsets.data_ptr(), first.data_ptr(),
                                          second.data_ptr(), out.data_ptr(), ws, ws_bytes, skip_fill, wait_limit_cycles,
-                                         _gemm._stream(stream))
+                                         _stream(stream, dev))
 
 
 # ------------------------------------------------------------------- adapters
@@ -206,23 +223,25 @@ def gemm_lora_nt(x, w, a, b, ids, scale=None, y=None, workspace=None, stream=Non
     x [rows, k], w [n, k], a [adapters, rank, k], b [adapters, n, rank], ids [rows] int32, scale [adapters] float32 or
     None for 1; returns y [rows, n].  The workspace (gemm_lora_workspace_size) is required."""
     torch = _gemm._tm()
-    _operand(x, "x", 2)
+    dev, kind = _operand(x, "x", 2), x.dtype
     rows, k = x.shape
     if w.dim() != 2 or a.dim() != 3:
         raise ValueError("w must be [n, k] and a [adapters, rank, k]")
-    n, adapters, rank = w.shape[0], a.shape[0], a.shape[1]
-    _need(w, "w", (n, k), x.dtype, x.device)
-    _need(a, "a", (adapters, rank, k), x.dtype, x.device)
-    _need(b, "b", (adapters, n, rank), x.dtype, x.device)
-    _need(ids, "ids", (rows,), torch.int32, x.device)
+    n = w.shape[0]
+    adapters, rank, _ = a.shape
+    _need(w, "w", (n, k), kind, dev)
+    _need(a, "a", (adapters, rank, k), kind, dev)
+    _need(b, "b", (adapters, n, rank), kind, dev)
+    _need(ids, "ids", (rows,), torch.int32, dev)
     if scale is not None:
-        _need(scale, "scale", (adapters,), torch.float32, x.device)
-    kind = _dtype(x.dtype)
-    y = _out(y, "y", (rows, n), x.dtype, x.device)
-    ws, ws_bytes = _workspace(workspace)
-    _check(lib().gemm_lora_nt(kind, rows, n, k, rank, adapters, x.data_ptr(), w.data_ptr(), a.data_ptr(), b.data_ptr(),
-                              ids.data_ptr(), None if scale is None else scale.data_ptr(), y.data_ptr(), ws, ws_bytes,
-                              _gemm._stream(stream)), "gemm_lora_nt")
+        _need(scale, "scale", (adapters,), torch.float32, dev)
+    code = _dtype(kind)
+    y = _out(y, "y", (rows, n), kind, x, dev)
+    ws, ws_bytes = _workspace(workspace, dev)
+    st = lib().gemm_lora_nt(code, rows, n, k, rank, adapters, x.data_ptr(), w.data_ptr(), a.data_ptr(), b.data_ptr(),
+                            ids.data_ptr(), None if scale is None else scale.data_ptr(), y.data_ptr(), ws, ws_bytes,
+                            _stream(stream, dev))
+    _check(st, "gemm_lora_nt")
     return y
 
 
@@ -239,38 +258,57 @@ def gemm_route_topk(logits, top, renorm=True, out=None, workspace=None, stream=N
     [experts + 1] and order [rows * top] (choices t * top + j sorted by expert).  The weights are softmax(logits) at
     ids, divided by their sum if `renorm`.  `out`: a Routing of tensors to write into."""
     torch = _gemm._tm()
-    _operand(logits, "logits", 2)
+    dev = _operand(logits, "logits", 2)
     rows, experts = logits.shape
-    kind = _dtype(logits.dtype, f32=True)
-    dev = logits.device
+    code = _dtype(logits.dtype, f32=True)
     top = int(top)
-    shapes = Routing((rows, top), (rows, top), (experts + 1,), (rows * top,), (rows, top))
-    kinds = Routing(torch.int32, torch.float32, torch.int32, torch.int32, torch.int32)
     if top < 1 or top > experts:
         raise ValueError("top must be in [1, experts]")
-    given = out if out is not None else Routing(None, None, None, None, None)
-    r = Routing(*(_out(t, name, shape, k, dev) for t, name, shape, k in zip(given, Routing._fields, shapes, kinds)))
-    ws, ws_bytes = _workspace(workspace)
-    _check(lib().gemm_route_topk(kind, rows, experts, top, int(bool(renorm)), logits.data_ptr(), r.ids.data_ptr(),
-                                 r.weights.data_ptr(), r.offsets.data_ptr(), r.order.data_ptr(), r.position.data_ptr(), ws,
-                                 ws_bytes, _gemm._stream(stream)), "gemm_route_topk")
+    i32 = torch.int32
+    if out is None:
+        # one allocation for the five: each part starts on a 16-byte boundary
+        c = rows * top
+        pad, eo = (c + 3) & ~3, (experts + 4) & ~3
+        buf = logits.new_empty(4 * pad + eo, dtype=i32)
+        at = buf.data_ptr()
+        ids_at, weights_at, position_at, order_at, offsets_at = at, at + 4 * pad, at + 8 * pad, at + 12 * pad, at + 16 * pad
+        r = None
+    else:
+        r = out
+        _need(r.ids, "ids", (rows, top), i32, dev)
+        _need(r.weights, "weights", (rows, top), torch.float32, dev)
+        _need(r.offsets, "offsets", (experts + 1,), i32, dev)
+        _need(r.order, "order", (rows * top,), i32, dev)
+        _need(r.position, "position", (rows, top), i32, dev)
+        ids_at, weights_at, offsets_at, order_at, position_at = (t.data_ptr() for t in (r.ids, r.weights, r.offsets, r.order,
+                                                                                        r.position))
+    ws, ws_bytes = _workspace(workspace, dev)
+    st = lib().gemm_route_topk(code, rows, experts, top, 1 if renorm else 0, logits.data_ptr(), ids_at, weights_at, offsets_at,
+                               order_at, position_at, ws, ws_bytes, _stream(stream, dev))
+    _check(st, "gemm_route_topk")
+    if r is None:
+        # (the views are made while the GPU already works)
+        shape, steps = (rows, top), (top, 1)
+        r = Routing(buf.as_strided(shape, steps, 0), buf.view(torch.float32).as_strided(shape, steps, pad),
+                    buf.as_strided((experts + 1,), (1,), 4 * pad), buf.as_strided((c,), (1,), 3 * pad),
+                    buf.as_strided(shape, steps, 2 * pad))
     return r
 
 
 def gemm_route_topk_grad(logits, ids, weights, dweights, renorm=True, dlogits=None, stream=None):
     """The gradient of the logits [rows, experts] float32 from that of gemm_route_topk's weights."""
     torch = _gemm._tm()
-    _operand(logits, "logits", 2)
+    dev = _operand(logits, "logits", 2)
     rows, experts = logits.shape
-    kind = _dtype(logits.dtype, f32=True)
+    code = _dtype(logits.dtype, f32=True)
     if ids.dim() != 2:
         raise ValueError("ids must be [rows, top]")
-    top = ids.shape[1]
-    _need(ids, "ids", (rows, top), torch.int32, logits.device)
-    _need(weights, "weights", (rows, top), torch.float32, logits.device)
-    _need(dweights, "dweights", (rows, top), torch.float32, logits.device)
-    dlogits = _out(dlogits, "dlogits", (rows, experts), torch.float32, logits.device)
-    _check(lib().gemm_route_topk_grad(kind, rows, experts, top, int(bool(renorm)), logits.data_ptr(), ids.data_ptr(),
-                                      weights.data_ptr(), dweights.data_ptr(), dlogits.data_ptr(), _gemm._stream(stream)),
-           "gemm_route_topk_grad")
+    shape = ids.shape
+    _need(ids, "ids", (rows, shape[1]), torch.int32, dev)
+    _need(weights, "weights", shape, torch.float32, dev)
+    _need(dweights, "dweights", shape, torch.float32, dev)
+    dlogits = _out(dlogits, "dlogits", (rows, experts), torch.float32, logits, dev)
+    st = lib().gemm_route_topk_grad(code, rows, experts, shape[1], 1 if renorm else 0, logits.data_ptr(), ids.data_ptr(),
+                                    weights.data_ptr(), dweights.data_ptr(), dlogits.data_ptr(), _stream(stream, dev))
+    _check(st, "gemm_route_topk_grad")
     return dlogits
