@@ -163,6 +163,30 @@ gemm_status_t encode_stack(CUtensorMap *map, const void *ptr, gemm_dtype_t dtype
     return r == CUDA_SUCCESS ? GEMM_OK : GEMM_ERR_UNSUPPORTED_SHAPE;
 }
 
+// `count` row-major matrices of rows x (64 groups + rest) columns, as (64 columns, row, group, matrix): boxes of two
+// groups x 64 rows.
+gemm_status_t encode_pairs(CUtensorMap *map, const void *ptr, gemm_dtype_t dtype, int64_t count, int64_t rows, int64_t cols,
+                           uint32_t *groups)
+{
+    *groups = uint32_t(cols / 64);
+    if (cols < 128) {
+        *groups = 0;
+        return GEMM_OK;
+    }
+    PFN_cuTensorMapEncodeTiled_v12000 enc = nullptr;
+    gemm_status_t st = ragged_encoder(&enc);
+    if (st != GEMM_OK) return st;
+    cuuint64_t dims[4] = {64, cuuint64_t(rows), cuuint64_t(cols / 64), cuuint64_t(count)};
+    cuuint64_t strides[3] = {cuuint64_t(cols) * 2u, 128, cuuint64_t(cols) * cuuint64_t(rows) * 2u};
+    cuuint32_t box[4] = {64, 64, 2, 1};
+    cuuint32_t estr[4] = {1, 1, 1, 1};
+    const CUtensorMapDataType type =
+        dtype == GEMM_DTYPE_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+    const CUresult r = enc(map, type, 4, const_cast<void *>(ptr), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                           CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? GEMM_OK : GEMM_ERR_UNSUPPORTED_SHAPE;
+}
+
 // The N-side operand [rows, cols] in boxes of `box` rows, half and a quarter of them.
 gemm_status_t encode_rows(CUtensorMap (&maps)[3], const void *ptr, gemm_dtype_t dtype, int64_t rows, int64_t cols, int box)
 {
@@ -341,9 +365,12 @@ gemm_status_t grouped(int mode, gemm_dtype_t dtype, gemm_dtype_t out_type, int64
     if (mode == kTN) {
         st = encode_stack(&p.tm_p, first, dtype, 1, rows, n, 64, 64);
         if (st == GEMM_OK) st = encode_stack(&p.tm_q[0], second, dtype, 1, rows, k, 64, 64);
+        if (st == GEMM_OK) st = encode_pairs(&p.tm_p2, first, dtype, 1, rows, n, &p.p_groups);
+        if (st == GEMM_OK) st = encode_pairs(&p.tm_q2, second, dtype, 1, rows, k, &p.q_groups);
         if (st == GEMM_OK) st = encode_stack(&p.tm_x, out, out_type, groups, n, k, p.out32 ? 32 : 64, 32);
     } else {
         st = encode_stack(&p.tm_p, second, dtype, groups, n, k, 64, mode == kNT ? 128 : 64);
+        if (st == GEMM_OK && mode == kNN) st = encode_pairs(&p.tm_p2, second, dtype, groups, n, k, &p.p_groups);
         if (st == GEMM_OK) st = encode_rows(p.tm_q, first, dtype, rows, kdim, var.qbox);
         if (ws && few_rows(groups, rows) && most * p.k_blocks < kIterLimit) {
             use_split(&p, var, dev->slots[variant], ws);

@@ -86,6 +86,11 @@ struct RaggedParams {
     CUtensorMap tm_p;     // M-side operand
     CUtensorMap tm_q[3];  // N-side operand: boxes of a stage's whole, half and quarter N side (kTN: the first, 64 columns)
     CUtensorMap tm_x;     // kTN: the output; kLoraY: the adapters' b
+    // MN-major operands again, as (64 columns, row, column group, matrix) with boxes of two neighbouring groups of 64
+    // rows each: one copy for a CTA's 128 columns where two took 0.35 us a K block instead of 0.22.  Whole groups
+    // only: the columns from 64 * groups on, and single groups, come by tm_p and tm_q.
+    CUtensorMap tm_p2, tm_q2;
+    uint32_t p_groups, q_groups;
     const int32_t *offsets;  // [groups + 1] row offsets (kNT, kNN, kTN)
     uint32_t groups;         // groups, or row tiles (kLoraU, kLoraY)
     uint32_t rows;           // rows t
@@ -598,6 +603,8 @@ __global__ void __launch_bounds__(kRagThreads, 1) gemm_ragged_kernel(const __gri
                 const uint32_t q_bytes = Cfg::kQMn ? boxes * 8192u : quarters * uint32_t(Cfg::kQBox / 4 * 128);
                 const int32_t p0 = int32_t(s.p0 + rank * 128u);
                 const int32_t q0 = int32_t(s.q0 + rank * hq);
+                const bool p_pairs = Cfg::kPMn && uint32_t(p0) / 64u + 2u <= p.p_groups;
+                const bool q_pairs = Cfg::kQMn && hq == 128u && uint32_t(q0) / 64u + 2u <= p.q_groups;
                 for (uint32_t kb = s.lo; kb < s.hi; ++kb, ++fills) {
                     if (!ragged_wait_warp<CG>(bar_empty(stage), phase ^ 1u, p, abort_flag, kRagErrEmpty)) return false;
                     const bool fix = fixed_block(s, kb);
@@ -625,12 +632,24 @@ __global__ void __launch_bounds__(kRagThreads, 1) gemm_ragged_kernel(const __gri
                             else ptx::tma_load_3d(dst, map, fb, x, y, z);
                         };
                         const int32_t k0 = int32_t(kb * kRagBlockK);
+                        auto load2 = [&](uint32_t dst, const CUtensorMap *map, int32_t y, int32_t z, int32_t w) {
+                            if (CG == 2 && !tail) ptx::tma_load_4d_pair(dst, map, fb, 0, y, z, w);
+                            else ptx::tma_load_4d(dst, map, fb, 0, y, z, w);
+                        };
                         if constexpr (MODE == kTN) {
                             const int32_t row = int32_t(s.row0) + k0;
-                            load(p_dst, &p.tm_p, p0, row, 0);
-                            load(p_dst + 8192u, &p.tm_p, p0 + 64, row, 0);
-                            for (uint32_t b = 0; b < boxes; ++b)
-                                load(q_dst + b * 8192u, &p.tm_q[0], q0 + int32_t(64u * b), row, 0);
+                            if (p_pairs) {
+                                load2(p_dst, &p.tm_p2, row, p0 / 64, 0);
+                            } else {
+                                load(p_dst, &p.tm_p, p0, row, 0);
+                                load(p_dst + 8192u, &p.tm_p, p0 + 64, row, 0);
+                            }
+                            if (q_pairs) {
+                                load2(q_dst, &p.tm_q2, row, q0 / 64, 0);
+                            } else {
+                                for (uint32_t b = 0; b < boxes; ++b)
+                                    load(q_dst + b * 8192u, &p.tm_q[0], q0 + int32_t(64u * b), row, 0);
+                            }
                         } else if (extra) {
                             const uint32_t e = kb - p.k_blocks;
                             const uint32_t slot = e / p.rank_blocks;
@@ -638,8 +657,12 @@ __global__ void __launch_bounds__(kRagThreads, 1) gemm_ragged_kernel(const __gri
                             load(p_dst, &p.tm_x, int32_t((e - slot * p.rank_blocks) * kRagBlockK), p0, adapter);
                         } else {
                             if constexpr (MODE == kNN) {
-                                load(p_dst, &p.tm_p, p0, k0, int32_t(s.g));
-                                load(p_dst + 8192u, &p.tm_p, p0 + 64, k0, int32_t(s.g));
+                                if (p_pairs) {
+                                    load2(p_dst, &p.tm_p2, k0, p0 / 64, int32_t(s.g));
+                                } else {
+                                    load(p_dst, &p.tm_p, p0, k0, int32_t(s.g));
+                                    load(p_dst + 8192u, &p.tm_p, p0 + 64, k0, int32_t(s.g));
+                                }
                             } else {
                                 const int32_t z = MODE == kNT ? int32_t(s.g) : MODE == kLoraU ? int32_t(s.row0) : 0;
                                 load(p_dst, &p.tm_p, k0, p0, z);

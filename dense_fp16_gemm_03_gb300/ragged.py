@@ -96,9 +96,20 @@ def _operand(t, what, dims):
     return dev
 
 
-def _out(t, what, shape, dtype, like, dev):
+_devices = {}
+
+
+def _empty(shape, dtype, dev):
+    # (a device object at hand is quicker than Tensor.new_empty by more than a microsecond)
+    device = _devices.get(dev)
+    if device is None:
+        device = _devices[dev] = _gemm._tm().device("cuda", dev)
+    return _gemm._tm().empty(shape, dtype=dtype, device=device)
+
+
+def _out(t, what, shape, dtype, dev):
     if t is None:
-        return like.new_empty(shape, dtype=dtype)
+        return _empty(shape, dtype, dev)
     _need(t, what, shape, dtype, dev)
     return t
 
@@ -148,7 +159,7 @@ def gemm_grouped_nt(x, w, offsets, y=None, workspace=None, stream=None):
     n = w.shape[1]
     _need(w, "w", (groups, n, k), kind, dev)
     code = _dtype(kind)
-    y = _out(y, "y", (rows, n), kind, x, dev)
+    y = _out(y, "y", (rows, n), kind, dev)
     ws, ws_bytes = _workspace(workspace, dev)
     st = lib().gemm_grouped_nt(code, groups, rows, n, k, offsets.data_ptr(), x.data_ptr(), w.data_ptr(), y.data_ptr(), ws,
                                ws_bytes, _stream(stream, dev))
@@ -166,7 +177,7 @@ def gemm_grouped_nn(dy, w, offsets, dx=None, workspace=None, stream=None):
     k = w.shape[2]
     _need(w, "w", (groups, n, k), kind, dev)
     code = _dtype(kind)
-    dx = _out(dx, "dx", (rows, k), kind, dy, dev)
+    dx = _out(dx, "dx", (rows, k), kind, dev)
     ws, ws_bytes = _workspace(workspace, dev)
     st = lib().gemm_grouped_nn(code, groups, rows, n, k, offsets.data_ptr(), dy.data_ptr(), w.data_ptr(), dx.data_ptr(), ws,
                                ws_bytes, _stream(stream, dev))
@@ -190,7 +201,7 @@ def gemm_grouped_tn(dy, x, offsets, dw=None, dtype=None, workspace=None, stream=
         dtype = kind if dw is None else dw.dtype
     if dtype is not kind and dtype is not _gemm._tm().float32:
         raise ValueError("dw must have the operands' type or float32")
-    dw = _out(dw, "dw", (groups, n, k), dtype, dy, dev)
+    dw = _out(dw, "dw", (groups, n, k), dtype, dev)
     ws, ws_bytes = _workspace(workspace, dev)
     st = lib().gemm_grouped_tn(code, _dtype(dtype, f32=True), groups, rows, n, k, offsets.data_ptr(), dy.data_ptr(),
                                x.data_ptr(), dw.data_ptr(), ws, ws_bytes, _stream(stream, dev))
@@ -236,7 +247,7 @@ def gemm_lora_nt(x, w, a, b, ids, scale=None, y=None, workspace=None, stream=Non
     if scale is not None:
         _need(scale, "scale", (adapters,), torch.float32, dev)
     code = _dtype(kind)
-    y = _out(y, "y", (rows, n), kind, x, dev)
+    y = _out(y, "y", (rows, n), kind, dev)
     ws, ws_bytes = _workspace(workspace, dev)
     st = lib().gemm_lora_nt(code, rows, n, k, rank, adapters, x.data_ptr(), w.data_ptr(), a.data_ptr(), b.data_ptr(),
                             ids.data_ptr(), None if scale is None else scale.data_ptr(), y.data_ptr(), ws, ws_bytes,
@@ -269,7 +280,7 @@ def gemm_route_topk(logits, top, renorm=True, out=None, workspace=None, stream=N
         # one allocation for the five: each part starts on a 16-byte boundary
         c = rows * top
         pad, eo = (c + 3) & ~3, (experts + 4) & ~3
-        buf = logits.new_empty(4 * pad + eo, dtype=i32)
+        buf = _empty((4 * pad + eo,), i32, dev)
         at = buf.data_ptr()
         ids_at, weights_at, position_at, order_at, offsets_at = at, at + 4 * pad, at + 8 * pad, at + 12 * pad, at + 16 * pad
         r = None
@@ -307,7 +318,7 @@ def gemm_route_topk_grad(logits, ids, weights, dweights, renorm=True, dlogits=No
     _need(ids, "ids", (rows, shape[1]), torch.int32, dev)
     _need(weights, "weights", shape, torch.float32, dev)
     _need(dweights, "dweights", shape, torch.float32, dev)
-    dlogits = _out(dlogits, "dlogits", (rows, experts), torch.float32, logits, dev)
+    dlogits = _out(dlogits, "dlogits", (rows, experts), torch.float32, dev)
     st = lib().gemm_route_topk_grad(code, rows, experts, shape[1], 1 if renorm else 0, logits.data_ptr(), ids.data_ptr(),
                                     weights.data_ptr(), dweights.data_ptr(), dlogits.data_ptr(), _stream(stream, dev))
     _check(st, "gemm_route_topk_grad")
