@@ -267,6 +267,19 @@ size_t split_bytes(const RaggedVariant &var, int slots)
     return ctas * 128u * size_t(var.qcap) * 4u + ctas * 8u;
 }
 
+// Bytes of a tile counter and, for the weight gradient, four tensor maps per group.
+constexpr size_t kCounterBytes = 256;
+size_t counted_bytes(int mode, int64_t groups)
+{
+    return kCounterBytes + (mode == kTN ? size_t(groups) * 4u * sizeof(CUtensorMap) : 0u);
+}
+
+// Tiles are handed out one by one where there are more of them than workers and each lasts long.  32 groups of
+// 16384 rows in all, 4096 x 4096: 352 against 358 us with 64 K blocks a tile, and with uneven groups 382 against
+// 388; the weight gradient's tiles of 8 K blocks lose what they would gain, 535 against 453, because the next
+// number takes about as long to come as such a tile.
+constexpr int64_t kCountedMinBlocks = 32;
+
 void use_split(RaggedParams *p, const RaggedVariant &var, int slots, void *ws)
 {
     const size_t ctas = size_t(slots) * size_t(var.cg);
@@ -303,6 +316,12 @@ int grouped_variant(int mode, int64_t groups, int64_t rows)
     return few ? kVNnFew : kVNnWide;
 }
 
+size_t grouped_bytes(int mode, int64_t groups, int64_t rows, const RaggedDevice *dev)
+{
+    const int v = grouped_variant(mode, groups, rows);
+    return mode != kTN && few_rows(groups, rows) ? split_bytes(kRagged[v], dev->slots[v]) : counted_bytes(mode, groups);
+}
+
 gemm_status_t grouped(int mode, gemm_dtype_t dtype, gemm_dtype_t out_type, int64_t groups, int64_t rows, int64_t n, int64_t k,
                       const int32_t *offsets, const void *first, const void *second, void *out, void *ws, size_t ws_bytes,
                       uint32_t skip_fill, long long wait_limit, cudaStream_t stream)
@@ -329,7 +348,7 @@ gemm_status_t grouped(int mode, gemm_dtype_t dtype, gemm_dtype_t out_type, int64
     if (st != GEMM_OK) return st;
     const int variant = grouped_variant(mode, groups, rows);
     const RaggedVariant &var = kRagged[variant];
-    const size_t need = mode == kTN ? 0 : split_bytes(var, dev->slots[variant]);
+    const size_t need = grouped_bytes(mode, groups, rows, dev);
     if (ws != nullptr || ws_bytes != 0) {
         if (ws == nullptr || ws_bytes < need) return GEMM_ERR_WORKSPACE;
         if (reinterpret_cast<uintptr_t>(ws) & 255u) return GEMM_ERR_ALIGNMENT;
@@ -378,6 +397,30 @@ gemm_status_t grouped(int mode, gemm_dtype_t dtype, gemm_dtype_t out_type, int64
         }
     }
     if (st != GEMM_OK) return st;
+    const bool counted = ws && mode != kTN && !p.sk && most > dev->slots[variant] && p.k_blocks >= kCountedMinBlocks;
+    const bool own_maps = ws && mode == kTN;
+    if (counted || own_maps) {
+        RaggedSetupParams sp;
+        memset(&sp, 0, sizeof(sp));
+        sp.counter = static_cast<uint32_t *>(ws);
+        if (own_maps) {
+            sp.maps[0] = p.tm_p;
+            sp.maps[1] = p.tm_q[0];
+            sp.maps[2] = p.tm_p2;
+            sp.maps[3] = p.tm_q2;
+            sp.have = 3u | (p.p_groups ? 4u : 0u) | (p.q_groups ? 8u : 0u);
+            sp.offsets = offsets;
+            sp.groups = uint32_t(groups);
+            sp.rows = uint32_t(rows);
+            sp.out = reinterpret_cast<CUtensorMap *>(static_cast<char *>(ws) + kCounterBytes);
+            p.maps = sp.out;
+        }
+        if (counted) p.counter = sp.counter;
+        void *args[1] = {&sp};
+        st = launch(reinterpret_cast<const void *>(&ragged_setup_kernel), dim3(own_maps ? unsigned(groups) : 1u, 1, 1), 128, 0, 1,
+                    args, stream);
+        if (st != GEMM_OK) return st;
+    }
     return launch_ragged(variant, dev, p, most, stream);
 }
 
@@ -395,7 +438,7 @@ struct LoraPlan {
     int64_t tiles_u;
     int64_t pass_rows;     // rows of one pass: the kernels' table holds kRagMaxGroups tiles
     int variant_y;
-    size_t counts, list, counts_u, list_u, u, split, total;  // offsets
+    size_t counter, counts, list, counts_u, list_u, u, split, total;  // offsets
 };
 
 LoraPlan lora_plan(const RaggedDevice *dev, int64_t rows, int64_t rank)
@@ -415,6 +458,7 @@ LoraPlan lora_plan(const RaggedDevice *dev, int64_t rows, int64_t rank)
         at += size_t(round_up(int64_t(bytes), 256));
         return was;
     };
+    l.counter = take(kCounterBytes);
     l.counts = take(l.few ? 0 : size_t(l.tiles) * 4u);
     l.list = take(l.few ? 0 : size_t(l.tiles) * size_t(l.per) * 4u);
     l.counts_u = take(l.few ? 0 : size_t(l.tiles_u) * 4u);
@@ -442,9 +486,8 @@ gemm_status_t gemm_grouped_workspace_size(int64_t groups, int64_t rows, int64_t 
     st = ragged_device(&dev);
     if (st != GEMM_OK) return st;
     *bytes = 0;
-    for (int mode : {int(kNT), int(kNN)}) {
-        const int v = grouped_variant(mode, groups, rows);
-        const size_t need = split_bytes(kRagged[v], dev->slots[v]);
+    for (int mode : {int(kNT), int(kNN), int(kTN)}) {
+        const size_t need = grouped_bytes(mode, groups, rows, dev);
         if (need > *bytes) *bytes = need;
     }
     return GEMM_OK;
@@ -607,6 +650,7 @@ gemm_status_t gemm_lora_nt(gemm_dtype_t dtype, int64_t rows, int64_t n, int64_t 
                 lp.adapters = u.adapters;
                 lp.counts = reinterpret_cast<int32_t *>(ws + side.counts);
                 lp.list = reinterpret_cast<int32_t *>(ws + side.list);
+                lp.counter = &side == &sides[0] ? reinterpret_cast<uint32_t *>(ws + l.counter) : nullptr;
                 void *args[1] = {&lp};
                 if (!adapted && &side == &sides[1]) break;
                 st = launch(reinterpret_cast<const void *>(&lora_list_kernel), dim3(unsigned(side.tiles), 1, 1), 256, 0, 1, args, s);
@@ -630,6 +674,9 @@ gemm_status_t gemm_lora_nt(gemm_dtype_t dtype, int64_t rows, int64_t n, int64_t 
         }
         int64_t most = int64_t(p.tiles_p) * tiles;
         p.sk = 0;
+        p.counter = nullptr;
+        if (!l.few && l.tiles > 1 && most > dev->slots[l.variant_y] && p.k_blocks >= kCountedMinBlocks)
+            p.counter = reinterpret_cast<uint32_t *>(ws + l.counter);
         if (l.tiles == 1 && most * (p.k_blocks + l.per * p.rank_blocks) < kIterLimit) {
             use_split(&p, vy, dev->slots[l.variant_y], ws + l.split);
             most *= p.k_blocks;

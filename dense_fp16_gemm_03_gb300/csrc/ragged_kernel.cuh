@@ -23,24 +23,27 @@
 // past a group's end (the rows there are finite work thrown away) but never
 // write there.
 //
-// Roles (256 threads; one CTA or a CTA pair per tile):
+// Roles (352 threads; one CTA or a CTA pair per tile):
 //   warp 0      TMA producer into a STAGES-deep ring of 128-byte-swizzled stages
 //   warp 1      tensor memory and the MMA issuer (of the pair's first CTA)
 //   warps 2..5  epilogue, on one of two accumulators while the other fills
-//   warps 6, 7  helper: kTN zeroes the rows past a group's end in its last K
+//   warps 6..9  helper: kTN without maps zeroes the rows past a group's end in its last K
 //               block (both operands: a zero times an infinity of the next group
 //               would be NaN); kLoraY builds the masked u operand, and for the same
 //               reason takes infinities and NaN out of the adapter's b and has the
 //               epilogue write NaN for them into that adapter's own rows alone.  A
 //               stage that the helper touches arrives on its CTA's `tail` barrier and is
 //               released to the MMA by the `fixed` barrier.
+//   warp 10     scheduler of launches with a tile counter
 //
 // Group ends are read on the device (no host copy of them exists): every CTA
 // turns the offsets into a table of tile counts in shared memory, where all
 // roles look their tiles up.
 //
-// Walks: data-parallel (tile u on worker u mod workers), or with `sk` each
-// worker takes an equal run of all K-block iterations.  A run that stops
+// Walks: data-parallel, tile u on worker u mod workers or, given a counter, each
+// next tile on the worker that comes for it first (groups of unlike sizes make
+// tiles of unlike cost; what a tile holds does not depend on who computes it); or
+// with `sk` each worker takes an equal run of all K-block iterations.  A run that stops
 // inside a tile publishes its fp32 partial for the worker that holds the tile's
 // last K block.  Workers walk their run backwards, so they publish first and
 // wait last, and only ever for lower-numbered workers.  Sums are added in a fixed
@@ -61,10 +64,12 @@
 namespace gemm_f16 {
 
 constexpr int kRagBlockK = 64;       // 16-bit elements per 128-byte swizzled row
-constexpr int kRagThreads = 256;
+constexpr int kRagThreads = 352;
+constexpr int kRagTickets = 3;       // tiles handed out but not yet read by every role
+constexpr uint32_t kRagNoTile = 0xFFFFFFFFu;
 constexpr int kRagMaxGroups = 1024;  // entries of the shared-memory group table
 constexpr int kRagEpiWarps = 4;
-constexpr int kRagHelpers = 64;      // threads of the helper warps
+constexpr int kRagHelpers = 128;     // threads of the helper warps: one for each row of a stage's M side
 constexpr int kRagMaxSmem = 232448;  // 227 KB opt-in dynamic shared memory per CTA
 
 enum RaggedMode : int { kNT = 0, kNN = 1, kTN = 2, kLoraU = 3, kLoraY = 4 };
@@ -79,7 +84,8 @@ enum : uint32_t {
     kRagErrPartial = 6,
     kRagErrRingDrain = 7,
     kRagErrFixed = 10,   // the helper did not finish a stage in time
-    kRagErrTail = 11,    // a group's last K block did not arrive in time
+    kRagErrTail = 11,    // a group's last K block, or an adapter's b, did not arrive in time
+    kRagErrTicket = 12,  // no tile was handed out in time
 };
 
 struct RaggedParams {
@@ -115,6 +121,8 @@ struct RaggedParams {
     const void *u;           // kLoraY: u [rows, rank]
     uint32_t rank;
     uint32_t rank_blocks;    // ceil(rank / 64)
+    uint32_t *counter;       // tiles handed out beyond each worker's first (zero at the start), or null
+    const CUtensorMap *maps; // kTN: for each group tm_p, tm_q[0], tm_p2, tm_q2 that end with the group's rows, or null
     float *partials;         // sk: one 128 x QCAP fp32 tile per CTA
     uint64_t *flags;         // sk: one per CTA, `stamp` while its partial waits to be added
     uint64_t stamp;
@@ -142,8 +150,10 @@ struct RaggedCfg {
     static constexpr int kStoreBytes = (MODE == kTN) ? 4096 : 2048;
     static constexpr int kOffTabRow = kOffStore + kRagEpiWarps * kStoreBytes;
     static constexpr int kOffTabTile = kOffTabRow + 4 * (kRagMaxGroups + 4);
-    // full, empty, fixed, tail per stage; acc_full x2, acc_empty x2, drain, bad_free x2
-    static constexpr int kNumBars = 4 * STAGES + 7;
+    // full, empty, fixed, tail per stage; acc_full x2, acc_empty x2, drain, bad_free x2, ticket_full, ticket_empty, request
+    static constexpr int kNumBars = 4 * STAGES + 7 + 2 * kRagTickets + 1;
+    // warps that read a ticket: both producers, the MMA issuer, every epilogue and helper warp
+    static constexpr int kReaders = 1 + CG * (1 + kRagEpiWarps + (kHelper ? kRagHelpers / 32 : 0));
     // kLoraY: for each of two tiles in flight, 128 bits per adapter of the tile (b rows that hold an infinity or
     // NaN), and for each helper warp whether it found any
     static constexpr int kOffBad = kOffTabTile + 4 * (kRagMaxGroups + 4);
@@ -154,7 +164,8 @@ struct RaggedCfg {
     static constexpr int kOffTmemSlot = kOffRec + STAGES * 16;
     static constexpr int kOffAbort = kOffTmemSlot + 4;
     static constexpr int kOffAnyBad = kOffAbort + 4;
-    static constexpr int kSmemBytes = kOffAnyBad + 16 + 1024;
+    static constexpr int kOffTicket = kOffAnyBad + 32;
+    static constexpr int kSmemBytes = kOffTicket + 4 * kRagTickets + 1024;
     static constexpr int kTmemCols = 2 * QCAP < 32 ? 32 : 2 * QCAP;
     static_assert(kQBytes % 1024 == 0 && kOffBar % 8 == 0, "layout");
     static_assert(kSmemBytes <= kRagMaxSmem, "shared memory budget");
@@ -176,12 +187,47 @@ struct RaggedSeg {
     uint32_t lo, hi;
 };
 
+template <int CG>
+__device__ __forceinline__ bool ragged_wait(uint32_t bar, uint32_t parity, const RaggedParams &p,
+                                            volatile uint32_t *abort_flag, uint32_t code)
+{
+    auto try_once = [&]() {
+        if constexpr (CG > 1) return ptx::mbar_try_wait_cluster(bar, parity);
+        else return ptx::mbar_try_wait(bar, parity);
+    };
+    if (try_once()) return true;
+    const long long t0 = clock64();
+    for (uint32_t it = 1;; ++it) {
+        if (try_once()) return true;
+        if ((it & 31u) == 0) {
+            if (*abort_flag) return false;
+            if (clock64() - t0 > p.wait_limit) {
+                *abort_flag = 1u;
+                atomicCAS(p.error_word, 0u, code | (blockIdx.x << 8));
+                return false;
+            }
+        }
+    }
+}
+
+// The same wait by a whole warp, which leaves it together.
+template <int CG>
+__device__ __forceinline__ bool ragged_wait_warp(uint32_t bar, uint32_t parity, const RaggedParams &p,
+                                                 volatile uint32_t *abort_flag, uint32_t code)
+{
+    const bool ok = ragged_wait<CG>(bar, parity, p, abort_flag, code);
+    return __all_sync(0xffffffffu, ok);
+}
+
 template <int MODE, int CG, int QCAP>
 struct RaggedWalk {
     const RaggedParams &p;
     const int32_t *tab_row;    // offsets (groups + 1), or counts per row tile
     const uint32_t *tab_tile;  // tiles before each group (groups + 1)
     const int32_t *list;       // kLoraU, kLoraY: the adapters of each row tile
+    const volatile uint32_t *tickets;
+    uint32_t bar_tickets;      // ticket_full, then ticket_empty
+    volatile uint32_t *abort_flag;
     uint32_t worker, workers, total;
     uint32_t run, longer;      // sk: K-block iterations of a worker; the first `longer` workers have one more
 
@@ -279,11 +325,25 @@ struct RaggedWalk {
     {
         RaggedSeg s;
         if (MODE == kTN || !p.sk) {
-            for (uint32_t u = worker; u < total; u += workers) {
+            uint32_t u = worker;
+            for (uint32_t i = 0; u < total; ++i) {
                 decode(u, s);
                 s.lo = 0;
                 s.hi = s.kb;
                 if (!f(s)) return;
+                if (p.counter == nullptr) {
+                    u += workers;
+                    continue;
+                }
+                const uint32_t slot = i % kRagTickets;
+                if (!ragged_wait_warp<CG>(bar_tickets + 8u * slot, (i / kRagTickets) & 1u, p, abort_flag, kRagErrTicket)) return;
+                u = tickets[slot];
+                __syncwarp();
+                if ((threadIdx.x & 31u) == 0u) {
+                    const uint32_t bar = bar_tickets + 8u * (kRagTickets + slot);
+                    if constexpr (CG == 1) ptx::mbar_arrive(bar);
+                    else ptx::mbar_arrive_cluster(ptx::map_to_rank(bar, 0u));
+                }
             }
             return;
         }
@@ -304,38 +364,6 @@ struct RaggedWalk {
         }
     }
 };
-
-template <int CG>
-__device__ __forceinline__ bool ragged_wait(uint32_t bar, uint32_t parity, const RaggedParams &p,
-                                            volatile uint32_t *abort_flag, uint32_t code)
-{
-    auto try_once = [&]() {
-        if constexpr (CG > 1) return ptx::mbar_try_wait_cluster(bar, parity);
-        else return ptx::mbar_try_wait(bar, parity);
-    };
-    if (try_once()) return true;
-    const long long t0 = clock64();
-    for (uint32_t it = 1;; ++it) {
-        if (try_once()) return true;
-        if ((it & 31u) == 0) {
-            if (*abort_flag) return false;
-            if (clock64() - t0 > p.wait_limit) {
-                *abort_flag = 1u;
-                atomicCAS(p.error_word, 0u, code | (blockIdx.x << 8));
-                return false;
-            }
-        }
-    }
-}
-
-// The same wait by a whole warp, which leaves it together.
-template <int CG>
-__device__ __forceinline__ bool ragged_wait_warp(uint32_t bar, uint32_t parity, const RaggedParams &p,
-                                                 volatile uint32_t *abort_flag, uint32_t code)
-{
-    const bool ok = ragged_wait<CG>(bar, parity, p, abort_flag, code);
-    return __all_sync(0xffffffffu, ok);
-}
 
 // A value all lanes hold, in a form the compiler can keep in uniform registers: the operands of TMA and MMA
 // instructions live there, and moving them over for every instruction delays the issue loops.
@@ -522,6 +550,8 @@ __global__ void __launch_bounds__(kRagThreads, 1) gemm_ragged_kernel(const __gri
     auto bar_acc_full = [&](uint32_t b) { return base + Cfg::kOffBar + 8u * (4 * STAGES + b); };
     auto bar_acc_empty = [&](uint32_t b) { return base + Cfg::kOffBar + 8u * (4 * STAGES + 2 + b); };
     const uint32_t bar_drain = base + Cfg::kOffBar + 8u * (4 * STAGES + 4);
+    const uint32_t bar_tickets = base + Cfg::kOffBar + 8u * (4 * STAGES + 7);
+    const uint32_t bar_request = bar_tickets + 8u * (2 * kRagTickets);
     auto bar_bad_free = [&](uint32_t b) { return base + Cfg::kOffBar + 8u * (4 * STAGES + 5 + b); };
     volatile uint32_t *any_bad = reinterpret_cast<volatile uint32_t *>(smem + Cfg::kOffAnyBad);
     volatile uint32_t *abort_flag = reinterpret_cast<volatile uint32_t *>(smem + Cfg::kOffAbort);
@@ -544,6 +574,11 @@ __global__ void __launch_bounds__(kRagThreads, 1) gemm_ragged_kernel(const __gri
             ptx::mbar_init(bar_bad_free(b), kRagEpiWarps);
         }
         ptx::mbar_init(bar_drain, 1);
+        for (int t = 0; t < kRagTickets; ++t) {
+            ptx::mbar_init(bar_tickets + 8u * t, 1);
+            ptx::mbar_init(bar_tickets + 8u * (kRagTickets + t), Cfg::kReaders);
+        }
+        ptx::mbar_init(bar_request, 1);
         *abort_flag = 0u;
         ptx::fence_mbar_init();
         ptx::prefetch_tmap(&p.tm_p);
@@ -567,6 +602,9 @@ __global__ void __launch_bounds__(kRagThreads, 1) gemm_ragged_kernel(const __gri
                                     tab_row,
                                     tab_tile,
                                     list,
+                                    reinterpret_cast<const volatile uint32_t *>(smem + Cfg::kOffTicket),
+                                    bar_tickets,
+                                    abort_flag,
                                     blockIdx.x / CG,
                                     gridDim.x / CG,
                                     MODE == kLoraY ? p.tiles_p * p.tiles_q : tab_tile[p.groups],
@@ -584,7 +622,7 @@ __global__ void __launch_bounds__(kRagThreads, 1) gemm_ragged_kernel(const __gri
     };
     // K blocks whose stage the helper has to finish
     auto fixed_block = [&](const RaggedSeg &s, uint32_t kb) -> bool {
-        if (MODE == kTN) return kb + 1u == s.kb && (s.krows & 15u) != 0u;
+        if (MODE == kTN) return p.maps == nullptr && kb + 1u == s.kb && (s.krows & 15u) != 0u;
         if (MODE == kLoraY) return kb >= p.k_blocks;
         return false;
     };
@@ -593,9 +631,25 @@ __global__ void __launch_bounds__(kRagThreads, 1) gemm_ragged_kernel(const __gri
         // ------------------------------------------------ TMA producer
         {
             const bool elected = ptx::elect_one();
-            uint32_t stage = 0, phase = 0, fills = 0, tail_uses = 0;
+            uint32_t stage = 0, phase = 0, fills = 0, tail_uses = 0, last_g = ~0u;
             walk.each([&](RaggedSeg &s) {
                 uniform(s);
+                if (p.counter != nullptr && leader && elected) ptx::mbar_arrive(bar_request);
+                // kTN: the group's own maps, whose rows end where the group's do
+                const CUtensorMap *map_p = &p.tm_p, *map_q = &p.tm_q[0], *map_p2 = &p.tm_p2, *map_q2 = &p.tm_q2;
+                if (MODE == kTN && p.maps != nullptr) {
+                    map_p = p.maps + 4u * s.g;
+                    map_q = map_p + 1;
+                    map_p2 = map_p + 2;
+                    map_q2 = map_p + 3;
+                    if (s.g != last_g && elected) {
+                        ptx::tensormap_acquire(map_p);
+                        ptx::tensormap_acquire(map_q);
+                        if (p.p_groups) ptx::tensormap_acquire(map_p2);
+                        if (p.q_groups) ptx::tensormap_acquire(map_q2);
+                    }
+                    last_g = s.g;
+                }
                 const uint32_t hq = s.nq / CG;
                 // N-side boxes: kTN 64 columns each; otherwise in units of a quarter of the stage's rows, 1, 2, 1 + 2 or 4
                 const uint32_t boxes = (hq + 63u) / 64u;
@@ -639,16 +693,16 @@ __global__ void __launch_bounds__(kRagThreads, 1) gemm_ragged_kernel(const __gri
                         if constexpr (MODE == kTN) {
                             const int32_t row = int32_t(s.row0) + k0;
                             if (p_pairs) {
-                                load2(p_dst, &p.tm_p2, row, p0 / 64, 0);
+                                load2(p_dst, map_p2, row, p0 / 64, 0);
                             } else {
-                                load(p_dst, &p.tm_p, p0, row, 0);
-                                load(p_dst + 8192u, &p.tm_p, p0 + 64, row, 0);
+                                load(p_dst, map_p, p0, row, 0);
+                                load(p_dst + 8192u, map_p, p0 + 64, row, 0);
                             }
                             if (q_pairs) {
-                                load2(q_dst, &p.tm_q2, row, q0 / 64, 0);
+                                load2(q_dst, map_q2, row, q0 / 64, 0);
                             } else {
                                 for (uint32_t b = 0; b < boxes; ++b)
-                                    load(q_dst + b * 8192u, &p.tm_q[0], q0 + int32_t(64u * b), row, 0);
+                                    load(q_dst + b * 8192u, map_q, q0 + int32_t(64u * b), row, 0);
                             }
                         } else if (extra) {
                             const uint32_t e = kb - p.k_blocks;
@@ -814,7 +868,8 @@ __global__ void __launch_bounds__(kRagThreads, 1) gemm_ragged_kernel(const __gri
             // kLoraY: NaN for the rows whose own adapter holds an infinity or NaN in this lane's row of b
             const bool has_adapters = MODE == kLoraY && s.hi > max(s.lo, p.k_blocks);
             const uint32_t bad_buf = adapted & 1u;
-            const bool any = has_adapters && (any_bad[2u * bad_buf] | any_bad[2u * bad_buf + 1u]) != 0u;
+            const bool any = has_adapters && (any_bad[4u * bad_buf] | any_bad[4u * bad_buf + 1u] | any_bad[4u * bad_buf + 2u] |
+                                               any_bad[4u * bad_buf + 3u]) != 0u;
             if (has_adapters) ++adapted;
             auto spoil = [&](uint32_t c, uint32_t (&r)[32]) {
                 if (!any) return;
@@ -997,11 +1052,33 @@ __global__ void __launch_bounds__(kRagThreads, 1) gemm_ragged_kernel(const __gri
             return true;
         });
         if (MODE == kTN && lane == 0) ptx::bulk_wait_group<0>();
+    } else if (warp == 10u) {
+        // ------------------------------------------------ scheduler
+        // The next tile is taken when the producer begins the one before it, not earlier: tiles taken ahead would
+        // leave workers waiting at the end for one that still has several.
+        if (p.counter != nullptr && leader && lane == 0 && walk.worker < walk.total) {
+            volatile uint32_t *tickets = reinterpret_cast<volatile uint32_t *>(smem + Cfg::kOffTicket);
+            for (uint32_t i = 0;; ++i) {
+                const uint32_t slot = i % kRagTickets;
+                if (!ragged_wait<CG>(bar_request, i & 1u, p, abort_flag, kRagErrTicket)) break;
+                const uint32_t bar = bar_tickets + 8u * slot;
+                if (!ragged_wait<CG>(bar + 8u * kRagTickets, ((i / kRagTickets) & 1u) ^ 1u, p, abort_flag, kRagErrTicket)) break;
+                const uint32_t next = walk.workers + atomicAdd(p.counter, 1u);
+                const uint32_t u = next < walk.total ? next : kRagNoTile;
+                tickets[slot] = u;
+                if constexpr (CG == 2) {
+                    ptx::st_shared_cluster_u32(ptx::map_to_rank(base + Cfg::kOffTicket + 4u * slot, 1u), u);
+                    ptx::mbar_arrive_cluster(ptx::map_to_rank(bar, 1u));
+                }
+                ptx::mbar_arrive(bar);
+                if (u == kRagNoTile) break;
+            }
+        }
     } else if constexpr (Cfg::kHelper) {
         // ------------------------------------------------ helper
-        // Two warps that share a stage's rows and never wait for each other: `fixed` counts them both.
+        // Four warps that share a stage's rows and never wait for each other: `fixed` counts them all.
         const uint32_t tid = threadIdx.x - 192u;
-        const uint32_t half = tid >> 5;
+        const uint32_t part = tid >> 5;
         uint32_t fills = 0, tail_uses = 0, adapted = 0;
         if (MODE == kLoraY && p.late) ptx::griddep_wait();
         auto wait_tail = [&](uint32_t stage) {
@@ -1039,31 +1116,27 @@ __global__ void __launch_bounds__(kRagThreads, 1) gemm_ragged_kernel(const __gri
             } else {
                 // adapter blocks: rows of this CTA's part of the tile, u where the row has the slot's adapter
                 if (s.hi <= max(s.lo, p.k_blocks)) return true;
-                constexpr uint32_t kMine = (Cfg::kQCta + kRagHelpers - 1) / kRagHelpers;  // rows of a thread
-                const uint32_t row0 = s.q0 + rank * hq;
-                int32_t id[kMine];
-                uint4 u[kMine][8];  // the first 64 of u's columns, loaded once for all slots
+                static_assert(Cfg::kQCta <= kRagHelpers, "one row of u per helper thread");
+                const uint32_t row = s.q0 + rank * hq + tid;
+                const int32_t id = (tid < hq && rank * hq + tid < s.qn) ? p.ids[row] : -1;
+                const uint4 *src = reinterpret_cast<const uint4 *>(static_cast<const char *>(p.u) + size_t(row) * p.rank * 2u);
+                uint4 u[8];  // the first 64 of u's columns, loaded once for all slots
 #pragma unroll
-                for (uint32_t i = 0; i < kMine; ++i) {
-                    const uint32_t t = tid + i * kRagHelpers;
-                    id[i] = (t < hq && rank * hq + t < s.qn) ? p.ids[row0 + t] : -1;
-                    const uint4 *src = reinterpret_cast<const uint4 *>(static_cast<const char *>(p.u) +
-                                                                       size_t(row0 + t) * p.rank * 2u);
-#pragma unroll
-                    for (uint32_t c = 0; c < 8u; ++c)
-                        u[i][c] = (uint32_t(id[i]) < p.adapters && 8u * c < p.rank) ? src[c] : make_uint4(0u, 0u, 0u, 0u);
-                }
+                for (uint32_t c = 0; c < 8u; ++c)
+                    u[c] = (uint32_t(id) < p.adapters && 8u * c < p.rank) ? src[c] : make_uint4(0u, 0u, 0u, 0u);
                 // the table of b rows with infinities is free once the epilogue is done with the tile before last;
-                // each warp keeps the words of its own rows, t / 32 = half and half + 2
+                // each warp keeps the words of its own rows
                 const uint32_t bad_buf = adapted & 1u;
                 if (!ragged_wait_warp<1>(bar_bad_free(bad_buf), ((adapted >> 1) & 1u) ^ 1u, p, abort_flag, kRagErrFixed))
                     return false;
                 ++adapted;
                 uint32_t *mask = reinterpret_cast<uint32_t *>(smem + Cfg::kOffBad + bad_buf * Cfg::kBadBytes);
-                for (uint32_t i = lane; i < uint32_t(tab_row[s.g]); i += 32u) mask[4u * i + half] = mask[4u * i + half + 2u] = 0u;
-                if (lane == 0) any_bad[2u * bad_buf + half] = 0u;
+                for (uint32_t i = lane; i < uint32_t(tab_row[s.g]); i += 32u) mask[4u * i + part] = 0u;
+                if (lane == 0) any_bad[4u * bad_buf + part] = 0u;
                 __syncwarp();
-                const uint32_t expo = p.bf16 ? 0x7F80u : 0x7C00u;  // all ones: infinity or NaN
+                // exponent bits of both halves of a word; all ones (infinity or NaN) carry into the top bit
+                const uint32_t expo = p.bf16 ? 0x7F807F80u : 0x7C007C00u;
+                const uint32_t carry = p.bf16 ? 0x00800080u : 0x04000400u;
                 uint32_t stage = (first + max(s.lo, p.k_blocks) - s.lo) % STAGES;
                 for (uint32_t kb = max(s.lo, p.k_blocks); kb < s.hi; ++kb) {
                     const uint32_t e = kb - p.k_blocks;
@@ -1071,47 +1144,45 @@ __global__ void __launch_bounds__(kRagThreads, 1) gemm_ragged_kernel(const __gri
                     const uint32_t r0 = (e - slot * p.rank_blocks) * kRagBlockK;
                     const int32_t adapter = list[size_t(s.g) * p.per + slot];
                     const uint32_t chunks = 2u * steps_of(s, kb);
-                    const uint32_t q_at = base + Cfg::kOffQ + stage * Cfg::kQBytes;
+                    const bool mine = id == adapter;
                     // b has landed, so the stage is free: the producer waited for that.  (The stage's empty barrier
                     // cannot be waited for here: it may be more than one phase away.)
                     if (!wait_tail(stage)) return false;
-#pragma unroll
-                    for (uint32_t i = 0; i < kMine; ++i) {
-                        const uint32_t t = tid + i * kRagHelpers;
-                        if (t >= hq) continue;
-                        const bool mine = id[i] == adapter;
-                        const uint4 *src = reinterpret_cast<const uint4 *>(static_cast<const char *>(p.u) +
-                                                                           (size_t(row0 + t) * p.rank + r0) * 2u);
+                    // u where the row has the slot's adapter, zeros elsewhere
+                    if (tid < hq) {
+                        const uint32_t q_at = base + Cfg::kOffQ + stage * Cfg::kQBytes + tid * 128u;
 #pragma unroll
                         for (uint32_t c = 0; c < 8u; ++c) {
                             if (c >= chunks) continue;
-                            uint4 v = u[i][c];
-                            if (r0 != 0u && mine && r0 + 8u * c < p.rank) v = src[c];
+                            uint4 v = u[c];
+                            if (r0 != 0u && mine && r0 + 8u * c < p.rank) v = src[r0 / 8u + c];
                             if (!mine || r0 + 8u * c >= p.rank) v = make_uint4(0u, 0u, 0u, 0u);
-                            ptx::st_shared_v4(q_at + t * 128u + ((c ^ (t & 7u)) << 4), v.x, v.y, v.z, v.w);
+                            ptx::st_shared_v4(q_at + ((c ^ (tid & 7u)) << 4), v.x, v.y, v.z, v.w);
                         }
                     }
-                    // b's rows: zeros for infinities and NaN, which the other adapters' zero rows of u would turn into NaN
-                    const uint32_t p_at = base + Cfg::kOffP + stage * Cfg::kPBytes;
+                    // b's row tid: zeros for infinities and NaN, which the other adapters' zero rows of u would turn into NaN
+                    const uint32_t p_at = base + Cfg::kOffP + stage * Cfg::kPBytes + tid * 128u;
+                    uint32_t odd = 0u;
 #pragma unroll
-                    for (uint32_t t = tid; t < 128u; t += kRagHelpers) {
+                    for (uint32_t c = 0; c < 8u; ++c) {
+                        if (c >= chunks) continue;
+                        const uint4 v = ptx::ld_shared_v4(p_at + ((c ^ (tid & 7u)) << 4));
+                        odd |= ((v.x & expo) + carry) | ((v.y & expo) + carry) | ((v.z & expo) + carry) | ((v.w & expo) + carry);
+                    }
+                    if (odd & 0x80008000u) {
                         for (uint32_t c = 0; c < chunks; ++c) {
-                            const uint32_t at = p_at + t * 128u + ((c ^ (t & 7u)) << 4);
+                            const uint32_t at = p_at + ((c ^ (tid & 7u)) << 4);
                             const uint4 v = ptx::ld_shared_v4(at);
                             uint32_t w[4] = {v.x, v.y, v.z, v.w};
-                            bool bad = false;
 #pragma unroll
                             for (int j = 0; j < 4; ++j) {
-                                const bool lo = (w[j] & expo) == expo, hi = (w[j] & (expo << 16)) == (expo << 16);
-                                bad |= lo | hi;
-                                w[j] &= (lo ? 0xFFFF0000u : 0xFFFFFFFFu) & (hi ? 0x0000FFFFu : 0xFFFFFFFFu);
+                                const uint32_t top = ((w[j] & expo) + carry) & 0x80008000u;
+                                w[j] &= ((top & 0x8000u) ? 0xFFFF0000u : 0xFFFFFFFFu) & ((top & 0x80000000u) ? 0x0000FFFFu : 0xFFFFFFFFu);
                             }
-                            if (bad) {
-                                ptx::st_shared_v4(at, w[0], w[1], w[2], w[3]);
-                                atomicOr(mask + 4u * slot + (t >> 5), 1u << (t & 31u));
-                                any_bad[2u * bad_buf + half] = 1u;
-                            }
+                            ptx::st_shared_v4(at, w[0], w[1], w[2], w[3]);
                         }
+                        atomicOr(mask + 4u * slot + part, 1u << lane);
+                        any_bad[4u * bad_buf + part] = 1u;
                     }
                     hand_over(stage);
                     if (++stage == STAGES) stage = 0;
@@ -1139,6 +1210,39 @@ __global__ void __launch_bounds__(kRagThreads, 1) gemm_ragged_kernel(const __gri
     }
     if constexpr (CG == 2) ptx::cluster_sync();
     if (warp == 1) ptx::tmem_dealloc<CG>(tmem_base, Cfg::kTmemCols);
+}
+
+// What a launch with a tile counter needs before it: the counter at zero and, for kTN, every group's tensor maps
+// with the rows ending at the group's end, so that TMA fills the rest of its last K block with zeros.  One warp per map.
+struct RaggedSetupParams {
+    CUtensorMap maps[4];
+    const int32_t *offsets;
+    uint32_t groups, rows;
+    uint32_t have;      // bit i: maps[i] is one
+    uint32_t *counter;
+    CUtensorMap *out;   // [groups][4], or null
+};
+
+__global__ void __launch_bounds__(128) ragged_setup_kernel(const __grid_constant__ RaggedSetupParams p)
+{
+    __shared__ __align__(128) CUtensorMap s_map[4];
+    ptx::griddep_wait();
+    if (blockIdx.x == 0 && threadIdx.x == 0) *p.counter = 0u;
+    if (p.out != nullptr) {
+        const uint32_t lane = threadIdx.x & 31u, i = threadIdx.x >> 5, g = blockIdx.x;
+        // the group's end as ragged_table has it: the largest of the clamped offsets up to it
+        int32_t end = 0;
+        for (uint32_t k = lane; k <= g + 1u; k += 32u) end = max(end, min(p.offsets[k], int32_t(p.rows)));
+        end = __reduce_max_sync(0xffffffffu, end);
+        if ((p.have >> i) & 1u) {
+            reinterpret_cast<uint32_t *>(&s_map[i])[lane] = reinterpret_cast<const uint32_t *>(&p.maps[i])[lane];
+            __syncwarp();
+            if (lane == 0) ptx::tensormap_set_dim1(ptx::smem_addr(&s_map[i]), uint32_t(max(end, 1)));
+            __syncwarp();
+            ptx::tensormap_publish(p.out + 4u * g + i, ptx::smem_addr(&s_map[i]));
+        }
+    }
+    ptx::griddep_launch_dependents();
 }
 
 // u = scale x a^T for few rows, one block per row and four of its u's: four warps share k, each lane adds
@@ -1218,6 +1322,7 @@ struct LoraListParams {
     const int32_t *ids;
     uint32_t rows, per, adapters;
     int32_t *counts, *list;
+    uint32_t *counter;  // set to zero for the product's tile counter, or null
 };
 
 __global__ void __launch_bounds__(256) lora_list_kernel(const __grid_constant__ LoraListParams p)
@@ -1245,6 +1350,7 @@ __global__ void __launch_bounds__(256) lora_list_kernel(const __grid_constant__ 
         total += s_warp[w];
     }
     if (first) p.list[size_t(blockIdx.x) * p.per + at] = id;
+    if (t == 0 && blockIdx.x == 0 && p.counter) *p.counter = 0u;
     if (t == 0) p.counts[blockIdx.x] = int32_t(total);
     ptx::griddep_launch_dependents();
 }

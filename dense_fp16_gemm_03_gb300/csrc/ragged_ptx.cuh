@@ -62,6 +62,27 @@ __device__ __forceinline__ void tma_store_3d(const void *tmap, uint32_t src, int
                  : "memory");
 }
 
+// Tensor maps edited on the device: set the extent of dimension 1 of the map in shared memory at `smem`; a whole
+// warp copies it to 128-byte aligned global memory, visible to TMA after the acquire below by the thread that uses it.
+__device__ __forceinline__ void tensormap_set_dim1(uint32_t smem, uint32_t extent)
+{
+    asm volatile("tensormap.replace.tile.global_dim.shared::cta.b1024.b32 [%0], 1, %1;" ::"r"(smem), "r"(extent) : "memory");
+}
+
+__device__ __forceinline__ void tensormap_publish(void *global, uint32_t smem)
+{
+    asm volatile(
+        "tensormap.cp_fenceproxy.global.shared::cta.tensormap::generic.release.gpu.sync.aligned [%0], [%1], 128;" ::"l"(
+            reinterpret_cast<uint64_t>(global)),
+        "r"(smem)
+        : "memory");
+}
+
+__device__ __forceinline__ void tensormap_acquire(const void *global)
+{
+    asm volatile("fence.proxy.tensormap::generic.acquire.gpu [%0], 128;" ::"l"(reinterpret_cast<uint64_t>(global)) : "memory");
+}
+
 // True in one lane of a converged warp, always the same.
 __device__ __forceinline__ bool elect_one()
 {
