@@ -36,7 +36,7 @@ int64_t round_up(int64_t a, int64_t b)
 // One compiled kernel: the CTA pair of each mode for many rows, the single CTA with a 64-row N side
 // for few.
 struct RaggedVariant {
-    int mode, cg, qcap, qbox, smem;
+    int mode, cg, qcap, qbox, smem, threads;
     const void *fn;
 };
 
@@ -44,18 +44,26 @@ struct RaggedVariant {
     RaggedVariant                                                                                        \
     {                                                                                                    \
         MODE, CG, QCAP, RaggedCfg<MODE, CG, QCAP, ST>::kQBox, RaggedCfg<MODE, CG, QCAP, ST>::kSmemBytes, \
+            RaggedCfg<MODE, CG, QCAP, ST>::kThreads,                                                     \
             reinterpret_cast<const void *>(&gemm_ragged_kernel<MODE, CG, QCAP, ST>)                      \
     }
 
-enum RaggedVariantId { kVNtWide, kVNtFew, kVNnWide, kVNnFew, kVTn, kVLoraU, kVLoraYWide, kVLoraYFew };
+enum RaggedVariantId { kVNtWide, kVNtFew, kVNnWide, kVNnFew, kVTn, kVLoraU, kVLoraY };
 const RaggedVariant kRagged[] = {
     RAGGED_VARIANT(kNT, 2, 256, 6), RAGGED_VARIANT(kNT, 1, 64, 8),
     RAGGED_VARIANT(kNN, 2, 256, 6), RAGGED_VARIANT(kNN, 1, 64, 8),
     RAGGED_VARIANT(kTN, 2, 256, 6),
     RAGGED_VARIANT(kLoraU, 1, 64, 8),
-    RAGGED_VARIANT(kLoraY, 2, 256, 6), RAGGED_VARIANT(kLoraY, 1, 64, 8),
+    RAGGED_VARIANT(kLoraY, 2, 256, 6),
 };
 constexpr int kNumRagged = int(sizeof(kRagged) / sizeof(kRagged[0]));
+
+const void *const kBeside[] = {
+    reinterpret_cast<const void *>(&lora_shrink_kernel),     reinterpret_cast<const void *>(&lora_expand_kernel<1>),
+    reinterpret_cast<const void *>(&lora_expand_kernel<2>),  reinterpret_cast<const void *>(&lora_expand_kernel<4>),
+    reinterpret_cast<const void *>(&lora_expand_kernel<8>),  reinterpret_cast<const void *>(&lora_expand_kernel<16>),
+    reinterpret_cast<const void *>(&lora_list_kernel),       reinterpret_cast<const void *>(&ragged_maps_kernel),
+};
 
 struct RaggedDevice {
     bool ready = false;
@@ -97,7 +105,7 @@ gemm_status_t ragged_device(RaggedDevice **out)
                 cudaLaunchConfig_t cfg;
                 memset(&cfg, 0, sizeof(cfg));
                 cfg.gridDim = dim3(unsigned(made.slots[v] * var.cg), 1, 1);
-                cfg.blockDim = dim3(kRagThreads, 1, 1);
+                cfg.blockDim = dim3(unsigned(var.threads), 1, 1);
                 cfg.dynamicSmemBytes = size_t(var.smem);
                 cudaLaunchAttribute attr;
                 attr.id = cudaLaunchAttributeClusterDimension;
@@ -111,6 +119,15 @@ gemm_status_t ragged_device(RaggedDevice **out)
                     made.slots[v] = clusters;
                 else
                     cudaGetLastError();
+            }
+        }
+        // The small kernels in front of a product run with the SM's memory split as the product wants it: an SM does not
+        // change the split under a running block, and the product's CTA would wait for the block to end.
+        for (const void *fn : kBeside) {
+            if (cudaFuncSetAttribute(fn, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared) !=
+                cudaSuccess) {
+                cudaGetLastError();
+                return GEMM_ERR_CUDA;
             }
         }
         made.ready = true;
@@ -267,18 +284,11 @@ size_t split_bytes(const RaggedVariant &var, int slots)
     return ctas * 128u * size_t(var.qcap) * 4u + ctas * 8u;
 }
 
-// Bytes of a tile counter and, for the weight gradient, four tensor maps per group.
-constexpr size_t kCounterBytes = 256;
-size_t counted_bytes(int mode, int64_t groups)
+// Bytes of the weight gradient's tensor maps, four per group.
+size_t maps_bytes(int64_t groups)
 {
-    return kCounterBytes + (mode == kTN ? size_t(groups) * 4u * sizeof(CUtensorMap) : 0u);
+    return size_t(groups) * 4u * sizeof(CUtensorMap);
 }
-
-// Tiles are handed out one by one where there are more of them than workers and each lasts long.  32 groups of
-// 16384 rows in all, 4096 x 4096: 352 against 358 us with 64 K blocks a tile, and with uneven groups 382 against
-// 388; the weight gradient's tiles of 8 K blocks lose what they would gain, 535 against 453, because the next
-// number takes about as long to come as such a tile.
-constexpr int64_t kCountedMinBlocks = 32;
 
 void use_split(RaggedParams *p, const RaggedVariant &var, int slots, void *ws)
 {
@@ -296,7 +306,7 @@ gemm_status_t launch_ragged(int variant, const RaggedDevice *dev, RaggedParams &
     if (most_units < workers) workers = most_units < 1 ? 1 : most_units;
     p.error_word = dev->error_word;
     void *args[1] = {&p};
-    return launch(var.fn, dim3(unsigned(workers * var.cg), 1, 1), kRagThreads, var.smem, var.cg, args, stream);
+    return launch(var.fn, dim3(unsigned(workers * var.cg), 1, 1), unsigned(var.threads), var.smem, var.cg, args, stream);
 }
 
 // ------------------------------------------------------ grouped products
@@ -318,8 +328,9 @@ int grouped_variant(int mode, int64_t groups, int64_t rows)
 
 size_t grouped_bytes(int mode, int64_t groups, int64_t rows, const RaggedDevice *dev)
 {
+    if (mode == kTN) return maps_bytes(groups);
     const int v = grouped_variant(mode, groups, rows);
-    return mode != kTN && few_rows(groups, rows) ? split_bytes(kRagged[v], dev->slots[v]) : counted_bytes(mode, groups);
+    return few_rows(groups, rows) ? split_bytes(kRagged[v], dev->slots[v]) : 0;
 }
 
 gemm_status_t grouped(int mode, gemm_dtype_t dtype, gemm_dtype_t out_type, int64_t groups, int64_t rows, int64_t n, int64_t k,
@@ -397,28 +408,22 @@ gemm_status_t grouped(int mode, gemm_dtype_t dtype, gemm_dtype_t out_type, int64
         }
     }
     if (st != GEMM_OK) return st;
-    const bool counted = ws && mode != kTN && !p.sk && most > dev->slots[variant] && p.k_blocks >= kCountedMinBlocks;
-    const bool own_maps = ws && mode == kTN;
-    if (counted || own_maps) {
-        RaggedSetupParams sp;
-        memset(&sp, 0, sizeof(sp));
-        sp.counter = static_cast<uint32_t *>(ws);
-        if (own_maps) {
-            sp.maps[0] = p.tm_p;
-            sp.maps[1] = p.tm_q[0];
-            sp.maps[2] = p.tm_p2;
-            sp.maps[3] = p.tm_q2;
-            sp.have = 3u | (p.p_groups ? 4u : 0u) | (p.q_groups ? 8u : 0u);
-            sp.offsets = offsets;
-            sp.groups = uint32_t(groups);
-            sp.rows = uint32_t(rows);
-            sp.out = reinterpret_cast<CUtensorMap *>(static_cast<char *>(ws) + kCounterBytes);
-            p.maps = sp.out;
-        }
-        if (counted) p.counter = sp.counter;
-        void *args[1] = {&sp};
-        st = launch(reinterpret_cast<const void *>(&ragged_setup_kernel), dim3(own_maps ? unsigned(groups) : 1u, 1, 1), 128, 0, 1,
-                    args, stream);
+    // (one or two tiles a worker: the kernel that writes the maps would take longer than the helper it spares)
+    if (ws && mode == kTN && most > 2 * dev->slots[variant]) {
+        RaggedMapsParams mp;
+        memset(&mp, 0, sizeof(mp));
+        mp.maps[0] = p.tm_p;
+        mp.maps[1] = p.tm_q[0];
+        mp.maps[2] = p.tm_p2;
+        mp.maps[3] = p.tm_q2;
+        mp.have = 3u | (p.p_groups ? 4u : 0u) | (p.q_groups ? 8u : 0u);
+        mp.offsets = offsets;
+        mp.groups = uint32_t(groups);
+        mp.rows = uint32_t(rows);
+        mp.out = static_cast<CUtensorMap *>(ws);
+        p.maps = mp.out;
+        void *args[1] = {&mp};
+        st = launch(reinterpret_cast<const void *>(&ragged_maps_kernel), dim3(unsigned(groups), 1, 1), 128, 0, 1, args, stream);
         if (st != GEMM_OK) return st;
     }
     return launch_ragged(variant, dev, p, most, stream);
@@ -426,45 +431,53 @@ gemm_status_t grouped(int mode, gemm_dtype_t dtype, gemm_dtype_t out_type, int64
 
 // ------------------------------------------------------------- adapters
 
-// Rows up to which u is computed by lora_shrink_kernel and the whole product is one row tile of a single CTA.
+// Rows up to which the adapters run beside the projection without tensor cores, one row tile of a single CTA.
 constexpr int64_t kLoraFewRows = 64;
 constexpr int64_t kLoraURows = 64;  // rows of a tile of the product that computes u for more rows
 
-// Rows of a tile and how the workspace is laid out: counts and lists of the adapters per row tile (of u's product
-// and of y's), u, split work.
+// How the work and the workspace are laid out.  Few rows: u and delta in fp32.  More: counts and lists
+// of the adapters per row tile (of y's product and of u's), and u; rows beyond what the kernels' table holds go in passes.
 struct LoraPlan {
     bool few;
+    int variant_y;
     int64_t per, tiles;    // y's row tiles, of one pass
     int64_t tiles_u;
-    int64_t pass_rows;     // rows of one pass: the kernels' table holds kRagMaxGroups tiles
-    int variant_y;
-    size_t counter, counts, list, counts_u, list_u, u, split, total;  // offsets
+    int64_t pass_rows;
+    size_t counts, list, counts_u, list_u, u, delta, split, total;  // offsets
 };
 
-LoraPlan lora_plan(const RaggedDevice *dev, int64_t rows, int64_t rank)
+LoraPlan lora_plan(const RaggedDevice *dev, int64_t rows, int64_t n, int64_t rank)
 {
     LoraPlan l;
+    memset(&l, 0, sizeof(l));
     l.few = rows <= kLoraFewRows;
-    l.variant_y = l.few ? kVLoraYFew : kVLoraYWide;
+    l.variant_y = l.few ? kVNtFew : kVLoraY;
     const RaggedVariant &y = kRagged[l.variant_y];
-    l.pass_rows = int64_t(kRagMaxGroups) * kLoraURows;
-    if (rows < l.pass_rows) l.pass_rows = rows;
-    l.tiles = cdiv(l.pass_rows, y.qcap);
-    l.per = round_up(cdiv(l.pass_rows, l.tiles), 16 * y.cg);
-    l.tiles_u = cdiv(l.pass_rows, kLoraURows);
     size_t at = 0;
     auto take = [&](size_t bytes) {
         const size_t was = at;
         at += size_t(round_up(int64_t(bytes), 256));
         return was;
     };
-    l.counter = take(kCounterBytes);
-    l.counts = take(l.few ? 0 : size_t(l.tiles) * 4u);
-    l.list = take(l.few ? 0 : size_t(l.tiles) * size_t(l.per) * 4u);
-    l.counts_u = take(l.few ? 0 : size_t(l.tiles_u) * 4u);
-    l.list_u = take(l.few ? 0 : size_t(l.tiles_u) * size_t(kLoraURows) * 4u);
+    if (l.few) {
+        l.pass_rows = rows;
+        l.u = take(size_t(rows) * size_t(rank) * 4u);
+        l.delta = take(size_t(rows) * size_t(n) * 4u);
+        l.split = take(split_bytes(y, dev->slots[l.variant_y]));
+        l.total = at;
+        return l;
+    }
+    l.pass_rows = int64_t(kRagMaxGroups) * kLoraURows;
+    if (rows < l.pass_rows) l.pass_rows = rows;
+    l.tiles = cdiv(l.pass_rows, y.qcap);
+    l.per = round_up(cdiv(l.pass_rows, l.tiles), 16 * y.cg);
+    l.tiles_u = cdiv(l.pass_rows, kLoraURows);
+    l.counts = take(size_t(l.tiles) * 4u);
+    l.list = take(size_t(l.tiles) * size_t(l.per) * 4u);
+    l.counts_u = take(size_t(l.tiles_u) * 4u);
+    l.list_u = take(size_t(l.tiles_u) * size_t(kLoraURows) * 4u);
     l.u = take(size_t(l.pass_rows) * size_t(rank) * 2u);
-    size_t split = l.few ? 0 : split_bytes(kRagged[kVLoraU], dev->slots[kVLoraU]);
+    size_t split = split_bytes(kRagged[kVLoraU], dev->slots[kVLoraU]);
     const size_t split_y = l.tiles == 1 ? split_bytes(y, dev->slots[l.variant_y]) : 0;
     if (split_y > split) split = split_y;
     l.split = take(split);
@@ -533,7 +546,7 @@ gemm_status_t gemm_lora_workspace_size(int64_t rows, int64_t n, int64_t k, int64
     RaggedDevice *dev = nullptr;
     st = ragged_device(&dev);
     if (st != GEMM_OK) return st;
-    *bytes = rows ? lora_plan(dev, rows, rank).total : 0;
+    *bytes = rows ? lora_plan(dev, rows, n, rank).total : 0;
     return GEMM_OK;
 }
 
@@ -560,7 +573,7 @@ gemm_status_t gemm_lora_nt(gemm_dtype_t dtype, int64_t rows, int64_t n, int64_t 
     RaggedDevice *dev = nullptr;
     st = ragged_device(&dev);
     if (st != GEMM_OK) return st;
-    const LoraPlan l = lora_plan(dev, rows, rank);
+    const LoraPlan l = lora_plan(dev, rows, n, rank);
     if (workspace == nullptr || ws_bytes < l.total) return GEMM_ERR_WORKSPACE;
     if (reinterpret_cast<uintptr_t>(workspace) & 255u) return GEMM_ERR_ALIGNMENT;
     if (k == 0) {
@@ -571,6 +584,65 @@ gemm_status_t gemm_lora_nt(gemm_dtype_t dtype, int64_t rows, int64_t n, int64_t 
         return GEMM_OK;
     }
     char *ws = static_cast<char *>(workspace);
+    if (l.few) {
+        RaggedParams p;
+        memset(&p, 0, sizeof(p));
+        p.groups = 1;
+        p.rows = uint32_t(rows);
+        p.pdim = uint32_t(n);
+        p.kdim = uint32_t(k);
+        p.k_blocks = uint32_t(cdiv(k, kRagBlockK));
+        const RaggedVariant &vy = kRagged[l.variant_y];
+        p.tiles_p = uint32_t(cdiv(n, 128 * vy.cg));
+        p.band = 8;
+        p.bf16 = dtype == GEMM_DTYPE_BF16;
+        p.out = y;
+        p.skip_fill = ~0u;
+        p.wait_limit = wait_limit_for(p.k_blocks);
+        st = encode_stack(&p.tm_p, w, dtype, 1, n, k, kRagBlockK, 128);
+        if (st == GEMM_OK) st = encode_rows(p.tm_q, x, dtype, rows, k, vy.qbox);
+        if (st != GEMM_OK) return st;
+        if (adapted) {
+            LoraFewParams f;
+            f.x = x;
+            f.a = a;
+            f.b = b;
+            f.ids = ids;
+            f.scale = scale;
+            f.u = reinterpret_cast<float *>(ws + l.u);
+            f.delta = reinterpret_cast<float *>(ws + l.delta);
+            f.rows = uint32_t(rows);
+            f.n = uint32_t(n);
+            f.k = uint32_t(k);
+            f.rank = uint32_t(rank);
+            f.adapters = uint32_t(adapters);
+            f.bf16 = p.bf16;
+            void *args[1] = {&f};
+            // few enough blocks on an SM to leave room for the product's CTA beside them: with four and two, 64 rows with
+            // 64 adapters of rank 16, 8192 x 4096, take 29.1 us, with four and four 30.8, with one and two 33.5
+            const int64_t shrink = rows * (rank / 4), expand = cdiv(rows * cdiv(n, 128), 4);
+            const void *expand_fn = rank <= 8    ? reinterpret_cast<const void *>(&lora_expand_kernel<1>)
+                                    : rank <= 16 ? reinterpret_cast<const void *>(&lora_expand_kernel<2>)
+                                    : rank <= 32 ? reinterpret_cast<const void *>(&lora_expand_kernel<4>)
+                                    : rank <= 64 ? reinterpret_cast<const void *>(&lora_expand_kernel<8>)
+                                                 : reinterpret_cast<const void *>(&lora_expand_kernel<16>);
+            const int64_t room = dev->num_sms;
+            st = launch(reinterpret_cast<const void *>(&lora_shrink_kernel),
+                        dim3(unsigned(shrink < 4 * room ? shrink : 4 * room), 1, 1), 128, 0, 1, args, s);
+            if (st != GEMM_OK) return st;
+            st = launch(expand_fn, dim3(unsigned(expand < 2 * room ? expand : 2 * room), 1, 1), 128, 0, 1, args, s);
+            if (st != GEMM_OK) return st;
+            p.delta = f.delta;
+            p.ids = ids;
+            p.adapters = f.adapters;
+        }
+        int64_t most = p.tiles_p;
+        if (most * p.k_blocks < kIterLimit) {
+            use_split(&p, vy, dev->slots[l.variant_y], ws + l.split);
+            most *= p.k_blocks;
+        }
+        return launch_ragged(l.variant_y, dev, p, most, s);
+    }
     const RaggedVariant &vu = kRagged[kVLoraU], &vy = kRagged[l.variant_y];
 
     RaggedParams u, p;
@@ -595,7 +667,7 @@ gemm_status_t gemm_lora_nt(gemm_dtype_t dtype, int64_t rows, int64_t n, int64_t 
     if (st == GEMM_OK && adapted) st = encode_stack(&p.tm_x, b, dtype, adapters, n, rank, kRagBlockK, 128);
     if (!adapted) p.tm_x = p.tm_p;  // (never loaded from)
     // u = scale x a^T for many rows: one tile per row tile and adapter in it
-    if (!l.few && adapted) {
+    if (adapted) {
         u.pdim = uint32_t(rank);
         u.tiles_p = 1;
         u.per = uint32_t(kLoraURows);
@@ -617,27 +689,7 @@ gemm_status_t gemm_lora_nt(gemm_dtype_t dtype, int64_t rows, int64_t n, int64_t 
         p.out = static_cast<char *>(y) + size_t(r0) * size_t(n) * 2u;
         st = encode_rows(p.tm_q, xr, dtype, r, k, vy.qbox);
         if (st != GEMM_OK) return st;
-        if (l.few) {
-            // u by itself, beside the product: both start after what was in the stream before them
-            if (adapted) {
-                LoraShrinkParams sp;
-                sp.x = xr;
-                sp.a = a;
-                sp.ids = idr;
-                sp.scale = scale;
-                sp.u = ws + l.u;
-                sp.k = uint32_t(k);
-                sp.rank = uint32_t(rank);
-                sp.adapters = uint32_t(adapters);
-                sp.bf16 = u.bf16;
-                void *args[1] = {&sp};
-                st = launch(reinterpret_cast<const void *>(&lora_shrink_kernel), dim3(unsigned(rank / 4), unsigned(r), 1), 128, 0, 1,
-                            args, s);
-                if (st != GEMM_OK) return st;
-                p.late = 1;
-            }
-            p.counts = p.list = nullptr;
-        } else {
+        {
             struct Side {
                 int64_t per, tiles;
                 size_t counts, list;
@@ -650,7 +702,6 @@ gemm_status_t gemm_lora_nt(gemm_dtype_t dtype, int64_t rows, int64_t n, int64_t 
                 lp.adapters = u.adapters;
                 lp.counts = reinterpret_cast<int32_t *>(ws + side.counts);
                 lp.list = reinterpret_cast<int32_t *>(ws + side.list);
-                lp.counter = &side == &sides[0] ? reinterpret_cast<uint32_t *>(ws + l.counter) : nullptr;
                 void *args[1] = {&lp};
                 if (!adapted && &side == &sides[1]) break;
                 st = launch(reinterpret_cast<const void *>(&lora_list_kernel), dim3(unsigned(side.tiles), 1, 1), 256, 0, 1, args, s);
@@ -674,9 +725,6 @@ gemm_status_t gemm_lora_nt(gemm_dtype_t dtype, int64_t rows, int64_t n, int64_t 
         }
         int64_t most = int64_t(p.tiles_p) * tiles;
         p.sk = 0;
-        p.counter = nullptr;
-        if (!l.few && l.tiles > 1 && most > dev->slots[l.variant_y] && p.k_blocks >= kCountedMinBlocks)
-            p.counter = reinterpret_cast<uint32_t *>(ws + l.counter);
         if (l.tiles == 1 && most * (p.k_blocks + l.per * p.rank_blocks) < kIterLimit) {
             use_split(&p, vy, dev->slots[l.variant_y], ws + l.split);
             most *= p.k_blocks;
@@ -767,7 +815,8 @@ gemm_status_t gemm_route_topk(gemm_dtype_t dtype, int64_t rows, int64_t experts,
     void *args[1] = {&p};
     st = launch(ROUTE_INSTANCE(route_topk_kernel, experts), dim3(unsigned(blocks), 1, 1), kRouteThreads, 0, 1, args, s);
     if (st != GEMM_OK || blocks == 1) return st;
-    st = launch(reinterpret_cast<const void *>(&route_scan_kernel), dim3(unsigned(cdiv(experts, 32)), 1, 1), 1024, 0, 1, args, s);
+    if (blocks > kRouteDirectBlocks)
+        st = launch(reinterpret_cast<const void *>(&route_scan_kernel), dim3(unsigned(cdiv(experts, 32)), 1, 1), 1024, 0, 1, args, s);
     if (st != GEMM_OK) return st;
     return launch(reinterpret_cast<const void *>(&route_place_kernel), dim3(unsigned(blocks), 1, 1), kRouteThreads, 0, 1, args, s);
 }

@@ -23,7 +23,7 @@
 // past a group's end (the rows there are finite work thrown away) but never
 // write there.
 //
-// Roles (352 threads; one CTA or a CTA pair per tile):
+// Roles (192 threads, 320 with helpers; one CTA or a CTA pair per tile):
 //   warp 0      TMA producer into a STAGES-deep ring of 128-byte-swizzled stages
 //   warp 1      tensor memory and the MMA issuer (of the pair's first CTA)
 //   warps 2..5  epilogue, on one of two accumulators while the other fills
@@ -34,16 +34,17 @@
 //               epilogue write NaN for them into that adapter's own rows alone.  A
 //               stage that the helper touches arrives on its CTA's `tail` barrier and is
 //               released to the MMA by the `fixed` barrier.
-//   warp 10     scheduler of launches with a tile counter
 //
 // Group ends are read on the device (no host copy of them exists): every CTA
 // turns the offsets into a table of tile counts in shared memory, where all
 // roles look their tiles up.
 //
-// Walks: data-parallel, tile u on worker u mod workers or, given a counter, each
-// next tile on the worker that comes for it first (groups of unlike sizes make
-// tiles of unlike cost; what a tile holds does not depend on who computes it); or
-// with `sk` each worker takes an equal run of all K-block iterations.  A run that stops
+// Walks: data-parallel (tile u on worker u mod workers), or with `sk` each
+// worker takes an equal run of all K-block iterations.  (Handing each next tile to
+// the worker that comes for it first, by a counter, was measured for groups of
+// unlike sizes: 32 groups of 16384 rows in all, 4096 x 4096, took 388 us against 380,
+// and one group 371 against 352: the number's way through the roles costs more
+// than the balance brings.)  A run that stops
 // inside a tile publishes its fp32 partial for the worker that holds the tile's
 // last K block.  Workers walk their run backwards, so they publish first and
 // wait last, and only ever for lower-numbered workers.  Sums are added in a fixed
@@ -64,9 +65,6 @@
 namespace gemm_f16 {
 
 constexpr int kRagBlockK = 64;       // 16-bit elements per 128-byte swizzled row
-constexpr int kRagThreads = 352;
-constexpr int kRagTickets = 3;       // tiles handed out but not yet read by every role
-constexpr uint32_t kRagNoTile = 0xFFFFFFFFu;
 constexpr int kRagMaxGroups = 1024;  // entries of the shared-memory group table
 constexpr int kRagEpiWarps = 4;
 constexpr int kRagHelpers = 128;     // threads of the helper warps: one for each row of a stage's M side
@@ -85,7 +83,6 @@ enum : uint32_t {
     kRagErrRingDrain = 7,
     kRagErrFixed = 10,   // the helper did not finish a stage in time
     kRagErrTail = 11,    // a group's last K block, or an adapter's b, did not arrive in time
-    kRagErrTicket = 12,  // no tile was handed out in time
 };
 
 struct RaggedParams {
@@ -97,7 +94,7 @@ struct RaggedParams {
     // only: the columns from 64 * groups on, and single groups, come by tm_p and tm_q.
     CUtensorMap tm_p2, tm_q2;
     uint32_t p_groups, q_groups;
-    const int32_t *offsets;  // [groups + 1] row offsets (kNT, kNN, kTN)
+    const int32_t *offsets;  // [groups + 1] row offsets (kNT, kNN, kTN), or null: one group of all rows
     uint32_t groups;         // groups, or row tiles (kLoraU, kLoraY)
     uint32_t rows;           // rows t
     uint32_t pdim;           // extent on the M side
@@ -116,12 +113,12 @@ struct RaggedParams {
     const int32_t *counts;   // adapters present in each row tile
     const int32_t *list;     // their numbers, `per` slots a row tile
     const float *scale;      // per adapter, or null
-    uint32_t adapters;       // kLoraY without a list
-    uint32_t late;           // kLoraY: only u comes from the previous kernel, so only the helper waits for it
+    uint32_t adapters;       // ids outside [0, adapters) have none
+    const float *delta;      // kNT: added to the rows that have an adapter, [rows, pdim]; only this comes from the
+                             // previous kernel, so only the epilogue waits for it
     const void *u;           // kLoraY: u [rows, rank]
     uint32_t rank;
     uint32_t rank_blocks;    // ceil(rank / 64)
-    uint32_t *counter;       // tiles handed out beyond each worker's first (zero at the start), or null
     const CUtensorMap *maps; // kTN: for each group tm_p, tm_q[0], tm_p2, tm_q2 that end with the group's rows, or null
     float *partials;         // sk: one 128 x QCAP fp32 tile per CTA
     uint64_t *flags;         // sk: one per CTA, `stamp` while its partial waits to be added
@@ -137,6 +134,7 @@ struct RaggedCfg {
     static constexpr bool kPMn = (MODE == kNN || MODE == kTN);  // M-side operand MN-major
     static constexpr bool kQMn = (MODE == kTN);                 // N-side operand MN-major
     static constexpr bool kHelper = (MODE == kTN || MODE == kLoraY);
+    static constexpr int kThreads = 192 + (kHelper ? kRagHelpers : 0);
     static constexpr int kQCta = QCAP / CG;                     // N-side extent in one CTA's stage
     // rows of a whole N-side box; a tile takes at most two boxes (halves and quarters) and at most a quarter's
     // rows too many, because every further box in a K block costs the producer more than the rows do
@@ -150,10 +148,8 @@ struct RaggedCfg {
     static constexpr int kStoreBytes = (MODE == kTN) ? 4096 : 2048;
     static constexpr int kOffTabRow = kOffStore + kRagEpiWarps * kStoreBytes;
     static constexpr int kOffTabTile = kOffTabRow + 4 * (kRagMaxGroups + 4);
-    // full, empty, fixed, tail per stage; acc_full x2, acc_empty x2, drain, bad_free x2, ticket_full, ticket_empty, request
-    static constexpr int kNumBars = 4 * STAGES + 7 + 2 * kRagTickets + 1;
-    // warps that read a ticket: both producers, the MMA issuer, every epilogue and helper warp
-    static constexpr int kReaders = 1 + CG * (1 + kRagEpiWarps + (kHelper ? kRagHelpers / 32 : 0));
+    // full, empty, fixed, tail per stage; acc_full x2, acc_empty x2, drain, bad_free x2
+    static constexpr int kNumBars = 4 * STAGES + 7;
     // kLoraY: for each of two tiles in flight, 128 bits per adapter of the tile (b rows that hold an infinity or
     // NaN), and for each helper warp whether it found any
     static constexpr int kOffBad = kOffTabTile + 4 * (kRagMaxGroups + 4);
@@ -164,8 +160,7 @@ struct RaggedCfg {
     static constexpr int kOffTmemSlot = kOffRec + STAGES * 16;
     static constexpr int kOffAbort = kOffTmemSlot + 4;
     static constexpr int kOffAnyBad = kOffAbort + 4;
-    static constexpr int kOffTicket = kOffAnyBad + 32;
-    static constexpr int kSmemBytes = kOffTicket + 4 * kRagTickets + 1024;
+    static constexpr int kSmemBytes = kOffAnyBad + 32 + 1024;
     static constexpr int kTmemCols = 2 * QCAP < 32 ? 32 : 2 * QCAP;
     static_assert(kQBytes % 1024 == 0 && kOffBar % 8 == 0, "layout");
     static_assert(kSmemBytes <= kRagMaxSmem, "shared memory budget");
@@ -185,6 +180,34 @@ struct RaggedSeg {
     uint32_t krows;   // kTN: rows of the group
     uint32_t kb;      // K blocks of the whole tile
     uint32_t lo, hi;
+    uint32_t extra;   // kLoraY: how many of them are adapter blocks
+    uint32_t e_lo, e_hi;  // and which of those lie in [lo, hi)
+};
+
+// The order of a kLoraY tile's K blocks: the adapter blocks are spread evenly between the projection's, so that the
+// helper prepares one while the tensor cores work on the others, and every run of a split tile has its share
+// (64 rows with 64 adapters of rank 16: 43.8 us with the adapter blocks last, XX spread).  Block v is an adapter
+// block where floor(v extra / kb) steps.
+struct RaggedMix {
+    uint32_t kb, extra, left, e, m;  // left = v extra mod kb; e and m: adapter and projection blocks before v
+    __device__ __forceinline__ explicit RaggedMix(const RaggedSeg &s) : kb(s.kb), extra(s.extra)
+    {
+        e = s.e_lo;
+        left = uint32_t(uint64_t(s.lo) * extra - uint64_t(e) * kb);
+        m = s.lo - e;
+    }
+    // whether the current block is an adapter block; then on to the next
+    __device__ __forceinline__ bool step()
+    {
+        left += extra;
+        if (left >= kb) {
+            left -= kb;
+            ++e;
+            return true;
+        }
+        ++m;
+        return false;
+    }
 };
 
 template <int CG>
@@ -219,17 +242,41 @@ __device__ __forceinline__ bool ragged_wait_warp(uint32_t bar, uint32_t parity, 
     return __all_sync(0xffffffffu, ok);
 }
 
+// A value all lanes hold, in a form the compiler can keep in uniform registers: the operands of TMA and MMA
+// instructions live there, and moving them over for every instruction delays the issue loops.
+__device__ __forceinline__ uint32_t uniform(uint32_t v)
+{
+    return __reduce_or_sync(0xffffffffu, v);
+}
+
+template <int MODE>
+__device__ __forceinline__ void uniform(RaggedSeg &s)
+{
+    s.g = uniform(s.g);
+    s.p0 = uniform(s.p0);
+    s.q0 = uniform(s.q0);
+    s.nq = uniform(s.nq);
+    s.lo = uniform(s.lo);
+    s.hi = uniform(s.hi);
+    s.kb = uniform(s.kb);
+    if constexpr (MODE == kTN || MODE == kLoraU) s.row0 = uniform(s.row0);
+    if constexpr (MODE == kTN) s.krows = uniform(s.krows);
+    if constexpr (MODE == kLoraY) {
+        s.extra = uniform(s.extra);
+        s.e_lo = uniform(s.e_lo);
+        s.e_hi = uniform(s.e_hi);
+    }
+}
+
 template <int MODE, int CG, int QCAP>
 struct RaggedWalk {
     const RaggedParams &p;
     const int32_t *tab_row;    // offsets (groups + 1), or counts per row tile
     const uint32_t *tab_tile;  // tiles before each group (groups + 1)
     const int32_t *list;       // kLoraU, kLoraY: the adapters of each row tile
-    const volatile uint32_t *tickets;
-    uint32_t bar_tickets;      // ticket_full, then ticket_empty
-    volatile uint32_t *abort_flag;
     uint32_t worker, workers, total;
     uint32_t run, longer;      // sk: K-block iterations of a worker; the first `longer` workers have one more
+    uint32_t tile_blocks;      // sk: K blocks of every tile
 
     __device__ __forceinline__ void decode(uint32_t u, RaggedSeg &s) const
     {
@@ -243,7 +290,8 @@ struct RaggedWalk {
             s.q0 = qi * p.per;
             s.qn = min(p.per, p.rows - s.q0);
             s.row0 = 0;
-            s.kb = p.k_blocks + uint32_t(tab_row[qi]) * p.rank_blocks;
+            s.extra = uint32_t(tab_row[qi]) * p.rank_blocks;
+            s.kb = p.k_blocks + s.extra;
         } else {
             uint32_t lo = 0, hi = p.groups;  // tab_tile[lo] <= u < tab_tile[hi]
             while (hi - lo > 1u) {
@@ -271,11 +319,18 @@ struct RaggedWalk {
                     s.krows = rows;
                     s.kb = (rows + kRagBlockK - 1u) / kRagBlockK;
                 } else {
-                    const uint32_t tq = (rows + QCAP - 1u) / QCAP;
-                    const uint32_t each = ((rows + tq - 1u) / tq + kStep - 1u) / kStep * kStep;
-                    raster(local, tq, pi, qi);
-                    s.q0 = r0 + qi * each;
-                    s.qn = min(each, r0 + rows - s.q0);
+                    // equal tiles, in whole steps of the instruction's N (one tile: no division on the way to the
+                    // first load)
+                    pi = local;
+                    s.q0 = r0;
+                    s.qn = rows;
+                    if (rows > uint32_t(QCAP)) {
+                        const uint32_t tq = (rows + QCAP - 1u) / QCAP;
+                        const uint32_t each = ((rows + tq - 1u) / tq + kStep - 1u) / kStep * kStep;
+                        raster(local, tq, pi, qi);
+                        s.q0 = r0 + qi * each;
+                        s.qn = min(each, r0 + rows - s.q0);
+                    }
                     s.row0 = r0;
                 }
                 s.p0 = pi * 128u * CG;
@@ -300,15 +355,25 @@ struct RaggedWalk {
         qi = b * p.band + (r - pi * w);
     }
 
+    __device__ __forceinline__ void count_extra(RaggedSeg &s) const
+    {
+        if constexpr (MODE == kLoraY) {
+            s.e_lo = uint32_t(uint64_t(s.lo) * s.extra / s.kb);
+            s.e_hi = uint32_t(uint64_t(s.hi) * s.extra / s.kb);
+        } else {
+            s.e_lo = s.e_hi = 0u;
+        }
+    }
+
     // sk: all tiles have the same K blocks (kLoraY: there is one row tile).  A run shorter than kMinRun blocks
     // would cost more in adding partials than it saves, so few iterations go to fewer workers.
     static constexpr uint32_t kMinRun = 4;
     __device__ __forceinline__ void plan_runs()
     {
         if (MODE == kTN || !p.sk || total == 0u) return;
-        RaggedSeg s;
-        decode(0, s);
-        const uint32_t iters = total * s.kb;  // below 2^32: the host checks
+        tile_blocks = p.k_blocks;
+        if (MODE == kLoraY) tile_blocks += uniform(uint32_t(tab_row[0])) * p.rank_blocks;
+        const uint32_t iters = total * tile_blocks;  // below 2^32: the host checks
         const uint32_t most = max(1u, iters / kMinRun);
         if (most < workers) workers = most;
         run = iters / workers;
@@ -320,38 +385,25 @@ struct RaggedWalk {
     }
 
     // f(seg) returns false to stop early (abort)
-    template <class F>
+    template <bool UNIFORM, class F>
     __device__ __forceinline__ void each(F &&f) const
     {
         RaggedSeg s;
         if (MODE == kTN || !p.sk) {
-            uint32_t u = worker;
-            for (uint32_t i = 0; u < total; ++i) {
+            for (uint32_t u = worker; u < total; u += workers) {
                 decode(u, s);
                 s.lo = 0;
                 s.hi = s.kb;
+                count_extra(s);
+                if constexpr (UNIFORM) uniform<MODE>(s);
                 if (!f(s)) return;
-                if (p.counter == nullptr) {
-                    u += workers;
-                    continue;
-                }
-                const uint32_t slot = i % kRagTickets;
-                if (!ragged_wait_warp<CG>(bar_tickets + 8u * slot, (i / kRagTickets) & 1u, p, abort_flag, kRagErrTicket)) return;
-                u = tickets[slot];
-                __syncwarp();
-                if ((threadIdx.x & 31u) == 0u) {
-                    const uint32_t bar = bar_tickets + 8u * (kRagTickets + slot);
-                    if constexpr (CG == 1) ptx::mbar_arrive(bar);
-                    else ptx::mbar_arrive_cluster(ptx::map_to_rank(bar, 0u));
-                }
             }
             return;
         }
         if (total == 0u || worker >= workers) return;
         const uint32_t begin = run_begin(worker);
         uint32_t it = run_begin(worker + 1u);
-        decode(0, s);
-        const uint32_t kb = s.kb;
+        const uint32_t kb = tile_blocks;
         while (it > begin) {
             const uint32_t u = (it - 1u) / kb;
             const uint32_t start = u * kb;
@@ -359,32 +411,13 @@ struct RaggedWalk {
             s.lo = begin > start ? begin - start : 0u;
             s.hi = it - start;
             const uint32_t lo = s.lo;
+            count_extra(s);
+            if constexpr (UNIFORM) uniform<MODE>(s);
             if (!f(s)) return;
             it = start + lo;
         }
     }
 };
-
-// A value all lanes hold, in a form the compiler can keep in uniform registers: the operands of TMA and MMA
-// instructions live there, and moving them over for every instruction delays the issue loops.
-__device__ __forceinline__ uint32_t uniform(uint32_t v)
-{
-    return __shfl_sync(0xffffffffu, v, 0);
-}
-
-__device__ __forceinline__ void uniform(RaggedSeg &s)
-{
-    s.g = uniform(s.g);
-    s.p0 = uniform(s.p0);
-    s.q0 = uniform(s.q0);
-    s.qn = uniform(s.qn);
-    s.nq = uniform(s.nq);
-    s.row0 = uniform(s.row0);
-    s.krows = uniform(s.krows);
-    s.kb = uniform(s.kb);
-    s.lo = uniform(s.lo);
-    s.hi = uniform(s.hi);
-}
 
 __device__ __forceinline__ uint32_t ragged_pack(float lo, float hi, bool bf16)
 {
@@ -398,45 +431,16 @@ __device__ __forceinline__ uint32_t ragged_pack(float lo, float hi, bool bf16)
 
 // The group table: row offsets clamped to [0, rows] and made monotone (offsets that are not can
 // then reach no other memory), and the number of tiles before each group.  Run by the whole CTA.
-//
-// kLoraY without a list (one row tile): the adapters present, in order of first appearance, are found here and
-// listed in the table's second half.
 template <int MODE, int QCAP>
 __device__ __forceinline__ void ragged_table(const RaggedParams &p, int32_t *tab_row, uint32_t *tab_tile)
 {
-    if (MODE == kLoraY && p.list == nullptr) {
-        const uint32_t t = threadIdx.x;
-        int32_t id = -1;
-        if (t < uint32_t(QCAP)) {
-            id = (p.adapters != 0u && t < p.rows) ? p.ids[t] : -1;
-            if (uint32_t(id) >= p.adapters) id = -1;
-            tab_row[t] = id;
-        }
-        __syncthreads();
-        bool first = id >= 0;
-        if (t < uint32_t(QCAP))
-            for (uint32_t i = 0; i < t; ++i) first &= tab_row[i] != id;
-        // at most 256 rows, in warps of 32: the number of first ones before this row
-        const uint32_t vote = __ballot_sync(0xffffffffu, first);
-        if ((t & 31u) == 0u) tab_tile[kRagMaxGroups - 16u + (t >> 5)] = uint32_t(__popc(vote));
-        __syncthreads();
-        uint32_t at = uint32_t(__popc(vote & ((1u << (t & 31u)) - 1u))), total = 0;
-        for (uint32_t w = 0; w < uint32_t(kRagThreads / 32); ++w) {
-            const uint32_t c = tab_tile[kRagMaxGroups - 16u + w];
-            if (w < (t >> 5)) at += c;
-            total += c;
-        }
-        __syncthreads();
-        if (first) tab_tile[at] = uint32_t(id);
-        if (t == 0u) tab_row[0] = int32_t(total);
-        __syncthreads();
-        return;
-    }
     constexpr bool kOffsets = (MODE == kNT || MODE == kNN || MODE == kTN);
     const uint32_t n = p.groups + (kOffsets ? 1u : 0u);
     for (uint32_t i = threadIdx.x; i < n; i += blockDim.x) {
-        int32_t v = kOffsets ? p.offsets[i] : p.counts[i];
-        if (kOffsets) v = max(0, min(v, int32_t(p.rows)));
+        int32_t v;
+        if (!kOffsets) v = p.counts[i];
+        else if (p.offsets == nullptr) v = i ? int32_t(p.rows) : 0;  // one group of all rows
+        else v = max(0, min(p.offsets[i], int32_t(p.rows)));
         tab_row[i] = v;
     }
     __syncthreads();
@@ -530,7 +534,7 @@ __device__ __noinline__ void ragged_drain(uint32_t bars, uint32_t rec, bool lead
 }
 
 template <int MODE, int CG, int QCAP, int STAGES>
-__global__ void __launch_bounds__(kRagThreads, 1) gemm_ragged_kernel(const __grid_constant__ RaggedParams p)
+__global__ void __launch_bounds__(RaggedCfg<MODE, CG, QCAP, STAGES>::kThreads, 1) gemm_ragged_kernel(const __grid_constant__ RaggedParams p)
 {
     using Cfg = RaggedCfg<MODE, CG, QCAP, STAGES>;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -550,8 +554,6 @@ __global__ void __launch_bounds__(kRagThreads, 1) gemm_ragged_kernel(const __gri
     auto bar_acc_full = [&](uint32_t b) { return base + Cfg::kOffBar + 8u * (4 * STAGES + b); };
     auto bar_acc_empty = [&](uint32_t b) { return base + Cfg::kOffBar + 8u * (4 * STAGES + 2 + b); };
     const uint32_t bar_drain = base + Cfg::kOffBar + 8u * (4 * STAGES + 4);
-    const uint32_t bar_tickets = base + Cfg::kOffBar + 8u * (4 * STAGES + 7);
-    const uint32_t bar_request = bar_tickets + 8u * (2 * kRagTickets);
     auto bar_bad_free = [&](uint32_t b) { return base + Cfg::kOffBar + 8u * (4 * STAGES + 5 + b); };
     volatile uint32_t *any_bad = reinterpret_cast<volatile uint32_t *>(smem + Cfg::kOffAnyBad);
     volatile uint32_t *abort_flag = reinterpret_cast<volatile uint32_t *>(smem + Cfg::kOffAbort);
@@ -574,15 +576,10 @@ __global__ void __launch_bounds__(kRagThreads, 1) gemm_ragged_kernel(const __gri
             ptx::mbar_init(bar_bad_free(b), kRagEpiWarps);
         }
         ptx::mbar_init(bar_drain, 1);
-        for (int t = 0; t < kRagTickets; ++t) {
-            ptx::mbar_init(bar_tickets + 8u * t, 1);
-            ptx::mbar_init(bar_tickets + 8u * (kRagTickets + t), Cfg::kReaders);
-        }
-        ptx::mbar_init(bar_request, 1);
         *abort_flag = 0u;
         ptx::fence_mbar_init();
         ptx::prefetch_tmap(&p.tm_p);
-        ptx::prefetch_tmap(&p.tm_q[0]);
+        for (int i = 0; i < 3; ++i) ptx::prefetch_tmap(&p.tm_q[i]);
         if (MODE == kTN || MODE == kLoraY) ptx::prefetch_tmap(&p.tm_x);
     }
     if (warp == 1) {
@@ -594,37 +591,36 @@ __global__ void __launch_bounds__(kRagThreads, 1) gemm_ragged_kernel(const __gri
     else __syncthreads();
     ptx::tc_fence_after_sync();
     const uint32_t tmem_base = *tmem_slot;
-    if (MODE != kLoraY || !p.late) ptx::griddep_wait();
+    const bool late = MODE == kNT && p.delta != nullptr;
+    if (!late) ptx::griddep_wait();
     ragged_table<MODE, QCAP>(p, tab_row, tab_tile);
 
-    const int32_t *list = (MODE == kLoraY && p.list == nullptr) ? reinterpret_cast<const int32_t *>(tab_tile) : p.list;
+    const int32_t *list = p.list;
     RaggedWalk<MODE, CG, QCAP> walk{p,
                                     tab_row,
                                     tab_tile,
                                     list,
-                                    reinterpret_cast<const volatile uint32_t *>(smem + Cfg::kOffTicket),
-                                    bar_tickets,
-                                    abort_flag,
                                     blockIdx.x / CG,
                                     gridDim.x / CG,
-                                    MODE == kLoraY ? p.tiles_p * p.tiles_q : tab_tile[p.groups],
+                                    MODE == kLoraY ? p.tiles_p * p.tiles_q : uniform(tab_tile[p.groups]),
+                                    0u,
                                     0u,
                                     0u};
     walk.plan_runs();
 
-    // K = 16 steps of K block kb that hold anything
+    // K = 16 steps of K block kb that hold anything (kLoraY: of the projection's)
     auto steps_of = [&](const RaggedSeg &s, uint32_t kb) -> uint32_t {
-        uint32_t left;
-        if (MODE == kTN) left = s.krows - kb * kRagBlockK;
-        else if (MODE == kLoraY && kb >= p.k_blocks) left = p.rank - ((kb - p.k_blocks) % p.rank_blocks) * kRagBlockK;
-        else left = p.kdim - kb * kRagBlockK;
+        const uint32_t left = (MODE == kTN ? s.krows : p.kdim) - kb * kRagBlockK;
         return min(4u, (left + 15u) / 16u);
     };
-    // K blocks whose stage the helper has to finish
+    // kLoraY: the same of adapter block e, whose columns of b and u start at rank_from(e)
+    auto rank_from = [&](uint32_t e) -> uint32_t {
+        return p.rank_blocks == 1u ? 0u : (e % p.rank_blocks) * kRagBlockK;
+    };
+    auto rank_steps = [&](uint32_t e) -> uint32_t { return min(4u, (p.rank - rank_from(e) + 15u) / 16u); };
+    // kTN: a last K block that the helper has to finish
     auto fixed_block = [&](const RaggedSeg &s, uint32_t kb) -> bool {
-        if (MODE == kTN) return p.maps == nullptr && kb + 1u == s.kb && (s.krows & 15u) != 0u;
-        if (MODE == kLoraY) return kb >= p.k_blocks;
-        return false;
+        return MODE == kTN && p.maps == nullptr && kb + 1u == s.kb && (s.krows & 15u) != 0u;
     };
 
     if (warp == 0) {
@@ -632,9 +628,7 @@ __global__ void __launch_bounds__(kRagThreads, 1) gemm_ragged_kernel(const __gri
         {
             const bool elected = ptx::elect_one();
             uint32_t stage = 0, phase = 0, fills = 0, tail_uses = 0, last_g = ~0u;
-            walk.each([&](RaggedSeg &s) {
-                uniform(s);
-                if (p.counter != nullptr && leader && elected) ptx::mbar_arrive(bar_request);
+            walk.template each<true>([&](const RaggedSeg &s) {
                 // kTN: the group's own maps, whose rows end where the group's do
                 const CUtensorMap *map_p = &p.tm_p, *map_q = &p.tm_q[0], *map_p2 = &p.tm_p2, *map_q2 = &p.tm_q2;
                 if (MODE == kTN && p.maps != nullptr) {
@@ -659,14 +653,15 @@ __global__ void __launch_bounds__(kRagThreads, 1) gemm_ragged_kernel(const __gri
                 const int32_t q0 = int32_t(s.q0 + rank * hq);
                 const bool p_pairs = Cfg::kPMn && uint32_t(p0) / 64u + 2u <= p.p_groups;
                 const bool q_pairs = Cfg::kQMn && hq == 128u && uint32_t(q0) / 64u + 2u <= p.q_groups;
-                for (uint32_t kb = s.lo; kb < s.hi; ++kb, ++fills) {
+                RaggedMix mix(s);
+                for (uint32_t v = s.lo; v < s.hi; ++v, ++fills) {
+                    const uint32_t e = mix.e, kb = MODE == kLoraY ? mix.m : v;
+                    const bool extra = MODE == kLoraY && mix.step();  // adapter block: only P comes by TMA
                     if (!ragged_wait_warp<CG>(bar_empty(stage), phase ^ 1u, p, abort_flag, kRagErrEmpty)) return false;
-                    const bool fix = fixed_block(s, kb);
-                    const bool tail = fix;                       // to this CTA's own tail barrier
+                    const bool tail = extra || fixed_block(s, kb);    // to this CTA's own tail barrier
                     if (elected && !(blockIdx.x == 0 && fills == p.skip_fill)) {
                         const uint32_t p_dst = base + Cfg::kOffP + stage * Cfg::kPBytes;
                         const uint32_t q_dst = base + Cfg::kOffQ + stage * Cfg::kQBytes;
-                        const bool extra = (MODE == kLoraY) && fix;  // adapter block: only P comes by TMA
                         const uint32_t bytes = Cfg::kPBytes + (extra ? 0u : q_bytes);
                         rec[4 * stage + 1] = bytes;
                         rec[4 * stage + 2] = bytes * CG;
@@ -705,10 +700,8 @@ __global__ void __launch_bounds__(kRagThreads, 1) gemm_ragged_kernel(const __gri
                                     load(q_dst + b * 8192u, map_q, q0 + int32_t(64u * b), row, 0);
                             }
                         } else if (extra) {
-                            const uint32_t e = kb - p.k_blocks;
-                            const uint32_t slot = e / p.rank_blocks;
-                            const int32_t adapter = list[size_t(s.g) * p.per + slot];
-                            load(p_dst, &p.tm_x, int32_t((e - slot * p.rank_blocks) * kRagBlockK), p0, adapter);
+                            const int32_t adapter = list[size_t(s.g) * p.per + e / p.rank_blocks];
+                            load(p_dst, &p.tm_x, int32_t(rank_from(e)), p0, adapter);
                         } else {
                             if constexpr (MODE == kNN) {
                                 if (p_pairs) {
@@ -750,8 +743,7 @@ __global__ void __launch_bounds__(kRagThreads, 1) gemm_ragged_kernel(const __gri
             constexpr uint64_t kPStep = Cfg::kPMn ? (2048u >> 4) : 2u;  // K = 16 inside a swizzle atom, or two 8-row groups
             constexpr uint64_t kQStep = Cfg::kQMn ? (2048u >> 4) : 2u;
             uint32_t stage = 0, phase = 0, acc = 0, acc_phase = 0, fixed_uses = 0;
-            walk.each([&](RaggedSeg &s) {
-                uniform(s);
+            walk.template each<true>([&](const RaggedSeg &s) {
                 if (!ragged_wait_warp<CG>(bar_acc_empty(acc), acc_phase ^ 1u, p, abort_flag, kRagErrAccEmpty)) return false;
                 ptx::tc_fence_after_sync();
                 const uint32_t d_tmem = tmem_u + acc * uint32_t(QCAP);
@@ -759,7 +751,7 @@ __global__ void __launch_bounds__(kRagThreads, 1) gemm_ragged_kernel(const __gri
                 // K blocks that are full and need no helper come first, four instructions each and nothing else:
                 // the issue loop has to stay ahead of the tensor cores
                 uint32_t accumulate = 0u;
-                const uint32_t whole = min(s.hi, (MODE == kTN ? s.krows : p.kdim) / uint32_t(kRagBlockK));
+                const uint32_t whole = (MODE == kTN ? s.krows : p.kdim) / uint32_t(kRagBlockK);
                 auto block = [&](uint32_t steps, bool fixed) -> bool {
                     if (!ragged_wait_warp<CG>(bar_full(stage), phase, p, abort_flag, kRagErrFull)) return false;
                     if (Cfg::kHelper && fixed) {
@@ -786,11 +778,21 @@ __global__ void __launch_bounds__(kRagThreads, 1) gemm_ragged_kernel(const __gri
                     }
                     return true;
                 };
-                uint32_t kb = s.lo;
-                for (; kb < whole; ++kb)
-                    if (!block(4u, false)) return false;
-                for (; kb < s.hi; ++kb)
-                    if (!block(steps_of(s, kb), fixed_block(s, kb))) return false;
+                if (MODE == kLoraY && s.e_hi > s.e_lo) {
+                    RaggedMix mix(s);
+                    for (uint32_t v = s.lo; v < s.hi; ++v) {
+                        const uint32_t e = mix.e, kb = mix.m;
+                        const bool extra = mix.step();
+                        if (!block(extra ? rank_steps(e) : steps_of(s, kb), extra)) return false;
+                    }
+                } else {
+                    uint32_t kb = MODE == kLoraY ? s.lo - s.e_lo : s.lo;
+                    const uint32_t end = MODE == kLoraY ? s.hi - s.e_lo : s.hi;
+                    for (; kb < min(end, whole); ++kb)
+                        if (!block(4u, false)) return false;
+                    for (; kb < end; ++kb)
+                        if (!block(steps_of(s, kb), fixed_block(s, kb))) return false;
+                }
                 if (elected) {
                     if constexpr (CG == 1) ptx::mma_commit(bar_acc_full(acc));
                     else ptx::mma_commit_pair(bar_acc_full(acc), uint16_t(3u));
@@ -842,10 +844,11 @@ __global__ void __launch_bounds__(kRagThreads, 1) gemm_ragged_kernel(const __gri
             }
         }
 
+        if (late) ptx::griddep_wait();
         uint32_t acc = 0, acc_phase = 0;
         uint32_t adapted = 0;  // kLoraY: segments with adapter blocks so far
         bool let_in = false;
-        walk.each([&](const RaggedSeg &s) {
+        walk.template each<false>([&](const RaggedSeg &s) {
             const bool ok = ragged_wait<CG>(bar_acc_full(acc), acc_phase, p, abort_flag, kRagErrAccFull);
             const bool split = MODE != kTN && p.sk != 0u && (s.lo != 0u || s.hi != s.kb);
             // the four warps meet at named barriers below when the tile is split: stop together
@@ -866,7 +869,7 @@ __global__ void __launch_bounds__(kRagThreads, 1) gemm_ragged_kernel(const __gri
             // partial tile in the workspace: warp quarter, 32-column chunk, then float4 j of every lane
             const uint32_t piece = quarter * 32u * QCAP + lane * 4u;
             // kLoraY: NaN for the rows whose own adapter holds an infinity or NaN in this lane's row of b
-            const bool has_adapters = MODE == kLoraY && s.hi > max(s.lo, p.k_blocks);
+            const bool has_adapters = MODE == kLoraY && s.e_hi > s.e_lo;
             const uint32_t bad_buf = adapted & 1u;
             const bool any = has_adapters && (any_bad[4u * bad_buf] | any_bad[4u * bad_buf + 1u] | any_bad[4u * bad_buf + 2u] |
                                                any_bad[4u * bad_buf + 3u]) != 0u;
@@ -947,36 +950,43 @@ __global__ void __launch_bounds__(kRagThreads, 1) gemm_ragged_kernel(const __gri
                 ptx::named_barrier_sync(1, 32 * kRagEpiWarps);
             }
             // 32 columns of the finished tile: the accumulator plus the other workers' partials, lowest first,
-            // four workers' loads in flight
+            // two workers' loads in flight
             auto chunk32 = [&](uint32_t c, uint32_t (&r)[32]) {
                 ptx::tmem_ld_32x32b_x32_wait(t_col + 32u * c, r);
                 if (MODE == kLoraY) spoil(c, r);
                 if (MODE != kTN && split) {
+                    for (uint32_t w = w_lo; w < walk.worker; w += 2u) {
+                        float4 v[2][8];
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        if (2u * c + uint32_t(h) >= halves) continue;
-                        for (uint32_t w = w_lo; w < walk.worker; w += 4u) {
-                            float4 v[4][4];
+                        for (int i = 0; i < 2; ++i) {
+                            const float *src = p.partials + size_t((w + i) * CG + rank) * kSlot + piece + c * 1024u;
 #pragma unroll
-                            for (int i = 0; i < 4; ++i) {
-                                const float *src = p.partials + size_t((w + i) * CG + rank) * kSlot + piece + c * 1024u + h * 512;
-#pragma unroll
-                                for (int j = 0; j < 4; ++j)
-                                    v[i][j] = w + i < walk.worker ? ptx::ld_global_cg_f4(src + j * 128) : make_float4(0.f, 0.f, 0.f, 0.f);
-                            }
-#pragma unroll
-                            for (int i = 0; i < 4; ++i)
-#pragma unroll
-                                for (int j = 0; j < 4; ++j) {
-                                    uint32_t *q = r + 16 * h + 4 * j;
-                                    q[0] = __float_as_uint(__uint_as_float(q[0]) + v[i][j].x);
-                                    q[1] = __float_as_uint(__uint_as_float(q[1]) + v[i][j].y);
-                                    q[2] = __float_as_uint(__uint_as_float(q[2]) + v[i][j].z);
-                                    q[3] = __float_as_uint(__uint_as_float(q[3]) + v[i][j].w);
-                                }
+                            for (int j = 0; j < 8; ++j)
+                                v[i][j] = (w + i < walk.worker && 2u * c + uint32_t(j / 4) < halves) ? ptx::ld_global_cg_f4(src + j * 128)
+                                                                                                : make_float4(0.f, 0.f, 0.f, 0.f);
                         }
+#pragma unroll
+                        for (int i = 0; i < 2; ++i)
+#pragma unroll
+                            for (int j = 0; j < 8; ++j) {
+                                uint32_t *q = r + 4 * j;
+                                q[0] = __float_as_uint(__uint_as_float(q[0]) + v[i][j].x);
+                                q[1] = __float_as_uint(__uint_as_float(q[1]) + v[i][j].y);
+                                q[2] = __float_as_uint(__uint_as_float(q[2]) + v[i][j].z);
+                                q[3] = __float_as_uint(__uint_as_float(q[3]) + v[i][j].w);
+                            }
                     }
                 }
+            };
+            // low-rank part of this lane's output column, for the rows that have an adapter
+            auto load_delta = [&](uint32_t c, float (&d)[32]) {
+                const uint32_t t = 32u * c + lane;
+                const int32_t id = t < s.qn ? p.ids[s.q0 + t] : -1;
+                const uint32_t rows = __ballot_sync(0xffffffffu, uint32_t(id) < p.adapters);
+                const float *from = p.delta + size_t(s.q0 + 32u * c) * p.pdim + prow + lane;
+                const bool column = prow + lane < p.pdim;
+#pragma unroll
+                for (uint32_t j = 0; j < 32u; ++j) d[j] = (column && ((rows >> j) & 1u)) ? from[size_t(j) * p.pdim] : 0.0f;
             };
             if constexpr (MODE == kTN) {
                 // rows of dw[g] on lanes: boxes of 32 rows x 128 bytes through the swizzled staging buffer
@@ -1021,7 +1031,15 @@ __global__ void __launch_bounds__(kRagThreads, 1) gemm_ragged_kernel(const __gri
                     const uint32_t col = prow + 4u * (lane & 7u);
                     for (uint32_t c = 0; c < chunks; ++c) {
                         uint32_t r[32];
+                        float d[MODE == kNT ? 32 : 1];
+                        if constexpr (MODE == kNT)
+                            if (late) load_delta(c, d);  // on its way while the partials come
                         chunk32(c, r);
+                        if constexpr (MODE == kNT)
+                            if (late) {
+#pragma unroll
+                                for (int j = 0; j < 32; ++j) r[j] = __float_as_uint(__uint_as_float(r[j]) + d[j]);
+                            }
                         __syncwarp();
 #pragma unroll
                         for (int i = 0; i < 16; ++i)
@@ -1052,35 +1070,12 @@ __global__ void __launch_bounds__(kRagThreads, 1) gemm_ragged_kernel(const __gri
             return true;
         });
         if (MODE == kTN && lane == 0) ptx::bulk_wait_group<0>();
-    } else if (warp == 10u) {
-        // ------------------------------------------------ scheduler
-        // The next tile is taken when the producer begins the one before it, not earlier: tiles taken ahead would
-        // leave workers waiting at the end for one that still has several.
-        if (p.counter != nullptr && leader && lane == 0 && walk.worker < walk.total) {
-            volatile uint32_t *tickets = reinterpret_cast<volatile uint32_t *>(smem + Cfg::kOffTicket);
-            for (uint32_t i = 0;; ++i) {
-                const uint32_t slot = i % kRagTickets;
-                if (!ragged_wait<CG>(bar_request, i & 1u, p, abort_flag, kRagErrTicket)) break;
-                const uint32_t bar = bar_tickets + 8u * slot;
-                if (!ragged_wait<CG>(bar + 8u * kRagTickets, ((i / kRagTickets) & 1u) ^ 1u, p, abort_flag, kRagErrTicket)) break;
-                const uint32_t next = walk.workers + atomicAdd(p.counter, 1u);
-                const uint32_t u = next < walk.total ? next : kRagNoTile;
-                tickets[slot] = u;
-                if constexpr (CG == 2) {
-                    ptx::st_shared_cluster_u32(ptx::map_to_rank(base + Cfg::kOffTicket + 4u * slot, 1u), u);
-                    ptx::mbar_arrive_cluster(ptx::map_to_rank(bar, 1u));
-                }
-                ptx::mbar_arrive(bar);
-                if (u == kRagNoTile) break;
-            }
-        }
     } else if constexpr (Cfg::kHelper) {
         // ------------------------------------------------ helper
         // Four warps that share a stage's rows and never wait for each other: `fixed` counts them all.
         const uint32_t tid = threadIdx.x - 192u;
         const uint32_t part = tid >> 5;
         uint32_t fills = 0, tail_uses = 0, adapted = 0;
-        if (MODE == kLoraY && p.late) ptx::griddep_wait();
         auto wait_tail = [&](uint32_t stage) {
             const bool ok = ragged_wait_warp<1>(bar_tail(stage), (tail_uses >> stage) & 1u, p, abort_flag, kRagErrTail);
             tail_uses ^= 1u << stage;
@@ -1094,7 +1089,7 @@ __global__ void __launch_bounds__(kRagThreads, 1) gemm_ragged_kernel(const __gri
                 else ptx::mbar_arrive_cluster(ptx::map_to_rank(bar_fixed(stage), 0u));
             }
         };
-        walk.each([&](const RaggedSeg &s) {
+        walk.template each<false>([&](const RaggedSeg &s) {
             const uint32_t hq = s.nq / CG;
             const uint32_t first = fills;
             fills += s.hi - s.lo;
@@ -1115,7 +1110,7 @@ __global__ void __launch_bounds__(kRagThreads, 1) gemm_ragged_kernel(const __gri
                 hand_over(stage);
             } else {
                 // adapter blocks: rows of this CTA's part of the tile, u where the row has the slot's adapter
-                if (s.hi <= max(s.lo, p.k_blocks)) return true;
+                if (s.e_hi <= s.e_lo) return true;
                 static_assert(Cfg::kQCta <= kRagHelpers, "one row of u per helper thread");
                 const uint32_t row = s.q0 + rank * hq + tid;
                 const int32_t id = (tid < hq && rank * hq + tid < s.qn) ? p.ids[row] : -1;
@@ -1137,13 +1132,23 @@ __global__ void __launch_bounds__(kRagThreads, 1) gemm_ragged_kernel(const __gri
                 // exponent bits of both halves of a word; all ones (infinity or NaN) carry into the top bit
                 const uint32_t expo = p.bf16 ? 0x7F807F80u : 0x7C007C00u;
                 const uint32_t carry = p.bf16 ? 0x00800080u : 0x04000400u;
-                uint32_t stage = (first + max(s.lo, p.k_blocks) - s.lo) % STAGES;
-                for (uint32_t kb = max(s.lo, p.k_blocks); kb < s.hi; ++kb) {
-                    const uint32_t e = kb - p.k_blocks;
+                // adapter block e stands at v = ceil((e + 1) kb / extra) - 1
+                const uint64_t scaled = uint64_t(s.e_lo + 1u) * s.kb;
+                uint32_t quot = uint32_t(scaled / s.extra), rest = uint32_t(scaled - uint64_t(quot) * s.extra);
+                const uint32_t quot_step = s.kb / s.extra, rest_step = s.kb - quot_step * s.extra;
+                for (uint32_t e = s.e_lo; e < s.e_hi; ++e) {
+                    const uint32_t v = quot + (rest ? 1u : 0u) - 1u;
+                    const uint32_t stage = (first + v - s.lo) % STAGES;
+                    quot += quot_step;
+                    rest += rest_step;
+                    if (rest >= s.extra) {
+                        rest -= s.extra;
+                        ++quot;
+                    }
                     const uint32_t slot = p.rank_blocks == 1u ? e : e / p.rank_blocks;
-                    const uint32_t r0 = (e - slot * p.rank_blocks) * kRagBlockK;
+                    const uint32_t r0 = rank_from(e);
                     const int32_t adapter = list[size_t(s.g) * p.per + slot];
-                    const uint32_t chunks = 2u * steps_of(s, kb);
+                    const uint32_t chunks = 2u * rank_steps(e);
                     const bool mine = id == adapter;
                     // b has landed, so the stage is free: the producer waited for that.  (The stage's empty barrier
                     // cannot be waited for here: it may be more than one phase away.)
@@ -1185,7 +1190,6 @@ __global__ void __launch_bounds__(kRagThreads, 1) gemm_ragged_kernel(const __gri
                         any_bad[4u * bad_buf + part] = 1u;
                     }
                     hand_over(stage);
-                    if (++stage == STAGES) stage = 0;
                 }
             }
             return true;
@@ -1195,7 +1199,7 @@ __global__ void __launch_bounds__(kRagThreads, 1) gemm_ragged_kernel(const __gri
     // ---------------------------------------------------- teardown
     ptx::griddep_launch_dependents();
     // (a kernel that ends counts as the end of those before it)
-    if (MODE == kLoraY && p.late) ptx::griddep_wait();
+    if (late) ptx::griddep_wait();
     __syncwarp();
     ptx::tc_fence_before_sync();
     if constexpr (CG == 2) ptx::cluster_sync();
@@ -1212,48 +1216,45 @@ __global__ void __launch_bounds__(kRagThreads, 1) gemm_ragged_kernel(const __gri
     if (warp == 1) ptx::tmem_dealloc<CG>(tmem_base, Cfg::kTmemCols);
 }
 
-// What a launch with a tile counter needs before it: the counter at zero and, for kTN, every group's tensor maps
-// with the rows ending at the group's end, so that TMA fills the rest of its last K block with zeros.  One warp per map.
-struct RaggedSetupParams {
+// kTN: every group's tensor maps with the rows ending at the group's end, so that TMA fills the rest of its last K block
+// with zeros.  One block per group, one warp per map.
+struct RaggedMapsParams {
     CUtensorMap maps[4];
     const int32_t *offsets;
     uint32_t groups, rows;
     uint32_t have;      // bit i: maps[i] is one
-    uint32_t *counter;
-    CUtensorMap *out;   // [groups][4], or null
+    CUtensorMap *out;   // [groups][4]
 };
 
-__global__ void __launch_bounds__(128) ragged_setup_kernel(const __grid_constant__ RaggedSetupParams p)
+__global__ void __launch_bounds__(128) ragged_maps_kernel(const __grid_constant__ RaggedMapsParams p)
 {
     __shared__ __align__(128) CUtensorMap s_map[4];
     ptx::griddep_wait();
-    if (blockIdx.x == 0 && threadIdx.x == 0) *p.counter = 0u;
-    if (p.out != nullptr) {
-        const uint32_t lane = threadIdx.x & 31u, i = threadIdx.x >> 5, g = blockIdx.x;
-        // the group's end as ragged_table has it: the largest of the clamped offsets up to it
-        int32_t end = 0;
-        for (uint32_t k = lane; k <= g + 1u; k += 32u) end = max(end, min(p.offsets[k], int32_t(p.rows)));
-        end = __reduce_max_sync(0xffffffffu, end);
-        if ((p.have >> i) & 1u) {
-            reinterpret_cast<uint32_t *>(&s_map[i])[lane] = reinterpret_cast<const uint32_t *>(&p.maps[i])[lane];
-            __syncwarp();
-            if (lane == 0) ptx::tensormap_set_dim1(ptx::smem_addr(&s_map[i]), uint32_t(max(end, 1)));
-            __syncwarp();
-            ptx::tensormap_publish(p.out + 4u * g + i, ptx::smem_addr(&s_map[i]));
-        }
+    const uint32_t lane = threadIdx.x & 31u, i = threadIdx.x >> 5, g = blockIdx.x;
+    // the group's end as ragged_table has it: the largest of the clamped offsets up to it
+    int32_t end = 0;
+    for (uint32_t k = lane; k <= g + 1u; k += 32u) end = max(end, min(p.offsets[k], int32_t(p.rows)));
+    end = __reduce_max_sync(0xffffffffu, end);
+    if ((p.have >> i) & 1u) {
+        reinterpret_cast<uint32_t *>(&s_map[i])[lane] = reinterpret_cast<const uint32_t *>(&p.maps[i])[lane];
+        __syncwarp();
+        if (lane == 0) ptx::tensormap_set_dim1(ptx::smem_addr(&s_map[i]), uint32_t(max(end, 1)));
+        __syncwarp();
+        ptx::tensormap_publish(p.out + 4u * g + i, ptx::smem_addr(&s_map[i]));
     }
     ptx::griddep_launch_dependents();
 }
 
-// u = scale x a^T for few rows, one block per row and four of its u's: four warps share k, each lane adds
-// products of 8 elements at a time in fp32.  Bound by the latency of one pass over a's rows; it runs beside the
-// product that follows it, which waits for it only where it reads u.
-struct LoraShrinkParams {
-    const void *x, *a;
+// Adapters of few rows, without the tensor cores: with an adapter to nearly every row, all of the work is reading a
+// and b once, and each row sees its own adapter only.  u = scale x a^T and delta = u b^T stay in fp32.  Both kernels run
+// beside the projection, which starts at once and waits for delta in its epilogue.
+struct LoraFewParams {
+    const void *x, *a, *b;
     const int32_t *ids;
     const float *scale;
-    void *u;
-    uint32_t k, rank, adapters, bf16;
+    float *u;       // [rows, rank]
+    float *delta;   // [rows, n]
+    uint32_t rows, n, k, rank, adapters, bf16;
 };
 
 __device__ __forceinline__ float2 ragged_unpack(uint32_t w, bool bf16)
@@ -1262,57 +1263,108 @@ __device__ __forceinline__ float2 ragged_unpack(uint32_t w, bool bf16)
     return __half22float2(*reinterpret_cast<const __half2 *>(&w));
 }
 
-__global__ void __launch_bounds__(128) lora_shrink_kernel(const __grid_constant__ LoraShrinkParams p)
+// An item is a row and four of its u's: four warps share k, each lane multiplies 8 elements at a time.
+__global__ void __launch_bounds__(128) lora_shrink_kernel(const __grid_constant__ LoraFewParams p)
 {
     __shared__ float s_sum[4][4];
     ptx::griddep_wait();
-    // (after the wait: what the next kernel reads from before this one is complete as well)
+    // (after the wait: what the next kernels read from before this one is complete as well)
     ptx::griddep_launch_dependents();
-    const uint32_t row = blockIdx.y, r0 = blockIdx.x * 4u;
     const uint32_t lane = threadIdx.x & 31u, warp = threadIdx.x >> 5;
-    const int32_t id = p.ids[row];
-    if (uint32_t(id) >= p.adapters) return;
     const bool bf16 = p.bf16 != 0u;
-    const uint4 *x = reinterpret_cast<const uint4 *>(static_cast<const char *>(p.x) + size_t(row) * p.k * 2u);
-    const char *a = static_cast<const char *>(p.a) + (size_t(id) * p.rank + r0) * p.k * 2u;
-    float sum[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 2
-    for (uint32_t i = threadIdx.x; i < p.k / 8u; i += 128u) {
-        const uint4 xv = x[i];
-        uint4 av[4];
+    const uint32_t parts = p.rank / 4u;
+    for (uint32_t item = blockIdx.x; item < p.rows * parts; item += gridDim.x) {
+        const uint32_t row = item / parts, r0 = (item - row * parts) * 4u;
+        const int32_t id = p.ids[row];
+        if (uint32_t(id) >= p.adapters) continue;
+        const uint4 *x = reinterpret_cast<const uint4 *>(static_cast<const char *>(p.x) + size_t(row) * p.k * 2u);
+        const char *a = static_cast<const char *>(p.a) + (size_t(id) * p.rank + r0) * p.k * 2u;
+        float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+        for (uint32_t i = threadIdx.x; i < p.k / 8u; i += 128u) {
+            const uint4 xv = x[i];
+            uint4 av[4];
 #pragma unroll
-        for (int r = 0; r < 4; ++r) av[r] = reinterpret_cast<const uint4 *>(a + size_t(r) * p.k * 2u)[i];
-        const uint32_t xw[4] = {xv.x, xv.y, xv.z, xv.w};
+            for (int r = 0; r < 4; ++r) av[r] = reinterpret_cast<const uint4 *>(a + size_t(r) * p.k * 2u)[i];
+            const uint32_t xw[4] = {xv.x, xv.y, xv.z, xv.w};
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const float2 xf = ragged_unpack(xw[j], bf16);
+            for (int j = 0; j < 4; ++j) {
+                const float2 xf = ragged_unpack(xw[j], bf16);
 #pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const uint32_t aw = j == 0 ? av[r].x : j == 1 ? av[r].y : j == 2 ? av[r].z : av[r].w;
-                const float2 af = ragged_unpack(aw, bf16);
-                sum[r] = fmaf(xf.x, af.x, sum[r]);
-                sum[r] = fmaf(xf.y, af.y, sum[r]);
+                for (int r = 0; r < 4; ++r) {
+                    const uint32_t aw = j == 0 ? av[r].x : j == 1 ? av[r].y : j == 2 ? av[r].z : av[r].w;
+                    const float2 af = ragged_unpack(aw, bf16);
+                    sum[r] = fmaf(xf.x, af.x, sum[r]);
+                    sum[r] = fmaf(xf.y, af.y, sum[r]);
+                }
             }
         }
-    }
 #pragma unroll
-    for (int r = 0; r < 4; ++r)
+        for (int r = 0; r < 4; ++r)
 #pragma unroll
-        for (int d = 16; d > 0; d >>= 1) sum[r] += __shfl_xor_sync(0xffffffffu, sum[r], d);
-    if (lane == 0)
+            for (int d = 16; d > 0; d >>= 1) sum[r] += __shfl_xor_sync(0xffffffffu, sum[r], d);
+        __syncthreads();  // the item before has been written
+        if (lane == 0)
 #pragma unroll
-        for (int r = 0; r < 4; ++r) s_sum[warp][r] = sum[r];
-    __syncthreads();
-    if (threadIdx.x < 2u) {
-        const float mul = p.scale ? p.scale[id] : 1.0f;
-        float v[2];
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const uint32_t r = threadIdx.x * 2u + uint32_t(h);
-            v[h] = ((s_sum[0][r] + s_sum[1][r]) + (s_sum[2][r] + s_sum[3][r])) * mul;
+            for (int r = 0; r < 4; ++r) s_sum[warp][r] = sum[r];
+        __syncthreads();
+        if (threadIdx.x < 4u) {
+            const uint32_t r = threadIdx.x;
+            const float mul = p.scale ? p.scale[id] : 1.0f;
+            p.u[size_t(row) * p.rank + r0 + r] = ((s_sum[0][r] + s_sum[1][r]) + (s_sum[2][r] + s_sum[3][r])) * mul;
         }
-        reinterpret_cast<uint32_t *>(static_cast<char *>(p.u) + (size_t(row) * p.rank + r0) * 2u)[threadIdx.x] =
-            ragged_pack(v[0], v[1], bf16);
+    }
+}
+
+// An item, a warp's, is a row and 128 of its columns.  LANES lanes share a row of b, 16 bytes each, with their part of
+// u in registers.  (One lane to a row of b read a line per lane and load.)
+template <int LANES>
+__global__ void __launch_bounds__(128) lora_expand_kernel(const __grid_constant__ LoraFewParams p)
+{
+    // The product behind this kernel reads nothing of the kernel before this one; that one has waited for all before it.
+    ptx::griddep_launch_dependents();
+    ptx::griddep_wait();
+    const bool bf16 = p.bf16 != 0u;
+    const uint32_t lane = threadIdx.x & 31u, part = lane % LANES;
+    const uint32_t parts = (p.n + 127u) / 128u;
+    const bool live = 8u * part < p.rank;
+    constexpr uint32_t kRows = 32 / LANES;  // rows of b a warp reads at a time
+    constexpr uint32_t kFlight = 8;         // and such reads in flight
+    for (uint32_t item = blockIdx.x * 4u + (threadIdx.x >> 5); item < p.rows * parts; item += gridDim.x * 4u) {
+        const uint32_t row = item / parts, col0 = (item - row * parts) * 128u;
+        const int32_t id = p.ids[row];
+        if (uint32_t(id) >= p.adapters) continue;
+        float u[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) u[j] = live ? p.u[size_t(row) * p.rank + 8u * part + j] : 0.0f;
+        const char *b = static_cast<const char *>(p.b) + size_t(id) * p.n * p.rank * 2u + 16u * part;
+#pragma unroll 1
+        for (uint32_t i0 = 0; i0 < 128u; i0 += kFlight * kRows) {
+            uint4 v[kFlight];
+#pragma unroll
+            for (int i = 0; i < int(kFlight); ++i) {
+                const uint32_t col = col0 + i0 + uint32_t(i) * kRows + lane / LANES;
+                v[i] = (live && col < p.n && i0 + uint32_t(i) * kRows < 128u)
+                           ? *reinterpret_cast<const uint4 *>(b + size_t(col) * p.rank * 2u)
+                           : make_uint4(0u, 0u, 0u, 0u);
+            }
+#pragma unroll
+            for (int i = 0; i < int(kFlight); ++i) {
+                if (i0 + uint32_t(i) * kRows >= 128u) continue;
+                const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+                float sum = 0.0f;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const float2 f = ragged_unpack(w[j], bf16);
+                    sum = fmaf(f.x, u[2 * j], sum);
+                    sum = fmaf(f.y, u[2 * j + 1], sum);
+                }
+#pragma unroll
+                for (int d = LANES / 2; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+                const uint32_t col = col0 + i0 + uint32_t(i) * kRows + lane / LANES;
+                if (part == 0u && col < p.n) p.delta[size_t(row) * p.n + col] = sum;
+            }
+        }
     }
 }
 
@@ -1322,7 +1374,6 @@ struct LoraListParams {
     const int32_t *ids;
     uint32_t rows, per, adapters;
     int32_t *counts, *list;
-    uint32_t *counter;  // set to zero for the product's tile counter, or null
 };
 
 __global__ void __launch_bounds__(256) lora_list_kernel(const __grid_constant__ LoraListParams p)
@@ -1350,7 +1401,6 @@ __global__ void __launch_bounds__(256) lora_list_kernel(const __grid_constant__ 
         total += s_warp[w];
     }
     if (first) p.list[size_t(blockIdx.x) * p.per + at] = id;
-    if (t == 0 && blockIdx.x == 0 && p.counter) *p.counter = 0u;
     if (t == 0) p.counts[blockIdx.x] = int32_t(total);
     ptx::griddep_launch_dependents();
 }

@@ -6,11 +6,12 @@
 // whose unsigned order is the floats' order, so one step of the choice is a
 // register maximum, a warp maximum of the key and a warp minimum of the index
 // (ties to the lowest).  One block takes 64 rows; which rows of the block chose
-// an expert is a 64-bit mask in shared memory, so a choice's rank among the
+// an expert is two 32-bit masks in shared memory, so a choice's rank among the
 // block's rows is a population count, independent of the order in which the
 // warps set the bits.  One block serves up to 64 rows in one launch; for more,
-// the blocks' counts are scanned over the blocks (route_scan_kernel) and each
-// block turns its ranks into positions (route_place_kernel).
+// route_place_kernel turns the ranks into positions with the counts of the
+// blocks before, which it sums itself or, for very many blocks, finds summed by
+// route_scan_kernel.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -21,8 +22,10 @@
 
 namespace gemm_f16 {
 
-constexpr int kRouteRows = 64;       // rows of a block: the bits of a mask
+constexpr int kRouteRows = 64;       // rows of a block: two for each warp, the bits of two masks
 constexpr int kRouteThreads = 1024;
+constexpr int kRouteDirectBlocks = 512;  // up to so many blocks each one sums the counts before it by itself
+static_assert(kRouteRows == 2 * (kRouteThreads / 32), "two rows a warp");
 constexpr int kRouteMaxExperts = 1024;
 
 struct RouteParams {
@@ -94,74 +97,105 @@ __device__ __forceinline__ int32_t route_block_scan(int32_t v, int32_t *s, int32
 template <int VPT>
 __global__ void __launch_bounds__(kRouteThreads) route_topk_kernel(const __grid_constant__ RouteParams p)
 {
-    __shared__ unsigned long long s_mask[kRouteMaxExperts];
+    __shared__ uint32_t s_mask[2][kRouteMaxExperts];  // rows 0..31 and 32..63 of the block
     __shared__ int32_t s_base[kRouteMaxExperts];
     __shared__ int32_t s_scan[32];
     const uint32_t lane = threadIdx.x & 31u, warp = threadIdx.x >> 5;
-    for (uint32_t e = threadIdx.x; e < p.experts; e += kRouteThreads) s_mask[e] = 0ull;
+    for (uint32_t e = threadIdx.x; e < p.experts; e += kRouteThreads) s_mask[0][e] = s_mask[1][e] = 0u;
     __syncthreads();
     ptx::griddep_wait();
 
+    // A warp's two rows go through the choice side by side where their keys fit the registers: a step is a
+    // chain of warp reductions, and the other row's fills its gaps.
     constexpr int kRowsPerWarp = kRouteRows / (kRouteThreads / 32);
+    constexpr int kTogether = VPT <= 8 ? kRowsPerWarp : 1;
     int32_t id[kRowsPerWarp];
     const uint32_t row0 = blockIdx.x * kRouteRows;
 #pragma unroll
-    for (int q = 0; q < kRowsPerWarp; ++q) {
-        const uint32_t r = warp + uint32_t(q) * (kRouteThreads / 32), row = row0 + r;
-        id[q] = -1;
-        if (row >= p.rows) continue;
-        uint32_t key[VPT];
-        float top_value = -INFINITY;
+    for (int q0 = 0; q0 < kRowsPerWarp; q0 += kTogether) {
+        uint32_t key[kTogether][VPT], mine[kTogether];
+        float top_value[kTogether], sum[kTogether];
+        bool live[kTogether];
 #pragma unroll
-        for (int i = 0; i < VPT; ++i) {
-            const uint32_t e = uint32_t(i) * 32u + lane;
-            const float f = e < p.experts ? route_load(p.logits, p.dtype, size_t(row) * p.experts + e) : -INFINITY;
-            key[i] = route_key(f);
-            top_value = fmaxf(top_value, f);
+        for (int q = 0; q < kTogether; ++q) {
+            const uint32_t row = row0 + warp + uint32_t(q0 + q) * 32u;
+            live[q] = row < p.rows;
+            id[q0 + q] = -1;
+            mine[q] = 0u;  // key of choice `lane`
+            top_value[q] = -INFINITY;
+#pragma unroll
+            for (int i = 0; i < VPT; ++i) {
+                const uint32_t e = uint32_t(i) * 32u + lane;
+                const float f =
+                    (live[q] && e < p.experts) ? route_load(p.logits, p.dtype, size_t(row) * p.experts + e) : -INFINITY;
+                key[q][i] = route_key(f);
+                top_value[q] = fmaxf(top_value[q], f);
+            }
         }
 #pragma unroll
-        for (int d = 16; d > 0; d >>= 1) top_value = fmaxf(top_value, __shfl_xor_sync(0xffffffffu, top_value, d));
-        float sum = 0.0f;
+        for (int d = 16; d > 0; d >>= 1)
 #pragma unroll
-        for (int i = 0; i < VPT; ++i)
-            if (key[i]) sum += expf(route_value(key[i]) - top_value);
-        sum = warp_sum(sum);
-        uint32_t mine = 0u;  // key of choice `lane`
-        for (uint32_t j = 0; j < p.top; ++j) {
-            uint32_t best = 0u, at = 0u;
+            for (int q = 0; q < kTogether; ++q)
+                top_value[q] = fmaxf(top_value[q], __shfl_xor_sync(0xffffffffu, top_value[q], d));
+#pragma unroll
+        for (int q = 0; q < kTogether; ++q) {
+            sum[q] = 0.0f;
 #pragma unroll
             for (int i = 0; i < VPT; ++i)
-                if (key[i] > best) {
-                    best = key[i];
-                    at = uint32_t(i);
-                }
-            const uint32_t k = __reduce_max_sync(0xffffffffu, best);
-            if (k == 0u) break;  // only experts at -infinity are left
-            const uint32_t e = __reduce_min_sync(0xffffffffu, best == k ? at * 32u + lane : 0xffffffffu);
-            if ((e & 31u) == lane) {
+                if (key[q][i]) sum[q] += expf(route_value(key[q][i]) - top_value[q]);
+        }
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1)
+#pragma unroll
+            for (int q = 0; q < kTogether; ++q) sum[q] += __shfl_xor_sync(0xffffffffu, sum[q], d);
+        for (uint32_t j = 0; j < p.top; ++j) {
+            uint32_t best[kTogether], at[kTogether], k[kTogether], e[kTogether];
+#pragma unroll
+            for (int q = 0; q < kTogether; ++q) {
+                best[q] = at[q] = 0u;
 #pragma unroll
                 for (int i = 0; i < VPT; ++i)
-                    if (uint32_t(i) == (e >> 5)) key[i] = 0u;
+                    if (key[q][i] > best[q]) {
+                        best[q] = key[q][i];
+                        at[q] = uint32_t(i);
+                    }
+                k[q] = __reduce_max_sync(0xffffffffu, best[q]);
             }
-            if (lane == j) {
-                mine = k;
-                id[q] = int32_t(e);
+#pragma unroll
+            for (int q = 0; q < kTogether; ++q)
+                e[q] = __reduce_min_sync(0xffffffffu, best[q] == k[q] ? at[q] * 32u + lane : 0xffffffffu);
+#pragma unroll
+            for (int q = 0; q < kTogether; ++q) {
+                // (k = 0: only experts at -infinity are left, nothing to take)
+                if ((e[q] & 31u) == lane) {
+#pragma unroll
+                    for (int i = 0; i < VPT; ++i)
+                        if (uint32_t(i) == (e[q] >> 5)) key[q][i] = 0u;
+                }
+                if (lane == j && k[q] != 0u) {
+                    mine[q] = k[q];
+                    id[q0 + q] = int32_t(e[q]);
+                }
             }
         }
-        float w = mine ? expf(route_value(mine) - top_value) : 0.0f;
-        const float chosen = warp_sum(w);
-        // (a NaN anywhere in the row shows in every weight, chosen or not)
-        if (p.renorm && sum == sum) sum = chosen;
-        w = mine ? w / sum : 0.0f;
-        if (lane < p.top) {
-            p.ids[size_t(row) * p.top + lane] = id[q];
-            p.weights[size_t(row) * p.top + lane] = w;
-            if (id[q] >= 0) atomicOr(&s_mask[id[q]], 1ull << r);
+#pragma unroll
+        for (int q = 0; q < kTogether; ++q) {
+            const uint32_t row = row0 + warp + uint32_t(q0 + q) * 32u;
+            float w = mine[q] ? expf(route_value(mine[q]) - top_value[q]) : 0.0f;
+            const float chosen = warp_sum(w);
+            // (a NaN anywhere in the row shows in every weight, chosen or not)
+            if (p.renorm && sum[q] == sum[q]) sum[q] = chosen;
+            w = mine[q] ? w / sum[q] : 0.0f;
+            if (live[q] && lane < p.top) {
+                p.ids[size_t(row) * p.top + lane] = id[q0 + q];
+                p.weights[size_t(row) * p.top + lane] = w;
+                if (id[q0 + q] >= 0) atomicOr(&s_mask[q0 + q][id[q0 + q]], 1u << warp);
+            }
         }
     }
     __syncthreads();
     const uint32_t t = threadIdx.x;
-    const int32_t count = t < p.experts ? __popcll(s_mask[t]) : 0;
+    const int32_t count = t < p.experts ? __popc(s_mask[0][t]) + __popc(s_mask[1][t]) : 0;
     if (p.blocks > 1u) {
         if (t < p.experts) p.hist[size_t(blockIdx.x) * p.experts + t] = count;
     } else {
@@ -177,12 +211,13 @@ __global__ void __launch_bounds__(kRouteThreads) route_topk_kernel(const __grid_
     }
 #pragma unroll
     for (int q = 0; q < kRowsPerWarp; ++q) {
-        const uint32_t r = warp + uint32_t(q) * (kRouteThreads / 32), row = row0 + r;
+        const uint32_t row = row0 + warp + uint32_t(q) * 32u;
         if (row >= p.rows || lane >= p.top) continue;
         const size_t flat = size_t(row) * p.top + lane;
         int32_t at = -1;
         if (id[q] >= 0) {
-            at = __popcll(s_mask[id[q]] & ((1ull << r) - 1ull));
+            // the block's rows before this one that chose the same expert (rows of this warp: r = warp, 32 + warp)
+            at = __popc(s_mask[q][id[q]] & ((1u << warp) - 1u)) + (q ? __popc(s_mask[0][id[q]]) : 0);
             if (p.blocks == 1u) {
                 at += s_base[id[q]];
                 p.order[at] = int32_t(flat);
@@ -234,12 +269,40 @@ __global__ void __launch_bounds__(kRouteThreads) route_place_kernel(const __grid
 {
     __shared__ int32_t s_base[kRouteMaxExperts];
     __shared__ int32_t s_scan[32];
+    __shared__ int2 s_part[kRouteThreads];
     ptx::griddep_wait();
     const uint32_t t = threadIdx.x;
+    int32_t count = 0, prefix = 0;  // of expert t: all its rows, and those of the blocks before this one
+    if (p.blocks <= kRouteDirectBlocks) {
+        // `lanes` threads to an expert, each sums every lanes-th block; then one adds them up
+        uint32_t lanes = kRouteThreads / p.experts;
+        lanes = lanes > 32u ? 32u : lanes;
+        const uint32_t e = t % p.experts, part = t / p.experts;
+        int32_t a = 0, b = 0;
+        if (part < lanes) {
+#pragma unroll 8
+            for (uint32_t i = part; i < p.blocks; i += lanes) {
+                const int32_t c = p.hist[size_t(i) * p.experts + e];
+                a += c;
+                b += i < blockIdx.x ? c : 0;
+            }
+        }
+        s_part[t] = make_int2(a, b);
+        __syncthreads();
+        if (t < p.experts)
+            for (uint32_t i = 0; i < lanes; ++i) {
+                const int2 c = s_part[i * p.experts + t];
+                count += c.x;
+                prefix += c.y;
+            }
+    } else if (t < p.experts) {
+        count = p.totals[t];
+        prefix = p.hist[size_t(blockIdx.x) * p.experts + t];
+    }
     int32_t total;
-    const int32_t before = route_block_scan(t < p.experts ? p.totals[t] : 0, s_scan, &total);
+    const int32_t before = route_block_scan(count, s_scan, &total);
     if (t < p.experts) {
-        s_base[t] = before + p.hist[size_t(blockIdx.x) * p.experts + t];
+        s_base[t] = before + prefix;
         if (blockIdx.x == 0) p.offsets[t] = before;
     }
     if (blockIdx.x == 0 && t == 0) p.offsets[p.experts] = total;
@@ -263,6 +326,7 @@ __global__ void __launch_bounds__(kRouteThreads) route_place_kernel(const __grid
 template <int VPT>
 __global__ void __launch_bounds__(256) route_grad_kernel(const __grid_constant__ RouteParams p)
 {
+    __shared__ float s_row[8 * VPT * 32];
     ptx::griddep_wait();
     const uint32_t lane = threadIdx.x & 31u;
     const uint32_t row = blockIdx.x * 8u + (threadIdx.x >> 5);
@@ -274,17 +338,15 @@ __global__ void __launch_bounds__(256) route_grad_kernel(const __grid_constant__
         const float inner = warp_sum(id >= 0 ? w * dw : 0.0f);
         float f[VPT], d[VPT];
         float top_value = -INFINITY, sum = 0.0f;
+        // the chosen experts' values, put in their places through shared memory
+        float *mine = s_row + (threadIdx.x >> 5) * (VPT * 32);
 #pragma unroll
-        for (int i = 0; i < VPT; ++i) d[i] = 0.0f;
-        for (uint32_t j = 0; j < p.top; ++j) {
-            const int32_t e = __shfl_sync(0xffffffffu, id, j);
-            const float v = __shfl_sync(0xffffffffu, p.renorm ? w * (dw - inner) : dw, j);
-            if (e >= 0 && (uint32_t(e) & 31u) == lane) {
+        for (int i = 0; i < VPT; ++i) mine[i * 32 + lane] = 0.0f;
+        __syncwarp();
+        if (id >= 0 && id < int32_t(p.experts)) mine[id] = p.renorm ? w * (dw - inner) : dw;
+        __syncwarp();
 #pragma unroll
-                for (int i = 0; i < VPT; ++i)
-                    if (uint32_t(i) == (uint32_t(e) >> 5)) d[i] = v;
-            }
-        }
+        for (int i = 0; i < VPT; ++i) d[i] = mine[i * 32 + lane];
         if (!p.renorm) {
 #pragma unroll
             for (int i = 0; i < VPT; ++i) {

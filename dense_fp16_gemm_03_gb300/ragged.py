@@ -277,12 +277,11 @@ def gemm_route_topk(logits, top, renorm=True, out=None, workspace=None, stream=N
         raise ValueError("top must be in [1, experts]")
     i32 = torch.int32
     if out is None:
-        # one allocation for the five: each part starts on a 16-byte boundary
-        c = rows * top
-        pad, eo = (c + 3) & ~3, (experts + 4) & ~3
-        buf = _empty((4 * pad + eo,), i32, dev)
-        at = buf.data_ptr()
-        ids_at, weights_at, position_at, order_at, offsets_at = at, at + 4 * pad, at + 8 * pad, at + 12 * pad, at + 16 * pad
+        # one allocation for the four of a choice's size, their views made while the GPU already works
+        buf = _empty((4, rows, top), i32, dev)
+        offsets = _empty((experts + 1,), i32, dev)
+        size, at = 4 * rows * top, buf.data_ptr()
+        ids_at, weights_at, position_at, order_at, offsets_at = at, at + size, at + 2 * size, at + 3 * size, offsets.data_ptr()
         r = None
     else:
         r = out
@@ -298,11 +297,8 @@ def gemm_route_topk(logits, top, renorm=True, out=None, workspace=None, stream=N
                                order_at, position_at, ws, ws_bytes, _stream(stream, dev))
     _check(st, "gemm_route_topk")
     if r is None:
-        # (the views are made while the GPU already works)
-        shape, steps = (rows, top), (top, 1)
-        r = Routing(buf.as_strided(shape, steps, 0), buf.view(torch.float32).as_strided(shape, steps, pad),
-                    buf.as_strided((experts + 1,), (1,), 4 * pad), buf.as_strided((c,), (1,), 3 * pad),
-                    buf.as_strided(shape, steps, 2 * pad))
+        ids, weights, position, order = buf.unbind(0)
+        r = Routing(ids, weights.view(torch.float32), offsets, order.view(-1), position)
     return r
 
 

@@ -68,10 +68,11 @@ typedef enum gemm_dtype {
  * contraction writes zeros.  The contents of rows of other groups never reach a
  * result, whatever they hold (infinities, NaN).
  *
- * gemm_grouped_workspace_size: bytes that let any of the three split work over
- * K (its largest need on the current device).  A workspace may be NULL/0: then
- * nothing is split, which costs time where there are few rows; one that is given
- * but too small is GEMM_ERR_WORKSPACE.
+ * gemm_grouped_workspace_size: bytes that serve any of the three calls of these
+ * sizes on the current device (partial sums of split tiles, tensor maps of the
+ * groups; it may be 0).  A workspace may be NULL/0 all the same: that costs time
+ * where there are few rows, and in gemm_grouped_tn; one that is given but too
+ * small is GEMM_ERR_WORKSPACE.
  */
 gemm_status_t gemm_grouped_workspace_size(int64_t groups, int64_t rows, int64_t n, int64_t k, size_t *bytes);
 gemm_status_t gemm_grouped_nt(gemm_dtype_t dtype, int64_t groups, int64_t rows, int64_t n, int64_t k,
@@ -92,10 +93,10 @@ gemm_status_t gemm_grouped_tn(gemm_dtype_t dtype, gemm_dtype_t out, int64_t grou
  * x [rows, k], w [n, k], a [adapters, rank, k], b [adapters, n, rank],
  * y [rows, n]; ids: rows int32 in any order, a row whose id is outside
  * [0, adapters) has no adapter; scale: adapters fp32, or NULL for 1.  The inner
- * product scale (x a^T) is rounded to the operands' type; the two products are
+ * product scale (x a^T) is rounded to the operands' type for more than 64 rows; the two products are
  * added in fp32 and rounded once.  What an adapter holds reaches the rows that
- * have it and no others, infinities and NaN included (an infinity in b acts as a
- * NaN).  The workspace is required (gemm_lora_workspace_size on the current
+ * have it and no others, infinities and NaN included (a product with an infinity
+ * of b may come out as NaN).  The workspace is required (gemm_lora_workspace_size on the current
  * device; GEMM_ERR_WORKSPACE).
  */
 gemm_status_t gemm_lora_workspace_size(int64_t rows, int64_t n, int64_t k, int64_t rank, int64_t adapters, size_t *bytes);

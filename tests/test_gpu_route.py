@@ -173,3 +173,8 @@ def test_route_then_experts():
     no_device_error()
     assert torch.equal(y.cpu(), grouped_ref("nt", xs.cpu(), w, r.offsets, experts).half())
     assert G.gemm_f16_take_device_error()[0] == G.GEMM_OK
+
+
+def test_very_many_rows():
+    """More blocks than one sums by itself: the counts are scanned by a kernel of their own."""
+    check(draw(40000, 16, "bf16", 2), 4, False)
