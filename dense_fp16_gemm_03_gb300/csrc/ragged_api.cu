@@ -748,24 +748,32 @@ static gemm_status_t check_route(gemm_dtype_t dtype, int64_t rows, int64_t exper
     return GEMM_OK;
 }
 
+static int64_t route_blocks(int64_t rows)
+{
+    return rows <= kRouteFewRows ? 1 : cdiv(rows, kRouteRows);
+}
+
 gemm_status_t gemm_route_workspace_size(int64_t rows, int64_t experts, int64_t top, size_t *bytes)
 {
     if (!bytes) return GEMM_ERR_INVALID_ARG;
     gemm_status_t st = check_route(GEMM_DTYPE_F32, rows, experts, top);
     if (st != GEMM_OK) return st;
-    const int64_t blocks = cdiv(rows, kRouteRows);
+    const int64_t blocks = route_blocks(rows);
     *bytes = blocks > 1 ? size_t(blocks + 1) * size_t(experts) * 4u : 0;
     return GEMM_OK;
 }
 
-// The instance of a kernel template whose lanes hold enough values for `experts`.
-#define ROUTE_INSTANCE(KERNEL, experts)                                                                               \
-    ((experts) <= 32    ? reinterpret_cast<const void *>(&KERNEL<1>)                                                  \
-     : (experts) <= 64  ? reinterpret_cast<const void *>(&KERNEL<2>)                                                  \
-     : (experts) <= 128 ? reinterpret_cast<const void *>(&KERNEL<4>)                                                  \
-     : (experts) <= 256 ? reinterpret_cast<const void *>(&KERNEL<8>)                                                  \
-     : (experts) <= 512 ? reinterpret_cast<const void *>(&KERNEL<16>)                                                 \
-                        : reinterpret_cast<const void *>(&KERNEL<32>))
+// The instance of a kernel whose lanes hold enough values for `experts`.
+#define ROUTE_INSTANCE(F, experts)                                                                                       \
+    ((experts) <= 32    ? F(1)                                                                                           \
+     : (experts) <= 64  ? F(2)                                                                                           \
+     : (experts) <= 128 ? F(4)                                                                                           \
+     : (experts) <= 256 ? F(8)                                                                                           \
+     : (experts) <= 512 ? F(16)                                                                                          \
+                        : F(32))
+#define ROUTE_TOPK_FEW(V) reinterpret_cast<const void *>(&route_topk_kernel<V, kRouteThreads>)
+#define ROUTE_TOPK(V) reinterpret_cast<const void *>(&route_topk_kernel<V, 16 * kRouteRows>)
+#define ROUTE_GRAD(V) reinterpret_cast<const void *>(&route_grad_kernel<V>)
 
 gemm_status_t gemm_route_topk(gemm_dtype_t dtype, int64_t rows, int64_t experts, int64_t top, int32_t renorm, const void *logits,
                               int32_t *ids, float *weights, int32_t *offsets, int32_t *order, int32_t *position, void *workspace,
@@ -791,7 +799,7 @@ gemm_status_t gemm_route_topk(gemm_dtype_t dtype, int64_t rows, int64_t experts,
         }
         return GEMM_OK;
     }
-    const int64_t blocks = cdiv(rows, kRouteRows);
+    const int64_t blocks = route_blocks(rows);
     if (blocks > 1) {
         if (workspace == nullptr || ws_bytes < size_t(blocks + 1) * size_t(experts) * 4u) return GEMM_ERR_WORKSPACE;
         if (reinterpret_cast<uintptr_t>(workspace) & 255u) return GEMM_ERR_ALIGNMENT;
@@ -813,8 +821,9 @@ gemm_status_t gemm_route_topk(gemm_dtype_t dtype, int64_t rows, int64_t experts,
     p.hist = static_cast<int32_t *>(workspace);
     p.totals = p.hist ? p.hist + size_t(blocks) * size_t(experts) : nullptr;
     void *args[1] = {&p};
-    st = launch(ROUTE_INSTANCE(route_topk_kernel, experts), dim3(unsigned(blocks), 1, 1), kRouteThreads, 0, 1, args, s);
-    if (st != GEMM_OK || blocks == 1) return st;
+    if (blocks == 1) return launch(ROUTE_INSTANCE(ROUTE_TOPK_FEW, experts), dim3(1, 1, 1), kRouteThreads, 0, 1, args, s);
+    st = launch(ROUTE_INSTANCE(ROUTE_TOPK, experts), dim3(unsigned(blocks), 1, 1), 16 * kRouteRows, 0, 1, args, s);
+    if (st != GEMM_OK) return st;
     if (blocks > kRouteDirectBlocks)
         st = launch(reinterpret_cast<const void *>(&route_scan_kernel), dim3(unsigned(cdiv(experts, 32)), 1, 1), 1024, 0, 1, args, s);
     if (st != GEMM_OK) return st;
@@ -849,7 +858,7 @@ gemm_status_t gemm_route_topk_grad(gemm_dtype_t dtype, int64_t rows, int64_t exp
     p.dweights = dweights;
     p.dlogits = dlogits;
     void *args[1] = {&p};
-    return launch(ROUTE_INSTANCE(route_grad_kernel, experts), dim3(unsigned(cdiv(rows, 8)), 1, 1), 256, 0, 1, args,
+    return launch(ROUTE_INSTANCE(ROUTE_GRAD, experts), dim3(unsigned(cdiv(rows, 8)), 1, 1), 256, 0, 1, args,
                   reinterpret_cast<cudaStream_t>(stream));
 }
 

@@ -22,10 +22,12 @@
 
 namespace gemm_f16 {
 
-constexpr int kRouteRows = 64;       // rows of a block: two for each warp, the bits of two masks
-constexpr int kRouteThreads = 1024;
-constexpr int kRouteDirectBlocks = 512;  // up to so many blocks each one sums the counts before it by itself
-static_assert(kRouteRows == 2 * (kRouteThreads / 32), "two rows a warp");
+// A block's rows, two for each of its warps (the bits of two masks).  Up to kRouteFewRows rows one block does
+// everything; more go 32 to a block, which keeps more warps on an SM.
+constexpr int kRouteFewRows = 64;
+constexpr int kRouteRows = 32;
+constexpr int kRouteThreads = 1024;  // of the block for few rows, and of the kernels that place rows
+constexpr int kRouteDirectBlocks = 32;  // up to so many blocks each one sums the counts before it by itself
 constexpr int kRouteMaxExperts = 1024;
 
 struct RouteParams {
@@ -41,11 +43,26 @@ struct RouteParams {
     float *dlogits;
 };
 
-__device__ __forceinline__ float route_load(const void *base, uint32_t dtype, size_t i)
+// A row's logits, `lane`, 32 + lane, ... (-infinity past the last): all loads before the first conversion.
+template <int VPT>
+__device__ __forceinline__ void route_load(const void *base, uint32_t dtype, size_t row, uint32_t experts, bool live,
+                                           float (&f)[VPT])
 {
-    if (dtype == 2u) return static_cast<const float *>(base)[i];
-    if (dtype == 1u) return __bfloat162float(static_cast<const __nv_bfloat16 *>(base)[i]);
-    return __half2float(static_cast<const __half *>(base)[i]);
+    const uint32_t lane = threadIdx.x & 31u;
+    if (dtype == 2u) {
+        const float *p = static_cast<const float *>(base) + row * experts + lane;
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) f[i] = (live && uint32_t(i) * 32u + lane < experts) ? p[i * 32] : -INFINITY;
+        return;
+    }
+    const uint16_t *p = static_cast<const uint16_t *>(base) + row * experts + lane;
+    const uint32_t none = dtype == 1u ? 0xFF80u : 0xFC00u;  // -infinity
+    uint32_t raw[VPT];
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) raw[i] = (live && uint32_t(i) * 32u + lane < experts) ? uint32_t(p[i * 32]) : none;
+#pragma unroll
+    for (int i = 0; i < VPT; ++i)
+        f[i] = dtype == 1u ? __uint_as_float(raw[i] << 16) : __half2float(__ushort_as_half(static_cast<unsigned short>(raw[i])));
 }
 
 // Unsigned order = float order; -0 counts as +0.  0: never chosen (-infinity), 1: NaN.
@@ -94,44 +111,46 @@ __device__ __forceinline__ int32_t route_block_scan(int32_t v, int32_t *s, int32
     return x - v + (warp ? before : 0);
 }
 
-template <int VPT>
-__global__ void __launch_bounds__(kRouteThreads) route_topk_kernel(const __grid_constant__ RouteParams p)
+template <int VPT, int THREADS>
+__global__ void __launch_bounds__(THREADS) route_topk_kernel(const __grid_constant__ RouteParams p)
 {
-    __shared__ uint32_t s_mask[2][kRouteMaxExperts];  // rows 0..31 and 32..63 of the block
+    constexpr uint32_t kWarps = THREADS / 32;
+    __shared__ uint32_t s_mask[2][kRouteMaxExperts];  // bit w: the block's row w, kWarps + w
     __shared__ int32_t s_base[kRouteMaxExperts];
     __shared__ int32_t s_scan[32];
     const uint32_t lane = threadIdx.x & 31u, warp = threadIdx.x >> 5;
-    for (uint32_t e = threadIdx.x; e < p.experts; e += kRouteThreads) s_mask[0][e] = s_mask[1][e] = 0u;
+    for (uint32_t e = threadIdx.x; e < p.experts; e += THREADS) s_mask[0][e] = s_mask[1][e] = 0u;
     __syncthreads();
     ptx::griddep_wait();
 
     // A warp's two rows go through the choice side by side where their keys fit the registers: a step is a
     // chain of warp reductions, and the other row's fills its gaps.
-    constexpr int kRowsPerWarp = kRouteRows / (kRouteThreads / 32);
+    constexpr int kRowsPerWarp = 2;
     constexpr int kTogether = VPT <= 8 ? kRowsPerWarp : 1;
+    constexpr bool kSort = VPT <= 4;  // (28 exchanges for eight keys are more than they spare)
     int32_t id[kRowsPerWarp];
-    const uint32_t row0 = blockIdx.x * kRouteRows;
+    const uint32_t row0 = blockIdx.x * (2u * kWarps);
 #pragma unroll
     for (int q0 = 0; q0 < kRowsPerWarp; q0 += kTogether) {
         uint32_t key[kTogether][VPT], mine[kTogether];
-        float top_value[kTogether], sum[kTogether];
+        float f[kTogether][VPT], top_value[kTogether], sum[kTogether];
         bool live[kTogether];
 #pragma unroll
         for (int q = 0; q < kTogether; ++q) {
-            const uint32_t row = row0 + warp + uint32_t(q0 + q) * 32u;
+            const uint32_t row = row0 + warp + uint32_t(q0 + q) * kWarps;
             live[q] = row < p.rows;
             id[q0 + q] = -1;
             mine[q] = 0u;  // key of choice `lane`
             top_value[q] = -INFINITY;
+            route_load<VPT>(p.logits, p.dtype, row, p.experts, live[q], f[q]);
+        }
+#pragma unroll
+        for (int q = 0; q < kTogether; ++q)
 #pragma unroll
             for (int i = 0; i < VPT; ++i) {
-                const uint32_t e = uint32_t(i) * 32u + lane;
-                const float f =
-                    (live[q] && e < p.experts) ? route_load(p.logits, p.dtype, size_t(row) * p.experts + e) : -INFINITY;
-                key[q][i] = route_key(f);
-                top_value[q] = fmaxf(top_value[q], f);
+                key[q][i] = route_key(f[q][i]);
+                top_value[q] = fmaxf(top_value[q], f[q][i]);
             }
-        }
 #pragma unroll
         for (int d = 16; d > 0; d >>= 1)
 #pragma unroll
@@ -142,35 +161,69 @@ __global__ void __launch_bounds__(kRouteThreads) route_topk_kernel(const __grid_
             sum[q] = 0.0f;
 #pragma unroll
             for (int i = 0; i < VPT; ++i)
-                if (key[q][i]) sum[q] += expf(route_value(key[q][i]) - top_value[q]);
+                if (key[q][i]) sum[q] += expf(f[q][i] - top_value[q]);
         }
 #pragma unroll
         for (int d = 16; d > 0; d >>= 1)
 #pragma unroll
             for (int q = 0; q < kTogether; ++q) sum[q] += __shfl_xor_sync(0xffffffffu, sum[q], d);
+        // A lane's keys in falling order, equal ones by rising index: a step then looks at the first alone.
+        uint32_t slot[kTogether][kSort ? VPT : 1];
+        if constexpr (kSort) {
+#pragma unroll
+            for (int q = 0; q < kTogether; ++q) {
+#pragma unroll
+                for (int i = 0; i < VPT; ++i) slot[q][i] = uint32_t(i) * 32u + lane;
+#pragma unroll
+                for (int end = VPT - 1; end > 0; --end)
+#pragma unroll
+                    for (int i = 0; i < end; ++i)
+                        if (key[q][i + 1] > key[q][i]) {
+                            const uint32_t k = key[q][i], a = slot[q][i];
+                            key[q][i] = key[q][i + 1];
+                            slot[q][i] = slot[q][i + 1];
+                            key[q][i + 1] = k;
+                            slot[q][i + 1] = a;
+                        }
+            }
+        }
         for (uint32_t j = 0; j < p.top; ++j) {
             uint32_t best[kTogether], at[kTogether], k[kTogether], e[kTogether];
 #pragma unroll
             for (int q = 0; q < kTogether; ++q) {
-                best[q] = at[q] = 0u;
+                if constexpr (kSort) {
+                    best[q] = key[q][0];
+                    at[q] = slot[q][0];
+                } else {
+                    best[q] = at[q] = 0u;
 #pragma unroll
-                for (int i = 0; i < VPT; ++i)
-                    if (key[q][i] > best[q]) {
-                        best[q] = key[q][i];
-                        at[q] = uint32_t(i);
-                    }
+                    for (int i = 0; i < VPT; ++i)
+                        if (key[q][i] > best[q]) {
+                            best[q] = key[q][i];
+                            at[q] = uint32_t(i) * 32u + lane;
+                        }
+                }
                 k[q] = __reduce_max_sync(0xffffffffu, best[q]);
             }
 #pragma unroll
             for (int q = 0; q < kTogether; ++q)
-                e[q] = __reduce_min_sync(0xffffffffu, best[q] == k[q] ? at[q] * 32u + lane : 0xffffffffu);
+                e[q] = __reduce_min_sync(0xffffffffu, best[q] == k[q] ? at[q] : 0xffffffffu);
 #pragma unroll
             for (int q = 0; q < kTogether; ++q) {
                 // (k = 0: only experts at -infinity are left, nothing to take)
-                if ((e[q] & 31u) == lane) {
+                if (at[q] == e[q]) {
+                    if constexpr (kSort) {
 #pragma unroll
-                    for (int i = 0; i < VPT; ++i)
-                        if (uint32_t(i) == (e[q] >> 5)) key[q][i] = 0u;
+                        for (int i = 0; i + 1 < VPT; ++i) {
+                            key[q][i] = key[q][i + 1];
+                            slot[q][i] = slot[q][i + 1];
+                        }
+                        key[q][VPT - 1] = 0u;
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < VPT; ++i)
+                            if (uint32_t(i) == (e[q] >> 5)) key[q][i] = 0u;
+                    }
                 }
                 if (lane == j && k[q] != 0u) {
                     mine[q] = k[q];
@@ -180,7 +233,7 @@ __global__ void __launch_bounds__(kRouteThreads) route_topk_kernel(const __grid_
         }
 #pragma unroll
         for (int q = 0; q < kTogether; ++q) {
-            const uint32_t row = row0 + warp + uint32_t(q0 + q) * 32u;
+            const uint32_t row = row0 + warp + uint32_t(q0 + q) * kWarps;
             float w = mine[q] ? expf(route_value(mine[q]) - top_value[q]) : 0.0f;
             const float chosen = warp_sum(w);
             // (a NaN anywhere in the row shows in every weight, chosen or not)
@@ -195,10 +248,11 @@ __global__ void __launch_bounds__(kRouteThreads) route_topk_kernel(const __grid_
     }
     __syncthreads();
     const uint32_t t = threadIdx.x;
-    const int32_t count = t < p.experts ? __popc(s_mask[0][t]) + __popc(s_mask[1][t]) : 0;
-    if (p.blocks > 1u) {
-        if (t < p.experts) p.hist[size_t(blockIdx.x) * p.experts + t] = count;
+    if (THREADS < kRouteThreads || p.blocks > 1u) {
+        for (uint32_t e = t; e < p.experts; e += THREADS)
+            p.hist[size_t(blockIdx.x) * p.experts + e] = __popc(s_mask[0][e]) + __popc(s_mask[1][e]);
     } else {
+        const int32_t count = t < p.experts ? __popc(s_mask[0][t]) + __popc(s_mask[1][t]) : 0;
         int32_t total;
         const int32_t before = route_block_scan(count, s_scan, &total);
         if (t < p.experts) {
@@ -206,12 +260,12 @@ __global__ void __launch_bounds__(kRouteThreads) route_topk_kernel(const __grid_
             p.offsets[t] = before;
         }
         if (t == 0) p.offsets[p.experts] = total;
-        for (uint32_t i = uint32_t(total) + t; i < p.rows * p.top; i += kRouteThreads) p.order[i] = -1;
+        for (uint32_t i = uint32_t(total) + t; i < p.rows * p.top; i += THREADS) p.order[i] = -1;
         __syncthreads();
     }
 #pragma unroll
     for (int q = 0; q < kRowsPerWarp; ++q) {
-        const uint32_t row = row0 + warp + uint32_t(q) * 32u;
+        const uint32_t row = row0 + warp + uint32_t(q) * kWarps;
         if (row >= p.rows || lane >= p.top) continue;
         const size_t flat = size_t(row) * p.top + lane;
         int32_t at = -1;
@@ -338,6 +392,7 @@ __global__ void __launch_bounds__(256) route_grad_kernel(const __grid_constant__
         const float inner = warp_sum(id >= 0 ? w * dw : 0.0f);
         float f[VPT], d[VPT];
         float top_value = -INFINITY, sum = 0.0f;
+        if (!p.renorm) route_load<VPT>(p.logits, p.dtype, row, p.experts, true, f);
         // the chosen experts' values, put in their places through shared memory
         float *mine = s_row + (threadIdx.x >> 5) * (VPT * 32);
 #pragma unroll
@@ -349,11 +404,7 @@ __global__ void __launch_bounds__(256) route_grad_kernel(const __grid_constant__
         for (int i = 0; i < VPT; ++i) d[i] = mine[i * 32 + lane];
         if (!p.renorm) {
 #pragma unroll
-            for (int i = 0; i < VPT; ++i) {
-                const uint32_t e = uint32_t(i) * 32u + lane;
-                f[i] = e < p.experts ? route_load(p.logits, p.dtype, size_t(row) * p.experts + e) : -INFINITY;
-                top_value = fmaxf(top_value, f[i]);
-            }
+            for (int i = 0; i < VPT; ++i) top_value = fmaxf(top_value, f[i]);
 #pragma unroll
             for (int s = 16; s > 0; s >>= 1) top_value = fmaxf(top_value, __shfl_xor_sync(0xffffffffu, top_value, s));
 #pragma unroll

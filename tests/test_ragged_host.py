@@ -131,7 +131,7 @@ def test_workspace_queries_refuse(L):
     assert L.gemm_lora_workspace_size(1, 8, 8, 256, 1, ctypes.byref(b)) == SHAPE
     assert L.gemm_route_workspace_size(1, 8, 9, ctypes.byref(b)) == INVALID
     assert L.gemm_route_workspace_size(64, 128, 8, ctypes.byref(b)) == G.GEMM_OK and b.value == 0
-    assert L.gemm_route_workspace_size(65, 128, 8, ctypes.byref(b)) == G.GEMM_OK and b.value == 3 * 128 * 4
+    assert L.gemm_route_workspace_size(65, 128, 8, ctypes.byref(b)) == G.GEMM_OK and b.value == 4 * 128 * 4
 
 
 def test_binding_checks_tensors():
