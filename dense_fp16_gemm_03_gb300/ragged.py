@@ -276,29 +276,22 @@ def gemm_route_topk(logits, top, renorm=True, out=None, workspace=None, stream=N
     if top < 1 or top > experts:
         raise ValueError("top must be in [1, experts]")
     i32 = torch.int32
-    if out is None:
-        # one allocation for the four of a choice's size, their views made while the GPU already works
-        buf = _empty((4, rows, top), i32, dev)
-        offsets = _empty((experts + 1,), i32, dev)
-        size, at = 4 * rows * top, buf.data_ptr()
-        ids_at, weights_at, position_at, order_at, offsets_at = at, at + size, at + 2 * size, at + 3 * size, offsets.data_ptr()
-        r = None
+    shape, f32 = (rows, top), torch.float32
+    if out is None:  # (five allocations are quicker than views of one)
+        r = Routing(_empty(shape, i32, dev), _empty(shape, f32, dev), _empty((experts + 1,), i32, dev),
+                    _empty((rows * top,), i32, dev), _empty(shape, i32, dev))
     else:
         r = out
-        _need(r.ids, "ids", (rows, top), i32, dev)
-        _need(r.weights, "weights", (rows, top), torch.float32, dev)
+        _need(r.ids, "ids", shape, i32, dev)
+        _need(r.weights, "weights", shape, f32, dev)
         _need(r.offsets, "offsets", (experts + 1,), i32, dev)
         _need(r.order, "order", (rows * top,), i32, dev)
-        _need(r.position, "position", (rows, top), i32, dev)
-        ids_at, weights_at, offsets_at, order_at, position_at = (t.data_ptr() for t in (r.ids, r.weights, r.offsets, r.order,
-                                                                                        r.position))
+        _need(r.position, "position", shape, i32, dev)
     ws, ws_bytes = _workspace(workspace, dev)
-    st = lib().gemm_route_topk(code, rows, experts, top, 1 if renorm else 0, logits.data_ptr(), ids_at, weights_at, offsets_at,
-                               order_at, position_at, ws, ws_bytes, _stream(stream, dev))
+    st = lib().gemm_route_topk(code, rows, experts, top, 1 if renorm else 0, logits.data_ptr(), r.ids.data_ptr(),
+                               r.weights.data_ptr(), r.offsets.data_ptr(), r.order.data_ptr(), r.position.data_ptr(), ws,
+                               ws_bytes, _stream(stream, dev))
     _check(st, "gemm_route_topk")
-    if r is None:
-        ids, weights, position, order = buf.unbind(0)
-        r = Routing(ids, weights.view(torch.float32), offsets, order.view(-1), position)
     return r
 
 
