@@ -311,26 +311,54 @@ gemm_status_t launch_ragged(int variant, const RaggedDevice *dev, RaggedParams &
 
 // ------------------------------------------------------ grouped products
 
-// Few rows per group: single CTAs with a 64-row N side; each group's weights are then read once and the
-// time is theirs.  More: CTA pairs.
-bool few_rows(int64_t groups, int64_t rows)
+// Whether fewer tiles than CTA pairs are worth splitting over K: the pairs left idle against 20 us of adding partials.
+bool split_pays(int64_t tiles, int64_t blocks, int slots)
 {
-    return rows <= 64 * groups;
+    return tiles < slots && 0.27 * double(blocks) * (1.0 - double(tiles) / slots) > 16.0;
 }
 
-int grouped_variant(int mode, int64_t groups, int64_t rows)
+// Single CTAs with a 64-row N side, or CTA pairs with up to 256 rows: whichever an estimate of the time (us) has
+// ahead for groups of equal size.  A single CTA's K block brings 24 KB into its SM, all of which together take in about
+// 12 TB/s; a pair's K block takes 0.16 us of loads or, with all 256 rows, 0.27 of MMA, over whole waves of tiles or,
+// split, an even share and some 20 us of adding partials (128 KB for every CTA).  A tile's end costs about 2 us of a
+// single CTA and 4 of a pair (24 groups of 16121 rows in all, 2024 x 136: 64 us on single CTAs, 34 on pairs).
+int grouped_variant(int mode, int64_t groups, int64_t rows, int64_t pdim, int64_t kdim, const RaggedDevice *dev)
 {
     if (mode == kTN) return kVTn;
-    const bool few = few_rows(groups, rows);
-    if (mode == kNT) return few ? kVNtFew : kVNtWide;
-    return few ? kVNnFew : kVNnWide;
+    const int few_v = mode == kNT ? kVNtFew : kVNnFew, wide_v = mode == kNT ? kVNtWide : kVNnWide;
+    if (rows <= kRagged[few_v].qcap * groups) return few_v;
+    const double live = double(groups < rows ? groups : rows), each = double(rows) / live, blocks = double(cdiv(kdim, kRagBlockK));
+    const RaggedVariant &f = kRagged[few_v], &w = kRagged[wide_v];
+    const double few_tiles = live * double(cdiv(int64_t(each), f.qcap)) * double(cdiv(pdim, 128));
+    const double wide_tiles = live * double(cdiv(int64_t(each), w.qcap)) * double(cdiv(pdim, 256));
+    const double few = few_tiles * (blocks * 24576.0 / 12e6 + 2.0 / dev->slots[few_v]);
+    const double block = 0.16 + 0.11 * (each < 256.0 ? each / 256.0 : 1.0);
+    const double waves = double(cdiv(int64_t(wide_tiles), dev->slots[wide_v]));
+    double wide = waves * (blocks * block + 4.0);
+    if (split_pays(int64_t(wide_tiles), int64_t(blocks), dev->slots[wide_v]))
+        wide = wide_tiles / dev->slots[wide_v] * blocks * block + 20.0;
+    return few < wide ? few_v : wide_v;
 }
 
-size_t grouped_bytes(int mode, int64_t groups, int64_t rows, const RaggedDevice *dev)
+// Tiles of a forward or data-gradient launch, at most (a group's last tile may be a part of one).
+int64_t most_tiles(const RaggedVariant &var, int64_t groups, int64_t rows, int64_t pdim)
+{
+    return cdiv(pdim, 128 * var.cg) * (rows / var.qcap + (groups < rows ? groups : rows));
+}
+
+// Whether tiles are split over K: always for few rows, where every worker then reads the same number of weights; for
+// more rows only where it leaves fewer workers idle for long (a partial tile is 256 KB there, and tiles of one group
+// have to be worked on together to share its weights).
+bool split_tiles(int variant, int64_t most, int64_t kdim, const RaggedDevice *dev)
+{
+    return kRagged[variant].cg == 1 || split_pays(most, cdiv(kdim, kRagBlockK), dev->slots[variant]);
+}
+
+size_t grouped_bytes(int mode, int64_t groups, int64_t rows, int64_t pdim, int64_t kdim, const RaggedDevice *dev)
 {
     if (mode == kTN) return maps_bytes(groups);
-    const int v = grouped_variant(mode, groups, rows);
-    return few_rows(groups, rows) ? split_bytes(kRagged[v], dev->slots[v]) : 0;
+    const int v = grouped_variant(mode, groups, rows, pdim, kdim, dev);
+    return split_tiles(v, most_tiles(kRagged[v], groups, rows, pdim), kdim, dev) ? split_bytes(kRagged[v], dev->slots[v]) : 0;
 }
 
 gemm_status_t grouped(int mode, gemm_dtype_t dtype, gemm_dtype_t out_type, int64_t groups, int64_t rows, int64_t n, int64_t k,
@@ -357,9 +385,9 @@ gemm_status_t grouped(int mode, gemm_dtype_t dtype, gemm_dtype_t out_type, int64
     RaggedDevice *dev = nullptr;
     st = ragged_device(&dev);
     if (st != GEMM_OK) return st;
-    const int variant = grouped_variant(mode, groups, rows);
+    const int variant = grouped_variant(mode, groups, rows, pdim, kdim, dev);
     const RaggedVariant &var = kRagged[variant];
-    const size_t need = grouped_bytes(mode, groups, rows, dev);
+    const size_t need = grouped_bytes(mode, groups, rows, pdim, kdim, dev);
     if (ws != nullptr || ws_bytes != 0) {
         if (ws == nullptr || ws_bytes < need) return GEMM_ERR_WORKSPACE;
         if (reinterpret_cast<uintptr_t>(ws) & 255u) return GEMM_ERR_ALIGNMENT;
@@ -390,7 +418,7 @@ gemm_status_t grouped(int mode, gemm_dtype_t dtype, gemm_dtype_t out_type, int64
     p.wait_limit = wait_limit ? wait_limit : wait_limit_for(p.k_blocks);
     int64_t most;  // tiles, at most
     if (mode == kTN) most = int64_t(p.tiles_p) * p.tiles_q * (groups < rows ? groups : rows);
-    else most = int64_t(p.tiles_p) * (rows / var.qcap + (groups < rows ? groups : rows));
+    else most = most_tiles(var, groups, rows, pdim);
     if (most >= kSizeLimit) return GEMM_ERR_UNSUPPORTED_SHAPE;
     if (mode == kTN) {
         st = encode_stack(&p.tm_p, first, dtype, 1, rows, n, 64, 64);
@@ -402,7 +430,7 @@ gemm_status_t grouped(int mode, gemm_dtype_t dtype, gemm_dtype_t out_type, int64
         st = encode_stack(&p.tm_p, second, dtype, groups, n, k, 64, mode == kNT ? 128 : 64);
         if (st == GEMM_OK && mode == kNN) st = encode_pairs(&p.tm_p2, second, dtype, groups, n, k, &p.p_groups);
         if (st == GEMM_OK) st = encode_rows(p.tm_q, first, dtype, rows, kdim, var.qbox);
-        if (ws && few_rows(groups, rows) && most * p.k_blocks < kIterLimit) {
+        if (ws && split_tiles(variant, most, kdim, dev) && most * p.k_blocks < kIterLimit) {
             use_split(&p, var, dev->slots[variant], ws);
             most *= p.k_blocks;
         }
@@ -431,14 +459,26 @@ gemm_status_t grouped(int mode, gemm_dtype_t dtype, gemm_dtype_t out_type, int64
 
 // ------------------------------------------------------------- adapters
 
-// Rows up to which the adapters run beside the projection without tensor cores, one row tile of a single CTA.
-constexpr int64_t kLoraFewRows = 64;
-constexpr int64_t kLoraURows = 64;  // rows of a tile of the product that computes u for more rows
+constexpr int64_t kLoraURows = 64;  // rows of a tile of the product that computes u
 
-// How the work and the workspace are laid out.  Few rows: u and delta in fp32.  More: counts and lists
+// Whether the adapters run beside the projection without tensor cores, row by row.  That reads every row's a and b (from
+// L2, mostly) at about 5 TB/s; on the tensor cores each row tile takes a K block per adapter in it, at most 1.6 us of a
+// worker's time each, after some 15 us of launches that depend on one another.  1024 rows, 64 adapters of rank 16,
+// 8192 x 4096: 131 us beside, 300 on the tensor cores; 512 rows, 16 adapters of rank 64, 4096 x 4096: 130 and 73.
+bool lora_beside(const RaggedDevice *dev, int64_t rows, int64_t n, int64_t k, int64_t rank, int64_t adapters)
+{
+    if (rows <= kRagged[kVNtFew].qcap) return true;
+    const RaggedVariant &y = kRagged[kVLoraY];
+    const double alone = 2.0 * double(rows) * double(rank) * double(n + k) / 5e6;  // us
+    const double waves = double(cdiv(n, 128 * y.cg)) * double(cdiv(rows, y.qcap)) / dev->slots[kVLoraY];
+    const double blocks = double(adapters < y.qcap ? adapters : y.qcap) * double(cdiv(rank, kRagBlockK));
+    return alone < 15.0 + (waves < 1.0 ? 1.0 : waves) * blocks * 1.6;
+}
+
+// How the work and the workspace are laid out.  Beside: u and delta in fp32.  Otherwise: counts and lists
 // of the adapters per row tile (of y's product and of u's), and u; rows beyond what the kernels' table holds go in passes.
 struct LoraPlan {
-    bool few;
+    bool beside;
     int variant_y;
     int64_t per, tiles;    // y's row tiles, of one pass
     int64_t tiles_u;
@@ -446,12 +486,12 @@ struct LoraPlan {
     size_t counts, list, counts_u, list_u, u, delta, split, total;  // offsets
 };
 
-LoraPlan lora_plan(const RaggedDevice *dev, int64_t rows, int64_t n, int64_t rank)
+LoraPlan lora_plan(const RaggedDevice *dev, int64_t rows, int64_t n, int64_t k, int64_t rank, int64_t adapters)
 {
     LoraPlan l;
     memset(&l, 0, sizeof(l));
-    l.few = rows <= kLoraFewRows;
-    l.variant_y = l.few ? kVNtFew : kVLoraY;
+    l.beside = lora_beside(dev, rows, n, k, rank, adapters);
+    l.variant_y = l.beside ? grouped_variant(kNT, 1, rows, n, k, dev) : kVLoraY;
     const RaggedVariant &y = kRagged[l.variant_y];
     size_t at = 0;
     auto take = [&](size_t bytes) {
@@ -459,11 +499,12 @@ LoraPlan lora_plan(const RaggedDevice *dev, int64_t rows, int64_t n, int64_t ran
         at += size_t(round_up(int64_t(bytes), 256));
         return was;
     };
-    if (l.few) {
+    if (l.beside) {
         l.pass_rows = rows;
         l.u = take(size_t(rows) * size_t(rank) * 4u);
         l.delta = take(size_t(rows) * size_t(n) * 4u);
-        l.split = take(split_bytes(y, dev->slots[l.variant_y]));
+        const bool split = split_tiles(l.variant_y, most_tiles(y, 1, rows, n), k, dev);
+        l.split = take(split ? split_bytes(y, dev->slots[l.variant_y]) : 0);
         l.total = at;
         return l;
     }
@@ -500,7 +541,7 @@ gemm_status_t gemm_grouped_workspace_size(int64_t groups, int64_t rows, int64_t 
     if (st != GEMM_OK) return st;
     *bytes = 0;
     for (int mode : {int(kNT), int(kNN), int(kTN)}) {
-        const size_t need = grouped_bytes(mode, groups, rows, dev);
+        const size_t need = grouped_bytes(mode, groups, rows, mode == kNN ? k : n, mode == kNN ? n : k, dev);
         if (need > *bytes) *bytes = need;
     }
     return GEMM_OK;
@@ -546,7 +587,7 @@ gemm_status_t gemm_lora_workspace_size(int64_t rows, int64_t n, int64_t k, int64
     RaggedDevice *dev = nullptr;
     st = ragged_device(&dev);
     if (st != GEMM_OK) return st;
-    *bytes = rows ? lora_plan(dev, rows, n, rank).total : 0;
+    *bytes = rows ? lora_plan(dev, rows, n, k, rank, adapters).total : 0;
     return GEMM_OK;
 }
 
@@ -573,7 +614,7 @@ gemm_status_t gemm_lora_nt(gemm_dtype_t dtype, int64_t rows, int64_t n, int64_t 
     RaggedDevice *dev = nullptr;
     st = ragged_device(&dev);
     if (st != GEMM_OK) return st;
-    const LoraPlan l = lora_plan(dev, rows, n, rank);
+    const LoraPlan l = lora_plan(dev, rows, n, k, rank, adapters);
     if (workspace == nullptr || ws_bytes < l.total) return GEMM_ERR_WORKSPACE;
     if (reinterpret_cast<uintptr_t>(workspace) & 255u) return GEMM_ERR_ALIGNMENT;
     if (k == 0) {
@@ -584,7 +625,7 @@ gemm_status_t gemm_lora_nt(gemm_dtype_t dtype, int64_t rows, int64_t n, int64_t 
         return GEMM_OK;
     }
     char *ws = static_cast<char *>(workspace);
-    if (l.few) {
+    if (l.beside) {
         RaggedParams p;
         memset(&p, 0, sizeof(p));
         p.groups = 1;
@@ -636,8 +677,9 @@ gemm_status_t gemm_lora_nt(gemm_dtype_t dtype, int64_t rows, int64_t n, int64_t 
             p.ids = ids;
             p.adapters = f.adapters;
         }
-        int64_t most = p.tiles_p;
-        if (most * p.k_blocks < kIterLimit) {
+        int64_t most = most_tiles(vy, 1, rows, n);
+        if (most >= kSizeLimit) return GEMM_ERR_UNSUPPORTED_SHAPE;
+        if (split_tiles(l.variant_y, most, k, dev) && most * p.k_blocks < kIterLimit) {
             use_split(&p, vy, dev->slots[l.variant_y], ws + l.split);
             most *= p.k_blocks;
         }
@@ -690,29 +732,27 @@ gemm_status_t gemm_lora_nt(gemm_dtype_t dtype, int64_t rows, int64_t n, int64_t 
         st = encode_rows(p.tm_q, xr, dtype, r, k, vy.qbox);
         if (st != GEMM_OK) return st;
         {
-            struct Side {
-                int64_t per, tiles;
-                size_t counts, list;
-            } sides[2] = {{l.per, tiles, l.counts, l.list}, {kLoraURows, cdiv(r, kLoraURows), l.counts_u, l.list_u}};
-            for (const Side &side : sides) {
-                LoraListParams lp;
-                lp.ids = idr;
-                lp.rows = uint32_t(r);
-                lp.per = uint32_t(side.per);
-                lp.adapters = u.adapters;
-                lp.counts = reinterpret_cast<int32_t *>(ws + side.counts);
-                lp.list = reinterpret_cast<int32_t *>(ws + side.list);
-                void *args[1] = {&lp};
-                if (!adapted && &side == &sides[1]) break;
-                st = launch(reinterpret_cast<const void *>(&lora_list_kernel), dim3(unsigned(side.tiles), 1, 1), 256, 0, 1, args, s);
-                if (st != GEMM_OK) return st;
-            }
+            const int64_t tiles_u = adapted ? cdiv(r, kLoraURows) : 0;
+            LoraListParams lp;
+            lp.ids = idr;
+            lp.rows = uint32_t(r);
+            lp.adapters = u.adapters;
+            lp.tiles = uint32_t(tiles);
+            lp.per[0] = uint32_t(l.per);
+            lp.per[1] = uint32_t(kLoraURows);
+            lp.counts[0] = reinterpret_cast<int32_t *>(ws + l.counts);
+            lp.counts[1] = reinterpret_cast<int32_t *>(ws + l.counts_u);
+            lp.list[0] = reinterpret_cast<int32_t *>(ws + l.list);
+            lp.list[1] = reinterpret_cast<int32_t *>(ws + l.list_u);
+            void *args[1] = {&lp};
+            st = launch(reinterpret_cast<const void *>(&lora_list_kernel), dim3(unsigned(tiles + tiles_u), 1, 1), 256, 0, 1, args, s);
+            if (st != GEMM_OK) return st;
             p.counts = reinterpret_cast<int32_t *>(ws + l.counts);
             p.list = reinterpret_cast<int32_t *>(ws + l.list);
             if (adapted) {
                 u.counts = reinterpret_cast<int32_t *>(ws + l.counts_u);
                 u.list = reinterpret_cast<int32_t *>(ws + l.list_u);
-                u.groups = uint32_t(sides[1].tiles);
+                u.groups = uint32_t(tiles_u);
                 u.rows = uint32_t(r);
                 u.ids = idr;
                 st = encode_rows(u.tm_q, xr, dtype, r, k, vu.qbox);

@@ -186,7 +186,7 @@ struct RaggedSeg {
 
 // The order of a kLoraY tile's K blocks: the adapter blocks are spread evenly between the projection's, so that the
 // helper prepares one while the tensor cores work on the others, and every run of a split tile has its share
-// (64 rows with 64 adapters of rank 16: 43.8 us with the adapter blocks last, XX spread).  Block v is an adapter
+// (64 rows with 64 adapters of rank 16, on single CTAs: 43.8 us with the adapter blocks last, 36.2 spread).  Block v is an adapter
 // block where floor(v extra / kb) steps.
 struct RaggedMix {
     uint32_t kb, extra, left, e, m;  // left = v extra mod kb; e and m: adapter and projection blocks before v
@@ -1370,10 +1370,12 @@ __global__ void __launch_bounds__(128) lora_expand_kernel(const __grid_constant_
 
 // The adapters present in each tile of `per` rows (per <= 256), in order of first appearance: one block per
 // tile.  Rows with an id outside [0, adapters) have none.
+// Two cuttings of the same rows at once: `tiles` blocks for the first, the rest for the second.
 struct LoraListParams {
     const int32_t *ids;
-    uint32_t rows, per, adapters;
-    int32_t *counts, *list;
+    uint32_t rows, adapters, tiles;
+    uint32_t per[2];
+    int32_t *counts[2], *list[2];
 };
 
 __global__ void __launch_bounds__(256) lora_list_kernel(const __grid_constant__ LoraListParams p)
@@ -1381,8 +1383,9 @@ __global__ void __launch_bounds__(256) lora_list_kernel(const __grid_constant__ 
     __shared__ __align__(16) int32_t s_id[256];
     __shared__ uint32_t s_warp[8];
     ptx::griddep_wait();
-    const uint32_t t = threadIdx.x, row = blockIdx.x * p.per + t;
-    int32_t id = (p.adapters != 0u && t < p.per && row < p.rows) ? p.ids[row] : -1;
+    const uint32_t cut = blockIdx.x < p.tiles ? 0u : 1u, tile = blockIdx.x - cut * p.tiles, per = p.per[cut];
+    const uint32_t t = threadIdx.x, row = tile * per + t;
+    int32_t id = (p.adapters != 0u && t < per && row < p.rows) ? p.ids[row] : -1;
     if (uint32_t(id) >= p.adapters) id = -1;
     s_id[t] = id;
     __syncthreads();
@@ -1400,8 +1403,8 @@ __global__ void __launch_bounds__(256) lora_list_kernel(const __grid_constant__ 
         if (w < (t >> 5)) at += s_warp[w];
         total += s_warp[w];
     }
-    if (first) p.list[size_t(blockIdx.x) * p.per + at] = id;
-    if (t == 0) p.counts[blockIdx.x] = int32_t(total);
+    if (first) p.list[cut][size_t(tile) * per + at] = id;
+    if (t == 0) p.counts[cut][tile] = int32_t(total);
     ptx::griddep_launch_dependents();
 }
 

@@ -93,8 +93,8 @@ gemm_status_t gemm_grouped_tn(gemm_dtype_t dtype, gemm_dtype_t out, int64_t grou
  * x [rows, k], w [n, k], a [adapters, rank, k], b [adapters, n, rank],
  * y [rows, n]; ids: rows int32 in any order, a row whose id is outside
  * [0, adapters) has no adapter; scale: adapters fp32, or NULL for 1.  The inner
- * product scale (x a^T) is rounded to the operands' type for more than 64 rows; the two products are
- * added in fp32 and rounded once.  What an adapter holds reaches the rows that
+ * product scale (x a^T) may be rounded to the operands' type (where many rows go
+ * through the tensor cores); the two products are added in fp32 and rounded once.  What an adapter holds reaches the rows that
  * have it and no others, infinities and NaN included (a product with an infinity
  * of b may come out as NaN).  The workspace is required (gemm_lora_workspace_size on the current
  * device; GEMM_ERR_WORKSPACE).
