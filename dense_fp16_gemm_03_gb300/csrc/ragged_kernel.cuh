@@ -23,11 +23,14 @@
 // past a group's end (the rows there are finite work thrown away) but never
 // write there.
 //
-// Roles (192 threads, 320 with helpers; one CTA or a CTA pair per tile):
+// Roles (one CTA or a CTA pair per tile):
 //   warp 0      TMA producer into a STAGES-deep ring of 128-byte-swizzled stages
 //   warp 1      tensor memory and the MMA issuer (of the pair's first CTA)
-//   warps 2..5  epilogue, on one of two accumulators while the other fills
-//   warps 6..9  helper: kTN without maps zeroes the rows past a group's end in its last K
+//   warps 2..   epilogue, on one of two accumulators while the other fills: four warps,
+//               or eight that share the columns of 256-row tiles (with short
+//               contractions the tile's end is the longer part: 24 groups of 16121
+//               rows in all, 2024 x 136, took 34 us with four)
+//   the last 4  helper, where the mode has one: kTN without maps zeroes the rows past a group's end in its last K
 //               block (both operands: a zero times an infinity of the next group
 //               would be NaN); kLoraY builds the masked u operand, and for the same
 //               reason takes infinities and NaN out of the adapter's b and has the
@@ -66,7 +69,6 @@ namespace gemm_f16 {
 
 constexpr int kRagBlockK = 64;       // 16-bit elements per 128-byte swizzled row
 constexpr int kRagMaxGroups = 1024;  // entries of the shared-memory group table
-constexpr int kRagEpiWarps = 4;
 constexpr int kRagHelpers = 128;     // threads of the helper warps: one for each row of a stage's M side
 constexpr int kRagMaxSmem = 232448;  // 227 KB opt-in dynamic shared memory per CTA
 
@@ -134,7 +136,12 @@ struct RaggedCfg {
     static constexpr bool kPMn = (MODE == kNN || MODE == kTN);  // M-side operand MN-major
     static constexpr bool kQMn = (MODE == kTN);                 // N-side operand MN-major
     static constexpr bool kHelper = (MODE == kTN || MODE == kLoraY);
-    static constexpr int kThreads = 192 + (kHelper ? kRagHelpers : 0);
+    // (kTN: eight warps' boxes of 128 bytes a row do not fit; of 64 bytes, or shared by two warps, they took 481 and
+    // 452 us where four warps take 445 for 16384 rows, 32 groups, 4096 x 4096)
+    static constexpr int kEpiSets = (QCAP == 256 && MODE != kTN) ? 2 : 1;
+    static constexpr int kEpiWarps = 4 * kEpiSets;
+    static constexpr int kFirstHelper = 2 + kEpiWarps;          // warp
+    static constexpr int kThreads = 32 * kFirstHelper + (kHelper ? kRagHelpers : 0);
     static constexpr int kQCta = QCAP / CG;                     // N-side extent in one CTA's stage
     // rows of a whole N-side box; a tile takes at most two boxes (halves and quarters) and at most a quarter's
     // rows too many, because every further box in a K block costs the producer more than the rows do
@@ -146,7 +153,7 @@ struct RaggedCfg {
     static constexpr int kOffQ = STAGES * kPBytes;
     static constexpr int kOffStore = kOffQ + STAGES * kQBytes;  // per epilogue warp
     static constexpr int kStoreBytes = (MODE == kTN) ? 4096 : 2048;
-    static constexpr int kOffTabRow = kOffStore + kRagEpiWarps * kStoreBytes;
+    static constexpr int kOffTabRow = kOffStore + kEpiWarps * kStoreBytes;
     static constexpr int kOffTabTile = kOffTabRow + 4 * (kRagMaxGroups + 4);
     // full, empty, fixed, tail per stage; acc_full x2, acc_empty x2, drain, bad_free x2
     static constexpr int kNumBars = 4 * STAGES + 7;
@@ -572,8 +579,8 @@ __global__ void __launch_bounds__(RaggedCfg<MODE, CG, QCAP, STAGES>::kThreads, 1
         }
         for (int b = 0; b < 2; ++b) {
             ptx::mbar_init(bar_acc_full(b), 1);
-            ptx::mbar_init(bar_acc_empty(b), kRagEpiWarps * CG);
-            ptx::mbar_init(bar_bad_free(b), kRagEpiWarps);
+            ptx::mbar_init(bar_acc_empty(b), Cfg::kEpiWarps * CG);
+            ptx::mbar_init(bar_bad_free(b), Cfg::kEpiWarps);
         }
         ptx::mbar_init(bar_drain, 1);
         *abort_flag = 0u;
@@ -816,17 +823,18 @@ __global__ void __launch_bounds__(RaggedCfg<MODE, CG, QCAP, STAGES>::kThreads, 1
                 }
             }
         }
-    } else if (warp < 6u) {
+    } else if (warp < uint32_t(Cfg::kFirstHelper)) {
         // ------------------------------------------------ epilogue
         const uint32_t quarter = warp & 3u;  // tensor-memory lanes [32 quarter, +32)
-        const uint32_t buf = base + Cfg::kOffStore + quarter * Cfg::kStoreBytes;
+        const uint32_t set = (warp - 2u) >> 2;  // its 32-column chunks: set, set + kEpiSets, ...
+        const uint32_t buf = base + Cfg::kOffStore + (warp - 2u) * Cfg::kStoreBytes;
         const bool bf16 = p.bf16 != 0u;
         const uint32_t esize = (MODE == kTN && p.out32) ? 4u : 2u;
 
         // what no tile covers: rows in no group, and the gradients of groups without rows
         {
-            const uint64_t first = uint64_t(blockIdx.x) * 128u + (threadIdx.x - 64u);
-            const uint64_t stride = uint64_t(gridDim.x) * 128u;
+            const uint64_t first = uint64_t(blockIdx.x) * (32u * Cfg::kEpiWarps) + (threadIdx.x - 64u);
+            const uint64_t stride = uint64_t(gridDim.x) * (32u * Cfg::kEpiWarps);
             auto zero = [&](uint64_t from, uint64_t count) {  // 16-byte chunks
                 uint4 *dst = static_cast<uint4 *>(p.out) + from;
                 for (uint64_t i = first; i < count; i += stride) dst[i] = make_uint4(0u, 0u, 0u, 0u);
@@ -851,9 +859,9 @@ __global__ void __launch_bounds__(RaggedCfg<MODE, CG, QCAP, STAGES>::kThreads, 1
         walk.template each<false>([&](const RaggedSeg &s) {
             const bool ok = ragged_wait<CG>(bar_acc_full(acc), acc_phase, p, abort_flag, kRagErrAccFull);
             const bool split = MODE != kTN && p.sk != 0u && (s.lo != 0u || s.hi != s.kb);
-            // the four warps meet at named barriers below when the tile is split: stop together
+            // the warps meet at named barriers below when the tile is split: stop together
             if (MODE != kTN && p.sk) {
-                if (!ptx::named_barrier_and(1, 32 * kRagEpiWarps, ok)) return false;
+                if (!ptx::named_barrier_and(1, 32 * Cfg::kEpiWarps, ok)) return false;
             } else if (!__all_sync(0xffffffffu, ok)) {
                 return false;
             }
@@ -909,7 +917,7 @@ __global__ void __launch_bounds__(RaggedCfg<MODE, CG, QCAP, STAGES>::kThreads, 1
                 // ---- publish: the worker with the tile's last K block adds this partial
                 if (live) {
                     float *slot = p.partials + size_t(blockIdx.x) * kSlot + piece;
-                    for (uint32_t c = 0; c < chunks; ++c) {
+                    for (uint32_t c = set; c < chunks; c += Cfg::kEpiSets) {
                         uint32_t r[32];
                         ptx::tmem_ld_32x32b_x32_wait(t_col + 32u * c, r);
                         if (MODE == kLoraY) spoil(c, r);
@@ -923,7 +931,7 @@ __global__ void __launch_bounds__(RaggedCfg<MODE, CG, QCAP, STAGES>::kThreads, 1
                 }
                 release();
                 __threadfence();
-                ptx::named_barrier_sync(1, 32 * kRagEpiWarps);
+                ptx::named_barrier_sync(1, 32 * Cfg::kEpiWarps);
                 if (threadIdx.x == 64u) ptx::st_release_gpu_u64(p.flags + blockIdx.x, p.stamp);
                 return true;
             }
@@ -947,7 +955,7 @@ __global__ void __launch_bounds__(RaggedCfg<MODE, CG, QCAP, STAGES>::kThreads, 1
                     }
                     __syncwarp();
                 }
-                ptx::named_barrier_sync(1, 32 * kRagEpiWarps);
+                ptx::named_barrier_sync(1, 32 * Cfg::kEpiWarps);
             }
             // 32 columns of the finished tile: the accumulator plus the other workers' partials, lowest first,
             // two workers' loads in flight
@@ -1029,7 +1037,7 @@ __global__ void __launch_bounds__(RaggedCfg<MODE, CG, QCAP, STAGES>::kThreads, 1
                     const float mul = (MODE == kLoraU && p.scale) ? p.scale[s.row0] : 1.0f;
                     char *out = static_cast<char *>(p.out);
                     const uint32_t col = prow + 4u * (lane & 7u);
-                    for (uint32_t c = 0; c < chunks; ++c) {
+                    for (uint32_t c = set; c < chunks; c += Cfg::kEpiSets) {
                         uint32_t r[32];
                         float d[MODE == kNT ? 32 : 1];
                         if constexpr (MODE == kNT)
@@ -1073,7 +1081,7 @@ __global__ void __launch_bounds__(RaggedCfg<MODE, CG, QCAP, STAGES>::kThreads, 1
     } else if constexpr (Cfg::kHelper) {
         // ------------------------------------------------ helper
         // Four warps that share a stage's rows and never wait for each other: `fixed` counts them all.
-        const uint32_t tid = threadIdx.x - 192u;
+        const uint32_t tid = threadIdx.x - 32u * uint32_t(Cfg::kFirstHelper);
         const uint32_t part = tid >> 5;
         uint32_t fills = 0, tail_uses = 0, adapted = 0;
         auto wait_tail = [&](uint32_t stage) {
