@@ -487,11 +487,11 @@ struct LoraPlan {
     size_t counts, list, counts_u, list_u, u, delta, split, total;  // offsets
 };
 
-LoraPlan lora_plan(const RaggedDevice *dev, int64_t rows, int64_t n, int64_t k, int64_t rank, int64_t adapters)
+LoraPlan lora_layout(const RaggedDevice *dev, int64_t rows, int64_t n, int64_t k, int64_t rank, bool beside)
 {
     LoraPlan l;
     memset(&l, 0, sizeof(l));
-    l.beside = lora_beside(dev, rows, n, k, rank, adapters);
+    l.beside = beside;
     l.variant_y = l.beside ? grouped_variant(kNT, 1, rows, n, k, dev) : kVLoraY;
     const RaggedVariant &y = kRagged[l.variant_y];
     size_t at = 0;
@@ -527,6 +527,39 @@ LoraPlan lora_plan(const RaggedDevice *dev, int64_t rows, int64_t n, int64_t k, 
     return l;
 }
 
+LoraPlan lora_plan(const RaggedDevice *dev, int64_t rows, int64_t n, int64_t k, int64_t rank, int64_t adapters)
+{
+    return lora_layout(dev, rows, n, k, rank, lora_beside(dev, rows, n, k, rank, adapters));
+}
+
+// Bytes that serve any number of rows up to this one: the layout of the most rows that run beside the projection, that of
+// all rows on the tensor cores, and that of the one row tile that is split.
+size_t lora_bytes(const RaggedDevice *dev, int64_t rows, int64_t n, int64_t k, int64_t rank, int64_t adapters)
+{
+    size_t most = lora_plan(dev, rows, n, k, rank, adapters).total;
+    const int64_t tile = kRagged[kVLoraY].qcap;
+    if (rows > kRagged[kVNtFew].qcap) {
+        const size_t one = lora_layout(dev, rows < tile ? rows : tile, n, k, rank, false).total;
+        if (one > most) most = one;
+    }
+    // the limit of lora_beside is the same for all rows of a tile: the largest such row number of each tile, from the top
+    for (int64_t top = rows; top > 0; top = (top - 1) / tile * tile) {
+        const int64_t low = (top - 1) / tile * tile;
+        int64_t lo = low, hi = top;  // beside holds up to lo (or nowhere in this tile), not from hi + 1 on
+        while (lo < hi) {
+            const int64_t mid = lo + (hi - lo + 1) / 2;
+            if (lora_beside(dev, mid, n, k, rank, adapters)) lo = mid;
+            else hi = mid - 1;
+        }
+        if (lo > low) {
+            const size_t beside = lora_layout(dev, lo, n, k, rank, true).total;
+            if (beside > most) most = beside;
+            break;
+        }
+    }
+    return most;
+}
+
 }  // namespace
 
 extern "C" {
@@ -540,11 +573,13 @@ gemm_status_t gemm_grouped_workspace_size(int64_t groups, int64_t rows, int64_t 
     RaggedDevice *dev = nullptr;
     st = ragged_device(&dev);
     if (st != GEMM_OK) return st;
-    *bytes = 0;
-    for (int mode : {int(kNT), int(kNN), int(kTN)}) {
-        const size_t need = grouped_bytes(mode, groups, rows, mode == kNN ? k : n, mode == kNN ? n : k, dev);
-        if (need > *bytes) *bytes = need;
-    }
+    // what any number of rows up to this one may need, so that a buffer for the most rows serves them all
+    *bytes = maps_bytes(groups);
+    const size_t few = split_bytes(kRagged[kVNtFew], dev->slots[kVNtFew]);
+    const size_t wide = split_bytes(kRagged[kVNtWide], dev->slots[kVNtWide]);
+    if (few > *bytes) *bytes = few;
+    if (rows > kRagged[kVNtFew].qcap && split_pays(1, cdiv(n > k ? n : k, kRagBlockK), dev->slots[kVNtWide]) && wide > *bytes)
+        *bytes = wide;
     return GEMM_OK;
 }
 
@@ -588,7 +623,7 @@ gemm_status_t gemm_lora_workspace_size(int64_t rows, int64_t n, int64_t k, int64
     RaggedDevice *dev = nullptr;
     st = ragged_device(&dev);
     if (st != GEMM_OK) return st;
-    *bytes = rows ? lora_plan(dev, rows, n, k, rank, adapters).total : 0;
+    *bytes = rows ? lora_bytes(dev, rows, n, k, rank, adapters) : 0;
     return GEMM_OK;
 }
 

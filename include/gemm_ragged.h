@@ -69,8 +69,8 @@ typedef enum gemm_dtype {
  * result, whatever they hold (infinities, NaN).
  *
  * gemm_grouped_workspace_size: bytes that serve any of the three calls of these
- * sizes on the current device (partial sums of split tiles, tensor maps of the
- * groups; it may be 0).  A workspace may be NULL/0 all the same: that costs time
+ * sizes, or of fewer rows, on the current device (partial sums of split tiles,
+ * tensor maps of the groups).  A workspace may be NULL/0 all the same: that costs time
  * where there are few rows, and in gemm_grouped_tn; one that is given but too
  * small is GEMM_ERR_WORKSPACE.
  */
@@ -96,8 +96,9 @@ gemm_status_t gemm_grouped_tn(gemm_dtype_t dtype, gemm_dtype_t out, int64_t grou
  * product scale (x a^T) may be rounded to the operands' type (where many rows go
  * through the tensor cores); the two products are added in fp32 and rounded once.  What an adapter holds reaches the rows that
  * have it and no others, infinities and NaN included (a product with an infinity
- * of b may come out as NaN).  The workspace is required (gemm_lora_workspace_size on the current
- * device; GEMM_ERR_WORKSPACE).
+ * of b may come out as NaN).  The workspace is
+ * required (GEMM_ERR_WORKSPACE); gemm_lora_workspace_size gives the bytes that
+ * serve these sizes, or fewer rows, on the current device.
  */
 gemm_status_t gemm_lora_workspace_size(int64_t rows, int64_t n, int64_t k, int64_t rank, int64_t adapters, size_t *bytes);
 gemm_status_t gemm_lora_nt(gemm_dtype_t dtype, int64_t rows, int64_t n, int64_t k, int64_t rank, int64_t adapters,
@@ -125,7 +126,7 @@ gemm_status_t gemm_lora_nt(gemm_dtype_t dtype, int64_t rows, int64_t n, int64_t 
  *   renorm:     dl[ids[j]] = w[j] (dw[j] - sum_i w[i] dw[i]), zero elsewhere
  *   otherwise:  dl[e] = p[e] (sum_j [e = ids[j]] dw[j] - sum_j w[j] dw[j])
  */
-gemm_status_t gemm_route_workspace_size(int64_t rows, int64_t experts, int64_t top, size_t *bytes);
+gemm_status_t gemm_route_workspace_size(int64_t rows, int64_t experts, int64_t top, size_t *bytes); /* or fewer rows */
 gemm_status_t gemm_route_topk(gemm_dtype_t dtype, int64_t rows, int64_t experts, int64_t top, int32_t renorm,
                               const void *logits, int32_t *ids, float *weights, int32_t *offsets, int32_t *order,
                               int32_t *position, void *workspace, size_t ws_bytes, gemm_stream_t stream);

@@ -85,6 +85,30 @@ def test_many_groups(op):
     check_exact(op, sizes, 24, 40, torch.float16, seed=3)
 
 
+@pytest.mark.parametrize("kind", sorted(KINDS))
+@pytest.mark.parametrize("n,k", [(520, 600), (264, 1032), (448, 128), (1000, 72)])
+def test_weight_gradient_of_many_ragged_groups(kind, n, k):
+    """More tiles than the workers take in two turns: every group's rows end in tensor maps of its own."""
+    rng = np.random.default_rng(n + k)
+    sizes = rng.integers(0, 150, size=90).tolist()
+    check_exact("tn", sizes, n, k, KINDS[kind], seed=n, extra=30)
+    check_exact("tn", sizes, n, k, KINDS[kind], seed=k, head=3, dtype=torch.float32)
+
+
+def test_own_maps_keep_other_groups_infinities_out():
+    rng = np.random.default_rng(14)
+    sizes = rng.integers(1, 70, size=100).tolist()
+    dy, x = grouped_operands("tn", rng, sizes, 264, 520, torch.bfloat16)
+    offsets = offsets_of(sizes)
+    ref = grouped_ref("tn", dy, x, offsets, 100)
+    ends = offsets.numpy()
+    for g in range(1, 100, 2):  # every second group holds infinities and NaN
+        dy[ends[g]:ends[g + 1]] = float("inf")
+        x[ends[g]:ends[g + 1], ::2] = float("nan")
+    got = grouped_run("tn", dy, x, offsets)
+    assert torch.equal(got[::2], ref[::2].bfloat16())
+
+
 @pytest.mark.parametrize("op", OPS)
 def test_split_over_k_and_workers(op):
     """Few tiles with a long contraction: with a workspace a tile's K blocks lie on many workers."""

@@ -63,6 +63,11 @@ def test_many_tiles_with_long_contractions(rows, n, k, rank):
     check(rows, n, k, rank, 20, np.arange(rows) * 3 // rows, torch.float16, seed=14)
 
 
+def test_more_rows_than_one_pass_takes():
+    """The row tiles of one pass fit a table; 70000 rows take two passes."""
+    check(70000, 64, 72, 8, 2, np.arange(70000) // 9000 % 3 - 1, torch.float16, seed=15)
+
+
 @pytest.mark.parametrize("rows", [1, 64, 200])
 def test_every_row_another_adapter(rows):
     check(rows, 136, 264, 16, rows, np.random.default_rng(1).permutation(rows), torch.float16, seed=3)
