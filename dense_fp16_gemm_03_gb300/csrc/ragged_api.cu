@@ -306,6 +306,8 @@ gemm_status_t launch_ragged(int variant, const RaggedDevice *dev, RaggedParams &
     int64_t workers = dev->slots[variant];
     if (most_units < workers) workers = most_units < 1 ? 1 : most_units;
     p.error_word = dev->error_word;
+    p.by[0] = make_fastdiv(uint32_t(kRagBand) * p.tiles_p);
+    for (int d = 1; d <= kRagBand; ++d) p.by[d] = make_fastdiv(uint32_t(d));
     void *args[1] = {&p};
     return launch(var.fn, dim3(unsigned(workers * var.cg), 1, 1), unsigned(var.threads), var.smem, var.cg, args, stream);
 }
@@ -411,7 +413,6 @@ gemm_status_t grouped(int mode, gemm_dtype_t dtype, gemm_dtype_t out_type, int64
     p.k_blocks = uint32_t(cdiv(kdim, kRagBlockK));
     p.tiles_p = uint32_t(cdiv(pdim, 128 * var.cg));
     p.tiles_q = uint32_t(mode == kTN ? cdiv(k, var.qcap) : 0);
-    p.band = 8;
     p.bf16 = dtype == GEMM_DTYPE_BF16;
     p.out32 = out_type == GEMM_DTYPE_F32;
     p.out = out;
@@ -671,7 +672,6 @@ gemm_status_t gemm_lora_nt(gemm_dtype_t dtype, int64_t rows, int64_t n, int64_t 
         p.k_blocks = uint32_t(cdiv(k, kRagBlockK));
         const RaggedVariant &vy = kRagged[l.variant_y];
         p.tiles_p = uint32_t(cdiv(n, 128 * vy.cg));
-        p.band = 8;
         p.bf16 = dtype == GEMM_DTYPE_BF16;
         p.out = y;
         p.skip_fill = ~0u;
@@ -727,7 +727,6 @@ gemm_status_t gemm_lora_nt(gemm_dtype_t dtype, int64_t rows, int64_t n, int64_t 
     memset(&u, 0, sizeof(u));
     u.kdim = uint32_t(k);
     u.k_blocks = uint32_t(cdiv(k, kRagBlockK));
-    u.band = 8;
     u.bf16 = dtype == GEMM_DTYPE_BF16;
     u.scale = scale;
     u.adapters = adapted ? uint32_t(adapters) : 0u;

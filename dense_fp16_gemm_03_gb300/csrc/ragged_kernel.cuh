@@ -64,10 +64,12 @@
 #include <stdint.h>
 
 #include "ragged_ptx.cuh"
+#include "sched.cuh"
 
 namespace gemm_f16 {
 
 constexpr int kRagBlockK = 64;       // 16-bit elements per 128-byte swizzled row
+constexpr int kRagBand = 8;          // N-side tiles walked together before the M side advances
 constexpr int kRagMaxGroups = 1024;  // entries of the shared-memory group table
 constexpr int kRagHelpers = 128;     // threads of the helper warps: one for each row of a stage's M side
 constexpr int kRagMaxSmem = 232448;  // 227 KB opt-in dynamic shared memory per CTA
@@ -106,7 +108,7 @@ struct RaggedParams {
     uint32_t tiles_p;        // tiles along the M side
     uint32_t tiles_q;        // kTN, kLoraY: tiles along the N side
     uint32_t per;            // kLoraU, kLoraY: rows of a row tile
-    uint32_t band;           // N-side tiles walked together before the M side advances
+    FastDiv by[kRagBand + 1];  // by[d] divides by d; by[0] by kRagBand * tiles_p
     uint32_t sk;             // 1: equal runs of K-block iterations
     uint32_t bf16;           // operand type: 0 fp16, 1 bf16
     uint32_t out32;          // kTN: 1 = fp32 output
@@ -285,7 +287,10 @@ struct RaggedWalk {
     uint32_t run, longer;      // sk: K-block iterations of a worker; the first `longer` workers have one more
     uint32_t tile_blocks;      // sk: K blocks of every tile
 
-    __device__ __forceinline__ void decode(uint32_t u, RaggedSeg &s) const
+    // A producer that is late with a tile's first load leaves the ring short for the rest of it, so the way from a tile's
+    // number to its place is kept short: the group is looked for from the last one on, and divisors are known.  `near` is
+    // the group of the tile before (any group at first).
+    __device__ __forceinline__ void decode(uint32_t u, RaggedSeg &s, uint32_t &near) const
     {
         constexpr uint32_t kStep = 16u * CG;
         s.tile = u;
@@ -300,12 +305,18 @@ struct RaggedWalk {
             s.extra = uint32_t(tab_row[qi]) * p.rank_blocks;
             s.kb = p.k_blocks + s.extra;
         } else {
-            uint32_t lo = 0, hi = p.groups;  // tab_tile[lo] <= u < tab_tile[hi]
-            while (hi - lo > 1u) {
-                const uint32_t mid = (lo + hi) >> 1;
-                if (tab_tile[mid] <= u) lo = mid;
-                else hi = mid;
+            uint32_t lo = near;  // the group with tab_tile[lo] <= u < tab_tile[lo + 1]
+            for (int i = 0; i < 3 && tab_tile[lo + 1] <= u; ++i) ++lo;
+            if (tab_tile[lo] > u || tab_tile[lo + 1] <= u) {
+                lo = 0;
+                uint32_t hi = p.groups;
+                while (hi - lo > 1u) {
+                    const uint32_t mid = (lo + hi) >> 1;
+                    if (tab_tile[mid] <= u) lo = mid;
+                    else hi = mid;
+                }
             }
+            near = lo;
             s.g = lo;
             const uint32_t local = u - tab_tile[lo];
             s.kb = p.k_blocks;
@@ -333,7 +344,8 @@ struct RaggedWalk {
                     s.qn = rows;
                     if (rows > uint32_t(QCAP)) {
                         const uint32_t tq = (rows + QCAP - 1u) / QCAP;
-                        const uint32_t each = ((rows + tq - 1u) / tq + kStep - 1u) / kStep * kStep;
+                        const uint32_t share = tq <= uint32_t(kRagBand) ? fast_div(p.by[tq], rows + tq - 1u) : (rows + tq - 1u) / tq;
+                        const uint32_t each = (share + kStep - 1u) / kStep * kStep;
                         raster(local, tq, pi, qi);
                         s.q0 = r0 + qi * each;
                         s.qn = min(each, r0 + rows - s.q0);
@@ -346,20 +358,17 @@ struct RaggedWalk {
         s.nq = (s.qn + kStep - 1u) / kStep * kStep;
     }
 
-    // tile `t` of a tiles_p x tq grid, walked in bands of `band` N-side tiles, N side fastest
+    // tile `t` of a tiles_p x tq grid, walked in bands of N-side tiles, N side fastest
     __device__ __forceinline__ void raster(uint32_t t, uint32_t tq, uint32_t &pi, uint32_t &qi) const
     {
-        if (tq <= p.band) {
-            pi = t / tq;
-            qi = t - pi * tq;
-            return;
+        uint32_t b = 0, w = tq;
+        if (tq > uint32_t(kRagBand)) {
+            b = fast_div(p.by[0], t);
+            t -= b * p.by[0].d;
+            w = min(uint32_t(kRagBand), tq - b * kRagBand);
         }
-        const uint32_t full = p.band * p.tiles_p;
-        const uint32_t b = t / full;
-        const uint32_t r = t - b * full;
-        const uint32_t w = min(p.band, tq - b * p.band);
-        pi = r / w;
-        qi = b * p.band + (r - pi * w);
+        pi = fast_div(p.by[w], t);
+        qi = b * kRagBand + (t - pi * w);
     }
 
     __device__ __forceinline__ void count_extra(RaggedSeg &s) const
@@ -396,9 +405,10 @@ struct RaggedWalk {
     __device__ __forceinline__ void each(F &&f) const
     {
         RaggedSeg s;
+        uint32_t near = 0;
         if (MODE == kTN || !p.sk) {
             for (uint32_t u = worker; u < total; u += workers) {
-                decode(u, s);
+                decode(u, s, near);
                 s.lo = 0;
                 s.hi = s.kb;
                 count_extra(s);
@@ -414,7 +424,7 @@ struct RaggedWalk {
         while (it > begin) {
             const uint32_t u = (it - 1u) / kb;
             const uint32_t start = u * kb;
-            decode(u, s);
+            decode(u, s, near);
             s.lo = begin > start ? begin - start : 0u;
             s.hi = it - start;
             const uint32_t lo = s.lo;
