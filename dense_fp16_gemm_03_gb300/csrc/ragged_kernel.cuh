@@ -20,38 +20,47 @@
 // Everything but kTN yields tiles with the output column on tensor-memory
 // lanes and the row on columns; the epilogue transposes 32 x 32 pieces through
 // shared memory and stores only rows of the tile's own group, so tiles may read
-// past a group's end (the rows there are finite work thrown away) but never
-// write there.
+// past a group's end (what is computed for the rows there is thrown away) but
+// never write there.
+//
+// Two shapes.  A single CTA with 128 x 64 tiles in an eight-stage ring, for few
+// rows: bound by HBM (64 groups with 256 rows, 2048 x 4096: 149 us for 1.01 GB,
+// 6.8 TB/s).  A CTA pair with 256 x 256 tiles in a six-stage ring, for many:
+// bound by the tensor cores under the board's power limit (8192^3 in one group:
+// 1601 TFLOP/s sustained, beside 1592 of the dense 256 x 256 kernel), and with
+// groups of unlike size by what the narrower tiles load per multiply (32 groups
+// of 16384 rows in all, 4096 x 4096: 345 us with 512 rows each, 375 uneven).
 //
 // Roles (one CTA or a CTA pair per tile):
-//   warp 0      TMA producer into a STAGES-deep ring of 128-byte-swizzled stages
+//   warp 0      TMA producer into a ring of 128-byte-swizzled stages
 //   warp 1      tensor memory and the MMA issuer (of the pair's first CTA)
-//   warps 2..   epilogue, on one of two accumulators while the other fills: four warps,
-//               or eight that share the columns of 256-row tiles (with short
-//               contractions the tile's end is the longer part: 24 groups of 16121
-//               rows in all, 2024 x 136, took 34 us with four)
-//   the last 4  helper, where the mode has one: kTN without maps zeroes the rows past a group's end in its last K
-//               block (both operands: a zero times an infinity of the next group
-//               would be NaN); kLoraY builds the masked u operand, and for the same
-//               reason takes infinities and NaN out of the adapter's b and has the
-//               epilogue write NaN for them into that adapter's own rows alone.  A
-//               stage that the helper touches arrives on its CTA's `tail` barrier and is
-//               released to the MMA by the `fixed` barrier.
+//   warps 2..   epilogue, on one of two accumulators while the other fills: four
+//               warps, or eight that share the columns of 256-row tiles (with
+//               short contractions the tile's end is the longer part: 24 groups
+//               of 16121 rows in all, 2024 x 136, 34 us with four, 26.9 with eight)
+//   the last 4  helper, where the mode has one: kTN without maps zeroes the rows
+//               past a group's end in its last K block (both operands: a zero
+//               times an infinity of the next group would be NaN); kLoraY builds
+//               the masked u operand, and for the same reason takes infinities and
+//               NaN out of the adapter's b and has the epilogue write NaN for them
+//               into that adapter's own rows alone.  A stage that the helper touches
+//               arrives on its CTA's `tail` barrier and is released to the MMA by
+//               the `fixed` barrier.
 //
 // Group ends are read on the device (no host copy of them exists): every CTA
 // turns the offsets into a table of tile counts in shared memory, where all
 // roles look their tiles up.
 //
 // Walks: data-parallel (tile u on worker u mod workers), or with `sk` each
-// worker takes an equal run of all K-block iterations.  (Handing each next tile to
-// the worker that comes for it first, by a counter, was measured for groups of
-// unlike sizes: 32 groups of 16384 rows in all, 4096 x 4096, took 388 us against 380,
-// and one group 371 against 352: the number's way through the roles costs more
-// than the balance brings.)  A run that stops
-// inside a tile publishes its fp32 partial for the worker that holds the tile's
-// last K block.  Workers walk their run backwards, so they publish first and
-// wait last, and only ever for lower-numbered workers.  Sums are added in a fixed
-// order: results repeat bit for bit.
+// worker takes an equal run of all K-block iterations.  A run that stops inside a
+// tile publishes its fp32 partial for the worker that holds the tile's last K
+// block.  Workers walk their run backwards, so they publish first and wait last,
+// and only ever for lower-numbered workers, which start no later: launches that
+// share the GPU cannot hold each other up.  Sums are added in a fixed order:
+// results repeat bit for bit.  (Handing each next tile to the worker that comes
+// for it first, by a counter, was measured for groups of unlike sizes: 388 us
+// against 380 in the case above, and one group 371 against 352: the number's way
+// through the roles costs more than the balance brings.)
 //
 // Every wait is bounded as in gemm_kernel.cuh: past `wait_limit` cycles the
 // thread records an error code, raises the CTA's abort flag, and all roles
@@ -195,8 +204,9 @@ struct RaggedSeg {
 
 // The order of a kLoraY tile's K blocks: the adapter blocks are spread evenly between the projection's, so that the
 // helper prepares one while the tensor cores work on the others, and every run of a split tile has its share
-// (64 rows with 64 adapters of rank 16, on single CTAs: 43.8 us with the adapter blocks last, 36.2 spread).  Block v is an adapter
-// block where floor(v extra / kb) steps.
+// (64 rows with 64 adapters of rank 16, on single CTAs: 43.8 us with the adapter blocks last, 36.2 spread).  Block v
+// is an adapter block where floor(v extra / kb) steps.  Each costs up to 1.6 us, the latency of its load, the helper
+// and the release to the pair's first CTA, of which the ring holds three at a time.
 struct RaggedMix {
     uint32_t kb, extra, left, e, m;  // left = v extra mod kb; e and m: adapter and projection blocks before v
     __device__ __forceinline__ explicit RaggedMix(const RaggedSeg &s) : kb(s.kb), extra(s.extra)
@@ -1235,7 +1245,8 @@ __global__ void __launch_bounds__(RaggedCfg<MODE, CG, QCAP, STAGES>::kThreads, 1
 }
 
 // kTN: every group's tensor maps with the rows ending at the group's end, so that TMA fills the rest of its last K block
-// with zeros.  One block per group, one warp per map.
+// with zeros (32 uneven groups of 16384 rows in all, 4096 x 4096: 541 us with the helper zeroing each tile's last
+// block, 459 so).  One block per group, one warp per map; some 3 us in front of the product.
 struct RaggedMapsParams {
     CUtensorMap maps[4];
     const int32_t *offsets;
@@ -1265,7 +1276,9 @@ __global__ void __launch_bounds__(128) ragged_maps_kernel(const __grid_constant_
 
 // Adapters of few rows, without the tensor cores: with an adapter to nearly every row, all of the work is reading a
 // and b once, and each row sees its own adapter only.  u = scale x a^T and delta = u b^T stay in fp32.  Both kernels run
-// beside the projection, which starts at once and waits for delta in its epilogue.
+// beside the projection, which starts at once and waits for delta in its epilogue.  16 rows with 16 adapters of rank 16,
+// 8192 x 4096, take 23 us, as without adapters 21; 64 with 64 take 30 (as K blocks of the projection 36): there the two
+// kernels, 7 us each on an idle GPU, end after the projection's loads.
 struct LoraFewParams {
     const void *x, *a, *b;
     const int32_t *ids;
@@ -1386,9 +1399,9 @@ __global__ void __launch_bounds__(128) lora_expand_kernel(const __grid_constant_
     }
 }
 
-// The adapters present in each tile of `per` rows (per <= 256), in order of first appearance: one block per
-// tile.  Rows with an id outside [0, adapters) have none.
-// Two cuttings of the same rows at once: `tiles` blocks for the first, the rest for the second.
+// Lists for the tensor cores' form: the adapters present in each tile of `per` rows (per <= 256), in order of first
+// appearance.  Rows with an id outside [0, adapters) have none.  Two cuttings of the same rows at once: `tiles` blocks for
+// the first, the rest for the second.  Bound by latency, some 4 us.
 struct LoraListParams {
     const int32_t *ids;
     uint32_t rows, adapters, tiles;
