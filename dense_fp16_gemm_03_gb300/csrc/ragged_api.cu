@@ -58,11 +58,28 @@ const RaggedVariant kRagged[] = {
 };
 constexpr int kNumRagged = int(sizeof(kRagged) / sizeof(kRagged[0]));
 
+// The instances of the adapters' kernels whose lanes hold a rank's 16-byte pieces.
+const void *lora_rows_instance(int64_t rank)
+{
+    return rank <= 8    ? reinterpret_cast<const void *>(&lora_rows_kernel<1>)
+           : rank <= 16 ? reinterpret_cast<const void *>(&lora_rows_kernel<2>)
+                        : reinterpret_cast<const void *>(&lora_rows_kernel<4>);
+}
+
+const void *lora_expand_instance(int64_t rank)
+{
+    return rank <= 8    ? reinterpret_cast<const void *>(&lora_expand_kernel<1>)
+           : rank <= 16 ? reinterpret_cast<const void *>(&lora_expand_kernel<2>)
+           : rank <= 32 ? reinterpret_cast<const void *>(&lora_expand_kernel<4>)
+           : rank <= 64 ? reinterpret_cast<const void *>(&lora_expand_kernel<8>)
+                        : reinterpret_cast<const void *>(&lora_expand_kernel<16>);
+}
+
 const void *const kBeside[] = {
-    reinterpret_cast<const void *>(&lora_shrink_kernel),     reinterpret_cast<const void *>(&lora_expand_kernel<1>),
-    reinterpret_cast<const void *>(&lora_expand_kernel<2>),  reinterpret_cast<const void *>(&lora_expand_kernel<4>),
-    reinterpret_cast<const void *>(&lora_expand_kernel<8>),  reinterpret_cast<const void *>(&lora_expand_kernel<16>),
-    reinterpret_cast<const void *>(&lora_list_kernel),       reinterpret_cast<const void *>(&ragged_maps_kernel),
+    lora_rows_instance(8),    lora_rows_instance(16),   lora_rows_instance(32),
+    lora_expand_instance(8),  lora_expand_instance(16), lora_expand_instance(32),
+    lora_expand_instance(64), lora_expand_instance(128), reinterpret_cast<const void *>(&lora_shrink_kernel),
+    reinterpret_cast<const void *>(&lora_list_kernel), reinterpret_cast<const void *>(&ragged_maps_kernel),
 };
 
 struct RaggedDevice {
@@ -462,6 +479,8 @@ gemm_status_t grouped(int mode, gemm_dtype_t dtype, gemm_dtype_t out_type, int64
 // ------------------------------------------------------------- adapters
 
 constexpr int64_t kLoraURows = 64;  // rows of a tile of the product that computes u
+// Rows and rank up to which one kernel takes both of the adapters' steps beside the projection (measured at the kernel).
+constexpr int64_t kLoraRowsRows = 32, kLoraRowsRank = 32;
 
 // Whether the adapters run beside the projection without tensor cores, row by row.  That reads every row's a and b (from
 // L2, mostly) at about 5 TB/s; on the tensor cores each row tile takes a K block per adapter in it, at most 1.6 us of a
@@ -695,20 +714,22 @@ gemm_status_t gemm_lora_nt(gemm_dtype_t dtype, int64_t rows, int64_t n, int64_t 
             f.adapters = uint32_t(adapters);
             f.bf16 = p.bf16;
             void *args[1] = {&f};
-            // few enough blocks on an SM to leave room for the product's CTA beside them: with four and two, 64 rows with
-            // 64 adapters of rank 16, 8192 x 4096, take 29.1 us, with four and four 30.8, with one and two 33.5
-            const int64_t shrink = rows * (rank / 4), expand = cdiv(rows * cdiv(n, 128), 4);
-            const void *expand_fn = rank <= 8    ? reinterpret_cast<const void *>(&lora_expand_kernel<1>)
-                                    : rank <= 16 ? reinterpret_cast<const void *>(&lora_expand_kernel<2>)
-                                    : rank <= 32 ? reinterpret_cast<const void *>(&lora_expand_kernel<4>)
-                                    : rank <= 64 ? reinterpret_cast<const void *>(&lora_expand_kernel<8>)
-                                                 : reinterpret_cast<const void *>(&lora_expand_kernel<16>);
             const int64_t room = dev->num_sms;
-            st = launch(reinterpret_cast<const void *>(&lora_shrink_kernel),
-                        dim3(unsigned(shrink < 4 * room ? shrink : 4 * room), 1, 1), 128, 0, 1, args, s);
-            if (st != GEMM_OK) return st;
-            st = launch(expand_fn, dim3(unsigned(expand < 2 * room ? expand : 2 * room), 1, 1), 128, 0, 1, args, s);
-            if (st != GEMM_OK) return st;
+            if (rows <= kLoraRowsRows && rank <= kLoraRowsRank) {
+                st = launch(lora_rows_instance(rank), dim3(unsigned(rows * kLoraCluster), 1, 1), 128, 0, kLoraCluster,
+                            args, s);
+                if (st != GEMM_OK) return st;
+            } else {
+                // few enough blocks on an SM to leave room for the product's CTA beside them: with four and two, 64 rows
+                // with 64 adapters of rank 16, 8192 x 4096, take 29.1 us, with four and four 30.8, with one and two 33.5
+                const int64_t shrink = rows * (rank / 4), expand = cdiv(rows * cdiv(n, 128), 4);
+                st = launch(reinterpret_cast<const void *>(&lora_shrink_kernel),
+                            dim3(unsigned(shrink < 4 * room ? shrink : 4 * room), 1, 1), 128, 0, 1, args, s);
+                if (st != GEMM_OK) return st;
+                st = launch(lora_expand_instance(rank), dim3(unsigned(expand < 2 * room ? expand : 2 * room), 1, 1), 128,
+                            0, 1, args, s);
+                if (st != GEMM_OK) return st;
+            }
             p.delta = f.delta;
             p.ids = ids;
             p.adapters = f.adapters;

@@ -1274,11 +1274,16 @@ __global__ void __launch_bounds__(128) ragged_maps_kernel(const __grid_constant_
     ptx::griddep_launch_dependents();
 }
 
-// Adapters of few rows, without the tensor cores: with an adapter to nearly every row, all of the work is reading a
-// and b once, and each row sees its own adapter only.  u = scale x a^T and delta = u b^T stay in fp32.  Both kernels run
-// beside the projection, which starts at once and waits for delta in its epilogue.  16 rows with 16 adapters of rank 16,
-// 8192 x 4096, take 23 us, as without adapters 21; 64 with 64 take 30 (as K blocks of the projection 36): there the two
-// kernels, 7 us each on an idle GPU, end after the projection's loads.
+// Adapters without the tensor cores: with an adapter to nearly every row, all of the work is reading a and b once, and
+// each row sees its own adapter only.  u = scale x a^T and delta = u b^T stay in fp32.  They run beside the projection,
+// which starts at once and waits for delta in its epilogue.  16 rows with 16 adapters of rank 16, 8192 x 4096, take 22 us,
+// as without adapters 20; 64 with 64 take 30 (as K blocks of the projection 36): there the two kernels, 7 us each on an
+// idle GPU, end after the projection's loads.
+//
+// For a few rows of a low rank a cluster of eight CTAs takes a row through both steps and trades u through distributed
+// shared memory: one launch fewer, 2 to 4 us of the host's time, and the GPU's with it, then by the two kernels: 16 rows,
+// rank 16, 8192 x 4096, 21.7 us and 23.6; 32 rows 23.1 and 24.7; 1 row, 4096 x 4096, 14.4 and 13.9.  But 64 rows take 32.6
+// and 29.0, and rank 64 (16 rows, 11008 x 4096) 35.8 and 33.3: a row's work on eight SMs only.
 struct LoraFewParams {
     const void *x, *a, *b;
     const int32_t *ids;
@@ -1294,109 +1299,149 @@ __device__ __forceinline__ float2 ragged_unpack(uint32_t w, bool bf16)
     return __half22float2(*reinterpret_cast<const __half2 *>(&w));
 }
 
-// An item is a row and four of its u's: four warps share k, each lane multiplies 8 elements at a time.
+// Four of a row's u's by one block of 128 threads, which share k: each lane multiplies 8 elements at a time.  Thread
+// t < 4 returns number t (before the scale); s_sum is the block's.
+__device__ __forceinline__ float lora_dot4(const LoraFewParams &p, uint32_t row, int32_t id, uint32_t r0, float (&s_sum)[4][4])
+{
+    const uint32_t lane = threadIdx.x & 31u, warp = threadIdx.x >> 5;
+    const bool bf16 = p.bf16 != 0u;
+    const uint4 *x = reinterpret_cast<const uint4 *>(static_cast<const char *>(p.x) + size_t(row) * p.k * 2u);
+    const char *a = static_cast<const char *>(p.a) + (size_t(id) * p.rank + r0) * p.k * 2u;
+    float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+    for (uint32_t i = threadIdx.x; i < p.k / 8u; i += 128u) {
+        const uint4 xv = x[i];
+        uint4 av[4];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) av[r] = reinterpret_cast<const uint4 *>(a + size_t(r) * p.k * 2u)[i];
+        const uint32_t xw[4] = {xv.x, xv.y, xv.z, xv.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const float2 xf = ragged_unpack(xw[j], bf16);
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const uint32_t aw = j == 0 ? av[r].x : j == 1 ? av[r].y : j == 2 ? av[r].z : av[r].w;
+                const float2 af = ragged_unpack(aw, bf16);
+                sum[r] = fmaf(xf.x, af.x, sum[r]);
+                sum[r] = fmaf(xf.y, af.y, sum[r]);
+            }
+        }
+    }
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) sum[r] += __shfl_xor_sync(0xffffffffu, sum[r], d);
+    __syncthreads();  // the four before have been read
+    if (lane == 0)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) s_sum[warp][r] = sum[r];
+    __syncthreads();
+    const uint32_t r = threadIdx.x & 3u;
+    return (s_sum[0][r] + s_sum[1][r]) + (s_sum[2][r] + s_sum[3][r]);
+}
+
+// 128 columns of a row's delta by one warp.  LANES lanes share a row of b, 16 bytes each, with their part of u in
+// registers; eight rows' loads are in flight.  (One lane to a row of b read a line per lane and load.)
+template <int LANES>
+__device__ __forceinline__ void lora_columns(const LoraFewParams &p, uint32_t row, int32_t id, uint32_t col0, const float (&u)[8])
+{
+    const uint32_t lane = threadIdx.x & 31u, part = lane % LANES;
+    const bool bf16 = p.bf16 != 0u, live = 8u * part < p.rank;
+    constexpr uint32_t kRows = 32 / LANES;  // rows of b a warp reads at a time
+    constexpr uint32_t kFlight = 8;         // and such reads in flight
+    const char *b = static_cast<const char *>(p.b) + size_t(id) * p.n * p.rank * 2u + 16u * part;
+#pragma unroll 1
+    for (uint32_t i0 = 0; i0 < 128u; i0 += kFlight * kRows) {
+        uint4 v[kFlight];
+#pragma unroll
+        for (int i = 0; i < int(kFlight); ++i) {
+            const uint32_t col = col0 + i0 + uint32_t(i) * kRows + lane / LANES;
+            v[i] = (live && col < p.n && i0 + uint32_t(i) * kRows < 128u)
+                       ? *reinterpret_cast<const uint4 *>(b + size_t(col) * p.rank * 2u)
+                       : make_uint4(0u, 0u, 0u, 0u);
+        }
+#pragma unroll
+        for (int i = 0; i < int(kFlight); ++i) {
+            if (i0 + uint32_t(i) * kRows >= 128u) continue;
+            const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+            float sum = 0.0f;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float2 f = ragged_unpack(w[j], bf16);
+                sum = fmaf(f.x, u[2 * j], sum);
+                sum = fmaf(f.y, u[2 * j + 1], sum);
+            }
+#pragma unroll
+            for (int d = LANES / 2; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+            const uint32_t col = col0 + i0 + uint32_t(i) * kRows + lane / LANES;
+            if (part == 0u && col < p.n) p.delta[size_t(row) * p.n + col] = sum;
+        }
+    }
+}
+
+// An item, a block's, is a row and four of its u's.
 __global__ void __launch_bounds__(128) lora_shrink_kernel(const __grid_constant__ LoraFewParams p)
 {
     __shared__ float s_sum[4][4];
     ptx::griddep_wait();
     // (after the wait: what the next kernels read from before this one is complete as well)
     ptx::griddep_launch_dependents();
-    const uint32_t lane = threadIdx.x & 31u, warp = threadIdx.x >> 5;
-    const bool bf16 = p.bf16 != 0u;
     const uint32_t parts = p.rank / 4u;
     for (uint32_t item = blockIdx.x; item < p.rows * parts; item += gridDim.x) {
         const uint32_t row = item / parts, r0 = (item - row * parts) * 4u;
         const int32_t id = p.ids[row];
         if (uint32_t(id) >= p.adapters) continue;
-        const uint4 *x = reinterpret_cast<const uint4 *>(static_cast<const char *>(p.x) + size_t(row) * p.k * 2u);
-        const char *a = static_cast<const char *>(p.a) + (size_t(id) * p.rank + r0) * p.k * 2u;
-        float sum[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 4
-        for (uint32_t i = threadIdx.x; i < p.k / 8u; i += 128u) {
-            const uint4 xv = x[i];
-            uint4 av[4];
-#pragma unroll
-            for (int r = 0; r < 4; ++r) av[r] = reinterpret_cast<const uint4 *>(a + size_t(r) * p.k * 2u)[i];
-            const uint32_t xw[4] = {xv.x, xv.y, xv.z, xv.w};
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const float2 xf = ragged_unpack(xw[j], bf16);
-#pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const uint32_t aw = j == 0 ? av[r].x : j == 1 ? av[r].y : j == 2 ? av[r].z : av[r].w;
-                    const float2 af = ragged_unpack(aw, bf16);
-                    sum[r] = fmaf(xf.x, af.x, sum[r]);
-                    sum[r] = fmaf(xf.y, af.y, sum[r]);
-                }
-            }
-        }
-#pragma unroll
-        for (int r = 0; r < 4; ++r)
-#pragma unroll
-            for (int d = 16; d > 0; d >>= 1) sum[r] += __shfl_xor_sync(0xffffffffu, sum[r], d);
-        __syncthreads();  // the item before has been written
-        if (lane == 0)
-#pragma unroll
-            for (int r = 0; r < 4; ++r) s_sum[warp][r] = sum[r];
-        __syncthreads();
-        if (threadIdx.x < 4u) {
-            const uint32_t r = threadIdx.x;
-            const float mul = p.scale ? p.scale[id] : 1.0f;
-            p.u[size_t(row) * p.rank + r0 + r] = ((s_sum[0][r] + s_sum[1][r]) + (s_sum[2][r] + s_sum[3][r])) * mul;
-        }
+        const float v = lora_dot4(p, row, id, r0, s_sum) * (p.scale ? p.scale[id] : 1.0f);
+        if (threadIdx.x < 4u) p.u[size_t(row) * p.rank + r0 + threadIdx.x] = v;
     }
 }
 
-// An item, a warp's, is a row and 128 of its columns.  LANES lanes share a row of b, 16 bytes each, with their part of
-// u in registers.  (One lane to a row of b read a line per lane and load.)
+// An item, a warp's, is a row and 128 of its columns.
 template <int LANES>
 __global__ void __launch_bounds__(128) lora_expand_kernel(const __grid_constant__ LoraFewParams p)
 {
     // The product behind this kernel reads nothing of the kernel before this one; that one has waited for all before it.
     ptx::griddep_launch_dependents();
     ptx::griddep_wait();
-    const bool bf16 = p.bf16 != 0u;
-    const uint32_t lane = threadIdx.x & 31u, part = lane % LANES;
-    const uint32_t parts = (p.n + 127u) / 128u;
-    const bool live = 8u * part < p.rank;
-    constexpr uint32_t kRows = 32 / LANES;  // rows of b a warp reads at a time
-    constexpr uint32_t kFlight = 8;         // and such reads in flight
+    const uint32_t part = (threadIdx.x & 31u) % LANES, parts = (p.n + 127u) / 128u;
     for (uint32_t item = blockIdx.x * 4u + (threadIdx.x >> 5); item < p.rows * parts; item += gridDim.x * 4u) {
-        const uint32_t row = item / parts, col0 = (item - row * parts) * 128u;
+        const uint32_t row = item / parts;
         const int32_t id = p.ids[row];
         if (uint32_t(id) >= p.adapters) continue;
         float u[8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) u[j] = live ? p.u[size_t(row) * p.rank + 8u * part + j] : 0.0f;
-        const char *b = static_cast<const char *>(p.b) + size_t(id) * p.n * p.rank * 2u + 16u * part;
-#pragma unroll 1
-        for (uint32_t i0 = 0; i0 < 128u; i0 += kFlight * kRows) {
-            uint4 v[kFlight];
-#pragma unroll
-            for (int i = 0; i < int(kFlight); ++i) {
-                const uint32_t col = col0 + i0 + uint32_t(i) * kRows + lane / LANES;
-                v[i] = (live && col < p.n && i0 + uint32_t(i) * kRows < 128u)
-                           ? *reinterpret_cast<const uint4 *>(b + size_t(col) * p.rank * 2u)
-                           : make_uint4(0u, 0u, 0u, 0u);
-            }
-#pragma unroll
-            for (int i = 0; i < int(kFlight); ++i) {
-                if (i0 + uint32_t(i) * kRows >= 128u) continue;
-                const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
-                float sum = 0.0f;
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const float2 f = ragged_unpack(w[j], bf16);
-                    sum = fmaf(f.x, u[2 * j], sum);
-                    sum = fmaf(f.y, u[2 * j + 1], sum);
-                }
-#pragma unroll
-                for (int d = LANES / 2; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-                const uint32_t col = col0 + i0 + uint32_t(i) * kRows + lane / LANES;
-                if (part == 0u && col < p.n) p.delta[size_t(row) * p.n + col] = sum;
-            }
-        }
+        for (int j = 0; j < 8; ++j) u[j] = 8u * part < p.rank ? p.u[size_t(row) * p.rank + 8u * part + j] : 0.0f;
+        lora_columns<LANES>(p, row, id, (item - row * parts) * 128u, u);
     }
+}
+
+// Both steps of one row by a cluster.
+constexpr uint32_t kLoraCluster = 8;
+
+template <int LANES>
+__global__ void __launch_bounds__(128) lora_rows_kernel(const __grid_constant__ LoraFewParams p)
+{
+    __shared__ float s_sum[4][4];
+    __shared__ float s_u[32];
+    ptx::cluster_sync();  // every CTA of the cluster runs: its shared memory may be written
+    ptx::griddep_wait();
+    ptx::griddep_launch_dependents();  // (after the wait, as above)
+    const uint32_t part = (threadIdx.x & 31u) % LANES, rank = ptx::cluster_ctarank(), row = blockIdx.x / kLoraCluster;
+    const int32_t id = p.ids[row];
+    if (uint32_t(id) >= p.adapters) return;  // (the same for the whole cluster)
+    for (uint32_t r0 = 4u * rank; r0 < p.rank; r0 += 4u * kLoraCluster) {
+        const float v = lora_dot4(p, row, id, r0, s_sum) * (p.scale ? p.scale[id] : 1.0f);
+        if (threadIdx.x < 4u * kLoraCluster)  // four values to every CTA
+            ptx::st_shared_cluster_u32(ptx::map_to_rank(ptx::smem_addr(&s_u[r0 + (threadIdx.x & 3u)]), threadIdx.x >> 2),
+                                       __float_as_uint(v));
+    }
+    __syncwarp();
+    ptx::cluster_sync();
+    float u[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) u[j] = 8u * part < p.rank ? s_u[8u * part + j] : 0.0f;
+    for (uint32_t item = rank * 4u + (threadIdx.x >> 5); item < (p.n + 127u) / 128u; item += 4u * kLoraCluster)
+        lora_columns<LANES>(p, row, id, item * 128u, u);
 }
 
 // Lists for the tensor cores' form: the adapters present in each tile of `per` rows (per <= 256), in order of first

@@ -56,6 +56,13 @@ def test_requests_in_runs(kind, ends):
     check(ends[-1], 264, 328, 24, 4, ids, KINDS[kind], seed=len(ends))
 
 
+@pytest.mark.parametrize("rows", [16, 32, 33])
+@pytest.mark.parametrize("n,k,rank", [(1032, 2056, 8), (136, 1096, 24), (2200, 72, 32), (1032, 8, 40)])
+def test_few_rows_where_the_adapters_kernels_change(rows, n, k, rank):
+    rng = np.random.default_rng(rows * rank)
+    check(rows, n, k, rank, 40, rng.integers(-2, 42, size=rows), torch.bfloat16, seed=rows + rank)
+
+
 @pytest.mark.parametrize("rows,n,k,rank", [(64, 8200, 1096, 16), (30, 2056, 4104, 72), (2000, 4104, 648, 40)])
 def test_many_tiles_with_long_contractions(rows, n, k, rank):
     """Several tiles for every worker, and K blocks that go round the ring more than twice before the adapters'."""
