@@ -331,7 +331,8 @@ gemm_status_t launch_ragged(int variant, const RaggedDevice *dev, RaggedParams &
 
 // ------------------------------------------------------ grouped products
 
-// Whether fewer tiles than CTA pairs are worth splitting over K: the pairs left idle against 20 us of adding partials.
+// Whether fewer tiles than CTA pairs are worth splitting over K: what the idle pairs would save against the 16 to 20 us
+// that adding partials takes.
 bool split_pays(int64_t tiles, int64_t blocks, int slots)
 {
     return tiles < slots && 0.27 * double(blocks) * (1.0 - double(tiles) / slots) > 16.0;
