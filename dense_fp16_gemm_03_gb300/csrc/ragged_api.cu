@@ -331,34 +331,52 @@ gemm_status_t launch_ragged(int variant, const RaggedDevice *dev, RaggedParams &
 
 // ------------------------------------------------------ grouped products
 
-// Whether fewer tiles than CTA pairs are worth splitting over K: what the idle pairs would save against the 16 to 20 us
-// that adding partials takes.
-bool split_pays(int64_t tiles, int64_t blocks, int slots)
-{
-    return tiles < slots && 0.27 * double(blocks) * (1.0 - double(tiles) / slots) > 16.0;
-}
+constexpr int64_t kWideSplitBlocks = 16;  // K blocks below which splitting pairs' tiles never pays
 
-// Single CTAs with a 64-row N side, or CTA pairs with up to 256 rows: whichever an estimate of the time (us) has
-// ahead for groups of equal size.  A single CTA's K block brings 24 KB into its SM, all of which together take in about
-// 12 TB/s; a pair's K block takes 0.16 us of loads or, with all 256 rows, 0.27 of MMA, over whole waves of tiles or,
-// split, an even share and some 20 us of adding partials (128 KB for every CTA).  A tile's end costs about 2 us of a
-// single CTA and 4 of a pair (24 groups of 16121 rows in all, 2024 x 136: 64 us on single CTAs, 34 on pairs).
-int grouped_variant(int mode, int64_t groups, int64_t rows, int64_t pdim, int64_t kdim, const RaggedDevice *dev)
+// A forward or data-gradient launch: single CTAs with a 64-row N side, or CTA pairs with up to 256 rows, and whether
+// tiles are split over K (every worker then takes the same number of K blocks; the partial sums cost a join).
+struct RaggedChoice {
+    int variant;
+    bool split;
+};
+
+// Whichever of the four an estimate of the time has ahead for groups of equal size: the bytes at HBM's rate or whole
+// waves of tiles, split ones an even share, and each way's fixed time.  The constants (us) are fitted to 600 launches of
+// random sizes (1 to 64 groups, 1 to 30000 rows, n and k 128 to 6144; all four measured): on 549 others the choice is 1.5%
+// slower than the fastest on average, 20% when single CTAs always split and ran up to 64 rows a group
+// (16 rows in 36 groups, 1264 x 368: 6.6 us unsplit, 9.8 split; 12 rows in 2 groups, 728 x 4808: 18.8 and 10.7; 409 rows in
+// 50 groups, data gradient, 2968 x 5656: 419 split single CTAs, 253 pairs).  Splitting many tiles loses more than the join:
+// workers that are at different depths of K share no weights' pages, nor, with pairs, the rows in L2.
+RaggedChoice grouped_choice(int mode, int64_t groups, int64_t rows, int64_t pdim, int64_t kdim, bool may_split, const RaggedDevice *dev)
 {
-    if (mode == kTN) return kVTn;
     const int few_v = mode == kNT ? kVNtFew : kVNnFew, wide_v = mode == kNT ? kVNtWide : kVNnWide;
-    if (rows <= kRagged[few_v].qcap * groups) return few_v;
-    const double live = double(groups < rows ? groups : rows), each = double(rows) / live, blocks = double(cdiv(kdim, kRagBlockK));
     const RaggedVariant &f = kRagged[few_v], &w = kRagged[wide_v];
-    const double few_tiles = live * double(cdiv(int64_t(each), f.qcap)) * double(cdiv(pdim, 128));
-    const double wide_tiles = live * double(cdiv(int64_t(each), w.qcap)) * double(cdiv(pdim, 256));
-    const double few = few_tiles * (blocks * 24576.0 / 12e6 + 2.0 / dev->slots[few_v]);
-    const double block = 0.16 + 0.11 * (each < 256.0 ? each / 256.0 : 1.0);
-    const double waves = double(cdiv(int64_t(wide_tiles), dev->slots[wide_v]));
-    double wide = waves * (blocks * block + 4.0);
-    if (split_pays(int64_t(wide_tiles), int64_t(blocks), dev->slots[wide_v]))
-        wide = wide_tiles / dev->slots[wide_v] * blocks * block + 20.0;
-    return few < wide ? few_v : wide_v;
+    const int64_t live = groups < rows ? groups : rows;
+    if (live == 0) return {few_v, false};
+    const double each = double(rows) / double(live), blocks = double(cdiv(kdim, kRagBlockK));
+    const double bytes = 2.0 * (double(live) * double(pdim) * double(kdim) + double(rows) * double(pdim + kdim)) / 6.6e6;
+    const double part = each < w.qcap ? each / w.qcap : 1.0;  // of a pair's N side
+    const int64_t few_tiles = live * cdiv(int64_t(each), f.qcap) * cdiv(pdim, 128);
+    const int64_t wide_tiles = live * cdiv(int64_t(each), w.qcap) * cdiv(pdim, 256);
+    const double few_share = double(few_tiles) / dev->slots[few_v], wide_share = double(wide_tiles) / dev->slots[wide_v];
+    const double few_block = 0.195 + 0.093 * (few_share < 1.0 ? few_share : 1.0);  // a CTA alone, and with its share of L2's rate
+    const double wide_block = 0.226 + 0.08 * part;
+    auto most = [](double a, double b) { return a > b ? a : b; };
+    RaggedChoice best = {few_v, false};
+    double time = 3.6 + most(bytes, double(cdiv(few_tiles, dev->slots[few_v])) * (blocks * few_block + 0.4));
+    auto offer = [&](int variant, bool split, double t) {
+        if (t < time) {
+            time = t;
+            best = {variant, split};
+        }
+    };
+    offer(wide_v, false, 3.8 + most(bytes, double(cdiv(wide_tiles, dev->slots[wide_v])) * (blocks * wide_block + 0.8 + 1.76 * part)));
+    if (may_split) {
+        offer(few_v, true, 7.7 + most(bytes, few_share * blocks * 0.288 + 0.4));
+        if (rows > f.qcap && wide_share < 1.0 && blocks >= kWideSplitBlocks)
+            offer(wide_v, true, 8.5 + 9.6 * part + most(bytes, wide_share * blocks * wide_block));
+    }
+    return best;
 }
 
 // Tiles of a forward or data-gradient launch, at most (a group's last tile may be a part of one).
@@ -367,19 +385,12 @@ int64_t most_tiles(const RaggedVariant &var, int64_t groups, int64_t rows, int64
     return cdiv(pdim, 128 * var.cg) * (rows / var.qcap + (groups < rows ? groups : rows));
 }
 
-// Whether tiles are split over K: always for few rows, where every worker then reads the same number of weights; for
-// more rows only where it leaves fewer workers idle for long (a partial tile is 256 KB there, and tiles of one group
-// have to be worked on together to share its weights).
-bool split_tiles(int variant, int64_t most, int64_t kdim, const RaggedDevice *dev)
+// Bytes of split work that any number of rows up to this one may need.
+size_t split_room(int64_t rows, int64_t kdim, const RaggedDevice *dev)
 {
-    return kRagged[variant].cg == 1 || split_pays(most, cdiv(kdim, kRagBlockK), dev->slots[variant]);
-}
-
-size_t grouped_bytes(int mode, int64_t groups, int64_t rows, int64_t pdim, int64_t kdim, const RaggedDevice *dev)
-{
-    if (mode == kTN) return maps_bytes(groups);
-    const int v = grouped_variant(mode, groups, rows, pdim, kdim, dev);
-    return split_tiles(v, most_tiles(kRagged[v], groups, rows, pdim), kdim, dev) ? split_bytes(kRagged[v], dev->slots[v]) : 0;
+    const size_t few = split_bytes(kRagged[kVNtFew], dev->slots[kVNtFew]);
+    const size_t wide = split_bytes(kRagged[kVNtWide], dev->slots[kVNtWide]);
+    return rows > kRagged[kVNtFew].qcap && cdiv(kdim, kRagBlockK) >= kWideSplitBlocks && wide > few ? wide : few;
 }
 
 gemm_status_t grouped(int mode, gemm_dtype_t dtype, gemm_dtype_t out_type, int64_t groups, int64_t rows, int64_t n, int64_t k,
@@ -406,9 +417,11 @@ gemm_status_t grouped(int mode, gemm_dtype_t dtype, gemm_dtype_t out_type, int64
     RaggedDevice *dev = nullptr;
     st = ragged_device(&dev);
     if (st != GEMM_OK) return st;
-    const int variant = grouped_variant(mode, groups, rows, pdim, kdim, dev);
+    RaggedChoice choice = {kVTn, false};
+    if (mode != kTN) choice = grouped_choice(mode, groups, rows, pdim, kdim, ws != nullptr, dev);
+    const int variant = choice.variant;
     const RaggedVariant &var = kRagged[variant];
-    const size_t need = grouped_bytes(mode, groups, rows, pdim, kdim, dev);
+    const size_t need = mode == kTN ? maps_bytes(groups) : choice.split ? split_bytes(var, dev->slots[variant]) : 0;
     if (ws != nullptr || ws_bytes != 0) {
         if (ws == nullptr || ws_bytes < need) return GEMM_ERR_WORKSPACE;
         if (reinterpret_cast<uintptr_t>(ws) & 255u) return GEMM_ERR_ALIGNMENT;
@@ -450,7 +463,7 @@ gemm_status_t grouped(int mode, gemm_dtype_t dtype, gemm_dtype_t out_type, int64
         st = encode_stack(&p.tm_p, second, dtype, groups, n, k, 64, mode == kNT ? 128 : 64);
         if (st == GEMM_OK && mode == kNN) st = encode_pairs(&p.tm_p2, second, dtype, groups, n, k, &p.p_groups);
         if (st == GEMM_OK) st = encode_rows(p.tm_q, first, dtype, rows, kdim, var.qbox);
-        if (ws && split_tiles(variant, most, kdim, dev) && most * p.k_blocks < kIterLimit) {
+        if (choice.split && most * p.k_blocks < kIterLimit) {
             use_split(&p, var, dev->slots[variant], ws);
             most *= p.k_blocks;
         }
@@ -502,6 +515,7 @@ bool lora_beside(const RaggedDevice *dev, int64_t rows, int64_t n, int64_t k, in
 struct LoraPlan {
     bool beside;
     int variant_y;
+    bool split_y;          // beside: whether the projection's tiles are split
     int64_t per, tiles;    // y's row tiles, of one pass
     int64_t tiles_u;
     int64_t pass_rows;
@@ -513,7 +527,9 @@ LoraPlan lora_layout(const RaggedDevice *dev, int64_t rows, int64_t n, int64_t k
     LoraPlan l;
     memset(&l, 0, sizeof(l));
     l.beside = beside;
-    l.variant_y = l.beside ? grouped_variant(kNT, 1, rows, n, k, dev) : kVLoraY;
+    const RaggedChoice y_beside = grouped_choice(kNT, 1, rows, n, k, true, dev);
+    l.variant_y = l.beside ? y_beside.variant : kVLoraY;
+    l.split_y = l.beside && y_beside.split;
     const RaggedVariant &y = kRagged[l.variant_y];
     size_t at = 0;
     auto take = [&](size_t bytes) {
@@ -525,8 +541,7 @@ LoraPlan lora_layout(const RaggedDevice *dev, int64_t rows, int64_t n, int64_t k
         l.pass_rows = rows;
         l.u = take(size_t(rows) * size_t(rank) * 4u);
         l.delta = take(size_t(rows) * size_t(n) * 4u);
-        const bool split = split_tiles(l.variant_y, most_tiles(y, 1, rows, n), k, dev);
-        l.split = take(split ? split_bytes(y, dev->slots[l.variant_y]) : 0);
+        l.split = take(split_room(rows, k, dev));
         l.total = at;
         return l;
     }
@@ -595,12 +610,8 @@ gemm_status_t gemm_grouped_workspace_size(int64_t groups, int64_t rows, int64_t 
     st = ragged_device(&dev);
     if (st != GEMM_OK) return st;
     // what any number of rows up to this one may need, so that a buffer for the most rows serves them all
-    *bytes = maps_bytes(groups);
-    const size_t few = split_bytes(kRagged[kVNtFew], dev->slots[kVNtFew]);
-    const size_t wide = split_bytes(kRagged[kVNtWide], dev->slots[kVNtWide]);
-    if (few > *bytes) *bytes = few;
-    if (rows > kRagged[kVNtFew].qcap && split_pays(1, cdiv(n > k ? n : k, kRagBlockK), dev->slots[kVNtWide]) && wide > *bytes)
-        *bytes = wide;
+    const size_t maps = maps_bytes(groups), split = split_room(rows, n > k ? n : k, dev);
+    *bytes = maps > split ? maps : split;
     return GEMM_OK;
 }
 
@@ -737,7 +748,7 @@ gemm_status_t gemm_lora_nt(gemm_dtype_t dtype, int64_t rows, int64_t n, int64_t 
         }
         int64_t most = most_tiles(vy, 1, rows, n);
         if (most >= kSizeLimit) return GEMM_ERR_UNSUPPORTED_SHAPE;
-        if (split_tiles(l.variant_y, most, k, dev) && most * p.k_blocks < kIterLimit) {
+        if (l.split_y && most * p.k_blocks < kIterLimit) {
             use_split(&p, vy, dev->slots[l.variant_y], ws + l.split);
             most *= p.k_blocks;
         }

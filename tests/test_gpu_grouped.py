@@ -259,3 +259,61 @@ def test_starved_wait_reports_timeout_and_recovers(mode, sizes, skip):
     st, code = G.gemm_f16_take_device_error()
     assert st == G.GEMM_ERR_TIMEOUT and (code & 0xFF) in range(1, 12)
     assert torch.equal(grouped_run(op, first, second, offsets), ref)
+
+
+# Sizes at which single CTAs' tiles, and CTA pairs', are split over K.
+SPLIT = {"single CTAs": ([3, 4], 264, 8200), "pairs": ([700], 2000, 8192), "pairs, two groups": ([290, 300], 1032, 8200)}
+
+
+@pytest.mark.parametrize("op", ["nt", "nn"])
+@pytest.mark.parametrize("name", sorted(SPLIT))
+@pytest.mark.parametrize("workspace", [True, False])
+def test_split_tiles(op, name, workspace):
+    sizes, other, long = SPLIT[name]
+    check_exact(op, sizes, other if op == "nt" else long, long if op == "nt" else other, torch.bfloat16, seed=31, workspace=workspace)
+
+
+def test_split_tiles_in_a_graph():
+    """A partial sum's flag is spent by the launch that adds it: every replay, all of one number, waits for its own."""
+    rng = np.random.default_rng(8)
+    n, k, rows = 264, 8200, 7
+    w = eighths(rng, (2, n, k), torch.float16)
+    wd, od = w.cuda(), offsets_of([3, 4]).cuda()
+    xd = torch.zeros((rows, k), dtype=torch.float16, device="cuda")
+    ws = torch.full((R.gemm_grouped_workspace_size(2, rows, n, k),), 0x5A, dtype=torch.uint8, device="cuda")
+    y = R.gemm_grouped_nt(xd, wd, od, workspace=ws)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        R.gemm_grouped_nt(xd, wd, od, y=y, workspace=ws)
+    for _ in range(4):
+        x = eighths(rng, (rows, k), torch.float16)
+        xd.copy_(x)
+        graph.replay()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(y.cpu(), grouped_ref("nt", x, w, offsets_of([3, 4]), 2).half())
+    no_device_error()
+
+
+@pytest.mark.parametrize("mode", [0, 1])
+@pytest.mark.parametrize("name", ["single CTAs", "pairs"])
+def test_starved_split_reports_timeout_and_recovers(mode, name):
+    """The worker whose fill never comes publishes no partial sum: the one that waits for it gives up as well."""
+    op = OPS[mode]
+    rng = np.random.default_rng(3)
+    sizes, other, long = SPLIT[name]
+    n, k = (other, long) if op == "nt" else (long, other)
+    first, second = grouped_operands(op, rng, sizes, n, k, torch.float16)
+    offsets = offsets_of(sizes)
+    ref = grouped_ref(op, first, second, offsets, len(sizes)).half()
+    f, s, o = first.cuda(), second.cuda(), offsets.cuda()
+    out = torch.zeros(ref.shape, dtype=torch.float16, device="cuda")
+    ws = torch.zeros(R.gemm_grouped_workspace_size(len(sizes), sum(sizes), n, k), dtype=torch.uint8, device="cuda")
+    no_device_error()
+    assert R.gemm_grouped_stall_test(mode, f, s, o, out, ws, 0, 1 << 24) == G.GEMM_OK
+    st, code = G.gemm_f16_take_device_error()
+    assert st == G.GEMM_ERR_TIMEOUT and (code & 0xFF) in range(1, 12)
+    call = R.gemm_grouped_nt if op == "nt" else R.gemm_grouped_nn
+    assert torch.equal(call(f, s, o, workspace=ws).cpu(), ref)  # the same workspace, flags of the aborted launch in it
+    no_device_error()
