@@ -6,6 +6,7 @@
 #include <cuda_runtime.h>
 
 #include <mutex>
+#include <math.h>
 #include <string.h>
 
 #include "device_state.h"
@@ -347,7 +348,9 @@ struct RaggedChoice {
 // (16 rows in 36 groups, 1264 x 368: 6.6 us unsplit, 9.8 split; 12 rows in 2 groups, 728 x 4808: 18.8 and 10.7; 409 rows in
 // 50 groups, data gradient, 2968 x 5656: 419 split single CTAs, 253 pairs).  Splitting many tiles loses more than the join:
 // workers that are at different depths of K share no weights' pages, nor, with pairs, the rows in L2.
-RaggedChoice grouped_choice(int mode, int64_t groups, int64_t rows, int64_t pdim, int64_t kdim, bool may_split, const RaggedDevice *dev)
+// `beside` (us): other work that the main loops run beside and their ends wait for.
+RaggedChoice grouped_choice(int mode, int64_t groups, int64_t rows, int64_t pdim, int64_t kdim, bool may_split, double beside,
+                            const RaggedDevice *dev)
 {
     const int few_v = mode == kNT ? kVNtFew : kVNnFew, wide_v = mode == kNT ? kVNtWide : kVNnWide;
     const RaggedVariant &f = kRagged[few_v], &w = kRagged[wide_v];
@@ -361,20 +364,22 @@ RaggedChoice grouped_choice(int mode, int64_t groups, int64_t rows, int64_t pdim
     const double few_share = double(few_tiles) / dev->slots[few_v], wide_share = double(wide_tiles) / dev->slots[wide_v];
     const double few_block = 0.195 + 0.093 * (few_share < 1.0 ? few_share : 1.0);  // a CTA alone, and with its share of L2's rate
     const double wide_block = 0.226 + 0.08 * part;
-    auto most = [](double a, double b) { return a > b ? a : b; };
+    const double least = bytes > beside ? bytes : beside;
     RaggedChoice best = {few_v, false};
-    double time = 3.6 + most(bytes, double(cdiv(few_tiles, dev->slots[few_v])) * (blocks * few_block + 0.4));
-    auto offer = [&](int variant, bool split, double t) {
+    double time = 1e30;
+    auto offer = [&](int variant, bool split, double fixed, double loops) {
+        const double t = fixed + (loops > least ? loops : least);
         if (t < time) {
             time = t;
             best = {variant, split};
         }
     };
-    offer(wide_v, false, 3.8 + most(bytes, double(cdiv(wide_tiles, dev->slots[wide_v])) * (blocks * wide_block + 0.8 + 1.76 * part)));
+    offer(few_v, false, 3.6, double(cdiv(few_tiles, dev->slots[few_v])) * (blocks * few_block + 0.4));
+    offer(wide_v, false, 3.8, double(cdiv(wide_tiles, dev->slots[wide_v])) * (blocks * wide_block + 0.8 + 1.76 * part));
     if (may_split) {
-        offer(few_v, true, 7.7 + most(bytes, few_share * blocks * 0.288 + 0.4));
+        offer(few_v, true, 7.7, few_share * blocks * 0.288 + 0.4);
         if (rows > f.qcap && wide_share < 1.0 && blocks >= kWideSplitBlocks)
-            offer(wide_v, true, 8.5 + 9.6 * part + most(bytes, wide_share * blocks * wide_block));
+            offer(wide_v, true, 8.5 + 9.6 * part, wide_share * blocks * wide_block);
     }
     return best;
 }
@@ -418,7 +423,7 @@ gemm_status_t grouped(int mode, gemm_dtype_t dtype, gemm_dtype_t out_type, int64
     st = ragged_device(&dev);
     if (st != GEMM_OK) return st;
     RaggedChoice choice = {kVTn, false};
-    if (mode != kTN) choice = grouped_choice(mode, groups, rows, pdim, kdim, ws != nullptr, dev);
+    if (mode != kTN) choice = grouped_choice(mode, groups, rows, pdim, kdim, ws != nullptr, 0.0, dev);
     const int variant = choice.variant;
     const RaggedVariant &var = kRagged[variant];
     const size_t need = mode == kTN ? maps_bytes(groups) : choice.split ? split_bytes(var, dev->slots[variant]) : 0;
@@ -496,18 +501,26 @@ constexpr int64_t kLoraURows = 64;  // rows of a tile of the product that comput
 // Rows and rank up to which one kernel takes both of the adapters' steps beside the projection (measured at the kernel).
 constexpr int64_t kLoraRowsRows = 32, kLoraRowsRank = 32;
 
-// Whether the adapters run beside the projection without tensor cores, row by row.  That reads every row's a and b (from
-// L2, mostly) at about 5 TB/s; on the tensor cores each row tile takes a K block per adapter in it, at most 1.6 us of a
-// worker's time each, after some 15 us of launches that depend on one another.  1024 rows, 64 adapters of rank 16,
-// 8192 x 4096: 131 us beside, 300 on the tensor cores; 512 rows, 16 adapters of rank 64, 4096 x 4096: 130 and 73.
+// Time (us) of the adapters row by row, without tensor cores: every row's a and b, from L2 mostly, at about 5 TB/s.
+double lora_alone(int64_t rows, int64_t n, int64_t k, int64_t rank)
+{
+    return 2.0 * double(rows) * double(rank) * double(n + k) / 5e6;
+}
+
+// Whether the adapters run row by row beside the projection.  On the tensor cores each row tile takes a K block per
+// adapter in it, 1.6 us of a worker's time each, after some 15 us of launches that depend on one another.  How many adapters
+// a tile of up to 256 rows has is in ids on the device: one where rows come in prompts, all where each row is a request
+// of its own.  (adapters)^0.7 stands between: over 283 launches of random sizes, 65 to 16000 rows, it costs 1.4% over the
+// faster way on average where each row is a request and 5.7% where rows come in runs, at most 1.6 and 4.1 times; all adapters
+// cost 1.1% and 9.6%, at most 1.6 and 9.1 times (2489 rows of 10 prompts, 228 adapters of rank 72, 5776 x 2624: 952 us
+// beside, 104 on the tensor cores), their square root 4.3% and 2.7%, at most 4.1 and 1.5 times.
 bool lora_beside(const RaggedDevice *dev, int64_t rows, int64_t n, int64_t k, int64_t rank, int64_t adapters)
 {
     if (rows <= kRagged[kVNtFew].qcap) return true;
     const RaggedVariant &y = kRagged[kVLoraY];
-    const double alone = 2.0 * double(rows) * double(rank) * double(n + k) / 5e6;  // us
     const double waves = double(cdiv(n, 128 * y.cg)) * double(cdiv(rows, y.qcap)) / dev->slots[kVLoraY];
-    const double blocks = double(adapters < y.qcap ? adapters : y.qcap) * double(cdiv(rank, kRagBlockK));
-    return alone < 15.0 + (waves < 1.0 ? 1.0 : waves) * blocks * 1.6;
+    const double blocks = pow(double(adapters < y.qcap ? adapters : y.qcap), 0.7) * double(cdiv(rank, kRagBlockK));
+    return lora_alone(rows, n, k, rank) < 15.0 + (waves < 1.0 ? 1.0 : waves) * blocks * 1.6;
 }
 
 // How the work and the workspace are laid out.  Beside: u and delta in fp32.  Otherwise: counts and lists
@@ -527,7 +540,9 @@ LoraPlan lora_layout(const RaggedDevice *dev, int64_t rows, int64_t n, int64_t k
     LoraPlan l;
     memset(&l, 0, sizeof(l));
     l.beside = beside;
-    const RaggedChoice y_beside = grouped_choice(kNT, 1, rows, n, k, true, dev);
+    // (4 us more: their launches.  Loops that end before the adapters do anyhow are not worth a join: 320 launches of
+    // random sizes are 1.6% off the fastest of the four ways this way, 3.5% without)
+    const RaggedChoice y_beside = grouped_choice(kNT, 1, rows, n, k, true, 4.0 + lora_alone(rows, n, k, rank), dev);
     l.variant_y = l.beside ? y_beside.variant : kVLoraY;
     l.split_y = l.beside && y_beside.split;
     const RaggedVariant &y = kRagged[l.variant_y];
