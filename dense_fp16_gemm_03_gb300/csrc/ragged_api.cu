@@ -332,6 +332,7 @@ gemm_status_t launch_ragged(int variant, const RaggedDevice *dev, RaggedParams &
 
 // ------------------------------------------------------ grouped products
 
+constexpr int64_t kMinPartRows = 256;      // rows of a part of a weight gradient's group, at least
 constexpr int64_t kWideSplitBlocks = 16;  // K blocks below which splitting pairs' tiles never pays
 
 // A forward or data-gradient launch: single CTAs with a 64-row N side, or CTA pairs with up to 256 rows, and whether
@@ -384,6 +385,41 @@ RaggedChoice grouped_choice(int mode, int64_t groups, int64_t rows, int64_t pdim
     return best;
 }
 
+// Rows of the parts that a weight-gradient launch cuts its groups into, 0 for whole groups.  Tiles of few groups leave pairs
+// idle while each goes through all rows of its group, 0.35 us a K block; parts fill the pairs and cost the sum of their
+// matrices, written and read through L2 at some 4.5 TB/s, and a launch.
+int64_t grouped_part_rows(int64_t groups, int64_t rows, int64_t n, int64_t k, const RaggedDevice *dev)
+{
+    const RaggedVariant &v = kRagged[kVTn];
+    const int64_t each = cdiv(n, 128 * v.cg) * cdiv(k, v.qcap), slots = dev->slots[kVTn];  // tiles of a matrix
+    if (groups * each > slots || groups > int64_t(kRagPartGroups) || rows <= kMinPartRows) return 0;
+    const double live = double(groups < rows ? groups : rows), loops = 0.35 * double(rows) / kRagBlockK;
+    const double matrix = double(n) * double(k) * 8.0 / 4.5e6;  // us
+    double parts = double(slots / each) - 0.5 * live;  // (a group's last part is a half, on average)
+    const double best = sqrt(loops / matrix);
+    if (best < parts) parts = best;
+    if (parts <= live) return 0;
+    int64_t part = round_up(int64_t(double(rows) / parts) + 1, kRagBlockK);
+    if (part < kMinPartRows) part = kMinPartRows;
+    const double split = loops * double(part) / double(rows) + 3.0 + (double(rows) / double(part) + 0.5 * live) * matrix;
+    return split < loops / live ? part : 0;
+}
+
+// Bytes of the parts' matrices, of `parts` parts.
+size_t part_bytes(int64_t parts, int64_t n, int64_t k)
+{
+    return size_t(parts) * size_t(n) * size_t(k) * 4u;
+}
+
+// What any number of rows up to this one may need for parts.
+size_t part_room(int64_t groups, int64_t rows, int64_t n, int64_t k, const RaggedDevice *dev)
+{
+    const RaggedVariant &v = kRagged[kVTn];
+    const int64_t each = cdiv(n, 128 * v.cg) * cdiv(k, v.qcap), slots = dev->slots[kVTn];
+    if (groups * each > slots || each == 0 || groups > int64_t(kRagPartGroups) || rows <= kMinPartRows) return 0;
+    return part_bytes(slots / each + groups, n, k);
+}
+
 // Tiles of a forward or data-gradient launch, at most (a group's last tile may be a part of one).
 int64_t most_tiles(const RaggedVariant &var, int64_t groups, int64_t rows, int64_t pdim)
 {
@@ -426,7 +462,12 @@ gemm_status_t grouped(int mode, gemm_dtype_t dtype, gemm_dtype_t out_type, int64
     if (mode != kTN) choice = grouped_choice(mode, groups, rows, pdim, kdim, ws != nullptr, 0.0, dev);
     const int variant = choice.variant;
     const RaggedVariant &var = kRagged[variant];
-    const size_t need = mode == kTN ? maps_bytes(groups) : choice.split ? split_bytes(var, dev->slots[variant]) : 0;
+    const int64_t part_rows = mode == kTN && ws && skip_fill == ~0u ? grouped_part_rows(groups, rows, n, k, dev) : 0;
+    const int64_t parts = part_rows ? rows / part_rows + (groups < rows ? groups : rows) : 0;
+    const size_t need = part_rows       ? part_bytes(parts, n, k)
+                        : mode == kTN   ? maps_bytes(groups)
+                        : choice.split  ? split_bytes(var, dev->slots[variant])
+                                        : 0;
     if (ws != nullptr || ws_bytes != 0) {
         if (ws == nullptr || ws_bytes < need) return GEMM_ERR_WORKSPACE;
         if (reinterpret_cast<uintptr_t>(ws) & 255u) return GEMM_ERR_ALIGNMENT;
@@ -455,7 +496,7 @@ gemm_status_t grouped(int mode, gemm_dtype_t dtype, gemm_dtype_t out_type, int64
     p.skip_fill = skip_fill;
     p.wait_limit = wait_limit ? wait_limit : wait_limit_for(p.k_blocks);
     int64_t most;  // tiles, at most
-    if (mode == kTN) most = int64_t(p.tiles_p) * p.tiles_q * (groups < rows ? groups : rows);
+    if (mode == kTN) most = int64_t(p.tiles_p) * p.tiles_q * (part_rows ? parts : groups);  // (groups without rows are zeroed)
     else most = most_tiles(var, groups, rows, pdim);
     if (most >= kSizeLimit) return GEMM_ERR_UNSUPPORTED_SHAPE;
     if (mode == kTN) {
@@ -463,7 +504,16 @@ gemm_status_t grouped(int mode, gemm_dtype_t dtype, gemm_dtype_t out_type, int64
         if (st == GEMM_OK) st = encode_stack(&p.tm_q[0], second, dtype, 1, rows, k, 64, 64);
         if (st == GEMM_OK) st = encode_pairs(&p.tm_p2, first, dtype, 1, rows, n, &p.p_groups);
         if (st == GEMM_OK) st = encode_pairs(&p.tm_q2, second, dtype, 1, rows, k, &p.q_groups);
-        if (st == GEMM_OK) st = encode_stack(&p.tm_x, out, out_type, groups, n, k, p.out32 ? 32 : 64, 32);
+        if (part_rows) {
+            p.part_rows = uint32_t(part_rows);
+            p.whole_groups = uint32_t(groups);
+            p.groups = uint32_t(parts);
+            p.out32 = 1;
+            p.out = ws;
+            if (st == GEMM_OK) st = encode_stack(&p.tm_x, ws, GEMM_DTYPE_F32, parts, n, k, 32, 32);
+        } else if (st == GEMM_OK) {
+            st = encode_stack(&p.tm_x, out, out_type, groups, n, k, p.out32 ? 32 : 64, 32);
+        }
     } else {
         st = encode_stack(&p.tm_p, second, dtype, groups, n, k, 64, mode == kNT ? 128 : 64);
         if (st == GEMM_OK && mode == kNN) st = encode_pairs(&p.tm_p2, second, dtype, groups, n, k, &p.p_groups);
@@ -475,7 +525,8 @@ gemm_status_t grouped(int mode, gemm_dtype_t dtype, gemm_dtype_t out_type, int64
     }
     if (st != GEMM_OK) return st;
     // (one or two tiles a worker: the kernel that writes the maps would take longer than the helper it spares)
-    if (ws && mode == kTN && most > 2 * dev->slots[variant]) {
+    const int64_t live = groups < rows ? groups : rows;
+    if (ws && mode == kTN && !part_rows && int64_t(p.tiles_p) * p.tiles_q * live > 2 * dev->slots[variant]) {
         RaggedMapsParams mp;
         memset(&mp, 0, sizeof(mp));
         mp.maps[0] = p.tm_p;
@@ -492,7 +543,21 @@ gemm_status_t grouped(int mode, gemm_dtype_t dtype, gemm_dtype_t out_type, int64
         st = launch(reinterpret_cast<const void *>(&ragged_maps_kernel), dim3(unsigned(groups), 1, 1), 128, 0, 1, args, stream);
         if (st != GEMM_OK) return st;
     }
-    return launch_ragged(variant, dev, p, most, stream);
+    st = launch_ragged(variant, dev, p, most, stream);
+    if (st != GEMM_OK || !part_rows) return st;
+    RaggedPartsParams add;
+    add.parts = static_cast<const float4 *>(ws);
+    add.offsets = offsets;
+    add.out = out;
+    add.groups = uint32_t(groups);
+    add.rows = uint32_t(rows);
+    add.part_rows = uint32_t(part_rows);
+    add.quads = uint32_t(n * k / 4);
+    add.out32 = out_type == GEMM_DTYPE_F32;
+    add.bf16 = p.bf16;
+    void *args[1] = {&add};
+    return launch(reinterpret_cast<const void *>(&ragged_parts_kernel), dim3(unsigned(cdiv(add.quads, 256)), unsigned(groups), 1), 256, 0,
+                  1, args, stream);
 }
 
 // ------------------------------------------------------------- adapters
@@ -625,8 +690,9 @@ gemm_status_t gemm_grouped_workspace_size(int64_t groups, int64_t rows, int64_t 
     st = ragged_device(&dev);
     if (st != GEMM_OK) return st;
     // what any number of rows up to this one may need, so that a buffer for the most rows serves them all
-    const size_t maps = maps_bytes(groups), split = split_room(rows, n > k ? n : k, dev);
-    *bytes = maps > split ? maps : split;
+    *bytes = maps_bytes(groups);
+    for (size_t room : {split_room(rows, n > k ? n : k, dev), part_room(groups, rows, n, k, dev)})
+        if (room > *bytes) *bytes = room;
     return GEMM_OK;
 }
 

@@ -133,6 +133,8 @@ struct RaggedParams {
     uint32_t rank;
     uint32_t rank_blocks;    // ceil(rank / 64)
     const CUtensorMap *maps; // kTN: for each group tm_p, tm_q[0], tm_p2, tm_q2 that end with the group's rows, or null
+    uint32_t part_rows;      // kTN: not 0: groups are cut into parts of this many rows, which then are the `groups` of the
+    uint32_t whole_groups;   // launch, each with a matrix of its own in `out`; and the number of whole ones
     float *partials;         // sk: one 128 x QCAP fp32 tile per CTA
     uint64_t *flags;         // sk: one per CTA, `stamp` while its partial waits to be added
     uint64_t stamp;
@@ -462,7 +464,7 @@ template <int MODE, int QCAP>
 __device__ __forceinline__ void ragged_table(const RaggedParams &p, int32_t *tab_row, uint32_t *tab_tile)
 {
     constexpr bool kOffsets = (MODE == kNT || MODE == kNN || MODE == kTN);
-    const uint32_t n = p.groups + (kOffsets ? 1u : 0u);
+    const uint32_t n = (MODE == kTN && p.part_rows ? p.whole_groups : p.groups) + (kOffsets ? 1u : 0u);
     for (uint32_t i = threadIdx.x; i < n; i += blockDim.x) {
         int32_t v;
         if (!kOffsets) v = p.counts[i];
@@ -491,6 +493,29 @@ __device__ __forceinline__ void ragged_table(const RaggedParams &p, int32_t *tab
             }
             __syncwarp();
         }
+    }
+    if constexpr (MODE == kTN) {
+        if (p.part_rows) {  // the table of the parts; those that there are not have no rows
+            __syncthreads();
+            const uint32_t i = threadIdx.x;
+            const bool group = i + 1u < n;
+            const int32_t begin = group ? tab_row[i] : 0, end = tab_row[n - 1u];
+            const uint32_t count = group ? (uint32_t(tab_row[i + 1u] - begin) + p.part_rows - 1u) / p.part_rows : 0u;
+            if (group) tab_tile[i] = count;
+            __syncthreads();
+            uint32_t first = 0, all = 0;
+            for (uint32_t j = 0; j + 1u < n; ++j) {
+                if (j == i) first = all;
+                all += tab_tile[j];
+            }
+            __syncthreads();
+            for (uint32_t j = 0; j < count; ++j) tab_row[first + j] = begin + int32_t(j * p.part_rows);
+            for (uint32_t j = all + i; j <= p.groups; j += blockDim.x) tab_row[j] = end;
+            __syncthreads();
+        }
+    }
+    if (threadIdx.x < 32u && MODE != kLoraY) {
+        const uint32_t lane = threadIdx.x;
         auto tiles = [&](uint32_t g) -> uint32_t {
             if constexpr (MODE == kLoraU) return uint32_t(tab_row[g]);
             const uint32_t rows = uint32_t(tab_row[g + 1] - tab_row[g]);
@@ -867,7 +892,8 @@ __global__ void __launch_bounds__(RaggedCfg<MODE, CG, QCAP, STAGES>::kThreads, 1
             }
             if constexpr (MODE == kTN) {
                 const uint64_t each = uint64_t(p.pdim) * p.qdim * esize / 16u;
-                for (uint32_t g = 0; g < p.groups; ++g)
+                const uint32_t groups = p.part_rows ? 0u : p.groups;
+                for (uint32_t g = 0; g < groups; ++g)
                     if (tab_row[g] == tab_row[g + 1]) zero(g * each, each);
             }
         }
@@ -1272,6 +1298,58 @@ __global__ void __launch_bounds__(128) ragged_maps_kernel(const __grid_constant_
         ptx::tensormap_publish(p.out + 4u * g + i, ptx::smem_addr(&s_map[i]));
     }
     ptx::griddep_launch_dependents();
+}
+
+// kTN with few tiles: the rows of a group are cut into parts of `part_rows` (a multiple of a K block), each part's sum
+// goes to a matrix of its own in fp32, and this kernel adds a group's parts, in order, and rounds once.  Bound by L2 for
+// large matrices, else by its launch.  One block row per group.  (10560 rows in one group, 64 x 248: 63.6 us whole, 15.6
+// in parts; 27407 rows in 3 groups, 640 x 104: 89.3 and 18.7; 9426 in 2, 144 x 3328: 32.6 and 25.3.)
+constexpr uint32_t kRagPartGroups = 128;
+
+struct RaggedPartsParams {
+    const float4 *parts;  // [parts][n * k / 4]
+    const int32_t *offsets;
+    void *out;            // [groups, n, k]
+    uint32_t groups, rows, part_rows;
+    uint32_t quads;       // n * k / 4
+    uint32_t out32, bf16;
+};
+
+__global__ void __launch_bounds__(256) ragged_parts_kernel(const __grid_constant__ RaggedPartsParams p)
+{
+    __shared__ int32_t s_row[kRagPartGroups + 1];
+    __shared__ uint32_t s_parts[kRagPartGroups];
+    ptx::griddep_wait();
+    ptx::griddep_launch_dependents();
+    const uint32_t i = threadIdx.x, g = blockIdx.y;
+    if (i <= p.groups) s_row[i] = max(0, min(p.offsets[i], int32_t(p.rows)));
+    __syncthreads();
+    if (i < p.groups) {  // as ragged_table has them
+        int32_t begin = 0;
+        for (uint32_t j = 0; j <= i; ++j) begin = max(begin, s_row[j]);
+        s_parts[i] = uint32_t((max(begin, s_row[i + 1]) - begin + int32_t(p.part_rows) - 1) / int32_t(p.part_rows));
+    }
+    __syncthreads();
+    uint32_t first = 0;
+    for (uint32_t j = 0; j < g; ++j) first += s_parts[j];
+    const uint32_t count = s_parts[g];
+    const uint32_t q = blockIdx.x * 256u + i;
+    if (q >= p.quads) return;
+    const float4 *from = p.parts + size_t(first) * p.quads + q;
+    float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+    for (uint32_t j = 0; j < count; ++j) {
+        const float4 v = from[size_t(j) * p.quads];
+        sum.x += v.x;
+        sum.y += v.y;
+        sum.z += v.z;
+        sum.w += v.w;
+    }
+    const size_t at = size_t(g) * p.quads + q;
+    if (p.out32)
+        static_cast<float4 *>(p.out)[at] = sum;
+    else
+        static_cast<uint2 *>(p.out)[at] = make_uint2(ragged_pack(sum.x, sum.y, p.bf16 != 0u), ragged_pack(sum.z, sum.w, p.bf16 != 0u));
 }
 
 // Adapters without the tensor cores: with an adapter to nearly every row, all of the work is reading a and b once, and

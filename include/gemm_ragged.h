@@ -69,8 +69,8 @@ typedef enum gemm_dtype {
  * result, whatever they hold (infinities, NaN).
  *
  * gemm_grouped_workspace_size: bytes that serve any of the three calls of these
- * sizes, or of fewer rows, on the current device (partial sums of split tiles,
- * tensor maps of the groups).  A workspace may be NULL/0 all the same: that costs time
+ * sizes, or of fewer rows, on the current device (partial sums of split tiles and
+ * of parts of a group's rows, tensor maps of the groups).  A workspace may be NULL/0 all the same: that costs time
  * where there are few rows, and in gemm_grouped_tn; one that is given but too
  * small is GEMM_ERR_WORKSPACE.
  */

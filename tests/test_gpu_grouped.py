@@ -317,3 +317,54 @@ def test_starved_split_reports_timeout_and_recovers(mode, name):
     call = R.gemm_grouped_nt if op == "nt" else R.gemm_grouped_nn
     assert torch.equal(call(f, s, o, workspace=ws).cpu(), ref)  # the same workspace, flags of the aborted launch in it
     no_device_error()
+
+
+# Few tiles with many rows: the weight gradient's groups are cut into parts.
+PARTS = {"one group": [6000], "uneven": [3000, 0, 700, 65, 1], "ends in a part": [1024, 255, 2049], "empty ends": [0, 4000, 0]}
+
+
+@pytest.mark.parametrize("sizes", sorted(PARTS))
+@pytest.mark.parametrize("n,k", [(8, 8), (200, 136), (264, 520)])
+@pytest.mark.parametrize("dtype", [None, torch.float32])
+@pytest.mark.parametrize("workspace", [True, False])
+def test_weight_gradient_in_parts(sizes, n, k, dtype, workspace):
+    check_exact("tn", PARTS[sizes], n, k, torch.bfloat16, seed=41, dtype=dtype, workspace=workspace)
+    check_exact("tn", PARTS[sizes], n, k, torch.float16, seed=42, extra=90, head=7, dtype=dtype, workspace=workspace)
+
+
+def test_parts_keep_other_groups_infinities_out():
+    rng = np.random.default_rng(44)
+    sizes = [1500, 1301, 700]
+    dy, x = grouped_operands("tn", rng, sizes, 200, 136, torch.float16)
+    offsets = offsets_of(sizes)
+    ref = grouped_ref("tn", dy, x, offsets, 3)
+    dy[1500:2801] = float("inf")
+    x[1500:2801] = float("nan")
+    got = grouped_run("tn", dy, x, offsets)
+    assert torch.equal(got[::2], ref[::2].half()) and bool(torch.isnan(got[1]).all())
+
+
+def test_parts_repeat_bit_for_bit_in_a_graph():
+    rng = np.random.default_rng(45)
+    dy = torch.from_numpy(rng.standard_normal((5000, 200)).astype(np.float32)).half().cuda()
+    x = torch.from_numpy(rng.standard_normal((5000, 264)).astype(np.float32)).half().cuda()
+    offsets = offsets_of([1800, 3200]).cuda()
+    ws = torch.full((R.gemm_grouped_workspace_size(2, 5000, 200, 264),), 0xFF, dtype=torch.uint8, device="cuda")
+    first = R.gemm_grouped_tn(dy, x, offsets, workspace=ws)
+    out = torch.empty_like(first)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        for _ in range(3):
+            R.gemm_grouped_tn(dy, x, offsets, dw=out, workspace=ws)
+    ws.fill_(0xFF)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(first, out)
+    no_device_error()
+
+
+def test_weight_gradients_of_groups_without_rows_are_zero():
+    sizes = [0] * 30 + [1] + [0] * 40
+    check_exact("tn", sizes, 264, 136, torch.float16, seed=47)
+    check_exact("tn", sizes, 264, 136, torch.float16, seed=47, workspace=False)
