@@ -79,8 +79,8 @@ const void *lora_expand_instance(int64_t rank)
 const void *const kBeside[] = {
     lora_rows_instance(8),    lora_rows_instance(16),   lora_rows_instance(32),
     lora_expand_instance(8),  lora_expand_instance(16), lora_expand_instance(32),
-    lora_expand_instance(64), lora_expand_instance(128), reinterpret_cast<const void *>(&lora_shrink_kernel),
-    reinterpret_cast<const void *>(&lora_list_kernel), reinterpret_cast<const void *>(&ragged_maps_kernel),
+    lora_expand_instance(64), lora_expand_instance(128), reinterpret_cast<const void *>(&lora_shrink_kernel<1>),
+    reinterpret_cast<const void *>(&lora_shrink_kernel<4>), reinterpret_cast<const void *>(&lora_list_kernel), reinterpret_cast<const void *>(&ragged_maps_kernel),
 };
 
 struct RaggedDevice {
@@ -813,13 +813,21 @@ gemm_status_t gemm_lora_nt(gemm_dtype_t dtype, int64_t rows, int64_t n, int64_t 
                             args, s);
                 if (st != GEMM_OK) return st;
             } else {
-                // few enough blocks on an SM to leave room for the product's CTA beside them: with four and two, 64 rows
-                // with 64 adapters of rank 16, 8192 x 4096, take 29.1 us, with four and four 30.8, with one and two 33.5
+                // Few blocks on an SM where the product takes every SM's first CTA (64 rows with 64 adapters of rank 16,
+                // 8192 x 4096: four and two 28.6 us, eight and four 30.5, one and two 33.5) or is the longer part, more where
+                // its CTAs leave room (2749 rows, 17 adapters of rank 32, 160 x 216: 28.8 us, sixteen and eight 20.2; 139
+                // rows, 3544 x 448: 16.9 and 13.7).  Warps for items where eight blocks an SM would not hold them (913 rows,
+                // 208 x 304, rank 48: 33.2 us by blocks, 23.0 by warps; but 1024 items of 8192 x 4096 44.4 and 53.0).
+                const bool roomy = !l.split_y && vy.cg == 1;
                 const int64_t shrink = rows * (rank / 4), expand = cdiv(rows * cdiv(n, 128), 4);
-                st = launch(reinterpret_cast<const void *>(&lora_shrink_kernel),
-                            dim3(unsigned(shrink < 4 * room ? shrink : 4 * room), 1, 1), 128, 0, 1, args, s);
+                const bool warps = shrink > 8 * room;
+                const int64_t most_shrink = (roomy ? 16 : 4) * room, most_expand = (roomy ? 8 : 2) * room;
+                const int64_t blocks = warps ? cdiv(shrink, 4) : shrink;
+                st = launch(warps ? reinterpret_cast<const void *>(&lora_shrink_kernel<1>)
+                                  : reinterpret_cast<const void *>(&lora_shrink_kernel<4>),
+                            dim3(unsigned(blocks < most_shrink ? blocks : most_shrink), 1, 1), 128, 0, 1, args, s);
                 if (st != GEMM_OK) return st;
-                st = launch(lora_expand_instance(rank), dim3(unsigned(expand < 2 * room ? expand : 2 * room), 1, 1), 128,
+                st = launch(lora_expand_instance(rank), dim3(unsigned(expand < most_expand ? expand : most_expand), 1, 1), 128,
                             0, 1, args, s);
                 if (st != GEMM_OK) return st;
             }

@@ -1377,9 +1377,10 @@ __device__ __forceinline__ float2 ragged_unpack(uint32_t w, bool bf16)
     return __half22float2(*reinterpret_cast<const __half2 *>(&w));
 }
 
-// Four of a row's u's by one block of 128 threads, which share k: each lane multiplies 8 elements at a time.  Thread
-// t < 4 returns number t (before the scale); s_sum is the block's.
-__device__ __forceinline__ float lora_dot4(const LoraFewParams &p, uint32_t row, int32_t id, uint32_t r0, float (&s_sum)[4][4])
+// Four of a row's u's (before the scale) by WARPS warps that share k: each lane multiplies 8 elements at a time.  The sums
+// of a single warp are in all lanes; of four, thread t returns number t mod 4, and s_sum is the block's.
+template <int WARPS>
+__device__ __forceinline__ float lora_dot4(const LoraFewParams &p, uint32_t row, int32_t id, uint32_t r0, float (*s_sum)[4])
 {
     const uint32_t lane = threadIdx.x & 31u, warp = threadIdx.x >> 5;
     const bool bf16 = p.bf16 != 0u;
@@ -1387,7 +1388,7 @@ __device__ __forceinline__ float lora_dot4(const LoraFewParams &p, uint32_t row,
     const char *a = static_cast<const char *>(p.a) + (size_t(id) * p.rank + r0) * p.k * 2u;
     float sum[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll 4
-    for (uint32_t i = threadIdx.x; i < p.k / 8u; i += 128u) {
+    for (uint32_t i = WARPS == 1 ? lane : threadIdx.x; i < p.k / 8u; i += 32u * WARPS) {
         const uint4 xv = x[i];
         uint4 av[4];
 #pragma unroll
@@ -1409,13 +1410,17 @@ __device__ __forceinline__ float lora_dot4(const LoraFewParams &p, uint32_t row,
     for (int r = 0; r < 4; ++r)
 #pragma unroll
         for (int d = 16; d > 0; d >>= 1) sum[r] += __shfl_xor_sync(0xffffffffu, sum[r], d);
-    __syncthreads();  // the four before have been read
-    if (lane == 0)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) s_sum[warp][r] = sum[r];
-    __syncthreads();
     const uint32_t r = threadIdx.x & 3u;
-    return (s_sum[0][r] + s_sum[1][r]) + (s_sum[2][r] + s_sum[3][r]);
+    if constexpr (WARPS == 1) {
+        return r == 0u ? sum[0] : r == 1u ? sum[1] : r == 2u ? sum[2] : sum[3];
+    } else {
+        __syncthreads();  // the four before have been read
+        if (lane == 0)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) s_sum[warp][i] = sum[i];
+        __syncthreads();
+        return (s_sum[0][r] + s_sum[1][r]) + (s_sum[2][r] + s_sum[3][r]);
+    }
 }
 
 // 128 columns of a row's delta by one warp.  LANES lanes share a row of b, 16 bytes each, with their part of u in
@@ -1457,20 +1462,24 @@ __device__ __forceinline__ void lora_columns(const LoraFewParams &p, uint32_t ro
     }
 }
 
-// An item, a block's, is a row and four of its u's.
+// An item is a row and four of its u's: a block's (WARPS = 4), or, where there are more of them than the GPU has blocks at
+// a time, a warp's.
+template <int WARPS>
 __global__ void __launch_bounds__(128) lora_shrink_kernel(const __grid_constant__ LoraFewParams p)
 {
     __shared__ float s_sum[4][4];
     ptx::griddep_wait();
     // (after the wait: what the next kernels read from before this one is complete as well)
     ptx::griddep_launch_dependents();
+    constexpr uint32_t kItems = 4 / WARPS;  // of a block at a time
     const uint32_t parts = p.rank / 4u;
-    for (uint32_t item = blockIdx.x; item < p.rows * parts; item += gridDim.x) {
+    for (uint32_t item = blockIdx.x * kItems + (WARPS == 1 ? threadIdx.x >> 5 : 0u); item < p.rows * parts; item += gridDim.x * kItems) {
         const uint32_t row = item / parts, r0 = (item - row * parts) * 4u;
         const int32_t id = p.ids[row];
         if (uint32_t(id) >= p.adapters) continue;
-        const float v = lora_dot4(p, row, id, r0, s_sum) * (p.scale ? p.scale[id] : 1.0f);
-        if (threadIdx.x < 4u) p.u[size_t(row) * p.rank + r0 + threadIdx.x] = v;
+        const float v = lora_dot4<WARPS>(p, row, id, r0, s_sum) * (p.scale ? p.scale[id] : 1.0f);
+        const uint32_t t = WARPS == 1 ? threadIdx.x & 31u : threadIdx.x;
+        if (t < 4u) p.u[size_t(row) * p.rank + r0 + t] = v;
     }
 }
 
@@ -1508,7 +1517,7 @@ __global__ void __launch_bounds__(128) lora_rows_kernel(const __grid_constant__ 
     const int32_t id = p.ids[row];
     if (uint32_t(id) >= p.adapters) return;  // (the same for the whole cluster)
     for (uint32_t r0 = 4u * rank; r0 < p.rank; r0 += 4u * kLoraCluster) {
-        const float v = lora_dot4(p, row, id, r0, s_sum) * (p.scale ? p.scale[id] : 1.0f);
+        const float v = lora_dot4<4>(p, row, id, r0, s_sum) * (p.scale ? p.scale[id] : 1.0f);
         if (threadIdx.x < 4u * kLoraCluster)  // four values to every CTA
             ptx::st_shared_cluster_u32(ptx::map_to_rank(ptx::smem_addr(&s_u[r0 + (threadIdx.x & 3u)]), threadIdx.x >> 2),
                                        __float_as_uint(v));
