@@ -572,6 +572,14 @@ double lora_alone(int64_t rows, int64_t n, int64_t k, int64_t rank)
     return 2.0 * double(rows) * double(rank) * double(n + k) / 5e6;
 }
 
+// Rows whose items the adapters' two kernels can count: an item is four of a row's u's or 128 of its columns, and the 32-bit
+// number of the last one, a stride of the grid further (sixteen blocks of four items an SM at most), does not wrap.
+int64_t lora_beside_rows(int64_t n, int64_t rank)
+{
+    const int64_t each = rank / 4 > cdiv(n, 128) ? rank / 4 : cdiv(n, 128);
+    return ((int64_t(1) << 32) - (int64_t(1) << 20)) / (each < 1 ? 1 : each);
+}
+
 // Whether the adapters run row by row beside the projection.  On the tensor cores each row tile takes a K block per
 // adapter in it, 1.6 us of a worker's time each, after some 15 us of launches that depend on one another.  How many adapters
 // a tile of up to 256 rows has is in ids on the device: one where rows come in prompts, all where each row is a request
@@ -579,11 +587,13 @@ double lora_alone(int64_t rows, int64_t n, int64_t k, int64_t rank)
 // faster way on average where each row is a request and 5.7% where rows come in runs, at most 1.6 and 4.1 times; all adapters
 // cost 1.1% and 9.6%, at most 1.6 and 9.1 times (2489 rows of 10 prompts, 228 adapters of rank 72, 5776 x 2624: 952 us
 // beside, 104 on the tensor cores), their square root 4.3% and 2.7%, at most 4.1 and 1.5 times.
-bool lora_beside(const RaggedDevice *dev, int64_t rows, int64_t n, int64_t k, int64_t rank, int64_t adapters)
+// `pairs`: co-resident CTA pairs of the tensor cores' way.
+bool lora_beside(int pairs, int64_t rows, int64_t n, int64_t k, int64_t rank, int64_t adapters)
 {
+    if (rows > lora_beside_rows(n, rank)) return false;
     if (rows <= kRagged[kVNtFew].qcap) return true;
     const RaggedVariant &y = kRagged[kVLoraY];
-    const double waves = double(cdiv(n, 128 * y.cg)) * double(cdiv(rows, y.qcap)) / dev->slots[kVLoraY];
+    const double waves = double(cdiv(n, 128 * y.cg)) * double(cdiv(rows, y.qcap)) / pairs;
     const double blocks = pow(double(adapters < y.qcap ? adapters : y.qcap), 0.7) * double(cdiv(rank, kRagBlockK));
     return lora_alone(rows, n, k, rank) < 15.0 + (waves < 1.0 ? 1.0 : waves) * blocks * 1.6;
 }
@@ -645,7 +655,7 @@ LoraPlan lora_layout(const RaggedDevice *dev, int64_t rows, int64_t n, int64_t k
 
 LoraPlan lora_plan(const RaggedDevice *dev, int64_t rows, int64_t n, int64_t k, int64_t rank, int64_t adapters)
 {
-    return lora_layout(dev, rows, n, k, rank, lora_beside(dev, rows, n, k, rank, adapters));
+    return lora_layout(dev, rows, n, k, rank, lora_beside(dev->slots[kVLoraY], rows, n, k, rank, adapters));
 }
 
 // Bytes that serve any number of rows up to this one: the layout of the most rows that run beside the projection, that of
@@ -659,12 +669,13 @@ size_t lora_bytes(const RaggedDevice *dev, int64_t rows, int64_t n, int64_t k, i
         if (one > most) most = one;
     }
     // the limit of lora_beside is the same for all rows of a tile: the largest such row number of each tile, from the top
-    for (int64_t top = rows; top > 0; top = (top - 1) / tile * tile) {
+    const int64_t countable = lora_beside_rows(n, rank);
+    for (int64_t top = rows < countable ? rows : countable; top > 0; top = (top - 1) / tile * tile) {
         const int64_t low = (top - 1) / tile * tile;
         int64_t lo = low, hi = top;  // beside holds up to lo (or nowhere in this tile), not from hi + 1 on
         while (lo < hi) {
             const int64_t mid = lo + (hi - lo + 1) / 2;
-            if (lora_beside(dev, mid, n, k, rank, adapters)) lo = mid;
+            if (lora_beside(dev->slots[kVLoraY], mid, n, k, rank, adapters)) lo = mid;
             else hi = mid - 1;
         }
         if (lo > low) {
@@ -737,6 +748,23 @@ gemm_status_t gemm_lora_workspace_size(int64_t rows, int64_t n, int64_t k, int64
     st = ragged_device(&dev);
     if (st != GEMM_OK) return st;
     *bytes = rows ? lora_bytes(dev, rows, n, k, rank, adapters) : 0;
+    return GEMM_OK;
+}
+
+gemm_status_t gemm_lora_way(int64_t rows, int64_t n, int64_t k, int64_t rank, int64_t adapters, int32_t num_sms, int32_t *way)
+{
+    if (!way || num_sms < 0 || num_sms == 1) return GEMM_ERR_INVALID_ARG;
+    gemm_status_t st = check_sizes({rows, adapters}, {n, k, rank});
+    if (st != GEMM_OK) return st;
+    if (rank > GEMM_LORA_MAX_RANK) return GEMM_ERR_UNSUPPORTED_SHAPE;
+    int pairs = num_sms / 2;
+    if (num_sms == 0) {
+        RaggedDevice *dev = nullptr;
+        st = ragged_device(&dev);
+        if (st != GEMM_OK) return st;
+        pairs = dev->slots[kVLoraY];
+    }
+    *way = lora_beside(pairs, rows, n, k, rank, adapters) ? GEMM_LORA_BESIDE : GEMM_LORA_TENSOR_CORES;
     return GEMM_OK;
 }
 

@@ -1463,7 +1463,7 @@ __device__ __forceinline__ void lora_columns(const LoraFewParams &p, uint32_t ro
 }
 
 // An item is a row and four of its u's: a block's (WARPS = 4), or, where there are more of them than the GPU has blocks at
-// a time, a warp's.
+// a time, a warp's.  (Here and below items are counted in 32 bits: rows that have more go by the tensor cores.)
 template <int WARPS>
 __global__ void __launch_bounds__(128) lora_shrink_kernel(const __grid_constant__ LoraFewParams p)
 {

@@ -24,10 +24,13 @@ MAX_RANK = 128
 MAX_EXPERTS = 1024
 MAX_TOP = 32
 
+LORA_BESIDE = 0
+LORA_TENSOR_CORES = 1
+
 # every symbol the public header declares
 EXPORTED = [
     "gemm_grouped_workspace_size", "gemm_grouped_nt", "gemm_grouped_nn", "gemm_grouped_tn", "gemm_grouped_stall_test",
-    "gemm_lora_workspace_size", "gemm_lora_nt",
+    "gemm_lora_workspace_size", "gemm_lora_way", "gemm_lora_nt",
     "gemm_route_workspace_size", "gemm_route_topk", "gemm_route_topk_grad",
 ]
 
@@ -51,6 +54,7 @@ def lib():
         "gemm_grouped_tn": [dt, dt, i64, i64, i64, i64, vp, vp, vp, vp, vp, sz, vp],
         "gemm_grouped_stall_test": [i32, dt, i64, i64, i64, i64, vp, vp, vp, vp, vp, sz, u32, ctypes.c_longlong, vp],
         "gemm_lora_workspace_size": [i64, i64, i64, i64, i64, psz],
+        "gemm_lora_way": [i64, i64, i64, i64, i64, i32, ctypes.POINTER(i32)],
         "gemm_lora_nt": [dt, i64, i64, i64, i64, i64, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp],
         "gemm_route_workspace_size": [i64, i64, i64, psz],
         "gemm_route_topk": [dt, i64, i64, i64, i32, vp, vp, vp, vp, vp, vp, vp, sz, vp],
@@ -226,6 +230,13 @@ def gemm_grouped_stall_test(mode, first, second, offsets, out, workspace, skip_f
 
 def gemm_lora_workspace_size(rows, n, k, rank, adapters):
     return _size("gemm_lora_workspace_size", rows, n, k, rank, adapters)
+
+
+def gemm_lora_way(rows, n, k, rank, adapters, num_sms=0):
+    """LORA_BESIDE or LORA_TENSOR_CORES: how a call of these sizes runs, on the current device or on one of `num_sms` SMs."""
+    way = ctypes.c_int32()
+    _check(lib().gemm_lora_way(rows, n, k, rank, adapters, num_sms, ctypes.byref(way)), "gemm_lora_way")
+    return way.value
 
 
 def gemm_lora_nt(x, w, a, b, ids, scale=None, y=None, workspace=None, stream=None):

@@ -101,6 +101,10 @@ gemm_status_t gemm_grouped_tn(gemm_dtype_t dtype, gemm_dtype_t out, int64_t grou
  * serve these sizes, or fewer rows, on the current device.
  */
 gemm_status_t gemm_lora_workspace_size(int64_t rows, int64_t n, int64_t k, int64_t rank, int64_t adapters, size_t *bytes);
+/* Which way a call of these sizes takes: row by row beside the projection, or as K blocks of it on the tensor cores.  For
+ * the current device (num_sms 0), or, without touching one, for a device of num_sms SMs and half as many CTA pairs. */
+enum { GEMM_LORA_BESIDE = 0, GEMM_LORA_TENSOR_CORES = 1 };
+gemm_status_t gemm_lora_way(int64_t rows, int64_t n, int64_t k, int64_t rank, int64_t adapters, int32_t num_sms, int32_t *way);
 gemm_status_t gemm_lora_nt(gemm_dtype_t dtype, int64_t rows, int64_t n, int64_t k, int64_t rank, int64_t adapters,
                            const void *x, const void *w, const void *a, const void *b, const int32_t *ids,
                            const float *scale, void *y, void *workspace, size_t ws_bytes, gemm_stream_t stream);
