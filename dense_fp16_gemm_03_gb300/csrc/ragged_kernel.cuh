@@ -57,7 +57,8 @@
 // block.  Workers walk their run backwards, so they publish first and wait last,
 // and only ever for lower-numbered workers, which start no later: launches that
 // share the GPU cannot hold each other up.  Sums are added in a fixed order:
-// results repeat bit for bit.  (Handing each next tile to the worker that comes
+// results repeat bit for bit.  Every flag is clear at the launch's end, also after
+// an abort, so a replay of a captured launch never finds one of the last.  (Handing each next tile to the worker that comes
 // for it first, by a counter, was measured for groups of unlike sizes: 388 us
 // against 380 in the case above, and one group 371 against 352: the number's way
 // through the roles costs more than the balance brings.)
@@ -137,8 +138,8 @@ struct RaggedParams {
     uint32_t whole_groups;   // launch, each with a matrix of its own in `out`; and the number of whole ones
     float *partials;         // sk: one 128 x QCAP fp32 tile per CTA
     uint64_t *flags;         // sk: one per CTA, `stamp` while its partial waits to be added
-    uint64_t stamp;
-    uint32_t skip_fill;      // test hook: ring fill of CTA 0 left undone (~0u: none)
+    uint64_t stamp;          // (its high word is the same for all launches, so its complements are no other launch's stamp)
+    uint32_t skip_fill;      // test hook: ring fill of CTA 0 left undone while the error word is clear (~0u: none)
     long long wait_limit;
     uint32_t *error_word;
 };
@@ -289,6 +290,31 @@ __device__ __forceinline__ void uniform(RaggedSeg &s)
     }
 }
 
+// The flag of a partial sum.  A launch captured in a graph comes again with the same stamp, so whatever happens in a launch,
+// its end finds the flag cleared: of the CTA that has the sum to publish and the one that takes it, each writes the flag
+// once, also where it gives up, and the one that comes second clears it.
+__device__ __forceinline__ uint64_t flag_given_up(uint64_t stamp)  // by the taker
+{
+    return ~stamp;
+}
+
+__device__ __forceinline__ uint64_t flag_not_coming(uint64_t stamp)  // by the publisher
+{
+    return stamp ^ (uint64_t(1) << 63);
+}
+
+// `v`: the stamp, or flag_not_coming.
+__device__ __forceinline__ void flag_publish(uint64_t *flag, uint64_t stamp, uint64_t v)
+{
+    if (ptx::exch_gpu_u64(flag, v) == flag_given_up(stamp)) ptx::st_release_gpu_u64(flag, 0u);
+}
+
+__device__ __forceinline__ void flag_give_up(uint64_t *flag, uint64_t stamp)
+{
+    const uint64_t old = ptx::exch_gpu_u64(flag, flag_given_up(stamp));
+    if (old == stamp || old == flag_not_coming(stamp)) ptx::st_release_gpu_u64(flag, 0u);
+}
+
 template <int MODE, int CG, int QCAP>
 struct RaggedWalk {
     const RaggedParams &p;
@@ -410,6 +436,26 @@ struct RaggedWalk {
     __device__ __forceinline__ uint32_t run_begin(uint32_t w) const
     {
         return w * run + min(w, longer);
+    }
+
+    // the first of the workers before this one that hold K blocks of the tile that starts at iteration `start`
+    __device__ __forceinline__ uint32_t first_of(uint32_t start) const
+    {
+        uint32_t w = worker;
+        while (w > 0u && run_begin(w) > start) --w;
+        return w;
+    }
+
+    // sk, run by one warp of a CTA that stops early: what it has neither published nor taken, and now never will
+    __device__ __forceinline__ void leave_flags(uint32_t rank, bool published, bool taken) const
+    {
+        const uint32_t lane = threadIdx.x & 31u, kb = tile_blocks;
+        const uint32_t begin = run_begin(worker), end = run_begin(worker + 1u);
+        const uint32_t start = begin / kb * kb;
+        if (!published && lane == 0 && end % kb != 0u)  // the run stops inside a tile
+            flag_publish(p.flags + worker * CG + rank, p.stamp, flag_not_coming(p.stamp));
+        if (!taken && begin != start && end - start >= kb)  // it holds the end, not the beginning of its lowest tile
+            for (uint32_t w = first_of(start) + lane; w < worker; w += 32u) flag_give_up(p.flags + w * CG + rank, p.stamp);
     }
 
     // f(seg) returns false to stop early (abort)
@@ -711,7 +757,7 @@ __global__ void __launch_bounds__(RaggedCfg<MODE, CG, QCAP, STAGES>::kThreads, 1
                     const bool extra = MODE == kLoraY && mix.step();  // adapter block: only P comes by TMA
                     if (!ragged_wait_warp<CG>(bar_empty(stage), phase ^ 1u, p, abort_flag, kRagErrEmpty)) return false;
                     const bool tail = extra || fixed_block(s, kb);    // to this CTA's own tail barrier
-                    if (elected && !(blockIdx.x == 0 && fills == p.skip_fill)) {
+                    if (elected && !(blockIdx.x == 0 && fills == p.skip_fill && ptx::ld_relaxed_gpu_u32(p.error_word) == 0u)) {
                         const uint32_t p_dst = base + Cfg::kOffP + stage * Cfg::kPBytes;
                         const uint32_t q_dst = base + Cfg::kOffQ + stage * Cfg::kQBytes;
                         const uint32_t bytes = Cfg::kPBytes + (extra ? 0u : q_bytes);
@@ -902,12 +948,16 @@ __global__ void __launch_bounds__(RaggedCfg<MODE, CG, QCAP, STAGES>::kThreads, 1
         uint32_t acc = 0, acc_phase = 0;
         uint32_t adapted = 0;  // kLoraY: segments with adapter blocks so far
         bool let_in = false;
+        bool published = false, taken = false, stopped = false;  // sk: this CTA's flags
         walk.template each<false>([&](const RaggedSeg &s) {
             const bool ok = ragged_wait<CG>(bar_acc_full(acc), acc_phase, p, abort_flag, kRagErrAccFull);
             const bool split = MODE != kTN && p.sk != 0u && (s.lo != 0u || s.hi != s.kb);
             // the warps meet at named barriers below when the tile is split: stop together
             if (MODE != kTN && p.sk) {
-                if (!ptx::named_barrier_and(1, 32 * Cfg::kEpiWarps, ok)) return false;
+                if (!ptx::named_barrier_and(1, 32 * Cfg::kEpiWarps, ok)) {
+                    stopped = true;
+                    return false;
+                }
             } else if (!__all_sync(0xffffffffu, ok)) {
                 return false;
             }
@@ -978,29 +1028,31 @@ __global__ void __launch_bounds__(RaggedCfg<MODE, CG, QCAP, STAGES>::kThreads, 1
                 release();
                 __threadfence();
                 ptx::named_barrier_sync(1, 32 * Cfg::kEpiWarps);
-                if (threadIdx.x == 64u) ptx::st_release_gpu_u64(p.flags + blockIdx.x, p.stamp);
+                if (threadIdx.x == 64u) flag_publish(p.flags + blockIdx.x, p.stamp, p.stamp);
+                published = true;
                 return true;
             }
             uint32_t w_lo = walk.worker;  // workers [w_lo, worker) hold the tile's earlier K blocks
             if (split) {
-                const uint32_t start = s.tile * s.kb;
-                while (w_lo > 0u && walk.run_begin(w_lo) > start) --w_lo;
+                w_lo = walk.first_of(s.tile * s.kb);
                 if (warp == 2u) {
                     for (uint32_t w = w_lo + lane; w < walk.worker; w += 32u) {
                         uint64_t *flag = p.flags + w * CG + rank;
                         const long long t0 = clock64();
-                        while (ptx::ld_acquire_gpu_u64(flag) != p.stamp) {
-                            if (*abort_flag || clock64() - t0 > p.wait_limit) {
+                        uint64_t v;
+                        while ((v = ptx::ld_acquire_gpu_u64(flag)) != p.stamp) {
+                            if (v == flag_not_coming(p.stamp) || *abort_flag || clock64() - t0 > p.wait_limit) {
                                 *abort_flag = 1u;
                                 atomicCAS(p.error_word, 0u, kRagErrPartial | (blockIdx.x << 8));
                                 break;
                             }
                         }
-                        // taken: a launch captured in a graph comes again with the same stamp
-                        ptx::st_release_gpu_u64(flag, 0u);
+                        if (v == p.stamp) ptx::st_release_gpu_u64(flag, 0u);
+                        else flag_give_up(flag, p.stamp);
                     }
                     __syncwarp();
                 }
+                taken = true;
                 ptx::named_barrier_sync(1, 32 * Cfg::kEpiWarps);
             }
             // 32 columns of the finished tile: the accumulator plus the other workers' partials, lowest first,
@@ -1124,6 +1176,7 @@ __global__ void __launch_bounds__(RaggedCfg<MODE, CG, QCAP, STAGES>::kThreads, 1
             return true;
         });
         if (MODE == kTN && lane == 0) ptx::bulk_wait_group<0>();
+        if (MODE != kTN && stopped && warp == 2u) walk.leave_flags(rank, published, taken);
     } else if constexpr (Cfg::kHelper) {
         // ------------------------------------------------ helper
         // Four warps that share a stage's rows and never wait for each other: `fixed` counts them all.

@@ -24,7 +24,7 @@
  *
  * Workspaces are the caller's, 256-byte aligned, of any contents; calls that
  * share one must not overlap on the GPU.  One left over from an aborted launch
- * (GEMM_ERR_TIMEOUT) serves again.  A pipeline wait that runs past its limit is
+ * (GEMM_ERR_TIMEOUT) serves again, replays of that launch from a graph included.  A pipeline wait that runs past its limit is
  * reported by gemm_f16_take_device_error as for the dense product.
  */
 #ifndef GEMM_RAGGED_H_
@@ -142,7 +142,9 @@ gemm_status_t gemm_route_topk_grad(gemm_dtype_t dtype, int64_t rows, int64_t exp
  * Failure-detection hook for tests, as gemm_f16_nt_run_stall_test: `mode` 0, 1, 2
  * runs gemm_grouped_nt, _nn or _tn (first and second the two operands in that
  * order; tn writes the operands' type) with ring fill `skip_fill` of CTA 0 left
- * undone and waits limited to `wait_limit_cycles`.  No fault, trap or hang.
+ * undone while the device error word is clear, and waits limited to
+ * `wait_limit_cycles`: captured in a graph, a first replay is aborted and the
+ * next, before the error is taken, runs through.  No fault, trap or hang.
  */
 gemm_status_t gemm_grouped_stall_test(int32_t mode, gemm_dtype_t dtype, int64_t groups, int64_t rows, int64_t n, int64_t k,
                                       const int32_t *offsets, const void *first, const void *second, void *out,
