@@ -687,6 +687,199 @@ size_t lora_bytes(const RaggedDevice *dev, int64_t rows, int64_t n, int64_t k, i
     return most;
 }
 
+// `skip_fill`: of the product that writes y.
+gemm_status_t lora(gemm_dtype_t dtype, int64_t rows, int64_t n, int64_t k, int64_t rank, int64_t adapters, const void *x,
+                   const void *w, const void *a, const void *b, const int32_t *ids, const float *scale, void *y,
+                   void *workspace, size_t ws_bytes, uint32_t skip_fill, long long wait_limit, cudaStream_t s)
+{
+    gemm_status_t st = check_sizes({rows, adapters}, {n, k, rank});
+    if (st != GEMM_OK) return st;
+    if (!operand_type(dtype)) return GEMM_ERR_INVALID_ARG;
+    if (rank > GEMM_LORA_MAX_RANK) return GEMM_ERR_UNSUPPORTED_SHAPE;
+    const bool any = rows > 0 && n > 0;
+    const bool adapted = any && k > 0 && adapters > 0 && rank > 0;
+    st = check_pointer(y, any);
+    if (st == GEMM_OK) st = check_pointer(x, any && k > 0);
+    if (st == GEMM_OK) st = check_pointer(w, any && k > 0);
+    if (st == GEMM_OK) st = check_pointer(a, adapted);
+    if (st == GEMM_OK) st = check_pointer(b, adapted);
+    if (st == GEMM_OK) st = check_pointer(ids, adapted, 4);
+    if (st == GEMM_OK && scale) st = check_pointer(scale, adapted, 4);
+    if (st != GEMM_OK) return st;
+    if (!any) return GEMM_OK;
+    RaggedDevice *dev = nullptr;
+    st = ragged_device(&dev);
+    if (st != GEMM_OK) return st;
+    const LoraPlan l = lora_plan(dev, rows, n, k, rank, adapters);
+    if (workspace == nullptr || ws_bytes < l.total) return GEMM_ERR_WORKSPACE;
+    if (reinterpret_cast<uintptr_t>(workspace) & 255u) return GEMM_ERR_ALIGNMENT;
+    if (k == 0) {
+        if (cudaMemsetAsync(y, 0, size_t(rows) * size_t(n) * 2u, s) != cudaSuccess) {
+            cudaGetLastError();
+            return GEMM_ERR_LAUNCH;
+        }
+        return GEMM_OK;
+    }
+    char *ws = static_cast<char *>(workspace);
+    if (l.beside) {
+        RaggedParams p;
+        memset(&p, 0, sizeof(p));
+        p.groups = 1;
+        p.rows = uint32_t(rows);
+        p.pdim = uint32_t(n);
+        p.kdim = uint32_t(k);
+        p.k_blocks = uint32_t(cdiv(k, kRagBlockK));
+        const RaggedVariant &vy = kRagged[l.variant_y];
+        p.tiles_p = uint32_t(cdiv(n, 128 * vy.cg));
+        p.bf16 = dtype == GEMM_DTYPE_BF16;
+        p.out = y;
+        p.skip_fill = skip_fill;
+        p.wait_limit = wait_limit ? wait_limit : wait_limit_for(p.k_blocks);
+        st = encode_stack(&p.tm_p, w, dtype, 1, n, k, kRagBlockK, 128);
+        if (st == GEMM_OK) st = encode_rows(p.tm_q, x, dtype, rows, k, vy.qbox);
+        if (st != GEMM_OK) return st;
+        if (adapted) {
+            LoraFewParams f;
+            f.x = x;
+            f.a = a;
+            f.b = b;
+            f.ids = ids;
+            f.scale = scale;
+            f.u = reinterpret_cast<float *>(ws + l.u);
+            f.delta = reinterpret_cast<float *>(ws + l.delta);
+            f.rows = uint32_t(rows);
+            f.n = uint32_t(n);
+            f.k = uint32_t(k);
+            f.rank = uint32_t(rank);
+            f.adapters = uint32_t(adapters);
+            f.bf16 = p.bf16;
+            void *args[1] = {&f};
+            const int64_t room = dev->num_sms;
+            if (rows <= kLoraRowsRows && rank <= kLoraRowsRank) {
+                st = launch(lora_rows_instance(rank), dim3(unsigned(rows * kLoraCluster), 1, 1), 128, 0, kLoraCluster,
+                            args, s);
+                if (st != GEMM_OK) return st;
+            } else {
+                // Few blocks on an SM where the product takes every SM's first CTA (64 rows with 64 adapters of rank 16,
+                // 8192 x 4096: four and two 28.6 us, eight and four 30.5, one and two 33.5) or is the longer part, more where
+                // its CTAs leave room (2749 rows, 17 adapters of rank 32, 160 x 216: 28.8 us, sixteen and eight 20.2; 139
+                // rows, 3544 x 448: 16.9 and 13.7).  Warps for items where eight blocks an SM would not hold them (913 rows,
+                // 208 x 304, rank 48: 33.2 us by blocks, 23.0 by warps; but 1024 items of 8192 x 4096 44.4 and 53.0).
+                const bool roomy = !l.split_y && vy.cg == 1;
+                const int64_t shrink = rows * (rank / 4), expand = cdiv(rows * cdiv(n, 128), 4);
+                const bool warps = shrink > 8 * room;
+                const int64_t most_shrink = (roomy ? 16 : 4) * room, most_expand = (roomy ? 8 : 2) * room;
+                const int64_t blocks = warps ? cdiv(shrink, 4) : shrink;
+                st = launch(warps ? reinterpret_cast<const void *>(&lora_shrink_kernel<1>)
+                                  : reinterpret_cast<const void *>(&lora_shrink_kernel<4>),
+                            dim3(unsigned(blocks < most_shrink ? blocks : most_shrink), 1, 1), 128, 0, 1, args, s);
+                if (st != GEMM_OK) return st;
+                st = launch(lora_expand_instance(rank), dim3(unsigned(expand < most_expand ? expand : most_expand), 1, 1), 128,
+                            0, 1, args, s);
+                if (st != GEMM_OK) return st;
+            }
+            p.delta = f.delta;
+            p.ids = ids;
+            p.adapters = f.adapters;
+        }
+        int64_t most = most_tiles(vy, 1, rows, n);
+        if (most >= kSizeLimit) return GEMM_ERR_UNSUPPORTED_SHAPE;
+        if (l.split_y && most * p.k_blocks < kIterLimit) {
+            use_split(&p, vy, dev->slots[l.variant_y], ws + l.split);
+            most *= p.k_blocks;
+        }
+        return launch_ragged(l.variant_y, dev, p, most, s);
+    }
+    const RaggedVariant &vu = kRagged[kVLoraU], &vy = kRagged[l.variant_y];
+
+    RaggedParams u, p;
+    memset(&u, 0, sizeof(u));
+    u.kdim = uint32_t(k);
+    u.k_blocks = uint32_t(cdiv(k, kRagBlockK));
+    u.bf16 = dtype == GEMM_DTYPE_BF16;
+    u.scale = scale;
+    u.adapters = adapted ? uint32_t(adapters) : 0u;
+    u.rank = uint32_t(rank);
+    u.rank_blocks = uint32_t(cdiv(rank, kRagBlockK));
+    u.skip_fill = ~0u;
+    u.wait_limit = wait_limit ? wait_limit : wait_limit_for(cdiv(k, kRagBlockK) + 4096);
+    p = u;
+    p.skip_fill = skip_fill;
+    // y = x w^T + u b^T
+    p.pdim = uint32_t(n);
+    p.tiles_p = uint32_t(cdiv(n, 128 * vy.cg));
+    p.per = uint32_t(l.per);
+    p.u = ws + l.u;
+    st = encode_stack(&p.tm_p, w, dtype, 1, n, k, kRagBlockK, 128);
+    if (st == GEMM_OK && adapted) st = encode_stack(&p.tm_x, b, dtype, adapters, n, rank, kRagBlockK, 128);
+    if (!adapted) p.tm_x = p.tm_p;  // (never loaded from)
+    // u = scale x a^T for many rows: one tile per row tile and adapter in it
+    if (adapted) {
+        u.pdim = uint32_t(rank);
+        u.tiles_p = 1;
+        u.per = uint32_t(kLoraURows);
+        u.out = ws + l.u;
+        if (st == GEMM_OK) st = encode_stack(&u.tm_p, a, dtype, adapters, rank, k, kRagBlockK, 128);
+    }
+    if (st != GEMM_OK) return st;
+    if (int64_t(p.tiles_p) * l.tiles >= kSizeLimit) return GEMM_ERR_UNSUPPORTED_SHAPE;
+
+    for (int64_t r0 = 0; r0 < rows; r0 += l.pass_rows) {
+        const int64_t r = rows - r0 < l.pass_rows ? rows - r0 : l.pass_rows;
+        const int64_t tiles = cdiv(r, l.per);
+        const char *xr = static_cast<const char *>(x) + size_t(r0) * size_t(k) * 2u;
+        const int32_t *idr = adapted ? ids + r0 : nullptr;
+        p.groups = uint32_t(tiles);
+        p.tiles_q = uint32_t(tiles);
+        p.rows = uint32_t(r);
+        p.ids = idr;
+        p.out = static_cast<char *>(y) + size_t(r0) * size_t(n) * 2u;
+        st = encode_rows(p.tm_q, xr, dtype, r, k, vy.qbox);
+        if (st != GEMM_OK) return st;
+        {
+            const int64_t tiles_u = adapted ? cdiv(r, kLoraURows) : 0;
+            LoraListParams lp;
+            lp.ids = idr;
+            lp.rows = uint32_t(r);
+            lp.adapters = u.adapters;
+            lp.tiles = uint32_t(tiles);
+            lp.per[0] = uint32_t(l.per);
+            lp.per[1] = uint32_t(kLoraURows);
+            lp.counts[0] = reinterpret_cast<int32_t *>(ws + l.counts);
+            lp.counts[1] = reinterpret_cast<int32_t *>(ws + l.counts_u);
+            lp.list[0] = reinterpret_cast<int32_t *>(ws + l.list);
+            lp.list[1] = reinterpret_cast<int32_t *>(ws + l.list_u);
+            void *args[1] = {&lp};
+            st = launch(reinterpret_cast<const void *>(&lora_list_kernel), dim3(unsigned(tiles + tiles_u), 1, 1), 256, 0, 1, args, s);
+            if (st != GEMM_OK) return st;
+            p.counts = reinterpret_cast<int32_t *>(ws + l.counts);
+            p.list = reinterpret_cast<int32_t *>(ws + l.list);
+            if (adapted) {
+                u.counts = reinterpret_cast<int32_t *>(ws + l.counts_u);
+                u.list = reinterpret_cast<int32_t *>(ws + l.list_u);
+                u.groups = uint32_t(tiles_u);
+                u.rows = uint32_t(r);
+                u.ids = idr;
+                st = encode_rows(u.tm_q, xr, dtype, r, k, vu.qbox);
+                if (st != GEMM_OK) return st;
+                u.sk = 0;
+                if (r * int64_t(u.k_blocks) < kIterLimit) use_split(&u, vu, dev->slots[kVLoraU], ws + l.split);
+                st = launch_ragged(kVLoraU, dev, u, r * int64_t(u.k_blocks), s);
+                if (st != GEMM_OK) return st;
+            }
+        }
+        int64_t most = int64_t(p.tiles_p) * tiles;
+        p.sk = 0;
+        if (l.tiles == 1 && most * (p.k_blocks + l.per * p.rank_blocks) < kIterLimit) {
+            use_split(&p, vy, dev->slots[l.variant_y], ws + l.split);
+            most *= p.k_blocks;
+        }
+        st = launch_ragged(l.variant_y, dev, p, most, s);
+        if (st != GEMM_OK) return st;
+    }
+    return GEMM_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -772,192 +965,18 @@ gemm_status_t gemm_lora_nt(gemm_dtype_t dtype, int64_t rows, int64_t n, int64_t 
                            const void *x, const void *w, const void *a, const void *b, const int32_t *ids, const float *scale,
                            void *y, void *workspace, size_t ws_bytes, gemm_stream_t stream)
 {
-    gemm_status_t st = check_sizes({rows, adapters}, {n, k, rank});
-    if (st != GEMM_OK) return st;
-    if (!operand_type(dtype)) return GEMM_ERR_INVALID_ARG;
-    if (rank > GEMM_LORA_MAX_RANK) return GEMM_ERR_UNSUPPORTED_SHAPE;
-    const bool any = rows > 0 && n > 0;
-    const bool adapted = any && k > 0 && adapters > 0 && rank > 0;
-    st = check_pointer(y, any);
-    if (st == GEMM_OK) st = check_pointer(x, any && k > 0);
-    if (st == GEMM_OK) st = check_pointer(w, any && k > 0);
-    if (st == GEMM_OK) st = check_pointer(a, adapted);
-    if (st == GEMM_OK) st = check_pointer(b, adapted);
-    if (st == GEMM_OK) st = check_pointer(ids, adapted, 4);
-    if (st == GEMM_OK && scale) st = check_pointer(scale, adapted, 4);
-    if (st != GEMM_OK) return st;
-    if (!any) return GEMM_OK;
-    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    RaggedDevice *dev = nullptr;
-    st = ragged_device(&dev);
-    if (st != GEMM_OK) return st;
-    const LoraPlan l = lora_plan(dev, rows, n, k, rank, adapters);
-    if (workspace == nullptr || ws_bytes < l.total) return GEMM_ERR_WORKSPACE;
-    if (reinterpret_cast<uintptr_t>(workspace) & 255u) return GEMM_ERR_ALIGNMENT;
-    if (k == 0) {
-        if (cudaMemsetAsync(y, 0, size_t(rows) * size_t(n) * 2u, s) != cudaSuccess) {
-            cudaGetLastError();
-            return GEMM_ERR_LAUNCH;
-        }
-        return GEMM_OK;
-    }
-    char *ws = static_cast<char *>(workspace);
-    if (l.beside) {
-        RaggedParams p;
-        memset(&p, 0, sizeof(p));
-        p.groups = 1;
-        p.rows = uint32_t(rows);
-        p.pdim = uint32_t(n);
-        p.kdim = uint32_t(k);
-        p.k_blocks = uint32_t(cdiv(k, kRagBlockK));
-        const RaggedVariant &vy = kRagged[l.variant_y];
-        p.tiles_p = uint32_t(cdiv(n, 128 * vy.cg));
-        p.bf16 = dtype == GEMM_DTYPE_BF16;
-        p.out = y;
-        p.skip_fill = ~0u;
-        p.wait_limit = wait_limit_for(p.k_blocks);
-        st = encode_stack(&p.tm_p, w, dtype, 1, n, k, kRagBlockK, 128);
-        if (st == GEMM_OK) st = encode_rows(p.tm_q, x, dtype, rows, k, vy.qbox);
-        if (st != GEMM_OK) return st;
-        if (adapted) {
-            LoraFewParams f;
-            f.x = x;
-            f.a = a;
-            f.b = b;
-            f.ids = ids;
-            f.scale = scale;
-            f.u = reinterpret_cast<float *>(ws + l.u);
-            f.delta = reinterpret_cast<float *>(ws + l.delta);
-            f.rows = uint32_t(rows);
-            f.n = uint32_t(n);
-            f.k = uint32_t(k);
-            f.rank = uint32_t(rank);
-            f.adapters = uint32_t(adapters);
-            f.bf16 = p.bf16;
-            void *args[1] = {&f};
-            const int64_t room = dev->num_sms;
-            if (rows <= kLoraRowsRows && rank <= kLoraRowsRank) {
-                st = launch(lora_rows_instance(rank), dim3(unsigned(rows * kLoraCluster), 1, 1), 128, 0, kLoraCluster,
-                            args, s);
-                if (st != GEMM_OK) return st;
-            } else {
-                // Few blocks on an SM where the product takes every SM's first CTA (64 rows with 64 adapters of rank 16,
-                // 8192 x 4096: four and two 28.6 us, eight and four 30.5, one and two 33.5) or is the longer part, more where
-                // its CTAs leave room (2749 rows, 17 adapters of rank 32, 160 x 216: 28.8 us, sixteen and eight 20.2; 139
-                // rows, 3544 x 448: 16.9 and 13.7).  Warps for items where eight blocks an SM would not hold them (913 rows,
-                // 208 x 304, rank 48: 33.2 us by blocks, 23.0 by warps; but 1024 items of 8192 x 4096 44.4 and 53.0).
-                const bool roomy = !l.split_y && vy.cg == 1;
-                const int64_t shrink = rows * (rank / 4), expand = cdiv(rows * cdiv(n, 128), 4);
-                const bool warps = shrink > 8 * room;
-                const int64_t most_shrink = (roomy ? 16 : 4) * room, most_expand = (roomy ? 8 : 2) * room;
-                const int64_t blocks = warps ? cdiv(shrink, 4) : shrink;
-                st = launch(warps ? reinterpret_cast<const void *>(&lora_shrink_kernel<1>)
-                                  : reinterpret_cast<const void *>(&lora_shrink_kernel<4>),
-                            dim3(unsigned(blocks < most_shrink ? blocks : most_shrink), 1, 1), 128, 0, 1, args, s);
-                if (st != GEMM_OK) return st;
-                st = launch(lora_expand_instance(rank), dim3(unsigned(expand < most_expand ? expand : most_expand), 1, 1), 128,
-                            0, 1, args, s);
-                if (st != GEMM_OK) return st;
-            }
-            p.delta = f.delta;
-            p.ids = ids;
-            p.adapters = f.adapters;
-        }
-        int64_t most = most_tiles(vy, 1, rows, n);
-        if (most >= kSizeLimit) return GEMM_ERR_UNSUPPORTED_SHAPE;
-        if (l.split_y && most * p.k_blocks < kIterLimit) {
-            use_split(&p, vy, dev->slots[l.variant_y], ws + l.split);
-            most *= p.k_blocks;
-        }
-        return launch_ragged(l.variant_y, dev, p, most, s);
-    }
-    const RaggedVariant &vu = kRagged[kVLoraU], &vy = kRagged[l.variant_y];
+    return lora(dtype, rows, n, k, rank, adapters, x, w, a, b, ids, scale, y, workspace, ws_bytes, ~0u, 0,
+                reinterpret_cast<cudaStream_t>(stream));
+}
 
-    RaggedParams u, p;
-    memset(&u, 0, sizeof(u));
-    u.kdim = uint32_t(k);
-    u.k_blocks = uint32_t(cdiv(k, kRagBlockK));
-    u.bf16 = dtype == GEMM_DTYPE_BF16;
-    u.scale = scale;
-    u.adapters = adapted ? uint32_t(adapters) : 0u;
-    u.rank = uint32_t(rank);
-    u.rank_blocks = uint32_t(cdiv(rank, kRagBlockK));
-    u.skip_fill = ~0u;
-    u.wait_limit = wait_limit_for(cdiv(k, kRagBlockK) + 4096);
-    p = u;
-    // y = x w^T + u b^T
-    p.pdim = uint32_t(n);
-    p.tiles_p = uint32_t(cdiv(n, 128 * vy.cg));
-    p.per = uint32_t(l.per);
-    p.u = ws + l.u;
-    st = encode_stack(&p.tm_p, w, dtype, 1, n, k, kRagBlockK, 128);
-    if (st == GEMM_OK && adapted) st = encode_stack(&p.tm_x, b, dtype, adapters, n, rank, kRagBlockK, 128);
-    if (!adapted) p.tm_x = p.tm_p;  // (never loaded from)
-    // u = scale x a^T for many rows: one tile per row tile and adapter in it
-    if (adapted) {
-        u.pdim = uint32_t(rank);
-        u.tiles_p = 1;
-        u.per = uint32_t(kLoraURows);
-        u.out = ws + l.u;
-        if (st == GEMM_OK) st = encode_stack(&u.tm_p, a, dtype, adapters, rank, k, kRagBlockK, 128);
-    }
-    if (st != GEMM_OK) return st;
-    if (int64_t(p.tiles_p) * l.tiles >= kSizeLimit) return GEMM_ERR_UNSUPPORTED_SHAPE;
-
-    for (int64_t r0 = 0; r0 < rows; r0 += l.pass_rows) {
-        const int64_t r = rows - r0 < l.pass_rows ? rows - r0 : l.pass_rows;
-        const int64_t tiles = cdiv(r, l.per);
-        const char *xr = static_cast<const char *>(x) + size_t(r0) * size_t(k) * 2u;
-        const int32_t *idr = adapted ? ids + r0 : nullptr;
-        p.groups = uint32_t(tiles);
-        p.tiles_q = uint32_t(tiles);
-        p.rows = uint32_t(r);
-        p.ids = idr;
-        p.out = static_cast<char *>(y) + size_t(r0) * size_t(n) * 2u;
-        st = encode_rows(p.tm_q, xr, dtype, r, k, vy.qbox);
-        if (st != GEMM_OK) return st;
-        {
-            const int64_t tiles_u = adapted ? cdiv(r, kLoraURows) : 0;
-            LoraListParams lp;
-            lp.ids = idr;
-            lp.rows = uint32_t(r);
-            lp.adapters = u.adapters;
-            lp.tiles = uint32_t(tiles);
-            lp.per[0] = uint32_t(l.per);
-            lp.per[1] = uint32_t(kLoraURows);
-            lp.counts[0] = reinterpret_cast<int32_t *>(ws + l.counts);
-            lp.counts[1] = reinterpret_cast<int32_t *>(ws + l.counts_u);
-            lp.list[0] = reinterpret_cast<int32_t *>(ws + l.list);
-            lp.list[1] = reinterpret_cast<int32_t *>(ws + l.list_u);
-            void *args[1] = {&lp};
-            st = launch(reinterpret_cast<const void *>(&lora_list_kernel), dim3(unsigned(tiles + tiles_u), 1, 1), 256, 0, 1, args, s);
-            if (st != GEMM_OK) return st;
-            p.counts = reinterpret_cast<int32_t *>(ws + l.counts);
-            p.list = reinterpret_cast<int32_t *>(ws + l.list);
-            if (adapted) {
-                u.counts = reinterpret_cast<int32_t *>(ws + l.counts_u);
-                u.list = reinterpret_cast<int32_t *>(ws + l.list_u);
-                u.groups = uint32_t(tiles_u);
-                u.rows = uint32_t(r);
-                u.ids = idr;
-                st = encode_rows(u.tm_q, xr, dtype, r, k, vu.qbox);
-                if (st != GEMM_OK) return st;
-                u.sk = 0;
-                if (r * int64_t(u.k_blocks) < kIterLimit) use_split(&u, vu, dev->slots[kVLoraU], ws + l.split);
-                st = launch_ragged(kVLoraU, dev, u, r * int64_t(u.k_blocks), s);
-                if (st != GEMM_OK) return st;
-            }
-        }
-        int64_t most = int64_t(p.tiles_p) * tiles;
-        p.sk = 0;
-        if (l.tiles == 1 && most * (p.k_blocks + l.per * p.rank_blocks) < kIterLimit) {
-            use_split(&p, vy, dev->slots[l.variant_y], ws + l.split);
-            most *= p.k_blocks;
-        }
-        st = launch_ragged(l.variant_y, dev, p, most, s);
-        if (st != GEMM_OK) return st;
-    }
-    return GEMM_OK;
+gemm_status_t gemm_lora_stall_test(gemm_dtype_t dtype, int64_t rows, int64_t n, int64_t k, int64_t rank, int64_t adapters,
+                                   const void *x, const void *w, const void *a, const void *b, const int32_t *ids,
+                                   const float *scale, void *y, void *workspace, size_t ws_bytes, uint32_t skip_fill,
+                                   long long wait_limit_cycles, gemm_stream_t stream)
+{
+    if (wait_limit_cycles <= 0) return GEMM_ERR_INVALID_ARG;
+    return lora(dtype, rows, n, k, rank, adapters, x, w, a, b, ids, scale, y, workspace, ws_bytes, skip_fill, wait_limit_cycles,
+                reinterpret_cast<cudaStream_t>(stream));
 }
 
 // --------------------------------------------------------------- router

@@ -30,7 +30,7 @@ LORA_TENSOR_CORES = 1
 # every symbol the public header declares
 EXPORTED = [
     "gemm_grouped_workspace_size", "gemm_grouped_nt", "gemm_grouped_nn", "gemm_grouped_tn", "gemm_grouped_stall_test",
-    "gemm_lora_workspace_size", "gemm_lora_way", "gemm_lora_nt",
+    "gemm_lora_workspace_size", "gemm_lora_way", "gemm_lora_nt", "gemm_lora_stall_test",
     "gemm_route_workspace_size", "gemm_route_topk", "gemm_route_topk_grad",
 ]
 
@@ -56,6 +56,7 @@ def lib():
         "gemm_lora_workspace_size": [i64, i64, i64, i64, i64, psz],
         "gemm_lora_way": [i64, i64, i64, i64, i64, i32, ctypes.POINTER(i32)],
         "gemm_lora_nt": [dt, i64, i64, i64, i64, i64, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp],
+        "gemm_lora_stall_test": [dt, i64, i64, i64, i64, i64, vp, vp, vp, vp, vp, vp, vp, vp, sz, u32, ctypes.c_longlong, vp],
         "gemm_route_workspace_size": [i64, i64, i64, psz],
         "gemm_route_topk": [dt, i64, i64, i64, i32, vp, vp, vp, vp, vp, vp, vp, sz, vp],
         "gemm_route_topk_grad": [dt, i64, i64, i64, i32, vp, vp, vp, vp, vp, vp],
@@ -239,11 +240,8 @@ def gemm_lora_way(rows, n, k, rank, adapters, num_sms=0):
     return way.value
 
 
-def gemm_lora_nt(x, w, a, b, ids, scale=None, y=None, workspace=None, stream=None):
-    """y[t] = x[t] . w^T + scale[i] (x[t] . a[i]^T) . b[i]^T with i = ids[t]; no adapter where ids[t] is not in [0, adapters).
-
-    x [rows, k], w [n, k], a [adapters, rank, k], b [adapters, n, rank], ids [rows] int32, scale [adapters] float32 or
-    None for 1; returns y [rows, n].  The workspace (gemm_lora_workspace_size) is required."""
+def _lora_sizes(x, w, a, b, ids, scale):
+    """Device number, rows, n, k, rank and adapters of a call, its operands checked."""
     torch = _gemm._tm()
     dev, kind = _operand(x, "x", 2), x.dtype
     rows, k = x.shape
@@ -257,6 +255,16 @@ def gemm_lora_nt(x, w, a, b, ids, scale=None, y=None, workspace=None, stream=Non
     _need(ids, "ids", (rows,), torch.int32, dev)
     if scale is not None:
         _need(scale, "scale", (adapters,), torch.float32, dev)
+    return dev, rows, n, k, rank, adapters
+
+
+def gemm_lora_nt(x, w, a, b, ids, scale=None, y=None, workspace=None, stream=None):
+    """y[t] = x[t] . w^T + scale[i] (x[t] . a[i]^T) . b[i]^T with i = ids[t]; no adapter where ids[t] is not in [0, adapters).
+
+    x [rows, k], w [n, k], a [adapters, rank, k], b [adapters, n, rank], ids [rows] int32, scale [adapters] float32 or
+    None for 1; returns y [rows, n].  The workspace (gemm_lora_workspace_size) is required."""
+    dev, rows, n, k, rank, adapters = _lora_sizes(x, w, a, b, ids, scale)
+    kind = x.dtype
     code = _dtype(kind)
     y = _out(y, "y", (rows, n), kind, dev)
     ws, ws_bytes = _workspace(workspace, dev)
@@ -265,6 +273,16 @@ def gemm_lora_nt(x, w, a, b, ids, scale=None, y=None, workspace=None, stream=Non
                             _stream(stream, dev))
     _check(st, "gemm_lora_nt")
     return y
+
+
+def gemm_lora_stall_test(x, w, a, b, ids, y, workspace, skip_fill, wait_limit_cycles, scale=None, stream=None):
+    """Status of the failure-detection launch."""
+    dev, rows, n, k, rank, adapters = _lora_sizes(x, w, a, b, ids, scale)
+    _need(y, "y", (rows, n), x.dtype, dev)
+    ws, ws_bytes = _workspace(workspace, dev)
+    return lib().gemm_lora_stall_test(_dtype(x.dtype), rows, n, k, rank, adapters, x.data_ptr(), w.data_ptr(), a.data_ptr(),
+                                      b.data_ptr(), ids.data_ptr(), None if scale is None else scale.data_ptr(), y.data_ptr(),
+                                      ws, ws_bytes, skip_fill, wait_limit_cycles, _stream(stream, dev))
 
 
 # --------------------------------------------------------------------- router

@@ -150,6 +150,11 @@ gemm_status_t gemm_grouped_stall_test(int32_t mode, gemm_dtype_t dtype, int64_t 
                                       const int32_t *offsets, const void *first, const void *second, void *out,
                                       void *workspace, size_t ws_bytes, uint32_t skip_fill, long long wait_limit_cycles,
                                       gemm_stream_t stream);
+/* The same of gemm_lora_nt: a fill of the product that writes y. */
+gemm_status_t gemm_lora_stall_test(gemm_dtype_t dtype, int64_t rows, int64_t n, int64_t k, int64_t rank, int64_t adapters,
+                                   const void *x, const void *w, const void *a, const void *b, const int32_t *ids,
+                                   const float *scale, void *y, void *workspace, size_t ws_bytes, uint32_t skip_fill,
+                                   long long wait_limit_cycles, gemm_stream_t stream);
 
 #ifdef __cplusplus
 }
