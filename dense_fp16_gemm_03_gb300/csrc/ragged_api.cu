@@ -580,13 +580,13 @@ int64_t lora_beside_rows(int64_t n, int64_t rank)
     return ((int64_t(1) << 32) - (int64_t(1) << 20)) / (each < 1 ? 1 : each);
 }
 
-// Whether the adapters run row by row beside the projection.  On the tensor cores each row tile takes a K block per
-// adapter in it, 1.6 us of a worker's time each, after some 15 us of launches that depend on one another.  How many adapters
-// a tile of up to 256 rows has is in ids on the device: one where rows come in prompts, all where each row is a request
-// of its own.  (adapters)^0.7 stands between: over 283 launches of random sizes, 65 to 16000 rows, it costs 1.4% over the
-// faster way on average where each row is a request and 5.7% where rows come in runs, at most 1.6 and 4.1 times; all adapters
-// cost 1.1% and 9.6%, at most 1.6 and 9.1 times (2489 rows of 10 prompts, 228 adapters of rank 72, 5776 x 2624: 952 us
-// beside, 104 on the tensor cores), their square root 4.3% and 2.7%, at most 4.1 and 1.5 times.
+// Whether the adapters run row by row beside the projection.  On the tensor cores each row tile takes K blocks for every
+// adapter in it, 1.6 us of a worker's time for 64 of the rank, after some 15 us of launches that depend on one another.  How
+// many adapters a tile of up to 256 rows has is in ids on the device: one where rows come in prompts, all where each row is
+// a request of its own.  (adapters)^0.7 stands between: over 400 launches of random sizes (65 to 16000 rows, n 128 to 8192, k
+// 128 to 4096, 1 to 256 adapters of rank 8 to 128, all even over their logarithms but the rank) it costs 21% over the faster
+// way on average where each row is a request, at most 4.8 times, and 4.7% where rows come in up to 128 runs, at most 3.1
+// times; all adapters cost 3.4% and 45%, at most 2.0 and 15.7 times, their square root 36% and 3.3%, at most 5.4 and 2.1.
 // `pairs`: co-resident CTA pairs of the tensor cores' way.
 bool lora_beside(int pairs, int64_t rows, int64_t n, int64_t k, int64_t rank, int64_t adapters)
 {
@@ -644,7 +644,7 @@ LoraPlan lora_layout(const RaggedDevice *dev, int64_t rows, int64_t n, int64_t k
     l.list = take(size_t(l.tiles) * size_t(l.per) * 4u);
     l.counts_u = take(size_t(l.tiles_u) * 4u);
     l.list_u = take(size_t(l.tiles_u) * size_t(kLoraURows) * 4u);
-    l.u = take(size_t(l.pass_rows) * size_t(rank) * 2u);
+    l.u = take(size_t(l.pass_rows) * size_t(rank) * 4u);  // in two parts of the operands' type
     size_t split = split_bytes(kRagged[kVLoraU], dev->slots[kVLoraU]);
     const size_t split_y = l.tiles == 1 ? split_bytes(y, dev->slots[l.variant_y]) : 0;
     if (split_y > split) split = split_y;
@@ -800,7 +800,7 @@ gemm_status_t lora(gemm_dtype_t dtype, int64_t rows, int64_t n, int64_t k, int64
     u.scale = scale;
     u.adapters = adapted ? uint32_t(adapters) : 0u;
     u.rank = uint32_t(rank);
-    u.rank_blocks = uint32_t(cdiv(rank, kRagBlockK));
+    u.rank_blocks = uint32_t(cdiv(rank, kRagRank));
     u.skip_fill = ~0u;
     u.wait_limit = wait_limit ? wait_limit : wait_limit_for(cdiv(k, kRagBlockK) + 4096);
     p = u;

@@ -16,6 +16,13 @@
 //   kLoraY   y[t, n]  = sum_k w[n, k] x[t, k] + sum_r b[i][n, r] u[t, r]
 //                                                    kNT with one group, then K blocks of b[i] against u with
 //                                                    the rows of other adapters zeroed, one per adapter of the tile
+//                                                    and 32 of its rank
+//
+// u is an fp32 sum that the tensor cores take again as an operand.  Rounded to the operands' type it would add to y's error
+// nearly as much as y's own rounding, so it goes in two values, hi = round(u) and lo = round(u - hi), 16 bits in bf16 and 22
+// in fp16, side by side in one K block: b's 32 columns against hi, and again against lo.  (8192 rows of 16 prompts,
+// 8192 x 4096, rank 64, bf16: relative error 0.00204 and 341 us with one value, 0.00166 and 349 with two; 32-bit sums
+// throughout have 0.00166.)
 //
 // Everything but kTN yields tiles with the output column on tensor-memory
 // lanes and the row on columns; the epilogue transposes 32 x 32 pieces through
@@ -33,7 +40,7 @@
 //
 // Roles (one CTA or a CTA pair per tile):
 //   warp 0      TMA producer into a ring of 128-byte-swizzled stages
-//   warp 1      tensor memory and the MMA issuer (of the pair's first CTA)
+//   warp 1      tensor memory and the MMA issuer (of the pair's first CTA; kLoraY: in the second, the relay)
 //   warps 2..   epilogue, on one of two accumulators while the other fills: four
 //               warps, or eight that share the columns of 256-row tiles (with
 //               short contractions the tile's end is the longer part: 24 groups
@@ -45,7 +52,7 @@
 //               NaN out of the adapter's b and has the epilogue write NaN for them
 //               into that adapter's own rows alone.  A stage that the helper touches
 //               arrives on its CTA's `tail` barrier and is released to the MMA by
-//               the `fixed` barrier.
+//               the `fixed` barrier (kLoraY: from the second CTA by way of the relay).
 //
 // Group ends are read on the device (no host copy of them exists): every CTA
 // turns the offsets into a table of tile counts in shared memory, where all
@@ -79,6 +86,7 @@
 namespace gemm_f16 {
 
 constexpr int kRagBlockK = 64;       // 16-bit elements per 128-byte swizzled row
+constexpr int kRagRank = 32;         // columns of b in an adapter's K block, each against the two parts of u
 constexpr int kRagBand = 8;          // N-side tiles walked together before the M side advances
 constexpr int kRagMaxGroups = 1024;  // entries of the shared-memory group table
 constexpr int kRagHelpers = 128;     // threads of the helper warps: one for each row of a stage's M side
@@ -130,9 +138,9 @@ struct RaggedParams {
     uint32_t adapters;       // ids outside [0, adapters) have none
     const float *delta;      // kNT: added to the rows that have an adapter, [rows, pdim]; only this comes from the
                              // previous kernel, so only the epilogue waits for it
-    const void *u;           // kLoraY: u [rows, rank]
+    const void *u;           // kLoraY: u [rows, rank], a word each: hi in its low half, lo in its high half
     uint32_t rank;
-    uint32_t rank_blocks;    // ceil(rank / 64)
+    uint32_t rank_blocks;    // ceil(rank / 32)
     const CUtensorMap *maps; // kTN: for each group tm_p, tm_q[0], tm_p2, tm_q2 that end with the group's rows, or null
     uint32_t part_rows;      // kTN: not 0: groups are cut into parts of this many rows, which then are the `groups` of the
     uint32_t whole_groups;   // launch, each with a matrix of its own in `out`; and the number of whole ones
@@ -201,34 +209,95 @@ struct RaggedSeg {
     uint32_t krows;   // kTN: rows of the group
     uint32_t kb;      // K blocks of the whole tile
     uint32_t lo, hi;
-    uint32_t extra;   // kLoraY: how many of them are adapter blocks
+    uint32_t slots;   // kLoraY: adapters of the tile
+    uint32_t extra;   // kLoraY: how many of the K blocks are theirs
     uint32_t e_lo, e_hi;  // and which of those lie in [lo, hi)
 };
 
-// The order of a kLoraY tile's K blocks: the adapter blocks are spread evenly between the projection's, so that the
-// helper prepares one while the tensor cores work on the others, and every run of a split tile has its share
-// (64 rows with 64 adapters of rank 16, on single CTAs: 43.8 us with the adapter blocks last, 36.2 spread).  Block v
-// is an adapter block where floor(v extra / kb) steps.  Each costs up to 1.6 us, the latency of its load, the helper
-// and the release to the pair's first CTA, of which the ring holds three at a time.
+// The order of a kLoraY tile's K blocks: items, the projection's blocks and the adapters, each adapter's blocks in a row.  The
+// adapters are spread evenly between the others, so that the helper prepares one while the tensor cores work on the others,
+// and every run of a split tile has its share.  An adapter's blocks come later than the ring can look ahead, by some 1.6 us
+// (their load, the helper, the release to the pair's first CTA), but the blocks of one adapter share that: 2048 rows with
+// one of 64 adapters of rank 64 each, 4096 x 4096, took 620 us with the blocks spread one by one, 529 in a row and released
+// two at a time, and 413 with the relay.  Item i is an adapter where floor(i slots / items) steps.
 struct RaggedMix {
-    uint32_t kb, extra, left, e, m;  // left = v extra mod kb; e and m: adapter and projection blocks before v
-    __device__ __forceinline__ explicit RaggedMix(const RaggedSeg &s) : kb(s.kb), extra(s.extra)
+    uint32_t items, slots, blocks, left, run, begun, e, m;  // left = i slots mod items; run: blocks of the present adapter
+                                                            // still to come; adapters begun, adapter and projection blocks
+    __device__ __forceinline__ RaggedMix(const RaggedSeg &s, uint32_t rank_blocks) : slots(s.slots), blocks(rank_blocks)
     {
+        items = s.kb - s.extra + s.slots;
         e = s.e_lo;
-        left = uint32_t(uint64_t(s.lo) * extra - uint64_t(e) * kb);
         m = s.lo - e;
+        left = run = begun = 0u;
+        if (e != 0u) {
+            const uint32_t j = (e + blocks - 1u) / blocks;
+            run = j * blocks - e;
+            begun = j;
+            left = uint32_t(uint64_t(m + j) * slots - uint64_t(j) * items);
+        } else {
+            left = m * slots;
+        }
     }
     // whether the current block is an adapter block; then on to the next
     __device__ __forceinline__ bool step()
     {
-        left += extra;
-        if (left >= kb) {
-            left -= kb;
+        if (run != 0u) {
+            --run;
+            ++e;
+            return true;
+        }
+        left += slots;
+        if (left >= items) {
+            left -= items;
+            run = blocks - 1u;
+            ++begun;
             ++e;
             return true;
         }
         ++m;
         return false;
+    }
+    // adapter blocks before block v
+    static __device__ __forceinline__ uint32_t before(const RaggedSeg &s, uint32_t v, uint32_t blocks)
+    {
+        if (v == 0u || s.extra == 0u) return 0u;
+        if (v == s.kb) return s.extra;
+        const uint32_t items = s.kb - s.extra + s.slots;
+        uint32_t i = v;
+        if (blocks > 1u) {  // the last item that begins at v or before
+            uint32_t lo = 0u, hi = min(v, items - 1u);
+            while (lo < hi) {
+                const uint32_t mid = (lo + hi + 1u) >> 1;
+                if (mid + (blocks - 1u) * uint32_t(uint64_t(mid) * s.slots / items) <= v) lo = mid;
+                else hi = mid - 1u;
+            }
+            i = lo;
+        }
+        const uint32_t j = uint32_t(uint64_t(i) * s.slots / items);
+        return j * blocks + (v - i - j * (blocks - 1u));
+    }
+};
+
+// The adapters of a kLoraY tile by slot, 32 at a time in the lanes of a warp: the list's latency is not on the way of every
+// block.  Called by whole warps.
+struct RaggedNames {
+    const int32_t *list;
+    uint32_t slots, chunk;
+    int32_t name;
+    __device__ __forceinline__ RaggedNames(const int32_t *of_tile, uint32_t count, uint32_t slot) : list(of_tile), slots(count)
+    {
+        load(slot >> 5);
+    }
+    __device__ __forceinline__ void load(uint32_t c)
+    {
+        chunk = c;
+        const uint32_t i = 32u * c + (threadIdx.x & 31u);
+        name = i < slots ? list[i] : -1;
+    }
+    __device__ __forceinline__ int32_t operator[](uint32_t slot)
+    {
+        if ((slot >> 5) != chunk) load(slot >> 5);
+        return __shfl_sync(0xffffffffu, name, slot & 31u);
     }
 };
 
@@ -284,6 +353,7 @@ __device__ __forceinline__ void uniform(RaggedSeg &s)
     if constexpr (MODE == kTN || MODE == kLoraU) s.row0 = uniform(s.row0);
     if constexpr (MODE == kTN) s.krows = uniform(s.krows);
     if constexpr (MODE == kLoraY) {
+        s.slots = uniform(s.slots);
         s.extra = uniform(s.extra);
         s.e_lo = uniform(s.e_lo);
         s.e_hi = uniform(s.e_hi);
@@ -340,7 +410,8 @@ struct RaggedWalk {
             s.q0 = qi * p.per;
             s.qn = min(p.per, p.rows - s.q0);
             s.row0 = 0;
-            s.extra = uint32_t(tab_row[qi]) * p.rank_blocks;
+            s.slots = uint32_t(tab_row[qi]);
+            s.extra = s.slots * p.rank_blocks;
             s.kb = p.k_blocks + s.extra;
         } else {
             uint32_t lo = near;  // the group with tab_tile[lo] <= u < tab_tile[lo + 1]
@@ -412,8 +483,8 @@ struct RaggedWalk {
     __device__ __forceinline__ void count_extra(RaggedSeg &s) const
     {
         if constexpr (MODE == kLoraY) {
-            s.e_lo = uint32_t(uint64_t(s.lo) * s.extra / s.kb);
-            s.e_hi = uint32_t(uint64_t(s.hi) * s.extra / s.kb);
+            s.e_lo = RaggedMix::before(s, s.lo, p.rank_blocks);
+            s.e_hi = RaggedMix::before(s, s.hi, p.rank_blocks);
         } else {
             s.e_lo = s.e_hi = 0u;
         }
@@ -502,6 +573,18 @@ __device__ __forceinline__ uint32_t ragged_pack(float lo, float hi, bool bf16)
     }
     __half2 h = __floats2half2_rn(lo, hi);
     return *reinterpret_cast<uint32_t *>(&h);
+}
+
+__device__ __forceinline__ float2 ragged_unpack(uint32_t w, bool bf16)
+{
+    if (bf16) return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+    return __half22float2(*reinterpret_cast<const __half2 *>(&w));
+}
+
+// What is left of v beside its rounding `hi`: nothing where that is infinite or NaN.
+__device__ __forceinline__ float ragged_rest(float v, float hi)
+{
+    return hi - hi == 0.0f ? v - hi : 0.0f;
 }
 
 // The group table: row offsets clamped to [0, rows] and made monotone (offsets that are not can
@@ -664,7 +747,8 @@ __global__ void __launch_bounds__(RaggedCfg<MODE, CG, QCAP, STAGES>::kThreads, 1
         for (int s = 0; s < STAGES; ++s) {
             ptx::mbar_init(bar_full(s), 1);
             ptx::mbar_init(bar_empty(s), 1);
-            ptx::mbar_init(bar_fixed(s), (kRagHelpers / 32) * CG);
+            // (kLoraY: each CTA's own helpers, and in the pair's first CTA the other's relay)
+            ptx::mbar_init(bar_fixed(s), MODE == kLoraY ? kRagHelpers / 32 + (leader ? 1 : 0) : (kRagHelpers / 32) * CG);
             ptx::mbar_init(bar_tail(s), 1);
             rec[4 * s] = 0u;
         }
@@ -713,9 +797,9 @@ __global__ void __launch_bounds__(RaggedCfg<MODE, CG, QCAP, STAGES>::kThreads, 1
     };
     // kLoraY: the same of adapter block e, whose columns of b and u start at rank_from(e)
     auto rank_from = [&](uint32_t e) -> uint32_t {
-        return p.rank_blocks == 1u ? 0u : (e % p.rank_blocks) * kRagBlockK;
+        return p.rank_blocks == 1u ? 0u : (e % p.rank_blocks) * kRagRank;
     };
-    auto rank_steps = [&](uint32_t e) -> uint32_t { return min(4u, (p.rank - rank_from(e) + 15u) / 16u); };
+    auto rank_steps = [&](uint32_t e) -> uint32_t { return min(uint32_t(kRagRank) / 16u, (p.rank - rank_from(e) + 15u) / 16u); };
     // kTN: a last K block that the helper has to finish
     auto fixed_block = [&](const RaggedSeg &s, uint32_t kb) -> bool {
         return MODE == kTN && p.maps == nullptr && kb + 1u == s.kb && (s.krows & 15u) != 0u;
@@ -751,10 +835,12 @@ __global__ void __launch_bounds__(RaggedCfg<MODE, CG, QCAP, STAGES>::kThreads, 1
                 const int32_t q0 = int32_t(s.q0 + rank * hq);
                 const bool p_pairs = Cfg::kPMn && uint32_t(p0) / 64u + 2u <= p.p_groups;
                 const bool q_pairs = Cfg::kQMn && hq == 128u && uint32_t(q0) / 64u + 2u <= p.q_groups;
-                RaggedMix mix(s);
+                RaggedMix mix(s, p.rank_blocks);
+                RaggedNames names(list + size_t(s.g) * p.per, MODE == kLoraY ? s.slots : 0u, MODE == kLoraY ? mix.begun : 0u);
                 for (uint32_t v = s.lo; v < s.hi; ++v, ++fills) {
                     const uint32_t e = mix.e, kb = MODE == kLoraY ? mix.m : v;
                     const bool extra = MODE == kLoraY && mix.step();  // adapter block: only P comes by TMA
+                    const int32_t adapter = extra ? names[mix.begun - 1u] : 0;
                     if (!ragged_wait_warp<CG>(bar_empty(stage), phase ^ 1u, p, abort_flag, kRagErrEmpty)) return false;
                     const bool tail = extra || fixed_block(s, kb);    // to this CTA's own tail barrier
                     if (elected && !(blockIdx.x == 0 && fills == p.skip_fill && ptx::ld_relaxed_gpu_u32(p.error_word) == 0u)) {
@@ -798,7 +884,6 @@ __global__ void __launch_bounds__(RaggedCfg<MODE, CG, QCAP, STAGES>::kThreads, 1
                                     load(q_dst + b * 8192u, map_q, q0 + int32_t(64u * b), row, 0);
                             }
                         } else if (extra) {
-                            const int32_t adapter = list[size_t(s.g) * p.per + e / p.rank_blocks];
                             load(p_dst, &p.tm_x, int32_t(rank_from(e)), p0, adapter);
                         } else {
                             if constexpr (MODE == kNN) {
@@ -866,6 +951,12 @@ __global__ void __launch_bounds__(RaggedCfg<MODE, CG, QCAP, STAGES>::kThreads, 1
                             if (kk < steps)
                                 ptx::mma_f16<CG>(d_tmem, p_desc + kPStep * kk, q_desc + kQStep * kk, idesc,
                                                  kk == 0u ? accumulate : 1u);
+                        if (MODE == kLoraY && fixed) {  // the same of b against u's lower parts
+#pragma unroll
+                            for (uint32_t kk = 0; kk < uint32_t(kRagRank) / 16u; ++kk)
+                                if (kk < steps)
+                                    ptx::mma_f16<CG>(d_tmem, p_desc + kPStep * kk, q_desc + kQStep * (kk + kRagRank / 16), idesc, 1u);
+                        }
                         if constexpr (CG == 1) ptx::mma_commit(bar_empty(stage));
                         else ptx::mma_commit_pair(bar_empty(stage), uint16_t(3u));
                     }
@@ -877,7 +968,7 @@ __global__ void __launch_bounds__(RaggedCfg<MODE, CG, QCAP, STAGES>::kThreads, 1
                     return true;
                 };
                 if (MODE == kLoraY && s.e_hi > s.e_lo) {
-                    RaggedMix mix(s);
+                    RaggedMix mix(s, p.rank_blocks);
                     for (uint32_t v = s.lo; v < s.hi; ++v) {
                         const uint32_t e = mix.e, kb = mix.m;
                         const bool extra = mix.step();
@@ -913,6 +1004,43 @@ __global__ void __launch_bounds__(RaggedCfg<MODE, CG, QCAP, STAGES>::kThreads, 1
                     }
                 }
             }
+        } else if constexpr (MODE == kLoraY) {
+            // ------------------------------------------------ relay
+            // What this CTA's helpers have done is made visible in the pair's first CTA, where the MMA issuer waits for it: a
+            // release in the cluster takes 1300 to 1800 cycles, which the helpers do not wait for.  One serves two
+            // blocks of an adapter.
+            uint32_t stage = 0, uses = 0;
+            auto advance = [&]() { stage = stage + 1u == STAGES ? 0u : stage + 1u; };
+            auto wait_fixed = [&]() {
+                const bool ok = ragged_wait_warp<1>(bar_fixed(stage), (uses >> stage) & 1u, p, abort_flag, kRagErrFixed);
+                uses ^= 1u << stage;
+                return ok;
+            };
+            walk.template each<true>([&](const RaggedSeg &s) {
+                RaggedMix mix(s, p.rank_blocks);
+                for (uint32_t v = s.lo; v < s.hi; ++v) {
+                    const bool extra = mix.step();
+                    const uint32_t at = stage;
+                    if (extra && !wait_fixed()) return false;
+                    advance();
+                    if (!extra) continue;
+                    const bool two = mix.run != 0u && v + 1u < s.hi;
+                    const uint32_t then = stage;
+                    if (two) {
+                        mix.step();
+                        ++v;
+                        if (!wait_fixed()) return false;
+                        advance();
+                    }
+                    if (lane == 0) {
+                        ptx::fence_cluster();
+                        ptx::mbar_arrive_cluster_relaxed(ptx::map_to_rank(bar_fixed(at), 0u));
+                        if (two) ptx::mbar_arrive_cluster_relaxed(ptx::map_to_rank(bar_fixed(then), 0u));
+                    }
+                    __syncwarp();
+                }
+                return true;
+            });
         }
     } else if (warp < uint32_t(Cfg::kFirstHelper)) {
         // ------------------------------------------------ epilogue
@@ -1129,10 +1257,27 @@ __global__ void __launch_bounds__(RaggedCfg<MODE, CG, QCAP, STAGES>::kThreads, 1
                 }
                 release();
             } else {
-                // rows t on columns: 32 x 32 pieces transposed through shared memory.  A word holds rows
-                // 2i and 2i + 1 of one output column; a lane reads four columns' words and takes them apart.
-                if (live) {
-                    const float mul = (MODE == kLoraU && p.scale) ? p.scale[s.row0] : 1.0f;
+                if (live && MODE == kLoraU) {
+                    // a row's values on lanes, a word each: the two parts of u.  Few rows of a tile may have its adapter.
+                    const float mul = p.scale ? p.scale[s.row0] : 1.0f;
+                    for (uint32_t c = set; c < chunks; c += Cfg::kEpiSets) {
+                        const uint32_t t = 32u * c + lane;
+                        const uint32_t mine = __ballot_sync(0xffffffffu, (t < s.qn ? p.ids[s.q0 + t] : -1) == int32_t(s.row0));
+                        if (mine == 0u) continue;
+                        uint32_t r[32];
+                        chunk32(c, r);
+                        uint32_t *out = static_cast<uint32_t *>(p.out) + size_t(s.q0 + 32u * c) * p.pdim + prow + lane;
+                        const uint32_t stored = prow + lane < p.pdim ? mine : 0u;
+#pragma unroll
+                        for (uint32_t j = 0; j < 32u; ++j) {
+                            const float v = __uint_as_float(r[j]) * mul, hi = ragged_unpack(ragged_pack(v, 0.0f, bf16), bf16).x;
+                            const uint32_t word = ragged_pack(v, ragged_rest(v, hi), bf16);
+                            if ((stored >> j) & 1u) out[j * p.pdim] = word;  // (within a tile: 32 bits)
+                        }
+                    }
+                } else if (live) {
+                    // rows t on columns: 32 x 32 pieces transposed through shared memory.  A word holds rows
+                    // 2i and 2i + 1 of one output column; a lane reads four columns' words and takes them apart.
                     char *out = static_cast<char *>(p.out);
                     const uint32_t col = prow + 4u * (lane & 7u);
                     for (uint32_t c = set; c < chunks; c += Cfg::kEpiSets) {
@@ -1150,8 +1295,7 @@ __global__ void __launch_bounds__(RaggedCfg<MODE, CG, QCAP, STAGES>::kThreads, 1
 #pragma unroll
                         for (int i = 0; i < 16; ++i)
                             ptx::st_shared_u32(buf + uint32_t(i) * 128u + lane * 4u,
-                                               ragged_pack(__uint_as_float(r[2 * i]) * mul, __uint_as_float(r[2 * i + 1]) * mul,
-                                                           bf16));
+                                               ragged_pack(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1]), bf16));
                         __syncwarp();
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
@@ -1162,7 +1306,6 @@ __global__ void __launch_bounds__(RaggedCfg<MODE, CG, QCAP, STAGES>::kThreads, 1
 #pragma unroll
                                 for (uint32_t h = 0; h < 2u; ++h) {
                                     if (row + h >= s.qn) continue;
-                                    if (MODE == kLoraU && p.ids[s.q0 + row + h] != int32_t(s.row0)) continue;
                                     const uint32_t sel = h ? 0x7632u : 0x5410u;
                                     ptx::st_global_v2(out + (size_t(s.q0 + row + h) * p.pdim + col) * 2u,
                                                       __byte_perm(v.x, v.y, sel), __byte_perm(v.z, v.w, sel));
@@ -1192,7 +1335,7 @@ __global__ void __launch_bounds__(RaggedCfg<MODE, CG, QCAP, STAGES>::kThreads, 1
             ptx::fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) {
-                if constexpr (CG == 1) ptx::mbar_arrive(bar_fixed(stage));
+                if constexpr (CG == 1 || MODE == kLoraY) ptx::mbar_arrive(bar_fixed(stage));
                 else ptx::mbar_arrive_cluster(ptx::map_to_rank(bar_fixed(stage), 0u));
             }
         };
@@ -1221,11 +1364,25 @@ __global__ void __launch_bounds__(RaggedCfg<MODE, CG, QCAP, STAGES>::kThreads, 1
                 static_assert(Cfg::kQCta <= kRagHelpers, "one row of u per helper thread");
                 const uint32_t row = s.q0 + rank * hq + tid;
                 const int32_t id = (tid < hq && rank * hq + tid < s.qn) ? p.ids[row] : -1;
-                const uint4 *src = reinterpret_cast<const uint4 *>(static_cast<const char *>(p.u) + size_t(row) * p.rank * 2u);
-                uint4 u[8];  // the first 64 of u's columns, loaded once for all slots
+                const uint4 *src = reinterpret_cast<const uint4 *>(static_cast<const char *>(p.u) + size_t(row) * p.rank * 4u);
+                constexpr uint32_t kHalf = kRagRank / 8;  // 16-byte pieces of either part of u in a block
+                RaggedNames names(list + size_t(s.g) * p.per, s.slots, s.e_lo / p.rank_blocks);
+                uint4 u0[2 * kHalf], u1[2 * kHalf];  // of the first two blocks (rank <= 64: of all), or of the present ones
+                auto fetch = [&](uint32_t column, uint4 (&u)[2 * kHalf]) {
 #pragma unroll
-                for (uint32_t c = 0; c < 8u; ++c)
-                    u[c] = (uint32_t(id) < p.adapters && 8u * c < p.rank) ? src[c] : make_uint4(0u, 0u, 0u, 0u);
+                    for (uint32_t c = 0; c < kHalf; ++c) {
+                        const uint32_t at = column + 8u * c;
+                        const bool there = uint32_t(id) < p.adapters && at < p.rank;
+                        const uint4 v = there ? src[at / 4u] : make_uint4(0u, 0u, 0u, 0u);
+                        const uint4 w = there ? src[at / 4u + 1u] : make_uint4(0u, 0u, 0u, 0u);
+                        u[c] = make_uint4(__byte_perm(v.x, v.y, 0x5410u), __byte_perm(v.z, v.w, 0x5410u),
+                                          __byte_perm(w.x, w.y, 0x5410u), __byte_perm(w.z, w.w, 0x5410u));
+                        u[c + kHalf] = make_uint4(__byte_perm(v.x, v.y, 0x7632u), __byte_perm(v.z, v.w, 0x7632u),
+                                                  __byte_perm(w.x, w.y, 0x7632u), __byte_perm(w.z, w.w, 0x7632u));
+                    }
+                };
+                fetch(0u, u0);
+                fetch(kRagRank, u1);
                 // the table of b rows with infinities is free once the epilogue is done with the tile before last;
                 // each warp keeps the words of its own rows
                 const uint32_t bad_buf = adapted & 1u;
@@ -1239,36 +1396,28 @@ __global__ void __launch_bounds__(RaggedCfg<MODE, CG, QCAP, STAGES>::kThreads, 1
                 // exponent bits of both halves of a word; all ones (infinity or NaN) carry into the top bit
                 const uint32_t expo = p.bf16 ? 0x7F807F80u : 0x7C007C00u;
                 const uint32_t carry = p.bf16 ? 0x00800080u : 0x04000400u;
-                // adapter block e stands at v = ceil((e + 1) kb / extra) - 1
-                const uint64_t scaled = uint64_t(s.e_lo + 1u) * s.kb;
-                uint32_t quot = uint32_t(scaled / s.extra), rest = uint32_t(scaled - uint64_t(quot) * s.extra);
-                const uint32_t quot_step = s.kb / s.extra, rest_step = s.kb - quot_step * s.extra;
-                for (uint32_t e = s.e_lo; e < s.e_hi; ++e) {
-                    const uint32_t v = quot + (rest ? 1u : 0u) - 1u;
-                    const uint32_t stage = (first + v - s.lo) % STAGES;
-                    quot += quot_step;
-                    rest += rest_step;
-                    if (rest >= s.extra) {
-                        rest -= s.extra;
-                        ++quot;
-                    }
-                    const uint32_t slot = p.rank_blocks == 1u ? e : e / p.rank_blocks;
-                    const uint32_t r0 = rank_from(e);
-                    const int32_t adapter = list[size_t(s.g) * p.per + slot];
-                    const uint32_t chunks = 2u * rank_steps(e);
-                    const bool mine = id == adapter;
+                // adapter number `slot` is item ceil((slot + 1) items / slots) - 1
+                const uint32_t items = s.kb - s.extra + s.slots;
+                uint32_t slot = p.rank_blocks == 1u ? s.e_lo : s.e_lo / p.rank_blocks;
+                const uint64_t scaled = uint64_t(slot + 1u) * items;
+                uint32_t quot = uint32_t(scaled / s.slots), rest = uint32_t(scaled - uint64_t(quot) * s.slots);
+                const uint32_t quot_step = items / s.slots, rest_step = items - quot_step * s.slots;
+                for (uint32_t e = s.e_lo; e < s.e_hi;) {
+                    const uint32_t stage = (first + quot + (rest ? 1u : 0u) - 1u + e - slot - s.lo) % STAGES;
+                    const bool mine = id == names[slot];
+                    const uint32_t sub = e - slot * p.rank_blocks;
+                    const bool second = sub == 1u && p.rank_blocks == 2u;
+                    if (mine && p.rank_blocks > 2u) fetch(sub * kRagRank, u0);
                     // b has landed, so the stage is free: the producer waited for that.  (The stage's empty barrier
                     // cannot be waited for here: it may be more than one phase away.)
                     if (!wait_tail(stage)) return false;
                     // u where the row has the slot's adapter, zeros elsewhere
+                    const uint32_t q_at = base + Cfg::kOffQ + stage * Cfg::kQBytes + tid * 128u;
                     if (tid < hq) {
-                        const uint32_t q_at = base + Cfg::kOffQ + stage * Cfg::kQBytes + tid * 128u;
 #pragma unroll
-                        for (uint32_t c = 0; c < 8u; ++c) {
-                            if (c >= chunks) continue;
-                            uint4 v = u[c];
-                            if (r0 != 0u && mine && r0 + 8u * c < p.rank) v = src[r0 / 8u + c];
-                            if (!mine || r0 + 8u * c >= p.rank) v = make_uint4(0u, 0u, 0u, 0u);
+                        for (uint32_t c = 0; c < 2u * kHalf; ++c) {
+                            uint4 v = second ? u1[c] : u0[c];
+                            if (!mine) v = make_uint4(0u, 0u, 0u, 0u);
                             ptx::st_shared_v4(q_at + ((c ^ (tid & 7u)) << 4), v.x, v.y, v.z, v.w);
                         }
                     }
@@ -1276,13 +1425,13 @@ __global__ void __launch_bounds__(RaggedCfg<MODE, CG, QCAP, STAGES>::kThreads, 1
                     const uint32_t p_at = base + Cfg::kOffP + stage * Cfg::kPBytes + tid * 128u;
                     uint32_t odd = 0u;
 #pragma unroll
-                    for (uint32_t c = 0; c < 8u; ++c) {
-                        if (c >= chunks) continue;
+                    for (uint32_t c = 0; c < kHalf; ++c) {
                         const uint4 v = ptx::ld_shared_v4(p_at + ((c ^ (tid & 7u)) << 4));
                         odd |= ((v.x & expo) + carry) | ((v.y & expo) + carry) | ((v.z & expo) + carry) | ((v.w & expo) + carry);
                     }
                     if (odd & 0x80008000u) {
-                        for (uint32_t c = 0; c < chunks; ++c) {
+#pragma unroll 1
+                        for (uint32_t c = 0; c < kHalf; ++c) {
                             const uint32_t at = p_at + ((c ^ (tid & 7u)) << 4);
                             const uint4 v = ptx::ld_shared_v4(at);
                             uint32_t w[4] = {v.x, v.y, v.z, v.w};
@@ -1297,6 +1446,16 @@ __global__ void __launch_bounds__(RaggedCfg<MODE, CG, QCAP, STAGES>::kThreads, 1
                         any_bad[4u * bad_buf + part] = 1u;
                     }
                     hand_over(stage);
+                    ++e;
+                    if (e == (slot + 1u) * p.rank_blocks) {
+                        ++slot;
+                        quot += quot_step;
+                        rest += rest_step;
+                        if (rest >= s.slots) {
+                            rest -= s.slots;
+                            ++quot;
+                        }
+                    }
                 }
             }
             return true;
@@ -1423,12 +1582,6 @@ struct LoraFewParams {
     float *delta;   // [rows, n]
     uint32_t rows, n, k, rank, adapters, bf16;
 };
-
-__device__ __forceinline__ float2 ragged_unpack(uint32_t w, bool bf16)
-{
-    if (bf16) return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
-    return __half22float2(*reinterpret_cast<const __half2 *>(&w));
-}
 
 // Four of a row's u's (before the scale) by WARPS warps that share k: each lane multiplies 8 elements at a time.  The sums
 // of a single warp are in all lanes; of four, thread t returns number t mod 4, and s_sum is the block's.

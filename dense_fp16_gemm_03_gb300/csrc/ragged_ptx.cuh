@@ -83,6 +83,18 @@ __device__ __forceinline__ void tensormap_acquire(const void *global)
     asm volatile("fence.proxy.tensormap::generic.acquire.gpu [%0], 128;" ::"l"(reinterpret_cast<uint64_t>(global)) : "memory");
 }
 
+// A release by several arrivals: the fence makes all earlier writes visible in the cluster, the arrivals behind it wait
+// for nothing more.
+__device__ __forceinline__ void fence_cluster()
+{
+    asm volatile("fence.acq_rel.cluster;" ::: "memory");
+}
+
+__device__ __forceinline__ void mbar_arrive_cluster_relaxed(uint32_t bar_cluster)
+{
+    asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar_cluster) : "memory");
+}
+
 // True in one lane of a converged warp, always the same.
 __device__ __forceinline__ bool elect_one()
 {

@@ -93,8 +93,10 @@ gemm_status_t gemm_grouped_tn(gemm_dtype_t dtype, gemm_dtype_t out, int64_t grou
  * x [rows, k], w [n, k], a [adapters, rank, k], b [adapters, n, rank],
  * y [rows, n]; ids: rows int32 in any order, a row whose id is outside
  * [0, adapters) has no adapter; scale: adapters fp32, or NULL for 1.  The inner
- * product scale (x a^T) may be rounded to the operands' type (where many rows go
- * through the tensor cores); the two products are added in fp32 and rounded once.  What an adapter holds reaches the rows that
+ * product scale (x a^T) stays in fp32, or, where many rows go through the tensor
+ * cores, is the sum of two values of the operands' type (and infinite beyond the
+ * range of fp16, if that is the type); the two products are added in fp32 and
+ * rounded once.  What an adapter holds reaches the rows that
  * have it and no others, infinities and NaN included (a product with an infinity
  * of b may come out as NaN).  The workspace is
  * required (GEMM_ERR_WORKSPACE); gemm_lora_workspace_size gives the bytes that

@@ -186,6 +186,31 @@ def test_repeats_bit_for_bit_on_another_stream():
         assert torch.equal(lora_run(x, w, a, b, ids), first)
 
 
+@pytest.mark.parametrize("kind", sorted(KINDS))
+@pytest.mark.parametrize("rows,rank", [(130, 128), (600, 24), (600, 64), (900, 104)])
+def test_the_inner_product_is_not_rounded_to_the_type(kind, rows, rank):
+    """u = s x a^T of up to 16 significant bits, more than either type holds, and sums that fp32 holds exactly: the result
+    is the exact sum rounded once."""
+    kind = KINDS[kind]
+    n, adapters = 264, 3
+    k = k_for(rows, n, rank, adapters)
+    assert R.gemm_lora_way(rows, n, k, rank, adapters) == R.LORA_TENSOR_CORES
+    rng = np.random.default_rng(17)
+    x, w = small_ints(rng, (rows, k), kind, 100), small_ints(rng, (n, k), kind, 1)
+    a, b = small_ints(rng, (adapters, rank, k), kind, 7), small_ints(rng, (adapters, n, rank), kind, 2)
+    w[torch.from_numpy(rng.random((n, k)) < 1 - 8.0 / k)] = 0
+    a[torch.from_numpy(rng.random((adapters, rank, k)) < 1 - 48.0 / k)] = 0
+    scale = torch.tensor([2.0 ** -5, 2.0 ** -4, 2.0 ** -5])
+    ids = torch.from_numpy(rng.integers(-1, adapters, size=rows).astype(np.int32))
+    most = torch.stack([(x.double() @ a[i].double().T).abs().max() for i in range(adapters)]).max()
+    assert 2 ** 11 < most < 2 ** 16
+    ref = lora_ref(x, w, a, b, ids, scale)
+    assert ref.abs().max() < 65504
+    got = lora_run(x, w, a, b, ids, scale)
+    bad = torch.nonzero(got != ref.to(kind))
+    assert bad.shape[0] == 0, "%d of %d differ" % (bad.shape[0], got.numel())
+
+
 @pytest.mark.parametrize("rows", [200, 600])
 def test_captured_in_a_graph_follows_new_inputs(rows):
     n, rank, adapters = 136, 72, 4
