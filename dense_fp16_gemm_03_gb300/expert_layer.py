@@ -52,7 +52,8 @@ class ExpertLayer:
         h = ragged.gemm_grouped_nt(xs, self.up, r.offsets, workspace=self.work)
         a = torch.relu(h).square()
         ys = ragged.gemm_grouped_nt(a, self.down, r.offsets, workspace=self.work)
-        mine = ys[r.position.clamp(min=0).long()].float()  # [rows, top, width]
+        # [rows, top, width]; nothing where there is no choice (a weight of 0 would not keep row 0's infinities out)
+        mine = torch.where((r.position >= 0)[:, :, None], ys[r.position.clamp(min=0).long()].float(), 0.0)
         out = (r.weights[:, :, None] * mine).sum(1).to(x.dtype)
         return out, (x, logits, r, token, xs, h, a, mine)
 
