@@ -62,18 +62,17 @@ class ExpertLayer:
         x, logits, r, token, xs, h, a, mine = saved
         dmine = r.weights[:, :, None] * dout.float()[:, None, :]
         dweights = (mine * dout.float()[:, None, :]).sum(2)
-        chosen = (r.position >= 0).flatten()
-        dys = torch.zeros_like(xs)
-        dys[r.position.flatten()[chosen].long()] = dmine.reshape(-1, self.width)[chosen].to(dys.dtype)
+        # rows sorted by expert are gathered by `order`, rows as they came by `position`: nothing waits for the GPU (a
+        # training step can be captured), and no sum depends on the order of atomics
+        dys = torch.where((r.order >= 0)[:, None], dmine.reshape(-1, self.width)[r.order.clamp(min=0).long()], 0.0).to(xs.dtype)
         da = ragged.gemm_grouped_nn(dys, self.down, r.offsets, workspace=self.work)
         ddown = ragged.gemm_grouped_tn(dys, a, r.offsets, dtype=torch.float32, workspace=self.work)
         dh = (da.float() * 2 * torch.relu(h.float())).to(h.dtype)
         dup = ragged.gemm_grouped_tn(dh, xs, r.offsets, dtype=torch.float32, workspace=self.work)
         dxs = ragged.gemm_grouped_nn(dh, self.up, r.offsets, workspace=self.work)
         dlogits = ragged.gemm_route_topk_grad(logits, r.ids, r.weights, dweights)
-        dx = dlogits @ self.router.float()
-        live = int(chosen.sum())
-        dx.index_add_(0, token[:live], dxs[:live].float())
+        dmine_x = torch.where((r.position >= 0)[:, :, None], dxs[r.position.clamp(min=0).long()].float(), 0.0)
+        dx = dlogits @ self.router.float() + dmine_x.sum(1)
         return dx.to(x.dtype), dlogits.T @ x.float(), dup, ddown
 
 
