@@ -296,7 +296,8 @@ def gemm_route_topk(logits, top, renorm=True, out=None, workspace=None, stream=N
 
     logits [rows, experts] float16, bfloat16 or float32; returns ids, weights and position [rows, top], offsets
     [experts + 1] and order [rows * top] (choices t * top + j sorted by expert).  The weights are softmax(logits) at
-    ids, divided by their sum if `renorm`.  `out`: a Routing of tensors to write into."""
+    ids, divided by their sum if `renorm`.  `out`: a Routing of tensors to write into.  The workspace
+    (gemm_route_workspace_size) is required above 64 rows."""
     torch = _gemm._tm()
     dev = _operand(logits, "logits", 2)
     rows, experts = logits.shape

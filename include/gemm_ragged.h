@@ -127,6 +127,9 @@ gemm_status_t gemm_lora_nt(gemm_dtype_t dtype, int64_t rows, int64_t n, int64_t 
  * with a NaN or +infinity among its logits has NaN weights; NaN logits are
  * chosen after all others but before -infinity.
  *
+ * The workspace (gemm_route_workspace_size: 0 bytes for up to 64 rows) is
+ * required where its size is > 0 (GEMM_ERR_WORKSPACE).
+ *
  * gemm_route_topk_grad: dlogits [rows, experts] fp32 from the weights' gradient
  * dweights [rows, top] fp32, with logits, ids and weights of the forward call:
  *   renorm:     dl[ids[j]] = w[j] (dw[j] - sum_i w[i] dw[i]), zero elsewhere
