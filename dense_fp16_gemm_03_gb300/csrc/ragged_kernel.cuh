@@ -36,7 +36,7 @@
 // bound by the tensor cores under the board's power limit (8192^3 in one group:
 // 1601 TFLOP/s sustained, beside 1592 of the dense 256 x 256 kernel), and with
 // groups of unlike size by what the narrower tiles load per multiply (32 groups
-// of 16384 rows in all, 4096 x 4096: 345 us with 512 rows each, 375 uneven).
+// of 16384 rows in all, 4096 x 4096: 312 us with 512 rows each, 339 uneven).
 //
 // Roles (one CTA or a CTA pair per tile):
 //   warp 0      TMA producer into a ring of 128-byte-swizzled stages
@@ -44,7 +44,7 @@
 //   warps 2..   epilogue, on one of two accumulators while the other fills: four
 //               warps, or eight that share the columns of 256-row tiles (with
 //               short contractions the tile's end is the longer part: 24 groups
-//               of 16121 rows in all, 2024 x 136, 34 us with four, 26.9 with eight)
+//               of 16121 rows in all, 2024 x 136, 34 us with four, 26.2 with eight)
 //   the last 4  helper, where the mode has one: kTN without maps zeroes the rows
 //               past a group's end in its last K block (both operands: a zero
 //               times an infinity of the next group would be NaN); kLoraY builds
@@ -65,10 +65,10 @@
 // and only ever for lower-numbered workers, which start no later: launches that
 // share the GPU cannot hold each other up.  Sums are added in a fixed order:
 // results repeat bit for bit.  Every flag is clear at the launch's end, also after
-// an abort, so a replay of a captured launch never finds one of the last.  (Handing each next tile to the worker that comes
-// for it first, by a counter, was measured for groups of unlike sizes: 388 us
-// against 380 in the case above, and one group 371 against 352: the number's way
-// through the roles costs more than the balance brings.)
+// an abort, so a replay of a captured launch never finds one of the last.
+// (Handing each next tile to the worker that comes for it first, by a counter,
+// took 2% longer for the uneven groups above and 5% for one group of as many
+// rows: the number's way through the roles costs more than the balance brings.)
 //
 // Every wait is bounded as in gemm_kernel.cuh: past `wait_limit` cycles the
 // thread records an error code, raises the CTA's abort flag, and all roles
@@ -158,8 +158,8 @@ struct RaggedCfg {
     static constexpr bool kPMn = (MODE == kNN || MODE == kTN);  // M-side operand MN-major
     static constexpr bool kQMn = (MODE == kTN);                 // N-side operand MN-major
     static constexpr bool kHelper = (MODE == kTN || MODE == kLoraY);
-    // (kTN: eight warps' boxes of 128 bytes a row do not fit; of 64 bytes, or shared by two warps, they took 481 and
-    // 452 us where four warps take 445 for 16384 rows, 32 groups, 4096 x 4096)
+    // (kTN: eight warps' boxes of 128 bytes a row do not fit; of 64 bytes, or shared by two warps, they took 8 and
+    // 2% longer than four for 16384 rows, 32 groups, 4096 x 4096)
     static constexpr int kEpiSets = (QCAP == 256 && MODE != kTN) ? 2 : 1;
     static constexpr int kEpiWarps = 4 * kEpiSets;
     static constexpr int kFirstHelper = 2 + kEpiWarps;          // warp
@@ -1483,8 +1483,8 @@ __global__ void __launch_bounds__(RaggedCfg<MODE, CG, QCAP, STAGES>::kThreads, 1
 }
 
 // kTN: every group's tensor maps with the rows ending at the group's end, so that TMA fills the rest of its last K block
-// with zeros (32 uneven groups of 16384 rows in all, 4096 x 4096: 541 us with the helper zeroing each tile's last
-// block, 459 so).  One block per group, one warp per map; some 3 us in front of the product.
+// with zeros (32 uneven groups of 16384 rows in all, 4096 x 4096: 442 us with the helper zeroing each tile's last
+// block, 358 so).  One block per group, one warp per map; some 3 us in front of the product.
 struct RaggedMapsParams {
     CUtensorMap maps[4];
     const int32_t *offsets;

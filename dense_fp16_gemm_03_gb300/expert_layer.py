@@ -5,7 +5,7 @@
 The layer sends every row to ``top`` experts, each a product of its own, a square of the positive part, and a product
 back, and adds their results weighted by the router:
 
-    l = x . router^T;  w, e = top-k of softmax(l)
+    l = x . router^T;  w, e = top-k of softmax(l), w divided by their sum
     out[t] = sum_j w[t, j] relu(x[t] . up[e_tj]^T)^2 . down[e_tj]^T
 
 The grouped products, the router and its gradient are this package's; what is between them (gathering rows, the
