@@ -6,4 +6,4 @@ same entry-point names.  ``inputs`` draws the seeded synthetic operands.
 Importing this package loads nothing; the library is loaded on first use and
 a missing library is an error, never a fallback.
 """
-__all__ = ["inputs", "gemm", "ragged"]
+__all__ = ["inputs", "gemm", "ragged", "linear"]

@@ -1,7 +1,7 @@
 """Build the C-ABI shared library libgemm_f16.so in-tree (``_build/``).
 
-Two translation units compiled side by side (the dense product, and the
-ragged products with the router), one ``-gencode`` (sm_103a), shared cudart;
+Three translation units compiled side by side (the dense product, the ragged
+products with the router, and the products with an epilogue), one ``-gencode`` (sm_103a), shared cudart;
 nvcc cross-compiles them on a machine without a GPU.
 """
 import glob
@@ -15,7 +15,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 OUT_DIR = os.path.join(PKG, "_build")
 LIB = os.path.join(OUT_DIR, "libgemm_f16.so")
-SOURCES = [os.path.join(CSRC, "gemm_api.cu"), os.path.join(CSRC, "ragged_api.cu")]
+SOURCES = [os.path.join(CSRC, "gemm_api.cu"), os.path.join(CSRC, "ragged_api.cu"), os.path.join(CSRC, "linear_api.cu")]
 DEPS = (SOURCES + sorted(glob.glob(os.path.join(CSRC, "*.cuh"))) + sorted(glob.glob(os.path.join(CSRC, "*.h")))
         + sorted(glob.glob(os.path.join(INCLUDE, "*.h"))))
 

@@ -1,0 +1,274 @@
+// C ABI of the products with an epilogue and of their gradients (declared in
+// include/gemm_linear.h): argument validation, the choice of kernel variant,
+// workspace layout, tensor maps and launches.  The kernels are in
+// ragged_kernel.cuh (the product), linear_act.cuh and linear_kernel.cuh.
+#include "linear_kernel.cuh"
+#include "ragged_launch.cuh"
+
+using namespace gemm_f16;
+
+namespace {
+
+enum LinearVariantId { kVNtWide, kVNtFew, kVNnWide, kVNnFew };
+const RaggedVariant kLinear[] = {
+    RAGGED_VARIANT(kNT, 2, 256, 6, true), RAGGED_VARIANT(kNT, 1, 64, 8, true),
+    RAGGED_VARIANT(kNN, 2, 256, 6, true), RAGGED_VARIANT(kNN, 1, 64, 8, true),
+};
+constexpr int kSetsWide = RaggedCfg<kNN, 2, 256, 6, true>::kEpiSets, kSetsFew = RaggedCfg<kNN, 1, 64, 8, true>::kEpiSets;
+using LinearDevice = RaggedDeviceOf<int(sizeof(kLinear) / sizeof(kLinear[0]))>;
+
+gemm_status_t linear_device(LinearDevice **out)
+{
+    return ragged_device_of(kLinear, nullptr, 0, out);
+}
+
+int64_t live_groups(int64_t groups, int64_t rows)
+{
+    return groups < rows ? groups : rows;
+}
+
+// Bytes of the partial sums of a bias gradient: a line for each set of epilogue warps of each N-side tile.
+size_t sums_bytes(int64_t per, int sets, int64_t groups, int64_t rows, int64_t cols)
+{
+    return size_t(round_up((rows / per + live_groups(groups, rows)) * sets * cols * 4, 256));
+}
+
+// Rows of a piece of linear_grad_kernel: enough pieces to fill the SMs, few enough lines to add up.
+int64_t grad_rows(int64_t rows, int64_t cols, int num_sms)
+{
+    const int64_t strips = cdiv(cols, 256);
+    int64_t per = 128;
+    while (per > 32 && cdiv(rows, per) * strips < 8 * num_sms) per /= 2;
+    return per;
+}
+
+// What any number of rows up to this one may need for the partial sums of linear_grad_kernel.
+size_t grad_room(int64_t groups, int64_t rows, int64_t cols, int num_sms)
+{
+    size_t most = 0;
+    for (int64_t per = 32; per <= 128; per *= 2) {
+        // the most rows that take pieces of this size
+        int64_t r = rows;
+        if (grad_rows(rows, cols, num_sms) > per) r = (8 * num_sms / cdiv(cols, 256) + 1) * 2 * per;
+        if (r > rows) r = rows;
+        const size_t bytes = sums_bytes(per, 1, groups, r, cols);
+        if (bytes > most) most = bytes;
+    }
+    return most;
+}
+
+gemm_status_t check_linear(gemm_dtype_t dtype, gemm_act_t act, int64_t groups, int64_t rows, int64_t n, int64_t k,
+                           const int32_t *offsets)
+{
+    gemm_status_t st = check_sizes({groups, rows}, {n, k});
+    if (st != GEMM_OK) return st;
+    if (!operand_type(dtype) || act < GEMM_ACT_NONE || act > GEMM_ACT_SILU) return GEMM_ERR_INVALID_ARG;
+    if (groups < 1 || (groups > 1 && rows > 0 && offsets == nullptr)) return GEMM_ERR_INVALID_ARG;
+    if (groups > GEMM_GROUPED_MAX_GROUPS) return GEMM_ERR_UNSUPPORTED_SHAPE;
+    return check_pointer(offsets, offsets != nullptr, 4);
+}
+
+// A bias gradient of no rows.
+gemm_status_t zero_bias(float *dbias, int64_t count, cudaStream_t stream)
+{
+    if (dbias == nullptr || count == 0) return GEMM_OK;
+    LinearDevice *dev = nullptr;
+    gemm_status_t st = linear_device(&dev);
+    if (st != GEMM_OK) return st;
+    if (cudaMemsetAsync(dbias, 0, size_t(count) * 4u, stream) != cudaSuccess) {
+        cudaGetLastError();
+        return GEMM_ERR_LAUNCH;
+    }
+    return GEMM_OK;
+}
+
+gemm_status_t launch_sum(const float *sums, const int32_t *offsets, float *dbias, int64_t groups, int64_t rows, int64_t cols,
+                         int64_t per, int sets, cudaStream_t stream)
+{
+    LinearSumParams p;
+    p.sums = sums;
+    p.offsets = offsets;
+    p.dbias = dbias;
+    p.groups = uint32_t(groups);
+    p.rows = uint32_t(rows);
+    p.per = uint32_t(per);
+    p.sets = uint32_t(sets);
+    p.cols = uint32_t(cols);
+    void *args[1] = {&p};
+    return launch(reinterpret_cast<const void *>(&linear_sum_kernel), dim3(unsigned(cdiv(cols, 32)), unsigned(groups), 1),
+                  kLinearThreads, 0, 1, args, stream);
+}
+
+// mode kNT: first = x, in = residual, out = y; mode kNN: first = dy, in = z, out = dx.
+gemm_status_t linear(int mode, gemm_dtype_t dtype, gemm_act_t act, int64_t groups, int64_t rows, int64_t n, int64_t k,
+                     const int32_t *offsets, const void *first, const void *w, const void *bias, const void *in, void *kept,
+                     void *out, float *dbias, void *ws, size_t ws_bytes, uint32_t skip_fill, long long wait_limit,
+                     cudaStream_t stream)
+{
+    gemm_status_t st = check_linear(dtype, act, groups, rows, n, k, offsets);
+    if (st != GEMM_OK) return st;
+    const int64_t pdim = mode == kNT ? n : k, kdim = mode == kNT ? k : n;
+    const bool any = rows > 0 && pdim > 0;
+    if (mode == kNN && act == GEMM_ACT_NONE) in = nullptr;
+    if (any && kdim == 0) return GEMM_ERR_UNSUPPORTED_SHAPE;
+    st = check_pointer(out, any);
+    if (st == GEMM_OK) st = check_pointer(first, any);
+    if (st == GEMM_OK) st = check_pointer(w, any);
+    if (st == GEMM_OK) st = check_pointer(in, any && (in != nullptr || (mode == kNN && act != GEMM_ACT_NONE)));
+    if (st == GEMM_OK) st = check_pointer(bias, any && bias != nullptr);
+    if (st == GEMM_OK) st = check_pointer(kept, any && kept != nullptr);
+    if (st == GEMM_OK) st = check_pointer(dbias, pdim > 0 && dbias != nullptr);
+    if (st != GEMM_OK) return st;
+    if (!any) return zero_bias(dbias, groups * pdim, stream);
+    LinearDevice *dev = nullptr;
+    st = linear_device(&dev);
+    if (st != GEMM_OK) return st;
+    const int few = mode == kNT ? kVNtFew : kVNnFew, wide = mode == kNT ? kVNtWide : kVNnWide;
+    const RaggedChoice choice = ragged_choice(kLinear[few], dev->slots[few], kLinear[wide], dev->slots[wide], groups, rows, pdim, kdim,
+                                              ws != nullptr, 0.0);
+    const int variant = choice.wide ? wide : few;
+    const RaggedVariant &var = kLinear[variant];
+    const int sets = choice.wide ? kSetsWide : kSetsFew;
+    // the sums of one tile are dbias
+    const bool whole = offsets == nullptr && rows <= var.qcap && sets == 1;
+    const size_t sums = dbias && !whole ? sums_bytes(var.qcap, sets, groups, rows, pdim) : 0;
+    const size_t need = sums + (choice.split ? split_bytes(var, dev->slots[variant]) : 0);
+    if (ws != nullptr || ws_bytes != 0 || sums > 0) {
+        if (ws == nullptr || ws_bytes < need) return GEMM_ERR_WORKSPACE;
+        if (reinterpret_cast<uintptr_t>(ws) & 255u) return GEMM_ERR_ALIGNMENT;
+    }
+    LinearParams p;
+    memset(&p, 0, sizeof(p));
+    p.offsets = offsets;
+    p.groups = uint32_t(groups);
+    p.rows = uint32_t(rows);
+    p.pdim = uint32_t(pdim);
+    p.kdim = uint32_t(kdim);
+    p.k_blocks = uint32_t(cdiv(kdim, kRagBlockK));
+    p.tiles_p = uint32_t(cdiv(pdim, 128 * var.cg));
+    p.bf16 = dtype == GEMM_DTYPE_BF16;
+    p.out = out;
+    p.skip_fill = skip_fill;
+    p.wait_limit = wait_limit ? wait_limit : wait_limit_for(p.k_blocks);
+    p.bias = bias;
+    p.in = in;
+    p.kept = kept;
+    p.sums = dbias == nullptr ? nullptr : whole ? dbias : static_cast<float *>(ws);
+    p.act = uint32_t(act);
+    int64_t most = most_tiles(var, groups, rows, pdim);
+    if (most >= kSizeLimit) return GEMM_ERR_UNSUPPORTED_SHAPE;
+    st = encode_stack(&p.tm_p, w, dtype, groups, n, k, 64, mode == kNT ? 128 : 64);
+    if (st == GEMM_OK && mode == kNN) st = encode_pairs(&p.tm_p2, w, dtype, groups, n, k, &p.p_groups);
+    if (st == GEMM_OK) st = encode_rows(p.tm_q, first, dtype, rows, kdim, var.qbox);
+    if (st != GEMM_OK) return st;
+    if (choice.split && most * p.k_blocks < kIterLimit) {
+        use_split(&p, var, dev->slots[variant], static_cast<char *>(ws) + sums);
+        most *= p.k_blocks;
+    }
+    st = launch_variant(var, dev->slots[variant], dev->error_word, p, &p, most, stream);
+    if (st != GEMM_OK || sums == 0) return st;
+    return launch_sum(p.sums, offsets, dbias, groups, rows, pdim, var.qcap, sets, stream);
+}
+
+}  // namespace
+
+extern "C" {
+
+gemm_status_t gemm_linear_workspace_size(int64_t groups, int64_t rows, int64_t n, int64_t k, size_t *bytes)
+{
+    if (!bytes) return GEMM_ERR_INVALID_ARG;
+    gemm_status_t st = check_sizes({groups, rows}, {n, k});
+    if (st != GEMM_OK) return st;
+    if (groups < 1) return GEMM_ERR_INVALID_ARG;
+    if (groups > GEMM_GROUPED_MAX_GROUPS) return GEMM_ERR_UNSUPPORTED_SHAPE;
+    LinearDevice *dev = nullptr;
+    st = linear_device(&dev);
+    if (st != GEMM_OK) return st;
+    *bytes = 0;
+    if (rows == 0) return GEMM_OK;
+    const RaggedVariant &few = kLinear[kVNtFew], &wide = kLinear[kVNtWide];
+    size_t sums = sums_bytes(few.qcap, kSetsFew, groups, rows, k);
+    const size_t wide_sums = sums_bytes(wide.qcap, kSetsWide, groups, rows, k);
+    if (wide_sums > sums) sums = wide_sums;
+    size_t split = split_bytes(few, dev->slots[kVNtFew]);
+    const size_t wide_split = split_bytes(wide, dev->slots[kVNtWide]);
+    if (rows > few.qcap && wide_split > split) split = wide_split;
+    *bytes = k > 0 ? sums + split : 0;
+    const size_t grad = grad_room(groups, rows, n, dev->num_sms);
+    if (grad > *bytes) *bytes = grad;
+    return GEMM_OK;
+}
+
+gemm_status_t gemm_linear_nt(gemm_dtype_t dtype, gemm_act_t act, int64_t groups, int64_t rows, int64_t n, int64_t k,
+                             const int32_t *offsets, const void *x, const void *w, const void *bias, const void *residual, void *z,
+                             void *y, void *workspace, size_t ws_bytes, gemm_stream_t stream)
+{
+    return linear(kNT, dtype, act, groups, rows, n, k, offsets, x, w, bias, residual, z, y, nullptr, workspace, ws_bytes, ~0u, 0,
+                  reinterpret_cast<cudaStream_t>(stream));
+}
+
+gemm_status_t gemm_linear_nn(gemm_dtype_t dtype, gemm_act_t act, int64_t groups, int64_t rows, int64_t n, int64_t k,
+                             const int32_t *offsets, const void *dy, const void *w, const void *z, void *dx, float *dbias,
+                             void *workspace, size_t ws_bytes, gemm_stream_t stream)
+{
+    return linear(kNN, dtype, act, groups, rows, n, k, offsets, dy, w, nullptr, z, nullptr, dx, dbias, workspace, ws_bytes, ~0u, 0,
+                  reinterpret_cast<cudaStream_t>(stream));
+}
+
+gemm_status_t gemm_linear_grad(gemm_dtype_t dtype, gemm_act_t act, int64_t groups, int64_t rows, int64_t n, const int32_t *offsets,
+                               const void *dy, const void *z, void *dz, float *dbias, void *workspace, size_t ws_bytes,
+                               gemm_stream_t stream)
+{
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    gemm_status_t st = check_linear(dtype, act, groups, rows, n, 0, offsets);
+    if (st != GEMM_OK) return st;
+    const bool any = rows > 0 && n > 0;
+    st = check_pointer(dy, any);
+    if (st == GEMM_OK) st = check_pointer(z, any && act != GEMM_ACT_NONE);
+    if (st == GEMM_OK) st = check_pointer(dz, any && (dz != nullptr || act != GEMM_ACT_NONE));
+    if (st == GEMM_OK) st = check_pointer(dbias, n > 0 && dbias != nullptr);
+    if (st != GEMM_OK) return st;
+    if (!any) return zero_bias(dbias, groups * n, s);
+    if (dz == nullptr && dbias == nullptr) return GEMM_OK;
+    LinearDevice *dev = nullptr;
+    st = linear_device(&dev);
+    if (st != GEMM_OK) return st;
+    const int64_t per = grad_rows(rows, n, dev->num_sms), strips = cdiv(n, 256);
+    const bool whole = offsets == nullptr && rows <= per;  // the sums of one piece are dbias
+    const size_t need = dbias && !whole ? sums_bytes(per, 1, groups, rows, n) : 0;
+    if (workspace != nullptr || ws_bytes != 0 || need > 0) {
+        if (workspace == nullptr || ws_bytes < need) return GEMM_ERR_WORKSPACE;
+        if (reinterpret_cast<uintptr_t>(workspace) & 255u) return GEMM_ERR_ALIGNMENT;
+    }
+    const int64_t blocks = (rows / per + live_groups(groups, rows)) * strips;  // at most: a group's last piece may be a part of one
+    if (blocks >= kSizeLimit) return GEMM_ERR_UNSUPPORTED_SHAPE;
+    LinearGradParams p;
+    p.dy = dy;
+    p.z = act == GEMM_ACT_NONE ? nullptr : z;
+    p.dz = dz;
+    p.sums = dbias == nullptr ? nullptr : whole ? dbias : static_cast<float *>(workspace);
+    p.offsets = offsets;
+    p.groups = uint32_t(groups);
+    p.rows = uint32_t(rows);
+    p.cols = uint32_t(n);
+    p.per = uint32_t(per);
+    p.strips = uint32_t(strips);
+    p.act = uint32_t(act);
+    p.bf16 = dtype == GEMM_DTYPE_BF16;
+    void *args[1] = {&p};
+    st = launch(reinterpret_cast<const void *>(&linear_grad_kernel), dim3(unsigned(blocks), 1, 1), kLinearThreads, 0, 1, args, s);
+    if (st != GEMM_OK || need == 0) return st;
+    return launch_sum(p.sums, offsets, dbias, groups, rows, n, per, 1, s);
+}
+
+gemm_status_t gemm_linear_stall_test(int32_t mode, gemm_dtype_t dtype, gemm_act_t act, int64_t groups, int64_t rows, int64_t n,
+                                     int64_t k, const int32_t *offsets, const void *first, const void *w, const void *extra,
+                                     void *out, float *dbias, void *workspace, size_t ws_bytes, uint32_t skip_fill,
+                                     long long wait_limit_cycles, gemm_stream_t stream)
+{
+    if ((mode != kNT && mode != kNN) || wait_limit_cycles <= 0) return GEMM_ERR_INVALID_ARG;
+    return linear(mode, dtype, act, groups, rows, n, k, offsets, first, w, nullptr, extra, nullptr, out, mode == kNN ? dbias : nullptr,
+                  workspace, ws_bytes, skip_fill, wait_limit_cycles, reinterpret_cast<cudaStream_t>(stream));
+}
+
+}  // extern "C"

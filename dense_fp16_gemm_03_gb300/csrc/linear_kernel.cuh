@@ -1,0 +1,192 @@
+// The kernels beside the linear products (whose own is gemm_ragged_kernel with
+// an epilogue): the gradient through an activation where no product comes
+// before, and the sum of the bias gradient's parts.
+//
+// A bias gradient is a sum over a group's rows.  Each tile of the product, or
+// block of linear_grad_kernel, adds up its own rows and writes one line of partial
+// sums; linear_sum_kernel adds a group's lines in a fixed order, so results repeat
+// bit for bit, and no atomics or cleared buffers are needed.
+#pragma once
+
+#include "ragged_kernel.cuh"
+
+namespace gemm_f16 {
+
+constexpr int kLinearThreads = 256;
+
+// Row offsets as ragged_table has them (clamped, running maximum; null: one group of all rows), and the number of pieces
+// of `per` rows before each group.  Run by the whole block.
+__device__ __forceinline__ void linear_table(const int32_t *offsets, uint32_t groups, uint32_t rows, uint32_t per, int32_t *row,
+                                             uint32_t *piece)
+{
+    for (uint32_t i = threadIdx.x; i <= groups; i += kLinearThreads)
+        row[i] = offsets ? max(0, min(offsets[i], int32_t(rows))) : (i ? int32_t(rows) : 0);
+    __syncthreads();
+    if (threadIdx.x < 32u) {
+        const uint32_t lane = threadIdx.x, n = groups + 1u;
+        const uint32_t c = (n + 31u) / 32u, b = min(lane * c, n), e = min(b + c, n);
+        int32_t top = 0;
+        for (uint32_t i = b; i < e; ++i) top = max(top, row[i]);
+        int32_t before = top;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int32_t o = __shfl_up_sync(0xffffffffu, before, d);
+            if (lane >= uint32_t(d)) before = max(before, o);
+        }
+        before = __shfl_up_sync(0xffffffffu, before, 1);
+        if (lane == 0) before = 0;
+        for (uint32_t i = b; i < e; ++i) {
+            before = max(before, row[i]);
+            row[i] = before;
+        }
+        __syncwarp();
+        uint32_t sum = 0;
+        for (uint32_t i = b; i < min(e, groups); ++i) sum += (uint32_t(row[i + 1] - row[i]) + per - 1u) / per;
+        uint32_t first = sum;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const uint32_t o = __shfl_up_sync(0xffffffffu, first, d);
+            if (lane >= uint32_t(d)) first += o;
+        }
+        first -= sum;
+        for (uint32_t i = b; i < e; ++i) {
+            piece[i] = first;
+            if (i < groups) first += (uint32_t(row[i + 1] - row[i]) + per - 1u) / per;
+        }
+    }
+    __syncthreads();
+}
+
+// dbias[g] from the lines of partial sums of group g: 32 columns a block, eight threads a column.
+struct LinearSumParams {
+    const float *sums;       // [lines, cols]
+    const int32_t *offsets;  // or null
+    float *dbias;            // [groups, cols]
+    uint32_t groups, rows;
+    uint32_t per, sets;      // rows of a piece, lines of a piece
+    uint32_t cols;
+};
+
+__global__ void __launch_bounds__(kLinearThreads) linear_sum_kernel(const __grid_constant__ LinearSumParams p)
+{
+    __shared__ int32_t s_row[kRagMaxGroups + 1];
+    __shared__ uint32_t s_piece[kRagMaxGroups + 1];
+    __shared__ float s_sum[kLinearThreads / 32][33];
+    ptx::griddep_wait();
+    ptx::griddep_launch_dependents();
+    linear_table(p.offsets, p.groups, p.rows, p.per, s_row, s_piece);
+    const uint32_t g = blockIdx.y, lane = threadIdx.x & 31u, warp = threadIdx.x >> 5;
+    const uint32_t col = blockIdx.x * 32u + lane;
+    const uint32_t first = s_piece[g] * p.sets, end = s_piece[g + 1u] * p.sets;
+    float sum = 0.0f;
+    if (col < p.cols) {
+#pragma unroll 4
+        for (uint32_t i = first + warp; i < end; i += kLinearThreads / 32) sum += p.sums[size_t(i) * p.cols + col];
+    }
+    s_sum[warp][lane] = sum;
+    __syncthreads();
+    if (warp == 0 && col < p.cols) {
+        float all = 0.0f;
+#pragma unroll
+        for (int i = 0; i < kLinearThreads / 32; ++i) all += s_sum[i][lane];
+        p.dbias[size_t(g) * p.cols + col] = all;
+    }
+}
+
+// dz = dy f'(z) and the sums of its columns: a block takes a piece of `per` rows of a group and 256 columns, a warp every
+// eighth row, a lane eight columns (16 bytes).  Bound by HBM for many rows.
+struct LinearGradParams {
+    const void *dy, *z;      // z: null without activation
+    void *dz;                // or null
+    float *sums;             // [pieces, cols] (one piece: dbias itself), or null
+    const int32_t *offsets;  // or null
+    uint32_t groups, rows, cols, per;
+    uint32_t strips;         // ceil(cols / 256)
+    uint32_t act, bf16;
+};
+
+template <int ACT>
+__device__ __forceinline__ void linear_grad_rows(const LinearGradParams &p, uint32_t begin, uint32_t end, uint32_t col, float (&sum)[8])
+{
+    const bool bf16 = p.bf16 != 0u;
+    constexpr uint32_t kStep = kLinearThreads / 32;
+    constexpr int kAhead = 4;
+    const size_t pitch = size_t(p.cols) * 2u;
+    const char *dy = static_cast<const char *>(p.dy) + size_t(col) * 2u;
+    const char *z = static_cast<const char *>(p.z) + size_t(col) * 2u;
+    char *dz = static_cast<char *>(p.dz) + size_t(col) * 2u;
+    for (uint32_t r = begin + (threadIdx.x >> 5); r < end; r += kStep * kAhead) {
+        uint4 d[kAhead], v[kAhead];
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+            const uint32_t row = r + uint32_t(i) * kStep;
+            const bool there = row < end;
+            d[i] = there ? *reinterpret_cast<const uint4 *>(dy + row * pitch) : make_uint4(0u, 0u, 0u, 0u);
+            v[i] = (ACT != GEMM_ACT_NONE && there) ? *reinterpret_cast<const uint4 *>(z + row * pitch) : make_uint4(0u, 0u, 0u, 0u);
+        }
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+            const uint32_t row = r + uint32_t(i) * kStep;
+            if (row >= end) break;
+            const uint32_t a[4] = {d[i].x, d[i].y, d[i].z, d[i].w}, b[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+            uint32_t w[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                float2 g = ragged_unpack(a[j], bf16);
+                const float2 at = ragged_unpack(b[j], bf16);
+                g.x = act::apply_grad<ACT>(g.x, at.x);
+                g.y = act::apply_grad<ACT>(g.y, at.y);
+                sum[2 * j] += g.x;
+                sum[2 * j + 1] += g.y;
+                w[j] = ragged_pack(g.x, g.y, bf16);
+            }
+            if (p.dz) *reinterpret_cast<uint4 *>(dz + row * pitch) = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+    }
+}
+
+__global__ void __launch_bounds__(kLinearThreads) linear_grad_kernel(const __grid_constant__ LinearGradParams p)
+{
+    __shared__ int32_t s_row[kRagMaxGroups + 1];
+    __shared__ uint32_t s_piece[kRagMaxGroups + 1];
+    __shared__ float s_sum[kLinearThreads / 32][kLinearThreads];
+    ptx::griddep_wait();
+    ptx::griddep_launch_dependents();
+    linear_table(p.offsets, p.groups, p.rows, p.per, s_row, s_piece);
+    const uint32_t lane = threadIdx.x & 31u, warp = threadIdx.x >> 5;
+    const uint32_t piece = blockIdx.x / p.strips, strip = blockIdx.x - piece * p.strips;
+    const uint32_t col = strip * 256u + lane * 8u;
+    if (p.dz) {  // rows of no group
+        const uint64_t quads = p.cols / 8u, first = uint64_t(blockIdx.x) * kLinearThreads + threadIdx.x;
+        const uint64_t stride = uint64_t(gridDim.x) * kLinearThreads;
+        const uint32_t head = uint32_t(s_row[0]), end = uint32_t(s_row[p.groups]);
+        uint4 *out = static_cast<uint4 *>(p.dz);
+        for (uint64_t i = first; i < head * quads; i += stride) out[i] = make_uint4(0u, 0u, 0u, 0u);
+        for (uint64_t i = end * quads + first; i < p.rows * quads; i += stride) out[i] = make_uint4(0u, 0u, 0u, 0u);
+    }
+    if (piece >= s_piece[p.groups]) return;
+    uint32_t g = 0, hi = p.groups;  // the group with s_piece[g] <= piece < s_piece[g + 1]
+    while (hi - g > 1u) {
+        const uint32_t mid = (g + hi) >> 1;
+        if (s_piece[mid] <= piece) g = mid;
+        else hi = mid;
+    }
+    const uint32_t begin = uint32_t(s_row[g]) + (piece - s_piece[g]) * p.per;
+    const uint32_t end = min(begin + p.per, uint32_t(s_row[g + 1u]));
+    float sum[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    if (col < p.cols)
+        act::with_kind(p.act, [&](auto kind) { linear_grad_rows<decltype(kind)::value>(p, begin, end, col, sum); });
+    if (p.sums == nullptr) return;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) s_sum[warp][lane * 8u + uint32_t(j)] = sum[j];
+    __syncthreads();
+    const uint32_t mine = strip * 256u + threadIdx.x;
+    if (mine < p.cols) {
+        float all = 0.0f;
+#pragma unroll
+        for (int i = 0; i < kLinearThreads / 32; ++i) all += s_sum[i][threadIdx.x];
+        p.sums[size_t(piece) * p.cols + mine] = all;
+    }
+}
+
+}  // namespace gemm_f16

@@ -79,7 +79,9 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <stdint.h>
+#include <type_traits>
 
+#include "linear_act.cuh"
 #include "ragged_ptx.cuh"
 #include "sched.cuh"
 
@@ -152,8 +154,19 @@ struct RaggedParams {
     uint32_t *error_word;
 };
 
-template <int MODE, int CG, int QCAP, int STAGES>
+// kNT and kNN with an epilogue: what it reads and writes besides `out`.
+struct LinearParams : RaggedParams {
+    const void *bias;      // kNT: [groups, pdim], or null
+    const void *in;        // kNT: the residual, kNN: z, [rows, pdim], or null
+    void *kept;            // kNT: z [rows, pdim], or null
+    float *sums;           // kNN: sums of dx's columns over the rows of each N-side tile and epilogue set, or null
+    uint32_t act;
+};
+
+template <int MODE, int CG, int QCAP, int STAGES, bool EPI = false>
 struct RaggedCfg {
+    static_assert(!EPI || MODE == kNT || MODE == kNN, "epilogue");
+    using Params = std::conditional_t<EPI, LinearParams, RaggedParams>;
     static_assert(CG == 1 || CG == 2, "cta group");
     static constexpr bool kPMn = (MODE == kNN || MODE == kTN);  // M-side operand MN-major
     static constexpr bool kQMn = (MODE == kTN);                 // N-side operand MN-major
@@ -203,6 +216,7 @@ struct RaggedSeg {
     uint32_t g;       // group (kNT, kNN, kTN), row tile (kLoraU, kLoraY)
     uint32_t p0;      // M-side origin of the tile (of the pair)
     uint32_t q0;      // first row (kTN: column) on the N side
+    uint32_t qi;      // kNT, kNN: number of the tile among those of the group's rows
     uint32_t qn;      // rows (columns) of the tile that count
     uint32_t nq;      // the instruction's N
     uint32_t row0;    // kTN: first row of the group; kLoraU: the adapter
@@ -449,6 +463,7 @@ struct RaggedWalk {
                     // equal tiles, in whole steps of the instruction's N (one tile: no division on the way to the
                     // first load)
                     pi = local;
+                    qi = 0u;
                     s.q0 = r0;
                     s.qn = rows;
                     if (rows > uint32_t(QCAP)) {
@@ -460,6 +475,7 @@ struct RaggedWalk {
                         s.qn = min(each, r0 + rows - s.q0);
                     }
                     s.row0 = r0;
+                    s.qi = qi;
                 }
                 s.p0 = pi * 128u * CG;
             }
@@ -670,6 +686,73 @@ __device__ __forceinline__ void ragged_table(const RaggedParams &p, int32_t *tab
     __syncthreads();
 }
 
+__device__ __forceinline__ float ragged_value(uint16_t v, bool bf16)
+{
+    return ragged_unpack(v, bf16).x;
+}
+
+// A piece of 32 rows x 32 columns of a row-major matrix, as an epilogue warp moves it: a lane has four neighbouring columns
+// (8 bytes) of eight rows, a quarter of the warp 64 bytes of a row.  Between that and a column per lane lies a turn through
+// the warp's buffer, 16 lines of 32 words: word l of line i holds rows 2i (low half) and 2i + 1 of column l.
+template <bool USED>
+struct LinearPiece {
+    uint2 v[8];  // rows 2 (4i + lane / 8) + h in v[2i + h]
+    __device__ __forceinline__ void fetch(const void *from, uint32_t pitch, const RaggedSeg &s, uint32_t prow, uint32_t c)
+    {
+        const uint32_t lane = threadIdx.x & 31u, col = prow + 4u * (lane & 7u);
+        const char *at = static_cast<const char *>(from) + (size_t(s.q0) * pitch + col) * 2u;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const uint32_t row = 32u * c + 2u * (4u * uint32_t(i >> 1) + (lane >> 3)) + uint32_t(i & 1);
+            v[i] = (col < pitch && row < s.qn) ? *reinterpret_cast<const uint2 *>(at + size_t(row) * pitch * 2u) : make_uint2(0u, 0u);
+        }
+    }
+    // rows 2i and 2i + 1 of this lane's column in w[i]
+    __device__ __forceinline__ void columns(uint32_t buf, uint32_t (&w)[16]) const
+    {
+        const uint32_t lane = threadIdx.x & 31u;
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint2 a = v[2 * i], b = v[2 * i + 1];
+            ptx::st_shared_v4(buf + (uint32_t(i) * 4u + (lane >> 3)) * 128u + (lane & 7u) * 16u, __byte_perm(a.x, b.x, 0x5410u),
+                              __byte_perm(a.x, b.x, 0x7632u), __byte_perm(a.y, b.y, 0x5410u), __byte_perm(a.y, b.y, 0x7632u));
+        }
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < 16; ++i) w[i] = ptx::ld_shared_u32(buf + uint32_t(i) * 128u + lane * 4u);
+    }
+};
+
+template <>
+struct LinearPiece<false> {
+};
+
+// The same piece the other way: 32 rows of this lane's column in fp32, rounded.
+__device__ __forceinline__ void linear_store(void *to, uint32_t pitch, const RaggedSeg &s, uint32_t prow, uint32_t c, uint32_t buf,
+                                             const uint32_t (&r)[32], bool bf16)
+{
+    const uint32_t lane = threadIdx.x & 31u, col = prow + 4u * (lane & 7u);
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+        ptx::st_shared_u32(buf + uint32_t(i) * 128u + lane * 4u,
+                           ragged_pack(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1]), bf16));
+    __syncwarp();
+    char *at = static_cast<char *>(to) + (size_t(s.q0) * pitch + col) * 2u;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t pr = uint32_t(i) * 4u + (lane >> 3);
+        const uint4 v = ptx::ld_shared_v4(buf + pr * 128u + (lane & 7u) * 16u);
+        const uint32_t row = 32u * c + 2u * pr;
+        if (col >= pitch) continue;
+        if (row < s.qn)
+            ptx::st_global_v2(at + size_t(row) * pitch * 2u, __byte_perm(v.x, v.y, 0x5410u), __byte_perm(v.z, v.w, 0x5410u));
+        if (row + 1u < s.qn)
+            ptx::st_global_v2(at + size_t(row + 1u) * pitch * 2u, __byte_perm(v.x, v.y, 0x7632u), __byte_perm(v.z, v.w, 0x7632u));
+    }
+}
+
 // After an abort: wait (bounded) until no copy into this CTA's ring, or armed on its barriers, is in
 // flight.  Run by one thread of each CTA between the teardown's two cluster barriers; `own` and
 // `peer` point at the two CTAs' fill records (peer 0: none).  The pair's first CTA owns the full
@@ -714,10 +797,11 @@ __device__ __noinline__ void ragged_drain(uint32_t bars, uint32_t rec, bool lead
     }
 }
 
-template <int MODE, int CG, int QCAP, int STAGES>
-__global__ void __launch_bounds__(RaggedCfg<MODE, CG, QCAP, STAGES>::kThreads, 1) gemm_ragged_kernel(const __grid_constant__ RaggedParams p)
+template <int MODE, int CG, int QCAP, int STAGES, bool EPI = false>
+__global__ void __launch_bounds__(RaggedCfg<MODE, CG, QCAP, STAGES, EPI>::kThreads, 1)
+    gemm_ragged_kernel(const __grid_constant__ typename RaggedCfg<MODE, CG, QCAP, STAGES, EPI>::Params p)
 {
-    using Cfg = RaggedCfg<MODE, CG, QCAP, STAGES>;
+    using Cfg = RaggedCfg<MODE, CG, QCAP, STAGES, EPI>;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     const uint32_t raw = ptx::smem_addr(smem_raw);
     const uint32_t base = (raw + 1023u) & ~1023u;
@@ -773,7 +857,7 @@ __global__ void __launch_bounds__(RaggedCfg<MODE, CG, QCAP, STAGES>::kThreads, 1
     else __syncthreads();
     ptx::tc_fence_after_sync();
     const uint32_t tmem_base = *tmem_slot;
-    const bool late = MODE == kNT && p.delta != nullptr;
+    const bool late = MODE == kNT && !EPI && p.delta != nullptr;
     if (!late) ptx::griddep_wait();
     ragged_table<MODE, QCAP>(p, tab_row, tab_tile);
 
@@ -1054,9 +1138,14 @@ __global__ void __launch_bounds__(RaggedCfg<MODE, CG, QCAP, STAGES>::kThreads, 1
         {
             const uint64_t first = uint64_t(blockIdx.x) * (32u * Cfg::kEpiWarps) + (threadIdx.x - 64u);
             const uint64_t stride = uint64_t(gridDim.x) * (32u * Cfg::kEpiWarps);
-            auto zero = [&](uint64_t from, uint64_t count) {  // 16-byte chunks
-                uint4 *dst = static_cast<uint4 *>(p.out) + from;
+            auto zero_in = [&](void *out, uint64_t from, uint64_t count) {  // 16-byte chunks
+                uint4 *dst = static_cast<uint4 *>(out) + from;
                 for (uint64_t i = first; i < count; i += stride) dst[i] = make_uint4(0u, 0u, 0u, 0u);
+            };
+            auto zero = [&](uint64_t from, uint64_t count) {
+                zero_in(p.out, from, count);
+                if constexpr (EPI)
+                    if (p.kept != nullptr) zero_in(p.kept, from, count);
             };
             if constexpr (MODE == kNT || MODE == kNN) {
                 const uint64_t pitch = uint64_t(p.pdim) / 8u;
@@ -1078,8 +1167,19 @@ __global__ void __launch_bounds__(RaggedCfg<MODE, CG, QCAP, STAGES>::kThreads, 1
         bool let_in = false;
         bool published = false, taken = false, stopped = false;  // sk: this CTA's flags
         walk.template each<false>([&](const RaggedSeg &s) {
-            const bool ok = ragged_wait<CG>(bar_acc_full(acc), acc_phase, p, abort_flag, kRagErrAccFull);
             const bool split = MODE != kTN && p.sk != 0u && (s.lo != 0u || s.hi != s.kb);
+            // what the epilogue takes besides the product is on its way before the product is there
+            LinearPiece<EPI> piece_in;
+            float bias = 0.0f;
+            if constexpr (EPI) {
+                const uint32_t prow = s.p0 + rank * 128u + quarter * 32u;
+                if (!split || s.hi == s.kb) {
+                    if (p.in != nullptr) piece_in.fetch(p.in, p.pdim, s, prow, set);
+                    if (MODE == kNT && p.bias != nullptr && prow + lane < p.pdim)
+                        bias = ragged_value(static_cast<const uint16_t *>(p.bias)[size_t(s.g) * p.pdim + prow + lane], bf16);
+                }
+            }
+            const bool ok = ragged_wait<CG>(bar_acc_full(acc), acc_phase, p, abort_flag, kRagErrAccFull);
             // the warps meet at named barriers below when the tile is split: stop together
             if (MODE != kTN && p.sk) {
                 if (!ptx::named_barrier_and(1, 32 * Cfg::kEpiWarps, ok)) {
@@ -1275,6 +1375,51 @@ __global__ void __launch_bounds__(RaggedCfg<MODE, CG, QCAP, STAGES>::kThreads, 1
                             if ((stored >> j) & 1u) out[j * p.pdim] = word;  // (within a tile: 32 bits)
                         }
                     }
+                } else if (EPI && live) {
+                    if constexpr (EPI)
+                        act::with_kind(p.act, [&](auto kind) {
+                            constexpr int kAct = decltype(kind)::value;
+                            float sum = 0.0f;
+                            for (uint32_t c = set; c < chunks; c += Cfg::kEpiSets) {
+                                uint32_t r[32], w[16];
+                                if (p.in != nullptr) {
+                                    piece_in.columns(buf, w);
+                                    if (c + Cfg::kEpiSets < chunks) piece_in.fetch(p.in, p.pdim, s, prow, c + Cfg::kEpiSets);
+                                } else {
+#pragma unroll
+                                    for (int i = 0; i < 16; ++i) w[i] = 0u;
+                                }
+                                chunk32(c, r);
+                                if constexpr (MODE == kNT) {
+#pragma unroll
+                                    for (int j = 0; j < 32; ++j) r[j] = __float_as_uint(__uint_as_float(r[j]) + bias);
+                                    if (p.kept != nullptr) linear_store(p.kept, p.pdim, s, prow, c, buf, r, bf16);
+#pragma unroll
+                                    for (int i = 0; i < 16; ++i) {
+                                        const float2 add = ragged_unpack(w[i], bf16);
+                                        r[2 * i] = __float_as_uint(act::apply<kAct>(__uint_as_float(r[2 * i])) + add.x);
+                                        r[2 * i + 1] = __float_as_uint(act::apply<kAct>(__uint_as_float(r[2 * i + 1])) + add.y);
+                                    }
+                                } else {
+#pragma unroll
+                                    for (int i = 0; i < 16; ++i) {
+                                        const float2 z = ragged_unpack(w[i], bf16);
+                                        r[2 * i] = __float_as_uint(act::apply_grad<kAct>(__uint_as_float(r[2 * i]), z.x));
+                                        r[2 * i + 1] = __float_as_uint(act::apply_grad<kAct>(__uint_as_float(r[2 * i + 1]), z.y));
+                                    }
+                                    if (p.sums != nullptr) {
+#pragma unroll
+                                        for (uint32_t j = 0; j < 32u; ++j)
+                                            if (32u * c + j < s.qn) sum += __uint_as_float(r[j]);
+                                    }
+                                }
+                                linear_store(p.out, p.pdim, s, prow, c, buf, r, bf16);
+                            }
+                            if (MODE == kNN && p.sums != nullptr && prow + lane < p.pdim) {
+                                const uint32_t slot = (tab_tile[s.g] / p.tiles_p + s.qi) * uint32_t(Cfg::kEpiSets) + set;
+                                p.sums[size_t(slot) * p.pdim + prow + lane] = sum;
+                            }
+                        });
                 } else if (live) {
                     // rows t on columns: 32 x 32 pieces transposed through shared memory.  A word holds rows
                     // 2i and 2i + 1 of one output column; a lane reads four columns' words and takes them apart.
@@ -1480,301 +1625,6 @@ __global__ void __launch_bounds__(RaggedCfg<MODE, CG, QCAP, STAGES>::kThreads, 1
     }
     if constexpr (CG == 2) ptx::cluster_sync();
     if (warp == 1) ptx::tmem_dealloc<CG>(tmem_base, Cfg::kTmemCols);
-}
-
-// kTN: every group's tensor maps with the rows ending at the group's end, so that TMA fills the rest of its last K block
-// with zeros (32 uneven groups of 16384 rows in all, 4096 x 4096: 442 us with the helper zeroing each tile's last
-// block, 358 so).  One block per group, one warp per map; some 3 us in front of the product.
-struct RaggedMapsParams {
-    CUtensorMap maps[4];
-    const int32_t *offsets;
-    uint32_t groups, rows;
-    uint32_t have;      // bit i: maps[i] is one
-    CUtensorMap *out;   // [groups][4]
-};
-
-__global__ void __launch_bounds__(128) ragged_maps_kernel(const __grid_constant__ RaggedMapsParams p)
-{
-    __shared__ __align__(128) CUtensorMap s_map[4];
-    ptx::griddep_wait();
-    const uint32_t lane = threadIdx.x & 31u, i = threadIdx.x >> 5, g = blockIdx.x;
-    // the group's end as ragged_table has it: the largest of the clamped offsets up to it
-    int32_t end = 0;
-    for (uint32_t k = lane; k <= g + 1u; k += 32u) end = max(end, min(p.offsets[k], int32_t(p.rows)));
-    end = __reduce_max_sync(0xffffffffu, end);
-    if ((p.have >> i) & 1u) {
-        reinterpret_cast<uint32_t *>(&s_map[i])[lane] = reinterpret_cast<const uint32_t *>(&p.maps[i])[lane];
-        __syncwarp();
-        if (lane == 0) ptx::tensormap_set_dim1(ptx::smem_addr(&s_map[i]), uint32_t(max(end, 1)));
-        __syncwarp();
-        ptx::tensormap_publish(p.out + 4u * g + i, ptx::smem_addr(&s_map[i]));
-    }
-    ptx::griddep_launch_dependents();
-}
-
-// kTN with few tiles: the rows of a group are cut into parts of `part_rows` (a multiple of a K block), each part's sum
-// goes to a matrix of its own in fp32, and this kernel adds a group's parts, in order, and rounds once.  Bound by L2 for
-// large matrices, else by its launch.  One block row per group.  (10560 rows in one group, 64 x 248: 63.6 us whole, 15.6
-// in parts; 27407 rows in 3 groups, 640 x 104: 89.3 and 18.7; 9426 in 2, 144 x 3328: 32.6 and 25.3.)
-constexpr uint32_t kRagPartGroups = 128;
-
-struct RaggedPartsParams {
-    const float4 *parts;  // [parts][n * k / 4]
-    const int32_t *offsets;
-    void *out;            // [groups, n, k]
-    uint32_t groups, rows, part_rows;
-    uint32_t quads;       // n * k / 4
-    uint32_t out32, bf16;
-};
-
-__global__ void __launch_bounds__(256) ragged_parts_kernel(const __grid_constant__ RaggedPartsParams p)
-{
-    __shared__ int32_t s_row[kRagPartGroups + 1];
-    __shared__ uint32_t s_parts[kRagPartGroups];
-    ptx::griddep_wait();
-    ptx::griddep_launch_dependents();
-    const uint32_t i = threadIdx.x, g = blockIdx.y;
-    if (i <= p.groups) s_row[i] = max(0, min(p.offsets[i], int32_t(p.rows)));
-    __syncthreads();
-    if (i < p.groups) {  // as ragged_table has them
-        int32_t begin = 0;
-        for (uint32_t j = 0; j <= i; ++j) begin = max(begin, s_row[j]);
-        s_parts[i] = uint32_t((max(begin, s_row[i + 1]) - begin + int32_t(p.part_rows) - 1) / int32_t(p.part_rows));
-    }
-    __syncthreads();
-    uint32_t first = 0;
-    for (uint32_t j = 0; j < g; ++j) first += s_parts[j];
-    const uint32_t count = s_parts[g];
-    const uint32_t q = blockIdx.x * 256u + i;
-    if (q >= p.quads) return;
-    const float4 *from = p.parts + size_t(first) * p.quads + q;
-    float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-    for (uint32_t j = 0; j < count; ++j) {
-        const float4 v = from[size_t(j) * p.quads];
-        sum.x += v.x;
-        sum.y += v.y;
-        sum.z += v.z;
-        sum.w += v.w;
-    }
-    const size_t at = size_t(g) * p.quads + q;
-    if (p.out32)
-        static_cast<float4 *>(p.out)[at] = sum;
-    else
-        static_cast<uint2 *>(p.out)[at] = make_uint2(ragged_pack(sum.x, sum.y, p.bf16 != 0u), ragged_pack(sum.z, sum.w, p.bf16 != 0u));
-}
-
-// Adapters without the tensor cores: with an adapter to nearly every row, all of the work is reading a and b once, and
-// each row sees its own adapter only.  u = scale x a^T and delta = u b^T stay in fp32.  They run beside the projection,
-// which starts at once and waits for delta in its epilogue.  16 rows with 16 adapters of rank 16, 8192 x 4096, take 22 us,
-// as without adapters 20; 64 with 64 take 30 (as K blocks of the projection 36): there the two kernels, 7 us each on an
-// idle GPU, end after the projection's loads.
-//
-// For a few rows of a low rank a cluster of eight CTAs takes a row through both steps and trades u through distributed
-// shared memory: one launch fewer, 2 to 4 us of the host's time, and the GPU's with it, then by the two kernels: 16 rows,
-// rank 16, 8192 x 4096, 21.7 us and 23.6; 32 rows 23.1 and 24.7; 1 row, 4096 x 4096, 14.4 and 13.9.  But 64 rows take 32.6
-// and 29.0, and rank 64 (16 rows, 11008 x 4096) 35.8 and 33.3: a row's work on eight SMs only.
-struct LoraFewParams {
-    const void *x, *a, *b;
-    const int32_t *ids;
-    const float *scale;
-    float *u;       // [rows, rank]
-    float *delta;   // [rows, n]
-    uint32_t rows, n, k, rank, adapters, bf16;
-};
-
-// Four of a row's u's (before the scale) by WARPS warps that share k: each lane multiplies 8 elements at a time.  The sums
-// of a single warp are in all lanes; of four, thread t returns number t mod 4, and s_sum is the block's.
-template <int WARPS>
-__device__ __forceinline__ float lora_dot4(const LoraFewParams &p, uint32_t row, int32_t id, uint32_t r0, float (*s_sum)[4])
-{
-    const uint32_t lane = threadIdx.x & 31u, warp = threadIdx.x >> 5;
-    const bool bf16 = p.bf16 != 0u;
-    const uint4 *x = reinterpret_cast<const uint4 *>(static_cast<const char *>(p.x) + size_t(row) * p.k * 2u);
-    const char *a = static_cast<const char *>(p.a) + (size_t(id) * p.rank + r0) * p.k * 2u;
-    float sum[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 4
-    for (uint32_t i = WARPS == 1 ? lane : threadIdx.x; i < p.k / 8u; i += 32u * WARPS) {
-        const uint4 xv = x[i];
-        uint4 av[4];
-#pragma unroll
-        for (int r = 0; r < 4; ++r) av[r] = reinterpret_cast<const uint4 *>(a + size_t(r) * p.k * 2u)[i];
-        const uint32_t xw[4] = {xv.x, xv.y, xv.z, xv.w};
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const float2 xf = ragged_unpack(xw[j], bf16);
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const uint32_t aw = j == 0 ? av[r].x : j == 1 ? av[r].y : j == 2 ? av[r].z : av[r].w;
-                const float2 af = ragged_unpack(aw, bf16);
-                sum[r] = fmaf(xf.x, af.x, sum[r]);
-                sum[r] = fmaf(xf.y, af.y, sum[r]);
-            }
-        }
-    }
-#pragma unroll
-    for (int r = 0; r < 4; ++r)
-#pragma unroll
-        for (int d = 16; d > 0; d >>= 1) sum[r] += __shfl_xor_sync(0xffffffffu, sum[r], d);
-    const uint32_t r = threadIdx.x & 3u;
-    if constexpr (WARPS == 1) {
-        return r == 0u ? sum[0] : r == 1u ? sum[1] : r == 2u ? sum[2] : sum[3];
-    } else {
-        __syncthreads();  // the four before have been read
-        if (lane == 0)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) s_sum[warp][i] = sum[i];
-        __syncthreads();
-        return (s_sum[0][r] + s_sum[1][r]) + (s_sum[2][r] + s_sum[3][r]);
-    }
-}
-
-// 128 columns of a row's delta by one warp.  LANES lanes share a row of b, 16 bytes each, with their part of u in
-// registers; eight rows' loads are in flight.  (One lane to a row of b read a line per lane and load.)
-template <int LANES>
-__device__ __forceinline__ void lora_columns(const LoraFewParams &p, uint32_t row, int32_t id, uint32_t col0, const float (&u)[8])
-{
-    const uint32_t lane = threadIdx.x & 31u, part = lane % LANES;
-    const bool bf16 = p.bf16 != 0u, live = 8u * part < p.rank;
-    constexpr uint32_t kRows = 32 / LANES;  // rows of b a warp reads at a time
-    constexpr uint32_t kFlight = 8;         // and such reads in flight
-    const char *b = static_cast<const char *>(p.b) + size_t(id) * p.n * p.rank * 2u + 16u * part;
-#pragma unroll 1
-    for (uint32_t i0 = 0; i0 < 128u; i0 += kFlight * kRows) {
-        uint4 v[kFlight];
-#pragma unroll
-        for (int i = 0; i < int(kFlight); ++i) {
-            const uint32_t col = col0 + i0 + uint32_t(i) * kRows + lane / LANES;
-            v[i] = (live && col < p.n && i0 + uint32_t(i) * kRows < 128u)
-                       ? *reinterpret_cast<const uint4 *>(b + size_t(col) * p.rank * 2u)
-                       : make_uint4(0u, 0u, 0u, 0u);
-        }
-#pragma unroll
-        for (int i = 0; i < int(kFlight); ++i) {
-            if (i0 + uint32_t(i) * kRows >= 128u) continue;
-            const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
-            float sum = 0.0f;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const float2 f = ragged_unpack(w[j], bf16);
-                sum = fmaf(f.x, u[2 * j], sum);
-                sum = fmaf(f.y, u[2 * j + 1], sum);
-            }
-#pragma unroll
-            for (int d = LANES / 2; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-            const uint32_t col = col0 + i0 + uint32_t(i) * kRows + lane / LANES;
-            if (part == 0u && col < p.n) p.delta[size_t(row) * p.n + col] = sum;
-        }
-    }
-}
-
-// An item is a row and four of its u's: a block's (WARPS = 4), or, where there are more of them than the GPU has blocks at
-// a time, a warp's.  (Here and below items are counted in 32 bits: rows that have more go by the tensor cores.)
-template <int WARPS>
-__global__ void __launch_bounds__(128) lora_shrink_kernel(const __grid_constant__ LoraFewParams p)
-{
-    __shared__ float s_sum[4][4];
-    ptx::griddep_wait();
-    // (after the wait: what the next kernels read from before this one is complete as well)
-    ptx::griddep_launch_dependents();
-    constexpr uint32_t kItems = 4 / WARPS;  // of a block at a time
-    const uint32_t parts = p.rank / 4u;
-    for (uint32_t item = blockIdx.x * kItems + (WARPS == 1 ? threadIdx.x >> 5 : 0u); item < p.rows * parts; item += gridDim.x * kItems) {
-        const uint32_t row = item / parts, r0 = (item - row * parts) * 4u;
-        const int32_t id = p.ids[row];
-        if (uint32_t(id) >= p.adapters) continue;
-        const float v = lora_dot4<WARPS>(p, row, id, r0, s_sum) * (p.scale ? p.scale[id] : 1.0f);
-        const uint32_t t = WARPS == 1 ? threadIdx.x & 31u : threadIdx.x;
-        if (t < 4u) p.u[size_t(row) * p.rank + r0 + t] = v;
-    }
-}
-
-// An item, a warp's, is a row and 128 of its columns.
-template <int LANES>
-__global__ void __launch_bounds__(128) lora_expand_kernel(const __grid_constant__ LoraFewParams p)
-{
-    // The product behind this kernel reads nothing of the kernel before this one; that one has waited for all before it.
-    ptx::griddep_launch_dependents();
-    ptx::griddep_wait();
-    const uint32_t part = (threadIdx.x & 31u) % LANES, parts = (p.n + 127u) / 128u;
-    for (uint32_t item = blockIdx.x * 4u + (threadIdx.x >> 5); item < p.rows * parts; item += gridDim.x * 4u) {
-        const uint32_t row = item / parts;
-        const int32_t id = p.ids[row];
-        if (uint32_t(id) >= p.adapters) continue;
-        float u[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) u[j] = 8u * part < p.rank ? p.u[size_t(row) * p.rank + 8u * part + j] : 0.0f;
-        lora_columns<LANES>(p, row, id, (item - row * parts) * 128u, u);
-    }
-}
-
-// Both steps of one row by a cluster.
-constexpr uint32_t kLoraCluster = 8;
-
-template <int LANES>
-__global__ void __launch_bounds__(128) lora_rows_kernel(const __grid_constant__ LoraFewParams p)
-{
-    __shared__ float s_sum[4][4];
-    __shared__ float s_u[32];
-    ptx::cluster_sync();  // every CTA of the cluster runs: its shared memory may be written
-    ptx::griddep_wait();
-    ptx::griddep_launch_dependents();  // (after the wait, as above)
-    const uint32_t part = (threadIdx.x & 31u) % LANES, rank = ptx::cluster_ctarank(), row = blockIdx.x / kLoraCluster;
-    const int32_t id = p.ids[row];
-    if (uint32_t(id) >= p.adapters) return;  // (the same for the whole cluster)
-    for (uint32_t r0 = 4u * rank; r0 < p.rank; r0 += 4u * kLoraCluster) {
-        const float v = lora_dot4<4>(p, row, id, r0, s_sum) * (p.scale ? p.scale[id] : 1.0f);
-        if (threadIdx.x < 4u * kLoraCluster)  // four values to every CTA
-            ptx::st_shared_cluster_u32(ptx::map_to_rank(ptx::smem_addr(&s_u[r0 + (threadIdx.x & 3u)]), threadIdx.x >> 2),
-                                       __float_as_uint(v));
-    }
-    __syncwarp();
-    ptx::cluster_sync();
-    float u[8];
-#pragma unroll
-    for (int j = 0; j < 8; ++j) u[j] = 8u * part < p.rank ? s_u[8u * part + j] : 0.0f;
-    for (uint32_t item = rank * 4u + (threadIdx.x >> 5); item < (p.n + 127u) / 128u; item += 4u * kLoraCluster)
-        lora_columns<LANES>(p, row, id, item * 128u, u);
-}
-
-// Lists for the tensor cores' form: the adapters present in each tile of `per` rows (per <= 256), in order of first
-// appearance.  Rows with an id outside [0, adapters) have none.  Two cuttings of the same rows at once: `tiles` blocks for
-// the first, the rest for the second.  Bound by latency, some 4 us.
-struct LoraListParams {
-    const int32_t *ids;
-    uint32_t rows, adapters, tiles;
-    uint32_t per[2];
-    int32_t *counts[2], *list[2];
-};
-
-__global__ void __launch_bounds__(256) lora_list_kernel(const __grid_constant__ LoraListParams p)
-{
-    __shared__ __align__(16) int32_t s_id[256];
-    __shared__ uint32_t s_warp[8];
-    ptx::griddep_wait();
-    const uint32_t cut = blockIdx.x < p.tiles ? 0u : 1u, tile = blockIdx.x - cut * p.tiles, per = p.per[cut];
-    const uint32_t t = threadIdx.x, row = tile * per + t;
-    int32_t id = (p.adapters != 0u && t < per && row < p.rows) ? p.ids[row] : -1;
-    if (uint32_t(id) >= p.adapters) id = -1;
-    s_id[t] = id;
-    __syncthreads();
-    // the first row with its id: every earlier one differs (four at a time, the same words for the whole warp)
-    bool first = id >= 0;
-    for (uint32_t i = 0; i < (t | 31u) + 1u; i += 4u) {
-        const int4 v = *reinterpret_cast<const int4 *>(s_id + i);
-        first &= !((v.x == id && i < t) || (v.y == id && i + 1u < t) || (v.z == id && i + 2u < t) || (v.w == id && i + 3u < t));
-    }
-    const uint32_t vote = __ballot_sync(0xffffffffu, first);
-    if ((t & 31u) == 0) s_warp[t >> 5] = __popc(vote);
-    __syncthreads();
-    uint32_t at = __popc(vote & ((1u << (t & 31u)) - 1u)), total = 0;
-    for (uint32_t w = 0; w < 8u; ++w) {
-        if (w < (t >> 5)) at += s_warp[w];
-        total += s_warp[w];
-    }
-    if (first) p.list[cut][size_t(tile) * per + at] = id;
-    if (t == 0) p.counts[cut][tile] = int32_t(total);
-    ptx::griddep_launch_dependents();
 }
 
 }  // namespace gemm_f16

@@ -1,0 +1,189 @@
+"""ctypes binding of include/gemm_linear.h (same entry-point names): products
+with a bias, an activation and a residual in their epilogue, and their gradients.
+
+Argument marshalling only, as in ``ragged``, with its rules for operands, streams,
+outputs and workspaces.  ``w`` is one matrix [n, k], or with ``offsets`` one per
+group of rows [groups, n, k], as the grouped products take them; bias and
+dbias then have a line per group.  ``act``: None or "none", "relu", "relu2",
+"gelu", "gelu_tanh" or "silu".
+
+A layer y = f(x w^T + bias) and its backward pass:
+
+    y, z = gemm_linear_nt(x, w, bias=bias, act="gelu", keep=True, workspace=ws)
+    dz, dbias = gemm_linear_grad(dy, z, act="gelu", bias_grad=True, workspace=ws)
+    dx = gemm_linear_nn(dz, w, workspace=ws)
+    dw = ragged.gemm_grouped_tn(dz, x, ...)
+
+and where another layer's activation lies below, gemm_linear_nn(dz, w, z=z_below,
+act=..., bias_grad=True) gives that layer's dz and dbias at once.
+"""
+import ctypes
+
+from . import gemm as _gemm
+from .ragged import _check, _dtype, _need, _offsets, _operand, _out, _size, _stream, _workspace
+
+ACTS = {None: 0, "none": 0, "relu": 1, "relu2": 2, "gelu": 3, "gelu_tanh": 4, "silu": 5}
+
+# every symbol the public header declares
+EXPORTED = ["gemm_linear_workspace_size", "gemm_linear_nt", "gemm_linear_nn", "gemm_linear_grad", "gemm_linear_stall_test"]
+
+_lib = None
+
+
+def lib():
+    """The library of ``gemm.lib()`` with this header's signatures."""
+    global _lib
+    if _lib is not None:
+        return _lib
+    L = _gemm.lib()
+    i32, i64, u32, vp, sz = ctypes.c_int32, ctypes.c_int64, ctypes.c_uint32, ctypes.c_void_p, ctypes.c_size_t
+    kind = ctypes.c_int
+    sig = {
+        "gemm_linear_workspace_size": [i64, i64, i64, i64, ctypes.POINTER(ctypes.c_size_t)],
+        "gemm_linear_nt": [kind, kind, i64, i64, i64, i64, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp],
+        "gemm_linear_nn": [kind, kind, i64, i64, i64, i64, vp, vp, vp, vp, vp, vp, vp, sz, vp],
+        "gemm_linear_grad": [kind, kind, i64, i64, i64, vp, vp, vp, vp, vp, vp, sz, vp],
+        "gemm_linear_stall_test": [i32, kind, kind, i64, i64, i64, i64, vp, vp, vp, vp, vp, vp, vp, sz, u32, ctypes.c_longlong, vp],
+    }
+    for name, args in sig.items():
+        f = getattr(L, name)
+        f.restype = ctypes.c_int
+        f.argtypes = args
+    _lib = L
+    return L
+
+
+def _act(act):
+    code = ACTS.get(act)
+    if code is None:
+        raise ValueError("act must be one of %s" % ", ".join(repr(a) for a in ACTS))
+    return code
+
+
+def _groups(offsets, dev):
+    """(number of groups, address of the offsets, leading sizes of what each group has of its own)"""
+    if offsets is None:
+        return 1, None, ()
+    groups = _offsets(offsets, dev)
+    return groups, offsets.data_ptr(), (groups,)
+
+
+def _weights(w, stack, which, size, kind, dev):
+    """n and k of the weights, whose extent `which` has to be `size`."""
+    if w.dim() != len(stack) + 2:
+        raise ValueError("w must be [groups, n, k]" if stack else "w must be [n, k] without offsets")
+    n, k = w.shape[-2:]
+    _need(w, "w", stack + ((n, size) if which == "k" else (size, k)), kind, dev)
+    return n, k
+
+
+def _optional(t, what, shape, dtype, dev):
+    if t is None:
+        return None
+    _need(t, what, shape, dtype, dev)
+    return t.data_ptr()
+
+
+def gemm_linear_workspace_size(groups, rows, n, k):
+    return _size("gemm_linear_workspace_size", groups, rows, n, k)
+
+
+def gemm_linear_nt(x, w, bias=None, residual=None, act=None, offsets=None, keep=False, y=None, z=None, workspace=None, stream=None):
+    """y = f(x w^T + bias) + residual; with `keep` (y, z), where z = x w^T + bias is what the backward pass needs.
+
+    x [rows, k], w [n, k], bias [n], residual [rows, n] (y may be the residual itself); with offsets [groups + 1] int32 on the
+    device w [groups, n, k], bias [groups, n], and rows of no group are zero."""
+    lib()
+    code = _act(act)
+    dev, kind = _operand(x, "x", 2), x.dtype
+    groups, ends, stack = _groups(offsets, dev)
+    rows, k = x.shape
+    n, _ = _weights(w, stack, "k", k, kind, dev)
+    dtype = _dtype(kind)
+    b = _optional(bias, "bias", stack + (n,), kind, dev)
+    r = _optional(residual, "residual", (rows, n), kind, dev)
+    if keep:
+        z = _out(z, "z", (rows, n), kind, dev)
+    elif z is not None:
+        raise ValueError("z is written with keep only")
+    y = _out(y, "y", (rows, n), kind, dev)
+    ws, ws_bytes = _workspace(workspace, dev)
+    st = _lib.gemm_linear_nt(dtype, code, groups, rows, n, k, ends, x.data_ptr(), w.data_ptr(), b, r,
+                             z.data_ptr() if keep else None, y.data_ptr(), ws, ws_bytes, _stream(stream, dev))
+    _check(st, "gemm_linear_nt")
+    return (y, z) if keep else y
+
+
+def gemm_linear_nn(dy, w, z=None, act=None, offsets=None, bias_grad=False, dx=None, dbias=None, workspace=None, stream=None):
+    """dx = (dy w) * f'(z), the gradient of z = x w^T + bias one layer below; with `bias_grad` (dx, dbias), dbias the sum of dx
+    over the rows (of each group) in float32.
+
+    dy [rows, n], w [n, k] or [groups, n, k], z [rows, k] (not needed without `act`; dx may be z itself)."""
+    lib()
+    code = _act(act)
+    dev, kind = _operand(dy, "dy", 2), dy.dtype
+    groups, ends, stack = _groups(offsets, dev)
+    rows, n = dy.shape
+    _, k = _weights(w, stack, "n", n, kind, dev)
+    dtype = _dtype(kind)
+    if code and z is None:
+        raise ValueError("z is needed for act=%r" % (act,))
+    at = _optional(z, "z", (rows, k), kind, dev)
+    dx = _out(dx, "dx", (rows, k), kind, dev)
+    db = None
+    if bias_grad:
+        dbias = _out(dbias, "dbias", stack + (k,), _gemm._tm().float32, dev)
+        db = dbias.data_ptr()
+    elif dbias is not None:
+        raise ValueError("dbias is written with bias_grad only")
+    ws, ws_bytes = _workspace(workspace, dev)
+    st = _lib.gemm_linear_nn(dtype, code, groups, rows, n, k, ends, dy.data_ptr(), w.data_ptr(), at, dx.data_ptr(), db, ws, ws_bytes,
+                             _stream(stream, dev))
+    _check(st, "gemm_linear_nn")
+    return (dx, dbias) if bias_grad else dx
+
+
+def gemm_linear_grad(dy, z=None, act=None, offsets=None, bias_grad=False, dz=None, dbias=None, workspace=None, stream=None):
+    """dz = dy * f'(z); with `bias_grad` (dz, dbias), dbias the sum of dz over the rows (of each group) in float32.
+
+    dy, z [rows, n]; dz may be dy or z.  Without `act` dz is dy, which is returned as it is unless another dz is given."""
+    lib()
+    code = _act(act)
+    dev, kind = _operand(dy, "dy", 2), dy.dtype
+    groups, ends, stack = _groups(offsets, dev)
+    rows, n = dy.shape
+    dtype = _dtype(kind)
+    if code and z is None:
+        raise ValueError("z is needed for act=%r" % (act,))
+    at = _optional(z, "z", (rows, n), kind, dev)
+    if code or dz is not None:
+        dz = _out(dz, "dz", (rows, n), kind, dev)
+        to = dz.data_ptr()
+    else:
+        dz, to = dy, None
+    db = None
+    if bias_grad:
+        dbias = _out(dbias, "dbias", stack + (n,), _gemm._tm().float32, dev)
+        db = dbias.data_ptr()
+    elif dbias is not None:
+        raise ValueError("dbias is written with bias_grad only")
+    ws, ws_bytes = _workspace(workspace, dev)
+    st = _lib.gemm_linear_grad(dtype, code, groups, rows, n, ends, dy.data_ptr(), at, to, db, ws, ws_bytes, _stream(stream, dev))
+    _check(st, "gemm_linear_grad")
+    return (dz, dbias) if bias_grad else dz
+
+
+def gemm_linear_stall_test(mode, first, w, extra, out, dbias, workspace, skip_fill, wait_limit_cycles, act=None, offsets=None, stream=None):
+    """Status of the failure-detection launch (mode 0: nt with a residual, 1: nn with z and dbias)."""
+    lib()
+    dev, kind = _operand(first, "first", 2), first.dtype
+    groups, ends, stack = _groups(offsets, dev)
+    rows = first.shape[0]
+    n, k = _weights(w, stack, "n" if mode else "k", first.shape[1], kind, dev)
+    shape = (rows, k if mode else n)
+    _need(out, "out", shape, kind, dev)
+    more = _optional(extra, "extra", shape, kind, dev)
+    db = _optional(dbias, "dbias", stack + (k,), _gemm._tm().float32, dev)
+    ws, ws_bytes = _workspace(workspace, dev)
+    return _lib.gemm_linear_stall_test(mode, _dtype(kind), _act(act), groups, rows, n, k, ends, first.data_ptr(), w.data_ptr(), more,
+                                       out.data_ptr(), db, ws, ws_bytes, skip_fill, wait_limit_cycles, _stream(stream, dev))
