@@ -1,12 +1,13 @@
 // C ABI of the ragged products and the router (declared in include/gemm_ragged.h):
 // argument validation, the choice of kernel variant, workspace layout, tensor
-// maps and launches.  The kernels are in ragged_kernel.cuh, ragged_side_kernels.cuh and
-// route_kernel.cuh.
+// maps and launches.  The kernels are in ragged_kernel.cuh, ragged_side_kernels.cuh,
+// route_kernel.cuh and route_scored_kernel.cuh.
 #include <math.h>
 
 #include "ragged_launch.cuh"
 #include "ragged_side_kernels.cuh"
 #include "route_kernel.cuh"
+#include "route_scored_kernel.cuh"
 
 using namespace gemm_f16;
 
@@ -711,23 +712,22 @@ gemm_status_t gemm_route_workspace_size(int64_t rows, int64_t experts, int64_t t
 #define ROUTE_TOPK(V) reinterpret_cast<const void *>(&route_topk_kernel<V, 16 * kRouteRows>)
 #define ROUTE_GRAD(V) reinterpret_cast<const void *>(&route_grad_kernel<V>)
 
-gemm_status_t gemm_route_topk(gemm_dtype_t dtype, int64_t rows, int64_t experts, int64_t top, int32_t renorm, const void *logits,
-                              int32_t *ids, float *weights, int32_t *offsets, int32_t *order, int32_t *position, void *workspace,
-                              size_t ws_bytes, gemm_stream_t stream)
+// The checks and parameters that both routers' calls begin with; *done where nothing is left to do.
+static gemm_status_t route_begin(RouteParams *p, gemm_dtype_t dtype, int64_t rows, int64_t experts, int64_t top, int32_t renorm,
+                                 const void *logits, int32_t *ids, float *weights, int32_t *offsets, int32_t *order,
+                                 int32_t *position, void *workspace, size_t ws_bytes, cudaStream_t s, bool *done)
 {
-    gemm_status_t st = check_route(dtype, rows, experts, top);
-    if (st != GEMM_OK) return st;
     const bool any = rows > 0;
-    st = check_pointer(logits, any);
+    gemm_status_t st = check_pointer(logits, any);
     if (st == GEMM_OK) st = check_pointer(offsets, true, 4);
     for (const void *ptr : {static_cast<const void *>(ids), static_cast<const void *>(weights), static_cast<const void *>(order),
                             static_cast<const void *>(position)})
         if (st == GEMM_OK) st = check_pointer(ptr, any, 4);
     if (st != GEMM_OK) return st;
-    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     DeviceState state;
     st = current_device_state(&state);
     if (st != GEMM_OK) return st;
+    *done = !any;
     if (!any) {
         if (cudaMemsetAsync(offsets, 0, size_t(experts + 1) * 4u, s) != cudaSuccess) {
             cudaGetLastError();
@@ -740,30 +740,49 @@ gemm_status_t gemm_route_topk(gemm_dtype_t dtype, int64_t rows, int64_t experts,
         if (workspace == nullptr || ws_bytes < size_t(blocks + 1) * size_t(experts) * 4u) return GEMM_ERR_WORKSPACE;
         if (reinterpret_cast<uintptr_t>(workspace) & 255u) return GEMM_ERR_ALIGNMENT;
     }
+    memset(p, 0, sizeof(*p));
+    p->logits = logits;
+    p->dtype = uint32_t(dtype);
+    p->rows = uint32_t(rows);
+    p->experts = uint32_t(experts);
+    p->top = uint32_t(top);
+    p->renorm = renorm != 0;
+    p->blocks = uint32_t(blocks);
+    p->ids = ids;
+    p->weights = weights;
+    p->offsets = offsets;
+    p->order = order;
+    p->position = position;
+    p->hist = static_cast<int32_t *>(workspace);
+    p->totals = p->hist ? p->hist + size_t(blocks) * size_t(experts) : nullptr;
+    return GEMM_OK;
+}
+
+// The choice by kernel `fn` with its parameters `own`, then the places of all choices.
+static gemm_status_t route_launch(const void *fn, RouteParams &p, void *own, cudaStream_t s)
+{
+    void *args[1] = {own}, *base[1] = {&p};
+    if (p.blocks == 1u) return launch(fn, dim3(1, 1, 1), kRouteThreads, 0, 1, args, s);
+    gemm_status_t st = launch(fn, dim3(p.blocks, 1, 1), 16 * kRouteRows, 0, 1, args, s);
+    if (st == GEMM_OK && p.blocks > uint32_t(kRouteDirectBlocks))
+        st = launch(reinterpret_cast<const void *>(&route_scan_kernel), dim3(unsigned(cdiv(p.experts, 32)), 1, 1), 1024, 0, 1, base, s);
+    if (st != GEMM_OK) return st;
+    return launch(reinterpret_cast<const void *>(&route_place_kernel), dim3(p.blocks, 1, 1), kRouteThreads, 0, 1, base, s);
+}
+
+gemm_status_t gemm_route_topk(gemm_dtype_t dtype, int64_t rows, int64_t experts, int64_t top, int32_t renorm, const void *logits,
+                              int32_t *ids, float *weights, int32_t *offsets, int32_t *order, int32_t *position, void *workspace,
+                              size_t ws_bytes, gemm_stream_t stream)
+{
+    gemm_status_t st = check_route(dtype, rows, experts, top);
+    if (st != GEMM_OK) return st;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     RouteParams p;
-    memset(&p, 0, sizeof(p));
-    p.logits = logits;
-    p.dtype = uint32_t(dtype);
-    p.rows = uint32_t(rows);
-    p.experts = uint32_t(experts);
-    p.top = uint32_t(top);
-    p.renorm = renorm != 0;
-    p.blocks = uint32_t(blocks);
-    p.ids = ids;
-    p.weights = weights;
-    p.offsets = offsets;
-    p.order = order;
-    p.position = position;
-    p.hist = static_cast<int32_t *>(workspace);
-    p.totals = p.hist ? p.hist + size_t(blocks) * size_t(experts) : nullptr;
-    void *args[1] = {&p};
-    if (blocks == 1) return launch(ROUTE_INSTANCE(ROUTE_TOPK_FEW, experts), dim3(1, 1, 1), kRouteThreads, 0, 1, args, s);
-    st = launch(ROUTE_INSTANCE(ROUTE_TOPK, experts), dim3(unsigned(blocks), 1, 1), 16 * kRouteRows, 0, 1, args, s);
-    if (st != GEMM_OK) return st;
-    if (blocks > kRouteDirectBlocks)
-        st = launch(reinterpret_cast<const void *>(&route_scan_kernel), dim3(unsigned(cdiv(experts, 32)), 1, 1), 1024, 0, 1, args, s);
-    if (st != GEMM_OK) return st;
-    return launch(reinterpret_cast<const void *>(&route_place_kernel), dim3(unsigned(blocks), 1, 1), kRouteThreads, 0, 1, args, s);
+    bool done = false;
+    st = route_begin(&p, dtype, rows, experts, top, renorm, logits, ids, weights, offsets, order, position, workspace, ws_bytes, s, &done);
+    if (st != GEMM_OK || done) return st;
+    const bool one = p.blocks == 1u;
+    return route_launch(one ? ROUTE_INSTANCE(ROUTE_TOPK_FEW, experts) : ROUTE_INSTANCE(ROUTE_TOPK, experts), p, &p, s);
 }
 
 gemm_status_t gemm_route_topk_grad(gemm_dtype_t dtype, int64_t rows, int64_t experts, int64_t top, int32_t renorm,
@@ -795,6 +814,80 @@ gemm_status_t gemm_route_topk_grad(gemm_dtype_t dtype, int64_t rows, int64_t exp
     p.dlogits = dlogits;
     void *args[1] = {&p};
     return launch(ROUTE_INSTANCE(ROUTE_GRAD, experts), dim3(unsigned(cdiv(rows, 8)), 1, 1), 256, 0, 1, args,
+                  reinterpret_cast<cudaStream_t>(stream));
+}
+
+// ---------------------------------------------------- router with scores
+
+#define ROUTE_SCORED_FEW(V) reinterpret_cast<const void *>(&route_scored_kernel<V, kRouteThreads>)
+#define ROUTE_SCORED(V) reinterpret_cast<const void *>(&route_scored_kernel<V, 16 * kRouteRows>)
+#define ROUTE_SCORED_GRAD(V) reinterpret_cast<const void *>(&route_scored_grad_kernel<V>)
+
+gemm_status_t gemm_route_scored(gemm_dtype_t dtype, gemm_route_score_t score, int64_t rows, int64_t experts, int64_t top,
+                                int64_t groups, int64_t top_groups, int32_t group_top, int32_t renorm, float scale,
+                                const void *logits, const float *bias, int32_t *ids, float *weights, int32_t *offsets,
+                                int32_t *order, int32_t *position, void *workspace, size_t ws_bytes, gemm_stream_t stream)
+{
+    gemm_status_t st = check_route(dtype, rows, experts, top);
+    if (st != GEMM_OK) return st;
+    if (score != GEMM_ROUTE_SOFTMAX && score != GEMM_ROUTE_SIGMOID) return GEMM_ERR_INVALID_ARG;
+    if (groups < 1 || experts % groups != 0 || top_groups < 1 || top_groups > groups || (group_top != 1 && group_top != 2))
+        return GEMM_ERR_INVALID_ARG;
+    if (groups > GEMM_ROUTE_MAX_GROUPS || (groups & (groups - 1)) != 0) return GEMM_ERR_UNSUPPORTED_SHAPE;
+    if (top > top_groups * (experts / groups)) return GEMM_ERR_INVALID_ARG;
+    st = check_pointer(bias, bias != nullptr, 4);
+    if (st != GEMM_OK) return st;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    RouteScoredParams p;
+    memset(&p, 0, sizeof(p));
+    bool done = false;
+    st = route_begin(&p, dtype, rows, experts, top, renorm, logits, ids, weights, offsets, order, position, workspace, ws_bytes, s, &done);
+    if (st != GEMM_OK || done) return st;
+    p.bias = bias;
+    p.sigmoid = score == GEMM_ROUTE_SIGMOID;
+    p.groups = uint32_t(groups);
+    p.top_groups = uint32_t(top_groups);
+    p.group_top = uint32_t(group_top);
+    p.size = uint32_t(experts / groups);
+    p.run = uint32_t(cdiv(experts / groups, 32 / groups));
+    // (a kept group then is one of those with the largest logits, and the scores' order is the logits')
+    p.by_logit = bias == nullptr && (group_top == 1 || top_groups == groups);
+    p.scale = scale;
+    const int64_t lanes = int64_t(p.run) * 32;  // the instance whose lanes hold a run
+    const bool one = p.blocks == 1u;
+    return route_launch(one ? ROUTE_INSTANCE(ROUTE_SCORED_FEW, lanes) : ROUTE_INSTANCE(ROUTE_SCORED, lanes), p, &p, s);
+}
+
+gemm_status_t gemm_route_scored_grad(gemm_dtype_t dtype, gemm_route_score_t score, int64_t rows, int64_t experts, int64_t top,
+                                     int32_t renorm, float scale, const void *logits, const int32_t *ids, const float *dweights,
+                                     float *dlogits, gemm_stream_t stream)
+{
+    gemm_status_t st = check_route(dtype, rows, experts, top);
+    if (st != GEMM_OK) return st;
+    if (score != GEMM_ROUTE_SOFTMAX && score != GEMM_ROUTE_SIGMOID) return GEMM_ERR_INVALID_ARG;
+    const bool any = rows > 0;
+    st = check_pointer(logits, any);
+    for (const void *ptr : {static_cast<const void *>(ids), static_cast<const void *>(dweights), static_cast<const void *>(dlogits)})
+        if (st == GEMM_OK) st = check_pointer(ptr, any, 4);
+    if (st != GEMM_OK || !any) return st;
+    DeviceState state;
+    st = current_device_state(&state);
+    if (st != GEMM_OK) return st;
+    RouteScoredParams p;
+    memset(&p, 0, sizeof(p));
+    p.logits = logits;
+    p.dtype = uint32_t(dtype);
+    p.rows = uint32_t(rows);
+    p.experts = uint32_t(experts);
+    p.top = uint32_t(top);
+    p.renorm = renorm != 0;
+    p.ids = const_cast<int32_t *>(ids);
+    p.dweights = dweights;
+    p.dlogits = dlogits;
+    p.sigmoid = score == GEMM_ROUTE_SIGMOID;
+    p.scale = scale;
+    void *args[1] = {&p};
+    return launch(ROUTE_INSTANCE(ROUTE_SCORED_GRAD, experts), dim3(unsigned(cdiv(rows, 8)), 1, 1), 256, 0, 1, args,
                   reinterpret_cast<cudaStream_t>(stream));
 }
 

@@ -119,6 +119,51 @@ __device__ __forceinline__ int32_t route_block_scan(int32_t v, int32_t *s, int32
     return x - v + (warp ? before : 0);
 }
 
+// What a block's choices come to: with one block the offsets, the order and the positions, with more its counts per
+// expert and each choice's rank among the block's rows.  `id`: the choice number `lane` of this warp's rows (row0 + warp and
+// kWarps further), whose bits s_mask has.
+template <int THREADS>
+__device__ __forceinline__ void route_rank(const RouteParams &p, uint32_t row0, const int32_t (&id)[2],
+                                           const uint32_t (*s_mask)[kRouteMaxExperts], int32_t *s_base, int32_t *s_scan)
+{
+    constexpr uint32_t kWarps = THREADS / 32;
+    constexpr int kRowsPerWarp = 2;
+    const uint32_t lane = threadIdx.x & 31u, warp = threadIdx.x >> 5;
+    __syncthreads();
+    const uint32_t t = threadIdx.x;
+    if (THREADS < kRouteThreads || p.blocks > 1u) {
+        for (uint32_t e = t; e < p.experts; e += THREADS)
+            p.hist[size_t(blockIdx.x) * p.experts + e] = __popc(s_mask[0][e]) + __popc(s_mask[1][e]);
+    } else {
+        const int32_t count = t < p.experts ? __popc(s_mask[0][t]) + __popc(s_mask[1][t]) : 0;
+        int32_t total;
+        const int32_t before = route_block_scan(count, s_scan, &total);
+        if (t < p.experts) {
+            s_base[t] = before;
+            p.offsets[t] = before;
+        }
+        if (t == 0) p.offsets[p.experts] = total;
+        for (uint32_t i = uint32_t(total) + t; i < p.rows * p.top; i += THREADS) p.order[i] = -1;
+        __syncthreads();
+    }
+#pragma unroll
+    for (int q = 0; q < kRowsPerWarp; ++q) {
+        const uint32_t row = row0 + warp + uint32_t(q) * kWarps;
+        if (row >= p.rows || lane >= p.top) continue;
+        const size_t flat = size_t(row) * p.top + lane;
+        int32_t at = -1;
+        if (id[q] >= 0) {
+            // the block's rows before this one that chose the same expert (rows of this warp: r = warp, 32 + warp)
+            at = __popc(s_mask[q][id[q]] & ((1u << warp) - 1u)) + (q ? __popc(s_mask[0][id[q]]) : 0);
+            if (p.blocks == 1u) {
+                at += s_base[id[q]];
+                p.order[at] = int32_t(flat);
+            }
+        }
+        p.position[flat] = at;  // more blocks: the rank in this block, completed by route_place_kernel
+    }
+}
+
 template <int VPT, int THREADS>
 __global__ void __launch_bounds__(THREADS) route_topk_kernel(const __grid_constant__ RouteParams p)
 {
@@ -254,39 +299,7 @@ __global__ void __launch_bounds__(THREADS) route_topk_kernel(const __grid_consta
             }
         }
     }
-    __syncthreads();
-    const uint32_t t = threadIdx.x;
-    if (THREADS < kRouteThreads || p.blocks > 1u) {
-        for (uint32_t e = t; e < p.experts; e += THREADS)
-            p.hist[size_t(blockIdx.x) * p.experts + e] = __popc(s_mask[0][e]) + __popc(s_mask[1][e]);
-    } else {
-        const int32_t count = t < p.experts ? __popc(s_mask[0][t]) + __popc(s_mask[1][t]) : 0;
-        int32_t total;
-        const int32_t before = route_block_scan(count, s_scan, &total);
-        if (t < p.experts) {
-            s_base[t] = before;
-            p.offsets[t] = before;
-        }
-        if (t == 0) p.offsets[p.experts] = total;
-        for (uint32_t i = uint32_t(total) + t; i < p.rows * p.top; i += THREADS) p.order[i] = -1;
-        __syncthreads();
-    }
-#pragma unroll
-    for (int q = 0; q < kRowsPerWarp; ++q) {
-        const uint32_t row = row0 + warp + uint32_t(q) * kWarps;
-        if (row >= p.rows || lane >= p.top) continue;
-        const size_t flat = size_t(row) * p.top + lane;
-        int32_t at = -1;
-        if (id[q] >= 0) {
-            // the block's rows before this one that chose the same expert (rows of this warp: r = warp, 32 + warp)
-            at = __popc(s_mask[q][id[q]] & ((1u << warp) - 1u)) + (q ? __popc(s_mask[0][id[q]]) : 0);
-            if (p.blocks == 1u) {
-                at += s_base[id[q]];
-                p.order[at] = int32_t(flat);
-            }
-        }
-        p.position[flat] = at;  // more blocks: the rank in this block, completed by route_place_kernel
-    }
+    route_rank<THREADS>(p, row0, id, s_mask, s_base, s_scan);
     ptx::griddep_launch_dependents();
 }
 

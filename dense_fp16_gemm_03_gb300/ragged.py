@@ -23,6 +23,9 @@ MAX_GROUPS = 1024
 MAX_RANK = 128
 MAX_EXPERTS = 1024
 MAX_TOP = 32
+MAX_ROUTE_GROUPS = 32
+
+ROUTE_SCORES = {"softmax": 0, "sigmoid": 1}
 
 LORA_BESIDE = 0
 LORA_TENSOR_CORES = 1
@@ -31,7 +34,7 @@ LORA_TENSOR_CORES = 1
 EXPORTED = [
     "gemm_grouped_workspace_size", "gemm_grouped_nt", "gemm_grouped_nn", "gemm_grouped_tn", "gemm_grouped_stall_test",
     "gemm_lora_workspace_size", "gemm_lora_way", "gemm_lora_nt", "gemm_lora_stall_test",
-    "gemm_route_workspace_size", "gemm_route_topk", "gemm_route_topk_grad",
+    "gemm_route_workspace_size", "gemm_route_topk", "gemm_route_topk_grad", "gemm_route_scored", "gemm_route_scored_grad",
 ]
 
 Routing = collections.namedtuple("Routing", ["ids", "weights", "offsets", "order", "position"])
@@ -60,6 +63,8 @@ def lib():
         "gemm_route_workspace_size": [i64, i64, i64, psz],
         "gemm_route_topk": [dt, i64, i64, i64, i32, vp, vp, vp, vp, vp, vp, vp, sz, vp],
         "gemm_route_topk_grad": [dt, i64, i64, i64, i32, vp, vp, vp, vp, vp, vp],
+        "gemm_route_scored": [dt, dt, i64, i64, i64, i64, i64, i32, i32, ctypes.c_float, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp],
+        "gemm_route_scored_grad": [dt, dt, i64, i64, i64, i32, ctypes.c_float, vp, vp, vp, vp, vp],
     }
     for name, args in sig.items():
         f = getattr(L, name)
@@ -291,20 +296,9 @@ def gemm_route_workspace_size(rows, experts, top):
     return _size("gemm_route_workspace_size", rows, experts, top)
 
 
-def gemm_route_topk(logits, top, renorm=True, out=None, workspace=None, stream=None):
-    """The `top` largest logits of each row and the rows sorted by expert, as a Routing.
-
-    logits [rows, experts] float16, bfloat16 or float32; returns ids, weights and position [rows, top], offsets
-    [experts + 1] and order [rows * top] (choices t * top + j sorted by expert).  The weights are softmax(logits) at
-    ids, divided by their sum if `renorm`.  `out`: a Routing of tensors to write into.  The workspace
-    (gemm_route_workspace_size) is required above 64 rows."""
+def _routing(out, rows, experts, top, dev):
+    """A Routing to write into: `out`, checked, or a new one."""
     torch = _gemm._tm()
-    dev = _operand(logits, "logits", 2)
-    rows, experts = logits.shape
-    code = _dtype(logits.dtype, f32=True)
-    top = int(top)
-    if top < 1 or top > experts:
-        raise ValueError("top must be in [1, experts]")
     i32 = torch.int32
     shape, f32 = (rows, top), torch.float32
     if out is None:  # (five allocations are quicker than views of one)
@@ -317,6 +311,23 @@ def gemm_route_topk(logits, top, renorm=True, out=None, workspace=None, stream=N
         _need(r.offsets, "offsets", (experts + 1,), i32, dev)
         _need(r.order, "order", (rows * top,), i32, dev)
         _need(r.position, "position", shape, i32, dev)
+    return r
+
+
+def gemm_route_topk(logits, top, renorm=True, out=None, workspace=None, stream=None):
+    """The `top` largest logits of each row and the rows sorted by expert, as a Routing.
+
+    logits [rows, experts] float16, bfloat16 or float32; returns ids, weights and position [rows, top], offsets
+    [experts + 1] and order [rows * top] (choices t * top + j sorted by expert).  The weights are softmax(logits) at
+    ids, divided by their sum if `renorm`.  `out`: a Routing of tensors to write into.  The workspace
+    (gemm_route_workspace_size) is required above 64 rows."""
+    dev = _operand(logits, "logits", 2)
+    rows, experts = logits.shape
+    code = _dtype(logits.dtype, f32=True)
+    top = int(top)
+    if top < 1 or top > experts:
+        raise ValueError("top must be in [1, experts]")
+    r = _routing(out, rows, experts, top, dev)
     ws, ws_bytes = _workspace(workspace, dev)
     st = lib().gemm_route_topk(code, rows, experts, top, 1 if renorm else 0, logits.data_ptr(), r.ids.data_ptr(),
                                r.weights.data_ptr(), r.offsets.data_ptr(), r.order.data_ptr(), r.position.data_ptr(), ws,
@@ -341,4 +352,63 @@ def gemm_route_topk_grad(logits, ids, weights, dweights, renorm=True, dlogits=No
     st = lib().gemm_route_topk_grad(code, rows, experts, shape[1], 1 if renorm else 0, logits.data_ptr(), ids.data_ptr(),
                                     weights.data_ptr(), dweights.data_ptr(), dlogits.data_ptr(), _stream(stream, dev))
     _check(st, "gemm_route_topk_grad")
+    return dlogits
+
+
+def _score(score):
+    code = ROUTE_SCORES.get(score)
+    if code is None:
+        raise ValueError("score must be one of %s" % ", ".join(repr(n) for n in ROUTE_SCORES))
+    return code
+
+
+def gemm_route_scored(logits, top, score="sigmoid", bias=None, groups=1, top_groups=None, group_top=2, renorm=True, scale=1.0,
+                      out=None, workspace=None, stream=None):
+    """The `top` experts of each row with the largest s + bias among those of its best groups, as a Routing.
+
+    s = softmax(logits) or the logits' sigmoid; bias [experts] float32 moves the choice and not the weights.  The experts form
+    `groups` (1, 2, 4 ... 32) groups of neighbours; the `top_groups` (None: all) with the largest score are kept, a group's
+    score being its largest s + bias (group_top 1) or the sum of its two largest (2).  The weights are scale * s at ids,
+    divided by their sum if `renorm`.  `out` and the workspace as in gemm_route_topk."""
+    code = _score(score)
+    dev = _operand(logits, "logits", 2)
+    rows, experts = logits.shape
+    kind = _dtype(logits.dtype, f32=True)
+    top, groups = int(top), int(groups)
+    top_groups = groups if top_groups is None else int(top_groups)
+    if top < 1 or top > experts:
+        raise ValueError("top must be in [1, experts]")
+    if groups < 1 or experts % groups or not 1 <= top_groups <= groups:
+        raise ValueError("groups must divide the experts, and top_groups be in [1, groups]")
+    if top > top_groups * (experts // groups):
+        raise ValueError("the groups kept hold fewer than `top` experts")
+    if group_top not in (1, 2):
+        raise ValueError("group_top must be 1 or 2")
+    if bias is not None:
+        _need(bias, "bias", (experts,), _gemm._tm().float32, dev)
+    r = _routing(out, rows, experts, top, dev)
+    ws, ws_bytes = _workspace(workspace, dev)
+    st = lib().gemm_route_scored(kind, code, rows, experts, top, groups, top_groups, group_top, 1 if renorm else 0, scale,
+                                 logits.data_ptr(), None if bias is None else bias.data_ptr(), r.ids.data_ptr(), r.weights.data_ptr(),
+                                 r.offsets.data_ptr(), r.order.data_ptr(), r.position.data_ptr(), ws, ws_bytes, _stream(stream, dev))
+    _check(st, "gemm_route_scored")
+    return r
+
+
+def gemm_route_scored_grad(logits, ids, dweights, score="sigmoid", renorm=True, scale=1.0, dlogits=None, stream=None):
+    """The gradient of the logits [rows, experts] float32 from that of gemm_route_scored's weights."""
+    torch = _gemm._tm()
+    code = _score(score)
+    dev = _operand(logits, "logits", 2)
+    rows, experts = logits.shape
+    kind = _dtype(logits.dtype, f32=True)
+    if ids.dim() != 2:
+        raise ValueError("ids must be [rows, top]")
+    shape = ids.shape
+    _need(ids, "ids", (rows, shape[1]), torch.int32, dev)
+    _need(dweights, "dweights", shape, torch.float32, dev)
+    dlogits = _out(dlogits, "dlogits", (rows, experts), torch.float32, dev)
+    st = lib().gemm_route_scored_grad(kind, code, rows, experts, shape[1], 1 if renorm else 0, scale, logits.data_ptr(), ids.data_ptr(),
+                                      dweights.data_ptr(), dlogits.data_ptr(), _stream(stream, dev))
+    _check(st, "gemm_route_scored_grad")
     return dlogits

@@ -10,6 +10,8 @@
  *   gemm_route_topk / _grad       the router that makes the groups: top-k of the
  *                                 experts' logits, its weights, the rows sorted by
  *                                 expert, and the logits' gradient
+ *   gemm_route_scored / _grad     the same with softmax or sigmoid scores, a bias for
+ *                                 the choice, and the best groups of experts first
  *
  * Operands are fp16 or bf16 (all matrices of a call the same), accumulation is
  * fp32, results are rounded once to the operands' type (round to nearest even).
@@ -142,6 +144,47 @@ gemm_status_t gemm_route_topk(gemm_dtype_t dtype, int64_t rows, int64_t experts,
 gemm_status_t gemm_route_topk_grad(gemm_dtype_t dtype, int64_t rows, int64_t experts, int64_t top, int32_t renorm,
                                    const void *logits, const int32_t *ids, const float *weights, const float *dweights,
                                    float *dlogits, gemm_stream_t stream);
+
+/*
+ * Router with scores.  For every row, with s = softmax(l) or 1 / (1 + e^-l) of its
+ * logits l and c = s + bias (bias [experts] fp32, or NULL for 0; it moves the choice
+ * and not the weights):
+ *
+ *   groups    the experts form `groups` (a power of two up to 32 that divides them)
+ *             groups of neighbours, of which the `top_groups` best are kept; a group's
+ *             score is the largest of its c (group_top 1) or the sum of its two
+ *             largest (2; of one where the group has no second)
+ *   ids       the `top` largest c of the groups kept, in falling order (top at most
+ *             top_groups * experts / groups)
+ *   weights   scale * s at ids, divided by the sum of the chosen s if renorm != 0
+ *
+ * and offsets, order and position as gemm_route_topk.  Ties go to the lowest index.
+ * c is compared as exactly as 64 bits hold it; without a bias, and unless groups go by
+ * sums, by the logits themselves.  An expert whose logit or bias is -infinity is never
+ * chosen, and rows that run short are as in gemm_route_topk.  A NaN among c comes
+ * after all others; a softmax of NaN or +infinity is NaN throughout.
+ *
+ * The workspace is gemm_route_workspace_size's, under the same rule.
+ *
+ * gemm_route_scored_grad: dlogits [rows, experts] fp32 from dweights [rows, top] fp32
+ * and the forward call's logits and ids (the bias has no gradient):
+ *   sigmoid, renorm:   dl[ids[j]] = scale (1 - s[j]) v[j] (dw[j] - sum_i v[i] dw[i]),
+ *                      v = s / (sum of the chosen s)
+ *   sigmoid:           dl[ids[j]] = scale (1 - s[j]) s[j] dw[j]
+ *   softmax, renorm:   dl[ids[j]] = scale v[j] (dw[j] - sum_i v[i] dw[i])
+ *   softmax:           dl[e] = scale s[e] (sum_j [e = ids[j]] dw[j] - sum_j s[j] dw[j])
+ * zero elsewhere.  ids outside [0, experts) take no part.
+ */
+#define GEMM_ROUTE_MAX_GROUPS 32
+typedef enum gemm_route_score { GEMM_ROUTE_SOFTMAX = 0, GEMM_ROUTE_SIGMOID = 1 } gemm_route_score_t;
+
+gemm_status_t gemm_route_scored(gemm_dtype_t dtype, gemm_route_score_t score, int64_t rows, int64_t experts, int64_t top,
+                                int64_t groups, int64_t top_groups, int32_t group_top, int32_t renorm, float scale,
+                                const void *logits, const float *bias, int32_t *ids, float *weights, int32_t *offsets,
+                                int32_t *order, int32_t *position, void *workspace, size_t ws_bytes, gemm_stream_t stream);
+gemm_status_t gemm_route_scored_grad(gemm_dtype_t dtype, gemm_route_score_t score, int64_t rows, int64_t experts, int64_t top,
+                                     int32_t renorm, float scale, const void *logits, const int32_t *ids,
+                                     const float *dweights, float *dlogits, gemm_stream_t stream);
 
 /*
  * Failure-detection hook for tests, as gemm_f16_nt_run_stall_test: `mode` 0, 1, 2
