@@ -758,12 +758,12 @@ static gemm_status_t route_begin(RouteParams *p, gemm_dtype_t dtype, int64_t row
     return GEMM_OK;
 }
 
-// The choice by kernel `fn` with its parameters `own`, then the places of all choices.
-static gemm_status_t route_launch(const void *fn, RouteParams &p, void *own, cudaStream_t s)
+// The choice by kernel `fn` with its parameters `own` and `warp_smem` bytes a warp, then the places of all choices.
+static gemm_status_t route_launch(const void *fn, RouteParams &p, void *own, int warp_smem, cudaStream_t s)
 {
     void *args[1] = {own}, *base[1] = {&p};
-    if (p.blocks == 1u) return launch(fn, dim3(1, 1, 1), kRouteThreads, 0, 1, args, s);
-    gemm_status_t st = launch(fn, dim3(p.blocks, 1, 1), 16 * kRouteRows, 0, 1, args, s);
+    if (p.blocks == 1u) return launch(fn, dim3(1, 1, 1), kRouteThreads, kRouteThreads / 32 * warp_smem, 1, args, s);
+    gemm_status_t st = launch(fn, dim3(p.blocks, 1, 1), 16 * kRouteRows, kRouteRows / 2 * warp_smem, 1, args, s);
     if (st == GEMM_OK && p.blocks > uint32_t(kRouteDirectBlocks))
         st = launch(reinterpret_cast<const void *>(&route_scan_kernel), dim3(unsigned(cdiv(p.experts, 32)), 1, 1), 1024, 0, 1, base, s);
     if (st != GEMM_OK) return st;
@@ -782,7 +782,7 @@ gemm_status_t gemm_route_topk(gemm_dtype_t dtype, int64_t rows, int64_t experts,
     st = route_begin(&p, dtype, rows, experts, top, renorm, logits, ids, weights, offsets, order, position, workspace, ws_bytes, s, &done);
     if (st != GEMM_OK || done) return st;
     const bool one = p.blocks == 1u;
-    return route_launch(one ? ROUTE_INSTANCE(ROUTE_TOPK_FEW, experts) : ROUTE_INSTANCE(ROUTE_TOPK, experts), p, &p, s);
+    return route_launch(one ? ROUTE_INSTANCE(ROUTE_TOPK_FEW, experts) : ROUTE_INSTANCE(ROUTE_TOPK, experts), p, &p, 0, s);
 }
 
 gemm_status_t gemm_route_topk_grad(gemm_dtype_t dtype, int64_t rows, int64_t experts, int64_t top, int32_t renorm,
@@ -821,7 +821,17 @@ gemm_status_t gemm_route_topk_grad(gemm_dtype_t dtype, int64_t rows, int64_t exp
 
 #define ROUTE_SCORED_FEW(V) reinterpret_cast<const void *>(&route_scored_kernel<V, kRouteThreads>)
 #define ROUTE_SCORED(V) reinterpret_cast<const void *>(&route_scored_kernel<V, 16 * kRouteRows>)
+#define ROUTE_LIST(V) kRouteListBytes<V>
 #define ROUTE_SCORED_GRAD(V) reinterpret_cast<const void *>(&route_scored_grad_kernel<V>)
+
+// More than 48 KB of shared memory (12.2 KB of it static) have to be asked for: instances of many experts a lane.
+static gemm_status_t route_smem(const void *fn, int bytes)
+{
+    if (bytes <= 32 * 1024) return GEMM_OK;
+    if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) == cudaSuccess) return GEMM_OK;
+    cudaGetLastError();
+    return GEMM_ERR_CUDA;
+}
 
 gemm_status_t gemm_route_scored(gemm_dtype_t dtype, gemm_route_score_t score, int64_t rows, int64_t experts, int64_t top,
                                 int64_t groups, int64_t top_groups, int32_t group_top, int32_t renorm, float scale,
@@ -850,12 +860,17 @@ gemm_status_t gemm_route_scored(gemm_dtype_t dtype, gemm_route_score_t score, in
     p.group_top = uint32_t(group_top);
     p.size = uint32_t(experts / groups);
     p.run = uint32_t(cdiv(experts / groups, 32 / groups));
+    while ((groups << p.spread) < 32) ++p.spread;
     // (a kept group then is one of those with the largest logits, and the scores' order is the logits')
     p.by_logit = bias == nullptr && (group_top == 1 || top_groups == groups);
     p.scale = scale;
     const int64_t lanes = int64_t(p.run) * 32;  // the instance whose lanes hold a run
     const bool one = p.blocks == 1u;
-    return route_launch(one ? ROUTE_INSTANCE(ROUTE_SCORED_FEW, lanes) : ROUTE_INSTANCE(ROUTE_SCORED, lanes), p, &p, s);
+    const void *fn = one ? ROUTE_INSTANCE(ROUTE_SCORED_FEW, lanes) : ROUTE_INSTANCE(ROUTE_SCORED, lanes);
+    const int warp_smem = int(ROUTE_INSTANCE(ROUTE_LIST, lanes));
+    st = route_smem(fn, (one ? kRouteThreads : 16 * kRouteRows) / 32 * warp_smem);
+    if (st != GEMM_OK) return st;
+    return route_launch(fn, p, &p, warp_smem, s);
 }
 
 gemm_status_t gemm_route_scored_grad(gemm_dtype_t dtype, gemm_route_score_t score, int64_t rows, int64_t experts, int64_t top,
@@ -887,7 +902,7 @@ gemm_status_t gemm_route_scored_grad(gemm_dtype_t dtype, gemm_route_score_t scor
     p.sigmoid = score == GEMM_ROUTE_SIGMOID;
     p.scale = scale;
     void *args[1] = {&p};
-    return launch(ROUTE_INSTANCE(ROUTE_SCORED_GRAD, experts), dim3(unsigned(cdiv(rows, 8)), 1, 1), 256, 0, 1, args,
+    return launch(ROUTE_INSTANCE(ROUTE_SCORED_GRAD, experts), dim3(unsigned(cdiv(rows, experts <= 256 ? 16 : 8)), 1, 1), 256, 0, 1, args,
                   reinterpret_cast<cudaStream_t>(stream));
 }
 

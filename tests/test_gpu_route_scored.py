@@ -186,6 +186,19 @@ def test_ties_go_to_the_lowest_index(score, bias):
         check(z.bfloat16(), 8, score=score, bias=b, groups=8, top_groups=3, group_top=group_top, renorm=False)
 
 
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+def test_many_equal_scores(score):
+    """More experts with one score than a warp's lanes, alone, with one just beside them, and in groups."""
+    z = torch.full((70, 256), 0.75)
+    for t in range(1, 70):
+        z[t, (37 * t) % 256] = float(np.nextafter(np.float32(0.75), np.float32(1 if t % 2 else 0)))
+    for b in (None, torch.full((256,), 0.125)):
+        check(z, 8, score=score, bias=b)
+        for group_top in (1, 2):
+            check(z, 8, score=score, bias=b, groups=8, top_groups=4, group_top=group_top)
+            check(z.bfloat16(), 30, score=score, bias=b, groups=8, top_groups=1, group_top=group_top)
+
+
 def test_coarse_logits_with_an_even_bias():
     """bf16 logits repeat within a row; a bias that is the same for all, as at the start of a training, keeps their order."""
     z = draw(500, 256, "bf16", 13)
