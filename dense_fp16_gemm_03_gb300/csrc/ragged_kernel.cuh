@@ -129,7 +129,7 @@ struct RaggedParams {
     uint32_t tiles_q;        // kTN, kLoraY: tiles along the N side
     uint32_t per;            // kLoraU, kLoraY: rows of a row tile
     FastDiv by[kRagBand + 1];  // by[d] divides by d; by[0] by kRagBand * tiles_p
-    uint32_t sk;             // 1: equal runs of K-block iterations
+    uint32_t sk;             // 1: equal runs of K-block iterations; 2 (with an epilogue): of those of the last, partial wave
     uint32_t bf16;           // operand type: 0 fp16, 1 bf16
     uint32_t out32;          // kTN: 1 = fp32 output
     void *out;
@@ -399,7 +399,7 @@ __device__ __forceinline__ void flag_give_up(uint64_t *flag, uint64_t stamp)
     if (old == stamp || old == flag_not_coming(stamp)) ptx::st_release_gpu_u64(flag, 0u);
 }
 
-template <int MODE, int CG, int QCAP>
+template <int MODE, int CG, int QCAP, bool EPI>
 struct RaggedWalk {
     const RaggedParams &p;
     const int32_t *tab_row;    // offsets (groups + 1), or counts per row tile
@@ -408,6 +408,7 @@ struct RaggedWalk {
     uint32_t worker, workers, total;
     uint32_t run, longer;      // sk: K-block iterations of a worker; the first `longer` workers have one more
     uint32_t tile_blocks;      // sk: K blocks of every tile
+    uint32_t splitters, whole; // sk 2: workers that have a run, and tiles before the split ones
 
     // A producer that is late with a tile's first load leaves the ring short for the rest of it, so the way from a tile's
     // number to its place is kept short: the group is looked for from the last one on, and divisors are known.  `near` is
@@ -514,11 +515,25 @@ struct RaggedWalk {
         if (MODE == kTN || !p.sk || total == 0u) return;
         tile_blocks = p.k_blocks;
         if (MODE == kLoraY) tile_blocks += uniform(uint32_t(tab_row[0])) * p.rank_blocks;
+        if constexpr (EPI) {
+            // sk 2: the tiles that fill no wave are split, the others follow whole
+            splitters = workers;
+            whole = p.sk == 2u ? total / workers * workers : 0u;
+            const uint32_t iters = (total - whole) * tile_blocks;
+            splitters = min(workers, max(1u, iters / kMinRun));
+            run = iters / splitters;
+            longer = iters - run * splitters;
+            return;
+        }
         const uint32_t iters = total * tile_blocks;  // below 2^32: the host checks
         const uint32_t most = max(1u, iters / kMinRun);
         if (most < workers) workers = most;
         run = iters / workers;
         longer = iters - run * workers;
+    }
+    __device__ __forceinline__ uint32_t first_split() const  // tile
+    {
+        return EPI ? whole : 0u;
     }
     __device__ __forceinline__ uint32_t run_begin(uint32_t w) const
     {
@@ -537,6 +552,7 @@ struct RaggedWalk {
     __device__ __forceinline__ void leave_flags(uint32_t rank, bool published, bool taken) const
     {
         const uint32_t lane = threadIdx.x & 31u, kb = tile_blocks;
+        if (EPI && worker >= splitters) return;
         const uint32_t begin = run_begin(worker), end = run_begin(worker + 1u);
         const uint32_t start = begin / kb * kb;
         if (!published && lane == 0 && end % kb != 0u)  // the run stops inside a tile
@@ -562,14 +578,14 @@ struct RaggedWalk {
             }
             return;
         }
-        if (total == 0u || worker >= workers) return;
-        const uint32_t begin = run_begin(worker);
-        uint32_t it = run_begin(worker + 1u);
+        if (total == 0u || (!EPI && worker >= workers)) return;
+        const uint32_t begin = EPI && worker >= splitters ? 0u : run_begin(worker);
+        uint32_t it = EPI && worker >= splitters ? 0u : run_begin(worker + 1u);
         const uint32_t kb = tile_blocks;
         while (it > begin) {
             const uint32_t u = (it - 1u) / kb;
             const uint32_t start = u * kb;
-            decode(u, s, near);
+            decode(first_split() + u, s, near);
             s.lo = begin > start ? begin - start : 0u;
             s.hi = it - start;
             const uint32_t lo = s.lo;
@@ -577,6 +593,16 @@ struct RaggedWalk {
             if constexpr (UNIFORM) uniform<MODE>(s);
             if (!f(s)) return;
             it = start + lo;
+        }
+        if constexpr (EPI) {
+            for (uint32_t u = worker; u < whole; u += workers) {
+                decode(u, s, near);
+                s.lo = 0;
+                s.hi = s.kb;
+                count_extra(s);
+                if constexpr (UNIFORM) uniform<MODE>(s);
+                if (!f(s)) return;
+            }
         }
     }
 };
@@ -858,17 +884,32 @@ __global__ void __launch_bounds__(RaggedCfg<MODE, CG, QCAP, STAGES, EPI>::kThrea
     ptx::tc_fence_after_sync();
     const uint32_t tmem_base = *tmem_slot;
     const bool late = MODE == kNT && !EPI && p.delta != nullptr;
-    if (!late) ptx::griddep_wait();
-    ragged_table<MODE, QCAP>(p, tab_row, tab_tile);
+    // With one weight matrix nothing but the operands comes from the kernel before this one: the roles that read or write
+    // memory wait for it themselves, and the first weights are asked into L2 meanwhile.
+    const bool early = EPI && p.offsets == nullptr;
+    if (!late && !early) ptx::griddep_wait();
+    if (early) {
+        if (threadIdx.x == 0) {
+            tab_row[0] = 0;
+            tab_row[1] = int32_t(p.rows);
+            tab_tile[0] = 0u;
+            tab_tile[1] = (p.rows + QCAP - 1u) / QCAP * p.tiles_p;
+        }
+        __syncthreads();
+    } else {
+        ragged_table<MODE, QCAP>(p, tab_row, tab_tile);
+    }
 
     const int32_t *list = p.list;
-    RaggedWalk<MODE, CG, QCAP> walk{p,
+    RaggedWalk<MODE, CG, QCAP, EPI> walk{p,
                                     tab_row,
                                     tab_tile,
                                     list,
                                     blockIdx.x / CG,
                                     gridDim.x / CG,
                                     MODE == kLoraY ? p.tiles_p * p.tiles_q : uniform(tab_tile[p.groups]),
+                                    0u,
+                                    0u,
                                     0u,
                                     0u,
                                     0u};
@@ -894,7 +935,22 @@ __global__ void __launch_bounds__(RaggedCfg<MODE, CG, QCAP, STAGES, EPI>::kThrea
         {
             const bool elected = ptx::elect_one();
             uint32_t stage = 0, phase = 0, fills = 0, tail_uses = 0, last_g = ~0u;
+            bool waited = !early;
             walk.template each<true>([&](const RaggedSeg &s) {
+                if (EPI && !waited) {
+                    const int32_t p0 = int32_t(s.p0 + rank * 128u);
+                    if (elected)
+                        for (uint32_t v = s.lo; v < min(s.hi, s.lo + uint32_t(STAGES)); ++v) {
+                            const int32_t k0 = int32_t(v * kRagBlockK);
+                            if constexpr (MODE == kNN) {
+                                if (uint32_t(p0) / 64u + 2u <= p.p_groups) ptx::tma_prefetch_4d(&p.tm_p2, 0, k0, p0 / 64, 0);
+                            } else {
+                                ptx::tma_prefetch_3d(&p.tm_p, k0, p0, 0);
+                            }
+                        }
+                    ptx::griddep_wait();
+                    waited = true;
+                }
                 // kTN: the group's own maps, whose rows end where the group's do
                 const CUtensorMap *map_p = &p.tm_p, *map_q = &p.tm_q[0], *map_p2 = &p.tm_p2, *map_q2 = &p.tm_q2;
                 if (MODE == kTN && p.maps != nullptr) {
@@ -1134,6 +1190,7 @@ __global__ void __launch_bounds__(RaggedCfg<MODE, CG, QCAP, STAGES, EPI>::kThrea
         const bool bf16 = p.bf16 != 0u;
         const uint32_t esize = (MODE == kTN && p.out32) ? 4u : 2u;
 
+        if (early) ptx::griddep_wait();
         // what no tile covers: rows in no group, and the gradients of groups without rows
         {
             const uint64_t first = uint64_t(blockIdx.x) * (32u * Cfg::kEpiWarps) + (threadIdx.x - 64u);
@@ -1262,7 +1319,7 @@ __global__ void __launch_bounds__(RaggedCfg<MODE, CG, QCAP, STAGES, EPI>::kThrea
             }
             uint32_t w_lo = walk.worker;  // workers [w_lo, worker) hold the tile's earlier K blocks
             if (split) {
-                w_lo = walk.first_of(s.tile * s.kb);
+                w_lo = walk.first_of((s.tile - walk.first_split()) * s.kb);
                 if (warp == 2u) {
                     for (uint32_t w = w_lo + lane; w < walk.worker; w += 32u) {
                         uint64_t *flag = p.flags + w * CG + rank;
@@ -1610,7 +1667,7 @@ __global__ void __launch_bounds__(RaggedCfg<MODE, CG, QCAP, STAGES, EPI>::kThrea
     // ---------------------------------------------------- teardown
     ptx::griddep_launch_dependents();
     // (a kernel that ends counts as the end of those before it)
-    if (late) ptx::griddep_wait();
+    if (late || early) ptx::griddep_wait();
     __syncwarp();
     ptx::tc_fence_before_sync();
     if constexpr (CG == 2) ptx::cluster_sync();
