@@ -16,7 +16,6 @@ const RaggedVariant kLinear[] = {
     RAGGED_VARIANT(kNT, 2, 256, 6, true), RAGGED_VARIANT(kNT, 1, 64, 8, true),
     RAGGED_VARIANT(kNN, 2, 256, 6, true), RAGGED_VARIANT(kNN, 1, 64, 8, true),
 };
-constexpr int kSetsWide = RaggedCfg<kNN, 2, 256, 6, true>::kEpiSets, kSetsFew = RaggedCfg<kNN, 1, 64, 8, true>::kEpiSets;
 using LinearDevice = RaggedDeviceOf<int(sizeof(kLinear) / sizeof(kLinear[0]))>;
 
 gemm_status_t linear_device(LinearDevice **out)
@@ -33,10 +32,10 @@ int64_t live_groups(int64_t groups, int64_t rows)
     return groups < rows ? groups : rows;
 }
 
-// Bytes of the partial sums of a bias gradient: a line for each set of epilogue warps of each N-side tile.
-size_t sums_bytes(int64_t per, int sets, int64_t groups, int64_t rows, int64_t cols)
+// Bytes of the partial sums of a bias gradient: a line for each piece of `per` rows.
+size_t sums_bytes(int64_t per, int64_t groups, int64_t rows, int64_t cols)
 {
-    return size_t(round_up((rows / per + live_groups(groups, rows)) * sets * cols * 4, 256));
+    return size_t(round_up((rows / per + live_groups(groups, rows)) * cols * 4, 256));
 }
 
 // Rows of a piece of linear_grad_kernel: enough pieces to fill the SMs, few enough lines to add up.
@@ -57,7 +56,7 @@ size_t grad_room(int64_t groups, int64_t rows, int64_t cols, int num_sms)
         int64_t r = rows;
         if (grad_rows(rows, cols, num_sms) > per) r = (8 * num_sms / cdiv(cols, 256) + 1) * 2 * per;
         if (r > rows) r = rows;
-        const size_t bytes = sums_bytes(per, 1, groups, r, cols);
+        const size_t bytes = sums_bytes(per, groups, r, cols);
         if (bytes > most) most = bytes;
     }
     return most;
@@ -101,7 +100,7 @@ gemm_status_t zero_bias(float *dbias, int64_t count, cudaStream_t stream)
 }
 
 gemm_status_t launch_sum(const float *sums, const int32_t *offsets, float *dbias, int64_t groups, int64_t rows, int64_t cols,
-                         int64_t per, int sets, cudaStream_t stream)
+                         int64_t per, cudaStream_t stream)
 {
     LinearSumParams p;
     p.sums = sums;
@@ -110,7 +109,6 @@ gemm_status_t launch_sum(const float *sums, const int32_t *offsets, float *dbias
     p.groups = uint32_t(groups);
     p.rows = uint32_t(rows);
     p.per = uint32_t(per);
-    p.sets = uint32_t(sets);
     p.cols = uint32_t(cols);
     void *args[1] = {&p};
     return launch(reinterpret_cast<const void *>(&linear_sum_kernel), dim3(unsigned(cdiv(cols, 32)), unsigned(groups), 1),
@@ -147,10 +145,9 @@ gemm_status_t linear(int mode, gemm_dtype_t dtype, gemm_act_t act, int64_t group
     const int variant = choice.wide ? wide : few;
     const RaggedVariant &var = kLinear[variant];
     const bool split_last = choice.wide && !choice.split && ws != nullptr && split_last_wave(var, dev->slots[variant], groups, rows, pdim, kdim);
-    const int sets = choice.wide ? kSetsWide : kSetsFew;
     // the sums of one tile are dbias
-    const bool whole = offsets == nullptr && rows <= var.qcap && sets == 1;
-    const size_t sums = dbias && !whole ? sums_bytes(var.qcap, sets, groups, rows, pdim) : 0;
+    const bool whole = offsets == nullptr && rows <= var.qcap;
+    const size_t sums = dbias && !whole ? sums_bytes(var.qcap, groups, rows, pdim) : 0;
     const size_t need = sums + (choice.split || split_last ? split_bytes(var, dev->slots[variant]) : 0);
     if (ws != nullptr || ws_bytes != 0 || sums > 0) {
         if (ws == nullptr || ws_bytes < need) return GEMM_ERR_WORKSPACE;
@@ -187,7 +184,7 @@ gemm_status_t linear(int mode, gemm_dtype_t dtype, gemm_act_t act, int64_t group
     }
     st = launch_variant(var, dev->slots[variant], dev->error_word, p, &p, most, stream);
     if (st != GEMM_OK || sums == 0) return st;
-    return launch_sum(p.sums, offsets, dbias, groups, rows, pdim, var.qcap, sets, stream);
+    return launch_sum(p.sums, offsets, dbias, groups, rows, pdim, var.qcap, stream);
 }
 
 }  // namespace
@@ -207,9 +204,7 @@ gemm_status_t gemm_linear_workspace_size(int64_t groups, int64_t rows, int64_t n
     *bytes = 0;
     if (rows == 0) return GEMM_OK;
     const RaggedVariant &few = kLinear[kVNtFew], &wide = kLinear[kVNtWide];
-    size_t sums = sums_bytes(few.qcap, kSetsFew, groups, rows, k);
-    const size_t wide_sums = sums_bytes(wide.qcap, kSetsWide, groups, rows, k);
-    if (wide_sums > sums) sums = wide_sums;
+    const size_t sums = sums_bytes(few.qcap, groups, rows, k);  // (of pairs: fewer)
     size_t split = split_bytes(few, dev->slots[kVNtFew]);
     const size_t wide_split = split_bytes(wide, dev->slots[kVNtWide]);
     if (rows > few.qcap && wide_split > split) split = wide_split;
@@ -255,7 +250,7 @@ gemm_status_t gemm_linear_grad(gemm_dtype_t dtype, gemm_act_t act, int64_t group
     if (st != GEMM_OK) return st;
     const int64_t per = grad_rows(rows, n, dev->num_sms), strips = cdiv(n, 256);
     const bool whole = offsets == nullptr && rows <= per;  // the sums of one piece are dbias
-    const size_t need = dbias && !whole ? sums_bytes(per, 1, groups, rows, n) : 0;
+    const size_t need = dbias && !whole ? sums_bytes(per, groups, rows, n) : 0;
     if (workspace != nullptr || ws_bytes != 0 || need > 0) {
         if (workspace == nullptr || ws_bytes < need) return GEMM_ERR_WORKSPACE;
         if (reinterpret_cast<uintptr_t>(workspace) & 255u) return GEMM_ERR_ALIGNMENT;
@@ -278,7 +273,7 @@ gemm_status_t gemm_linear_grad(gemm_dtype_t dtype, gemm_act_t act, int64_t group
     void *args[1] = {&p};
     st = launch(reinterpret_cast<const void *>(&linear_grad_kernel), dim3(unsigned(blocks), 1, 1), kLinearThreads, 0, 1, args, s);
     if (st != GEMM_OK || need == 0) return st;
-    return launch_sum(p.sums, offsets, dbias, groups, rows, n, per, 1, s);
+    return launch_sum(p.sums, offsets, dbias, groups, rows, n, per, s);
 }
 
 gemm_status_t gemm_linear_stall_test(int32_t mode, gemm_dtype_t dtype, gemm_act_t act, int64_t groups, int64_t rows, int64_t n,

@@ -63,7 +63,7 @@ struct LinearSumParams {
     const int32_t *offsets;  // or null
     float *dbias;            // [groups, cols]
     uint32_t groups, rows;
-    uint32_t per, sets;      // rows of a piece, lines of a piece
+    uint32_t per;            // rows of a line's piece
     uint32_t cols;
 };
 
@@ -77,7 +77,7 @@ __global__ void __launch_bounds__(kLinearThreads) linear_sum_kernel(const __grid
     linear_table(p.offsets, p.groups, p.rows, p.per, s_row, s_piece);
     const uint32_t g = blockIdx.y, lane = threadIdx.x & 31u, warp = threadIdx.x >> 5;
     const uint32_t col = blockIdx.x * 32u + lane;
-    const uint32_t first = s_piece[g] * p.sets, end = s_piece[g + 1u] * p.sets;
+    const uint32_t first = s_piece[g], end = s_piece[g + 1u];
     float sum = 0.0f;
     if (col < p.cols) {
 #pragma unroll 4

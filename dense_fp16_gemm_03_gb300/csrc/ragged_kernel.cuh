@@ -159,7 +159,7 @@ struct LinearParams : RaggedParams {
     const void *bias;      // kNT: [groups, pdim], or null
     const void *in;        // kNT: the residual, kNN: z, [rows, pdim], or null
     void *kept;            // kNT: z [rows, pdim], or null
-    float *sums;           // kNN: sums of dx's columns over the rows of each N-side tile and epilogue set, or null
+    float *sums;           // kNN: sums of dx's columns over the rows of each N-side tile, or null
     uint32_t act;
 };
 
@@ -173,7 +173,7 @@ struct RaggedCfg {
     static constexpr bool kHelper = (MODE == kTN || MODE == kLoraY);
     // (kTN: eight warps' boxes of 128 bytes a row do not fit; of 64 bytes, or shared by two warps, they took 8 and
     // 2% longer than four for 16384 rows, 32 groups, 4096 x 4096)
-    static constexpr int kEpiSets = (QCAP == 256 && MODE != kTN) ? 2 : 1;
+    static constexpr int kEpiSets = ((QCAP == 256 && MODE != kTN) || EPI) ? 2 : 1;
     static constexpr int kEpiWarps = 4 * kEpiSets;
     static constexpr int kFirstHelper = 2 + kEpiWarps;          // warp
     static constexpr int kThreads = 32 * kFirstHelper + (kHelper ? kRagHelpers : 0);
@@ -202,7 +202,9 @@ struct RaggedCfg {
     static constexpr int kOffTmemSlot = kOffRec + STAGES * 16;
     static constexpr int kOffAbort = kOffTmemSlot + 4;
     static constexpr int kOffAnyBad = kOffAbort + 4;
-    static constexpr int kSmemBytes = kOffAnyBad + 32 + 1024;
+    // column sums on their way from the second epilogue set to the first, of two tiles
+    static constexpr int kOffSums = kOffAnyBad + 32;
+    static constexpr int kSmemBytes = kOffSums + (EPI && MODE == kNN ? 2 * 128 * 4 : 0) + 1024;
     static constexpr int kTmemCols = 2 * QCAP < 32 ? 32 : 2 * QCAP;
     static_assert(kQBytes % 1024 == 0 && kOffBar % 8 == 0, "layout");
     static_assert(kSmemBytes <= kRagMaxSmem, "shared memory budget");
@@ -1237,8 +1239,10 @@ __global__ void __launch_bounds__(RaggedCfg<MODE, CG, QCAP, STAGES, EPI>::kThrea
                 }
             }
             const bool ok = ragged_wait<CG>(bar_acc_full(acc), acc_phase, p, abort_flag, kRagErrAccFull);
-            // the warps meet at named barriers below when the tile is split: stop together
-            if (MODE != kTN && p.sk) {
+            // the warps meet at named barriers below when the tile is split, or has its columns summed: stop together
+            bool together = MODE != kTN && p.sk != 0u;
+            if constexpr (EPI && MODE == kNN) together = together || p.sums != nullptr;
+            if (together) {
                 if (!ptx::named_barrier_and(1, 32 * Cfg::kEpiWarps, ok)) {
                     stopped = true;
                     return false;
@@ -1472,9 +1476,16 @@ __global__ void __launch_bounds__(RaggedCfg<MODE, CG, QCAP, STAGES, EPI>::kThrea
                                 }
                                 linear_store(p.out, p.pdim, s, prow, c, buf, r, bf16);
                             }
-                            if (MODE == kNN && p.sums != nullptr && prow + lane < p.pdim) {
-                                const uint32_t slot = (tab_tile[s.g] / p.tiles_p + s.qi) * uint32_t(Cfg::kEpiSets) + set;
-                                p.sums[size_t(slot) * p.pdim + prow + lane] = sum;
+                            if (MODE == kNN && p.sums != nullptr) {
+                                // the two sets of this quarter's warps meet; a sum is read before the set comes to the next tile
+                                // but one, which takes its place
+                                volatile float *from = reinterpret_cast<volatile float *>(smem + Cfg::kOffSums) + (acc * 128u + quarter * 32u);
+                                if (set == 1u) from[lane] = sum;
+                                ptx::named_barrier_sync(2 + quarter, 64);
+                                if (set == 0u && prow + lane < p.pdim) {
+                                    const uint32_t slot = tab_tile[s.g] / p.tiles_p + s.qi;
+                                    p.sums[size_t(slot) * p.pdim + prow + lane] = sum + from[lane];
+                                }
                             }
                         });
                 } else if (live) {
@@ -1521,7 +1532,7 @@ __global__ void __launch_bounds__(RaggedCfg<MODE, CG, QCAP, STAGES, EPI>::kThrea
             return true;
         });
         if (MODE == kTN && lane == 0) ptx::bulk_wait_group<0>();
-        if (MODE != kTN && stopped && warp == 2u) walk.leave_flags(rank, published, taken);
+        if (MODE != kTN && stopped && p.sk && warp == 2u) walk.leave_flags(rank, published, taken);
     } else if constexpr (Cfg::kHelper) {
         // ------------------------------------------------ helper
         // Four warps that share a stage's rows and never wait for each other: `fixed` counts them all.
