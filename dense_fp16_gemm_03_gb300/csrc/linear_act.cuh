@@ -47,70 +47,152 @@ __device__ __forceinline__ float sigmoid(float x)
     return rcp(1.0f + ex2(-kLog2e * x));
 }
 
-// P(z), and e^(-z^2/2) in `*e`
-__device__ __forceinline__ float normal_cdf(float z, float *e)
+// Two values side by side: sm_100 and later multiply and add them in one instruction, and with two values' exponentials and
+// reciprocals that is most of an activation (16384 x 4096 through gelu's derivative: 26 instructions a value one by one,
+// some 15 in pairs, where the bytes leave room for 30).
+struct Two {
+    uint64_t v;
+};
+
+__device__ __forceinline__ Two two(float a, float b)
 {
-    const float x = fabsf(z);
-    const float t = rcp(fmaf(0.3f, x, 1.0f));
-    const float g = ex2(z * z * (-0.5f * kLog2e));
-    float q = 0.03567477688193321f;
-    q = fmaf(q, t, -0.15720310807228088f);
-    q = fmaf(q, t, 0.20635353028774261f);
-    q = fmaf(q, t, -0.05368367210030556f);
-    q = fmaf(q, t, 0.12856164574623108f);
-    q = fmaf(q, t, 0.09991348534822464f);
-    q = fmaf(q, t, 0.12075395882129669f);
-    q = fmaf(q, t, 0.11962930113077164f);
-    q *= t * g;  // P(-x)
+    Two r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(a), "f"(b));
+    return r;
+}
+
+__device__ __forceinline__ Two two(float a)
+{
+    return two(a, a);
+}
+
+__device__ __forceinline__ float2 apart(Two a)
+{
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(a.v));
+    return r;
+}
+
+__device__ __forceinline__ Two operator*(Two a, Two b)
+{
+    Two r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
+}
+
+__device__ __forceinline__ Two operator+(Two a, Two b)
+{
+    Two r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
+}
+
+__device__ __forceinline__ Two fma(Two a, Two b, Two c)
+{
+    Two r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+    return r;
+}
+
+__device__ __forceinline__ Two ex2(Two a)
+{
+    const float2 x = apart(a);
+    return two(ex2(x.x), ex2(x.y));
+}
+
+__device__ __forceinline__ Two rcp(Two a)
+{
+    const float2 x = apart(a);
+    return two(rcp(x.x), rcp(x.y));
+}
+
+__device__ __forceinline__ Two sigmoid(Two x)
+{
+    return rcp(two(1.0f) + ex2(x * two(-kLog2e)));
+}
+
+// P(z), and e^(-z^2/2) in `*e`
+__device__ __forceinline__ Two normal_cdf(Two z, Two *e)
+{
+    const float2 s = apart(z);
+    const Two t = rcp(fma(two(0.3f), two(fabsf(s.x), fabsf(s.y)), two(1.0f)));
+    const Two g = ex2(z * z * two(-0.5f * kLog2e));
+    Two q = two(0.03567477688193321f);
+    q = fma(q, t, two(-0.15720310807228088f));
+    q = fma(q, t, two(0.20635353028774261f));
+    q = fma(q, t, two(-0.05368367210030556f));
+    q = fma(q, t, two(0.12856164574623108f));
+    q = fma(q, t, two(0.09991348534822464f));
+    q = fma(q, t, two(0.12075395882129669f));
+    q = fma(q, t, two(0.11962930113077164f));
+    q = q * (t * g);  // P(-|z|)
     *e = g;
-    return z > 0.0f ? 1.0f - q : q;
+    const float2 low = apart(q), high = apart(fma(q, two(-1.0f), two(1.0f)));
+    return two(s.x > 0.0f ? high.x : low.x, s.y > 0.0f ? high.y : low.y);
 }
 
 constexpr float kTanh1 = 1.5957691216057308f;             // 2 sqrt(2/pi)
 constexpr float kTanh3 = 1.5957691216057308f * 0.044715f;
 
-// s(2u)
-__device__ __forceinline__ float tanh_gate(float z)
+// s(2u), and z^2 in `*square`
+__device__ __forceinline__ Two tanh_gate(Two z, Two *square)
 {
-    return sigmoid(z * fmaf(kTanh3, z * z, kTanh1));
+    *square = z * z;
+    return sigmoid(z * fma(two(kTanh3), *square, two(kTanh1)));
+}
+
+__device__ __forceinline__ float relu(float z)
+{
+    return z <= 0.0f ? 0.0f : z;
 }
 
 template <int ACT>
-__device__ __forceinline__ float apply(float z)
+__device__ __forceinline__ Two apply(Two z)
 {
-    if constexpr (ACT == GEMM_ACT_RELU) return z <= 0.0f ? 0.0f : z;
+    const float2 s = apart(z);
+    if constexpr (ACT == GEMM_ACT_RELU) return two(relu(s.x), relu(s.y));
     if constexpr (ACT == GEMM_ACT_RELU2) {
-        const float r = z <= 0.0f ? 0.0f : z;
+        const Two r = two(relu(s.x), relu(s.y));
         return r * r;
     }
     if constexpr (ACT == GEMM_ACT_GELU) {
-        float e;
+        Two e;
         return z * normal_cdf(z, &e);
     }
-    if constexpr (ACT == GEMM_ACT_GELU_TANH) return z * tanh_gate(z);
+    if constexpr (ACT == GEMM_ACT_GELU_TANH) {
+        Two square;
+        return z * tanh_gate(z, &square);
+    }
     if constexpr (ACT == GEMM_ACT_SILU) return z * sigmoid(z);
     return z;
 }
 
 // d f'(z)
 template <int ACT>
-__device__ __forceinline__ float apply_grad(float d, float z)
+__device__ __forceinline__ Two apply_grad(Two d, Two z)
 {
-    if constexpr (ACT == GEMM_ACT_RELU) return z > 0.0f ? d : 0.0f;
-    if constexpr (ACT == GEMM_ACT_RELU2) return d * (2.0f * (z <= 0.0f ? 0.0f : z));
+    const float2 s = apart(z);
+    if constexpr (ACT == GEMM_ACT_RELU) {
+        const float2 g = apart(d);
+        return two(s.x > 0.0f ? g.x : 0.0f, s.y > 0.0f ? g.y : 0.0f);
+    }
+    if constexpr (ACT == GEMM_ACT_RELU2) return d * (two(relu(s.x), relu(s.y)) * two(2.0f));
     if constexpr (ACT == GEMM_ACT_GELU) {
-        float e;
-        const float p = normal_cdf(z, &e);
-        return d * fmaf(z * 0.3989422804014327f, e, p);
+        Two e;
+        const Two p = normal_cdf(z, &e);
+        return d * fma(z * two(0.3989422804014327f), e, p);
     }
     if constexpr (ACT == GEMM_ACT_GELU_TANH) {
-        const float s = tanh_gate(z);
-        // (where z^2 would be infinite, 1 - s is 0)
-        return d * fmaf(z * s * (1.0f - s), fmaf(3.0f * kTanh3, fminf(z * z, 1e30f), kTanh1), s);
+        Two square;
+        const Two p = tanh_gate(z, &square);
+        // (where z^2 would be infinite, 1 - p is 0)
+        const float2 sq = apart(square);
+        const Two slope = fma(two(3.0f * kTanh3), two(fminf(sq.x, 1e30f), fminf(sq.y, 1e30f)), two(kTanh1));
+        return d * fma(z * p * fma(p, two(-1.0f), two(1.0f)), slope, p);
     }
     if constexpr (ACT == GEMM_ACT_SILU) {
-        const float s = sigmoid(z);
-        return d * fmaf(z * s, 1.0f - s, s);
+        const Two p = sigmoid(z);
+        return d * fma(z * p, fma(p, two(-1.0f), two(1.0f)), p);
     }
     return d;
 }

@@ -38,28 +38,49 @@ size_t sums_bytes(int64_t per, int64_t groups, int64_t rows, int64_t cols)
     return size_t(round_up((rows / per + live_groups(groups, rows)) * cols * 4, 256));
 }
 
-// Rows of a piece of linear_grad_kernel: enough pieces to fill the SMs, few enough lines to add up.
+// How linear_grad_kernel cuts a matrix of so many columns: threads to a row of a strip (their logarithm), and strips.
+struct GradStrips {
+    int lanes;
+    int64_t count;
+};
+
+GradStrips grad_strips(int64_t cols)
+{
+    const int64_t quads = cols / 8;
+    GradStrips best = {5, cdiv(quads, 32)};
+    double use = 0.0;
+    for (int lanes = 5; lanes >= 3; --lanes) {
+        const int64_t count = cdiv(quads, int64_t(1) << lanes);
+        const double u = double(quads) / double(count << lanes);
+        if (u > use + 0.1) {  // (wide strips read longer pieces of a row)
+            use = u;
+            best = {lanes, count};
+        }
+    }
+    return best;
+}
+
+// Rows of a piece of linear_grad_kernel, in whole rounds of its threads: as many pieces as the SMs hold twice (once, three or
+// four times: 16384 x 4096 68.3, 69.2, 68.9 and 70.2 us, 8192 x 8192 71.6, 66.6, 66.2 and 65.9, 65536 x 1024 69.6, 70.3, 73.1
+// and 74.6), or small ones.
+constexpr int64_t kGradRows = 32;
+
+int64_t grad_pieces(int64_t cols, int num_sms)  // of one group, at most
+{
+    const int64_t most = 2 * kLinearGradBlocks * int64_t(num_sms) / grad_strips(cols).count;
+    return most < 1 ? 1 : most;
+}
+
 int64_t grad_rows(int64_t rows, int64_t cols, int num_sms)
 {
-    const int64_t strips = cdiv(cols, 256);
-    int64_t per = 128;
-    while (per > 32 && cdiv(rows, per) * strips < 8 * num_sms) per /= 2;
-    return per;
+    return round_up(cdiv(rows, grad_pieces(cols, num_sms)), kGradRows);
 }
 
 // What any number of rows up to this one may need for the partial sums of linear_grad_kernel.
 size_t grad_room(int64_t groups, int64_t rows, int64_t cols, int num_sms)
 {
-    size_t most = 0;
-    for (int64_t per = 32; per <= 128; per *= 2) {
-        // the most rows that take pieces of this size
-        int64_t r = rows;
-        if (grad_rows(rows, cols, num_sms) > per) r = (8 * num_sms / cdiv(cols, 256) + 1) * 2 * per;
-        if (r > rows) r = rows;
-        const size_t bytes = sums_bytes(per, groups, r, cols);
-        if (bytes > most) most = bytes;
-    }
-    return most;
+    const int64_t pieces = grad_pieces(cols, num_sms), small = cdiv(rows, kGradRows);
+    return size_t(round_up(((pieces < small ? pieces : small) + live_groups(groups, rows)) * cols * 4, 256));
 }
 
 gemm_status_t check_linear(gemm_dtype_t dtype, gemm_act_t act, int64_t groups, int64_t rows, int64_t n, int64_t k,
@@ -248,7 +269,7 @@ gemm_status_t gemm_linear_grad(gemm_dtype_t dtype, gemm_act_t act, int64_t group
     LinearDevice *dev = nullptr;
     st = linear_device(&dev);
     if (st != GEMM_OK) return st;
-    const int64_t per = grad_rows(rows, n, dev->num_sms), strips = cdiv(n, 256);
+    const int64_t per = grad_rows(rows, n, dev->num_sms), strips = grad_strips(n).count;
     const bool whole = offsets == nullptr && rows <= per;  // the sums of one piece are dbias
     const size_t need = dbias && !whole ? sums_bytes(per, groups, rows, n) : 0;
     if (workspace != nullptr || ws_bytes != 0 || need > 0) {
@@ -267,6 +288,7 @@ gemm_status_t gemm_linear_grad(gemm_dtype_t dtype, gemm_act_t act, int64_t group
     p.rows = uint32_t(rows);
     p.cols = uint32_t(n);
     p.per = uint32_t(per);
+    p.lanes = uint32_t(grad_strips(n).lanes);
     p.strips = uint32_t(strips);
     p.act = uint32_t(act);
     p.bf16 = dtype == GEMM_DTYPE_BF16;

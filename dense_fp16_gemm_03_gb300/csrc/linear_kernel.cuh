@@ -13,6 +13,7 @@
 namespace gemm_f16 {
 
 constexpr int kLinearThreads = 256;
+constexpr int kLinearGradBlocks = 4;  // of linear_grad_kernel on an SM
 
 // Row offsets as ragged_table has them (clamped, running maximum; null: one group of all rows), and the number of pieces
 // of `per` rows before each group.  Run by the whole block.
@@ -93,69 +94,69 @@ __global__ void __launch_bounds__(kLinearThreads) linear_sum_kernel(const __grid
     }
 }
 
-// dz = dy f'(z) and the sums of its columns: a block takes a piece of `per` rows of a group and 256 columns, a warp every
-// eighth row, a lane eight columns (16 bytes).  Bound by HBM for many rows.
+// dz = dy f'(z) and the sums of its columns: a block takes a piece of `per` rows of a group and a strip of columns, a thread
+// eight columns (16 bytes) of every so many rows.  A strip is 256, 128 or 64 columns, as they fill the matrix's width
+// best (40000 rows of 264 columns in strips of 256: 23 us).  Bound by HBM for many rows.
 struct LinearGradParams {
     const void *dy, *z;      // z: null without activation
     void *dz;                // or null
     float *sums;             // [pieces, cols] (one piece: dbias itself), or null
     const int32_t *offsets;  // or null
     uint32_t groups, rows, cols, per;
-    uint32_t strips;         // ceil(cols / 256)
+    uint32_t lanes;          // 2^lanes threads to a row of a strip
+    uint32_t strips;
     uint32_t act, bf16;
 };
 
 template <int ACT>
-__device__ __forceinline__ void linear_grad_rows(const LinearGradParams &p, uint32_t begin, uint32_t end, uint32_t col, float (&sum)[8])
+__device__ __forceinline__ void linear_grad_rows(const LinearGradParams &p, uint32_t begin, uint32_t end, uint32_t col, act::Two (&sum)[4])
 {
     const bool bf16 = p.bf16 != 0u;
-    constexpr uint32_t kStep = kLinearThreads / 32;
+    const uint32_t step = kLinearThreads >> p.lanes;
     constexpr int kAhead = 4;
     const size_t pitch = size_t(p.cols) * 2u;
     const char *dy = static_cast<const char *>(p.dy) + size_t(col) * 2u;
     const char *z = static_cast<const char *>(p.z) + size_t(col) * 2u;
     char *dz = static_cast<char *>(p.dz) + size_t(col) * 2u;
-    for (uint32_t r = begin + (threadIdx.x >> 5); r < end; r += kStep * kAhead) {
+    for (uint32_t r = begin + (threadIdx.x >> p.lanes); r < end; r += step * kAhead) {
         uint4 d[kAhead], v[kAhead];
 #pragma unroll
         for (int i = 0; i < kAhead; ++i) {
-            const uint32_t row = r + uint32_t(i) * kStep;
+            const uint32_t row = r + uint32_t(i) * step;
             const bool there = row < end;
             d[i] = there ? *reinterpret_cast<const uint4 *>(dy + row * pitch) : make_uint4(0u, 0u, 0u, 0u);
             v[i] = (ACT != GEMM_ACT_NONE && there) ? *reinterpret_cast<const uint4 *>(z + row * pitch) : make_uint4(0u, 0u, 0u, 0u);
         }
 #pragma unroll
         for (int i = 0; i < kAhead; ++i) {
-            const uint32_t row = r + uint32_t(i) * kStep;
+            const uint32_t row = r + uint32_t(i) * step;
             if (row >= end) break;
             const uint32_t a[4] = {d[i].x, d[i].y, d[i].z, d[i].w}, b[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
             uint32_t w[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                float2 g = ragged_unpack(a[j], bf16);
-                const float2 at = ragged_unpack(b[j], bf16);
-                g.x = act::apply_grad<ACT>(g.x, at.x);
-                g.y = act::apply_grad<ACT>(g.y, at.y);
-                sum[2 * j] += g.x;
-                sum[2 * j + 1] += g.y;
-                w[j] = ragged_pack(g.x, g.y, bf16);
+                const float2 g = ragged_unpack(a[j], bf16), at = ragged_unpack(b[j], bf16);
+                const act::Two f = act::apply_grad<ACT>(act::two(g.x, g.y), act::two(at.x, at.y));
+                sum[j] = sum[j] + f;
+                const float2 out = act::apart(f);
+                w[j] = ragged_pack(out.x, out.y, bf16);
             }
             if (p.dz) *reinterpret_cast<uint4 *>(dz + row * pitch) = make_uint4(w[0], w[1], w[2], w[3]);
         }
     }
 }
 
-__global__ void __launch_bounds__(kLinearThreads) linear_grad_kernel(const __grid_constant__ LinearGradParams p)
+__global__ void __launch_bounds__(kLinearThreads, kLinearGradBlocks) linear_grad_kernel(const __grid_constant__ LinearGradParams p)
 {
     __shared__ int32_t s_row[kRagMaxGroups + 1];
     __shared__ uint32_t s_piece[kRagMaxGroups + 1];
-    __shared__ float s_sum[kLinearThreads / 32][kLinearThreads];
+    __shared__ __align__(8) float s_sum[8 * kLinearThreads];  // a line of a strip's columns for each of its rows' threads
     ptx::griddep_wait();
     ptx::griddep_launch_dependents();
     linear_table(p.offsets, p.groups, p.rows, p.per, s_row, s_piece);
-    const uint32_t lane = threadIdx.x & 31u, warp = threadIdx.x >> 5;
+    const uint32_t width = 8u << p.lanes;  // columns of a strip
     const uint32_t piece = blockIdx.x / p.strips, strip = blockIdx.x - piece * p.strips;
-    const uint32_t col = strip * 256u + lane * 8u;
+    const uint32_t at = (threadIdx.x * 8u) & (width - 1u), col = strip * width + at;
     if (p.dz) {  // rows of no group
         const uint64_t quads = p.cols / 8u, first = uint64_t(blockIdx.x) * kLinearThreads + threadIdx.x;
         const uint64_t stride = uint64_t(gridDim.x) * kLinearThreads;
@@ -173,18 +174,20 @@ __global__ void __launch_bounds__(kLinearThreads) linear_grad_kernel(const __gri
     }
     const uint32_t begin = uint32_t(s_row[g]) + (piece - s_piece[g]) * p.per;
     const uint32_t end = min(begin + p.per, uint32_t(s_row[g + 1u]));
-    float sum[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    act::Two sum[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) sum[j] = act::two(0.0f);
     if (col < p.cols)
         act::with_kind(p.act, [&](auto kind) { linear_grad_rows<decltype(kind)::value>(p, begin, end, col, sum); });
     if (p.sums == nullptr) return;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) s_sum[warp][lane * 8u + uint32_t(j)] = sum[j];
+    for (int j = 0; j < 4; ++j) *reinterpret_cast<float2 *>(&s_sum[threadIdx.x * 8u + 2u * uint32_t(j)]) = act::apart(sum[j]);
     __syncthreads();
-    const uint32_t mine = strip * 256u + threadIdx.x;
-    if (mine < p.cols) {
+    const uint32_t mine = strip * width + threadIdx.x;
+    if (threadIdx.x < width && mine < p.cols) {
         float all = 0.0f;
-#pragma unroll
-        for (int i = 0; i < kLinearThreads / 32; ++i) all += s_sum[i][threadIdx.x];
+#pragma unroll 8
+        for (uint32_t i = threadIdx.x; i < 8u * kLinearThreads; i += width) all += s_sum[i];
         p.sums[size_t(piece) * p.cols + mine] = all;
     }
 }

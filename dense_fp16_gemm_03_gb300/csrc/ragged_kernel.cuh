@@ -1440,7 +1440,7 @@ __global__ void __launch_bounds__(RaggedCfg<MODE, CG, QCAP, STAGES, EPI>::kThrea
                     if constexpr (EPI)
                         act::with_kind(p.act, [&](auto kind) {
                             constexpr int kAct = decltype(kind)::value;
-                            float sum = 0.0f;
+                            act::Two both = act::two(0.0f);
                             for (uint32_t c = set; c < chunks; c += Cfg::kEpiSets) {
                                 uint32_t r[32], w[16];
                                 if (p.in != nullptr) {
@@ -1458,20 +1458,26 @@ __global__ void __launch_bounds__(RaggedCfg<MODE, CG, QCAP, STAGES, EPI>::kThrea
 #pragma unroll
                                     for (int i = 0; i < 16; ++i) {
                                         const float2 add = ragged_unpack(w[i], bf16);
-                                        r[2 * i] = __float_as_uint(act::apply<kAct>(__uint_as_float(r[2 * i])) + add.x);
-                                        r[2 * i + 1] = __float_as_uint(act::apply<kAct>(__uint_as_float(r[2 * i + 1])) + add.y);
+                                        const act::Two z = act::two(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1]));
+                                        const float2 f = act::apart(act::apply<kAct>(z) + act::two(add.x, add.y));
+                                        r[2 * i] = __float_as_uint(f.x);
+                                        r[2 * i + 1] = __float_as_uint(f.y);
                                     }
                                 } else {
 #pragma unroll
                                     for (int i = 0; i < 16; ++i) {
                                         const float2 z = ragged_unpack(w[i], bf16);
-                                        r[2 * i] = __float_as_uint(act::apply_grad<kAct>(__uint_as_float(r[2 * i]), z.x));
-                                        r[2 * i + 1] = __float_as_uint(act::apply_grad<kAct>(__uint_as_float(r[2 * i + 1]), z.y));
+                                        const act::Two d = act::two(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1]));
+                                        const float2 f = act::apart(act::apply_grad<kAct>(d, act::two(z.x, z.y)));
+                                        r[2 * i] = __float_as_uint(f.x);
+                                        r[2 * i + 1] = __float_as_uint(f.y);
                                     }
                                     if (p.sums != nullptr) {
+                                        const uint32_t left = s.qn - 32u * c;  // rows of the tile in this piece and behind it
 #pragma unroll
-                                        for (uint32_t j = 0; j < 32u; ++j)
-                                            if (32u * c + j < s.qn) sum += __uint_as_float(r[j]);
+                                        for (uint32_t j = 0; j < 32u; j += 2u)
+                                            both = both + act::two(left >= 32u || j < left ? __uint_as_float(r[j]) : 0.0f,
+                                                                   left >= 32u || j + 1u < left ? __uint_as_float(r[j + 1]) : 0.0f);
                                     }
                                 }
                                 linear_store(p.out, p.pdim, s, prow, c, buf, r, bf16);
@@ -1480,6 +1486,8 @@ __global__ void __launch_bounds__(RaggedCfg<MODE, CG, QCAP, STAGES, EPI>::kThrea
                                 // the two sets of this quarter's warps meet; a sum is read before the set comes to the next tile
                                 // but one, which takes its place
                                 volatile float *from = reinterpret_cast<volatile float *>(smem + Cfg::kOffSums) + (acc * 128u + quarter * 32u);
+                                const float2 sums = act::apart(both);
+                                const float sum = sums.x + sums.y;
                                 if (set == 1u) from[lane] = sum;
                                 ptx::named_barrier_sync(2 + quarter, 64);
                                 if (set == 0u && prow + lane < p.pdim) {
