@@ -1,6 +1,7 @@
 """An expert layer and an adapted projection, run with the ragged products as a model would: forward, backward, decode.
 
     python -m dense_fp16_gemm_03_gb300.expert_layer [--rows 4096] [--width 1024] [--hidden 2048] [--experts 32] [--top 4]
+                                                    [--groups 8] [--top-groups 4] [--shared 2048]
 
 The layer sends every row to ``top`` experts, each a product of its own, a square of the positive part, and a product
 back, and adds their results weighted by the router:
@@ -9,14 +10,16 @@ back, and adds their results weighted by the router:
     out[t] = sum_j w[t, j] relu(x[t] . up[e_tj]^T)^2 . down[e_tj]^T
 
 The grouped products, the router and its gradient are this package's; what is between them (gathering rows, the
-activation, adding rows up) is plain torch.  ``adapted`` is a projection with a low-rank adapter per row.
+activation, adding rows up) is plain torch.  ``SharedExpertLayer`` has the activations in the products, a router that scores
+by sigmoid, chooses with a bias within the best groups of experts, and an expert that every row shares.  ``adapted`` is a
+projection with a low-rank adapter per row.
 """
 import argparse
 import time
 
 import torch
 
-from . import gemm, ragged
+from . import gemm, linear, ragged
 
 
 class ExpertLayer:
@@ -76,6 +79,78 @@ class ExpertLayer:
         return dx.to(x.dtype), dlogits.T @ x.float(), dup, ddown
 
 
+class SharedExpertLayer(ExpertLayer):
+    """An expert layer with a shared expert of `shared` hidden columns beside the routed ones:
+
+        l = x . router^T;  s = sigmoid(l);  e = top-k of s + balance within the best groups of experts
+        w = scale s[e] / sum of s[e]
+        out[t] = sum_j w[t, j] relu(x[t] . up[e_tj]^T)^2 . down[e_tj]^T + gelu(x[t] . w1^T + b1) . w2^T + b2
+
+    The activations, the biases and the sum with the routed experts are in the products' epilogues, their gradients in those of
+    the products backwards."""
+
+    def __init__(self, width, hidden, experts, top, rows, shared, groups=1, top_groups=None, scale=1.0, dtype=torch.bfloat16, seed=0,
+                 device="cuda"):
+        super().__init__(width, hidden, experts, top, rows, dtype=dtype, seed=seed, device=device)
+        gen = torch.Generator(device=device).manual_seed(seed + 1)
+
+        def normal(shape, scale):
+            return torch.empty(shape, dtype=dtype, device=device).normal_(0.0, scale, generator=gen)
+
+        self.groups, self.top_groups, self.scale = groups, groups if top_groups is None else top_groups, scale
+        self.balance = torch.zeros(experts, device=device)
+        self.w1, self.b1 = normal((shared, width), width ** -0.5), normal((shared,), 0.1)
+        self.w2, self.b2 = normal((width, shared), shared ** -0.5), normal((width,), 0.1)
+        sizes = [linear.gemm_linear_workspace_size(experts, rows * top, hidden, width),
+                 linear.gemm_linear_workspace_size(experts, rows * top, width, hidden),
+                 linear.gemm_linear_workspace_size(1, rows, shared, width), linear.gemm_linear_workspace_size(1, rows, width, shared),
+                 ragged.gemm_grouped_workspace_size(1, rows, shared, width), ragged.gemm_grouped_workspace_size(1, rows, width, shared),
+                 self.work.numel()]
+        self.work = torch.empty(max(sizes), dtype=torch.uint8, device=device)
+
+    def forward(self, x):
+        """out [rows, width], and what the backward pass needs."""
+        logits = x.float() @ self.router.float().T
+        r = ragged.gemm_route_scored(logits, self.top, score="sigmoid", bias=self.balance, groups=self.groups, top_groups=self.top_groups,
+                                     scale=self.scale, workspace=self.route_work)
+        token = (r.order.clamp(min=0) // self.top).long()
+        xs = x[token]
+        a, h = linear.gemm_linear_nt(xs, self.up, act="relu2", offsets=r.offsets, keep=True, workspace=self.work)
+        ys = ragged.gemm_grouped_nt(a, self.down, r.offsets, workspace=self.work)
+        mine = torch.where((r.position >= 0)[:, :, None], ys[r.position.clamp(min=0).long()].float(), 0.0)
+        routed = (r.weights[:, :, None] * mine).sum(1).to(x.dtype)
+        s, z = linear.gemm_linear_nt(x, self.w1, bias=self.b1, act="gelu", keep=True, workspace=self.work)
+        out = linear.gemm_linear_nt(s, self.w2, bias=self.b2, residual=routed, workspace=self.work)
+        return out, (x, logits, r, token, xs, h, a, mine, s, z)
+
+    def backward(self, dout, saved):
+        """Gradients of x, router, up, down, w1, b1, w2 and b2."""
+        x, logits, r, token, xs, h, a, mine, s, z = saved
+        rows = x.shape[0]
+        every = torch.arange(0, rows + 1, max(rows, 1), dtype=torch.int32, device=x.device)  # all rows as one group
+        _, db2 = linear.gemm_linear_grad(dout, bias_grad=True, workspace=self.work)
+        dw2 = ragged.gemm_grouped_tn(dout, s, every, dtype=torch.float32, workspace=self.work)[0]
+        dz, db1 = linear.gemm_linear_nn(dout, self.w2, z=z, act="gelu", bias_grad=True, workspace=self.work)
+        dw1 = ragged.gemm_grouped_tn(dz, x, every, dtype=torch.float32, workspace=self.work)[0]
+        dshared = linear.gemm_linear_nn(dz, self.w1, workspace=self.work)
+        dmine = r.weights[:, :, None] * dout.float()[:, None, :]
+        dweights = (mine * dout.float()[:, None, :]).sum(2)
+        dys = torch.where((r.order >= 0)[:, None], dmine.reshape(-1, self.width)[r.order.clamp(min=0).long()], 0.0).to(xs.dtype)
+        ddown = ragged.gemm_grouped_tn(dys, a, r.offsets, dtype=torch.float32, workspace=self.work)
+        dh = linear.gemm_linear_nn(dys, self.down, z=h, act="relu2", offsets=r.offsets, workspace=self.work)
+        dup = ragged.gemm_grouped_tn(dh, xs, r.offsets, dtype=torch.float32, workspace=self.work)
+        dxs = ragged.gemm_grouped_nn(dh, self.up, r.offsets, workspace=self.work)
+        dlogits = ragged.gemm_route_scored_grad(logits, r.ids, dweights, score="sigmoid", scale=self.scale)
+        dmine_x = torch.where((r.position >= 0)[:, :, None], dxs[r.position.clamp(min=0).long()].float(), 0.0)
+        dx = dlogits @ self.router.float() + dmine_x.sum(1) + dshared.float()
+        return dx.to(x.dtype), dlogits.T @ x.float(), dup, ddown, dw1, db1, dw2, db2
+
+    def rebalance(self, routing, rate=1e-3):
+        """Moves the experts' bias a step towards those with fewer rows than the mean."""
+        counts = torch.diff(routing.offsets).float()
+        self.balance += rate * torch.sign(counts.mean() - counts)
+
+
 def adapted(x, w, a, b, ids, scale):
     """A shared projection of rows that belong to many requests, each with an adapter of its own."""
     size = ragged.gemm_lora_workspace_size(x.shape[0], w.shape[0], x.shape[1], a.shape[1], a.shape[0])
@@ -84,7 +159,8 @@ def adapted(x, w, a, b, ids, scale):
 
 def main():
     ap = argparse.ArgumentParser(description=__doc__.splitlines()[0])
-    for name, default in (("rows", 4096), ("width", 1024), ("hidden", 2048), ("experts", 32), ("top", 4)):
+    for name, default in (("rows", 4096), ("width", 1024), ("hidden", 2048), ("experts", 32), ("top", 4), ("groups", 8),
+                          ("top-groups", 4), ("shared", 2048)):
         ap.add_argument("--" + name, type=int, default=default)
     args = ap.parse_args()
     layer = ExpertLayer(args.width, args.hidden, args.experts, args.top, args.rows)
@@ -99,13 +175,18 @@ def main():
         for _ in range(n):
             r = f()
         torch.cuda.synchronize()
-        print("%-28s %9.1f us" % (name, (time.perf_counter() - t) / n * 1e6))
+        print("%-32s %9.1f us" % (name, (time.perf_counter() - t) / n * 1e6))
         return r
 
     _, saved = timed("expert layer, forward", lambda: layer.forward(x))
     timed("expert layer, backward", lambda: layer.backward(dout, saved))
     one = x[:1].contiguous()
     timed("expert layer, one token", lambda: layer.forward(one))
+    both = SharedExpertLayer(args.width, args.hidden, args.experts, args.top, args.rows, args.shared, groups=args.groups,
+                             top_groups=args.top_groups)
+    _, saved = timed("with a shared expert, forward", lambda: both.forward(x))
+    timed("with a shared expert, backward", lambda: both.backward(dout, saved))
+    timed("with a shared expert, one token", lambda: both.forward(one))
     rank, adapters = 16, 64
     a = (torch.randn(adapters, rank, args.width, device="cuda") * args.width ** -0.5).bfloat16()
     b = (torch.randn(adapters, args.hidden, rank, device="cuda") * rank ** -0.5).bfloat16()
