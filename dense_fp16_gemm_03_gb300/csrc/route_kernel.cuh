@@ -35,13 +35,16 @@ namespace gemm_f16 {
 constexpr int kRouteFewRows = 64;
 constexpr int kRouteRows = 32;
 constexpr int kRouteThreads = 1024;  // of the block for few rows, and of the kernels that place rows
-constexpr int kRouteDirectBlocks = 32;  // up to so many blocks each one sums the counts before it by itself
+constexpr int kRouteDirectBlocks = 32;  // up to so many blocks each one sums the counts before it by itself,
+constexpr int kRouteDirectMost = 256;   // or up to so many with few counts in all (top-k and places, summed by the blocks and by
+constexpr int kRouteDirectCounts = 8192;  // the scan: 4096 x 64 9.2 and 11.8 us, 8192 x 32 10.5 and 11.4; 4096 x 128 11.2 and 9.5)
 constexpr int kRouteMaxExperts = 1024;
 
 struct RouteParams {
     const void *logits;
     uint32_t dtype;  // 0 fp16, 1 bf16, 2 fp32
     uint32_t rows, experts, top, renorm, blocks;
+    uint32_t direct;  // the blocks that place rows sum the counts themselves
     int32_t *ids;
     float *weights;
     int32_t *offsets, *order, *position;
@@ -348,7 +351,7 @@ __global__ void __launch_bounds__(kRouteThreads) route_place_kernel(const __grid
     ptx::griddep_wait();
     const uint32_t t = threadIdx.x;
     int32_t count = 0, prefix = 0;  // of expert t: all its rows, and those of the blocks before this one
-    if (p.blocks <= kRouteDirectBlocks) {
+    if (p.direct) {
         // `lanes` threads to an expert, each sums every lanes-th block; then one adds them up
         uint32_t lanes = kRouteThreads / p.experts;
         lanes = lanes > 32u ? 32u : lanes;

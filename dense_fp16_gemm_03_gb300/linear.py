@@ -68,19 +68,20 @@ def _groups(offsets, dev):
     return groups, offsets.data_ptr(), (groups,)
 
 
-def _weights(w, stack, which, size, kind, dev):
-    """n and k of the weights, whose extent `which` has to be `size`."""
-    if w.dim() != len(stack) + 2:
+def _weights(w, stack):
+    """n and k of the weights."""
+    shape = w.shape
+    if len(shape) != len(stack) + 2:
         raise ValueError("w must be [groups, n, k]" if stack else "w must be [n, k] without offsets")
-    n, k = w.shape[-2:]
-    _need(w, "w", stack + ((n, size) if which == "k" else (size, k)), kind, dev)
-    return n, k
+    return shape[-2], shape[-1]
 
 
-def _optional(t, what, shape, dtype, dev):
+def _at(t, what, shape, dtype, dev):
+    """The address of a tensor that has to be as _need says, or None."""
     if t is None:
         return None
-    _need(t, what, shape, dtype, dev)
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != dev or not t.is_contiguous():
+        _need(t, what, shape, dtype, dev)
     return t.data_ptr()
 
 
@@ -93,24 +94,30 @@ def gemm_linear_nt(x, w, bias=None, residual=None, act=None, offsets=None, keep=
 
     x [rows, k], w [n, k], bias [n], residual [rows, n] (y may be the residual itself); with offsets [groups + 1] int32 on the
     device w [groups, n, k], bias [groups, n], and rows of no group are zero."""
-    lib()
+    if _lib is None:
+        lib()
     code = _act(act)
     dev, kind = _operand(x, "x", 2), x.dtype
     groups, ends, stack = _groups(offsets, dev)
     rows, k = x.shape
-    n, _ = _weights(w, stack, "k", k, kind, dev)
+    n, _ = _weights(w, stack)
     dtype = _dtype(kind)
-    b = _optional(bias, "bias", stack + (n,), kind, dev)
-    r = _optional(residual, "residual", (rows, n), kind, dev)
+    wp = _at(w, "w", (*stack, n, k), kind, dev)
+    b = _at(bias, "bias", (*stack, n), kind, dev)
+    shape = (rows, n)
+    r = _at(residual, "residual", shape, kind, dev)
+    zp = None
     if keep:
-        z = _out(z, "z", (rows, n), kind, dev)
+        z = _out(z, "z", shape, kind, dev)
+        zp = z.data_ptr()
     elif z is not None:
         raise ValueError("z is written with keep only")
-    y = _out(y, "y", (rows, n), kind, dev)
+    y = _out(y, "y", shape, kind, dev)
     ws, ws_bytes = _workspace(workspace, dev)
-    st = _lib.gemm_linear_nt(dtype, code, groups, rows, n, k, ends, x.data_ptr(), w.data_ptr(), b, r,
-                             z.data_ptr() if keep else None, y.data_ptr(), ws, ws_bytes, _stream(stream, dev))
-    _check(st, "gemm_linear_nt")
+    st = _lib.gemm_linear_nt(dtype, code, groups, rows, n, k, ends, x.data_ptr(), wp, b, r, zp, y.data_ptr(), ws, ws_bytes,
+                             _stream(stream, dev))
+    if st:
+        _check(st, "gemm_linear_nt")
     return (y, z) if keep else y
 
 
@@ -119,27 +126,31 @@ def gemm_linear_nn(dy, w, z=None, act=None, offsets=None, bias_grad=False, dx=No
     over the rows (of each group) in float32.
 
     dy [rows, n], w [n, k] or [groups, n, k], z [rows, k] (not needed without `act`; dx may be z itself)."""
-    lib()
+    if _lib is None:
+        lib()
     code = _act(act)
     dev, kind = _operand(dy, "dy", 2), dy.dtype
     groups, ends, stack = _groups(offsets, dev)
     rows, n = dy.shape
-    _, k = _weights(w, stack, "n", n, kind, dev)
+    _, k = _weights(w, stack)
     dtype = _dtype(kind)
+    wp = _at(w, "w", (*stack, n, k), kind, dev)
     if code and z is None:
         raise ValueError("z is needed for act=%r" % (act,))
-    at = _optional(z, "z", (rows, k), kind, dev)
-    dx = _out(dx, "dx", (rows, k), kind, dev)
+    shape = (rows, k)
+    at = _at(z, "z", shape, kind, dev)
+    dx = _out(dx, "dx", shape, kind, dev)
     db = None
     if bias_grad:
-        dbias = _out(dbias, "dbias", stack + (k,), _gemm._tm().float32, dev)
+        dbias = _out(dbias, "dbias", (*stack, k), _gemm._tm().float32, dev)
         db = dbias.data_ptr()
     elif dbias is not None:
         raise ValueError("dbias is written with bias_grad only")
     ws, ws_bytes = _workspace(workspace, dev)
-    st = _lib.gemm_linear_nn(dtype, code, groups, rows, n, k, ends, dy.data_ptr(), w.data_ptr(), at, dx.data_ptr(), db, ws, ws_bytes,
+    st = _lib.gemm_linear_nn(dtype, code, groups, rows, n, k, ends, dy.data_ptr(), wp, at, dx.data_ptr(), db, ws, ws_bytes,
                              _stream(stream, dev))
-    _check(st, "gemm_linear_nn")
+    if st:
+        _check(st, "gemm_linear_nn")
     return (dx, dbias) if bias_grad else dx
 
 
@@ -147,7 +158,8 @@ def gemm_linear_grad(dy, z=None, act=None, offsets=None, bias_grad=False, dz=Non
     """dz = dy * f'(z); with `bias_grad` (dz, dbias), dbias the sum of dz over the rows (of each group) in float32.
 
     dy, z [rows, n]; dz may be dy or z.  Without `act` dz is dy, which is returned as it is unless another dz is given."""
-    lib()
+    if _lib is None:
+        lib()
     code = _act(act)
     dev, kind = _operand(dy, "dy", 2), dy.dtype
     groups, ends, stack = _groups(offsets, dev)
@@ -155,7 +167,7 @@ def gemm_linear_grad(dy, z=None, act=None, offsets=None, bias_grad=False, dz=Non
     dtype = _dtype(kind)
     if code and z is None:
         raise ValueError("z is needed for act=%r" % (act,))
-    at = _optional(z, "z", (rows, n), kind, dev)
+    at = _at(z, "z", dy.shape, kind, dev)
     if code or dz is not None:
         dz = _out(dz, "dz", (rows, n), kind, dev)
         to = dz.data_ptr()
@@ -163,13 +175,14 @@ def gemm_linear_grad(dy, z=None, act=None, offsets=None, bias_grad=False, dz=Non
         dz, to = dy, None
     db = None
     if bias_grad:
-        dbias = _out(dbias, "dbias", stack + (n,), _gemm._tm().float32, dev)
+        dbias = _out(dbias, "dbias", (*stack, n), _gemm._tm().float32, dev)
         db = dbias.data_ptr()
     elif dbias is not None:
         raise ValueError("dbias is written with bias_grad only")
     ws, ws_bytes = _workspace(workspace, dev)
     st = _lib.gemm_linear_grad(dtype, code, groups, rows, n, ends, dy.data_ptr(), at, to, db, ws, ws_bytes, _stream(stream, dev))
-    _check(st, "gemm_linear_grad")
+    if st:
+        _check(st, "gemm_linear_grad")
     return (dz, dbias) if bias_grad else dz
 
 
@@ -179,11 +192,12 @@ def gemm_linear_stall_test(mode, first, w, extra, out, dbias, workspace, skip_fi
     dev, kind = _operand(first, "first", 2), first.dtype
     groups, ends, stack = _groups(offsets, dev)
     rows = first.shape[0]
-    n, k = _weights(w, stack, "n" if mode else "k", first.shape[1], kind, dev)
+    n, k = _weights(w, stack)
+    wp = _at(w, "w", (*stack, first.shape[1], k) if mode else (*stack, n, first.shape[1]), kind, dev)
     shape = (rows, k if mode else n)
     _need(out, "out", shape, kind, dev)
-    more = _optional(extra, "extra", shape, kind, dev)
-    db = _optional(dbias, "dbias", stack + (k,), _gemm._tm().float32, dev)
+    more = _at(extra, "extra", shape, kind, dev)
+    db = _at(dbias, "dbias", (*stack, k), _gemm._tm().float32, dev)
     ws, ws_bytes = _workspace(workspace, dev)
-    return _lib.gemm_linear_stall_test(mode, _dtype(kind), _act(act), groups, rows, n, k, ends, first.data_ptr(), w.data_ptr(), more,
+    return _lib.gemm_linear_stall_test(mode, _dtype(kind), _act(act), groups, rows, n, k, ends, first.data_ptr(), wp, more,
                                        out.data_ptr(), db, ws, ws_bytes, skip_fill, wait_limit_cycles, _stream(stream, dev))
