@@ -20,7 +20,7 @@ using LinearDevice = RaggedDeviceOf<int(sizeof(kLinear) / sizeof(kLinear[0]))>;
 
 gemm_status_t linear_device(LinearDevice **out)
 {
-    return ragged_device_of(kLinear, nullptr, 0, out);
+    return ragged_device_of(kLinear, nullptr, 0, nullptr, 0, out);
 }
 
 // What splitting the last wave costs, us: 3000 rows, 5000 x 4096 86.1 -> 78.4, 2500 rows, 4096 x 8192 120.7 -> 98.4, but 4096 rows,
@@ -79,6 +79,7 @@ int64_t grad_rows(int64_t rows, int64_t cols, int num_sms)
 // What any number of rows up to this one may need for the partial sums of linear_grad_kernel.
 size_t grad_room(int64_t groups, int64_t rows, int64_t cols, int num_sms)
 {
+    if (cols == 0) return 0;
     const int64_t pieces = grad_pieces(cols, num_sms), small = cdiv(rows, kGradRows);
     return size_t(round_up(((pieces < small ? pieces : small) + live_groups(groups, rows)) * cols * 4, 256));
 }

@@ -49,10 +49,19 @@ const void *const kBeside[] = {
     reinterpret_cast<const void *>(&lora_shrink_kernel<4>), reinterpret_cast<const void *>(&lora_list_kernel), reinterpret_cast<const void *>(&ragged_maps_kernel),
 };
 
+// The router's instances for few and for many rows, with a warp's lists.
+#define ROUTE_SCORED_LARGE(V)                                                                                                       \
+    {reinterpret_cast<const void *>(&route_scored_kernel<V, kRouteThreads>), kRouteThreads / 32 * int(kRouteListBytes<V>)},         \
+        {reinterpret_cast<const void *>(&route_scored_kernel<V, 16 * kRouteRows>), kRouteRows / 2 * int(kRouteListBytes<V>)}
+
+const KernelSmem kLarge[] = {ROUTE_SCORED_LARGE(1), ROUTE_SCORED_LARGE(2),  ROUTE_SCORED_LARGE(4),
+                             ROUTE_SCORED_LARGE(8), ROUTE_SCORED_LARGE(16), ROUTE_SCORED_LARGE(32)};
+
 // State of the current device for these kernels.
 gemm_status_t ragged_device(RaggedDevice **out)
 {
-    return ragged_device_of(kRagged, kBeside, int(sizeof(kBeside) / sizeof(kBeside[0])), out);
+    return ragged_device_of(kRagged, kBeside, int(sizeof(kBeside) / sizeof(kBeside[0])), kLarge,
+                            int(sizeof(kLarge) / sizeof(kLarge[0])), out);
 }
 
 gemm_status_t launch_ragged(int variant, const RaggedDevice *dev, RaggedParams &p, int64_t most_units, cudaStream_t stream)
@@ -724,8 +733,8 @@ static gemm_status_t route_begin(RouteParams *p, gemm_dtype_t dtype, int64_t row
                             static_cast<const void *>(position)})
         if (st == GEMM_OK) st = check_pointer(ptr, any, 4);
     if (st != GEMM_OK) return st;
-    DeviceState state;
-    st = current_device_state(&state);
+    RaggedDevice *dev = nullptr;
+    st = ragged_device(&dev);
     if (st != GEMM_OK) return st;
     *done = !any;
     if (!any) {
@@ -826,15 +835,6 @@ gemm_status_t gemm_route_topk_grad(gemm_dtype_t dtype, int64_t rows, int64_t exp
 #define ROUTE_LIST(V) kRouteListBytes<V>
 #define ROUTE_SCORED_GRAD(V) reinterpret_cast<const void *>(&route_scored_grad_kernel<V>)
 
-// More than 48 KB of shared memory (12.2 KB of it static) have to be asked for: instances of many experts a lane.
-static gemm_status_t route_smem(const void *fn, int bytes)
-{
-    if (bytes <= 32 * 1024) return GEMM_OK;
-    if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) == cudaSuccess) return GEMM_OK;
-    cudaGetLastError();
-    return GEMM_ERR_CUDA;
-}
-
 gemm_status_t gemm_route_scored(gemm_dtype_t dtype, gemm_route_score_t score, int64_t rows, int64_t experts, int64_t top,
                                 int64_t groups, int64_t top_groups, int32_t group_top, int32_t renorm, float scale,
                                 const void *logits, const float *bias, int32_t *ids, float *weights, int32_t *offsets,
@@ -870,8 +870,6 @@ gemm_status_t gemm_route_scored(gemm_dtype_t dtype, gemm_route_score_t score, in
     const bool one = p.blocks == 1u;
     const void *fn = one ? ROUTE_INSTANCE(ROUTE_SCORED_FEW, lanes) : ROUTE_INSTANCE(ROUTE_SCORED, lanes);
     const int warp_smem = int(ROUTE_INSTANCE(ROUTE_LIST, lanes));
-    st = route_smem(fn, (one ? kRouteThreads : 16 * kRouteRows) / 32 * warp_smem);
-    if (st != GEMM_OK) return st;
     return route_launch(fn, p, &p, warp_smem, s);
 }
 

@@ -60,11 +60,17 @@ struct RaggedDeviceOf {
     uint32_t *error_word = nullptr;
 };
 
-// State of the current device for a table of variants, and `beside` small kernels that run in front of them, made once per
-// context.
+// A kernel and its dynamic shared memory.
+struct KernelSmem {
+    const void *fn;
+    int bytes;
+};
+
+// State of the current device for a table of variants, `beside` small kernels that run in front of them, and `large` ones that
+// need more shared memory than a launch has unasked, made once per context.
 template <int COUNT>
 gemm_status_t ragged_device_of(const RaggedVariant (&variants)[COUNT], const void *const *beside, int num_beside,
-                               RaggedDeviceOf<COUNT> **out)
+                               const KernelSmem *large, int num_large, RaggedDeviceOf<COUNT> **out)
 {
     DeviceState state;
     gemm_status_t st = current_device_state(&state);
@@ -108,6 +114,12 @@ gemm_status_t ragged_device_of(const RaggedVariant (&variants)[COUNT], const voi
                     made.slots[v] = clusters;
                 else
                     cudaGetLastError();
+            }
+        }
+        for (int i = 0; i < num_large; ++i) {
+            if (cudaFuncSetAttribute(large[i].fn, cudaFuncAttributeMaxDynamicSharedMemorySize, large[i].bytes) != cudaSuccess) {
+                cudaGetLastError();
+                return GEMM_ERR_CUDA;
             }
         }
         // The small kernels in front of a product run with the SM's memory split as the product wants it: an SM does not

@@ -292,6 +292,27 @@ def test_no_rows_and_no_columns():
     no_device_error()
 
 
+def test_workspace_sizes_of_nothing():
+    for rows in (0, 5):
+        for n, k in ((0, 0), (0, 64), (64, 0)):
+            assert L.gemm_linear_workspace_size(3, rows, n, k) >= 0
+    assert L.gemm_linear_workspace_size(1, 0, 64, 64) == 0
+    empty = torch.empty((5, 0), device="cuda").half()
+    assert L.gemm_linear_nt(torch.randn(5, 64, device="cuda").half(), torch.empty((0, 64), device="cuda").half()).shape == (5, 0)
+    dz, db = L.gemm_linear_grad(empty, z=empty, act="gelu", bias_grad=True)
+    assert dz.shape == (5, 0) and db.shape == (0,)
+
+
+def test_as_many_groups_as_there_may_be():
+    rng = np.random.default_rng(21)
+    sizes = rng.integers(0, 3, 1024)
+    check_nt(sizes, 64, 72, torch.float16, "silu", True, seed=1, extra=5, head=3)
+    check_nn(sizes, 72, 64, torch.bfloat16, "gelu", True, seed=2, extra=5, head=3)
+    check_grad(sizes, 264, torch.float16, "gelu", True, seed=3, extra=5, head=3)
+    with pytest.raises(G.GemmError):
+        check_grad([1] * 1025, 8, torch.float16, "gelu", True, seed=4)
+
+
 def test_an_empty_contraction_is_refused():
     x, w = torch.empty((4, 0), device="cuda").half(), torch.empty((72, 0), device="cuda").half()
     with pytest.raises(G.GemmError):
