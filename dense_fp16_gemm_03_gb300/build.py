@@ -1,13 +1,17 @@
-"""Build the C-ABI shared library libgemm_f16.so in-tree (``_build/``).
+"""Build the C-ABI shared library libgemm_f16.so in-tree (``_build/``), and the
+Python binding gemm_binding.so that links to it.
 
 Three translation units compiled side by side (the dense product, the ragged
 products with the router, and the products with an epilogue), one ``-gencode`` (sm_103a), shared cudart;
-nvcc cross-compiles them on a machine without a GPU.
+nvcc cross-compiles them on a machine without a GPU.  The binding is host code
+against PyTorch's headers; without PyTorch there is none.
 """
 import glob
+import importlib.util
 import os
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -16,10 +20,13 @@ INCLUDE = os.path.join(ROOT, "include")
 OUT_DIR = os.path.join(PKG, "_build")
 LIB = os.path.join(OUT_DIR, "libgemm_f16.so")
 SOURCES = [os.path.join(CSRC, "gemm_api.cu"), os.path.join(CSRC, "ragged_api.cu"), os.path.join(CSRC, "linear_api.cu")]
+BINDING = os.path.join(OUT_DIR, "gemm_binding.so")
+BINDING_SOURCE = os.path.join(CSRC, "binding.cpp")
 DEPS = (SOURCES + sorted(glob.glob(os.path.join(CSRC, "*.cuh"))) + sorted(glob.glob(os.path.join(CSRC, "*.h")))
         + sorted(glob.glob(os.path.join(INCLUDE, "*.h"))))
 
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
+CXX = os.environ.get("CXX", "g++")
 FLAGS = [
     "-gencode", "arch=compute_103a,code=sm_103a",
     "-O3", "-lineinfo", "-std=c++17",
@@ -35,28 +42,73 @@ def _stale_lib(lib):
     return any(os.path.getmtime(f) > t for f in DEPS)
 
 
-def _compile(lib, extra):
+def _torch_dir():
+    """Where PyTorch is installed, without importing it; None where it is not."""
+    spec = importlib.util.find_spec("torch")
+    return spec.submodule_search_locations[0] if spec and spec.submodule_search_locations else None
+
+
+def _stale_binding():
+    headers = glob.glob(os.path.join(INCLUDE, "*.h"))
+    if not os.path.exists(BINDING):
+        return True
+    t = os.path.getmtime(BINDING)
+    return any(os.path.getmtime(f) > t for f in [BINDING_SOURCE, *headers])
+
+
+def _binding_command(torch, out):
+    """The compiler's command for the binding's object."""
+    cuda = os.path.join(os.path.dirname(os.path.dirname(NVCC)), "include")
+    return [CXX, "-O2", "-std=c++17", "-fPIC", "-I" + INCLUDE, "-I" + os.path.join(torch, "include"),
+            "-I" + sysconfig.get_paths()["include"], "-I" + cuda, "-c", "-o", out, BINDING_SOURCE]
+
+
+def _link_binding(torch, obj):
+    cuda = os.path.join(os.path.dirname(os.path.dirname(NVCC)), "lib64")
+    tmp = BINDING + ".tmp%d" % os.getpid()
+    subprocess.run([CXX, "-shared", "-o", tmp, obj, "-L" + OUT_DIR, "-lgemm_f16", "-Wl,-rpath,$ORIGIN", "-L" + os.path.join(torch, "lib"),
+                    "-ltorch_cpu", "-ltorch_python", "-lc10", "-lc10_cuda", "-L" + cuda, "-lcudart"], check=True)
+    os.replace(tmp, BINDING)
+
+
+def _compile(lib, extra, binding=None):
+    """The library, and with `binding` (PyTorch's folder) the binding beside it."""
     tmp = lib + ".tmp%d" % os.getpid()
     objects = ["%s.%d.o" % (tmp, i) for i in range(len(SOURCES))]
+    commands = [[NVCC, *FLAGS, *extra, "-c", "-o", o, src] for o, src in zip(objects, SOURCES)]
+    if binding:
+        objects.append(tmp + ".binding.o")
+        commands.append(_binding_command(binding, objects[-1]))
     try:
-        jobs = [subprocess.Popen([NVCC, *FLAGS, *extra, "-c", "-o", o, src]) for o, src in zip(objects, SOURCES)]
-        codes = [job.wait() for job in jobs]
-        if any(codes):
-            raise subprocess.CalledProcessError(next(c for c in codes if c), NVCC)
-        subprocess.run([NVCC, *FLAGS, "-shared", "-o", tmp, *objects], check=True)
+        jobs = [subprocess.Popen(c) for c in commands]
+        for job, command, code in zip(jobs, commands, [job.wait() for job in jobs]):
+            if code:
+                raise subprocess.CalledProcessError(code, command)
+        subprocess.run([NVCC, *FLAGS, "-shared", "-o", tmp, *objects[:len(SOURCES)]], check=True)
+        os.replace(tmp, lib)
+        if binding:
+            _link_binding(binding, objects[-1])
     finally:
         for o in objects:
             if os.path.exists(o):
                 os.remove(o)
-    os.replace(tmp, lib)
     return lib
 
 
 def build(force=False, verbose_ptxas=False):
     os.makedirs(OUT_DIR, exist_ok=True)
-    if not force and not _stale_lib(LIB):
-        return LIB
-    return _compile(LIB, ["-Xptxas", "-v"] if verbose_ptxas else [])
+    torch = _torch_dir()
+    if force or _stale_lib(LIB):
+        return _compile(LIB, ["-Xptxas", "-v"] if verbose_ptxas else [], binding=torch)
+    if torch and _stale_binding():
+        obj = BINDING + ".tmp%d.o" % os.getpid()
+        try:
+            subprocess.run(_binding_command(torch, obj), check=True)
+            _link_binding(torch, obj)
+        finally:
+            if os.path.exists(obj):
+                os.remove(obj)
+    return LIB
 
 
 # The measurement build with phase stamps in the single-CTA / CTA-pair kernel

@@ -1,8 +1,8 @@
 """ctypes binding of include/gemm_linear.h (same entry-point names): products
 with a bias, an activation and a residual in their epilogue, and their gradients.
 
-Argument marshalling only, as in ``ragged``, with its rules for operands, streams,
-outputs and workspaces.  ``w`` is one matrix [n, k], or with ``offsets`` one per
+Argument marshalling only (the calls' in csrc/binding.cpp), with the rules of
+``ragged`` for operands, streams, outputs and workspaces.  ``w`` is one matrix [n, k], or with ``offsets`` one per
 group of rows [groups, n, k], as the grouped products take them; bias and
 dbias then have a line per group.  ``act``: None or "none", "relu", "relu2",
 "gelu", "gelu_tanh" or "silu".
@@ -19,8 +19,9 @@ act=..., bias_grad=True) gives that layer's dz and dbias at once.
 """
 import ctypes
 
+from . import _binding
 from . import gemm as _gemm
-from .ragged import _check, _dtype, _need, _offsets, _operand, _out, _size, _stream, _workspace
+from .ragged import _dtype, _need, _offsets, _operand, _size, _stream, _workspace
 
 ACTS = {None: 0, "none": 0, "relu": 1, "relu2": 2, "gelu": 3, "gelu_tanh": 4, "silu": 5}
 
@@ -28,6 +29,18 @@ ACTS = {None: 0, "none": 0, "relu": 1, "relu2": 2, "gelu": 3, "gelu_tanh": 4, "s
 EXPORTED = ["gemm_linear_workspace_size", "gemm_linear_nt", "gemm_linear_nn", "gemm_linear_grad", "gemm_linear_stall_test"]
 
 _lib = None
+_native = None
+_checked = _binding.checked
+
+
+def _load():
+    global _native
+    _native = _binding.native()
+    return _native
+
+
+def _raw(stream):
+    return None if stream is None else _gemm._stream(stream)
 
 
 def lib():
@@ -94,31 +107,8 @@ def gemm_linear_nt(x, w, bias=None, residual=None, act=None, offsets=None, keep=
 
     x [rows, k], w [n, k], bias [n], residual [rows, n] (y may be the residual itself); with offsets [groups + 1] int32 on the
     device w [groups, n, k], bias [groups, n], and rows of no group are zero."""
-    if _lib is None:
-        lib()
-    code = _act(act)
-    dev, kind = _operand(x, "x", 2), x.dtype
-    groups, ends, stack = _groups(offsets, dev)
-    rows, k = x.shape
-    n, _ = _weights(w, stack)
-    dtype = _dtype(kind)
-    wp = _at(w, "w", (*stack, n, k), kind, dev)
-    b = _at(bias, "bias", (*stack, n), kind, dev)
-    shape = (rows, n)
-    r = _at(residual, "residual", shape, kind, dev)
-    zp = None
-    if keep:
-        z = _out(z, "z", shape, kind, dev)
-        zp = z.data_ptr()
-    elif z is not None:
-        raise ValueError("z is written with keep only")
-    y = _out(y, "y", shape, kind, dev)
-    ws, ws_bytes = _workspace(workspace, dev)
-    st = _lib.gemm_linear_nt(dtype, code, groups, rows, n, k, ends, x.data_ptr(), wp, b, r, zp, y.data_ptr(), ws, ws_bytes,
-                             _stream(stream, dev))
-    if st:
-        _check(st, "gemm_linear_nt")
-    return (y, z) if keep else y
+    r = (_native or _load()).linear_nt(x, w, bias, residual, _act(act), offsets, keep, y, z, workspace, _raw(stream))
+    return _checked(r, "gemm_linear_nt")
 
 
 def gemm_linear_nn(dy, w, z=None, act=None, offsets=None, bias_grad=False, dx=None, dbias=None, workspace=None, stream=None):
@@ -126,64 +116,16 @@ def gemm_linear_nn(dy, w, z=None, act=None, offsets=None, bias_grad=False, dx=No
     over the rows (of each group) in float32.
 
     dy [rows, n], w [n, k] or [groups, n, k], z [rows, k] (not needed without `act`; dx may be z itself)."""
-    if _lib is None:
-        lib()
-    code = _act(act)
-    dev, kind = _operand(dy, "dy", 2), dy.dtype
-    groups, ends, stack = _groups(offsets, dev)
-    rows, n = dy.shape
-    _, k = _weights(w, stack)
-    dtype = _dtype(kind)
-    wp = _at(w, "w", (*stack, n, k), kind, dev)
-    if code and z is None:
-        raise ValueError("z is needed for act=%r" % (act,))
-    shape = (rows, k)
-    at = _at(z, "z", shape, kind, dev)
-    dx = _out(dx, "dx", shape, kind, dev)
-    db = None
-    if bias_grad:
-        dbias = _out(dbias, "dbias", (*stack, k), _gemm._tm().float32, dev)
-        db = dbias.data_ptr()
-    elif dbias is not None:
-        raise ValueError("dbias is written with bias_grad only")
-    ws, ws_bytes = _workspace(workspace, dev)
-    st = _lib.gemm_linear_nn(dtype, code, groups, rows, n, k, ends, dy.data_ptr(), wp, at, dx.data_ptr(), db, ws, ws_bytes,
-                             _stream(stream, dev))
-    if st:
-        _check(st, "gemm_linear_nn")
-    return (dx, dbias) if bias_grad else dx
+    r = (_native or _load()).linear_nn(dy, w, z, _act(act), offsets, bias_grad, dx, dbias, workspace, _raw(stream))
+    return _checked(r, "gemm_linear_nn")
 
 
 def gemm_linear_grad(dy, z=None, act=None, offsets=None, bias_grad=False, dz=None, dbias=None, workspace=None, stream=None):
     """dz = dy * f'(z); with `bias_grad` (dz, dbias), dbias the sum of dz over the rows (of each group) in float32.
 
     dy, z [rows, n]; dz may be dy or z.  Without `act` dz is dy, which is returned as it is unless another dz is given."""
-    if _lib is None:
-        lib()
-    code = _act(act)
-    dev, kind = _operand(dy, "dy", 2), dy.dtype
-    groups, ends, stack = _groups(offsets, dev)
-    rows, n = dy.shape
-    dtype = _dtype(kind)
-    if code and z is None:
-        raise ValueError("z is needed for act=%r" % (act,))
-    at = _at(z, "z", dy.shape, kind, dev)
-    if code or dz is not None:
-        dz = _out(dz, "dz", (rows, n), kind, dev)
-        to = dz.data_ptr()
-    else:
-        dz, to = dy, None
-    db = None
-    if bias_grad:
-        dbias = _out(dbias, "dbias", (*stack, n), _gemm._tm().float32, dev)
-        db = dbias.data_ptr()
-    elif dbias is not None:
-        raise ValueError("dbias is written with bias_grad only")
-    ws, ws_bytes = _workspace(workspace, dev)
-    st = _lib.gemm_linear_grad(dtype, code, groups, rows, n, ends, dy.data_ptr(), at, to, db, ws, ws_bytes, _stream(stream, dev))
-    if st:
-        _check(st, "gemm_linear_grad")
-    return (dz, dbias) if bias_grad else dz
+    r = (_native or _load()).linear_grad(dy, z, _act(act), offsets, bias_grad, dz, dbias, workspace, _raw(stream))
+    return _checked(r, "gemm_linear_grad")
 
 
 def gemm_linear_stall_test(mode, first, w, extra, out, dbias, workspace, skip_fill, wait_limit_cycles, act=None, offsets=None, stream=None):

@@ -2,7 +2,8 @@
 products by expert with their gradients, low-rank adapters beside a shared
 projection, and the experts' router.
 
-Argument marshalling only, as in ``gemm``: every step runs in the CUDA library,
+Argument marshalling only, as in ``gemm`` (that of the router with scores in
+csrc/binding.cpp): every step runs in the CUDA library,
 a missing library raises, and there is no fallback.  Operands are contiguous
 CUDA tensors; a call runs on ``stream`` (a torch.cuda.Stream, a raw integer, or
 None for the current torch stream).  Outputs that are not given are allocated
@@ -12,6 +13,7 @@ on the current torch stream; workspaces are the caller's (sizes from the
 import collections
 import ctypes
 
+from . import _binding
 from . import gemm as _gemm
 from .gemm import GemmError, gemm_f16_take_device_error  # noqa: F401  (the same errors, the same device word)
 
@@ -370,45 +372,15 @@ def gemm_route_scored(logits, top, score="sigmoid", bias=None, groups=1, top_gro
     `groups` (1, 2, 4 ... 32) groups of neighbours; the `top_groups` (None: all) with the largest score are kept, a group's
     score being its largest s + bias (group_top 1) or the sum of its two largest (2).  The weights are scale * s at ids,
     divided by their sum if `renorm`.  `out` and the workspace as in gemm_route_topk."""
-    code = _score(score)
-    dev = _operand(logits, "logits", 2)
-    rows, experts = logits.shape
-    kind = _dtype(logits.dtype, f32=True)
-    top, groups = int(top), int(groups)
-    top_groups = groups if top_groups is None else int(top_groups)
-    if top < 1 or top > experts:
-        raise ValueError("top must be in [1, experts]")
-    if groups < 1 or experts % groups or not 1 <= top_groups <= groups:
-        raise ValueError("groups must divide the experts, and top_groups be in [1, groups]")
-    if top > top_groups * (experts // groups):
-        raise ValueError("the groups kept hold fewer than `top` experts")
-    if group_top not in (1, 2):
-        raise ValueError("group_top must be 1 or 2")
-    if bias is not None:
-        _need(bias, "bias", (experts,), _gemm._tm().float32, dev)
-    r = _routing(out, rows, experts, top, dev)
-    ws, ws_bytes = _workspace(workspace, dev)
-    st = lib().gemm_route_scored(kind, code, rows, experts, top, groups, top_groups, group_top, 1 if renorm else 0, scale,
-                                 logits.data_ptr(), None if bias is None else bias.data_ptr(), r.ids.data_ptr(), r.weights.data_ptr(),
-                                 r.offsets.data_ptr(), r.order.data_ptr(), r.position.data_ptr(), ws, ws_bytes, _stream(stream, dev))
-    _check(st, "gemm_route_scored")
-    return r
+    groups = int(groups)
+    r = _binding.native().route_scored(logits, int(top), _score(score), bias, groups, groups if top_groups is None else int(top_groups), group_top,
+                               renorm, scale, out, workspace, None if stream is None else _gemm._stream(stream))
+    _binding.checked(r, "gemm_route_scored")
+    return Routing._make(r) if out is None else out
 
 
 def gemm_route_scored_grad(logits, ids, dweights, score="sigmoid", renorm=True, scale=1.0, dlogits=None, stream=None):
     """The gradient of the logits [rows, experts] float32 from that of gemm_route_scored's weights."""
-    torch = _gemm._tm()
-    code = _score(score)
-    dev = _operand(logits, "logits", 2)
-    rows, experts = logits.shape
-    kind = _dtype(logits.dtype, f32=True)
-    if ids.dim() != 2:
-        raise ValueError("ids must be [rows, top]")
-    shape = ids.shape
-    _need(ids, "ids", (rows, shape[1]), torch.int32, dev)
-    _need(dweights, "dweights", shape, torch.float32, dev)
-    dlogits = _out(dlogits, "dlogits", (rows, experts), torch.float32, dev)
-    st = lib().gemm_route_scored_grad(kind, code, rows, experts, shape[1], 1 if renorm else 0, scale, logits.data_ptr(), ids.data_ptr(),
-                                      dweights.data_ptr(), dlogits.data_ptr(), _stream(stream, dev))
-    _check(st, "gemm_route_scored_grad")
-    return dlogits
+    r = _binding.native().route_scored_grad(logits, ids, dweights, _score(score), renorm, scale, dlogits,
+                                    None if stream is None else _gemm._stream(stream))
+    return _binding.checked(r, "gemm_route_scored_grad")
