@@ -50,9 +50,9 @@ const void *const kBeside[] = {
 };
 
 // The router's instances for few and for many rows, with a warp's lists.
-#define ROUTE_SCORED_LARGE(V)                                                                                                       \
-    {reinterpret_cast<const void *>(&route_scored_kernel<V, kRouteThreads>), kRouteThreads / 32 * int(kRouteListBytes<V>)},         \
-        {reinterpret_cast<const void *>(&route_scored_kernel<V, 16 * kRouteRows>), kRouteRows / 2 * int(kRouteListBytes<V>)}
+#define ROUTE_SCORED_LARGE(V)                                                                                      \
+    {reinterpret_cast<const void *>(&route_scored_few_kernel<V>), kRouteFewPer * int(kRouteListBytes<V>)},         \
+        {reinterpret_cast<const void *>(&route_scored_kernel<V>), kRouteRows / 2 * int(kRouteListBytes<V>)}
 
 const KernelSmem kLarge[] = {ROUTE_SCORED_LARGE(1), ROUTE_SCORED_LARGE(2),  ROUTE_SCORED_LARGE(4),
                              ROUTE_SCORED_LARGE(8), ROUTE_SCORED_LARGE(16), ROUTE_SCORED_LARGE(32)};
@@ -773,7 +773,7 @@ static gemm_status_t route_launch(const void *fn, RouteParams &p, void *own, int
     p.direct = p.blocks <= uint32_t(kRouteDirectBlocks) ||
                (p.blocks <= uint32_t(kRouteDirectMost) && p.blocks * p.experts <= uint32_t(kRouteDirectCounts));
     void *args[1] = {own}, *base[1] = {&p};
-    if (p.blocks == 1u) return launch(fn, dim3(1, 1, 1), kRouteThreads, kRouteThreads / 32 * warp_smem, 1, args, s);
+    if (p.blocks == 1u) return launch(fn, dim3(1, 1, 1), kRouteThreads, 0, 1, args, s);
     gemm_status_t st = launch(fn, dim3(p.blocks, 1, 1), 16 * kRouteRows, kRouteRows / 2 * warp_smem, 1, args, s);
     if (st == GEMM_OK && !p.direct)
         st = launch(reinterpret_cast<const void *>(&route_scan_kernel), dim3(unsigned(cdiv(p.experts, 32)), 1, 1), 1024, 0, 1, base, s);
@@ -830,8 +830,8 @@ gemm_status_t gemm_route_topk_grad(gemm_dtype_t dtype, int64_t rows, int64_t exp
 
 // ---------------------------------------------------- router with scores
 
-#define ROUTE_SCORED_FEW(V) reinterpret_cast<const void *>(&route_scored_kernel<V, kRouteThreads>)
-#define ROUTE_SCORED(V) reinterpret_cast<const void *>(&route_scored_kernel<V, 16 * kRouteRows>)
+#define ROUTE_SCORED_FEW(V) reinterpret_cast<const void *>(&route_scored_few_kernel<V>)
+#define ROUTE_SCORED(V) reinterpret_cast<const void *>(&route_scored_kernel<V>)
 #define ROUTE_LIST(V) kRouteListBytes<V>
 #define ROUTE_SCORED_GRAD(V) reinterpret_cast<const void *>(&route_scored_grad_kernel<V>)
 
@@ -868,9 +868,12 @@ gemm_status_t gemm_route_scored(gemm_dtype_t dtype, gemm_route_score_t score, in
     p.scale = scale;
     const int64_t lanes = int64_t(p.run) * 32;  // the instance whose lanes hold a run
     const bool one = p.blocks == 1u;
-    const void *fn = one ? ROUTE_INSTANCE(ROUTE_SCORED_FEW, lanes) : ROUTE_INSTANCE(ROUTE_SCORED, lanes);
     const int warp_smem = int(ROUTE_INSTANCE(ROUTE_LIST, lanes));
-    return route_launch(fn, p, &p, warp_smem, s);
+    if (!one) return route_launch(ROUTE_INSTANCE(ROUTE_SCORED, lanes), p, &p, warp_smem, s);
+    int ctas = 1;  // (a power of two)
+    while (ctas * kRouteFewPer < rows) ctas *= 2;
+    void *args[1] = {&p};
+    return launch(ROUTE_INSTANCE(ROUTE_SCORED_FEW, lanes), dim3(unsigned(ctas), 1, 1), kRouteFewThreads, kRouteFewPer * warp_smem, ctas, args, s);
 }
 
 gemm_status_t gemm_route_scored_grad(gemm_dtype_t dtype, gemm_route_score_t score, int64_t rows, int64_t experts, int64_t top,

@@ -567,17 +567,40 @@ __device__ __forceinline__ int32_t route_choose(const RouteScoredParams &p, size
     return lane < p.top ? id : -1;
 }
 
-template <int VPT, int THREADS>
-__global__ void __launch_bounds__(THREADS, VPT <= 8 ? 1024 / THREADS : 1)
-    route_scored_kernel(const __grid_constant__ RouteScoredParams p)
+// The choice of one row and its weights, stored.  Returns the id of choice `lane`.
+template <int VPT>
+__device__ __forceinline__ int32_t route_row(const RouteScoredParams &p, uint32_t row, const RouteLane &at, const RouteBias<VPT> &bias,
+                                             uint32_t *keep, uint2 *pick)
 {
-    constexpr uint32_t kWarps = THREADS / 32;
+    const uint32_t lane = threadIdx.x & 31u;
+    RouteRow r;
+    const int32_t id = route_choose<VPT>(p, row, at, bias, keep, pick, &r);
+    const float l = id >= 0 ? route_logit(p, size_t(row) * p.experts + id) : -INFINITY;
+    float w = 0.0f, over = p.sigmoid ? 1.0f : r.sum;
+    const float from = p.renorm ? route_top(l) : p.sigmoid ? 0.0f : r.most;
+    if (id >= 0) w = p.sigmoid ? route_sigmoid(l, fminf(from, 0.0f)) : r.bad ? __uint_as_float(0x7FC00000u) : act::ex2((l - from) * act::kLog2e);
+    if (p.renorm) over = warp_sum(w);
+    w *= p.scale * act::rcp(over);
+    if (lane < p.top) {
+        p.ids[size_t(row) * p.top + lane] = id;
+        p.weights[size_t(row) * p.top + lane] = id >= 0 ? w : 0.0f;
+    }
+    __syncwarp();  // (the picks are read)
+    return id;
+}
+
+// Many rows: 32 to a block.
+template <int VPT>
+__global__ void __launch_bounds__(16 * kRouteRows, VPT <= 8 ? 2 : 1) route_scored_kernel(const __grid_constant__ RouteScoredParams p)
+{
+    constexpr int kThreads = 16 * kRouteRows;
+    constexpr uint32_t kWarps = kThreads / 32;
     __shared__ uint32_t s_mask[2][kRouteMaxExperts];  // bit w: the block's row w, kWarps + w
     __shared__ int32_t s_base[kRouteMaxExperts];
     __shared__ int32_t s_scan[32];
     extern __shared__ __align__(8) uint8_t s_lists[];  // for each warp its picks (256 bytes) and keys (128 VPT)
-    const uint32_t lane = threadIdx.x & 31u, warp = threadIdx.x >> 5;
-    for (uint32_t e = threadIdx.x; e < p.experts; e += THREADS) s_mask[0][e] = s_mask[1][e] = 0u;
+    const uint32_t warp = threadIdx.x >> 5;
+    for (uint32_t e = threadIdx.x; e < p.experts; e += kThreads) s_mask[0][e] = s_mask[1][e] = 0u;
     __syncthreads();
     ptx::griddep_wait();
 
@@ -591,27 +614,97 @@ __global__ void __launch_bounds__(THREADS, VPT <= 8 ? 1024 / THREADS : 1)
     for (uint32_t q = 0; q < 2u; ++q) {
         const uint32_t row = row0 + warp + q * kWarps;
         if (row >= p.rows) break;  // (a whole warp)
-        RouteRow r;
-        const int32_t id = route_choose<VPT>(p, row, at, bias, keep, pick, &r);
-        // weights, from the chosen logits
-        const float l = id >= 0 ? route_logit(p, size_t(row) * p.experts + id) : -INFINITY;
-        float w = 0.0f, over = p.sigmoid ? 1.0f : r.sum;
-        const float from = p.renorm ? route_top(l) : p.sigmoid ? 0.0f : r.most;
-        if (id >= 0) w = p.sigmoid ? route_sigmoid(l, fminf(from, 0.0f)) : r.bad ? __uint_as_float(0x7FC00000u) : act::ex2((l - from) * act::kLog2e);
-        if (p.renorm) over = warp_sum(w);
-        w *= p.scale * act::rcp(over);
-        if (lane < p.top) {
-            p.ids[size_t(row) * p.top + lane] = id;
-            p.weights[size_t(row) * p.top + lane] = id >= 0 ? w : 0.0f;
-            if (id >= 0) atomicOr(&s_mask[q][id], 1u << warp);
-        }
-        __syncwarp();  // (the picks are read)
+        const int32_t id = route_row<VPT>(p, row, at, bias, keep, pick);
+        if (id >= 0) atomicOr(&s_mask[q][id], 1u << warp);
         if (q == 0u) id0 = id;
         else id1 = id;
     }
     const int32_t id[2] = {id0, id1};
-    route_rank<THREADS>(p, row0, id, s_mask, s_base, s_scan);
+    route_rank<kThreads>(p, row0, id, s_mask, s_base, s_scan);
     ptx::griddep_launch_dependents();
+}
+
+// Few rows: a cluster of CTAs, each with a row for each of its warps, that read one another's masks and so all know the
+// counts.  (64 rows of 256 experts on one SM took 12.4 us, of 1024 72.6.)
+constexpr int kRouteFewThreads = 256;
+constexpr int kRouteFewPer = kRouteFewThreads / 32;  // rows of a CTA
+constexpr int kRouteFewCtas = kRouteFewRows / kRouteFewPer;
+static_assert(kRouteFewCtas <= 8, "a portable cluster");
+
+template <int VPT>
+__global__ void __launch_bounds__(kRouteFewThreads) route_scored_few_kernel(const __grid_constant__ RouteScoredParams p)
+{
+    constexpr uint32_t kMost = kRouteMaxExperts / kRouteFewThreads;  // experts of a thread, at most
+    __shared__ uint32_t s_mask[kRouteMaxExperts];  // bit w: the CTA's row w
+    __shared__ int32_t s_base[kRouteMaxExperts];
+    __shared__ int32_t s_scan[kRouteFewPer];
+    extern __shared__ __align__(8) uint8_t s_lists[];  // as above
+    const uint32_t lane = threadIdx.x & 31u, warp = threadIdx.x >> 5, cta = blockIdx.x, ctas = gridDim.x;  // (one cluster)
+    for (uint32_t e = threadIdx.x; e < p.experts; e += kRouteFewThreads) s_mask[e] = 0u;
+    __syncthreads();
+    ptx::griddep_wait();
+
+    const uint32_t row = cta * kRouteFewPer + warp;
+    int32_t id = -1;
+    if (row < p.rows) {
+        const RouteLane at(p);
+        const RouteBias<VPT> bias(p, at);
+        uint2 *pick = reinterpret_cast<uint2 *>(s_lists + warp * kRouteListBytes<VPT>);
+        id = route_row<VPT>(p, row, at, bias, reinterpret_cast<uint32_t *>(pick + 32), pick);
+        if (id >= 0) atomicOr(&s_mask[id], 1u << warp);
+    }
+    if (ctas > 1u) ptx::cluster_sync();
+    else __syncthreads();
+    // a thread's experts are neighbours: the rows of all CTAs that chose them, and those of the CTAs before this one
+    const uint32_t per = (p.experts + kRouteFewThreads - 1u) / kRouteFewThreads, first = threadIdx.x * per;
+    int32_t count[kMost], before[kMost], sum = 0;
+#pragma unroll
+    for (uint32_t i = 0; i < kMost; ++i) {
+        count[i] = before[i] = 0;
+        if (i >= per || first + i >= p.experts) continue;
+        const uint32_t mine = ptx::smem_addr(&s_mask[first + i]);
+        for (uint32_t c = 0; c < ctas; ++c) {
+            const int32_t n = __popc(c == cta ? s_mask[first + i] : ptx::ld_shared_cluster_u32(ptx::map_to_rank(mine, c)));
+            count[i] += n;
+            before[i] += c < cta ? n : 0;
+        }
+        sum += count[i];
+    }
+    int32_t x = sum;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const int32_t o = __shfl_up_sync(0xffffffffu, x, d);
+        if (lane >= uint32_t(d)) x += o;
+    }
+    if (lane == 31u) s_scan[warp] = x;
+    __syncthreads();
+    int32_t start = x - sum, total = 0;
+#pragma unroll
+    for (uint32_t w = 0; w < uint32_t(kRouteFewPer); ++w) {
+        if (w < warp) start += s_scan[w];
+        total += s_scan[w];
+    }
+#pragma unroll
+    for (uint32_t i = 0; i < kMost; ++i) {
+        if (i >= per || first + i >= p.experts) continue;
+        s_base[first + i] = start + before[i];
+        if (cta == 0u) p.offsets[first + i] = start;
+        start += count[i];
+    }
+    if (cta == 0u && threadIdx.x == 0u) p.offsets[p.experts] = total;
+    for (uint32_t i = uint32_t(total) + cta * kRouteFewThreads + threadIdx.x; i < p.rows * p.top; i += ctas * kRouteFewThreads) p.order[i] = -1;
+    __syncthreads();
+    if (row < p.rows && lane < p.top) {
+        const uint32_t flat = row * p.top + lane;
+        int32_t at = -1;
+        if (id >= 0) {
+            at = s_base[id] + __popc(s_mask[id] & ((1u << warp) - 1u));
+            p.order[at] = int32_t(flat);
+        }
+        p.position[flat] = at;
+    }
+    ptx::griddep_launch_dependents();
+    if (ctas > 1u) ptx::cluster_sync();  // (the masks are read)
 }
 
 // A row's logits as the gradient's kernel takes them: four neighbours to a lane, or (fours false) `lane`, 32 + lane, ...

@@ -117,7 +117,7 @@ FORMS = [  # experts, groups, top_groups, top
 
 @pytest.mark.parametrize("score", ["sigmoid", "softmax"])
 @pytest.mark.parametrize("kind", sorted(TYPES))
-@pytest.mark.parametrize("rows", [1, 64, 65])
+@pytest.mark.parametrize("rows", [1, 9, 30, 64, 65])
 @pytest.mark.parametrize("experts,groups,top_groups,top", FORMS)
 def test_choice(experts, groups, top_groups, top, rows, kind, score):
     z = draw(rows, experts, kind, rows + experts)
