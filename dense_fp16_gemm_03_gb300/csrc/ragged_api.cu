@@ -770,15 +770,19 @@ static gemm_status_t route_begin(RouteParams *p, gemm_dtype_t dtype, int64_t row
 // The choice by kernel `fn` with its parameters `own` and `warp_smem` bytes a warp, then the places of all choices.
 static gemm_status_t route_launch(const void *fn, RouteParams &p, void *own, int warp_smem, cudaStream_t s)
 {
-    p.direct = p.blocks <= uint32_t(kRouteDirectBlocks) ||
-               (p.blocks <= uint32_t(kRouteDirectMost) && p.blocks * p.experts <= uint32_t(kRouteDirectCounts));
+    const bool direct = p.blocks <= uint32_t(kRouteDirectBlocks) ||
+                        (p.blocks <= uint32_t(kRouteDirectMost) && p.blocks * p.experts <= uint32_t(kRouteDirectCounts));
     void *args[1] = {own}, *base[1] = {&p};
     if (p.blocks == 1u) return launch(fn, dim3(1, 1, 1), kRouteThreads, 0, 1, args, s);
     gemm_status_t st = launch(fn, dim3(p.blocks, 1, 1), 16 * kRouteRows, kRouteRows / 2 * warp_smem, 1, args, s);
-    if (st == GEMM_OK && !p.direct)
-        st = launch(reinterpret_cast<const void *>(&route_scan_kernel), dim3(unsigned(cdiv(p.experts, 32)), 1, 1), 1024, 0, 1, base, s);
     if (st != GEMM_OK) return st;
-    return launch(reinterpret_cast<const void *>(&route_place_kernel), dim3(p.blocks, 1, 1), kRouteThreads, 0, 1, base, s);
+    if (direct) return launch(reinterpret_cast<const void *>(&route_place_kernel), dim3(p.blocks, 1, 1), kRouteThreads, 0, 1, base, s);
+    const void *scan = p.blocks <= 32u * 4u    ? reinterpret_cast<const void *>(&route_scan_kernel<4>)
+                       : p.blocks <= 32u * 16u ? reinterpret_cast<const void *>(&route_scan_kernel<16>)
+                                               : reinterpret_cast<const void *>(&route_scan_kernel<0>);
+    st = launch(scan, dim3(unsigned(cdiv(p.experts, 32)), 1, 1), 1024, 0, 1, base, s);
+    if (st != GEMM_OK) return st;
+    return launch(reinterpret_cast<const void *>(&route_place_scanned_kernel), dim3(p.blocks, 1, 1), kRoutePlaceThreads, 0, 1, base, s);
 }
 
 gemm_status_t gemm_route_topk(gemm_dtype_t dtype, int64_t rows, int64_t experts, int64_t top, int32_t renorm, const void *logits,

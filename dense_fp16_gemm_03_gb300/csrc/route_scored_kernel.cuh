@@ -285,23 +285,48 @@ __device__ __forceinline__ void route_sort(uint32_t (&key)[N])
                     }
 }
 
-// What the choice needs of the biases: a lane's own, and how large the finite ones are.
-template <int VPT>
+// What the choice needs to know of the biases: how large the finite ones are, and whether this lane's others are -infinity or
+// worse.  (The biases themselves are read again for each row: in registers they would cost more than they spare.)
 struct RouteBias {
-    float of[VPT], widest;
+    float widest;
     bool plain, masks;  // none is +infinity or NaN; one is -infinity (this lane's)
     __device__ __forceinline__ RouteBias(const RouteScoredParams &p, const RouteLane &at) : widest(0.0f), plain(true), masks(false)
     {
-#pragma unroll
-        for (int i = 0; i < VPT; ++i) {
-            of[i] = (p.bias && uint32_t(i) < at.count) ? p.bias[at.first + i] : 0.0f;
-            if (fabsf(of[i]) < INFINITY) widest = fmaxf(widest, fabsf(of[i]));
-            plain = plain && of[i] < INFINITY;
-            masks = masks || of[i] == -INFINITY;
-        }
+        if (p.bias)
+            for (uint32_t i = 0; i < at.count; ++i) {
+                const float b = p.bias[at.first + i];
+                if (fabsf(b) < INFINITY) widest = fmaxf(widest, fabsf(b));
+                plain = plain && b < INFINITY;
+                masks = masks || b == -INFINITY;
+            }
         widest = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(widest)));
     }
 };
+
+// A lane's biases (0 without), as route_load_run has its logits.
+template <int VPT>
+__device__ __forceinline__ void route_load_bias(const RouteScoredParams &p, const RouteLane &at, bool full, float (&b)[VPT])
+{
+    if (p.bias == nullptr) {
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) b[i] = 0.0f;
+        return;
+    }
+    const float *from = p.bias + at.first;
+    if (VPT >= 4 && full && (reinterpret_cast<uintptr_t>(p.bias) & 15u) == 0u) {
+#pragma unroll
+        for (int i = 0; i < VPT / 4; ++i) {
+            const float4 v = reinterpret_cast<const float4 *>(from)[i];
+            b[(4 * i) % VPT] = v.x;
+            b[(4 * i + 1) % VPT] = v.y;
+            b[(4 * i + 2) % VPT] = v.z;
+            b[(4 * i + 3) % VPT] = v.w;
+        }
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) b[i] = uint32_t(i) < at.count ? from[i] : 0.0f;
+}
 
 // What a row's weights need besides the chosen logits.
 struct RouteRow {
@@ -390,7 +415,7 @@ __device__ __noinline__ int32_t route_order64(const RouteScoredParams &p, size_t
 // The choice of one row: the id of choice `lane`, or -1.  `keep`: a lane's keys but the first, one behind another at a step
 // of 32 words, `pick`: 32 pairs of words, both the warp's own.
 template <int VPT>
-__device__ __forceinline__ int32_t route_choose(const RouteScoredParams &p, size_t row, const RouteLane &at, const RouteBias<VPT> &bias,
+__device__ __forceinline__ int32_t route_choose(const RouteScoredParams &p, size_t row, const RouteLane &at, const RouteBias &bias,
                                                 uint32_t *keep, uint2 *pick, RouteRow *r)
 {
     using Key = RouteKey<VPT>;
@@ -439,9 +464,11 @@ __device__ __forceinline__ int32_t route_choose(const RouteScoredParams &p, size
                 const float over = act::rcp(sum);
                 tol = (132.0f * over + 4.0f * bias.widest) * 0x1p-24f + (over + bias.widest) * float(Key::kMask + 1u) * 0x1p-23f;
                 if (!p.by_logit) {
+                    float b[VPT];
+                    route_load_bias<VPT>(p, at, full, b);
 #pragma unroll
                     for (int i = 0; i < VPT; ++i)  // (-infinity stays what it is)
-                        f[i] = whole || f[i] != -INFINITY ? fmaf(c[i], over, bias.of[i]) : f[i];
+                        f[i] = whole || f[i] != -INFINITY ? fmaf(c[i], over, b[i]) : f[i];
                 }
             }
             if (bad) {
@@ -450,8 +477,10 @@ __device__ __forceinline__ int32_t route_choose(const RouteScoredParams &p, size
                     if (f[i] != -INFINITY) f[i] = __uint_as_float(0x7FC00000u);
             }
         } else if (!p.by_logit) {
+            float b[VPT];
+            route_load_bias<VPT>(p, at, full, b);
 #pragma unroll
-            for (int i = 0; i < VPT; ++i) f[i] = whole || f[i] != -INFINITY ? act::sigmoid(f[i]) + bias.of[i] : f[i];
+            for (int i = 0; i < VPT; ++i) f[i] = whole || f[i] != -INFINITY ? act::sigmoid(f[i]) + b[i] : f[i];
         }
         if (whole) {
 #pragma unroll
@@ -569,7 +598,7 @@ __device__ __forceinline__ int32_t route_choose(const RouteScoredParams &p, size
 
 // The choice of one row and its weights, stored.  Returns the id of choice `lane`.
 template <int VPT>
-__device__ __forceinline__ int32_t route_row(const RouteScoredParams &p, uint32_t row, const RouteLane &at, const RouteBias<VPT> &bias,
+__device__ __forceinline__ int32_t route_row(const RouteScoredParams &p, uint32_t row, const RouteLane &at, const RouteBias &bias,
                                              uint32_t *keep, uint2 *pick)
 {
     const uint32_t lane = threadIdx.x & 31u;
@@ -606,7 +635,7 @@ __global__ void __launch_bounds__(16 * kRouteRows, VPT <= 8 ? 2 : 1) route_score
 
     const RouteLane at(p);
     const uint32_t row0 = blockIdx.x * (2u * kWarps);
-    const RouteBias<VPT> bias(p, at);
+    const RouteBias bias(p, at);
     uint2 *pick = reinterpret_cast<uint2 *>(s_lists + warp * kRouteListBytes<VPT>);
     uint32_t *keep = reinterpret_cast<uint32_t *>(pick + 32);
     int32_t id0 = -1, id1 = -1;
@@ -648,7 +677,7 @@ __global__ void __launch_bounds__(kRouteFewThreads) route_scored_few_kernel(cons
     int32_t id = -1;
     if (row < p.rows) {
         const RouteLane at(p);
-        const RouteBias<VPT> bias(p, at);
+        const RouteBias bias(p, at);
         uint2 *pick = reinterpret_cast<uint2 *>(s_lists + warp * kRouteListBytes<VPT>);
         id = route_row<VPT>(p, row, at, bias, reinterpret_cast<uint32_t *>(pick + 32), pick);
         if (id >= 0) atomicOr(&s_mask[id], 1u << warp);
