@@ -99,6 +99,16 @@ at::Tensor output(PyObject *o, const char *what, c10::IntArrayRef shape, at::Sca
     return at::empty(shape, at::TensorOptions().dtype(type).device(c10::Device(c10::kCUDA, static_cast<c10::DeviceIndex>(dev))));
 }
 
+// A tensor of 32-bit elements in another one's memory, which it keeps: one allocation for several small outputs (0.8 us each,
+// views by torch's own functions as much).
+at::Tensor cut(const at::Tensor &base, int64_t first, c10::IntArrayRef shape, at::ScalarType type)
+{
+    auto impl = c10::make_intrusive<c10::TensorImpl>(c10::Storage(base.storage()), base.key_set(), c10::scalarTypeToTypeMeta(type));
+    impl->set_sizes_contiguous(shape);
+    impl->set_storage_offset(first);
+    return at::Tensor(std::move(impl));
+}
+
 struct Space {
     void *at = nullptr;
     size_t bytes = 0;
@@ -329,15 +339,28 @@ PyObject *route_scored(PyObject *, PyObject *const *a, Py_ssize_t count)
         const void *bias = optional(a[3], "bias", each, at::kFloat, dev);
         const bool given = a[9] != Py_None;
         if (given && (!PyTuple_Check(a[9]) || PyTuple_GET_SIZE(a[9]) != 5)) throw Wrong("out must be a Routing");
-        auto to = [&](Py_ssize_t i) { return given ? PyTuple_GET_ITEM(a[9], i) : Py_None; };
+        auto to = [&](Py_ssize_t i) { return PyTuple_GET_ITEM(a[9], i); };
         const Space ws(a[10], dev);
         const gemm_stream_t stream = stream_of(a[11], dev);
         const bool renorm = truth(a[7]);
         const float scale = real(a[8]);
         const gemm_route_score_t score = static_cast<gemm_route_score_t>(number(a[2]));
-        const at::Tensor ids = output(to(0), "ids", chosen, at::kInt, dev), weights = output(to(1), "weights", chosen, at::kFloat, dev),
-                         offsets = output(to(2), "offsets", ends, at::kInt, dev), order = output(to(3), "order", flat, at::kInt, dev),
-                         position = output(to(4), "position", chosen, at::kInt, dev);
+        at::Tensor ids, weights, offsets, order, position;
+        if (given) {
+            ids = output(to(0), "ids", chosen, at::kInt, dev);
+            weights = output(to(1), "weights", chosen, at::kFloat, dev);
+            offsets = output(to(2), "offsets", ends, at::kInt, dev);
+            order = output(to(3), "order", flat, at::kInt, dev);
+            position = output(to(4), "position", chosen, at::kInt, dev);
+        } else {
+            const int64_t part = (rows * top + 3) / 4 * 4, all[1] = {4 * part + experts + 1};  // (parts of whole 16 bytes)
+            const at::Tensor base = output(Py_None, "", all, at::kInt, dev);
+            ids = cut(base, 0, chosen, at::kInt);
+            weights = cut(base, part, chosen, at::kFloat);
+            order = cut(base, 2 * part, flat, at::kInt);
+            position = cut(base, 3 * part, chosen, at::kInt);
+            offsets = cut(base, 4 * part, ends, at::kInt);
+        }
         auto i32 = [](const at::Tensor &t) { return static_cast<int32_t *>(t.data_ptr()); };
         const gemm_status_t st = gemm_route_scored(kind, score, rows, experts, top, groups, top_groups, int32_t(group_top), renorm ? 1 : 0, scale,
                                                    logits.data_ptr(), static_cast<const float *>(bias), i32(ids),

@@ -445,3 +445,21 @@ def test_route_then_experts():
     y = R.gemm_grouped_nt(xs, w.cuda(), r.offsets)
     no_device_error()
     assert torch.equal(y.cpu(), grouped_ref("nt", xs.cpu(), w, r.offsets, experts).half())
+
+
+def test_outputs_are_tensors_of_their_own():
+    """The outputs lie in one allocation: what is written to one, and what lives on, reaches no other."""
+    z = draw(70, 24, "f32", 18)
+    r = run(z, 5, bias=draw_bias(24, 1))
+    want = [t.clone() for t in r]
+    kept = r.offsets
+    for i, t in enumerate(r):
+        assert t.is_contiguous() and not t.requires_grad and t.data_ptr() % 16 == 0
+        t.fill_(3)
+        for j, o in enumerate(r):
+            if j != i:
+                assert torch.equal(o, want[j]) or j < i
+    del r, t, o
+    junk = [torch.full((100000,), 7, device="cuda", dtype=torch.int32) for _ in range(20)]
+    assert (kept == 3).all() and kept.shape == (25,)
+    assert (torch.cat([kept, kept]).cpu() == 3).all() and len(junk) == 20
