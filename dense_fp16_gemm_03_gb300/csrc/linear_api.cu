@@ -11,10 +11,11 @@ using namespace gemm_f16;
 
 namespace {
 
-enum LinearVariantId { kVNtWide, kVNtFew, kVNnWide, kVNnFew };
+enum LinearVariantId { kVNtWide, kVNtFew, kVNnWide, kVNnFew, kVSumWide, kVSumFew };
 const RaggedVariant kLinear[] = {
-    RAGGED_VARIANT(kNT, 2, 256, 6, true), RAGGED_VARIANT(kNT, 1, 64, 8, true),
-    RAGGED_VARIANT(kNN, 2, 256, 6, true), RAGGED_VARIANT(kNN, 1, 64, 8, true),
+    RAGGED_VARIANT(kNT, 2, 256, 6, true),       RAGGED_VARIANT(kNT, 1, 64, 8, true),
+    RAGGED_VARIANT(kNN, 2, 256, 6, true),       RAGGED_VARIANT(kNN, 1, 64, 8, true),
+    RAGGED_VARIANT(kNN, 2, 256, 6, true, true), RAGGED_VARIANT(kNN, 1, 64, 8, true, true),
 };
 using LinearDevice = RaggedDeviceOf<int(sizeof(kLinear) / sizeof(kLinear[0]))>;
 
@@ -161,7 +162,7 @@ gemm_status_t linear(int mode, gemm_dtype_t dtype, gemm_act_t act, int64_t group
     LinearDevice *dev = nullptr;
     st = linear_device(&dev);
     if (st != GEMM_OK) return st;
-    const int few = mode == kNT ? kVNtFew : kVNnFew, wide = mode == kNT ? kVNtWide : kVNnWide;
+    const int few = mode == kNT ? kVNtFew : dbias ? kVSumFew : kVNnFew, wide = mode == kNT ? kVNtWide : dbias ? kVSumWide : kVNnWide;
     const RaggedChoice choice = ragged_choice(kLinear[few], dev->slots[few], kLinear[wide], dev->slots[wide], groups, rows, pdim, kdim,
                                               ws != nullptr, 0.0);
     const int variant = choice.wide ? wide : few;
@@ -193,6 +194,7 @@ gemm_status_t linear(int mode, gemm_dtype_t dtype, gemm_act_t act, int64_t group
     p.kept = kept;
     p.sums = dbias == nullptr ? nullptr : whole ? dbias : static_cast<float *>(ws);
     p.act = uint32_t(act);
+    p.chain = uint32_t(cdiv(p.k_blocks, cdiv(p.k_blocks, kRagChain)));
     int64_t most = most_tiles(var, groups, rows, pdim);
     if (most >= kSizeLimit) return GEMM_ERR_UNSUPPORTED_SHAPE;
     st = encode_stack(&p.tm_p, w, dtype, groups, n, k, 64, mode == kNT ? 128 : 64);

@@ -18,6 +18,10 @@
 //                                                    the rows of other adapters zeroed, one per adapter of the tile
 //                                                    and 32 of its rank
 //
+// EPI adds to kNT a bias, an activation and a residual and keeps z, and to kNN the derivative of the activation (LinearParams);
+// SUM sums kNN's columns besides.  What the epilogue reads comes in 32 x 32 pieces by the way that the results leave, the first
+// while the product still runs.
+//
 // u is an fp32 sum that the tensor cores take again as an operand.  Rounded to the operands' type it would add to y's error
 // nearly as much as y's own rounding, so it goes in two values, hi = round(u) and lo = round(u - hi), 16 bits in bf16 and 22
 // in fp16, side by side in one K block: b's 32 columns against hi, and again against lo.  (8192 rows of 16 prompts,
@@ -45,6 +49,7 @@
 //               warps, or eight that share the columns of 256-row tiles (with
 //               short contractions the tile's end is the longer part: 24 groups
 //               of 16121 rows in all, 2024 x 136, 34 us with four, 26.2 with eight)
+//               (a SUM epilogue: warps 4.., 2 and 3 only hold registers for them)
 //   the last 4  helper, where the mode has one: kTN without maps zeroes the rows
 //               past a group's end in its last K block (both operands: a zero
 //               times an infinity of the next group would be NaN); kLoraY builds
@@ -159,13 +164,24 @@ struct LinearParams : RaggedParams {
     const void *bias;      // kNT: [groups, pdim], or null
     const void *in;        // kNT: the residual, kNN: z, [rows, pdim], or null
     void *kept;            // kNT: z [rows, pdim], or null
-    float *sums;           // kNN: sums of dx's columns over the rows of each N-side tile, or null
+    float *sums;           // SUM: sums of dx's columns over the rows of each N-side tile
     uint32_t act;
+    uint32_t chain;        // SUM: K blocks of a chain
 };
 
-template <int MODE, int CG, int QCAP, int STAGES, bool EPI = false>
+// SUM: an epilogue with the sums of dx's columns, in chains.  The tensor cores round every sum of 16 products toward zero, so a
+// long contraction loses what grows with its length (relative 4.3e-6 at 4096, 1.0e-6 at 1024): nothing that 16 bits show, but all
+// of it is in a sum over rows that is kept in 32.  So a tile's contraction is cut into equal chains of at most kRagChain K blocks
+// with an accumulator each, in turn, which the epilogue adds up in its registers, rounding to nearest: 7.9e-7 at 4096 and 5.0e-7
+// at 1024, where sums in fp32 throughout have 6.4e-7 and 2.4e-7.  It takes 0.7 us a chain and tile: 16384 rows, 4096 x 4096, 338 us
+// beside 304 in one chain, 360 with chains of 8; 32 groups of 16384 rows in all, 1024 x 2048, 90 to 104 beside 76 to 87.  (64
+// columns at a time from tensor memory, and the epilogue's pieces in a loop that is not unrolled, spill: 4% and more on top.)
+constexpr int kRagChain = 13;
+
+template <int MODE, int CG, int QCAP, int STAGES, bool EPI = false, bool SUM = false>
 struct RaggedCfg {
     static_assert(!EPI || MODE == kNT || MODE == kNN, "epilogue");
+    static_assert(!SUM || (EPI && MODE == kNN), "column sums");
     using Params = std::conditional_t<EPI, LinearParams, RaggedParams>;
     static_assert(CG == 1 || CG == 2, "cta group");
     static constexpr bool kPMn = (MODE == kNN || MODE == kTN);  // M-side operand MN-major
@@ -175,7 +191,12 @@ struct RaggedCfg {
     // 2% longer than four for 16384 rows, 32 groups, 4096 x 4096)
     static constexpr int kEpiSets = ((QCAP == 256 && MODE != kTN) || EPI) ? 2 : 1;
     static constexpr int kEpiWarps = 4 * kEpiSets;
-    static constexpr int kFirstHelper = 2 + kEpiWarps;          // warp
+    // SUM with 128 sums a thread: the epilogue's two warpgroups take registers over from the first (three warps to a quarter of an
+    // SM have 168 each: 3 x 168 = 72 + 2 x 216).  Only they ever ask for more, and the first gives before it does anything else.
+    static constexpr bool kRegs = SUM && QCAP == 256;
+    static constexpr uint32_t kRegsFirst = 72, kRegsEpi = 216, kRegsAll = 168;
+    static constexpr int kFirstEpi = kRegs ? 4 : 2;             // warp
+    static constexpr int kFirstHelper = kFirstEpi + kEpiWarps;  // warp
     static constexpr int kThreads = 32 * kFirstHelper + (kHelper ? kRagHelpers : 0);
     static constexpr int kQCta = QCAP / CG;                     // N-side extent in one CTA's stage
     // rows of a whole N-side box; a tile takes at most two boxes (halves and quarters) and at most a quarter's
@@ -204,7 +225,7 @@ struct RaggedCfg {
     static constexpr int kOffAnyBad = kOffAbort + 4;
     // column sums on their way from the second epilogue set to the first, of two tiles
     static constexpr int kOffSums = kOffAnyBad + 32;
-    static constexpr int kSmemBytes = kOffSums + (EPI && MODE == kNN ? 2 * 128 * 4 : 0) + 1024;
+    static constexpr int kSmemBytes = kOffSums + (SUM ? 2 * 128 * 4 : 0) + 1024;
     static constexpr int kTmemCols = 2 * QCAP < 32 ? 32 : 2 * QCAP;
     static_assert(kQBytes % 1024 == 0 && kOffBar % 8 == 0, "layout");
     static_assert(kSmemBytes <= kRagMaxSmem, "shared memory budget");
@@ -825,11 +846,11 @@ __device__ __noinline__ void ragged_drain(uint32_t bars, uint32_t rec, bool lead
     }
 }
 
-template <int MODE, int CG, int QCAP, int STAGES, bool EPI = false>
-__global__ void __launch_bounds__(RaggedCfg<MODE, CG, QCAP, STAGES, EPI>::kThreads, 1)
-    gemm_ragged_kernel(const __grid_constant__ typename RaggedCfg<MODE, CG, QCAP, STAGES, EPI>::Params p)
+template <int MODE, int CG, int QCAP, int STAGES, bool EPI = false, bool SUM = false>
+__global__ void __launch_bounds__(RaggedCfg<MODE, CG, QCAP, STAGES, EPI, SUM>::kThreads, 1)
+    gemm_ragged_kernel(const __grid_constant__ typename RaggedCfg<MODE, CG, QCAP, STAGES, EPI, SUM>::Params p)
 {
-    using Cfg = RaggedCfg<MODE, CG, QCAP, STAGES, EPI>;
+    using Cfg = RaggedCfg<MODE, CG, QCAP, STAGES, EPI, SUM>;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     const uint32_t raw = ptx::smem_addr(smem_raw);
     const uint32_t base = (raw + 1023u) & ~1023u;
@@ -932,6 +953,9 @@ __global__ void __launch_bounds__(RaggedCfg<MODE, CG, QCAP, STAGES, EPI>::kThrea
         return MODE == kTN && p.maps == nullptr && kb + 1u == s.kb && (s.krows & 15u) != 0u;
     };
 
+    static_assert(!Cfg::kRegs || Cfg::kRegsFirst + 2 * Cfg::kRegsEpi <= 3 * Cfg::kRegsAll, "registers of the launch");
+    if (warp < uint32_t(Cfg::kFirstEpi)) {
+    if constexpr (Cfg::kRegs) ptx::regs_dec<Cfg::kRegsFirst>();
     if (warp == 0) {
         // ------------------------------------------------ TMA producer
         {
@@ -1071,7 +1095,7 @@ __global__ void __launch_bounds__(RaggedCfg<MODE, CG, QCAP, STAGES, EPI>::kThrea
             walk.template each<true>([&](const RaggedSeg &s) {
                 if (!ragged_wait_warp<CG>(bar_acc_empty(acc), acc_phase ^ 1u, p, abort_flag, kRagErrAccEmpty)) return false;
                 ptx::tc_fence_after_sync();
-                const uint32_t d_tmem = tmem_u + acc * uint32_t(QCAP);
+                uint32_t d_tmem = tmem_u + acc * uint32_t(QCAP);
                 const uint32_t idesc = idesc0 | ragged_idesc_n(s.nq);
                 // K blocks that are full and need no helper come first, four instructions each and nothing else:
                 // the issue loop has to stay ahead of the tensor cores
@@ -1119,10 +1143,30 @@ __global__ void __launch_bounds__(RaggedCfg<MODE, CG, QCAP, STAGES, EPI>::kThrea
                 } else {
                     uint32_t kb = MODE == kLoraY ? s.lo - s.e_lo : s.lo;
                     const uint32_t end = MODE == kLoraY ? s.hi - s.e_lo : s.hi;
+                    // SUM: the next chain, in the other accumulator
+                    uint32_t linked = 0u, chain = 0u;
+                    if constexpr (SUM) chain = p.chain;
+                    auto next_chain = [&]() -> bool {
+                        if (!SUM || linked++ != chain) return true;
+                        linked = 1u;
+                        if (elected) {
+                            if constexpr (CG == 1) ptx::mma_commit(bar_acc_full(acc));
+                            else ptx::mma_commit_pair(bar_acc_full(acc), uint16_t(3u));
+                        }
+                        if (++acc == 2u) {
+                            acc = 0;
+                            acc_phase ^= 1u;
+                        }
+                        if (!ragged_wait_warp<CG>(bar_acc_empty(acc), acc_phase ^ 1u, p, abort_flag, kRagErrAccEmpty)) return false;
+                        ptx::tc_fence_after_sync();
+                        d_tmem = tmem_u + acc * uint32_t(QCAP);
+                        accumulate = 0u;
+                        return true;
+                    };
                     for (; kb < min(end, whole); ++kb)
-                        if (!block(4u, false)) return false;
+                        if (!next_chain() || !block(4u, false)) return false;
                     for (; kb < end; ++kb)
-                        if (!block(steps_of(s, kb), fixed_block(s, kb))) return false;
+                        if (!next_chain() || !block(steps_of(s, kb), fixed_block(s, kb))) return false;
                 }
                 if (elected) {
                     if constexpr (CG == 1) ptx::mma_commit(bar_acc_full(acc));
@@ -1184,18 +1228,20 @@ __global__ void __launch_bounds__(RaggedCfg<MODE, CG, QCAP, STAGES, EPI>::kThrea
                 return true;
             });
         }
+    }
     } else if (warp < uint32_t(Cfg::kFirstHelper)) {
         // ------------------------------------------------ epilogue
+        if constexpr (Cfg::kRegs) ptx::regs_inc<Cfg::kRegsEpi>();
         const uint32_t quarter = warp & 3u;  // tensor-memory lanes [32 quarter, +32)
-        const uint32_t set = (warp - 2u) >> 2;  // its 32-column chunks: set, set + kEpiSets, ...
-        const uint32_t buf = base + Cfg::kOffStore + (warp - 2u) * Cfg::kStoreBytes;
+        const uint32_t set = (warp - uint32_t(Cfg::kFirstEpi)) >> 2;  // its 32-column chunks: set, set + kEpiSets, ...
+        const uint32_t buf = base + Cfg::kOffStore + (warp - uint32_t(Cfg::kFirstEpi)) * Cfg::kStoreBytes;
         const bool bf16 = p.bf16 != 0u;
         const uint32_t esize = (MODE == kTN && p.out32) ? 4u : 2u;
 
         if (early) ptx::griddep_wait();
         // what no tile covers: rows in no group, and the gradients of groups without rows
         {
-            const uint64_t first = uint64_t(blockIdx.x) * (32u * Cfg::kEpiWarps) + (threadIdx.x - 64u);
+            const uint64_t first = uint64_t(blockIdx.x) * (32u * Cfg::kEpiWarps) + (threadIdx.x - 32u * Cfg::kFirstEpi);
             const uint64_t stride = uint64_t(gridDim.x) * (32u * Cfg::kEpiWarps);
             auto zero_in = [&](void *out, uint64_t from, uint64_t count) {  // 16-byte chunks
                 uint4 *dst = static_cast<uint4 *>(out) + from;
@@ -1222,11 +1268,166 @@ __global__ void __launch_bounds__(RaggedCfg<MODE, CG, QCAP, STAGES, EPI>::kThrea
 
         if (late) ptx::griddep_wait();
         uint32_t acc = 0, acc_phase = 0;
+        uint32_t tiles_done = 0;  // SUM
         uint32_t adapted = 0;  // kLoraY: segments with adapter blocks so far
         bool let_in = false;
         bool published = false, taken = false, stopped = false;  // sk: this CTA's flags
+        // sk: waits for the partial sums of a tile's earlier K blocks; returns the first worker that has some
+        auto wait_partials = [&](const RaggedSeg &s) -> uint32_t {
+            const uint32_t w_lo = walk.first_of((s.tile - walk.first_split()) * s.kb);
+            if (warp == uint32_t(Cfg::kFirstEpi)) {
+                for (uint32_t w = w_lo + lane; w < walk.worker; w += 32u) {
+                    uint64_t *flag = p.flags + w * CG + rank;
+                    const long long t0 = clock64();
+                    uint64_t v;
+                    while ((v = ptx::ld_acquire_gpu_u64(flag)) != p.stamp) {
+                        if (v == flag_not_coming(p.stamp) || *abort_flag || clock64() - t0 > p.wait_limit) {
+                            *abort_flag = 1u;
+                            atomicCAS(p.error_word, 0u, kRagErrPartial | (blockIdx.x << 8));
+                            break;
+                        }
+                    }
+                    if (v == p.stamp) ptx::st_release_gpu_u64(flag, 0u);
+                    else flag_give_up(flag, p.stamp);
+                }
+                __syncwarp();
+            }
+            taken = true;
+            ptx::named_barrier_sync(1, 32 * Cfg::kEpiWarps);
+            return w_lo;
+        };
         walk.template each<false>([&](const RaggedSeg &s) {
             const bool split = MODE != kTN && p.sk != 0u && (s.lo != 0u || s.hi != s.kb);
+            if constexpr (SUM) {
+                constexpr int kOwn = QCAP / 32 / Cfg::kEpiSets;  // 32-column pieces of a warp
+                constexpr uint32_t kSlot = 128u * QCAP;
+                const uint32_t prow = s.p0 + rank * 128u + quarter * 32u, chunks = (s.nq + 31u) / 32u;
+                const uint32_t halves = (s.nq + 15u) / 16u, piece = quarter * 32u * QCAP + lane * 4u;
+                const bool live = prow < p.pdim;
+                float run[kOwn][32];
+                auto piece_of = [&](int i) { return set + uint32_t(i) * Cfg::kEpiSets; };
+                LinearPiece<true> z;  // on its way before the product is there
+                if (live && p.in != nullptr && piece_of(0) < chunks && s.hi == s.kb) z.fetch(p.in, p.pdim, s, prow, piece_of(0));
+                for (uint32_t from = s.lo; from < s.hi; from += p.chain) {
+                    const bool ok = ragged_wait<CG>(bar_acc_full(acc), acc_phase, p, abort_flag, kRagErrAccFull);
+                    if (!ptx::named_barrier_and(1, 32 * Cfg::kEpiWarps, ok)) {  // (they meet below: stop together)
+                        stopped = true;
+                        return false;
+                    }
+                    if (!let_in) {
+                        ptx::griddep_launch_dependents();
+                        let_in = true;
+                    }
+                    ptx::tc_fence_after_sync();
+                    const uint32_t t_col = tmem_base + ((quarter * 32u) << 16) + acc * uint32_t(QCAP);
+#pragma unroll
+                    for (int i = 0; i < kOwn; ++i) {
+                        const uint32_t c = piece_of(i);
+                        if (!live || c >= chunks) continue;
+                        uint32_t r[32];
+                        ptx::tmem_ld_32x32b_x32_wait(t_col + 32u * c, r);
+                        if (from == s.lo) {
+#pragma unroll
+                            for (int j = 0; j < 32; ++j) run[i][j] = __uint_as_float(r[j]);
+                        } else {
+#pragma unroll
+                            for (int j = 0; j < 32; ++j) run[i][j] += __uint_as_float(r[j]);
+                        }
+                    }
+                    ptx::tc_fence_before_sync();
+                    __syncwarp();
+                    if (lane == 0) {
+                        if constexpr (CG == 1) ptx::mbar_arrive(bar_acc_empty(acc));
+                        else ptx::mbar_arrive_cluster_signal(ptx::map_to_rank(bar_acc_empty(acc), 0u));
+                    }
+                    if (++acc == 2u) {
+                        acc = 0;
+                        acc_phase ^= 1u;
+                    }
+                }
+                if (split && s.hi != s.kb) {
+                    float *slot = p.partials + size_t(blockIdx.x) * kSlot + piece;
+#pragma unroll
+                    for (int i = 0; i < kOwn; ++i) {
+                        const uint32_t c = piece_of(i);
+                        if (!live || c >= chunks) continue;
+#pragma unroll
+                        for (int j = 0; j < 8; ++j)
+                            if (2u * c + uint32_t(j / 4) < halves)
+                                ptx::st_global_cg_f4(slot + c * 1024u + j * 128, run[i][4 * j], run[i][4 * j + 1], run[i][4 * j + 2],
+                                                     run[i][4 * j + 3]);
+                    }
+                    __threadfence();
+                    ptx::named_barrier_sync(1, 32 * Cfg::kEpiWarps);
+                    if (threadIdx.x == 32u * Cfg::kFirstEpi) flag_publish(p.flags + blockIdx.x, p.stamp, p.stamp);
+                    published = true;
+                    return true;
+                }
+                if (split) {
+                    const uint32_t w_lo = wait_partials(s);
+                    for (uint32_t w = w_lo; w < walk.worker; ++w) {
+                        const float *slot = p.partials + size_t(w * CG + rank) * kSlot + piece;
+#pragma unroll
+                        for (int i = 0; i < kOwn; ++i) {
+                            const uint32_t c = piece_of(i);
+                            if (!live || c >= chunks) continue;
+                            float4 v[8];
+#pragma unroll
+                            for (int j = 0; j < 8; ++j)
+                                v[j] = 2u * c + uint32_t(j / 4) < halves ? ptx::ld_global_cg_f4(slot + c * 1024u + j * 128)
+                                                                         : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                            for (int j = 0; j < 8; ++j) {
+                                run[i][4 * j] += v[j].x;
+                                run[i][4 * j + 1] += v[j].y;
+                                run[i][4 * j + 2] += v[j].z;
+                                run[i][4 * j + 3] += v[j].w;
+                            }
+                        }
+                    }
+                }
+                act::Two both = act::two(0.0f);
+                if (live)
+                    act::with_kind(p.act, [&](auto kind) {
+                        constexpr int kAct = decltype(kind)::value;
+#pragma unroll
+                        for (int i = 0; i < kOwn; ++i) {
+                            const uint32_t c = piece_of(i);
+                            if (c >= chunks) continue;
+                            uint32_t r[32], w[16];
+                            if (kAct != GEMM_ACT_NONE) {
+                                z.columns(buf, w);
+                                if (i + 1 < kOwn && piece_of(i + 1) < chunks) z.fetch(p.in, p.pdim, s, prow, piece_of(i + 1));
+                            }
+                            const uint32_t left = s.qn - 32u * c;  // rows of the tile in this piece and behind it
+#pragma unroll
+                            for (int j = 0; j < 16; ++j) {
+                                act::Two d = act::two(run[i][2 * j], run[i][2 * j + 1]);
+                                if (kAct != GEMM_ACT_NONE) {
+                                    const float2 at = ragged_unpack(w[j], bf16);
+                                    d = act::apply_grad<kAct>(d, act::two(at.x, at.y));
+                                }
+                                const float2 f = act::apart(d);
+                                both = both + act::two(left >= 32u || 2u * uint32_t(j) < left ? f.x : 0.0f,
+                                                       left >= 32u || 2u * uint32_t(j) + 1u < left ? f.y : 0.0f);
+                                r[2 * j] = __float_as_uint(f.x);
+                                r[2 * j + 1] = __float_as_uint(f.y);
+                            }
+                            linear_store(p.out, p.pdim, s, prow, c, buf, r, bf16);
+                        }
+                    });
+                // the two sets of a quarter's warps meet; a sum is read before its place is taken by the next tile but one
+                const float2 pair = act::apart(both);
+                volatile float *from = reinterpret_cast<volatile float *>(smem + Cfg::kOffSums) + ((tiles_done & 1u) * 128u + quarter * 32u);
+                ++tiles_done;
+                if (set == 1u) from[lane] = pair.x + pair.y;
+                ptx::named_barrier_sync(2 + quarter, 64);
+                if (set == 0u && prow + lane < p.pdim) {
+                    const uint32_t slot = tab_tile[s.g] / p.tiles_p + s.qi;
+                    p.sums[size_t(slot) * p.pdim + prow + lane] = pair.x + pair.y + from[lane];
+                }
+                return true;
+            }
             // what the epilogue takes besides the product is on its way before the product is there
             LinearPiece<EPI> piece_in;
             float bias = 0.0f;
@@ -1239,10 +1440,8 @@ __global__ void __launch_bounds__(RaggedCfg<MODE, CG, QCAP, STAGES, EPI>::kThrea
                 }
             }
             const bool ok = ragged_wait<CG>(bar_acc_full(acc), acc_phase, p, abort_flag, kRagErrAccFull);
-            // the warps meet at named barriers below when the tile is split, or has its columns summed: stop together
-            bool together = MODE != kTN && p.sk != 0u;
-            if constexpr (EPI && MODE == kNN) together = together || p.sums != nullptr;
-            if (together) {
+            // the warps meet at named barriers below when the tile is split: stop together
+            if (MODE != kTN && p.sk) {
                 if (!ptx::named_barrier_and(1, 32 * Cfg::kEpiWarps, ok)) {
                     stopped = true;
                     return false;
@@ -1317,33 +1516,12 @@ __global__ void __launch_bounds__(RaggedCfg<MODE, CG, QCAP, STAGES, EPI>::kThrea
                 release();
                 __threadfence();
                 ptx::named_barrier_sync(1, 32 * Cfg::kEpiWarps);
-                if (threadIdx.x == 64u) flag_publish(p.flags + blockIdx.x, p.stamp, p.stamp);
+                if (threadIdx.x == 32u * Cfg::kFirstEpi) flag_publish(p.flags + blockIdx.x, p.stamp, p.stamp);
                 published = true;
                 return true;
             }
             uint32_t w_lo = walk.worker;  // workers [w_lo, worker) hold the tile's earlier K blocks
-            if (split) {
-                w_lo = walk.first_of((s.tile - walk.first_split()) * s.kb);
-                if (warp == 2u) {
-                    for (uint32_t w = w_lo + lane; w < walk.worker; w += 32u) {
-                        uint64_t *flag = p.flags + w * CG + rank;
-                        const long long t0 = clock64();
-                        uint64_t v;
-                        while ((v = ptx::ld_acquire_gpu_u64(flag)) != p.stamp) {
-                            if (v == flag_not_coming(p.stamp) || *abort_flag || clock64() - t0 > p.wait_limit) {
-                                *abort_flag = 1u;
-                                atomicCAS(p.error_word, 0u, kRagErrPartial | (blockIdx.x << 8));
-                                break;
-                            }
-                        }
-                        if (v == p.stamp) ptx::st_release_gpu_u64(flag, 0u);
-                        else flag_give_up(flag, p.stamp);
-                    }
-                    __syncwarp();
-                }
-                taken = true;
-                ptx::named_barrier_sync(1, 32 * Cfg::kEpiWarps);
-            }
+            if (split) w_lo = wait_partials(s);
             // 32 columns of the finished tile: the accumulator plus the other workers' partials, lowest first,
             // two workers' loads in flight
             auto chunk32 = [&](uint32_t c, uint32_t (&r)[32]) {
@@ -1440,7 +1618,6 @@ __global__ void __launch_bounds__(RaggedCfg<MODE, CG, QCAP, STAGES, EPI>::kThrea
                     if constexpr (EPI)
                         act::with_kind(p.act, [&](auto kind) {
                             constexpr int kAct = decltype(kind)::value;
-                            act::Two both = act::two(0.0f);
                             for (uint32_t c = set; c < chunks; c += Cfg::kEpiSets) {
                                 uint32_t r[32], w[16];
                                 if (p.in != nullptr) {
@@ -1472,28 +1649,8 @@ __global__ void __launch_bounds__(RaggedCfg<MODE, CG, QCAP, STAGES, EPI>::kThrea
                                         r[2 * i] = __float_as_uint(f.x);
                                         r[2 * i + 1] = __float_as_uint(f.y);
                                     }
-                                    if (p.sums != nullptr) {
-                                        const uint32_t left = s.qn - 32u * c;  // rows of the tile in this piece and behind it
-#pragma unroll
-                                        for (uint32_t j = 0; j < 32u; j += 2u)
-                                            both = both + act::two(left >= 32u || j < left ? __uint_as_float(r[j]) : 0.0f,
-                                                                   left >= 32u || j + 1u < left ? __uint_as_float(r[j + 1]) : 0.0f);
-                                    }
                                 }
                                 linear_store(p.out, p.pdim, s, prow, c, buf, r, bf16);
-                            }
-                            if (MODE == kNN && p.sums != nullptr) {
-                                // the two sets of this quarter's warps meet; a sum is read before the set comes to the next tile
-                                // but one, which takes its place
-                                volatile float *from = reinterpret_cast<volatile float *>(smem + Cfg::kOffSums) + (acc * 128u + quarter * 32u);
-                                const float2 sums = act::apart(both);
-                                const float sum = sums.x + sums.y;
-                                if (set == 1u) from[lane] = sum;
-                                ptx::named_barrier_sync(2 + quarter, 64);
-                                if (set == 0u && prow + lane < p.pdim) {
-                                    const uint32_t slot = tab_tile[s.g] / p.tiles_p + s.qi;
-                                    p.sums[size_t(slot) * p.pdim + prow + lane] = sum + from[lane];
-                                }
                             }
                         });
                 } else if (live) {
@@ -1540,7 +1697,8 @@ __global__ void __launch_bounds__(RaggedCfg<MODE, CG, QCAP, STAGES, EPI>::kThrea
             return true;
         });
         if (MODE == kTN && lane == 0) ptx::bulk_wait_group<0>();
-        if (MODE != kTN && stopped && p.sk && warp == 2u) walk.leave_flags(rank, published, taken);
+        if (MODE != kTN && stopped && p.sk && warp == uint32_t(Cfg::kFirstEpi)) walk.leave_flags(rank, published, taken);
+        if constexpr (Cfg::kRegs) ptx::regs_dec<Cfg::kRegsFirst>();  // (as the others: one teardown for all)
     } else if constexpr (Cfg::kHelper) {
         // ------------------------------------------------ helper
         // Four warps that share a stage's rows and never wait for each other: `fixed` counts them all.
