@@ -1092,10 +1092,11 @@ __global__ void __launch_bounds__(RaggedCfg<MODE, CG, QCAP, STAGES, EPI, SUM>::k
             constexpr uint64_t kPStep = Cfg::kPMn ? (2048u >> 4) : 2u;  // K = 16 inside a swizzle atom, or two 8-row groups
             constexpr uint64_t kQStep = Cfg::kQMn ? (2048u >> 4) : 2u;
             uint32_t stage = 0, phase = 0, acc = 0, acc_phase = 0, fixed_uses = 0;
-            walk.template each<true>([&](const RaggedSeg &s) {
+            // K blocks [s.lo, s.hi) into an accumulator
+            auto multiply = [&](const RaggedSeg &s) {
                 if (!ragged_wait_warp<CG>(bar_acc_empty(acc), acc_phase ^ 1u, p, abort_flag, kRagErrAccEmpty)) return false;
                 ptx::tc_fence_after_sync();
-                uint32_t d_tmem = tmem_u + acc * uint32_t(QCAP);
+                const uint32_t d_tmem = tmem_u + acc * uint32_t(QCAP);
                 const uint32_t idesc = idesc0 | ragged_idesc_n(s.nq);
                 // K blocks that are full and need no helper come first, four instructions each and nothing else:
                 // the issue loop has to stay ahead of the tensor cores
@@ -1143,30 +1144,10 @@ __global__ void __launch_bounds__(RaggedCfg<MODE, CG, QCAP, STAGES, EPI, SUM>::k
                 } else {
                     uint32_t kb = MODE == kLoraY ? s.lo - s.e_lo : s.lo;
                     const uint32_t end = MODE == kLoraY ? s.hi - s.e_lo : s.hi;
-                    // SUM: the next chain, in the other accumulator
-                    uint32_t linked = 0u, chain = 0u;
-                    if constexpr (SUM) chain = p.chain;
-                    auto next_chain = [&]() -> bool {
-                        if (!SUM || linked++ != chain) return true;
-                        linked = 1u;
-                        if (elected) {
-                            if constexpr (CG == 1) ptx::mma_commit(bar_acc_full(acc));
-                            else ptx::mma_commit_pair(bar_acc_full(acc), uint16_t(3u));
-                        }
-                        if (++acc == 2u) {
-                            acc = 0;
-                            acc_phase ^= 1u;
-                        }
-                        if (!ragged_wait_warp<CG>(bar_acc_empty(acc), acc_phase ^ 1u, p, abort_flag, kRagErrAccEmpty)) return false;
-                        ptx::tc_fence_after_sync();
-                        d_tmem = tmem_u + acc * uint32_t(QCAP);
-                        accumulate = 0u;
-                        return true;
-                    };
                     for (; kb < min(end, whole); ++kb)
-                        if (!next_chain() || !block(4u, false)) return false;
+                        if (!block(4u, false)) return false;
                     for (; kb < end; ++kb)
-                        if (!next_chain() || !block(steps_of(s, kb), fixed_block(s, kb))) return false;
+                        if (!block(steps_of(s, kb), fixed_block(s, kb))) return false;
                 }
                 if (elected) {
                     if constexpr (CG == 1) ptx::mma_commit(bar_acc_full(acc));
@@ -1177,6 +1158,18 @@ __global__ void __launch_bounds__(RaggedCfg<MODE, CG, QCAP, STAGES, EPI, SUM>::k
                     acc_phase ^= 1u;
                 }
                 return true;
+            };
+            walk.template each<true>([&](const RaggedSeg &s) {
+                if constexpr (SUM) {
+                    RaggedSeg chain = s;
+                    for (; chain.lo < s.hi; chain.lo += p.chain) {
+                        chain.hi = min(chain.lo + p.chain, s.hi);
+                        if (!multiply(chain)) return false;
+                    }
+                    return true;
+                } else {
+                    return multiply(s);
+                }
             });
             // no MMA may still be running when the tensor memory is freed
             if (elected) {

@@ -441,3 +441,36 @@ def test_bias_gradient_of_a_long_contraction(rows, kind):
     no_device_error()
     want = (dy.double().sum(0)[None, :] @ w.double())[0]
     assert ((db.double() - want).abs() / want).max().item() < 6e-6
+
+
+def test_a_workspace_that_captured_graphs_share():
+    """Two graphs in turn in one workspace: what one of them leaves there means nothing to the other, whose parts lie elsewhere."""
+    rng = np.random.default_rng(12)
+    sizes = [(2500, 2304, 2048), (7, 1000, 4096), (1, 2304, 8192)]
+    ws = torch.zeros(max(L.gemm_linear_workspace_size(1, *s) for s in sizes), dtype=torch.uint8, device="cuda")
+    jobs = []
+    for rows, n, k in sizes:
+        x, w, b, _, _ = draw(rng, [rows], n, k, torch.bfloat16, False)
+        xd, wd, bd = x.cuda(), w.cuda(), b.cuda()
+        y, dx, db = (torch.empty((rows, n), dtype=torch.bfloat16, device="cuda"), torch.empty_like(xd), torch.empty(k, device="cuda"))
+
+        def step(xd=xd, wd=wd, bd=bd, y=y, dx=dx, db=db):
+            L.gemm_linear_nt(xd, wd, bias=bd, act="gelu", y=y, workspace=ws)
+            L.gemm_linear_nn(y, wd, z=xd, act="silu", bias_grad=True, dx=dx, dbias=db, workspace=ws)
+
+        step()
+        torch.cuda.synchronize()
+        outs = (y, dx, db)
+        want = [t.clone() for t in outs]
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            step()
+        jobs.append((graph, outs, want, step))
+    for i in (0, 1, 0, 2, 1, 2, 0, 0, 1, 1, 2):
+        graph, outs, want, _ = jobs[i]
+        for t in outs:
+            t.fill_(0)
+        graph.replay()
+        assert all(torch.equal(a, b) for a, b in zip(want, outs))
+        jobs[(i + 1) % 3][3]()  # and one that is not captured between them
+    no_device_error()
