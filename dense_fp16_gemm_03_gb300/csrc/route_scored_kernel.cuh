@@ -31,7 +31,8 @@
 // Two c that are compared are off by twice that, two sums of two by four times that and
 // a rounding more.
 //
-// Bound by issued instructions, as the top-k router.
+// Bound by issued instructions, as the top-k router: 1032 a row of 256 experts, the eight best of the four best of eight
+// groups, at 61% of the issue slots; 16384 rows 33.4 us with the rows' places, the gradient 6.8, in a graph.
 #pragma once
 
 #include "gemm_ragged.h"

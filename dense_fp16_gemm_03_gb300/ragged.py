@@ -373,8 +373,8 @@ def gemm_route_scored(logits, top, score="sigmoid", bias=None, groups=1, top_gro
     score being its largest s + bias (group_top 1) or the sum of its two largest (2).  The weights are scale * s at ids,
     divided by their sum if `renorm`.  `out` and the workspace as in gemm_route_topk."""
     groups = int(groups)
-    r = _binding.native().route_scored(logits, int(top), _score(score), bias, groups, groups if top_groups is None else int(top_groups), group_top,
-                               renorm, scale, out, workspace, None if stream is None else _gemm._stream(stream))
+    r = _binding.native().route_scored(logits, int(top), _score(score), bias, groups, groups if top_groups is None else int(top_groups),
+                                       group_top, renorm, scale, out, workspace, None if stream is None else _gemm._stream(stream))
     _binding.checked(r, "gemm_route_scored")
     return Routing._make(r) if out is None else out
 
@@ -382,5 +382,5 @@ def gemm_route_scored(logits, top, score="sigmoid", bias=None, groups=1, top_gro
 def gemm_route_scored_grad(logits, ids, dweights, score="sigmoid", renorm=True, scale=1.0, dlogits=None, stream=None):
     """The gradient of the logits [rows, experts] float32 from that of gemm_route_scored's weights."""
     r = _binding.native().route_scored_grad(logits, ids, dweights, _score(score), renorm, scale, dlogits,
-                                    None if stream is None else _gemm._stream(stream))
+                                            None if stream is None else _gemm._stream(stream))
     return _binding.checked(r, "gemm_route_scored_grad")
