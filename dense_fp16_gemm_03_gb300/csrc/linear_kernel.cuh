@@ -96,7 +96,8 @@ __global__ void __launch_bounds__(kLinearThreads) linear_sum_kernel(const __grid
 
 // dz = dy f'(z) and the sums of its columns: a block takes a piece of `per` rows of a group and a strip of columns, a thread
 // eight columns (16 bytes) of every so many rows.  A strip is 256, 128 or 64 columns, as they fill the matrix's width
-// best (40000 rows of 264 columns in strips of 256: 23 us).  Bound by HBM for many rows.
+// best (40000 rows of 264 columns in strips of 256: 23 us).  Bound by HBM for many rows: 16384 x 4096 through gelu with its
+// bias gradient 70 us, 5.75 TB/s; few rows by the latency of the two launches (777 x 1000 in eight groups 7.2 us).
 struct LinearGradParams {
     const void *dy, *z;      // z: null without activation
     void *dz;                // or null

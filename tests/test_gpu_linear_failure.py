@@ -92,3 +92,29 @@ def test_calls_on_streams_of_their_own():
     torch.cuda.synchronize()
     no_device_error()
     assert all(torch.equal(o, want if i < 2 else few) for i, o in enumerate(outs))
+
+
+def test_column_sums_on_streams_of_their_own():
+    """Split products with column sums in chains, in place and not, that overlap on the GPU."""
+    torch.manual_seed(5)
+    rows, n, k = 2500, 4096, 2304
+    dyd = torch.randn(rows, n, device="cuda").bfloat16()
+    wd = (torch.randn(n, k, device="cuda") / 64).bfloat16()
+    z = torch.randn(rows, k, device="cuda").bfloat16()
+    want = [L.gemm_linear_nn(dyd[:r], wd, z=z[:r], act="gelu", bias_grad=True, workspace=buffer(1, rows, n, k)) for r in (rows, 40)]
+    streams = [torch.cuda.Stream() for _ in range(4)]
+    spaces = [buffer(1, rows, n, k) for _ in streams]
+    # (every second call writes dx over its z)
+    zs = [[z[:rows if i < 2 else 40].clone() for _ in range(10)] for i in range(4)]
+    dbs = [[torch.empty(k, device="cuda") for _ in range(10)] for _ in range(4)]
+    outs = [[zs[i][j] if j % 2 else torch.empty_like(zs[i][j]) for j in range(10)] for i in range(4)]
+    torch.cuda.synchronize()
+    for j in range(10):
+        for i, s in enumerate(streams):
+            r = rows if i < 2 else 40
+            L.gemm_linear_nn(dyd[:r], wd, z=zs[i][j], act="gelu", bias_grad=True, dx=outs[i][j], dbias=dbs[i][j], workspace=spaces[i], stream=s)
+    torch.cuda.synchronize()
+    no_device_error()
+    for i in range(4):
+        dx, db = want[0 if i < 2 else 1]
+        assert all(torch.equal(o, dx) for o in outs[i]) and all(torch.equal(d, db) for d in dbs[i])
