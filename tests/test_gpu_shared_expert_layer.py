@@ -110,3 +110,14 @@ def test_the_command_runs(monkeypatch, capsys):
     monkeypatch.setattr("sys.argv", argv.split())
     expert_layer.main()
     assert "with a shared expert, backward" in capsys.readouterr().out
+
+
+def test_no_rows():
+    layer = expert_layer.SharedExpertLayer(64, 128, 8, 2, 32, 96, groups=4, top_groups=2)
+    x = torch.empty((0, 64), dtype=torch.bfloat16, device="cuda")
+    out, saved = layer.forward(x)
+    grads = layer.backward(torch.empty_like(out), saved)
+    no_device_error()
+    assert out.shape == grads[0].shape == (0, 64)
+    for g, like in zip(grads[1:], (layer.router, layer.up, layer.down, layer.w1, layer.b1, layer.w2, layer.b2)):
+        assert g.shape == like.shape and not g.any()
