@@ -166,16 +166,17 @@ struct LinearParams : RaggedParams {
     void *kept;            // kNT: z [rows, pdim], or null
     float *sums;           // SUM: sums of dx's columns over the rows of each N-side tile
     uint32_t act;
-    uint32_t chain;        // SUM: K blocks of a chain
+    uint32_t first, chain; // SUM: K blocks of a whole tile's first chain, and of all others
 };
 
-// SUM: an epilogue with the sums of dx's columns, in chains.  The tensor cores round every sum of 16 products toward zero, so a
-// long contraction loses what grows with its length (relative 4.3e-6 at 4096, 1.0e-6 at 1024): nothing that 16 bits show, but all
-// of it is in a sum over rows that is kept in 32.  So a tile's contraction is cut into equal chains of at most kRagChain K blocks
-// with an accumulator each, in turn, which the epilogue adds up in its registers, rounding to nearest: 7.9e-7 at 4096 and 5.0e-7
-// at 1024, where sums in fp32 throughout have 6.4e-7 and 2.4e-7.  It takes 0.7 us a chain and tile: 16384 rows, 4096 x 4096, 338 us
-// beside 304 in one chain, 360 with chains of 8; 32 groups of 16384 rows in all, 1024 x 2048, 90 to 104 beside 76 to 87.  (64
-// columns at a time from tensor memory, and the epilogue's pieces in a loop that is not unrolled, spill: 4% and more on top.)
+// SUM: an epilogue with the sums of dx's columns.  The tensor cores round every sum of 16 products toward zero, so a long
+// contraction loses what grows with its length (relative 4.3e-6 at 4096, 1.0e-6 at 1024): nothing that 16 bits show, but all of it
+// is in a sum over rows that is kept in 32.  So a contraction of more than kRagChain K blocks is cut into chains with an
+// accumulator each, in turn, which the epilogue adds up in its registers, rounding to nearest, and puts back into tensor memory
+// in the last one's place: 8.5e-7 at 4096 and 5.8e-7 at 1024, where sums in fp32 throughout have 6.4e-7 and 2.4e-7.  Beside one
+// chain: 16384 rows, 4096 x 4096, 331 us and 313; 32 groups of 16384 rows in all, 1024 x 2048, 80 to 89 and 72 to 87.  (All pieces
+// kept in registers to the tile's end, so that both accumulators are free: the code is unrolled and waits for its
+// instructions, 338 and 104 us, and half as long again for contractions of 512.)
 constexpr int kRagChain = 13;
 
 template <int MODE, int CG, int QCAP, int STAGES, bool EPI = false, bool SUM = false>
@@ -846,6 +847,11 @@ __device__ __noinline__ void ragged_drain(uint32_t bars, uint32_t rec, bool lead
     }
 }
 
+__device__ __forceinline__ uint32_t ragged_first_chain(const LinearParams &p, const RaggedSeg &s)
+{
+    return s.lo == 0u && s.hi == s.kb ? p.first : p.chain;
+}
+
 template <int MODE, int CG, int QCAP, int STAGES, bool EPI = false, bool SUM = false>
 __global__ void __launch_bounds__(RaggedCfg<MODE, CG, QCAP, STAGES, EPI, SUM>::kThreads, 1)
     gemm_ragged_kernel(const __grid_constant__ typename RaggedCfg<MODE, CG, QCAP, STAGES, EPI, SUM>::Params p)
@@ -1162,8 +1168,9 @@ __global__ void __launch_bounds__(RaggedCfg<MODE, CG, QCAP, STAGES, EPI, SUM>::k
             walk.template each<true>([&](const RaggedSeg &s) {
                 if constexpr (SUM) {
                     RaggedSeg chain = s;
-                    for (; chain.lo < s.hi; chain.lo += p.chain) {
-                        chain.hi = min(chain.lo + p.chain, s.hi);
+                    for (chain.hi = s.lo; chain.hi < s.hi;) {
+                        chain.lo = chain.hi;
+                        chain.hi = min(chain.lo + (chain.lo == s.lo ? ragged_first_chain(p, s) : p.chain), s.hi);
                         if (!multiply(chain)) return false;
                     }
                     return true;
@@ -1291,136 +1298,6 @@ __global__ void __launch_bounds__(RaggedCfg<MODE, CG, QCAP, STAGES, EPI, SUM>::k
         };
         walk.template each<false>([&](const RaggedSeg &s) {
             const bool split = MODE != kTN && p.sk != 0u && (s.lo != 0u || s.hi != s.kb);
-            if constexpr (SUM) {
-                constexpr int kOwn = QCAP / 32 / Cfg::kEpiSets;  // 32-column pieces of a warp
-                constexpr uint32_t kSlot = 128u * QCAP;
-                const uint32_t prow = s.p0 + rank * 128u + quarter * 32u, chunks = (s.nq + 31u) / 32u;
-                const uint32_t halves = (s.nq + 15u) / 16u, piece = quarter * 32u * QCAP + lane * 4u;
-                const bool live = prow < p.pdim;
-                float run[kOwn][32];
-                auto piece_of = [&](int i) { return set + uint32_t(i) * Cfg::kEpiSets; };
-                LinearPiece<true> z;  // on its way before the product is there
-                if (live && p.in != nullptr && piece_of(0) < chunks && s.hi == s.kb) z.fetch(p.in, p.pdim, s, prow, piece_of(0));
-                for (uint32_t from = s.lo; from < s.hi; from += p.chain) {
-                    const bool ok = ragged_wait<CG>(bar_acc_full(acc), acc_phase, p, abort_flag, kRagErrAccFull);
-                    if (!ptx::named_barrier_and(1, 32 * Cfg::kEpiWarps, ok)) {  // (they meet below: stop together)
-                        stopped = true;
-                        return false;
-                    }
-                    if (!let_in) {
-                        ptx::griddep_launch_dependents();
-                        let_in = true;
-                    }
-                    ptx::tc_fence_after_sync();
-                    const uint32_t t_col = tmem_base + ((quarter * 32u) << 16) + acc * uint32_t(QCAP);
-#pragma unroll
-                    for (int i = 0; i < kOwn; ++i) {
-                        const uint32_t c = piece_of(i);
-                        if (!live || c >= chunks) continue;
-                        uint32_t r[32];
-                        ptx::tmem_ld_32x32b_x32_wait(t_col + 32u * c, r);
-                        if (from == s.lo) {
-#pragma unroll
-                            for (int j = 0; j < 32; ++j) run[i][j] = __uint_as_float(r[j]);
-                        } else {
-#pragma unroll
-                            for (int j = 0; j < 32; ++j) run[i][j] += __uint_as_float(r[j]);
-                        }
-                    }
-                    ptx::tc_fence_before_sync();
-                    __syncwarp();
-                    if (lane == 0) {
-                        if constexpr (CG == 1) ptx::mbar_arrive(bar_acc_empty(acc));
-                        else ptx::mbar_arrive_cluster_signal(ptx::map_to_rank(bar_acc_empty(acc), 0u));
-                    }
-                    if (++acc == 2u) {
-                        acc = 0;
-                        acc_phase ^= 1u;
-                    }
-                }
-                if (split && s.hi != s.kb) {
-                    float *slot = p.partials + size_t(blockIdx.x) * kSlot + piece;
-#pragma unroll
-                    for (int i = 0; i < kOwn; ++i) {
-                        const uint32_t c = piece_of(i);
-                        if (!live || c >= chunks) continue;
-#pragma unroll
-                        for (int j = 0; j < 8; ++j)
-                            if (2u * c + uint32_t(j / 4) < halves)
-                                ptx::st_global_cg_f4(slot + c * 1024u + j * 128, run[i][4 * j], run[i][4 * j + 1], run[i][4 * j + 2],
-                                                     run[i][4 * j + 3]);
-                    }
-                    __threadfence();
-                    ptx::named_barrier_sync(1, 32 * Cfg::kEpiWarps);
-                    if (threadIdx.x == 32u * Cfg::kFirstEpi) flag_publish(p.flags + blockIdx.x, p.stamp, p.stamp);
-                    published = true;
-                    return true;
-                }
-                if (split) {
-                    const uint32_t w_lo = wait_partials(s);
-                    for (uint32_t w = w_lo; w < walk.worker; ++w) {
-                        const float *slot = p.partials + size_t(w * CG + rank) * kSlot + piece;
-#pragma unroll
-                        for (int i = 0; i < kOwn; ++i) {
-                            const uint32_t c = piece_of(i);
-                            if (!live || c >= chunks) continue;
-                            float4 v[8];
-#pragma unroll
-                            for (int j = 0; j < 8; ++j)
-                                v[j] = 2u * c + uint32_t(j / 4) < halves ? ptx::ld_global_cg_f4(slot + c * 1024u + j * 128)
-                                                                         : make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-                            for (int j = 0; j < 8; ++j) {
-                                run[i][4 * j] += v[j].x;
-                                run[i][4 * j + 1] += v[j].y;
-                                run[i][4 * j + 2] += v[j].z;
-                                run[i][4 * j + 3] += v[j].w;
-                            }
-                        }
-                    }
-                }
-                act::Two both = act::two(0.0f);
-                if (live)
-                    act::with_kind(p.act, [&](auto kind) {
-                        constexpr int kAct = decltype(kind)::value;
-#pragma unroll
-                        for (int i = 0; i < kOwn; ++i) {
-                            const uint32_t c = piece_of(i);
-                            if (c >= chunks) continue;
-                            uint32_t r[32], w[16];
-                            if (kAct != GEMM_ACT_NONE) {
-                                z.columns(buf, w);
-                                if (i + 1 < kOwn && piece_of(i + 1) < chunks) z.fetch(p.in, p.pdim, s, prow, piece_of(i + 1));
-                            }
-                            const uint32_t left = s.qn - 32u * c;  // rows of the tile in this piece and behind it
-#pragma unroll
-                            for (int j = 0; j < 16; ++j) {
-                                act::Two d = act::two(run[i][2 * j], run[i][2 * j + 1]);
-                                if (kAct != GEMM_ACT_NONE) {
-                                    const float2 at = ragged_unpack(w[j], bf16);
-                                    d = act::apply_grad<kAct>(d, act::two(at.x, at.y));
-                                }
-                                const float2 f = act::apart(d);
-                                both = both + act::two(left >= 32u || 2u * uint32_t(j) < left ? f.x : 0.0f,
-                                                       left >= 32u || 2u * uint32_t(j) + 1u < left ? f.y : 0.0f);
-                                r[2 * j] = __float_as_uint(f.x);
-                                r[2 * j + 1] = __float_as_uint(f.y);
-                            }
-                            linear_store(p.out, p.pdim, s, prow, c, buf, r, bf16);
-                        }
-                    });
-                // the two sets of a quarter's warps meet; a sum is read before its place is taken by the next tile but one
-                const float2 pair = act::apart(both);
-                volatile float *from = reinterpret_cast<volatile float *>(smem + Cfg::kOffSums) + ((tiles_done & 1u) * 128u + quarter * 32u);
-                ++tiles_done;
-                if (set == 1u) from[lane] = pair.x + pair.y;
-                ptx::named_barrier_sync(2 + quarter, 64);
-                if (set == 0u && prow + lane < p.pdim) {
-                    const uint32_t slot = tab_tile[s.g] / p.tiles_p + s.qi;
-                    p.sums[size_t(slot) * p.pdim + prow + lane] = pair.x + pair.y + from[lane];
-                }
-                return true;
-            }
             // what the epilogue takes besides the product is on its way before the product is there
             LinearPiece<EPI> piece_in;
             float bias = 0.0f;
@@ -1432,24 +1309,73 @@ __global__ void __launch_bounds__(RaggedCfg<MODE, CG, QCAP, STAGES, EPI, SUM>::k
                         bias = ragged_value(static_cast<const uint16_t *>(p.bias)[size_t(s.g) * p.pdim + prow + lane], bf16);
                 }
             }
-            const bool ok = ragged_wait<CG>(bar_acc_full(acc), acc_phase, p, abort_flag, kRagErrAccFull);
-            // the warps meet at named barriers below when the tile is split: stop together
-            if (MODE != kTN && p.sk) {
-                if (!ptx::named_barrier_and(1, 32 * Cfg::kEpiWarps, ok)) {
-                    stopped = true;
-                    return false;
-                }
-            } else if (!__all_sync(0xffffffffu, ok)) {
-                return false;
-            }
-            if (!let_in) {
-                ptx::griddep_launch_dependents();
-                let_in = true;
-            }
-            ptx::tc_fence_after_sync();
-            const uint32_t t_col = tmem_base + ((quarter * 32u) << 16) + acc * uint32_t(QCAP);
             const uint32_t prow = s.p0 + rank * 128u + quarter * 32u;  // first M-side index of this warp
             const uint32_t chunks = (s.nq + 31u) / 32u;
+            // the product's next accumulator is full
+            auto arrived = [&]() -> bool {
+                const bool ok = ragged_wait<CG>(bar_acc_full(acc), acc_phase, p, abort_flag, kRagErrAccFull);
+                // the warps meet at named barriers below when the tile is split or has its columns summed: stop together
+                if (MODE != kTN && (SUM || p.sk)) {
+                    if (!ptx::named_barrier_and(1, 32 * Cfg::kEpiWarps, ok)) {
+                        stopped = true;
+                        return false;
+                    }
+                } else if (!__all_sync(0xffffffffu, ok)) {
+                    return false;
+                }
+                if (!let_in) {
+                    ptx::griddep_launch_dependents();
+                    let_in = true;
+                }
+                ptx::tc_fence_after_sync();
+                return true;
+            };
+            if (!arrived()) return false;
+            if constexpr (SUM) {
+                // the chains are added up in registers, and their sum goes back to tensor memory in the last one's place
+                const uint32_t first = ragged_first_chain(p, s);
+                if (s.lo + first < s.hi) {
+                    constexpr int kOwn = QCAP / 32 / Cfg::kEpiSets;  // 32-column pieces of a warp
+                    float run[kOwn][32];
+#pragma unroll
+                    for (int i = 0; i < kOwn; ++i)
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) run[i][j] = 0.0f;
+                    for (uint32_t next = s.lo + first;; next += p.chain) {
+                        const uint32_t column = tmem_base + ((quarter * 32u) << 16) + acc * uint32_t(QCAP);
+#pragma unroll
+                        for (int i = 0; i < kOwn; ++i) {
+                            const uint32_t c = set + uint32_t(i) * Cfg::kEpiSets;
+                            if (prow >= p.pdim || c >= chunks) continue;
+                            uint32_t r[32];
+                            ptx::tmem_ld_32x32b_x32_wait(column + 32u * c, r);
+#pragma unroll
+                            for (int j = 0; j < 32; ++j) run[i][j] += __uint_as_float(r[j]);
+                        }
+                        if (next >= s.hi) {
+#pragma unroll
+                            for (int i = 0; i < kOwn; ++i) {
+                                const uint32_t c = set + uint32_t(i) * Cfg::kEpiSets;
+                                if (prow < p.pdim && c < chunks) ptx::tmem_st_32x32b_x32(column + 32u * c, run[i]);
+                            }
+                            ptx::tmem_st_wait();
+                            break;
+                        }
+                        ptx::tc_fence_before_sync();
+                        __syncwarp();
+                        if (lane == 0) {
+                            if constexpr (CG == 1) ptx::mbar_arrive(bar_acc_empty(acc));
+                            else ptx::mbar_arrive_cluster_signal(ptx::map_to_rank(bar_acc_empty(acc), 0u));
+                        }
+                        if (++acc == 2u) {
+                            acc = 0;
+                            acc_phase ^= 1u;
+                        }
+                        if (!arrived()) return false;
+                    }
+                }
+            }
+            const uint32_t t_col = tmem_base + ((quarter * 32u) << 16) + acc * uint32_t(QCAP);
             constexpr uint32_t kSlot = 128u * QCAP;
             // partial tile in the workspace: warp quarter, 32-column chunk, then float4 j of every lane
             const uint32_t piece = quarter * 32u * QCAP + lane * 4u;
@@ -1611,6 +1537,7 @@ __global__ void __launch_bounds__(RaggedCfg<MODE, CG, QCAP, STAGES, EPI, SUM>::k
                     if constexpr (EPI)
                         act::with_kind(p.act, [&](auto kind) {
                             constexpr int kAct = decltype(kind)::value;
+                            act::Two both = act::two(0.0f);
                             for (uint32_t c = set; c < chunks; c += Cfg::kEpiSets) {
                                 uint32_t r[32], w[16];
                                 if (p.in != nullptr) {
@@ -1642,10 +1569,30 @@ __global__ void __launch_bounds__(RaggedCfg<MODE, CG, QCAP, STAGES, EPI, SUM>::k
                                         r[2 * i] = __float_as_uint(f.x);
                                         r[2 * i + 1] = __float_as_uint(f.y);
                                     }
+                                    if constexpr (SUM) {
+                                        const uint32_t left = s.qn - 32u * c;  // rows of the tile in this piece and behind it
+#pragma unroll
+                                        for (uint32_t j = 0; j < 32u; j += 2u)
+                                            both = both + act::two(left >= 32u || j < left ? __uint_as_float(r[j]) : 0.0f,
+                                                                   left >= 32u || j + 1u < left ? __uint_as_float(r[j + 1]) : 0.0f);
+                                    }
                                 }
                                 linear_store(p.out, p.pdim, s, prow, c, buf, r, bf16);
                             }
+                            if constexpr (SUM) {
+                                // the two sets of this quarter's warps meet; a sum is read before its place is taken by the next
+                                // tile but one
+                                const float2 pair = act::apart(both);
+                                volatile float *from = reinterpret_cast<volatile float *>(smem + Cfg::kOffSums) + ((tiles_done & 1u) * 128u + quarter * 32u);
+                                if (set == 1u) from[lane] = pair.x + pair.y;
+                                ptx::named_barrier_sync(2 + quarter, 64);
+                                if (set == 0u && prow + lane < p.pdim) {
+                                    const uint32_t slot = tab_tile[s.g] / p.tiles_p + s.qi;
+                                    p.sums[size_t(slot) * p.pdim + prow + lane] = pair.x + pair.y + from[lane];
+                                }
+                            }
                         });
+                    if constexpr (SUM) ++tiles_done;
                 } else if (live) {
                     // rows t on columns: 32 x 32 pieces transposed through shared memory.  A word holds rows
                     // 2i and 2i + 1 of one output column; a lane reads four columns' words and takes them apart.

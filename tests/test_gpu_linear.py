@@ -430,9 +430,10 @@ def test_guard_bands():
 def test_bias_gradient_of_a_long_contraction(rows, kind):
     """dbias stays a sum in 32 bits however long the contraction is.  All terms are positive, so no error cancels.  The tensor cores
     cut each sum of 16 products off, by less than 2^-23 of what it is: over a chain of 13 x 64 products, 52 sums that grow evenly, at
-    most 26.5 x 2^-23 = 3.2e-6 of the chain's value (1024 sums, uncut, could lose 6.1e-5).  20 chains and at most 4 partials of a
-    split tile are added to nearest, 24 x 2^-24 = 1.4e-6 at most, and the columns' sums over 2048 rows, by 16 in a piece in pairs,
-    4 pieces, 2 sets and 8 tiles, half as much again where every rounding is at its worst: 6e-6."""
+    most 26.5 x 2^-23 = 3.2e-6 of the chain's value (1024 sums, uncut, could lose 6.1e-5), and no more over chains of 20 and 9.
+    At most 29 chains and 4 partials of a split tile are added to nearest, and most of them to less than half of the sum, 1.4e-6, and
+    the columns' sums over 2048 rows, by 16 in a piece in pairs, 4 pieces, 2 sets and 8 tiles, half as much again where every
+    rounding is at its worst: 6e-6."""
     n, k = 16384, 256
     gen = torch.Generator(device="cuda").manual_seed(rows)
     dy = (torch.rand(rows, n, generator=gen, device="cuda") + 0.5).to(KINDS[kind])
