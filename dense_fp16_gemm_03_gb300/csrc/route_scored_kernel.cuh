@@ -584,11 +584,12 @@ __device__ __forceinline__ int32_t route_choose(const RouteScoredParams &p, size
         const uint32_t mine = lane < count ? got.x >> Key::kBits : 0u;
         const uint32_t next = __shfl_down_sync(0xffffffffu, mine, 1);
         bool beside = lane + 1u < count && near(mine, next);
-        if (__any_sync(0xffffffffu, beside)) {
+        const bool more = count == 32u && near(last, rest);  // others than those looked at may take the last one's place
+        if (more || __any_sync(0xffffffffu, beside)) {
             // equal logits and biases are equal scores, and their order by index is right
             const int32_t after = __shfl_down_sync(0xffffffffu, id, 1);
             if (beside && route_same(p, row, id, after)) beside = false;
-            if (count == 32u && near(last, rest)) again = again || !route_even(p, row);
+            if (more) again = again || !route_even(p, row);
             else if (__any_sync(0xffffffffu, beside) && numbers) id = route_order64(p, row, most, id, count);
             else again = again || __any_sync(0xffffffffu, beside);
         }
