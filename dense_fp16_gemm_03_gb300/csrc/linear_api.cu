@@ -108,6 +108,52 @@ bool split_last_wave(const RaggedVariant &v, int slots, int64_t groups, int64_t 
     return (ceil(share) - share) * tile > kSplitLastGain;
 }
 
+// How a product runs, and what it needs of a workspace: partial sums of a bias gradient, then those of split tiles.
+struct LinearPlan {
+    int variant;
+    bool split, split_last;  // over K: all tiles, or those of the last wave
+    bool whole;              // the sums of one tile are dbias
+    size_t sums, need;
+};
+
+LinearPlan linear_plan(const LinearDevice &dev, int mode, bool grouped, bool bias_grad, int64_t groups, int64_t rows, int64_t pdim,
+                       int64_t kdim, bool workspace)
+{
+    const int few = mode == kNT ? kVNtFew : bias_grad ? kVSumFew : kVNnFew, wide = mode == kNT ? kVNtWide : bias_grad ? kVSumWide : kVNnWide;
+    const RaggedChoice choice =
+        ragged_choice(kLinear[few], dev.slots[few], kLinear[wide], dev.slots[wide], groups, rows, pdim, kdim, workspace, 0.0);
+    LinearPlan p;
+    p.variant = choice.wide ? wide : few;
+    const RaggedVariant &var = kLinear[p.variant];
+    p.split = choice.split;
+    p.split_last = choice.wide && !choice.split && workspace && split_last_wave(var, dev.slots[p.variant], groups, rows, pdim, kdim);
+    p.whole = !grouped && rows <= var.qcap;
+    p.sums = bias_grad && !p.whole ? sums_bytes(var.qcap, groups, rows, pdim) : 0;
+    p.need = p.sums + (p.split || p.split_last ? split_bytes(var, dev.slots[p.variant]) : 0);
+    return p;
+}
+
+// What the products of these sizes, or of fewer rows, may need.  Up to a single CTA's rows pairs split tiles for wide layers
+// alone, where their last wave is (28672 x 8192, 64 rows 79.5 us and 86.3 unsplit; 22016 x 4096, one row 32.5 and 41.0), and the
+// space for that, four times the single CTAs', is asked for there only.
+size_t linear_room(const LinearDevice &dev, int64_t groups, int64_t rows, int64_t n, int64_t k)
+{
+    const int64_t one = kLinear[kVNtFew].qcap;
+    size_t split = split_bytes(kLinear[kVNtFew], dev.slots[kVNtFew]), room = 0;
+    if (rows > one)
+        for (int v : {kVNtWide, kVNnWide, kVSumWide}) {
+            const size_t wide = split_bytes(kLinear[v], dev.slots[v]);
+            if (wide > split) split = wide;
+        }
+    for (int64_t r = 1; r <= rows && r <= one; ++r)
+        for (int way = 0; way < 3; ++way) {
+            const LinearPlan p = linear_plan(dev, way == 0 ? kNT : kNN, true, way == 2, groups, r, way == 0 ? n : k, way == 0 ? k : n, true);
+            if (p.need > room) room = p.need;
+        }
+    const size_t most = sums_bytes(one, groups, rows, k) + split;  // (the pairs' sums have fewer lines)
+    return most > room ? most : room;
+}
+
 // The chains of a contraction with column sums.  A whole tile's first one runs while the epilogue has the other accumulator for the
 // end of the tile before, so it is long, and the others make up for its error (16384 rows, 4096 x 4096, beside one chain: chains
 // of 13 blocks +10%, a first one of 18 +6.6%, of 22 +4% but an error of 9.9e-7; 20 and the others 9 +5.7%, 8.5e-7).
@@ -174,18 +220,11 @@ gemm_status_t linear(int mode, gemm_dtype_t dtype, gemm_act_t act, int64_t group
     LinearDevice *dev = nullptr;
     st = linear_device(&dev);
     if (st != GEMM_OK) return st;
-    const int few = mode == kNT ? kVNtFew : dbias ? kVSumFew : kVNnFew, wide = mode == kNT ? kVNtWide : dbias ? kVSumWide : kVNnWide;
-    const RaggedChoice choice = ragged_choice(kLinear[few], dev->slots[few], kLinear[wide], dev->slots[wide], groups, rows, pdim, kdim,
-                                              ws != nullptr, 0.0);
-    const int variant = choice.wide ? wide : few;
+    const LinearPlan plan = linear_plan(*dev, mode, offsets != nullptr, dbias != nullptr, groups, rows, pdim, kdim, ws != nullptr);
+    const int variant = plan.variant;
     const RaggedVariant &var = kLinear[variant];
-    const bool split_last = choice.wide && !choice.split && ws != nullptr && split_last_wave(var, dev->slots[variant], groups, rows, pdim, kdim);
-    // the sums of one tile are dbias
-    const bool whole = offsets == nullptr && rows <= var.qcap;
-    const size_t sums = dbias && !whole ? sums_bytes(var.qcap, groups, rows, pdim) : 0;
-    const size_t need = sums + (choice.split || split_last ? split_bytes(var, dev->slots[variant]) : 0);
-    if (ws != nullptr || ws_bytes != 0 || sums > 0) {
-        if (ws == nullptr || ws_bytes < need) return GEMM_ERR_WORKSPACE;
+    if (ws != nullptr || ws_bytes != 0 || plan.sums > 0) {
+        if (ws == nullptr || ws_bytes < plan.need) return GEMM_ERR_WORKSPACE;
         if (reinterpret_cast<uintptr_t>(ws) & 255u) return GEMM_ERR_ALIGNMENT;
     }
     LinearParams p;
@@ -204,7 +243,7 @@ gemm_status_t linear(int mode, gemm_dtype_t dtype, gemm_act_t act, int64_t group
     p.bias = bias;
     p.in = in;
     p.kept = kept;
-    p.sums = dbias == nullptr ? nullptr : whole ? dbias : static_cast<float *>(ws);
+    p.sums = dbias == nullptr ? nullptr : plan.whole ? dbias : static_cast<float *>(ws);
     p.act = uint32_t(act);
     ragged_chains(p.k_blocks, &p.first, &p.chain);
     int64_t most = most_tiles(var, groups, rows, pdim);
@@ -213,13 +252,13 @@ gemm_status_t linear(int mode, gemm_dtype_t dtype, gemm_act_t act, int64_t group
     if (st == GEMM_OK && mode == kNN) st = encode_pairs(&p.tm_p2, w, dtype, groups, n, k, &p.p_groups);
     if (st == GEMM_OK) st = encode_rows(p.tm_q, first, dtype, rows, kdim, var.qbox);
     if (st != GEMM_OK) return st;
-    if ((choice.split || split_last) && most * p.k_blocks < kIterLimit) {
-        use_split(&p, var, dev->slots[variant], static_cast<char *>(ws) + sums);
-        if (split_last) p.sk = 2;
+    if ((plan.split || plan.split_last) && most * p.k_blocks < kIterLimit) {
+        use_split(&p, var, dev->slots[variant], static_cast<char *>(ws) + plan.sums);
+        if (plan.split_last) p.sk = 2;
         most *= p.k_blocks;
     }
     st = launch_variant(var, dev->slots[variant], dev->error_word, p, &p, most, stream);
-    if (st != GEMM_OK || sums == 0) return st;
+    if (st != GEMM_OK || plan.sums == 0) return st;
     return launch_sum(p.sums, offsets, dbias, groups, rows, pdim, var.qcap, stream);
 }
 
@@ -239,12 +278,7 @@ gemm_status_t gemm_linear_workspace_size(int64_t groups, int64_t rows, int64_t n
     if (st != GEMM_OK) return st;
     *bytes = 0;
     if (rows == 0) return GEMM_OK;
-    const RaggedVariant &few = kLinear[kVNtFew], &wide = kLinear[kVNtWide];
-    const size_t sums = sums_bytes(few.qcap, groups, rows, k);  // (of pairs: fewer)
-    size_t split = split_bytes(few, dev->slots[kVNtFew]);
-    const size_t wide_split = split_bytes(wide, dev->slots[kVNtWide]);
-    if (rows > few.qcap && wide_split > split) split = wide_split;
-    *bytes = k > 0 ? sums + split : 0;
+    if (n > 0 && k > 0) *bytes = linear_room(*dev, groups, rows, n, k);
     const size_t grad = grad_room(groups, rows, n, dev->num_sms);
     if (grad > *bytes) *bytes = grad;
     return GEMM_OK;
