@@ -326,6 +326,11 @@ PyObject *route_scored(PyObject *, PyObject *const *a, Py_ssize_t count)
     if (!counted(count, 12)) return nullptr;
     return guarded([&]() -> PyObject * {
         const at::Tensor &logits = needed(a[0], "logits");
+        // a Routing to write into has all five: one that were made here would end with the call
+        constexpr const char *names[5] = {"ids", "weights", "offsets", "order", "position"};
+        const bool given = a[9] != Py_None;
+        if (given && (!PyTuple_Check(a[9]) || PyTuple_GET_SIZE(a[9]) != 5)) throw Wrong("out must be a Routing");
+        for (Py_ssize_t i = 0; given && i < 5; ++i) needed(PyTuple_GET_ITEM(a[9], i), names[i]);
         const int dev = operand(logits, "logits");
         const gemm_dtype_t kind = kind_of(logits.scalar_type(), true);
         const int64_t rows = logits.size(0), experts = logits.size(1);
@@ -337,9 +342,6 @@ PyObject *route_scored(PyObject *, PyObject *const *a, Py_ssize_t count)
         if (group_top != 1 && group_top != 2) throw Wrong("group_top must be 1 or 2");
         const int64_t each[1] = {experts}, chosen[2] = {rows, top}, ends[1] = {experts + 1}, flat[1] = {rows * top};
         const void *bias = optional(a[3], "bias", each, at::kFloat, dev);
-        const bool given = a[9] != Py_None;
-        if (given && (!PyTuple_Check(a[9]) || PyTuple_GET_SIZE(a[9]) != 5)) throw Wrong("out must be a Routing");
-        auto to = [&](Py_ssize_t i) { return PyTuple_GET_ITEM(a[9], i); };
         const Space ws(a[10], dev);
         const gemm_stream_t stream = stream_of(a[11], dev);
         const bool renorm = truth(a[7]);
@@ -347,11 +349,14 @@ PyObject *route_scored(PyObject *, PyObject *const *a, Py_ssize_t count)
         const gemm_route_score_t score = static_cast<gemm_route_score_t>(number(a[2]));
         at::Tensor ids, weights, offsets, order, position;
         if (given) {
-            ids = output(to(0), "ids", chosen, at::kInt, dev);
-            weights = output(to(1), "weights", chosen, at::kFloat, dev);
-            offsets = output(to(2), "offsets", ends, at::kInt, dev);
-            order = output(to(3), "order", flat, at::kInt, dev);
-            position = output(to(4), "position", chosen, at::kInt, dev);
+            auto to = [&](Py_ssize_t i, c10::IntArrayRef shape, at::ScalarType type) {
+                return output(PyTuple_GET_ITEM(a[9], i), names[i], shape, type, dev);
+            };
+            ids = to(0, chosen, at::kInt);
+            weights = to(1, chosen, at::kFloat);
+            offsets = to(2, ends, at::kInt);
+            order = to(3, flat, at::kInt);
+            position = to(4, chosen, at::kInt);
         } else {
             const int64_t part = (rows * top + 3) / 4 * 4, all[1] = {4 * part + experts + 1};  // (parts of whole 16 bytes)
             const at::Tensor base = output(Py_None, "", all, at::kInt, dev);
