@@ -308,8 +308,8 @@ PyObject *linear_grad(PyObject *, PyObject *const *a, Py_ssize_t count)
         if (!bias && a[6] != Py_None) throw Wrong("dbias is written with bias_grad only");
         const Space ws(a[7], dev);
         const gemm_stream_t stream = stream_of(a[8], dev);
-        // (without act dz is dy, unless another is given)
-        const bool same = act == GEMM_ACT_NONE && a[5] == Py_None;
+        // (without act dz is dy, unless another is given, or offsets, which may leave rows out: they are zero in dz)
+        const bool same = act == GEMM_ACT_NONE && !g.given && a[5] == Py_None;
         const at::Tensor dz = same ? dy : output(a[5], "dz", dy.sizes(), type, dev);
         at::Tensor db;
         if (bias) db = output(a[6], "dbias", g.shape({n}), at::kFloat, dev);

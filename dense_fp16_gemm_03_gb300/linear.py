@@ -123,7 +123,7 @@ def gemm_linear_nn(dy, w, z=None, act=None, offsets=None, bias_grad=False, dx=No
 def gemm_linear_grad(dy, z=None, act=None, offsets=None, bias_grad=False, dz=None, dbias=None, workspace=None, stream=None):
     """dz = dy * f'(z); with `bias_grad` (dz, dbias), dbias the sum of dz over the rows (of each group) in float32.
 
-    dy, z [rows, n]; dz may be dy or z.  Without `act` dz is dy, which is returned as it is unless another dz is given."""
+    dy, z [rows, n]; dz may be dy or z.  Without `act` and offsets dz is dy, which is returned as it is unless another dz is given."""
     r = (_native or _load()).linear_grad(dy, z, _act(act), offsets, bias_grad, dz, dbias, workspace, _raw(stream))
     return _checked(r, "gemm_linear_grad")
 

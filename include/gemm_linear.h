@@ -53,7 +53,8 @@ typedef enum gemm_act {
  * y may be the residual itself, dx may be z, dz may be dy or z (in place); other
  * overlaps are undefined.  The sum of the product needs something to add up: the
  * contraction (k of nt, n of nn) must be > 0 (GEMM_ERR_UNSUPPORTED_SHAPE).  dz may
- * be NULL for GEMM_ACT_NONE, where it would be a copy of dy.
+ * be NULL for GEMM_ACT_NONE, where it would be a copy of dy (with rows of no group
+ * zero): it is not written then.
  *
  * gemm_linear_workspace_size: bytes that serve any of the three calls of these
  * sizes, or of fewer rows, on the current device (k 0 for gemm_linear_grad alone).
