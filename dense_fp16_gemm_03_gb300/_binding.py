@@ -14,7 +14,9 @@ def native():
     global _native
     if _native is None:
         if not os.path.exists(_build.BINDING):
-            raise RuntimeError("gemm_binding.so is not built (%s); run __graft_entry__.build()" % _build.BINDING)
+            lacks = _build.binding_lacks()
+            raise RuntimeError("gemm_binding.so is not built (%s); %srun __graft_entry__.build()" % (
+                _build.BINDING, "%s is missing here: install it and " % lacks if lacks else ""))
         _gemm._tm()   # PyTorch's libraries first, and the product's
         _gemm.lib()
         loader = importlib.machinery.ExtensionFileLoader("gemm_binding", _build.BINDING)

@@ -4,11 +4,13 @@ Python binding gemm_binding.so that links to it.
 Three translation units compiled side by side (the dense product, the ragged
 products with the router, and the products with an epilogue), one ``-gencode`` (sm_103a), shared cudart;
 nvcc cross-compiles them on a machine without a GPU.  The binding is host code
-against PyTorch's headers; without PyTorch there is none.
+against PyTorch's and Python's headers; where one of them is missing the library
+is built without it.
 """
 import glob
 import importlib.util
 import os
+import shutil
 import subprocess
 import sys
 import sysconfig
@@ -48,6 +50,18 @@ def _torch_dir():
     return spec.submodule_search_locations[0] if spec and spec.submodule_search_locations else None
 
 
+def binding_lacks():
+    """What the binding's build needs and does not find here, or None."""
+    torch = _torch_dir()
+    if not torch:
+        return "PyTorch"
+    if not shutil.which(CXX):
+        return CXX
+    needs = [os.path.join(torch, "include", "torch", "csrc", "autograd", "python_variable.h"), os.path.join(torch, "lib", "libtorch_python.so"),
+             os.path.join(torch, "lib", "libc10_cuda.so"), os.path.join(sysconfig.get_paths()["include"], "Python.h")]
+    return next((f for f in needs if not os.path.exists(f)), None)
+
+
 def _stale_binding():
     headers = glob.glob(os.path.join(INCLUDE, "*.h"))
     if not os.path.exists(BINDING):
@@ -72,7 +86,7 @@ def _link_binding(torch, obj):
 
 
 def _compile(lib, extra, binding=None):
-    """The library, and with `binding` (PyTorch's folder) the binding beside it."""
+    """The library, and with `binding` (PyTorch's folder) the binding beside it; the library also where the binding fails."""
     tmp = lib + ".tmp%d" % os.getpid()
     objects = ["%s.%d.o" % (tmp, i) for i in range(len(SOURCES))]
     commands = [[NVCC, *FLAGS, *extra, "-c", "-o", o, src] for o, src in zip(objects, SOURCES)]
@@ -81,12 +95,15 @@ def _compile(lib, extra, binding=None):
         commands.append(_binding_command(binding, objects[-1]))
     try:
         jobs = [subprocess.Popen(c) for c in commands]
-        for job, command, code in zip(jobs, commands, [job.wait() for job in jobs]):
-            if code:
-                raise subprocess.CalledProcessError(code, command)
+        failed = [subprocess.CalledProcessError(code, c) if code else None for c, code in zip(commands, [job.wait() for job in jobs])]
+        for error in failed[:len(SOURCES)]:
+            if error:
+                raise error
         subprocess.run([NVCC, *FLAGS, "-shared", "-o", tmp, *objects[:len(SOURCES)]], check=True)
         os.replace(tmp, lib)
         if binding:
+            if failed[-1]:
+                raise failed[-1]
             _link_binding(binding, objects[-1])
     finally:
         for o in objects:
@@ -97,7 +114,12 @@ def _compile(lib, extra, binding=None):
 
 def build(force=False, verbose_ptxas=False):
     os.makedirs(OUT_DIR, exist_ok=True)
-    torch = _torch_dir()
+    lacks = binding_lacks()
+    torch = None if lacks else _torch_dir()
+    if lacks and _stale_binding():
+        print("gemm_binding.so is left out: %s is missing (the library needs none of it)" % lacks, file=sys.stderr)
+        if os.path.exists(BINDING):
+            os.remove(BINDING)
     if force or _stale_lib(LIB):
         return _compile(LIB, ["-Xptxas", "-v"] if verbose_ptxas else [], binding=torch)
     if torch and _stale_binding():
