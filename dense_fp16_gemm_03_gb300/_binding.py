@@ -17,6 +17,9 @@ def native():
             lacks = _build.binding_lacks()
             raise RuntimeError("gemm_binding.so is not built (%s); %srun __graft_entry__.build()" % (
                 _build.BINDING, "%s is missing here: install it and " % lacks if lacks else ""))
+        if _build.binding_built_for() != _build.binding_target():
+            raise RuntimeError("gemm_binding.so was built for %s, and this is %s; run __graft_entry__.build()" % (
+                _build.binding_built_for() or "another version", _build.binding_target()))
         _gemm._tm()   # PyTorch's libraries first, and the product's
         _gemm.lib()
         loader = importlib.machinery.ExtensionFileLoader("gemm_binding", _build.BINDING)

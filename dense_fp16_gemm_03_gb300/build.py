@@ -62,9 +62,26 @@ def binding_lacks():
     return next((f for f in needs if not os.path.exists(f)), None)
 
 
+def binding_target():
+    """The PyTorch and the Python that a binding built here is for: its classes' layouts are theirs."""
+    torch, version = _torch_dir(), "none"
+    if torch and os.path.exists(os.path.join(torch, "version.py")):
+        with open(os.path.join(torch, "version.py")) as f:
+            version = next((line.split("=", 1)[1].strip() for line in f if line.startswith("__version__")), "unknown")
+    return "PyTorch %s, %s" % (version, sysconfig.get_config_var("SOABI"))
+
+
+def binding_built_for():
+    """What the binding in place was built for (a note beside it), or None."""
+    if not (os.path.exists(BINDING) and os.path.exists(BINDING + ".for")):
+        return None
+    with open(BINDING + ".for") as f:
+        return f.read()
+
+
 def _stale_binding():
     headers = glob.glob(os.path.join(INCLUDE, "*.h"))
-    if not os.path.exists(BINDING):
+    if binding_built_for() != binding_target():
         return True
     t = os.path.getmtime(BINDING)
     return any(os.path.getmtime(f) > t for f in [BINDING_SOURCE, *headers])
@@ -83,6 +100,10 @@ def _link_binding(torch, obj):
     subprocess.run([CXX, "-shared", "-o", tmp, obj, "-L" + OUT_DIR, "-lgemm_f16", "-Wl,-rpath,$ORIGIN", "-L" + os.path.join(torch, "lib"),
                     "-ltorch_cpu", "-ltorch_python", "-lc10", "-lc10_cuda", "-L" + cuda, "-lcudart"], check=True)
     os.replace(tmp, BINDING)
+    # (the note last: a build for another version that ends between the two is done again)
+    with open(tmp, "w") as f:
+        f.write(binding_target())
+    os.replace(tmp, BINDING + ".for")
 
 
 def _compile(lib, extra, binding=None):
