@@ -159,7 +159,7 @@ __device__ __noinline__ int32_t route_exact(const RouteScoredParams &p, size_t r
         if (c[i] == -INFINITY) continue;
         double v = p.by_logit ? c[i] : p.sigmoid ? 1.0 / (1.0 + exp(-c[i])) : exp(c[i] - double(most)) / sum;
         if (!p.sigmoid && bad) v = NAN;
-        if (p.bias) v += double(p.bias[at.first + i]);
+        if (p.bias) v = p.bias[at.first + i] == -INFINITY ? -INFINITY : v + double(p.bias[at.first + i]);
         if (v != v) v = last;
         c[i] = v;
         if (v > one) {
@@ -487,6 +487,11 @@ __device__ __forceinline__ int32_t route_choose(const RouteScoredParams &p, size
 #pragma unroll
             for (int i = 0; i < VPT; ++i) key[i] = full || uint32_t(i) < at.count ? Key::finite(f[i], i) : 0u;
         } else {
+            if (bias.masks) {  // (a score that is NaN would hide it)
+#pragma unroll
+                for (int i = 0; i < VPT; ++i)
+                    if (uint32_t(i) < at.count && p.bias[at.first + i] == -INFINITY) f[i] = -INFINITY;
+            }
 #pragma unroll
             for (int i = 0; i < VPT; ++i) key[i] = Key::any(f[i], i);
         }
