@@ -12,10 +12,15 @@
 // P(-x) for x >= 0 is e^(-x^2/2) t Q(t) with t = 1 / (1 + 0.3 x): the form
 // of Abramowitz and Stegun 7.1.26 with a polynomial of degree 7 fitted here
 // (weighted least squares on Chebyshev points until the relative error is even:
-// below 1.5e-7 for x up to 14, past which P(-x) is 0 in fp32).  It shares the
-// exponential with the density and has no cancellation in the tail.
-// Exponentials and reciprocals are the hardware's approximate ones (relative
-// error some 2^-22, which 16-bit results do not see).
+// below 1.7e-7 in 64 bits with the coefficients as they stand in fp32, for x up to
+// 14, past which P(-x) is 0 in fp32).  It shares the exponential with the density
+// and has no cancellation in the tail.
+// Exponentials and reciprocals are the hardware's approximate ones, with a relative
+// error of some 2^-22.  The exponential's argument is rounded before: one of size a
+// adds up to a 2^-23, so P(-x) in fp32 is off by 6e-7 up to x = 2, 1.6e-6 up to 5 and
+// 8e-6 at the end of its range, and by what the hardware's two add.  Results in 16
+// bits do not see that; in a bias gradient, a sum in fp32, the tail weighs as little
+// as it is small.
 #pragma once
 
 #include <stdint.h>
