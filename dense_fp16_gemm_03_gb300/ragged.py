@@ -371,7 +371,8 @@ def gemm_route_scored(logits, top, score="sigmoid", bias=None, groups=1, top_gro
     s = softmax(logits) or the logits' sigmoid; bias [experts] float32 moves the choice and not the weights.  The experts form
     `groups` (1, 2, 4 ... 32) groups of neighbours; the `top_groups` (None: all) with the largest score are kept, a group's
     score being its largest s + bias (group_top 1) or the sum of its two largest (2).  The weights are scale * s at ids,
-    divided by their sum if `renorm`.  `out` and the workspace as in gemm_route_topk."""
+    divided by their sum if `renorm`.  `out` (all five tensors) and the workspace as in gemm_route_topk.  Without `out` the five
+    lie in one allocation, which lives as long as any of them; clone one that is kept for long by itself."""
     groups = int(groups)
     r = _binding.native().route_scored(logits, int(top), _score(score), bias, groups, groups if top_groups is None else int(top_groups),
                                        group_top, renorm, scale, out, workspace, None if stream is None else _gemm._stream(stream))
